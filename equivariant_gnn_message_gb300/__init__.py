@@ -24,6 +24,11 @@ Entry points (same names as the C ABI):
   eqmp_radius_graph(pos, cutoff, box=None)      -> (dict(off, src, vec[, img, dst, rev]), E)
   eqmp_fused_lmax(l_max, vec, x, row_offsets, src, ...) -> out, degree 4..6
   eqmp_path_table()                             -> list of (l1, l2, l3)
+  eqmp_dropout(x, drop)                         -> out; drop = Dropout(p, seed, offset, group)
+  eqmp_layer_norm(x, w, b, residual=, drop=)    -> dict(y[, s][, stats])
+  eqmp_layer_norm_backward(grad_y, s, stats, w, grad_s=, drop=) -> dict of gradients
+  eqmp_degree_norm(x, w, b, residual=, drop=)   -> dict, on node features [N, C, (l_max+1)^2]
+  eqmp_degree_norm_backward(grad_y, s, stats, w, grad_s=, drop=) -> dict of gradients
 """
 import ctypes
 import os
@@ -34,7 +39,9 @@ __all__ = [
     "eqmp_fused_so2",
     "eqmp_validate_graph",
     "eqmp_device_error", "eqmp_fused_backward", "eqmp_fused_backward_noalloc", "eqmp_radius_graph", "eqmp_fused_lmax",
-    "eqmp_num_paths_lmax", "eqmp_watchdog_selftest", "eqmp_fp32_peak_probe", "sender_view", "EQMP_OK", "EQMP_ERR_INVALID_ARG", "EQMP_ERR_UNSUPPORTED",
+    "eqmp_num_paths_lmax", "eqmp_watchdog_selftest", "eqmp_fp32_peak_probe", "sender_view",
+    "Dropout", "eqmp_dropout", "eqmp_layer_norm", "eqmp_layer_norm_backward", "eqmp_layer_norm_backward_workspace_size",
+    "eqmp_degree_norm", "eqmp_degree_norm_backward", "eqmp_degree_norm_backward_workspace_size", "EQMP_OK", "EQMP_ERR_INVALID_ARG", "EQMP_ERR_UNSUPPORTED",
     "EQMP_ERR_CUDA", "EQMP_ERR_DEVICE_TIMEOUT", "EQMP_ERR_GRAPH",
 ]
 
@@ -57,6 +64,34 @@ class EqmpError(RuntimeError):
 class Weights(ctypes.Structure):
     _fields_ = [("w", ctypes.c_void_p), ("R", ctypes.c_void_p), ("M", ctypes.c_void_p),
                 ("K", ctypes.c_int32)]
+
+
+class Dropout(ctypes.Structure):
+    """Dropout of one call (eqmp_drop): rate p, seed and offset of the counter-based generator, and how many
+    consecutive columns share a draw (group).  The same Dropout gives the same mask, in the forward and in the
+    backward pass; another offset (a step or a layer) gives another one.  step: an int64 CUDA tensor of one
+    value that is added to offset when the kernel runs (for recorded CUDA graphs)."""
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("step_ptr", ctypes.c_void_p), ("group", ctypes.c_int32)]
+
+    def __init__(self, p, seed, offset=0, group=1, step=None):
+        if not 0.0 <= p <= 1.0:
+            raise ValueError("p must be in [0, 1]")
+        if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+            raise ValueError("seed and offset must be unsigned 64-bit")
+        if not 1 <= group < 1 << 31:
+            raise ValueError("group must be at least 1")
+        super().__init__(p, seed, offset, None, group)
+        if step is not None:
+            import torch
+
+            _require(step, "step", torch.int64)
+            if step.numel() != 1:
+                raise ValueError("step must hold one value")
+            self.step, self.step_ptr = step, step.data_ptr()  # keeps the tensor alive
+
+
+_NO_DROP = Dropout(0.0, 0)
 
 
 def library_path():
@@ -124,6 +159,20 @@ def load_library():
     lib.eqmp_radius_graph_pbc.argtypes = [vp, i64, ctypes.c_float, ctypes.POINTER(ctypes.c_float), vp, vp, vp, vp,
                                           vp, vp, i64, vp, vp, ctypes.c_size_t, vp]
     lib.eqmp_radius_graph_pbc.restype = i32
+    f32 = ctypes.c_float
+    lib.eqmp_dropout.argtypes = [vp, i64, i32, i64, i64, Dropout, vp, vp]
+    lib.eqmp_layer_norm.argtypes = [vp, i64, vp, i64, i32, i64, i64, Dropout, vp, vp, f32, vp, vp, vp, vp]
+    lib.eqmp_degree_norm.argtypes = [vp, vp, i32, i64, i32, i32, Dropout, vp, vp, f32, vp, vp, vp, vp]
+    lib.eqmp_layer_norm_backward.argtypes = [vp, i64, vp, i64, vp, i64, i32, i64, i64, Dropout, vp, vp, vp, vp, vp,
+                                             vp, vp, i64, vp]
+    lib.eqmp_degree_norm_backward.argtypes = [vp, vp, vp, i32, i64, i32, i32, Dropout, vp, vp, vp, vp, vp, vp, vp,
+                                              i64, vp]
+    for name in ("dropout", "layer_norm", "degree_norm", "layer_norm_backward", "degree_norm_backward"):
+        getattr(lib, "eqmp_" + name).restype = i32
+    lib.eqmp_layer_norm_backward_workspace_size.argtypes = [i64, i64]
+    lib.eqmp_layer_norm_backward_workspace_size.restype = i64
+    lib.eqmp_degree_norm_backward_workspace_size.argtypes = [i64, i32, i32]
+    lib.eqmp_degree_norm_backward_workspace_size.restype = i64
     _lib = lib
     return lib
 
@@ -555,3 +604,228 @@ def eqmp_fused_backward_noalloc(vec, x, row_offsets, src, dst, send_offsets, sen
                                      w, R, M, need)
     _check(load_library().eqmp_fused_backward_noalloc(*head, _stream(stream)), "eqmp_fused_backward_noalloc")
     return out
+
+
+# ------------------------------------------------------------------ norms and dropout
+def _norm_input(t, name, dtype, shape, dev):
+    """Checks an input of the norms and returns its row stride.  A row (everything behind the first dimension) is
+    packed; the rows of a matrix may be any distance apart."""
+    _same(t, name, dtype, shape, dev)
+    if t.dim() == 2:
+        if t.stride(1) != 1 and shape[1] > 1 and shape[0] > 0:
+            raise ValueError(f"{name} must have contiguous rows")
+        return t.stride(0)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.stride(0)
+
+
+def _same(t, name, dtype, shape, dev):
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, not {dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+
+
+def _packed(t, name, dtype, shape, dev):
+    """Checks a packed tensor (or None) and returns its address."""
+    if t is None:
+        return None
+    _same(t, name, dtype, shape, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _results(need, allowed, specs, out, dev):
+    """The requested result tensors, the caller's own from `out` where it has them, and the addresses of all."""
+    import torch
+
+    got, at = {}, {}
+    for k in need:
+        if k not in allowed:
+            raise ValueError(f"need has {k!r}; allowed are {', '.join(allowed)}")
+        dtype, shape = specs[k]
+        t = out.get(k) if out else None
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+            at[k] = t.data_ptr()
+        else:
+            at[k] = _packed(t, f"out[{k!r}]", dtype, shape, dev)
+        got[k] = t
+    return got, at
+
+
+def _norm_case(x, name, degree):
+    """Storage type, device, shape and the sizes of w and b of a norm's main input."""
+    import torch
+
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dtype, shape = x.dtype, tuple(x.shape)
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+        raise TypeError(f"{name} has dtype {dtype}")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = torch.cuda.current_device()
+    if degree:
+        l_max = {16: 3, 25: 4, 36: 5, 49: 6}.get(shape[2] if len(shape) == 3 else 0)
+        if l_max is None or shape[1] < 1:
+            raise ValueError(f"{name} must be [N, C, (l_max+1)^2] with l_max in 3..6 and C >= 1")
+        return dtype, dev, shape, l_max, (l_max + 1, shape[1]), (shape[1],)
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError(f"{name} must be [rows, cols] with cols >= 1")
+    return dtype, dev, shape, 0, (shape[1],), (shape[1],)
+
+
+def _raw_stream(stream, dev):
+    import torch
+
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _norm_forward(entry, degree, x, w, b, eps, residual, drop, need, out, stream):
+    import torch
+
+    f32 = torch.float32
+    dtype, dev, shape, l_max, w_shape, b_shape = _norm_case(x, "x", degree)
+    x_ld = _norm_input(x, "x", dtype, shape, dev)
+    r_ld = _norm_input(residual, "residual", dtype, shape, dev) if residual is not None else 0
+    wp, bp = _packed(w, "w", f32, w_shape, dev), _packed(b, "b", f32, b_shape, dev)
+    if need is None:
+        need = ("y",) if residual is None else ("y", "s")
+    got, at = _results(need, ("y", "s", "stats"), {"y": (dtype, shape), "s": (dtype, shape),
+                                                   "stats": (f32, (shape[0], l_max + 2))}, out, dev)
+    dt = EQMP_F32 if dtype is f32 else EQMP_BF16
+    dr = _NO_DROP if drop is None else drop
+    r = None if residual is None else residual.data_ptr()
+    lib = load_library()
+    tail = (dr, wp, bp, eps, at.get("s"), at.get("y"), at.get("stats"), _raw_stream(stream, dev))
+    if degree:
+        st = lib.eqmp_degree_norm(x.data_ptr(), r, dt, shape[0], shape[1], l_max, *tail)
+    else:
+        st = lib.eqmp_layer_norm(x.data_ptr(), x_ld, r, r_ld, dt, shape[0], shape[1], *tail)
+    _check(st, entry)
+    return got
+
+
+def _norm_backward(entry, degree, grad_y, s, stats, w, grad_s, drop, need, out, workspace, stream):
+    import torch
+
+    f32 = torch.float32
+    dtype, dev, shape, l_max, w_shape, b_shape = _norm_case(s, "s", degree)
+    s_ld = _norm_input(s, "s", dtype, shape, dev)
+    g_ld = _norm_input(grad_y, "grad_y", dtype, shape, dev)
+    gs_ld = _norm_input(grad_s, "grad_s", dtype, shape, dev) if grad_s is not None else 0
+    wp = _packed(w, "w", f32, w_shape, dev)
+    if stats is None:
+        raise TypeError("stats must be a torch.Tensor")
+    sp = _packed(stats, "stats", f32, (shape[0], l_max + 2), dev)
+    got, at = _results(need, ("x", "r", "w", "b"), {"x": (dtype, shape), "r": (dtype, shape), "w": (f32, w_shape),
+                                                    "b": (f32, b_shape)}, out, dev)
+    dt = EQMP_F32 if dtype is f32 else EQMP_BF16
+    dr = _NO_DROP if drop is None else drop
+    lib = load_library()
+    ws, nbytes = None, 0
+    if "w" in at or "b" in at:
+        nbytes = (lib.eqmp_degree_norm_backward_workspace_size(shape[0], shape[1], l_max) if degree else
+                  lib.eqmp_layer_norm_backward_workspace_size(shape[0], shape[1]))
+        if nbytes < 0:
+            raise EqmpError(EQMP_ERR_UNSUPPORTED, entry)
+        if workspace is None:
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=f"cuda:{dev}")
+        else:
+            _require(workspace, "workspace", torch.uint8)
+            nbytes = workspace.numel()
+        ws = workspace.data_ptr()
+    gs = None if grad_s is None else grad_s.data_ptr()
+    tail = (dr, wp, sp, at.get("r"), at.get("x"), at.get("w"), at.get("b"), ws, nbytes, _raw_stream(stream, dev))
+    if degree:
+        st = lib.eqmp_degree_norm_backward(grad_y.data_ptr(), s.data_ptr(), gs, dt, shape[0], shape[1], l_max, *tail)
+    else:
+        st = lib.eqmp_layer_norm_backward(grad_y.data_ptr(), g_ld, s.data_ptr(), s_ld, gs, gs_ld, dt, shape[0],
+                                          shape[1], *tail)
+    _check(st, entry)
+    return got
+
+
+def eqmp_dropout(x, drop, out=None, stream=None):
+    """dropout(x), fp32 or bf16, by a Dropout.  x: [rows, ...]; the row of an element and its place in the row choose
+    its draw.  The backward pass is the same call on the gradient.  out may be x (in place)."""
+    import torch
+
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dtype is not torch.float32 and x.dtype is not torch.bfloat16:
+        raise TypeError(f"x has dtype {x.dtype}")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    dev, shape = torch.cuda.current_device(), tuple(x.shape)
+    if not shape:
+        raise ValueError("x must be [rows, ...]")
+    ld = _norm_input(x, "x", x.dtype, shape, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    at = _packed(out, "out", x.dtype, shape, dev)
+    cols = 1
+    for n in shape[1:]:
+        cols *= n
+    if cols < 1:
+        raise ValueError("x must have columns")
+    if out is x:
+        ld = cols
+    _check(load_library().eqmp_dropout(x.data_ptr(), ld, EQMP_F32 if x.dtype is torch.float32 else EQMP_BF16, shape[0],
+                                       cols, drop if drop is not None else _NO_DROP, at, _raw_stream(stream, dev)),
+           "eqmp_dropout")
+    return out
+
+
+def eqmp_layer_norm(x, w=None, b=None, eps=1e-5, residual=None, drop=None, need=None, out=None, stream=None):
+    """Layer norm of the rows of x [rows, cols] (fp32 or bf16; w, b fp32 [cols] or None), behind an optional dropout
+    and residual sum: s = residual + dropout(x), y = norm(s).
+
+    Returns a dict of what `need` names: "y", "s" (default with a residual) and "stats" ([rows, 2], for the backward
+    pass).  `out` may hold tensors to write into, by the same names.  x and residual may be slices of wider
+    matrices (contiguous rows, any distance apart)."""
+    return _norm_forward("eqmp_layer_norm", False, x, w, b, eps, residual, drop, need, out, stream)
+
+
+def eqmp_layer_norm_backward(grad_y, s, stats, w=None, grad_s=None, drop=None, need=("x", "w", "b"), out=None,
+                             workspace=None, stream=None):
+    """Gradients of eqmp_layer_norm from dL/dy, the forward pass's s (x where there was neither residual nor dropout)
+    and stats, and grad_s = dL/ds from other uses of s.
+
+    Returns a dict of what `need` names: "x" (behind the dropout), "r" (dL/ds in all: of the residual), "w", "b"."""
+    return _norm_backward("eqmp_layer_norm_backward", False, grad_y, s, stats, w, grad_s, drop, need, out, workspace,
+                          stream)
+
+
+def eqmp_degree_norm(x, w=None, b=None, eps=1e-5, residual=None, drop=None, need=None, out=None, stream=None):
+    """The layer norm by degree of node features x [N, C, (l_max+1)^2], l_max 3..6, which commutes with rotations:
+    degree 0 as a layer norm over the channels, each degree l > 0 divided by its root mean square over channels and
+    orders.  w [l_max+1, C] and b [C] fp32 or None; drop.group must be (l_max+1)^2.  Otherwise as eqmp_layer_norm,
+    with stats [N, l_max+2]; tensors are contiguous."""
+    return _norm_forward("eqmp_degree_norm", True, x, w, b, eps, residual, drop, need, out, stream)
+
+
+def eqmp_degree_norm_backward(grad_y, s, stats, w=None, grad_s=None, drop=None, need=("x", "w", "b"), out=None,
+                              workspace=None, stream=None):
+    """Gradients of eqmp_degree_norm; as eqmp_layer_norm_backward, with "w" [l_max+1, C] and "b" [C]."""
+    return _norm_backward("eqmp_degree_norm_backward", True, grad_y, s, stats, w, grad_s, drop, need, out, workspace,
+                          stream)
+
+
+def eqmp_layer_norm_backward_workspace_size(rows, cols):
+    """Bytes of workspace that eqmp_layer_norm_backward needs for grad_w and grad_b."""
+    return int(load_library().eqmp_layer_norm_backward_workspace_size(int(rows), int(cols)))
+
+
+def eqmp_degree_norm_backward_workspace_size(n, channels, l_max):
+    """Bytes of workspace that eqmp_degree_norm_backward needs for grad_w and grad_b."""
+    return int(load_library().eqmp_degree_norm_backward_workspace_size(int(n), int(channels), int(l_max)))

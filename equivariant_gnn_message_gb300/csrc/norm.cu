@@ -1,0 +1,283 @@
+// Entry points of the norms and of dropout: argument checks and dispatch.
+// Contracts are in include/eqmp.h, the formulas in norm.cuh.
+#include <math.h>
+
+#include "launch.h"
+#include "norm.cuh"
+
+namespace eqmp {
+
+static bool aligned(const void* p, int dtype_bytes) { return reinterpret_cast<uintptr_t>(p) % dtype_bytes == 0; }
+
+// Checks d for rows of `cols` columns and resolves its rate to 1/65536.
+static eqmp_status drop_args(const eqmp_drop& d, long long cols, DropArgs* out) {
+  *out = DropArgs{};
+  out->group = 1;
+  if (!(d.p >= 0.0 && d.p <= 1.0)) return EQMP_ERR_INVALID_ARG;
+  if (d.p == 0.0) return EQMP_OK;
+  if (d.group < 1 || cols % d.group != 0 || !aligned(d.step, 8)) return EQMP_ERR_INVALID_ARG;
+  out->seed = d.seed;
+  out->offset = d.offset;
+  out->step = reinterpret_cast<const unsigned long long*>(d.step);
+  out->threshold = (uint32_t)floor(d.p * 65536.0 + 0.5);
+  out->scale = out->threshold < 65536 ? 65536.0f / (float)(65536 - out->threshold) : 0.0f;
+  out->group = d.group;
+  return EQMP_OK;
+}
+
+// One strided matrix: rows of `cols` elements, `ld` elements apart.
+struct Plane {
+  const void* p;
+  long long ld;
+};
+
+static bool overlap(const Plane& a, const Plane& b, long long rows, long long cols, int bytes) {
+  if (!a.p || !b.p) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  const uintptr_t a1 = a0 + ((rows - 1) * a.ld + cols) * bytes, b1 = b0 + ((rows - 1) * b.ld + cols) * bytes;
+  return a0 < b1 && b0 < a1;
+}
+
+// Inputs: aligned, strides that address forward.  Outputs (packed): aligned,
+// apart from the inputs and from one another.
+static bool planes_ok(const Plane* in, int n_in, void* const* outs, int n_out, long long rows, long long cols,
+                      int bytes) {
+  for (int i = 0; i < n_in; ++i)
+    if (in[i].p && (!aligned(in[i].p, bytes) || in[i].ld < 0)) return false;
+  for (int o = 0; o < n_out; ++o) {
+    if (!outs[o]) continue;
+    if (!aligned(outs[o], bytes)) return false;
+    for (int i = 0; i < n_in; ++i)
+      if (overlap(in[i], Plane{outs[o], cols}, rows, cols, bytes)) return false;
+    for (int q = 0; q < o; ++q)
+      if (overlap(Plane{outs[q], cols}, Plane{outs[o], cols}, rows, cols, bytes)) return false;
+  }
+  return true;
+}
+
+static int rows_grid(long long rows, const DeviceInfo& dev) {
+  const long long cap = (long long)dev.sms * 8;
+  return (int)(rows < cap ? rows : cap);
+}
+
+template <typename T, int L>
+static eqmp_status forward_t(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  k_norm_wide<T, L><<<rows_grid(a.rows, dev), kWideThreads, 0, st>>>(a);
+  return cuda_status(cudaGetLastError());
+}
+
+template <typename T, int L>
+static eqmp_status backward_t(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  if (a.gr || a.gx) {
+    k_norm_bwd_wide<T, L><<<rows_grid(a.rows, dev), kWideThreads, 0, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return EQMP_ERR_CUDA;
+  }
+  if (!a.gw && !a.gb) return EQMP_OK;
+  const long long M = (long long)(L + 2) * a.C;
+  const dim3 grid((unsigned)((a.C + kWideSumX - 1) / kWideSumX), (unsigned)a.parts);
+  k_norm_bwd_wide_w<T, L><<<grid, dim3(kWideSumX, kWideSumY), 0, st>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return EQMP_ERR_CUDA;
+  k_norm_bwd_sum<L><<<(unsigned)((M + kSumX - 1) / kSumX), dim3(kSumX, kSumY), 0, st>>>(a);
+  return cuda_status(cudaGetLastError());
+}
+
+template <int L>
+static eqmp_status dispatch_t(const NormArgs& a, bool bf16, bool backward, const DeviceInfo& dev, cudaStream_t st) {
+  if (backward) return bf16 ? backward_t<__nv_bfloat16, L>(a, dev, st) : backward_t<float, L>(a, dev, st);
+  return bf16 ? forward_t<__nv_bfloat16, L>(a, dev, st) : forward_t<float, L>(a, dev, st);
+}
+
+static eqmp_status dispatch(const NormArgs& a, int L, bool bf16, bool backward, cudaStream_t st) {
+  DeviceInfo dev;
+  const eqmp_status s = device_info(&dev);
+  if (s != EQMP_OK) return s;
+  switch (L) {
+    case 0: return dispatch_t<0>(a, bf16, backward, dev, st);
+    case 3: return dispatch_t<3>(a, bf16, backward, dev, st);
+    case 4: return dispatch_t<4>(a, bf16, backward, dev, st);
+    case 5: return dispatch_t<5>(a, bf16, backward, dev, st);
+    case 6: return dispatch_t<6>(a, bf16, backward, dev, st);
+  }
+  return EQMP_ERR_UNSUPPORTED;
+}
+
+// Row ranges of the partial weight gradients: enough to fill the device, at
+// least 64 rows each, so that the partials stay a small part of the traffic.
+static int weight_parts(long long rows) {
+  const long long want = (rows + 63) / 64;
+  return (int)(want < 1 ? 1 : want > 128 ? 128 : want);
+}
+
+static int64_t workspace_bytes(int64_t rows, int64_t C, int L) {
+  return (int64_t)weight_parts(rows) * (L + 2) * C * 4;
+}
+
+// Up to 2^30 rows of up to 2^30 values, so that a row or column index plus a
+// stride of the launch stays an int.
+static eqmp_status check_sizes(int64_t rows, int64_t C, int64_t K, eqmp_dtype dtype) {
+  if (rows < 0 || C < 1 || (dtype != EQMP_F32 && dtype != EQMP_BF16)) return EQMP_ERR_INVALID_ARG;
+  return rows > (1ll << 30) || C > (1ll << 30) / K ? EQMP_ERR_UNSUPPORTED : EQMP_OK;
+}
+
+static eqmp_status run_forward(Plane x, Plane r, eqmp_dtype dtype, int64_t rows, int64_t C, int L, eqmp_drop drop,
+                               const float* w, const float* b, float eps, void* s, void* y, float* stats,
+                               cudaStream_t st) {
+  const int64_t K = (L + 1) * (L + 1);
+  const eqmp_status zs = check_sizes(rows, C, K, dtype);
+  if (zs != EQMP_OK) return zs;
+  if (!(eps >= 0.0f) || isinf(eps)) return EQMP_ERR_INVALID_ARG;
+  NormArgs a{};
+  const eqmp_status ds = drop_args(drop, C * K, &a.drop);
+  if (ds != EQMP_OK) return ds;
+  if (rows == 0 || (!s && !y && !stats)) return EQMP_OK;
+  const bool bf16 = dtype == EQMP_BF16;
+  const Plane in[] = {x, r};
+  void* const outs[] = {s, y};
+  if (!x.p || !planes_ok(in, 2, outs, 2, rows, C * K, bf16 ? 2 : 4)) return EQMP_ERR_INVALID_ARG;
+  if (!aligned(w, 4) || !aligned(b, 4) || !aligned(stats, 4)) return EQMP_ERR_INVALID_ARG;
+  a.x = x.p;
+  a.x_ld = x.ld;
+  a.r = r.p;
+  a.r_ld = r.ld;
+  a.s = s;
+  a.y = y;
+  a.stats = stats;
+  a.w = w;
+  a.b = b;
+  a.rows = (int)rows;
+  a.cols = (int)(C * K);
+  a.C = (int)C;
+  a.eps = eps;
+  return dispatch(a, L, bf16, false, st);
+}
+
+static eqmp_status run_backward(Plane g, Plane x, Plane r, eqmp_dtype dtype, int64_t rows, int64_t C, int L,
+                                eqmp_drop drop, const float* w, const float* stats, void* gr, void* gx, float* gw,
+                                float* gb, void* workspace, int64_t ws_bytes, cudaStream_t st) {
+  const int64_t K = (L + 1) * (L + 1);
+  const eqmp_status zs = check_sizes(rows, C, K, dtype);
+  if (zs != EQMP_OK) return zs;
+  NormArgs a{};
+  const eqmp_status ds = drop_args(drop, C * K, &a.drop);
+  if (ds != EQMP_OK) return ds;
+  if (!gr && !gx && !gw && !gb) return EQMP_OK;
+  if (!aligned(gw, 4) || !aligned(gb, 4)) return EQMP_ERR_INVALID_ARG;
+  if (rows == 0) {  // no row: the sums are zero
+    if (gw && cudaMemsetAsync(gw, 0, (size_t)(L + 1) * C * 4, st) != cudaSuccess) return EQMP_ERR_CUDA;
+    if (gb && cudaMemsetAsync(gb, 0, (size_t)C * 4, st) != cudaSuccess) return EQMP_ERR_CUDA;
+    return EQMP_OK;
+  }
+  const bool bf16 = dtype == EQMP_BF16;
+  const Plane in[] = {x, g, r};
+  void* const outs[] = {gr, gx};
+  if (!x.p || !g.p || !stats || !planes_ok(in, 3, outs, 2, rows, C * K, bf16 ? 2 : 4)) return EQMP_ERR_INVALID_ARG;
+  if (!aligned(w, 4) || !aligned(stats, 4)) return EQMP_ERR_INVALID_ARG;
+  if ((gw || gb) && (!workspace || !aligned(workspace, 16) || ws_bytes < workspace_bytes(rows, C, L)))
+    return EQMP_ERR_INVALID_ARG;
+  a.x = x.p;
+  a.x_ld = x.ld;
+  a.g = g.p;
+  a.g_ld = g.ld;
+  a.r = r.p;
+  a.r_ld = r.ld;
+  a.gr = gr;
+  a.gx = gx;
+  a.gw = gw;
+  a.gb = gb;
+  a.stats = const_cast<float*>(stats);
+  a.w = w;
+  a.part = static_cast<float*>(workspace);
+  a.parts = weight_parts(rows);
+  a.rows = (int)rows;
+  a.cols = (int)(C * K);
+  a.C = (int)C;
+  return dispatch(a, L, bf16, true, st);
+}
+
+}  // namespace eqmp
+
+using namespace eqmp;
+
+extern "C" {
+
+eqmp_status eqmp_layer_norm(const void* x, int64_t x_ld, const void* residual, int64_t residual_ld, eqmp_dtype dtype,
+                            int64_t rows, int64_t cols, eqmp_drop drop, const float* w, const float* b, float eps,
+                            void* s, void* y, float* stats, eqmp_stream_t stream) {
+  return run_forward(Plane{x, x_ld}, Plane{residual, residual_ld}, dtype, rows, cols, 0, drop, w, b, eps, s, y, stats,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+int64_t eqmp_layer_norm_backward_workspace_size(int64_t rows, int64_t cols) {
+  return check_sizes(rows, cols, 1, EQMP_F32) == EQMP_OK ? workspace_bytes(rows, cols, 0) : -1;
+}
+
+eqmp_status eqmp_layer_norm_backward(const void* grad_y, int64_t grad_y_ld, const void* s, int64_t s_ld,
+                                     const void* grad_s, int64_t grad_s_ld, eqmp_dtype dtype, int64_t rows,
+                                     int64_t cols, eqmp_drop drop, const float* w, const float* stats, void* grad_r,
+                                     void* grad_x, float* grad_w, float* grad_b, void* workspace,
+                                     int64_t workspace_bytes, eqmp_stream_t stream) {
+  return run_backward(Plane{grad_y, grad_y_ld}, Plane{s, s_ld}, Plane{grad_s, grad_s_ld}, dtype, rows, cols, 0, drop,
+                      w, stats, grad_r, grad_x, grad_w, grad_b, workspace, workspace_bytes,
+                      reinterpret_cast<cudaStream_t>(stream));
+}
+
+static bool degree_ok(int32_t l_max) { return l_max >= 3 && l_max <= 6; }
+
+// A draw covers a whole channel: dropping single components would turn with
+// the frame.
+static bool whole_channels(const eqmp_drop& d, int32_t l_max) {
+  return d.p == 0.0 || d.group == (l_max + 1) * (l_max + 1);
+}
+
+eqmp_status eqmp_degree_norm(const void* x, const void* residual, eqmp_dtype dtype, int64_t N, int32_t C,
+                             int32_t l_max, eqmp_drop drop, const float* w, const float* b, float eps, void* s,
+                             void* y, float* stats, eqmp_stream_t stream) {
+  if (!degree_ok(l_max)) return EQMP_ERR_UNSUPPORTED;
+  if (!whole_channels(drop, l_max)) return EQMP_ERR_INVALID_ARG;
+  const long long ld = (long long)C * (l_max + 1) * (l_max + 1);
+  return run_forward(Plane{x, ld}, Plane{residual, ld}, dtype, N, C, l_max, drop, w, b, eps, s, y, stats,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+int64_t eqmp_degree_norm_backward_workspace_size(int64_t N, int32_t C, int32_t l_max) {
+  return degree_ok(l_max) && check_sizes(N, C, (l_max + 1) * (l_max + 1), EQMP_F32) == EQMP_OK ? workspace_bytes(N, C, l_max) : -1;
+}
+
+eqmp_status eqmp_degree_norm_backward(const void* grad_y, const void* s, const void* grad_s, eqmp_dtype dtype,
+                                      int64_t N, int32_t C, int32_t l_max, eqmp_drop drop, const float* w,
+                                      const float* stats, void* grad_r, void* grad_x, float* grad_w, float* grad_b,
+                                      void* workspace, int64_t workspace_bytes, eqmp_stream_t stream) {
+  if (!degree_ok(l_max)) return EQMP_ERR_UNSUPPORTED;
+  if (!whole_channels(drop, l_max)) return EQMP_ERR_INVALID_ARG;
+  const long long ld = (long long)C * (l_max + 1) * (l_max + 1);
+  return run_backward(Plane{grad_y, ld}, Plane{s, ld}, Plane{grad_s, ld}, dtype, N, C, l_max, drop, w, stats, grad_r,
+                      grad_x, grad_w, grad_b, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+eqmp_status eqmp_dropout(const void* x, int64_t x_ld, eqmp_dtype dtype, int64_t rows, int64_t cols, eqmp_drop drop,
+                         void* out, eqmp_stream_t stream) {
+  const eqmp_status zs = check_sizes(rows, cols, 1, dtype);
+  if (zs != EQMP_OK) return zs;
+  DropArgs d;
+  const eqmp_status ds = drop_args(drop, cols, &d);
+  if (ds != EQMP_OK) return ds;
+  if (rows == 0) return EQMP_OK;
+  const int bytes = dtype == EQMP_BF16 ? 2 : 4;
+  if (!x || !out || x_ld < 0 || !aligned(x, bytes) || !aligned(out, bytes)) return EQMP_ERR_INVALID_ARG;
+  const bool in_place = x == out && x_ld == cols;  // each element is read before it is written, by one thread
+  if (!in_place && overlap(Plane{x, x_ld}, Plane{out, cols}, rows, cols, bytes)) return EQMP_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  const eqmp_status s = device_info(&dev);
+  if (s != EQMP_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int grid = rows_grid(((long long)rows * cols + kWideThreads - 1) / kWideThreads, dev);
+  if (dtype == EQMP_BF16)
+    k_drop_wide<<<grid, kWideThreads, 0, st>>>(static_cast<const __nv_bfloat16*>(x), x_ld,
+                                               static_cast<__nv_bfloat16*>(out), (int)rows, (int)cols, d);
+  else
+    k_drop_wide<<<grid, kWideThreads, 0, st>>>(static_cast<const float*>(x), x_ld, static_cast<float*>(out),
+                                               (int)rows, (int)cols, d);
+  return cuda_status(cudaGetLastError());
+}
+
+}  // extern "C"

@@ -65,7 +65,7 @@ typedef struct CUstream_st* eqmp_stream_t;
 typedef enum {
   EQMP_OK = 0,
   EQMP_ERR_INVALID_ARG = 1,   /* null pointer, negative size, misalignment, bad enum */
-  EQMP_ERR_UNSUPPORTED = 2,   /* valid but not built: C not in {8,16,32,64,128}, K != 8 */
+  EQMP_ERR_UNSUPPORTED = 2,   /* valid but not built: C not in {8,16,32,64,128}, K != 8, ... */
   EQMP_ERR_CUDA = 3,          /* a CUDA runtime call or launch failed */
   EQMP_ERR_DEVICE_TIMEOUT = 4,/* a bounded device-side wait gave up (see eqmp_device_error) */
   EQMP_ERR_GRAPH = 5          /* eqmp_validate_graph found a violated precondition */
@@ -372,6 +372,128 @@ eqmp_status eqmp_radius_graph_pbc(const float* pos, int64_t N, float cutoff, con
                                   int32_t* row_offsets, int32_t* src, float* vec, int32_t* img,
                                   int32_t* dst, int32_t* rev, int64_t E_cap, int64_t* E_total,
                                   void* workspace, size_t workspace_bytes, eqmp_stream_t stream);
+
+/*
+ * Dropout: the rate and the generator's state of one call, passed by value.
+ * The mask is a function of (seed, offset + *step) and of the element's place
+ * alone: it is never stored, and a backward pass that is given the same
+ * eqmp_drop regenerates it.
+ *   - Row r has cols / group units of `group` consecutive columns.  Unit u is
+ *     drawn from Philox4x32-10 (Salmon et al., SC 2011) with the counter
+ *     (u / 8, r, low half, high half of offset + *step) and the key seed: the
+ *     low 16 bits of word (u % 8) / 2 for even u, the high 16 for odd u.
+ *   - A unit is kept where its draw is >= t = floor(65536 p + 1/2), and kept
+ *     values are multiplied by 65536 / (65536 - t): p is resolved to 1/65536
+ *     and the mean is kept exactly.  A dropped value is 0, whatever it held.
+ *   - p in [0, 1].  p == 0 turns dropout off and the other fields are not
+ *     read.  group >= 1 divides the columns of a row (1: each element by
+ *     itself; (l_max+1)^2: the whole channels of a feature row).
+ *   - step: NULL, or a counter in device memory that is added to offset when
+ *     the kernel runs, so that a recorded CUDA graph draws a new mask on each
+ *     launch after the counter was advanced.  8-byte aligned.
+ */
+typedef struct {
+  double p;
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* step;
+  int32_t group;
+} eqmp_drop;
+
+/*
+ * Conventions shared by the dropout and norm entry points below
+ *   - x, residual, s, y and their gradients are fp32 or bf16 (`dtype`, one
+ *     type for all of them); w, b, stats, grad_w and grad_b are fp32.
+ *     Statistics and sums are fp32; a bf16 result is rounded once, on its
+ *     store.
+ *   - Inputs with a `_ld` argument are rows `_ld` elements apart (any value
+ *     >= 0: cols for packed rows, more for a slice of a wider matrix, 0 for
+ *     one row that stands for all).  Everything else is packed.  No alignment
+ *     beyond the element's own is needed; 16-byte aligned rows are faster.
+ *   - Up to 2^30 rows of up to 2^30 values (EQMP_ERR_UNSUPPORTED above).
+ *     rows == 0 launches no kernel; the sums over rows are then 0.
+ *   - Outputs may be NULL to skip them, and must not overlap the inputs or
+ *     one another (EQMP_ERR_INVALID_ARG), but for eqmp_dropout in place.
+ *   - Results are bitwise reproducible on one device: every sum has a fixed
+ *     order, and nothing is added by atomics.
+ *   - A NaN or an infinity in a row makes that row's y NaN, as the formula
+ *     does; other rows are not touched.
+ */
+
+/*
+ * out = dropout(x) on rows of cols values.  The backward pass is the same call
+ * on the gradient.  Features [N][C][K] are N rows of C*K columns.  out may be
+ * x itself when x_ld == cols.
+ */
+eqmp_status eqmp_dropout(const void* x, int64_t x_ld, eqmp_dtype dtype, int64_t rows, int64_t cols, eqmp_drop drop,
+                         void* out, eqmp_stream_t stream);
+
+/*
+ * Layer norm of rows of cols values, behind an optional dropout and residual
+ * sum, in one pass:
+ *   s = residual + dropout(x)               (residual NULL: 0; drop.p 0: none)
+ *   y = (s - mean) rstd w + b,  rstd = 1 / sqrt(mean((s - mean)^2) + eps)
+ *   w, b   [cols], NULL: 1 and 0
+ *   eps    >= 0, finite
+ *   s, y   [rows][cols], written.  y is formed from the unrounded s.
+ *   stats  [rows][2], written: mean and rstd, for the backward pass
+ */
+eqmp_status eqmp_layer_norm(const void* x, int64_t x_ld, const void* residual, int64_t residual_ld, eqmp_dtype dtype,
+                            int64_t rows, int64_t cols, eqmp_drop drop, const float* w, const float* b, float eps,
+                            void* s, void* y, float* stats, eqmp_stream_t stream);
+
+/*
+ * Gradients of eqmp_layer_norm.  Given grad_y = dL/dy, the s and stats of the
+ * forward pass (x in place of s when there was neither a residual nor
+ * dropout), and grad_s = dL/ds from other uses of s (NULL: none), with
+ * h = (s - mean) rstd and a = grad_y w:
+ *   grad_r  [rows][cols]  grad_s + rstd (a - mean(a) - h mean(a h)): dL/ds in all,
+ *                         which is dL/d(residual)
+ *   grad_x  [rows][cols]  grad_r through the dropout
+ *   grad_w  [cols]        sum over rows of grad_y h
+ *   grad_b  [cols]        sum over rows of grad_y
+ * `drop` is the forward call's.  workspace: device memory of at least
+ * eqmp_layer_norm_backward_workspace_size(rows, cols) bytes, 16-byte aligned
+ * (needed for grad_w and grad_b only; -1 for sizes that are not supported);
+ * its contents on entry are ignored.
+ */
+int64_t eqmp_layer_norm_backward_workspace_size(int64_t rows, int64_t cols);
+
+eqmp_status eqmp_layer_norm_backward(const void* grad_y, int64_t grad_y_ld, const void* s, int64_t s_ld,
+                                     const void* grad_s, int64_t grad_s_ld, eqmp_dtype dtype, int64_t rows,
+                                     int64_t cols, eqmp_drop drop, const float* w, const float* stats, void* grad_r,
+                                     void* grad_x, float* grad_w, float* grad_b, void* workspace,
+                                     int64_t workspace_bytes, eqmp_stream_t stream);
+
+/*
+ * The layer norm by degree of node features [N][C][(l_max+1)^2], l_max 3..6
+ * (EQMP_ERR_UNSUPPORTED otherwise), which commutes with rotations where a
+ * plain layer norm over the row does not:
+ *   s = residual + dropout(x)
+ *   l = 0:  h = (s - mean) rstd_0, the mean and the variance over the channels
+ *   l > 0:  h = s rstd_l,  rstd_l = 1 / sqrt(mean of s^2 over channels and orders + eps)
+ *   y = h w[l][c]  (+ b[c] for l = 0)
+ *   w      [l_max+1][C], b [C]; NULL: 1 and 0
+ *   drop   group must be (l_max+1)^2 (whole channels), else EQMP_ERR_INVALID_ARG
+ *   stats  [N][l_max+2], written: the mean of degree 0, then rstd_0 .. rstd_l_max
+ * All arrays are packed; other arguments as eqmp_layer_norm.
+ */
+eqmp_status eqmp_degree_norm(const void* x, const void* residual, eqmp_dtype dtype, int64_t N, int32_t C,
+                             int32_t l_max, eqmp_drop drop, const float* w, const float* b, float eps, void* s,
+                             void* y, float* stats, eqmp_stream_t stream);
+
+/*
+ * Gradients of eqmp_degree_norm; arguments and workspace rule as
+ * eqmp_layer_norm_backward, with the means of a h taken over each degree:
+ *   grad_w [l_max+1][C]  sum over rows and orders of grad_y h
+ *   grad_b [C]           sum over rows of grad_y's degree 0
+ */
+int64_t eqmp_degree_norm_backward_workspace_size(int64_t N, int32_t C, int32_t l_max);
+
+eqmp_status eqmp_degree_norm_backward(const void* grad_y, const void* s, const void* grad_s, eqmp_dtype dtype,
+                                      int64_t N, int32_t C, int32_t l_max, eqmp_drop drop, const float* w,
+                                      const float* stats, void* grad_r, void* grad_x, float* grad_w, float* grad_b,
+                                      void* workspace, int64_t workspace_bytes, eqmp_stream_t stream);
 
 /*
  * Synchronous check of the graph preconditions on device data:
