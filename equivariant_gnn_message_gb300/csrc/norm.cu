@@ -4,6 +4,7 @@
 
 #include "launch.h"
 #include "norm.cuh"
+#include "norm_rows.cuh"
 
 namespace eqmp {
 
@@ -91,6 +92,11 @@ static eqmp_status dispatch(const NormArgs& a, int L, bool bf16, bool backward, 
   DeviceInfo dev;
   const eqmp_status s = device_info(&dev);
   if (s != EQMP_OK) return s;
+  if (!backward) {
+    bool done = false;
+    const eqmp_status rs = bf16 ? launch_norm_rows_bf16(a, L, dev, st, &done) : launch_norm_rows_f32(a, L, dev, st, &done);
+    if (rs != EQMP_OK || done) return rs;
+  }
   switch (L) {
     case 0: return dispatch_t<0>(a, bf16, backward, dev, st);
     case 3: return dispatch_t<3>(a, bf16, backward, dev, st);
