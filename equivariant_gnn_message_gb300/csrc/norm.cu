@@ -61,6 +61,12 @@ static int rows_grid(long long rows, const DeviceInfo& dev) {
   return (int)(rows < cap ? rows : cap);
 }
 
+eqmp_status launch_norm_bwd_sum(const NormArgs& a, int L, cudaStream_t st) {
+  const long long M = (long long)(L + 2) * a.C;
+  k_norm_bwd_sum<<<(unsigned)((M + kSumX - 1) / kSumX), dim3(kSumX, kSumY), 0, st>>>(a, L);
+  return cuda_status(cudaGetLastError());
+}
+
 template <typename T, int L>
 static eqmp_status forward_t(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   k_norm_wide<T, L><<<rows_grid(a.rows, dev), kWideThreads, 0, st>>>(a);
@@ -74,12 +80,10 @@ static eqmp_status backward_t(const NormArgs& a, const DeviceInfo& dev, cudaStre
     if (cudaGetLastError() != cudaSuccess) return EQMP_ERR_CUDA;
   }
   if (!a.gw && !a.gb) return EQMP_OK;
-  const long long M = (long long)(L + 2) * a.C;
   const dim3 grid((unsigned)((a.C + kWideSumX - 1) / kWideSumX), (unsigned)a.parts);
   k_norm_bwd_wide_w<T, L><<<grid, dim3(kWideSumX, kWideSumY), 0, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return EQMP_ERR_CUDA;
-  k_norm_bwd_sum<L><<<(unsigned)((M + kSumX - 1) / kSumX), dim3(kSumX, kSumY), 0, st>>>(a);
-  return cuda_status(cudaGetLastError());
+  return launch_norm_bwd_sum(a, L, st);
 }
 
 template <int L>
@@ -92,11 +96,11 @@ static eqmp_status dispatch(const NormArgs& a, int L, bool bf16, bool backward, 
   DeviceInfo dev;
   const eqmp_status s = device_info(&dev);
   if (s != EQMP_OK) return s;
-  if (!backward) {
-    bool done = false;
-    const eqmp_status rs = bf16 ? launch_norm_rows_bf16(a, L, dev, st, &done) : launch_norm_rows_f32(a, L, dev, st, &done);
-    if (rs != EQMP_OK || done) return rs;
-  }
+  bool done = false;
+  const auto rows = backward ? (bf16 ? launch_norm_bwd_rows_bf16 : launch_norm_bwd_rows_f32)
+                             : (bf16 ? launch_norm_rows_bf16 : launch_norm_rows_f32);
+  const eqmp_status rs = rows(a, L, dev, st, &done);
+  if (rs != EQMP_OK || done) return rs;
   switch (L) {
     case 0: return dispatch_t<0>(a, bf16, backward, dev, st);
     case 3: return dispatch_t<3>(a, bf16, backward, dev, st);
@@ -107,15 +111,17 @@ static eqmp_status dispatch(const NormArgs& a, int L, bool bf16, bool backward, 
   return EQMP_ERR_UNSUPPORTED;
 }
 
-// Row ranges of the partial weight gradients: enough to fill the device, at
-// least 64 rows each, so that the partials stay a small part of the traffic.
-static int weight_parts(long long rows) {
+// Row ranges of the partial weight gradients in the kernels for any shape:
+// enough to fill the device, at least 64 rows each, so that the partials stay
+// a small part of the traffic.
+static int wide_parts(long long rows) {
   const long long want = (rows + 63) / 64;
   return (int)(want < 1 ? 1 : want > 128 ? 128 : want);
 }
 
+// At most one part a row, at most kMaxParts.
 static int64_t workspace_bytes(int64_t rows, int64_t C, int L) {
-  return (int64_t)weight_parts(rows) * (L + 2) * C * 4;
+  return (rows < kMaxParts ? rows : kMaxParts) * (L + 2) * C * 4;
 }
 
 // Up to 2^30 rows of up to 2^30 values, so that a row or column index plus a
@@ -193,7 +199,7 @@ static eqmp_status run_backward(Plane g, Plane x, Plane r, eqmp_dtype dtype, int
   a.stats = const_cast<float*>(stats);
   a.w = w;
   a.part = static_cast<float*>(workspace);
-  a.parts = weight_parts(rows);
+  a.parts = wide_parts(rows);
   a.rows = (int)rows;
   a.cols = (int)(C * K);
   a.C = (int)C;

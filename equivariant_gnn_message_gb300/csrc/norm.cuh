@@ -282,16 +282,19 @@ __global__ void __launch_bounds__(kWideSumX * kWideSumY) k_norm_bwd_wide_w(NormA
   }
 }
 
-// dw and db: the parts' sums in their order.
-constexpr int kSumX = 32, kSumY = 8;
+// dw and db: the parts' sums.  Thread (x, y) adds the parts y, y + kSumY, ...
+// of column x, then the rows of the block are added in their order.
+constexpr int kSumX = 16, kSumY = 32;
+constexpr int kMaxParts = 608;  // four CTAs on each of 152 SMs
 
-template <int L>
-__global__ void __launch_bounds__(kSumX * kSumY) k_norm_bwd_sum(NormArgs a) {
+static __global__ void __launch_bounds__(kSumX * kSumY) k_norm_bwd_sum(NormArgs a, int L) {
   __shared__ float red[kSumY][kSumX];
   const long long M = (long long)(L + 2) * a.C, m = (long long)blockIdx.x * kSumX + threadIdx.x;
   float t = 0.0f;
-  if (m < M)
+  if (m < M) {
+#pragma unroll 8
     for (int p = threadIdx.y; p < a.parts; p += kSumY) t += a.part[p * M + m];
+  }
   red[threadIdx.y][threadIdx.x] = t;
   __syncthreads();
   if (threadIdx.y || m >= M) return;

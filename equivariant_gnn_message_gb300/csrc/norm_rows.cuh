@@ -324,6 +324,194 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
   }
 }
 
+// ---------------------------------------------------------------- backward
+// One pass over g and s (and dL/ds): the row's sums of a and a h, then dL/ds
+// and dL/dx from the registers, while each lane adds g h and g of its columns
+// over all the rows of its group.  At the end the groups of a CTA are added in
+// their order through shared memory, the orders of a degree with them, and
+// the CTA's (L+2) C sums go to its part of the workspace.  FUSED: with dL/ds
+// of a residual stream, dropout, or both gradients asked for.
+template <typename T, int L, int V, int NV, bool FUSED>
+__global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, RowShape sh) {
+  __shared__ float red[2 * (kMaxRowThreads / 32) * (L + 2)];
+  extern __shared__ float colsum[];  // [cols] g h, then [C] g
+  const Slots<L, V, NV> at(sh);
+  GroupSum<L + 2> sum(sh.lanes, red);
+  const Dropper drop(a.drop);
+  const T* x = static_cast<const T*>(a.x);
+  const T* g = static_cast<const T*>(a.g);
+  const T* r = static_cast<const T*>(a.r);
+  constexpr int NB = L ? 1 : V;  // degree-0 values of a vector, at most
+  constexpr int NQ = L ? V : 1;  // deviations of a lane's slots
+  bool has[NV];
+  float w[NV][V], dw[NV][V], db[NV][NB];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    has[j] = at.lane < sh.active && at.col(j) < a.cols;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (at.col(j) + i) / at.K, l = L ? at.cls[L ? i : 0] : 0;
+      w[j][i] = has[j] && a.w ? a.w[l * a.C + c] : 1.0f;
+      dw[j][i] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) db[j][i] = 0.0f;
+  }
+  const float inv = 1.0f / (float)a.C;
+  const int stride = gridDim.x * sh.groups;
+  Pack<T, V> nx[NV], ng[NV], nr[FUSED ? NV : 1];
+  float nmean, nq[NQ];
+  auto fetch = [&](int row) {
+    const bool live = row < a.rows;
+    const float* st = a.stats + (long long)row * (L + 2);
+    nmean = live ? st[0] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) nq[i] = live ? st[1 + (L ? at.cls[L ? i : 0] : 0)] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (has[j] && live) {
+        nx[j].load(x + (long long)row * a.x_ld + at.col(j));
+        ng[j].load(g + (long long)row * a.g_ld + at.col(j));
+      } else {
+        nx[j].zero();
+        ng[j].zero();
+      }
+      if (FUSED) {
+        if (has[j] && live && r)
+          nr[FUSED ? j : 0].load(r + (long long)row * a.r_ld + at.col(j));
+        else
+          nr[FUSED ? j : 0].zero();
+      }
+    }
+  };
+  int row = blockIdx.x * sh.groups + threadIdx.x / sh.lanes;
+  fetch(row);
+  for (int base = blockIdx.x * sh.groups; base < a.rows; base += stride, row += stride) {
+    float h[NV][V], av[NV][V], slot[V], tot[L + 2], q[NQ];
+    Pack<T, V> cr[FUSED ? NV : 1];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) q[i] = nq[i];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      nx[j].get(h[j]);
+      ng[j].get(av[j]);
+      if (FUSED) cr[FUSED ? j : 0] = nr[FUSED ? j : 0];
+    }
+    const float mean = nmean;
+    fetch(row + stride);
+    tot[0] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const bool first = at.is0(i);
+      const float mu = first ? mean : 0.0f, qi = q[L ? i : 0];
+      slot[i] = 0.0f;
+      float sa = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        h[j][i] = (h[j][i] - mu) * qi;
+        dw[j][i] += av[j][i] * h[j][i];
+        if (L == 0)
+          db[j][L ? 0 : i] += av[j][i];
+        else
+          db[j][0] += first ? av[j][i] : 0.0f;
+        av[j][i] *= w[j][i];
+        sa += av[j][i];
+        slot[i] += av[j][i] * h[j][i];
+      }
+      tot[0] += first ? sa : 0.0f;
+    }
+    float deg[L + 1];
+    at.by_degree(slot, deg);
+#pragma unroll
+    for (int l = 0; l <= L; ++l) tot[1 + l] = deg[l];
+    sum(tot);
+    if (row >= a.rows) continue;
+    const float m0 = tot[0] * inv;
+#pragma unroll
+    for (int l = 0; l <= L; ++l) deg[l] = tot[1 + l] * (inv * (1.0f / (2 * l + 1)));
+    at.to_slots(deg, slot);
+    const long long out = (long long)row * a.cols;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float f[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        f[i] = (av[j][i] - h[j][i] * slot[i] - (at.is0(i) ? m0 : 0.0f)) * q[L ? i : 0];
+      if (FUSED) {
+        float s[V];
+        cr[FUSED ? j : 0].get(s);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] += s[i];
+        if (a.gr && has[j]) Pack<T, V>::store(static_cast<T*>(a.gr) + out + at.col(j), f);
+        if (a.gx) {
+          if (drop.threshold) drop_values<V>(drop, f, row, at.col(j));
+          if (has[j]) Pack<T, V>::store(static_cast<T*>(a.gx) + out + at.col(j), f);
+        }
+      } else if (has[j]) {
+        T* dst = static_cast<T*>(a.gx ? a.gx : a.gr);
+        if (dst) Pack<T, V>::store(dst + out + at.col(j), f);
+      }
+    }
+  }
+  if (!a.gw && !a.gb) return;
+  // the CTA's sums: the groups of a warp by shuffles, the warps (or the
+  // groups of several warps) in turn
+  if (sh.lanes < 32) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      if (o >= sh.lanes) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) dw[j][i] += __shfl_xor_sync(0xffffffffu, dw[j][i], o);
+#pragma unroll
+          for (int i = 0; i < NB; ++i) db[j][i] += __shfl_xor_sync(0xffffffffu, db[j][i], o);
+        }
+      }
+    }
+  }
+  const int unit = sh.lanes <= 32 ? 32 : sh.lanes;  // threads that add together
+  const int units = (blockDim.x + unit - 1) / unit, mine = threadIdx.x / unit;
+  const bool speaks = (int)(threadIdx.x % unit) < sh.lanes;
+  for (int u = 0; u < units; ++u) {
+    if (u == mine && speaks) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (!has[j]) continue;
+        const int col = at.col(j);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          colsum[col + i] = u ? colsum[col + i] + dw[j][i] : dw[j][i];
+          if (at.is0(i)) {
+            float* d = colsum + a.cols + (col + i) / at.K;
+            const float v = db[j][L ? 0 : i];
+            *d = u ? *d + v : v;
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+  const int M = (L + 2) * a.C, nw = (L + 1) * a.C;
+  float* part = a.parts > 1 ? a.part + (long long)blockIdx.x * M : nullptr;
+  for (int m = threadIdx.x; m < M; m += blockDim.x) {
+    float t = 0.0f;
+    if (L && m < nw) {
+      const int l = m / a.C, c = m - l * a.C;
+      for (int k = l * l; k < (l + 1) * (l + 1); ++k) t += colsum[c * at.K + k];
+    } else {
+      t = colsum[L ? a.cols + m - nw : m];
+    }
+    if (part)
+      part[m] = t;
+    else if (m < nw) {
+      if (a.gw) a.gw[m] = t;
+    } else if (a.gb) {
+      a.gb[m - nw] = t;
+    }
+  }
+}
+
 // ---------------------------------------------------------------- launch
 // Lanes for a row of cols values in vectors of V, NV per lane.
 inline RowShape row_shape(int cols, int K, int V, int NV) {
@@ -342,6 +530,11 @@ inline RowShape row_shape(int cols, int K, int V, int NV) {
   return sh;
 }
 
+constexpr int kMaxColSum = 2 * 16 * kMaxRowThreads * 4;  // bytes of the column sums of the widest row
+
+// dw and db from the parts (norm.cu).
+eqmp_status launch_norm_bwd_sum(const NormArgs& a, int L, cudaStream_t st);
+
 // CTAs of a persistent launch: what the device holds at a time, at most one
 // per group of rows.
 template <typename Kernel>
@@ -359,7 +552,7 @@ inline int resident_grid(Kernel kernel, int threads, size_t smem, const DeviceIn
 }
 
 template <typename T, int L, int V, int NV, bool FUSED>
-static eqmp_status launch_rows(const NormArgs& a, const RowShape& sh, const DeviceInfo& dev, cudaStream_t st) {
+static eqmp_status launch_fwd(const NormArgs& a, const RowShape& sh, const DeviceInfo& dev, cudaStream_t st) {
   static int cache[64][33];
   const int threads = sh.lanes * sh.groups;
   auto kern = k_norm_rows<T, L, V, NV, FUSED>;
@@ -369,48 +562,79 @@ static eqmp_status launch_rows(const NormArgs& a, const RowShape& sh, const Devi
   return cuda_status(cudaGetLastError());
 }
 
-// 8 or 16 values a lane, whichever leaves fewer places empty; 8 where both
-// are equal and the row fits a warp (fewer registers, more rows in flight).
-template <typename T, int L, int V>
+template <typename T, int L, int V, int NV, bool FUSED>
+static eqmp_status launch_bwd(NormArgs a, const RowShape& sh, const DeviceInfo& dev, cudaStream_t st) {
+  static int cache[64][33];
+  const int threads = sh.lanes * sh.groups;
+  const size_t smem = a.gw || a.gb ? sizeof(float) * ((size_t)a.cols + a.C) : 0;
+  auto kern = k_norm_bwd_rows<T, L, V, NV, FUSED>;
+  static unsigned long long attr_done = 0;
+  if (ensure_smem_attr(kern, kMaxColSum, &attr_done) != cudaSuccess) return EQMP_ERR_CUDA;
+  int grid = resident_grid(kern, threads, smem, dev, ((long long)a.rows + sh.groups - 1) / sh.groups, cache);
+  if (grid < 1) return EQMP_ERR_CUDA;
+  if (grid > kMaxParts) grid = kMaxParts;
+  a.parts = grid;
+  kern<<<grid, threads, smem, st>>>(a, sh);
+  if (cudaGetLastError() != cudaSuccess) return EQMP_ERR_CUDA;
+  if ((!a.gw && !a.gb) || grid == 1) return EQMP_OK;
+  return launch_norm_bwd_sum(a, L, st);
+}
+
+template <typename T, int L, int V, int NV, bool BACKWARD>
+static eqmp_status launch_rows(const NormArgs& a, const RowShape& sh, const DeviceInfo& dev, cudaStream_t st) {
+  if constexpr (BACKWARD) {
+    const bool fused = a.r || a.drop.threshold || (a.gr && a.gx);
+    return fused ? launch_bwd<T, L, V, NV, true>(a, sh, dev, st) : launch_bwd<T, L, V, NV, false>(a, sh, dev, st);
+  } else {
+    const bool fused = a.r || a.drop.threshold || a.s;
+    return fused ? launch_fwd<T, L, V, NV, true>(a, sh, dev, st) : launch_fwd<T, L, V, NV, false>(a, sh, dev, st);
+  }
+}
+
+// 8 or 16 values a lane.  Forward: whichever leaves fewer places empty; 8
+// where both are equal and the row fits a warp (fewer registers, more rows in
+// flight).  Backward: 8 where the row fits, since 16 values of every array do
+// not fit 128 registers.
+template <typename T, int L, int V, bool BACKWARD>
 static eqmp_status launch_rows_v(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st, bool* done) {
   constexpr int K = (L + 1) * (L + 1), N8 = 8 / V, N16 = 16 / V;
   const RowShape s8 = row_shape(a.cols, K, V, N8), s16 = row_shape(a.cols, K, V, N16);
-  const bool fused = a.r || a.drop.threshold || a.s;
-  const bool take8 = s8.lanes <= kMaxRowThreads && (s8.lanes * N8 < s16.lanes * N16 || (s8.lanes * N8 == s16.lanes * N16 && s8.lanes <= 32));
+  const int p8 = s8.lanes * N8, p16 = s16.lanes * N16;
+  const bool take8 = s8.lanes <= kMaxRowThreads && (BACKWARD || p8 < p16 || (p8 == p16 && s8.lanes <= 32));
   *done = take8 || s16.lanes <= kMaxRowThreads;
   if (!*done) return EQMP_OK;
-  if (take8)
-    return fused ? launch_rows<T, L, V, N8, true>(a, s8, dev, st) : launch_rows<T, L, V, N8, false>(a, s8, dev, st);
-  return fused ? launch_rows<T, L, V, N16, true>(a, s16, dev, st) : launch_rows<T, L, V, N16, false>(a, s16, dev, st);
+  return take8 ? launch_rows<T, L, V, N8, BACKWARD>(a, s8, dev, st) : launch_rows<T, L, V, N16, BACKWARD>(a, s16, dev, st);
 }
 
 inline bool vec16(const void* p, long long ld, int bytes) {
   return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * bytes % 16 == 0);
 }
 
-// Runs the forward pass if the row fits; *done says whether it did.  Vectors
-// of 16 bytes where every row of every array starts on one.
-template <typename T, int L>
+// Runs the pass if the row fits; *done says whether it did.  Vectors of 16
+// bytes where every row of every array starts on one.
+template <typename T, int L, bool BACKWARD>
 static eqmp_status launch_rows_l(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st, bool* done) {
   constexpr int B = sizeof(T);
-  const bool vec = vec16(a.x, a.x_ld, B) && vec16(a.r, a.r_ld, B) && vec16(a.s, a.cols, B) && vec16(a.y, a.cols, B) &&
-                   a.cols * B % 16 == 0;
-  return vec ? launch_rows_v<T, L, 16 / B>(a, dev, st, done) : launch_rows_v<T, L, 1>(a, dev, st, done);
+  const bool vec = vec16(a.x, a.x_ld, B) && vec16(a.r, a.r_ld, B) && vec16(a.g, a.g_ld, B) && vec16(a.s, a.cols, B) &&
+                   vec16(a.y, a.cols, B) && vec16(a.gr, a.cols, B) && vec16(a.gx, a.cols, B) && a.cols * B % 16 == 0;
+  return vec ? launch_rows_v<T, L, 16 / B, BACKWARD>(a, dev, st, done) : launch_rows_v<T, L, 1, BACKWARD>(a, dev, st, done);
 }
 
-template <typename T>
+template <typename T, bool BACKWARD>
 static eqmp_status launch_rows_t(const NormArgs& a, int L, const DeviceInfo& dev, cudaStream_t st, bool* done) {
   switch (L) {
-    case 0: return launch_rows_l<T, 0>(a, dev, st, done);
-    case 3: return launch_rows_l<T, 3>(a, dev, st, done);
-    case 4: return launch_rows_l<T, 4>(a, dev, st, done);
-    case 5: return launch_rows_l<T, 5>(a, dev, st, done);
-    case 6: return launch_rows_l<T, 6>(a, dev, st, done);
+    case 0: return launch_rows_l<T, 0, BACKWARD>(a, dev, st, done);
+    case 3: return launch_rows_l<T, 3, BACKWARD>(a, dev, st, done);
+    case 4: return launch_rows_l<T, 4, BACKWARD>(a, dev, st, done);
+    case 5: return launch_rows_l<T, 5, BACKWARD>(a, dev, st, done);
+    case 6: return launch_rows_l<T, 6, BACKWARD>(a, dev, st, done);
   }
   return EQMP_ERR_UNSUPPORTED;
 }
 
 eqmp_status launch_norm_rows_f32(const NormArgs& a, int L, const DeviceInfo& dev, cudaStream_t st, bool* done);
 eqmp_status launch_norm_rows_bf16(const NormArgs& a, int L, const DeviceInfo& dev, cudaStream_t st, bool* done);
+eqmp_status launch_norm_bwd_rows_f32(const NormArgs& a, int L, const DeviceInfo& dev, cudaStream_t st, bool* done);
+eqmp_status launch_norm_bwd_rows_bf16(const NormArgs& a, int L, const DeviceInfo& dev, cudaStream_t st, bool* done);
 
 }  // namespace eqmp
