@@ -206,6 +206,58 @@ static eqmp_status run_backward(Plane g, Plane x, Plane r, eqmp_dtype dtype, int
   return dispatch(a, L, bf16, true, st);
 }
 
+// ---------------------------------------------------------------- dropout
+// A CTA takes a tile of kDropTile * kDropThreads vectors, counted along the
+// rows; a thread loads its kDropTile vectors before it draws for them.  The
+// tile's first row is one 64-bit division, the vectors' rows are 32-bit ones.
+constexpr int kDropThreads = 256, kDropTile = 4;
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kDropThreads) k_drop(const T* x, long long ld, T* out, int rows, int cols,
+                                                       DropArgs d) {
+  const Dropper drop(d);
+  const uint32_t per_row = cols / V;  // vectors
+  const long long first = (long long)blockIdx.x * (kDropTile * kDropThreads);
+  const int row0 = (int)(first / per_row);
+  const uint32_t v0 = (uint32_t)(first - (long long)row0 * per_row) + threadIdx.x;
+  Pack<T, V> in[kDropTile];
+  int row[kDropTile], col[kDropTile];
+#pragma unroll
+  for (int k = 0; k < kDropTile; ++k) {
+    const uint32_t v = v0 + k * kDropThreads, r = v / per_row;
+    row[k] = row0 + (int)r;
+    col[k] = (int)(v - r * per_row) * V;
+    if (row[k] < rows) in[k].load(x + row[k] * ld + col[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kDropTile; ++k) {
+    if (row[k] >= rows) break;
+    float f[V];
+    in[k].get(f);
+    if (drop.threshold) drop_values<V>(drop, f, row[k], col[k]);
+    Pack<T, V>::store(out + (long long)row[k] * cols + col[k], f);
+  }
+}
+
+template <typename T, int V>
+static eqmp_status launch_drop(const T* x, long long ld, T* out, int rows, int cols, const DropArgs& d, cudaStream_t st) {
+  const long long vectors = (long long)rows * (cols / V), tile = kDropTile * kDropThreads;
+  const long long grid = (vectors + tile - 1) / tile;
+  if (grid > INT32_MAX) return EQMP_ERR_UNSUPPORTED;
+  k_drop<T, V><<<(unsigned)grid, kDropThreads, 0, st>>>(x, ld, out, rows, cols, d);
+  return cuda_status(cudaGetLastError());
+}
+
+template <typename T>
+static eqmp_status run_dropout(const void* x, long long ld, void* out, int rows, int cols, const DropArgs& d,
+                               cudaStream_t st) {
+  constexpr int B = sizeof(T);
+  const T* in = static_cast<const T*>(x);
+  T* to = static_cast<T*>(out);
+  const bool vec = vec16(x, ld, B) && vec16(out, cols, B) && cols * (long long)B % 16 == 0;
+  return vec ? launch_drop<T, 16 / B>(in, ld, to, rows, cols, d, st) : launch_drop<T, 1>(in, ld, to, rows, cols, d, st);
+}
+
 }  // namespace eqmp
 
 using namespace eqmp;
@@ -278,18 +330,9 @@ eqmp_status eqmp_dropout(const void* x, int64_t x_ld, eqmp_dtype dtype, int64_t 
   if (!x || !out || x_ld < 0 || !aligned(x, bytes) || !aligned(out, bytes)) return EQMP_ERR_INVALID_ARG;
   const bool in_place = x == out && x_ld == cols;  // each element is read before it is written, by one thread
   if (!in_place && overlap(Plane{x, x_ld}, Plane{out, cols}, rows, cols, bytes)) return EQMP_ERR_INVALID_ARG;
-  DeviceInfo dev;
-  const eqmp_status s = device_info(&dev);
-  if (s != EQMP_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int grid = rows_grid(((long long)rows * cols + kWideThreads - 1) / kWideThreads, dev);
-  if (dtype == EQMP_BF16)
-    k_drop_wide<<<grid, kWideThreads, 0, st>>>(static_cast<const __nv_bfloat16*>(x), x_ld,
-                                               static_cast<__nv_bfloat16*>(out), (int)rows, (int)cols, d);
-  else
-    k_drop_wide<<<grid, kWideThreads, 0, st>>>(static_cast<const float*>(x), x_ld, static_cast<float*>(out),
-                                               (int)rows, (int)cols, d);
-  return cuda_status(cudaGetLastError());
+  return dtype == EQMP_BF16 ? run_dropout<__nv_bfloat16>(x, x_ld, out, (int)rows, (int)cols, d, st)
+                            : run_dropout<float>(x, x_ld, out, (int)rows, (int)cols, d, st);
 }
 
 }  // extern "C"

@@ -308,17 +308,4 @@ static __global__ void __launch_bounds__(kSumX * kSumY) k_norm_bwd_sum(NormArgs 
   }
 }
 
-// Elementwise, any shape: one thread per element of a row.
-template <typename T>
-__global__ void __launch_bounds__(kWideThreads) k_drop_wide(const T* x, long long ld, T* out, int rows, int cols,
-                                                            DropArgs d) {
-  const Dropper drop(d);
-  const long long n = (long long)rows * cols, stride = (long long)gridDim.x * blockDim.x;
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride) {
-    const int row = (int)(i / cols), col = (int)(i - (long long)row * cols);
-    const float v = load1(x + row * ld + col);
-    store1(out + i, drop.threshold ? drop.apply(v, row, col) : v);
-  }
-}
-
 }  // namespace eqmp
