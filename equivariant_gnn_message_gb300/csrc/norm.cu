@@ -232,10 +232,23 @@ __global__ void __launch_bounds__(kDropThreads) k_drop(const T* x, long long ld,
 #pragma unroll
   for (int k = 0; k < kDropTile; ++k) {
     if (row[k] >= rows) break;
-    float f[V];
-    in[k].get(f);
-    if (drop.threshold) drop_values<V>(drop, f, row[k], col[k]);
-    Pack<T, V>::store(out + (long long)row[k] * cols + col[k], f);
+    T* to = out + (long long)row[k] * cols + col[k];
+    if constexpr (V == 1) {
+      const float f = load1(&in[k].v);
+      store1(to, drop.on ? drop.apply(f, row[k], col[k]) : f);
+    } else {
+      float2 f[V / 2];
+      in[k].get(f);
+      if (drop.on) {
+        const uint32_t keep = drop.keep_bits(row[k], col[k], V);
+#pragma unroll
+        for (int s = 0; s < V / 2; ++s) {
+          f[s].x = keep >> (2 * s) & 1 ? f[s].x * drop.scale : 0.0f;
+          f[s].y = keep >> (2 * s + 1) & 1 ? f[s].y * drop.scale : 0.0f;
+        }
+      }
+      Pack<T, V>::store(to, f);
+    }
   }
 }
 

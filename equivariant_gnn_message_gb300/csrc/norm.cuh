@@ -52,31 +52,59 @@ struct DropArgs {
 };
 
 // The draws of one call: unit u of row r is word (u%8)/2 of block u/8, its
-// low half for even u.
+// low half for even u.  A half h of a word is compared in the upper half of a
+// register, with what lies below it left standing: h >= t is
+// (h, anything) > (t, 0) - 1, and t = 65536 gives a bound that nothing passes.
 struct Dropper {
-  uint32_t k0, k1, o0, o1, threshold;
+  uint32_t k0, k1, o0, o1, bound;
   float scale;
   int group;
+  bool on;
   __device__ __forceinline__ explicit Dropper(const DropArgs& d) {
+    on = d.threshold > 0;
     const unsigned long long off = d.offset + (d.step ? *d.step : 0ull);
     k0 = (uint32_t)d.seed;
     k1 = (uint32_t)(d.seed >> 32);
     o0 = (uint32_t)off;
     o1 = (uint32_t)(off >> 32);
-    threshold = d.threshold;
+    bound = (uint32_t)(((unsigned long long)d.threshold << 16) - 1);
     scale = d.scale;
     group = d.group;
   }
   __device__ __forceinline__ uint4 block(uint32_t row, uint32_t blk) const { return philox(blk, row, o0, o1, k0, k1); }
-  __device__ __forceinline__ static uint32_t draw(const uint4& w, uint32_t unit) {
+  __device__ __forceinline__ bool keeps(const uint4& w, uint32_t unit) const {
     const uint32_t a = (unit & 4) ? w.z : w.x, b = (unit & 4) ? w.w : w.y;
     const uint32_t v = (unit & 2) ? b : a;
-    return (unit & 1) ? v >> 16 : v & 0xffffu;
+    return ((unit & 1) ? v : v << 16) > bound;
   }
   // A dropped value is 0 whatever it held, a NaN or an infinity included.
   __device__ __forceinline__ float apply(float v, uint32_t row, int col) const {
     const uint32_t unit = (uint32_t)col / (uint32_t)group;
-    return draw(block(row, unit >> 3), unit) >= threshold ? v * scale : 0.0f;
+    return keeps(block(row, unit >> 3), unit) ? v * scale : 0.0f;
+  }
+  // Bit i: column col + i of the row is kept, i < n <= 8; col is a multiple
+  // of n, or n is 8 and col a multiple of 8.
+  __device__ __forceinline__ uint32_t keep_bits(uint32_t row, int col, int n) const {
+    uint32_t keep = 0;
+    if (group == 1) {
+      const uint4 w = block(row, (uint32_t)col >> 3);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) keep |= (uint32_t)keeps(w, i) << i;
+      return (keep >> (col & 7)) & ((1u << n) - 1);
+    }
+    // the units that the columns touch, one after the other
+    uint32_t unit = (uint32_t)col / (uint32_t)group, blk = unit >> 3;
+    int end = (int)((unit + 1) * (uint32_t)group) - col;  // of the unit, counted from col
+    uint4 w = block(row, blk);
+#pragma unroll 1
+    for (int from = 0;;) {
+      if (keeps(w, unit)) keep |= (end >= n ? 1u << n : 1u << end) - (1u << from);
+      if (end >= n) return keep;
+      from = end;
+      end += group;
+      ++unit;
+      if (unit >> 3 != blk) w = block(row, blk = unit >> 3);
+    }
   }
 };
 
@@ -147,7 +175,7 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_wide(NormArgs a) {
   constexpr int K = (L + 1) * (L + 1);
   __shared__ float red[(kWideThreads / 32) * (L + 1)];
   const Dropper drop(a.drop);
-  const bool dropping = drop.threshold > 0;
+  const bool dropping = drop.on;
   for (int row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + (long long)row * a.x_ld;
     const T* r = a.r ? static_cast<const T*>(a.r) + (long long)row * a.r_ld : nullptr;
@@ -203,7 +231,7 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_bwd_wide(NormArgs a) {
   constexpr int K = (L + 1) * (L + 1);
   __shared__ float red[(kWideThreads / 32) * (L + 2)];
   const Dropper drop(a.drop);
-  const bool dropping = drop.threshold > 0;
+  const bool dropping = drop.on;
   for (int row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + (long long)row * a.x_ld;
     const T* g = static_cast<const T*>(a.g) + (long long)row * a.g_ld;

@@ -6,9 +6,14 @@
 // or a multiple of 32 (sums by shuffles, then through shared memory).  With
 // degrees (L > 0), `active` is a multiple of K / gcd(K, V), so the component
 // of a lane's i-th value is the same in all of its vectors: what depends on
-// the degree (its class, its mean, its deviation) is one value per slot i,
-// and a row's sums of squares go to their degrees once per row, not once per
-// value.
+// the degree is one value per slot i, and a row's sums go to their degrees
+// once per row, not once per value.
+//
+// The values move from and to HBM once, so these kernels are bound by
+// instructions before they are bound by memory: a bf16 value that is read and
+// written once may cost about 20 of them.  Hence the arithmetic is on pairs
+// (fma.rn.f32x2), and sums of several values are scattered over the lanes as
+// they are formed.
 #pragma once
 
 #include "common.cuh"
@@ -23,6 +28,11 @@ struct RowShape {
   int groups;  // rows of a CTA at a time
 };
 
+constexpr int kRowThreads = 256;     // of a CTA, where a group is smaller
+constexpr int kMaxRowThreads = 512;  // 128 registers a thread
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // ---------------------------------------------------------------- vectors
 // V values of type T as loaded: 16 bytes, or one value.
 template <typename T, int V>
@@ -33,14 +43,12 @@ struct Pack<float, 4> {
   float4 v;
   __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
   __device__ __forceinline__ void zero() { v = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
-  __device__ __forceinline__ void get(float (&f)[4]) const {
-    f[0] = v.x;
-    f[1] = v.y;
-    f[2] = v.z;
-    f[3] = v.w;
+  __device__ __forceinline__ void get(float2* f) const {
+    f[0] = make_float2(v.x, v.y);
+    f[1] = make_float2(v.z, v.w);
   }
-  __device__ __forceinline__ static void store(float* p, const float (&f)[4]) {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  __device__ __forceinline__ static void store(float* p, const float2* f) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
   }
 };
 
@@ -49,19 +57,15 @@ struct Pack<__nv_bfloat16, 8> {
   uint4 v;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    f[0] = bf16_lo(v.x);
-    f[1] = bf16_hi(v.x);
-    f[2] = bf16_lo(v.y);
-    f[3] = bf16_hi(v.y);
-    f[4] = bf16_lo(v.z);
-    f[5] = bf16_hi(v.z);
-    f[6] = bf16_lo(v.w);
-    f[7] = bf16_hi(v.w);
+  __device__ __forceinline__ void get(float2* f) const {
+    f[0] = make_float2(bf16_lo(v.x), bf16_hi(v.x));
+    f[1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
+    f[2] = make_float2(bf16_lo(v.z), bf16_hi(v.z));
+    f[3] = make_float2(bf16_lo(v.w), bf16_hi(v.w));
   }
-  __device__ __forceinline__ static void store(__nv_bfloat16* p, const float (&f)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                              pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  __device__ __forceinline__ static void store(__nv_bfloat16* p, const float2* f) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
+                                              pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
   }
 };
 
@@ -70,146 +74,277 @@ struct Pack<T, 1> {
   T v;
   __device__ __forceinline__ void load(const T* p) { v = *p; }
   __device__ __forceinline__ void zero() { v = T(0.0f); }
-  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = load1(&v); }
-  __device__ __forceinline__ static void store(T* p, const float (&f)[1]) { store1(p, f[0]); }
 };
 
-// Dropout of V consecutive values of a row from column col (a multiple of V).
-template <int V>
-__device__ __forceinline__ void drop_values(const Dropper& d, float (&f)[V], uint32_t row, int col) {
-  if (V > 1 && d.group == 1) {
-    const uint4 w = d.block(row, (uint32_t)col >> 3);
-    const bool upper = V == 4 && (col & 4);
-    const uint32_t w0 = upper ? w.z : w.x, w1 = upper ? w.w : w.y;
-    const uint32_t words[4] = {w0, w1, w.z, w.w};
+// The NV vectors of a lane, as pairs of values: two neighbours, or for V = 1
+// the values of two vectors.
+template <typename T, int V, int NV>
+__device__ __forceinline__ void get_pairs(const Pack<T, V> (&v)[NV], float2 (&p)[NV * V / 2]) {
+  if constexpr (V == 1) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const uint32_t draw = (i & 1) ? words[i >> 1] >> 16 : words[i >> 1] & 0xffffu;
-      f[i] = draw >= d.threshold ? f[i] * d.scale : 0.0f;
-    }
-    return;
-  }
-  // the units that the vector touches, one after the other
-  uint32_t unit = (uint32_t)col / (uint32_t)d.group;
-  int end = (int)((unit + 1) * (uint32_t)d.group) - col;  // of the unit, counted from the vector's start
-  uint32_t blk = unit >> 3, keep = 0;
-  uint4 w = d.block(row, blk);
-#pragma unroll 1
-  for (int at = 0;;) {
-    if (Dropper::draw(w, unit) >= d.threshold) keep |= (end >= V ? 1u << V : 1u << end) - (1u << at);
-    if (end >= V) break;
-    at = end;
-    end += d.group;
-    ++unit;
-    if (unit >> 3 != blk) w = d.block(row, blk = unit >> 3);
-  }
+    for (int k = 0; k < NV / 2; ++k) p[k] = make_float2(load1(&v[2 * k].v), load1(&v[2 * k + 1].v));
+  } else {
 #pragma unroll
-  for (int i = 0; i < V; ++i) f[i] = (keep >> i) & 1 ? f[i] * d.scale : 0.0f;
+    for (int j = 0; j < NV; ++j) v[j].get(p + j * (V / 2));
+  }
 }
 
-// ---------------------------------------------------------------- sums
-// Sums N values over the lanes of each group, in a fixed order.  Groups of
-// several warps exchange their warps' sums through red (two halves of
-// N floats per warp of the CTA, taken in turn, so that one barrier per sum is
-// enough); every thread of the CTA takes part.
-template <int N>
-struct GroupSum {
-  int lanes, warps, first;  // of the group: lanes, warps, its first warp
-  float* red;
-  int half;
-  __device__ __forceinline__ GroupSum(int lanes_, float* red_) : lanes(lanes_), red(red_), half(0) {
-    warps = lanes_ >> 5;
-    first = warps > 1 ? (int)(threadIdx.x >> 5) / warps * warps : 0;
+template <typename T, int V, int NV>
+__device__ __forceinline__ void put_pairs(T* row, const uint32_t (&col)[NV], const bool (&has)[NV],
+                                          const float2 (&p)[NV * V / 2]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (!has[j]) continue;
+    if constexpr (V == 1)
+      store1(row + col[j], j & 1 ? p[j / 2].y : p[j / 2].x);
+    else
+      Pack<T, V>::store(row + col[j], p + j * (V / 2));
   }
-  template <int M>
-  __device__ __forceinline__ void operator()(float (&v)[M]) {
-    static_assert(M <= N, "buffer too small");
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      if (o < lanes) {
-#pragma unroll
-        for (int i = 0; i < M; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-      }
-    }
-    if (lanes <= 32) return;
-    const int all = blockDim.x >> 5;
-    float* buf = red + half * all * N;
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-      for (int i = 0; i < M; ++i) buf[i * all + (threadIdx.x >> 5)] = v[i];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < M; ++i) {
-      float t = buf[i * all + first];
-      for (int k = 1; k < warps; ++k) t += buf[i * all + first + k];
-      v[i] = t;
-    }
-    half ^= 1;
-  }
-};
+}
 
-// What a lane knows of its columns.
+// ---------------------------------------------------------------- slots
+// What a lane knows of its columns.  Values i = 0..V-1 of a vector fall into
+// GROUPS of one degree: all of them (L = 0, or V = 1), the first and the other
+// three of each four (K a multiple of 4: degrees begin at l^2 = 0 or 1 mod 4),
+// or each by itself.
 template <int L, int V, int NV>
 struct Slots {
   static constexpr int K = (L + 1) * (L + 1);
-  int lane, col0, stride;  // within the group; of vector 0; between vectors
-  int cls[L ? V : 1];      // degree of value i (L > 0)
-  uint32_t first;          // bit i: value i is a degree 0 (L > 0)
-  __device__ __forceinline__ Slots(const RowShape& sh) {
+  static constexpr bool FOURS = L > 0 && V > 1 && K % 4 == 0;
+  static constexpr int GROUPS = L == 0 || V == 1 ? 1 : FOURS ? V / 2 : V;
+  static constexpr int PAIRS = V > 1 ? V / 2 : 1;  // pairs of a vector
+  uint32_t col[NV];
+  bool has[NV];
+  int lane;         // within the group
+  int cls[GROUPS];  // degree
+  float2 first[PAIRS];  // 1 where a value is a degree 0, else 0
+
+  __device__ __forceinline__ Slots(const RowShape& sh, int cols) {
     lane = threadIdx.x % sh.lanes;
-    col0 = lane * V;
-    stride = sh.active * V;
-    first = 0;
-    if (L) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int k = (col0 + i) % K;
+    for (int j = 0; j < NV; ++j) {
+      col[j] = (lane + j * sh.active) * V;
+      has[j] = lane < sh.active && (int)col[j] < cols;
+    }
+    if constexpr (L == 0) {
+      cls[0] = 0;
+    } else {
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) {
+        const int k = (int)(col[0] + (FOURS ? g / 2 * 4 + g % 2 : g)) % K;
         int l = 0;
 #pragma unroll
         for (int m = 1; m <= L; ++m) l += k >= m * m;
-        cls[i] = l;
-        first |= (uint32_t)(l == 0) << i;
+        cls[g] = l;
       }
     }
-  }
-  __device__ __forceinline__ bool is0(int i) const { return L == 0 || ((first >> i) & 1); }
-  __device__ __forceinline__ int col(int j) const { return col0 + j * stride; }
-  // The slots' sums put to their degrees.
-  __device__ __forceinline__ void by_degree(const float (&slot)[V], float (&out)[L + 1]) const {
-    if (L == 0) {
-      float t = slot[0];
+    float f[GROUPS];
 #pragma unroll
-      for (int i = 1; i < V; ++i) t += slot[i];
-      out[0] = t;
+    for (int g = 0; g < GROUPS; ++g) f[g] = cls[g] == 0 ? 1.0f : 0.0f;
+    spread(f, first);
+  }
+  // Whether pair s of a vector may hold a degree 0.
+  __device__ __forceinline__ static constexpr bool may0(int s) { return !FOURS || s % 2 == 0; }
+  // One value per group put to the pairs of a vector.
+  __device__ __forceinline__ static void spread(const float (&g)[GROUPS], float2 (&p)[PAIRS]) {
+#pragma unroll
+    for (int s = 0; s < PAIRS; ++s) {
+      if (GROUPS == 1)
+        p[s] = both(g[0]);
+      else if (FOURS)
+        p[s] = s % 2 ? both(g[s / 2 * 2 + 1]) : make_float2(g[s / 2 * 2], g[s / 2 * 2 + 1]);
+      else
+        p[s] = make_float2(g[2 * s % GROUPS], g[(2 * s + 1) % GROUPS]);
+    }
+  }
+  // The sums of the pairs put to their degrees, out[FROM + l].
+  template <int FROM, int N>
+  __device__ __forceinline__ void by_degree(const float2 (&p)[PAIRS], float (&out)[N]) const {
+    if constexpr (L == 0) {
+      float2 t = p[0];
+#pragma unroll
+      for (int s = 1; s < PAIRS; ++s) t = __fadd2_rn(t, p[s]);
+      out[FROM] = t.x + t.y;
     } else {
+      float g[GROUPS];
+      if constexpr (V == 1) {
+        g[0] = p[0].x + p[0].y;
+      } else if constexpr (FOURS) {
+#pragma unroll
+        for (int k = 0; k < GROUPS; k += 2) {
+          g[k] = p[k].x;
+          g[k + 1] = p[k].y + (p[k + 1].x + p[k + 1].y);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < GROUPS; ++k) g[k] = k % 2 ? p[k / 2].y : p[k / 2].x;
+      }
 #pragma unroll
       for (int l = 0; l <= L; ++l) {
-        float t = 0.0f;
+        float t = cls[0] == l ? g[0] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) t += cls[i] == l ? slot[i] : 0.0f;
-        out[l] = t;
+        for (int k = 1; k < GROUPS; ++k) t += cls[k] == l ? g[k] : 0.0f;
+        out[FROM + l] = t;
       }
     }
-  }
-  // The degrees' values put to the slots.
-  __device__ __forceinline__ void to_slots(const float (&deg)[L + 1], float (&slot)[V]) const {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float t = deg[0];
-#pragma unroll
-      for (int l = 1; l <= L; ++l) t = cls[L ? i : 0] == l ? deg[l] : t;
-      slot[i] = t;
-    }
-  }
-  __device__ __forceinline__ void degree0(float v, float (&slot)[V]) const {
-#pragma unroll
-    for (int i = 0; i < V; ++i) slot[i] = is0(i) ? v : 0.0f;
   }
 };
 
-constexpr int kRowThreads = 256;     // of a CTA, where a group is smaller
-constexpr int kMaxRowThreads = 512;  // 128 registers a thread: 16 values of each array with their weights
+// ---------------------------------------------------------------- dropout
+// Which of a lane's values the dropout keeps.  V = 1: the group forms the keep
+// bits of its row together, eight columns a byte, in shared memory (form();
+// the caller waits until it is visible).  V > 1: each lane draws for its own
+// vectors; where a unit is at least as wide as a vector, a vector touches two
+// units at most, which are found once (meta: the first unit, and how many of
+// the vector's values it has).
+constexpr int kKeepBytes = kMaxRowThreads * 16 / 8 + kRowThreads;  // bits of a CTA's rows, a byte each begun
+
+template <int L, int V, int NV>
+struct Keeps {
+  uint32_t meta[NV];
+  uint8_t* bits;  // V = 1: of this row group, two halves taken in turn
+  int bytes;
+  int half;
+  __device__ __forceinline__ Keeps(const Dropper& d, const Slots<L, V, NV>& at, const RowShape& sh, int cols,
+                                   uint8_t* smem) {
+    if constexpr (V == 1) {
+      bytes = (cols + 7) / 8;
+      bits = smem + (threadIdx.x / sh.lanes) * bytes;
+      half = 0;
+    } else {
+      const uint32_t group = L ? (uint32_t)at.K : (uint32_t)d.group;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const uint32_t unit = at.col[j] / group, left = group - (at.col[j] - unit * group);
+        meta[j] = unit << 4 | (left < V ? left : V);
+      }
+    }
+  }
+  // V = 1: the bits of a row, by all lanes of its group.
+  __device__ __forceinline__ void form(const Dropper& d, const Slots<L, V, NV>& at, const RowShape& sh, int row) {
+    if constexpr (V == 1) {
+      half ^= 1;
+      for (int y = at.lane; y < bytes; y += sh.lanes) bits[half * kKeepBytes + y] = (uint8_t)d.keep_bits(row, 8 * y, 8);
+    }
+  }
+  // The values of a row, p, with the dropout applied.
+  __device__ __forceinline__ void apply(const Dropper& d, const Slots<L, V, NV>& at, int row,
+                                        float2 (&p)[NV * V / 2]) const {
+    if constexpr (V == 1) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float& f = j & 1 ? p[j / 2].y : p[j / 2].x;
+        const bool keep = at.has[j] && (bits[half * kKeepBytes + (at.col[j] >> 3)] >> (at.col[j] & 7)) & 1;
+        f = keep ? f * d.scale : 0.0f;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float2* f = p + j * (V / 2);
+        if (L == 0 && d.group == 1) {
+          const uint4 w = d.block(row, at.col[j] >> 3);
+          const bool upper = V == 4 && (at.col[j] & 4);
+          const uint32_t words[4] = {upper ? w.z : w.x, upper ? w.w : w.y, w.z, w.w};
+#pragma unroll
+          for (int s = 0; s < V / 2; ++s) {
+            f[s].x = words[s] << 16 > d.bound ? f[s].x * d.scale : 0.0f;
+            f[s].y = words[s] > d.bound ? f[s].y * d.scale : 0.0f;
+          }
+        } else if (L > 0 || d.group >= V) {
+          const uint32_t unit = meta[j] >> 4;
+          const int n = meta[j] & 15;
+          uint4 w = d.block(row, unit >> 3);
+          const bool k0 = d.keeps(w, unit);
+          bool k1 = k0;
+          if ((L == 0 || at.K % V) && n < V) {
+            if ((unit & 7) == 7) w = d.block(row, (unit + 1) >> 3);
+            k1 = d.keeps(w, unit + 1);
+          }
+#pragma unroll
+          for (int s = 0; s < V / 2; ++s) {
+            f[s].x = (2 * s < n ? k0 : k1) ? f[s].x * d.scale : 0.0f;
+            f[s].y = (2 * s + 1 < n ? k0 : k1) ? f[s].y * d.scale : 0.0f;
+          }
+        } else {
+          const uint32_t keep = d.keep_bits(row, at.col[j], V);
+#pragma unroll
+          for (int s = 0; s < V / 2; ++s) {
+            f[s].x = (keep >> (2 * s)) & 1 ? f[s].x * d.scale : 0.0f;
+            f[s].y = (keep >> (2 * s + 1)) & 1 ? f[s].y * d.scale : 0.0f;
+          }
+        }
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------- sums
+// Sums N values over the lanes of each group, in a fixed order, and leaves
+// them spread over the lanes: value n is then fetched by a shuffle.  For N > 2
+// the values are halved as the lanes are (each lane passes on the half that it
+// does not keep), so that N values take about as many shuffles as log2 G + N.
+// Groups of several warps exchange their warps' sums through red (two halves,
+// taken in turn, so that one barrier per sum is enough; every thread of the
+// CTA takes part).  N = 2 needs groups of at least 2 lanes, N > 2 of 8.
+template <int N>
+struct GroupSum {
+  static constexpr int P = N <= 1 ? 1 : N <= 2 ? 2 : N <= 4 ? 4 : 8;  // N rounded up to a power of two
+  static constexpr int kRed = 2 * (kMaxRowThreads / 32) * P;          // floats of red
+  int lanes, warps, first;  // of the group: lanes, warps, its first warp
+  int base;                 // of the group within the warp
+  float* red;
+  int half;
+  float val;  // after sum(): this lane's value
+  __device__ __forceinline__ GroupSum(int lanes_, float* red_) : lanes(lanes_), red(red_), half(0), val(0.0f) {
+    warps = lanes_ >> 5;
+    first = warps > 1 ? (int)(threadIdx.x >> 5) / warps * warps : 0;
+    base = lanes_ < 32 ? (int)(threadIdx.x & 31) / lanes_ * lanes_ : 0;
+  }
+  // The lane that holds value n.
+  __device__ __forceinline__ int source(int n) const {
+    if (N == 1) return threadIdx.x & 31;
+    if (lanes > 32) return n;
+    if (N == 2) return base + n * (lanes >> 1);
+    int lane = base;
+    if (P == 8) lane += (n >> 2 & 1) * (lanes >> 1) + (n >> 1 & 1) * (lanes >> 2) + (n & 1) * (lanes >> 3);
+    if (P == 4) lane += (n >> 1 & 1) * (lanes >> 1) + (n & 1) * (lanes >> 2);
+    return lane;
+  }
+  __device__ __forceinline__ float fetch(int source_lane) const {
+    return N == 1 ? val : __shfl_sync(0xffffffffu, val, source_lane);
+  }
+  __device__ __forceinline__ void operator()(const float (&v)[N]) {
+    const int in_warp = lanes < 32 ? lanes : 32;
+    int o = in_warp >> 1;
+    float x[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) x[i] = i < N ? v[i] : 0.0f;
+    int mine = 0;  // the value of this lane
+#pragma unroll
+    for (int n = P / 2; n > 0; n >>= 1) {
+      const bool up = threadIdx.x & o;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float send = up ? x[i] : x[i + n], keep = up ? x[i + n] : x[i];
+        x[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      }
+      mine += up ? n : 0;
+      o >>= 1;
+    }
+    for (; o > 0; o >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
+    val = x[0];
+    if (lanes <= 32) return;
+    const int lane = threadIdx.x & 31;
+    float* buf = red + half * (kRed / 2);
+    if (lane % (32 / P) == 0) buf[(threadIdx.x >> 5) * P + mine] = val;
+    __syncthreads();
+    float t = 0.0f;
+    for (int k = lane / P; k < warps; k += 32 / P) t += buf[(first + k) * P + lane % P];
+    for (o = P; o < 32 && o < warps * P; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    val = N == 1 ? __shfl_sync(0xffffffffu, t, 0) : t;
+    half ^= 1;
+  }
+};
 
 // ---------------------------------------------------------------- forward
 // One pass: each value is loaded once, kept in registers through the mean and
@@ -218,109 +353,154 @@ constexpr int kMaxRowThreads = 512;  // 128 registers a thread: 16 values of eac
 // or dropout in front.
 template <typename T, int L, int V, int NV, bool FUSED>
 __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowShape sh) {
-  __shared__ float red[2 * (kMaxRowThreads / 32) * (L + 1)];
-  const Slots<L, V, NV> at(sh);
-  GroupSum<L + 1> sum(sh.lanes, red);
-  Dropper drop(a.drop);
-  const T* x = static_cast<const T*>(a.x);
-  const T* r = static_cast<const T*>(a.r);
-  bool has[NV];
-  float w[NV][V], b[NV][V];
+  using S = Slots<L, V, NV>;
+  constexpr int P = NV * V / 2, PV = S::PAIRS, NS = L + 1;
+  constexpr bool EACH = L == 0 || V == 1;  // a bias per value; else one per vector, which has at most one degree 0
+  __shared__ float red1[GroupSum<1>::kRed], red2[GroupSum<NS>::kRed];
+  __shared__ uint8_t bits[FUSED && V == 1 ? 2 * kKeepBytes : 1];
+  const S at(sh, a.cols);
+  GroupSum<1> sum1(sh.lanes, red1);
+  GroupSum<NS> sum2(sh.lanes, red2);
+  const Dropper drop(a.drop);
+  Keeps<L, V, NV> keeps(drop, at, sh, a.cols, bits);
+  float2 w[P], b[EACH ? P : NV], m[V == 1 ? P : NV];  // m: -1 where a value is one of the row's, else 0
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    has[j] = at.lane < sh.active && at.col(j) < a.cols;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (at.col(j) + i) / at.K, l = L ? at.cls[L ? i : 0] : 0;
-      w[j][i] = has[j] && a.w ? a.w[l * a.C + c] : 1.0f;
-      b[j][i] = has[j] && a.b && at.is0(i) ? a.b[c] : 0.0f;
+      const int c = (int)(at.col[j] + i) / S::K;
+      int l = 0;
+      if (L) {
+        l = at.cls[S::GROUPS == 1 ? 0 : S::FOURS ? i / 4 * 2 + (i % 4 > 0) : i];
+      }
+      const float wi = at.has[j] && a.w ? a.w[l * a.C + c] : 1.0f;
+      const float bi = at.has[j] && a.b && l == 0 ? a.b[c] : 0.0f;
+      const float mi = at.has[j] ? -1.0f : 0.0f;
+      const int e = j * V + i;
+      (e & 1 ? w[e / 2].y : w[e / 2].x) = wi;
+      if (EACH)
+        (e & 1 ? b[e / 2].y : b[e / 2].x) = bi;
+      else if (i == 0 || l == 0)
+        b[EACH ? 0 : j] = both(bi);
+      if (V == 1)
+        (e & 1 ? m[e / 2].y : m[e / 2].x) = mi;
+      else
+        m[V == 1 ? 0 : j] = both(mi);
     }
   }
   const float inv = 1.0f / (float)a.C;
+  float scale[S::GROUPS];
+  int from[S::GROUPS];
+#pragma unroll
+  for (int g = 0; g < S::GROUPS; ++g) {
+    scale[g] = inv / (float)(2 * at.cls[g] + 1);
+    from[g] = sum2.source(at.cls[g]);
+  }
   const int stride = gridDim.x * sh.groups;
+  int row = blockIdx.x * sh.groups + threadIdx.x / sh.lanes;
+  const T* x = static_cast<const T*>(a.x) + (long long)row * a.x_ld;
+  const T* r = static_cast<const T*>(a.r) + (long long)row * a.r_ld;
   Pack<T, V> nx[NV], nr[FUSED ? NV : 1];
-  auto fetch = [&](int row) {
+  auto fetch = [&](bool live) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const bool ok = has[j] && row < a.rows;
-      if (ok)
-        nx[j].load(x + (long long)row * a.x_ld + at.col(j));
+      if (at.has[j] && live)
+        nx[j].load(x + at.col[j]);
       else
         nx[j].zero();
       if (FUSED) {
-        if (ok && r)
-          nr[FUSED ? j : 0].load(r + (long long)row * a.r_ld + at.col(j));
+        if (at.has[j] && live && a.r)
+          nr[FUSED ? j : 0].load(r + at.col[j]);
         else
           nr[FUSED ? j : 0].zero();
       }
     }
   };
-  int row = blockIdx.x * sh.groups + threadIdx.x / sh.lanes;
-  fetch(row);
+  fetch(row < a.rows);
+  if (FUSED && V == 1 && drop.on) {
+    keeps.form(drop, at, sh, row);
+    __syncthreads();
+  }
   // the same number of rounds for every group of the CTA
   for (int base = blockIdx.x * sh.groups; base < a.rows; base += stride, row += stride) {
-    float v[NV][V], slot[V];
+    float2 v[P], acc[PV];
+    get_pairs<T, V, NV>(nx, v);
+    if constexpr (FUSED) {
+      if (drop.on) keeps.apply(drop, at, row, v);
+      if (a.r) {
+        float2 f[P];
+        get_pairs<T, V, NV>(nr, f);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) nx[j].get(v[j]);
-    if (FUSED) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if (drop.threshold) drop_values<V>(drop, v[j], row, at.col(j));
-        float f[V];
-        nr[FUSED ? j : 0].get(f);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[j][i] += f[i];
+        for (int p = 0; p < P; ++p) v[p] = __fadd2_rn(v[p], f[p]);
       }
     }
-    fetch(row + stride);
+    x += stride * a.x_ld;
+    r += stride * a.r_ld;
+    fetch(row + stride < a.rows);
+    if (FUSED && V == 1 && drop.on) {  // the next row's, seen after a barrier of this row's sums
+      keeps.form(drop, at, sh, row + stride);
+      if (sh.lanes <= 32) __syncwarp();
+    }
     const bool live = row < a.rows;
     const long long out = (long long)row * a.cols;
-    if (FUSED && a.s && live) {
+    if (FUSED && a.s && live) put_pairs<T, V, NV>(static_cast<T*>(a.s) + out, at.col, at.has, v);
+    // the mean of degree 0
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (has[j]) Pack<T, V>::store(static_cast<T*>(a.s) + out + at.col(j), v[j]);
+    for (int s = 0; s < PV; ++s) {
+      acc[s] = v[s];
+#pragma unroll
+      for (int p = s + PV; p < P; p += PV) acc[s] = __fadd2_rn(acc[s], v[p]);
     }
-    float mean[1] = {0.0f};
+    float part[1] = {0.0f};
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float t = v[0][i];
-#pragma unroll
-      for (int j = 1; j < NV; ++j) t += v[j][i];
-      mean[0] += at.is0(i) ? t : 0.0f;
+    for (int s = 0; s < PV; ++s) {
+      if (!S::may0(s)) continue;
+      if (L) acc[s] = __fmul2_rn(acc[s], at.first[s]);
+      part[0] += acc[s].x + acc[s].y;
     }
-    sum(mean);
-    mean[0] *= inv;
-    at.degree0(mean[0], slot);
+    sum1(part);
+    const float mean = sum1.fetch(0) * inv;
+    // centred; what lies outside the row stays 0
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[j][i] = has[j] ? v[j][i] - slot[i] : 0.0f;
-    float q[L + 1];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      slot[i] = v[0][i] * v[0][i];
-#pragma unroll
-      for (int j = 1; j < NV; ++j) slot[i] += v[j][i] * v[j][i];
+    for (int p = 0; p < P; ++p) {
+      if (!S::may0(p % PV)) continue;
+      float2 mu = both(mean);
+      if (L) mu = __fmul2_rn(mu, at.first[p % PV]);
+      v[p] = __ffma2_rn(mu, m[V == 1 ? p : p / PV], v[p]);
     }
-    at.by_degree(slot, q);
-    sum(q);
 #pragma unroll
-    for (int l = 0; l <= L; ++l) q[l] = 1.0f / sqrtf(q[l] * (inv * (1.0f / (2 * l + 1))) + a.eps);
-    if (!live) continue;
-    if (a.stats && at.lane == 0) {
+    for (int s = 0; s < PV; ++s) {
+      acc[s] = __fmul2_rn(v[s], v[s]);
+#pragma unroll
+      for (int p = s + PV; p < P; p += PV) acc[s] = __ffma2_rn(v[p], v[p], acc[s]);
+    }
+    float sq[NS];
+    at.template by_degree<0>(acc, sq);
+    sum2(sq);
+    float q[S::GROUPS];
+#pragma unroll
+    for (int g = 0; g < S::GROUPS; ++g) q[g] = rsqrtf(sum2.fetch(from[g]) * scale[g] + a.eps);
+    if (a.stats) {
       float* st = a.stats + (long long)row * (L + 2);
-      st[0] = mean[0];
-#pragma unroll
-      for (int l = 0; l <= L; ++l) st[1 + l] = q[l];
+      const int l = at.lane < L ? at.lane : L;
+      const float ql = L ? rsqrtf(sum2.fetch(sum2.source(l)) * (inv / (float)(2 * l + 1)) + a.eps) : q[0];
+      if (live && at.lane <= L) st[1 + l] = ql;
+      if (live && at.lane == 0) st[0] = mean;
     }
-    if (!a.y) continue;
-    at.to_slots(q, slot);
+    if (!live || !a.y) continue;
+    float2 qs[PV];
+    S::spread(q, qs);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[j][i] = v[j][i] * slot[i] * w[j][i] + b[j][i];
-      if (has[j]) Pack<T, V>::store(static_cast<T*>(a.y) + out + at.col(j), v[j]);
+    for (int p = 0; p < P; ++p) {
+      const float2 h = __fmul2_rn(v[p], qs[p % PV]);
+      if (EACH)
+        v[p] = __ffma2_rn(h, w[p], b[EACH ? p : 0]);
+      else if (S::may0(p % PV))
+        v[p] = __ffma2_rn(h, w[p], __fmul2_rn(b[EACH ? 0 : p / PV], at.first[p % PV]));
+      else
+        v[p] = __fmul2_rn(h, w[p]);
     }
+    put_pairs<T, V, NV>(static_cast<T*>(a.y) + out, at.col, at.has, v);
   }
 }
 
@@ -333,159 +513,201 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
 // of a residual stream, dropout, or both gradients asked for.
 template <typename T, int L, int V, int NV, bool FUSED>
 __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, RowShape sh) {
-  __shared__ float red[2 * (kMaxRowThreads / 32) * (L + 2)];
+  using S = Slots<L, V, NV>;
+  constexpr int P = NV * V / 2, PV = S::PAIRS, NS = L + 2;
+  constexpr bool EACH = L == 0 || V == 1;  // db per value; else per vector, which has at most one degree 0
+  __shared__ float red[GroupSum<NS>::kRed];
+  __shared__ uint8_t bits[FUSED && V == 1 ? 2 * kKeepBytes : 1];
   extern __shared__ float colsum[];  // [cols] g h, then [C] g
-  const Slots<L, V, NV> at(sh);
-  GroupSum<L + 2> sum(sh.lanes, red);
+  const S at(sh, a.cols);
+  GroupSum<NS> sum(sh.lanes, red);
   const Dropper drop(a.drop);
-  const T* x = static_cast<const T*>(a.x);
-  const T* g = static_cast<const T*>(a.g);
-  const T* r = static_cast<const T*>(a.r);
-  constexpr int NB = L ? 1 : V;  // degree-0 values of a vector, at most
-  constexpr int NQ = L ? V : 1;  // deviations of a lane's slots
-  bool has[NV];
-  float w[NV][V], dw[NV][V], db[NV][NB];
+  Keeps<L, V, NV> keeps(drop, at, sh, a.cols, bits);
+  float2 w[P], dw[P], db[EACH ? P : NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    has[j] = at.lane < sh.active && at.col(j) < a.cols;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (at.col(j) + i) / at.K, l = L ? at.cls[L ? i : 0] : 0;
-      w[j][i] = has[j] && a.w ? a.w[l * a.C + c] : 1.0f;
-      dw[j][i] = 0.0f;
+      const int c = (int)(at.col[j] + i) / S::K;
+      int l = 0;
+      if (L) l = at.cls[S::GROUPS == 1 ? 0 : S::FOURS ? i / 4 * 2 + (i % 4 > 0) : i];
+      const float wi = at.has[j] && a.w ? a.w[l * a.C + c] : 1.0f;
+      const int e = j * V + i;
+      (e & 1 ? w[e / 2].y : w[e / 2].x) = wi;
     }
-#pragma unroll
-    for (int i = 0; i < NB; ++i) db[j][i] = 0.0f;
   }
+#pragma unroll
+  for (int p = 0; p < P; ++p) dw[p] = both(0.0f);
+#pragma unroll
+  for (int p = 0; p < (EACH ? P : NV); ++p) db[p] = both(0.0f);
   const float inv = 1.0f / (float)a.C;
+  float scale[S::GROUPS];
+  int from[S::GROUPS];
+#pragma unroll
+  for (int g = 0; g < S::GROUPS; ++g) {
+    scale[g] = -inv / (float)(2 * at.cls[g] + 1);
+    from[g] = sum.source(1 + at.cls[g]);
+  }
+  const int from0 = sum.source(0);
   const int stride = gridDim.x * sh.groups;
-  Pack<T, V> nx[NV], ng[NV], nr[FUSED ? NV : 1];
-  float nmean, nq[NQ];
-  auto fetch = [&](int row) {
-    const bool live = row < a.rows;
-    const float* st = a.stats + (long long)row * (L + 2);
+  int row = blockIdx.x * sh.groups + threadIdx.x / sh.lanes;
+  const T* x = static_cast<const T*>(a.x) + (long long)row * a.x_ld;
+  const T* g = static_cast<const T*>(a.g) + (long long)row * a.g_ld;
+  const T* r = static_cast<const T*>(a.r) + (long long)row * a.r_ld;
+  const float* st = a.stats + (long long)row * (L + 2);
+  Pack<T, V> nx[NV], ng[NV];
+  float nmean, nq[S::GROUPS];
+  auto fetch = [&](bool live) {
     nmean = live ? st[0] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) nq[i] = live ? st[1 + (L ? at.cls[L ? i : 0] : 0)] : 0.0f;
+    for (int k = 0; k < S::GROUPS; ++k) nq[k] = live ? st[1 + at.cls[k]] : 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (has[j] && live) {
-        nx[j].load(x + (long long)row * a.x_ld + at.col(j));
-        ng[j].load(g + (long long)row * a.g_ld + at.col(j));
+      if (at.has[j] && live) {
+        nx[j].load(x + at.col[j]);
+        ng[j].load(g + at.col[j]);
       } else {
         nx[j].zero();
         ng[j].zero();
       }
-      if (FUSED) {
-        if (has[j] && live && r)
-          nr[FUSED ? j : 0].load(r + (long long)row * a.r_ld + at.col(j));
-        else
-          nr[FUSED ? j : 0].zero();
-      }
     }
   };
-  int row = blockIdx.x * sh.groups + threadIdx.x / sh.lanes;
-  fetch(row);
+  fetch(row < a.rows);
   for (int base = blockIdx.x * sh.groups; base < a.rows; base += stride, row += stride) {
-    float h[NV][V], av[NV][V], slot[V], tot[L + 2], q[NQ];
+    const bool live = row < a.rows;
+    float2 h[P], av[P], qs[PV];
     Pack<T, V> cr[FUSED ? NV : 1];
+    float q[S::GROUPS];
+    get_pairs<T, V, NV>(nx, h);
+    get_pairs<T, V, NV>(ng, av);
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) q[i] = nq[i];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      nx[j].get(h[j]);
-      ng[j].get(av[j]);
-      if (FUSED) cr[FUSED ? j : 0] = nr[FUSED ? j : 0];
-    }
-    const float mean = nmean;
-    fetch(row + stride);
-    tot[0] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const bool first = at.is0(i);
-      const float mu = first ? mean : 0.0f, qi = q[L ? i : 0];
-      slot[i] = 0.0f;
-      float sa = 0.0f;
+    for (int k = 0; k < S::GROUPS; ++k) q[k] = nq[k];
+    const float2 mu = both(-nmean);
+    if constexpr (FUSED) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        h[j][i] = (h[j][i] - mu) * qi;
-        dw[j][i] += av[j][i] * h[j][i];
-        if (L == 0)
-          db[j][L ? 0 : i] += av[j][i];
+        if (at.has[j] && live && a.r)
+          cr[j].load(r + at.col[j]);
         else
-          db[j][0] += first ? av[j][i] : 0.0f;
-        av[j][i] *= w[j][i];
-        sa += av[j][i];
-        slot[i] += av[j][i] * h[j][i];
+          cr[j].zero();
       }
-      tot[0] += first ? sa : 0.0f;
     }
-    float deg[L + 1];
-    at.by_degree(slot, deg);
+    x += stride * a.x_ld;
+    g += stride * a.g_ld;
+    r += stride * a.r_ld;
+    st += (long long)stride * (L + 2);
+    fetch(row + stride < a.rows);
+    if (FUSED && V == 1 && drop.on) {  // seen after the barrier of this row's sums
+      keeps.form(drop, at, sh, row);
+      if (sh.lanes <= 32) __syncwarp();
+    }
+    S::spread(q, qs);
+    float2 sa[PV], sah[PV];
 #pragma unroll
-    for (int l = 0; l <= L; ++l) tot[1 + l] = deg[l];
+    for (int s = 0; s < PV; ++s) sa[s] = sah[s] = both(0.0f);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int s = p % PV;
+      if (L == 0)
+        h[p] = __fadd2_rn(h[p], mu);
+      else if (S::may0(s))
+        h[p] = __ffma2_rn(mu, at.first[s], h[p]);
+      h[p] = __fmul2_rn(h[p], qs[s]);
+      dw[p] = __ffma2_rn(av[p], h[p], dw[p]);
+      if (EACH)
+        db[EACH ? p : 0] = __fadd2_rn(db[EACH ? p : 0], av[p]);
+      else if (S::may0(s))
+        db[EACH ? 0 : p / PV] = __ffma2_rn(av[p], at.first[s], db[EACH ? 0 : p / PV]);
+      av[p] = __fmul2_rn(av[p], w[p]);
+      if (S::may0(s)) sa[s] = __fadd2_rn(sa[s], av[p]);
+      sah[s] = __ffma2_rn(av[p], h[p], sah[s]);
+    }
+    float tot[NS];
+    tot[0] = 0.0f;
+#pragma unroll
+    for (int s = 0; s < PV; ++s) {
+      if (!S::may0(s)) continue;
+      if (L) sa[s] = __fmul2_rn(sa[s], at.first[s]);
+      tot[0] += sa[s].x + sa[s].y;
+    }
+    at.template by_degree<1>(sah, tot);
     sum(tot);
-    if (row >= a.rows) continue;
-    const float m0 = tot[0] * inv;
+    // r = q a - (q mean(a h)) h - q mean(a) for degree 0
+    const float m0 = sum.fetch(from0) * -inv;
+    float c[S::GROUPS];
 #pragma unroll
-    for (int l = 0; l <= L; ++l) deg[l] = tot[1 + l] * (inv * (1.0f / (2 * l + 1)));
-    at.to_slots(deg, slot);
+    for (int k = 0; k < S::GROUPS; ++k) c[k] = sum.fetch(from[k]) * scale[k] * q[k];
+    if (!live) continue;
+    float2 cs[PV], c0[PV];
+    S::spread(c, cs);
+#pragma unroll
+    for (int s = 0; s < PV; ++s) c0[s] = L ? __fmul2_rn(__fmul2_rn(qs[s], both(m0)), at.first[s]) : __fmul2_rn(qs[s], both(m0));
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int s = p % PV;
+      const float2 t = S::may0(s) ? __ffma2_rn(av[p], qs[s], c0[s]) : __fmul2_rn(av[p], qs[s]);
+      av[p] = __ffma2_rn(h[p], cs[s], t);
+    }
     const long long out = (long long)row * a.cols;
+    if constexpr (FUSED) {
+      if (a.r) {
+        get_pairs<T, V, NV>(cr, h);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float f[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        f[i] = (av[j][i] - h[j][i] * slot[i] - (at.is0(i) ? m0 : 0.0f)) * q[L ? i : 0];
-      if (FUSED) {
-        float s[V];
-        cr[FUSED ? j : 0].get(s);
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] += s[i];
-        if (a.gr && has[j]) Pack<T, V>::store(static_cast<T*>(a.gr) + out + at.col(j), f);
-        if (a.gx) {
-          if (drop.threshold) drop_values<V>(drop, f, row, at.col(j));
-          if (has[j]) Pack<T, V>::store(static_cast<T*>(a.gx) + out + at.col(j), f);
-        }
-      } else if (has[j]) {
-        T* dst = static_cast<T*>(a.gx ? a.gx : a.gr);
-        if (dst) Pack<T, V>::store(dst + out + at.col(j), f);
+        for (int p = 0; p < P; ++p) av[p] = __fadd2_rn(av[p], h[p]);
       }
+      if (a.gr) put_pairs<T, V, NV>(static_cast<T*>(a.gr) + out, at.col, at.has, av);
+      if (a.gx) {
+        if (drop.on) keeps.apply(drop, at, row, av);
+        put_pairs<T, V, NV>(static_cast<T*>(a.gx) + out, at.col, at.has, av);
+      }
+    } else {
+      T* dst = static_cast<T*>(a.gx ? a.gx : a.gr);
+      if (dst) put_pairs<T, V, NV>(dst + out, at.col, at.has, av);
     }
   }
   if (!a.gw && !a.gb) return;
   // the CTA's sums: the groups of a warp by shuffles, the warps (or the
   // groups of several warps) in turn
-  if (sh.lanes < 32) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      if (o >= sh.lanes) {
+  for (int o = 16; o > 0; o >>= 1) {
+    if (o >= sh.lanes) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
+      for (int p = 0; p < P; ++p) {
+        dw[p].x += __shfl_xor_sync(0xffffffffu, dw[p].x, o);
+        dw[p].y += __shfl_xor_sync(0xffffffffu, dw[p].y, o);
+      }
 #pragma unroll
-          for (int i = 0; i < V; ++i) dw[j][i] += __shfl_xor_sync(0xffffffffu, dw[j][i], o);
-#pragma unroll
-          for (int i = 0; i < NB; ++i) db[j][i] += __shfl_xor_sync(0xffffffffu, db[j][i], o);
-        }
+      for (int p = 0; p < (EACH ? P : NV); ++p) {
+        db[p].x += __shfl_xor_sync(0xffffffffu, db[p].x, o);
+        db[p].y += __shfl_xor_sync(0xffffffffu, db[p].y, o);
       }
     }
   }
   const int unit = sh.lanes <= 32 ? 32 : sh.lanes;  // threads that add together
-  const int units = (blockDim.x + unit - 1) / unit, mine = threadIdx.x / unit;
+  const int units = blockDim.x / unit, mine = threadIdx.x / unit;
   const bool speaks = (int)(threadIdx.x % unit) < sh.lanes;
   for (int u = 0; u < units; ++u) {
     if (u == mine && speaks) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (!has[j]) continue;
-        const int col = at.col(j);
+        if (!at.has[j]) continue;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          colsum[col + i] = u ? colsum[col + i] + dw[j][i] : dw[j][i];
-          if (at.is0(i)) {
-            float* d = colsum + a.cols + (col + i) / at.K;
-            const float v = db[j][L ? 0 : i];
-            *d = u ? *d + v : v;
+          const int e = j * V + i, col = (int)at.col[j] + i;
+          const float t = e & 1 ? dw[e / 2].y : dw[e / 2].x;
+          colsum[col] = u ? colsum[col] + t : t;
+          if (EACH && col % S::K == 0) {
+            const float f = e & 1 ? db[EACH ? e / 2 : 0].y : db[EACH ? e / 2 : 0].x;
+            float* d = colsum + a.cols + col / S::K;
+            *d = u ? *d + f : f;
+          }
+        }
+        if (!EACH) {
+          const int c = (int)(at.col[j] + V - 1) / S::K;  // the channel that begins in the vector, if one does
+          if (c * S::K >= (int)at.col[j]) {
+            const float f = db[EACH ? 0 : j].x + db[EACH ? 0 : j].y;
+            float* d = colsum + a.cols + c;
+            *d = u ? *d + f : f;
           }
         }
       }
@@ -498,7 +720,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
     float t = 0.0f;
     if (L && m < nw) {
       const int l = m / a.C, c = m - l * a.C;
-      for (int k = l * l; k < (l + 1) * (l + 1); ++k) t += colsum[c * at.K + k];
+      for (int k = l * l; k < (l + 1) * (l + 1); ++k) t += colsum[c * S::K + k];
     } else {
       t = colsum[L ? a.cols + m - nw : m];
     }
@@ -513,15 +735,16 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
 }
 
 // ---------------------------------------------------------------- launch
-// Lanes for a row of cols values in vectors of V, NV per lane.
-inline RowShape row_shape(int cols, int K, int V, int NV) {
+// Lanes for a row of cols values in vectors of V, NV per lane, at least
+// min_lanes (a power of two).
+inline RowShape row_shape(int cols, int K, int V, int NV, int min_lanes) {
   int period = 1;  // K / gcd(K, V)
   while (period * V % K) ++period;
   const int vectors = cols / V;
   RowShape sh;
   sh.active = ((vectors + NV - 1) / NV + period - 1) / period * period;
   if (sh.active <= 32) {
-    sh.lanes = 1;
+    sh.lanes = min_lanes;
     while (sh.lanes < sh.active) sh.lanes *= 2;
   } else {
     sh.lanes = (sh.active + 31) / 32 * 32;
@@ -598,7 +821,8 @@ static eqmp_status launch_rows(const NormArgs& a, const RowShape& sh, const Devi
 template <typename T, int L, int V, bool BACKWARD>
 static eqmp_status launch_rows_v(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st, bool* done) {
   constexpr int K = (L + 1) * (L + 1), N8 = 8 / V, N16 = 16 / V;
-  const RowShape s8 = row_shape(a.cols, K, V, N8), s16 = row_shape(a.cols, K, V, N16);
+  constexpr int least = L ? 8 : BACKWARD ? 2 : 1;  // what GroupSum needs
+  const RowShape s8 = row_shape(a.cols, K, V, N8, least), s16 = row_shape(a.cols, K, V, N16, least);
   const int p8 = s8.lanes * N8, p16 = s16.lanes * N16;
   const bool take8 = s8.lanes <= kMaxRowThreads && (BACKWARD || p8 < p16 || (p8 == p16 && s8.lanes <= 32));
   *done = take8 || s16.lanes <= kMaxRowThreads;
