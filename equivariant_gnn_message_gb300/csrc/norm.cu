@@ -63,8 +63,17 @@ static int rows_grid(long long rows, const DeviceInfo& dev) {
 
 eqmp_status launch_norm_bwd_sum(const NormArgs& a, int L, cudaStream_t st) {
   const long long M = (long long)(L + 2) * a.C;
-  k_norm_bwd_sum<<<(unsigned)((M + kSumX - 1) / kSumX), dim3(kSumX, kSumY), 0, st>>>(a, L);
-  return cuda_status(cudaGetLastError());
+  // launched while the pass before it runs; the kernel waits for its parts
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((M + kSumX - 1) / kSumX));
+  cfg.blockDim = dim3(kSumX, kSumY);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, k_norm_bwd_sum, a, L));
 }
 
 template <typename T, int L>
@@ -207,57 +216,109 @@ static eqmp_status run_backward(Plane g, Plane x, Plane r, eqmp_dtype dtype, int
 }
 
 // ---------------------------------------------------------------- dropout
-// A CTA takes a tile of kDropTile * kDropThreads vectors, counted along the
-// rows; a thread loads its kDropTile vectors before it draws for them.  The
-// tile's first row is one 64-bit division, the vectors' rows are 32-bit ones.
-constexpr int kDropThreads = 256, kDropTile = 4;
+// A CTA takes `lanes` neighbouring vectors (a segment of the columns) of
+// kDropPasses * rows_per_pass rows; a thread keeps its columns, so that what
+// the generator makes of them is formed once, and loads its vectors before it
+// draws for them.  V = 1: the CTA forms the keep bits of its rows' units
+// together first, since neighbours share the generator's blocks.
+constexpr int kDropThreads = 256, kDropPasses = 8;
+
+struct DropShape {
+  int lanes, segments, rows_per_pass;
+};
 
 template <typename T, int V>
 __global__ void __launch_bounds__(kDropThreads) k_drop(const T* x, long long ld, T* out, int rows, int cols,
-                                                       DropArgs d) {
+                                                       DropArgs d, DropShape sh) {
   const Dropper drop(d);
-  const uint32_t per_row = cols / V;  // vectors
-  const long long first = (long long)blockIdx.x * (kDropTile * kDropThreads);
-  const int row0 = (int)(first / per_row);
-  const uint32_t v0 = (uint32_t)(first - (long long)row0 * per_row) + threadIdx.x;
-  Pack<T, V> in[kDropTile];
-  int row[kDropTile], col[kDropTile];
+  extern __shared__ uint8_t bits[];  // V = 1: [row][byte], from the segment's first unit on, rounded down to a byte
+  const int lane = threadIdx.x % sh.lanes, line = threadIdx.x / sh.lanes;
+  const int seg = blockIdx.x % sh.segments, tile = blockIdx.x / sh.segments;
+  const int col = (seg * sh.lanes + lane) * V;
+  const int row0 = tile * (kDropPasses * sh.rows_per_pass);
+  const bool mine = line < sh.rows_per_pass && col < cols;
+  Pack<T, V> in[kDropPasses];
 #pragma unroll
-  for (int k = 0; k < kDropTile; ++k) {
-    const uint32_t v = v0 + k * kDropThreads, r = v / per_row;
-    row[k] = row0 + (int)r;
-    col[k] = (int)(v - r * per_row) * V;
-    if (row[k] < rows) in[k].load(x + row[k] * ld + col[k]);
+  for (int k = 0; k < kDropPasses; ++k) {
+    const int row = row0 + k * sh.rows_per_pass + line;
+    if (mine && row < rows) in[k].load(x + row * ld + col);
   }
+  const uint32_t unit = (uint32_t)col / (uint32_t)drop.group;
+  if constexpr (V == 1) {
+    const uint32_t first = (uint32_t)(seg * sh.lanes) / (uint32_t)drop.group >> 3;
+    const uint32_t last = (uint32_t)(seg * sh.lanes + sh.lanes - 1) / (uint32_t)drop.group >> 3;
+    const int bytes = last - first + 1;
+    if (drop.on) {
+      for (int i = threadIdx.x; i < bytes * kDropPasses * sh.rows_per_pass; i += blockDim.x)
+        bits[i] = (uint8_t)drop.keep_bits(drop.block(row0 + i / bytes, first + i % bytes));
+      __syncthreads();
+    }
+    const uint8_t* b = bits + line * bytes + ((unit >> 3) - first);
 #pragma unroll
-  for (int k = 0; k < kDropTile; ++k) {
-    if (row[k] >= rows) break;
-    T* to = out + (long long)row[k] * cols + col[k];
-    if constexpr (V == 1) {
-      const float f = load1(&in[k].v);
-      store1(to, drop.on ? drop.apply(f, row[k], col[k]) : f);
-    } else {
+    for (int k = 0; k < kDropPasses; ++k) {
+      const int row = row0 + k * sh.rows_per_pass + line;
+      if (!mine || row >= rows) break;
+      float f = load1(&in[k].v);
+      if (drop.on) f = b[k * sh.rows_per_pass * bytes] >> (unit & 7) & 1 ? f * drop.scale : 0.0f;
+      store1(out + (long long)row * cols + col, f);
+    }
+  } else {
+    const PhiloxBlock pb = drop.of_block(unit >> 3);
+    const int left = (int)((unit + 1) * drop.group - col);  // of the vector's values in its first unit
+#pragma unroll
+    for (int k = 0; k < kDropPasses; ++k) {
+      const int row = row0 + k * sh.rows_per_pass + line;
+      if (!mine || row >= rows) break;
       float2 f[V / 2];
       in[k].get(f);
       if (drop.on) {
-        const uint32_t keep = drop.keep_bits(row[k], col[k], V);
+        uint4 w = drop.block(drop.of_row(row), pb);
+        if (drop.group == 1) {
+          const bool upper = V == 4 && (col & 4);
+          const uint32_t words[4] = {upper ? w.z : w.x, upper ? w.w : w.y, w.z, w.w};
 #pragma unroll
-        for (int s = 0; s < V / 2; ++s) {
-          f[s].x = keep >> (2 * s) & 1 ? f[s].x * drop.scale : 0.0f;
-          f[s].y = keep >> (2 * s + 1) & 1 ? f[s].y * drop.scale : 0.0f;
+          for (int s = 0; s < V / 2; ++s) {
+            f[s] = __fmul2_rn(f[s], both(drop.scale));
+            f[s].x = words[s] << 16 > drop.bound ? f[s].x : 0.0f;
+            f[s].y = words[s] > drop.bound ? f[s].y : 0.0f;
+          }
+        } else {
+          uint32_t keep = drop.keeps(w, unit) ? (1u << V) - 1 : 0;
+          if (left < V) {  // more units: one after the other
+            uint32_t u = unit;
+#pragma unroll 1
+            for (int i = left; i < V; i += drop.group) {
+              if ((++u & 7) == 0) w = drop.block(row, u >> 3);
+              const uint32_t from = 1u << i, rest = (1u << V) - from;
+              keep = drop.keeps(w, u) ? keep | rest : keep & ~rest;
+            }
+          }
+#pragma unroll
+          for (int s = 0; s < V / 2; ++s) {
+            f[s] = __fmul2_rn(f[s], both(drop.scale));
+            f[s].x = keep >> (2 * s) & 1 ? f[s].x : 0.0f;
+            f[s].y = keep >> (2 * s + 1) & 1 ? f[s].y : 0.0f;
+          }
         }
       }
-      Pack<T, V>::store(to, f);
+      Pack<T, V>::store(out + (long long)row * cols + col, f);
     }
   }
 }
 
 template <typename T, int V>
 static eqmp_status launch_drop(const T* x, long long ld, T* out, int rows, int cols, const DropArgs& d, cudaStream_t st) {
-  const long long vectors = (long long)rows * (cols / V), tile = kDropTile * kDropThreads;
-  const long long grid = (vectors + tile - 1) / tile;
+  const int vectors = cols / V;
+  DropShape sh;
+  sh.segments = (vectors + kDropThreads - 1) / kDropThreads;
+  sh.lanes = (vectors + sh.segments - 1) / sh.segments;
+  sh.rows_per_pass = kDropThreads / sh.lanes;
+  const int threads = (sh.lanes * sh.rows_per_pass + 31) / 32 * 32;
+  const int tile = kDropPasses * sh.rows_per_pass;
+  const long long grid = ((long long)rows + tile - 1) / tile * sh.segments;
   if (grid > INT32_MAX) return EQMP_ERR_UNSUPPORTED;
-  k_drop<T, V><<<(unsigned)grid, kDropThreads, 0, st>>>(x, ld, out, rows, cols, d);
+  const size_t smem = V == 1 ? (size_t)(sh.lanes / 8 + 2) * tile : 0;
+  k_drop<T, V><<<(unsigned)grid, threads, smem, st>>>(x, ld, out, rows, cols, d, sh);
   return cuda_status(cudaGetLastError());
 }
 

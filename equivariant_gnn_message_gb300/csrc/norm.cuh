@@ -43,6 +43,18 @@ __device__ __forceinline__ uint4 philox(uint32_t c0, uint32_t c1, uint32_t c2, u
   return make_uint4(c0, c1, c2, c3);
 }
 
+// The first three rounds take the block index (c0) and the row (c1) apart: of
+// their six products two are constant for a column block over all rows, one
+// for a row over all blocks, one for a call.  A kernel whose lanes keep their
+// columns forms those once and has 15 products a block left of 20.
+struct PhiloxRow {
+  uint32_t hi, lo;  // of the second round's first product
+};
+struct PhiloxBlock {
+  uint32_t e0, e1, e2, e3;
+};
+constexpr uint32_t kPhiloxM0 = 0xD2511F53u, kPhiloxM1 = 0xCD9E8D57u, kPhiloxW0 = 0x9E3779B9u, kPhiloxW1 = 0xBB67AE85u;
+
 struct DropArgs {
   unsigned long long seed, offset;
   const unsigned long long* step;  // device, added to offset; may be NULL
@@ -72,6 +84,35 @@ struct Dropper {
     group = d.group;
   }
   __device__ __forceinline__ uint4 block(uint32_t row, uint32_t blk) const { return philox(blk, row, o0, o1, k0, k1); }
+  __device__ __forceinline__ PhiloxBlock of_block(uint32_t blk) const {
+    const uint32_t c2 = __umulhi(blk, kPhiloxM0) ^ o1 ^ k1, lo = o0 * kPhiloxM1;
+    const uint32_t c0 = __umulhi(c2, kPhiloxM1) ^ lo ^ (k0 + kPhiloxW0);
+    PhiloxBlock b;
+    b.e0 = blk * kPhiloxM0 ^ (k1 + kPhiloxW1);
+    b.e1 = c2 * kPhiloxM1 ^ (k0 + 2 * kPhiloxW0);
+    b.e2 = __umulhi(c0, kPhiloxM0) ^ (k1 + 2 * kPhiloxW1);
+    b.e3 = c0 * kPhiloxM0;
+    return b;
+  }
+  __device__ __forceinline__ PhiloxRow of_row(uint32_t row) const {
+    const uint32_t c0 = __umulhi(o0, kPhiloxM1) ^ row ^ k0;
+    return PhiloxRow{__umulhi(c0, kPhiloxM0), c0 * kPhiloxM0};
+  }
+  // block(row, blk) from the two.
+  __device__ __forceinline__ uint4 block(const PhiloxRow& r, const PhiloxBlock& b) const {
+    unsigned long long m = (unsigned long long)(r.hi ^ b.e0) * kPhiloxM1;
+    uint32_t c0 = (uint32_t)(m >> 32) ^ b.e1, c1 = (uint32_t)m, c2 = b.e2 ^ r.lo, c3 = b.e3;
+#pragma unroll
+    for (uint32_t i = 3; i < 10; ++i) {
+      const unsigned long long a = (unsigned long long)c0 * kPhiloxM0;
+      m = (unsigned long long)c2 * kPhiloxM1;
+      c0 = (uint32_t)(m >> 32) ^ c1 ^ (k0 + i * kPhiloxW0);
+      c1 = (uint32_t)m;
+      c2 = (uint32_t)(a >> 32) ^ c3 ^ (k1 + i * kPhiloxW1);
+      c3 = (uint32_t)a;
+    }
+    return make_uint4(c0, c1, c2, c3);
+  }
   __device__ __forceinline__ bool keeps(const uint4& w, uint32_t unit) const {
     const uint32_t a = (unit & 4) ? w.z : w.x, b = (unit & 4) ? w.w : w.y;
     const uint32_t v = (unit & 2) ? b : a;
@@ -82,29 +123,12 @@ struct Dropper {
     const uint32_t unit = (uint32_t)col / (uint32_t)group;
     return keeps(block(row, unit >> 3), unit) ? v * scale : 0.0f;
   }
-  // Bit i: column col + i of the row is kept, i < n <= 8; col is a multiple
-  // of n, or n is 8 and col a multiple of 8.
-  __device__ __forceinline__ uint32_t keep_bits(uint32_t row, int col, int n) const {
+  // Bit i: unit i of the block is kept.
+  __device__ __forceinline__ uint32_t keep_bits(const uint4& w) const {
     uint32_t keep = 0;
-    if (group == 1) {
-      const uint4 w = block(row, (uint32_t)col >> 3);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) keep |= (uint32_t)keeps(w, i) << i;
-      return (keep >> (col & 7)) & ((1u << n) - 1);
-    }
-    // the units that the columns touch, one after the other
-    uint32_t unit = (uint32_t)col / (uint32_t)group, blk = unit >> 3;
-    int end = (int)((unit + 1) * (uint32_t)group) - col;  // of the unit, counted from col
-    uint4 w = block(row, blk);
-#pragma unroll 1
-    for (int from = 0;;) {
-      if (keeps(w, unit)) keep |= (end >= n ? 1u << n : 1u << end) - (1u << from);
-      if (end >= n) return keep;
-      from = end;
-      end += group;
-      ++unit;
-      if (unit >> 3 != blk) w = block(row, blk = unit >> 3);
-    }
+    for (int i = 0; i < 8; ++i) keep |= (uint32_t)keeps(w, i) << i;
+    return keep;
   }
 };
 
@@ -319,6 +343,7 @@ static __global__ void __launch_bounds__(kSumX * kSumY) k_norm_bwd_sum(NormArgs 
   __shared__ float red[kSumY][kSumX];
   const long long M = (long long)(L + 2) * a.C, m = (long long)blockIdx.x * kSumX + threadIdx.x;
   float t = 0.0f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // until the kernel that writes the parts is done
   if (m < M) {
 #pragma unroll 8
     for (int p = threadIdx.y; p < a.parts; p += kSumY) t += a.part[p * M + m];

@@ -102,6 +102,113 @@ __device__ __forceinline__ void put_pairs(T* row, const uint32_t (&col)[NV], con
   }
 }
 
+// ---------------------------------------------------------------- feed
+// The vectors of the rows to come.  A lane copies its own vectors of the next
+// DEPTH - 1 rows into shared memory asynchronously (cp.async; 0 is filled in
+// for what lies outside of a row) and reads nothing but its own copies, so no
+// barrier is needed, and what is on the way costs no registers.  Single bf16
+// values are too small for such copies; they wait in registers, one row ahead.
+template <typename T, int V, int NV, int STREAMS, int WORDS>
+struct Feed {
+  static constexpr int B = sizeof(T) * V;  // bytes of a vector
+  static constexpr bool RING = B >= 4;
+  static constexpr int ROW = STREAMS * NV * B + WORDS * 4;  // bytes of a lane and row
+  static constexpr int DEPTH = !RING ? 2 : ROW <= 48 ? 4 : ROW <= 144 ? 3 : 2;
+  static constexpr int BYTES = RING ? DEPTH * ROW : 0;  // of shared memory, a lane
+  uint32_t ring, at;  // the ring; the place in it that is loaded next
+  uint32_t step;      // bytes between a lane's vectors
+  Pack<T, V> reg[RING ? 1 : STREAMS * NV];
+  float word[RING ? 1 : WORDS ? WORDS : 1];
+
+  __device__ __forceinline__ explicit Feed(uint8_t* smem) : at(0) {
+    step = blockDim.x * B;
+    ring = RING ? smem_u32(smem) : 0;
+  }
+  __device__ __forceinline__ uint32_t row_bytes() const { return blockDim.x * ROW; }
+  __device__ __forceinline__ void load(int stream, int j, const T* p, bool ok) {
+    if constexpr (RING) {
+      const uint32_t to = ring + at + (stream * NV + j) * step + threadIdx.x * B;
+      if constexpr (B == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(ok ? 16 : 0) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(p), "r"(ok ? 4 : 0) : "memory");
+    } else {
+      if (ok)
+        reg[RING ? 0 : stream * NV + j].load(p);
+      else
+        reg[RING ? 0 : stream * NV + j].zero();
+    }
+  }
+  __device__ __forceinline__ void load_word(int k, const float* p, bool ok) {
+    if constexpr (RING) {
+      const uint32_t to = ring + at + STREAMS * NV * step + (k * blockDim.x + threadIdx.x) * 4;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(p), "r"(ok ? 4 : 0) : "memory");
+    } else {
+      word[RING ? 0 : k] = ok ? *p : 0.0f;
+    }
+  }
+  // After a row's loads: they are on the way.
+  __device__ __forceinline__ void loaded() {
+    if constexpr (RING) {
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      at += row_bytes();
+      if (at == DEPTH * row_bytes()) at = 0;
+    }
+  }
+  // Waits for the oldest row and returns its place, for get().  The place that
+  // the next load() fills is the one before it, read a round ago.
+  __device__ __forceinline__ uint32_t wait() {
+    if constexpr (RING) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 2) : "memory");
+      const uint32_t old = at + row_bytes();
+      return ring + (old == DEPTH * row_bytes() ? 0 : old);
+    }
+    return 0;
+  }
+  // Waits for all copies, those that only fill in zeros included.
+  __device__ __forceinline__ void drain() const {
+    if constexpr (RING) asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  __device__ __forceinline__ void get(uint32_t place, int stream, float2 (&p)[NV * V / 2]) const {
+    Pack<T, V> v[NV];
+    if constexpr (RING) {
+      const uint32_t from = place + stream * NV * step + threadIdx.x * B;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if constexpr (B == 16) {
+          uint32_t a, b, c, d;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+                       : "r"(from + j * step));
+          if constexpr (V == 4)
+            v[j].v = make_float4(__uint_as_float(a), __uint_as_float(b), __uint_as_float(c), __uint_as_float(d));
+          else
+            v[j].v = make_uint4(a, b, c, d);
+        } else {
+          float f;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(from + j * step));
+          v[j].v = f;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) v[j] = reg[RING ? 0 : stream * NV + j];
+    }
+    get_pairs<T, V, NV>(v, p);
+  }
+  __device__ __forceinline__ float get_word(uint32_t place, int k) const {
+    if constexpr (RING) {
+      float f;
+      asm volatile("ld.shared.f32 %0, [%1];"
+                   : "=f"(f)
+                   : "r"(place + STREAMS * NV * step + (k * blockDim.x + threadIdx.x) * 4));
+      return f;
+    } else {
+      return word[RING ? 0 : k];
+    }
+  }
+};
+
 // ---------------------------------------------------------------- slots
 // What a lane knows of its columns.  Values i = 0..V-1 of a vector fall into
 // GROUPS of one degree: all of them (L = 0, or V = 1), the first and the other
@@ -157,14 +264,13 @@ struct Slots {
         p[s] = make_float2(g[2 * s % GROUPS], g[(2 * s + 1) % GROUPS]);
     }
   }
-  // The sums of the pairs put to their degrees, out[FROM + l].
-  template <int FROM, int N>
-  __device__ __forceinline__ void by_degree(const float2 (&p)[PAIRS], float (&out)[N]) const {
+  // The sums of the pairs put to their degrees.
+  __device__ __forceinline__ void by_degree(const float2 (&p)[PAIRS], float* out) const {
     if constexpr (L == 0) {
       float2 t = p[0];
 #pragma unroll
       for (int s = 1; s < PAIRS; ++s) t = __fadd2_rn(t, p[s]);
-      out[FROM] = t.x + t.y;
+      out[0] = t.x + t.y;
     } else {
       float g[GROUPS];
       if constexpr (V == 1) {
@@ -184,94 +290,131 @@ struct Slots {
         float t = cls[0] == l ? g[0] : 0.0f;
 #pragma unroll
         for (int k = 1; k < GROUPS; ++k) t += cls[k] == l ? g[k] : 0.0f;
-        out[FROM + l] = t;
+        out[l] = t;
       }
     }
   }
 };
 
 // ---------------------------------------------------------------- dropout
-// Which of a lane's values the dropout keeps.  V = 1: the group forms the keep
-// bits of its row together, eight columns a byte, in shared memory (form();
-// the caller waits until it is visible).  V > 1: each lane draws for its own
-// vectors; where a unit is at least as wide as a vector, a vector touches two
-// units at most, which are found once (meta: the first unit, and how many of
-// the vector's values it has).
-constexpr int kKeepBytes = kMaxRowThreads * 16 / 8 + kRowThreads;  // bits of a CTA's rows, a byte each begun
+// Which of a lane's values the dropout keeps.  DIRECT (a draw per element,
+// V > 1): each lane draws for its own vectors.  Else the group forms the keep
+// bits of its rows' units together, eight a byte, in shared memory, and each
+// value looks its unit up: a channel's draw is made once, not once per vector
+// that has a part of it.  The bits are formed for as many rows at a time as
+// the lanes have blocks for (a batch), so that no warp of a group draws for
+// the others while they wait; the caller waits until they are visible.
+constexpr int kKeepBytes = kMaxRowThreads * 16 / 8 + kRowThreads;  // a bit a value, a byte each row begun
 
-template <int L, int V, int NV>
+template <int L, int V, int NV, bool DIRECT>
 struct Keeps {
-  uint32_t meta[NV];
-  uint8_t* bits;  // V = 1: of this row group, two halves taken in turn
-  int bytes;
-  int half;
+  PhiloxBlock blocks[DIRECT ? NV : 1];
+  uint32_t unit[DIRECT ? 1 : NV];       // of a vector's first value
+  int left[V == 1 || DIRECT ? 1 : NV];  // how many of the vector's values it has
+  uint8_t* bits;                        // of this row group, two halves taken in turn
+  int bytes;                            // of a row
+  int batch, my_row, my_byte;           // rows of a batch; the place that this lane forms
+  int half, at_row;                     // the current row's half and place in the batch
   __device__ __forceinline__ Keeps(const Dropper& d, const Slots<L, V, NV>& at, const RowShape& sh, int cols,
                                    uint8_t* smem) {
-    if constexpr (V == 1) {
-      bytes = (cols + 7) / 8;
-      bits = smem + (threadIdx.x / sh.lanes) * bytes;
-      half = 0;
+    if (!d.on) return;
+    if constexpr (DIRECT) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) blocks[j] = d.of_block(at.col[j] >> 3);
     } else {
       const uint32_t group = L ? (uint32_t)at.K : (uint32_t)d.group;
+      bytes = ((uint32_t)cols / group + 7) / 8;
+      batch = bytes < sh.lanes ? sh.lanes / bytes : 1;
+      my_row = bytes < sh.lanes ? at.lane / bytes : 0;
+      my_byte = at.lane - my_row * bytes;
+      bits = smem + (threadIdx.x / sh.lanes) * bytes * batch;
+      half = at_row = 0;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const uint32_t unit = at.col[j] / group, left = group - (at.col[j] - unit * group);
-        meta[j] = unit << 4 | (left < V ? left : V);
+        unit[j] = at.col[j] / group;
+        if (V > 1) left[V > 1 ? j : 0] = (int)((unit[j] + 1) * group - at.col[j]);
       }
     }
   }
-  // V = 1: the bits of a row, by all lanes of its group.
-  __device__ __forceinline__ void form(const Dropper& d, const Slots<L, V, NV>& at, const RowShape& sh, int row) {
-    if constexpr (V == 1) {
-      half ^= 1;
-      for (int y = at.lane; y < bytes; y += sh.lanes) bits[half * kKeepBytes + y] = (uint8_t)d.keep_bits(row, 8 * y, 8);
+  // The bits of a batch of rows, `stride` apart from `row` on, into half `to`.
+  __device__ __forceinline__ void form(const Dropper& d, const RowShape& sh, int row, int stride, int to) {
+    if constexpr (!DIRECT) {
+      if (my_row < batch)
+        for (int y = my_byte; y < bytes; y += sh.lanes)
+          bits[to * kKeepBytes + my_row * bytes + y] = (uint8_t)d.keep_bits(d.block(row + my_row * stride, y));
+      if (sh.lanes <= 32) __syncwarp();
     }
   }
-  // The values of a row, p, with the dropout applied.
+  // Before a row's barrier, with its bits wanted behind it.
+  __device__ __forceinline__ void form_now(const Dropper& d, const RowShape& sh, int row, int stride) {
+    if constexpr (!DIRECT) {
+      if (at_row == 0) form(d, sh, row, stride, half);
+    }
+  }
+  // Before a row's barrier, with the next row's bits wanted in front of that one's.
+  __device__ __forceinline__ void form_next(const Dropper& d, const RowShape& sh, int row, int stride) {
+    if constexpr (!DIRECT) {
+      if (at_row + 1 == batch) form(d, sh, row + stride, stride, half ^ 1);
+    }
+  }
+  __device__ __forceinline__ void next_row() {
+    if constexpr (!DIRECT) {
+      if (++at_row == batch) {
+        at_row = 0;
+        half ^= 1;
+      }
+    }
+  }
+  __device__ __forceinline__ bool kept(uint32_t n) const {
+    return bits[half * kKeepBytes + at_row * bytes + (n >> 3)] >> (n & 7) & 1;
+  }
+  // The values p of the current row, `row`, with the dropout applied.
   __device__ __forceinline__ void apply(const Dropper& d, const Slots<L, V, NV>& at, int row,
                                         float2 (&p)[NV * V / 2]) const {
-    if constexpr (V == 1) {
+    if constexpr (DIRECT) {
+      const PhiloxRow pr = d.of_row(row);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float2* f = p + j * (V / 2);
+        const uint4 w = d.block(pr, blocks[j]);
+        const bool upper = V == 4 && (at.col[j] & 4);
+        const uint32_t words[4] = {upper ? w.z : w.x, upper ? w.w : w.y, w.z, w.w};
+#pragma unroll
+        for (int s = 0; s < V / 2; ++s) {
+          f[s] = __fmul2_rn(f[s], both(d.scale));
+          f[s].x = words[s] << 16 > d.bound ? f[s].x : 0.0f;
+          f[s].y = words[s] > d.bound ? f[s].y : 0.0f;
+        }
+      }
+    } else if constexpr (V == 1) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float& f = j & 1 ? p[j / 2].y : p[j / 2].x;
-        const bool keep = at.has[j] && (bits[half * kKeepBytes + (at.col[j] >> 3)] >> (at.col[j] & 7)) & 1;
-        f = keep ? f * d.scale : 0.0f;
+        f = at.has[j] && kept(unit[j]) ? f * d.scale : 0.0f;
       }
     } else {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float2* f = p + j * (V / 2);
-        if (L == 0 && d.group == 1) {
-          const uint4 w = d.block(row, at.col[j] >> 3);
-          const bool upper = V == 4 && (at.col[j] & 4);
-          const uint32_t words[4] = {upper ? w.z : w.x, upper ? w.w : w.y, w.z, w.w};
-#pragma unroll
-          for (int s = 0; s < V / 2; ++s) {
-            f[s].x = words[s] << 16 > d.bound ? f[s].x * d.scale : 0.0f;
-            f[s].y = words[s] > d.bound ? f[s].y * d.scale : 0.0f;
-          }
-        } else if (L > 0 || d.group >= V) {
-          const uint32_t unit = meta[j] >> 4;
-          const int n = meta[j] & 15;
-          uint4 w = d.block(row, unit >> 3);
-          const bool k0 = d.keeps(w, unit);
-          bool k1 = k0;
+        const int n = left[j];
+        uint32_t keep = 0;  // bits of the vector's values
+        if (at.has[j]) {
+          keep = kept(unit[j]) ? (1u << V) - 1 : 0;
           if ((L == 0 || at.K % V) && n < V) {
-            if ((unit & 7) == 7) w = d.block(row, (unit + 1) >> 3);
-            k1 = d.keeps(w, unit + 1);
+            if (L > 0 || d.group >= V) {  // two units
+              keep = (keep & ((1u << n) - 1)) | (kept(unit[j] + 1) ? (1u << V) - (1u << n) : 0);
+            } else {
+              keep = 0;
+#pragma unroll 1
+              for (int i = 0; i < V; ++i) keep |= (uint32_t)kept((at.col[j] + i) / (uint32_t)d.group) << i;
+            }
           }
+        }
 #pragma unroll
-          for (int s = 0; s < V / 2; ++s) {
-            f[s].x = (2 * s < n ? k0 : k1) ? f[s].x * d.scale : 0.0f;
-            f[s].y = (2 * s + 1 < n ? k0 : k1) ? f[s].y * d.scale : 0.0f;
-          }
-        } else {
-          const uint32_t keep = d.keep_bits(row, at.col[j], V);
-#pragma unroll
-          for (int s = 0; s < V / 2; ++s) {
-            f[s].x = (keep >> (2 * s)) & 1 ? f[s].x * d.scale : 0.0f;
-            f[s].y = (keep >> (2 * s + 1)) & 1 ? f[s].y * d.scale : 0.0f;
-          }
+        for (int s = 0; s < V / 2; ++s) {
+          f[s] = __fmul2_rn(f[s], both(d.scale));
+          f[s].x = keep >> (2 * s) & 1 ? f[s].x : 0.0f;
+          f[s].y = keep >> (2 * s + 1) & 1 ? f[s].y : 0.0f;
         }
       }
     }
@@ -280,46 +423,37 @@ struct Keeps {
 
 // ---------------------------------------------------------------- sums
 // Sums N values over the lanes of each group, in a fixed order, and leaves
-// them spread over the lanes: value n is then fetched by a shuffle.  For N > 2
-// the values are halved as the lanes are (each lane passes on the half that it
-// does not keep), so that N values take about as many shuffles as log2 G + N.
+// them spread over the lanes: value n is then fetched by a shuffle.  The
+// values are halved as the lanes are (each lane passes on the half that it
+// does not keep), so that N values take about as many shuffles as N + log2 G.
 // Groups of several warps exchange their warps' sums through red (two halves,
 // taken in turn, so that one barrier per sum is enough; every thread of the
-// CTA takes part).  N = 2 needs groups of at least 2 lanes, N > 2 of 8.
+// CTA takes part).  A group has at least as many lanes as N rounded up to a
+// power of two.
+constexpr int pow2_above(int n) { return n <= 1 ? 1 : 2 * pow2_above((n + 1) / 2); }
+
 template <int N>
 struct GroupSum {
-  static constexpr int P = N <= 1 ? 1 : N <= 2 ? 2 : N <= 4 ? 4 : 8;  // N rounded up to a power of two
-  static constexpr int kRed = 2 * (kMaxRowThreads / 32) * P;          // floats of red
+  static constexpr int P = pow2_above(N);
+  static_assert(P <= 16, "more values than half a warp");
+  static constexpr int kRed = 2 * (kMaxRowThreads / 32) * P;  // floats of red
   int lanes, warps, first;  // of the group: lanes, warps, its first warp
-  int base;                 // of the group within the warp
+  int base, each;           // value n is at lane base + n each
   float* red;
   int half;
-  float val;  // after sum(): this lane's value
+  float val;
   __device__ __forceinline__ GroupSum(int lanes_, float* red_) : lanes(lanes_), red(red_), half(0), val(0.0f) {
     warps = lanes_ >> 5;
     first = warps > 1 ? (int)(threadIdx.x >> 5) / warps * warps : 0;
     base = lanes_ < 32 ? (int)(threadIdx.x & 31) / lanes_ * lanes_ : 0;
+    each = lanes_ > 32 ? 1 : lanes_ / P;
   }
-  // The lane that holds value n.
-  __device__ __forceinline__ int source(int n) const {
-    if (N == 1) return threadIdx.x & 31;
-    if (lanes > 32) return n;
-    if (N == 2) return base + n * (lanes >> 1);
-    int lane = base;
-    if (P == 8) lane += (n >> 2 & 1) * (lanes >> 1) + (n >> 1 & 1) * (lanes >> 2) + (n & 1) * (lanes >> 3);
-    if (P == 4) lane += (n >> 1 & 1) * (lanes >> 1) + (n & 1) * (lanes >> 2);
-    return lane;
-  }
-  __device__ __forceinline__ float fetch(int source_lane) const {
-    return N == 1 ? val : __shfl_sync(0xffffffffu, val, source_lane);
-  }
+  __device__ __forceinline__ float fetch(int n) const { return __shfl_sync(0xffffffffu, val, base + n * each); }
   __device__ __forceinline__ void operator()(const float (&v)[N]) {
-    const int in_warp = lanes < 32 ? lanes : 32;
-    int o = in_warp >> 1;
+    int o = (lanes < 32 ? lanes : 32) >> 1;
     float x[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) x[i] = i < N ? v[i] : 0.0f;
-    int mine = 0;  // the value of this lane
 #pragma unroll
     for (int n = P / 2; n > 0; n >>= 1) {
       const bool up = threadIdx.x & o;
@@ -328,7 +462,6 @@ struct GroupSum {
         const float send = up ? x[i] : x[i + n], keep = up ? x[i + n] : x[i];
         x[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
       }
-      mine += up ? n : 0;
       o >>= 1;
     }
     for (; o > 0; o >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
@@ -336,127 +469,133 @@ struct GroupSum {
     if (lanes <= 32) return;
     const int lane = threadIdx.x & 31;
     float* buf = red + half * (kRed / 2);
-    if (lane % (32 / P) == 0) buf[(threadIdx.x >> 5) * P + mine] = val;
+    if (lane % (32 / P) == 0) buf[(threadIdx.x >> 5) * P + lane / (32 / P)] = val;
     __syncthreads();
     float t = 0.0f;
     for (int k = lane / P; k < warps; k += 32 / P) t += buf[(first + k) * P + lane % P];
     for (o = P; o < 32 && o < warps * P; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    val = N == 1 ? __shfl_sync(0xffffffffu, t, 0) : t;
+    val = t;
     half ^= 1;
   }
 };
 
-// ---------------------------------------------------------------- forward
-// One pass: each value is loaded once, kept in registers through the mean and
-// the centred squares, and stored once.  The next row's vectors are loaded
-// before the sums of the current one are formed.  FUSED: with a residual sum
-// or dropout in front.
-template <typename T, int L, int V, int NV, bool FUSED>
-__global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowShape sh) {
+// What stands in front of the norm, and behind it in the backward pass.
+enum : int {
+  kPlain = 0,   // nothing
+  kMixed = 1,   // a residual sum, dropout by units, several results
+  kDirect = 2,  // as kMixed, with dropout by element drawn lane by lane (V > 1, L = 0)
+};
+
+// The weights of a lane's values.
+template <int L, int V, int NV>
+__device__ __forceinline__ void load_weights(const Slots<L, V, NV>& at, const NormArgs& a, float2 (&w)[NV * V / 2]) {
   using S = Slots<L, V, NV>;
-  constexpr int P = NV * V / 2, PV = S::PAIRS, NS = L + 1;
-  constexpr bool EACH = L == 0 || V == 1;  // a bias per value; else one per vector, which has at most one degree 0
-  __shared__ float red1[GroupSum<1>::kRed], red2[GroupSum<NS>::kRed];
-  __shared__ uint8_t bits[FUSED && V == 1 ? 2 * kKeepBytes : 1];
-  const S at(sh, a.cols);
-  GroupSum<1> sum1(sh.lanes, red1);
-  GroupSum<NS> sum2(sh.lanes, red2);
-  const Dropper drop(a.drop);
-  Keeps<L, V, NV> keeps(drop, at, sh, a.cols, bits);
-  float2 w[P], b[EACH ? P : NV], m[V == 1 ? P : NV];  // m: -1 where a value is one of the row's, else 0
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = (int)(at.col[j] + i) / S::K;
       int l = 0;
-      if (L) {
-        l = at.cls[S::GROUPS == 1 ? 0 : S::FOURS ? i / 4 * 2 + (i % 4 > 0) : i];
-      }
-      const float wi = at.has[j] && a.w ? a.w[l * a.C + c] : 1.0f;
-      const float bi = at.has[j] && a.b && l == 0 ? a.b[c] : 0.0f;
-      const float mi = at.has[j] ? -1.0f : 0.0f;
+      if constexpr (L > 0) l = at.cls[S::GROUPS == 1 ? 0 : S::FOURS ? i / 4 * 2 + (i % 4 > 0) : i];
+      const float t = at.has[j] && a.w ? a.w[l * a.C + c] : 1.0f;
       const int e = j * V + i;
-      (e & 1 ? w[e / 2].y : w[e / 2].x) = wi;
-      if (EACH)
-        (e & 1 ? b[e / 2].y : b[e / 2].x) = bi;
-      else if (i == 0 || l == 0)
-        b[EACH ? 0 : j] = both(bi);
-      if (V == 1)
-        (e & 1 ? m[e / 2].y : m[e / 2].x) = mi;
-      else
-        m[V == 1 ? 0 : j] = both(mi);
+      (e & 1 ? w[e / 2].y : w[e / 2].x) = t;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- forward
+// One pass: each value is loaded once, kept in registers through the mean and
+// the centred squares, and stored once.
+template <typename T, int L, int V, int NV, int MODE>
+__global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowShape sh) {
+  using S = Slots<L, V, NV>;
+  using F = Feed<T, V, NV, MODE ? 2 : 1, 0>;
+  constexpr int P = NV * V / 2, PV = S::PAIRS, NS = L + 1;
+  constexpr bool EACH = L == 0 || V == 1;  // a bias per value; else one per vector, which has at most one degree 0
+  __shared__ float red1[GroupSum<1>::kRed], red2[GroupSum<NS>::kRed];
+  __shared__ uint8_t bits[MODE == kMixed ? 2 * kKeepBytes : 1];
+  extern __shared__ __align__(16) uint8_t ring[];
+  const S at(sh, a.cols);
+  const int stride = gridDim.x * sh.groups;
+  int row = blockIdx.x * sh.groups + threadIdx.x / sh.lanes;
+  F feed(ring);
+  const T* x = static_cast<const T*>(a.x) + row * a.x_ld;
+  const T* r = static_cast<const T*>(a.r) + row * a.r_ld;
+  int ahead = row;  // the row that is loaded next
+  auto load_row = [&]() {
+    const bool live = ahead < a.rows;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      feed.load(0, j, x + at.col[j], at.has[j] && live);
+      if (MODE && a.r) feed.load(1, j, r + at.col[j], at.has[j] && live);
+    }
+    feed.loaded();
+    ahead += stride;
+    x += stride * a.x_ld;
+    if (MODE) r += stride * a.r_ld;
+  };
+#pragma unroll 1
+  for (int d = 0; d < F::DEPTH - 1; ++d) load_row();
+  GroupSum<1> sum1(sh.lanes, red1);
+  GroupSum<NS> sum2(sh.lanes, red2);
+  const Dropper drop(a.drop);
+  Keeps<L, V, NV, MODE == kDirect> keeps(drop, at, sh, a.cols, bits);
+  float2 w[P], b[EACH ? P : NV];
+  bool all = true;  // whether the lane's values are all of the row
+  load_weights<L, V, NV>(at, a, w);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    all = all && at.has[j];
+    if constexpr (EACH) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = j * V + i, c = (int)(at.col[j] + i) / S::K;
+        (e & 1 ? b[e / 2].y : b[e / 2].x) = at.has[j] && a.b && at.cls[0] == 0 ? a.b[c] : 0.0f;
+      }
+    } else {
+      const int c = (int)(at.col[j] + V - 1) / S::K;  // the channel that begins in the vector, if one does
+      b[j] = both(at.has[j] && a.b && c * S::K >= (int)at.col[j] ? a.b[c] : 0.0f);
     }
   }
   const float inv = 1.0f / (float)a.C;
   float scale[S::GROUPS];
-  int from[S::GROUPS];
 #pragma unroll
-  for (int g = 0; g < S::GROUPS; ++g) {
-    scale[g] = inv / (float)(2 * at.cls[g] + 1);
-    from[g] = sum2.source(at.cls[g]);
-  }
-  const int stride = gridDim.x * sh.groups;
-  int row = blockIdx.x * sh.groups + threadIdx.x / sh.lanes;
-  const T* x = static_cast<const T*>(a.x) + (long long)row * a.x_ld;
-  const T* r = static_cast<const T*>(a.r) + (long long)row * a.r_ld;
-  Pack<T, V> nx[NV], nr[FUSED ? NV : 1];
-  auto fetch = [&](bool live) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (at.has[j] && live)
-        nx[j].load(x + at.col[j]);
-      else
-        nx[j].zero();
-      if (FUSED) {
-        if (at.has[j] && live && a.r)
-          nr[FUSED ? j : 0].load(r + at.col[j]);
-        else
-          nr[FUSED ? j : 0].zero();
-      }
-    }
-  };
-  fetch(row < a.rows);
-  if (FUSED && V == 1 && drop.on) {
-    keeps.form(drop, at, sh, row);
+  for (int g = 0; g < S::GROUPS; ++g) scale[g] = inv / (float)(2 * at.cls[g] + 1);
+  all = __all_sync(0xffffffffu, all);
+  if (MODE == kMixed && drop.on) {
+    keeps.form(drop, sh, row, stride, 0);
     __syncthreads();
   }
   // the same number of rounds for every group of the CTA
   for (int base = blockIdx.x * sh.groups; base < a.rows; base += stride, row += stride) {
     float2 v[P], acc[PV];
-    get_pairs<T, V, NV>(nx, v);
-    if constexpr (FUSED) {
+    const uint32_t place = feed.wait();
+    feed.get(place, 0, v);
+    if constexpr (MODE != kPlain) {
       if (drop.on) keeps.apply(drop, at, row, v);
       if (a.r) {
         float2 f[P];
-        get_pairs<T, V, NV>(nr, f);
+        feed.get(place, 1, f);
 #pragma unroll
         for (int p = 0; p < P; ++p) v[p] = __fadd2_rn(v[p], f[p]);
       }
     }
-    x += stride * a.x_ld;
-    r += stride * a.r_ld;
-    fetch(row + stride < a.rows);
-    if (FUSED && V == 1 && drop.on) {  // the next row's, seen after a barrier of this row's sums
-      keeps.form(drop, at, sh, row + stride);
-      if (sh.lanes <= 32) __syncwarp();
-    }
+    load_row();
+    if (MODE == kMixed && drop.on) keeps.form_next(drop, sh, row, stride);
     const bool live = row < a.rows;
     const long long out = (long long)row * a.cols;
-    if (FUSED && a.s && live) put_pairs<T, V, NV>(static_cast<T*>(a.s) + out, at.col, at.has, v);
+    if (MODE && a.s && live) put_pairs<T, V, NV>(static_cast<T*>(a.s) + out, at.col, at.has, v);
     // the mean of degree 0
-#pragma unroll
-    for (int s = 0; s < PV; ++s) {
-      acc[s] = v[s];
-#pragma unroll
-      for (int p = s + PV; p < P; p += PV) acc[s] = __fadd2_rn(acc[s], v[p]);
-    }
     float part[1] = {0.0f};
 #pragma unroll
     for (int s = 0; s < PV; ++s) {
       if (!S::may0(s)) continue;
-      if (L) acc[s] = __fmul2_rn(acc[s], at.first[s]);
-      part[0] += acc[s].x + acc[s].y;
+      float2 t = v[s];
+#pragma unroll
+      for (int p = s + PV; p < P; p += PV) t = __fadd2_rn(t, v[p]);
+      if (L) t = __fmul2_rn(t, at.first[s]);
+      part[0] += t.x + t.y;
     }
     sum1(part);
     const float mean = sum1.fetch(0) * inv;
@@ -464,9 +603,14 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       if (!S::may0(p % PV)) continue;
-      float2 mu = both(mean);
-      if (L) mu = __fmul2_rn(mu, at.first[p % PV]);
-      v[p] = __ffma2_rn(mu, m[V == 1 ? p : p / PV], v[p]);
+      v[p] = L ? __ffma2_rn(both(-mean), at.first[p % PV], v[p]) : __fadd2_rn(both(-mean), v[p]);
+    }
+    if (!all) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        v[p].x = at.has[V == 1 ? 2 * p : p / PV] ? v[p].x : 0.0f;
+        v[p].y = at.has[V == 1 ? 2 * p + 1 : p / PV] ? v[p].y : 0.0f;
+      }
     }
 #pragma unroll
     for (int s = 0; s < PV; ++s) {
@@ -475,18 +619,19 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
       for (int p = s + PV; p < P; p += PV) acc[s] = __ffma2_rn(v[p], v[p], acc[s]);
     }
     float sq[NS];
-    at.template by_degree<0>(acc, sq);
+    at.by_degree(acc, sq);
     sum2(sq);
     float q[S::GROUPS];
 #pragma unroll
-    for (int g = 0; g < S::GROUPS; ++g) q[g] = rsqrtf(sum2.fetch(from[g]) * scale[g] + a.eps);
+    for (int g = 0; g < S::GROUPS; ++g) q[g] = rsqrtf(sum2.fetch(at.cls[g]) * scale[g] + a.eps);
     if (a.stats) {
       float* st = a.stats + (long long)row * (L + 2);
       const int l = at.lane < L ? at.lane : L;
-      const float ql = L ? rsqrtf(sum2.fetch(sum2.source(l)) * (inv / (float)(2 * l + 1)) + a.eps) : q[0];
+      const float ql = L ? rsqrtf(sum2.fetch(l) * (inv / (float)(2 * l + 1)) + a.eps) : q[0];
       if (live && at.lane <= L) st[1 + l] = ql;
       if (live && at.lane == 0) st[0] = mean;
     }
+    if (MODE == kMixed && drop.on) keeps.next_row();
     if (!live || !a.y) continue;
     float2 qs[PV];
     S::spread(q, qs);
@@ -509,98 +654,73 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
 // and dL/dx from the registers, while each lane adds g h and g of its columns
 // over all the rows of its group.  At the end the groups of a CTA are added in
 // their order through shared memory, the orders of a degree with them, and
-// the CTA's (L+2) C sums go to its part of the workspace.  FUSED: with dL/ds
-// of a residual stream, dropout, or both gradients asked for.
-template <typename T, int L, int V, int NV, bool FUSED>
+// the CTA's (L+2) C sums go to its part of the workspace.
+template <typename T, int L, int V, int NV, int MODE>
 __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, RowShape sh) {
   using S = Slots<L, V, NV>;
+  using F = Feed<T, V, NV, MODE ? 3 : 2, 1 + S::GROUPS>;
   constexpr int P = NV * V / 2, PV = S::PAIRS, NS = L + 2;
   constexpr bool EACH = L == 0 || V == 1;  // db per value; else per vector, which has at most one degree 0
   __shared__ float red[GroupSum<NS>::kRed];
-  __shared__ uint8_t bits[FUSED && V == 1 ? 2 * kKeepBytes : 1];
-  extern __shared__ float colsum[];  // [cols] g h, then [C] g
+  __shared__ uint8_t bits[MODE == kMixed ? 2 * kKeepBytes : 1];
+  extern __shared__ __align__(16) uint8_t ring[];  // at the end the column sums: [cols] g h, [C] g
   const S at(sh, a.cols);
+  const int stride = gridDim.x * sh.groups;
+  int row = blockIdx.x * sh.groups + threadIdx.x / sh.lanes;
+  F feed(ring);
+  const T* x = static_cast<const T*>(a.x) + row * a.x_ld;
+  const T* g = static_cast<const T*>(a.g) + row * a.g_ld;
+  const T* r = static_cast<const T*>(a.r) + row * a.r_ld;
+  const float* st = a.stats + (long long)row * (L + 2);
+  int ahead = row;  // the row that is loaded next
+  auto load_row = [&]() {
+    const bool live = ahead < a.rows;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      feed.load(0, j, x + at.col[j], at.has[j] && live);
+      feed.load(1, j, g + at.col[j], at.has[j] && live);
+      if (MODE && a.r) feed.load(2, j, r + at.col[j], at.has[j] && live);
+    }
+    feed.load_word(0, st, live);
+#pragma unroll
+    for (int k = 0; k < S::GROUPS; ++k) feed.load_word(1 + k, st + 1 + at.cls[k], live);
+    feed.loaded();
+    ahead += stride;
+    x += stride * a.x_ld;
+    g += stride * a.g_ld;
+    if (MODE) r += stride * a.r_ld;
+    st += (long long)stride * (L + 2);
+  };
+#pragma unroll 1
+  for (int d = 0; d < F::DEPTH - 1; ++d) load_row();
   GroupSum<NS> sum(sh.lanes, red);
   const Dropper drop(a.drop);
-  Keeps<L, V, NV> keeps(drop, at, sh, a.cols, bits);
+  Keeps<L, V, NV, MODE == kDirect> keeps(drop, at, sh, a.cols, bits);
   float2 w[P], dw[P], db[EACH ? P : NV];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (int)(at.col[j] + i) / S::K;
-      int l = 0;
-      if (L) l = at.cls[S::GROUPS == 1 ? 0 : S::FOURS ? i / 4 * 2 + (i % 4 > 0) : i];
-      const float wi = at.has[j] && a.w ? a.w[l * a.C + c] : 1.0f;
-      const int e = j * V + i;
-      (e & 1 ? w[e / 2].y : w[e / 2].x) = wi;
-    }
-  }
+  load_weights<L, V, NV>(at, a, w);
 #pragma unroll
   for (int p = 0; p < P; ++p) dw[p] = both(0.0f);
 #pragma unroll
   for (int p = 0; p < (EACH ? P : NV); ++p) db[p] = both(0.0f);
   const float inv = 1.0f / (float)a.C;
   float scale[S::GROUPS];
-  int from[S::GROUPS];
 #pragma unroll
-  for (int g = 0; g < S::GROUPS; ++g) {
-    scale[g] = -inv / (float)(2 * at.cls[g] + 1);
-    from[g] = sum.source(1 + at.cls[g]);
-  }
-  const int from0 = sum.source(0);
-  const int stride = gridDim.x * sh.groups;
-  int row = blockIdx.x * sh.groups + threadIdx.x / sh.lanes;
-  const T* x = static_cast<const T*>(a.x) + (long long)row * a.x_ld;
-  const T* g = static_cast<const T*>(a.g) + (long long)row * a.g_ld;
-  const T* r = static_cast<const T*>(a.r) + (long long)row * a.r_ld;
-  const float* st = a.stats + (long long)row * (L + 2);
-  Pack<T, V> nx[NV], ng[NV];
-  float nmean, nq[S::GROUPS];
-  auto fetch = [&](bool live) {
-    nmean = live ? st[0] : 0.0f;
-#pragma unroll
-    for (int k = 0; k < S::GROUPS; ++k) nq[k] = live ? st[1 + at.cls[k]] : 0.0f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (at.has[j] && live) {
-        nx[j].load(x + at.col[j]);
-        ng[j].load(g + at.col[j]);
-      } else {
-        nx[j].zero();
-        ng[j].zero();
-      }
-    }
-  };
-  fetch(row < a.rows);
+  for (int k = 0; k < S::GROUPS; ++k) scale[k] = -inv / (float)(2 * at.cls[k] + 1);
   for (int base = blockIdx.x * sh.groups; base < a.rows; base += stride, row += stride) {
     const bool live = row < a.rows;
-    float2 h[P], av[P], qs[PV];
-    Pack<T, V> cr[FUSED ? NV : 1];
+    float2 h[P], av[P], cr[MODE ? P : 1], qs[PV];
     float q[S::GROUPS];
-    get_pairs<T, V, NV>(nx, h);
-    get_pairs<T, V, NV>(ng, av);
-#pragma unroll
-    for (int k = 0; k < S::GROUPS; ++k) q[k] = nq[k];
-    const float2 mu = both(-nmean);
-    if constexpr (FUSED) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if (at.has[j] && live && a.r)
-          cr[j].load(r + at.col[j]);
-        else
-          cr[j].zero();
-      }
+    const uint32_t place = feed.wait();
+    feed.get(place, 0, h);
+    feed.get(place, 1, av);
+    if constexpr (MODE != kPlain && !F::RING) {
+      if (a.r) feed.get(place, 2, cr);
     }
-    x += stride * a.x_ld;
-    g += stride * a.g_ld;
-    r += stride * a.r_ld;
-    st += (long long)stride * (L + 2);
-    fetch(row + stride < a.rows);
-    if (FUSED && V == 1 && drop.on) {  // seen after the barrier of this row's sums
-      keeps.form(drop, at, sh, row);
-      if (sh.lanes <= 32) __syncwarp();
-    }
+    const float2 mu = both(-feed.get_word(place, 0));
+#pragma unroll
+    for (int k = 0; k < S::GROUPS; ++k) q[k] = feed.get_word(place, 1 + k);
+    load_row();
+    if (MODE == kMixed && drop.on) keeps.form_now(drop, sh, row, stride);
     S::spread(q, qs);
     float2 sa[PV], sah[PV];
 #pragma unroll
@@ -630,42 +750,51 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
       if (L) sa[s] = __fmul2_rn(sa[s], at.first[s]);
       tot[0] += sa[s].x + sa[s].y;
     }
-    at.template by_degree<1>(sah, tot);
+    at.by_degree(sah, tot + 1);
     sum(tot);
     // r = q a - (q mean(a h)) h - q mean(a) for degree 0
-    const float m0 = sum.fetch(from0) * -inv;
+    const float m0 = sum.fetch(0) * -inv;
     float c[S::GROUPS];
 #pragma unroll
-    for (int k = 0; k < S::GROUPS; ++k) c[k] = sum.fetch(from[k]) * scale[k] * q[k];
-    if (!live) continue;
-    float2 cs[PV], c0[PV];
+    for (int k = 0; k < S::GROUPS; ++k) c[k] = sum.fetch(1 + at.cls[k]) * scale[k] * q[k];
+    float2 cs[PV];
     S::spread(c, cs);
 #pragma unroll
-    for (int s = 0; s < PV; ++s) c0[s] = L ? __fmul2_rn(__fmul2_rn(qs[s], both(m0)), at.first[s]) : __fmul2_rn(qs[s], both(m0));
+    for (int s = 0; s < PV; ++s) {
+      if (!S::may0(s)) continue;
+      sa[s] = __fmul2_rn(qs[s], both(m0));
+      if (L) sa[s] = __fmul2_rn(sa[s], at.first[s]);
+    }
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int s = p % PV;
-      const float2 t = S::may0(s) ? __ffma2_rn(av[p], qs[s], c0[s]) : __fmul2_rn(av[p], qs[s]);
+      const float2 t = S::may0(s) ? __ffma2_rn(av[p], qs[s], sa[s]) : __fmul2_rn(av[p], qs[s]);
       av[p] = __ffma2_rn(h[p], cs[s], t);
     }
     const long long out = (long long)row * a.cols;
-    if constexpr (FUSED) {
+    if constexpr (MODE != kPlain) {
       if (a.r) {
-        get_pairs<T, V, NV>(cr, h);
+        if constexpr (F::RING) feed.get(place, 2, cr);
 #pragma unroll
-        for (int p = 0; p < P; ++p) av[p] = __fadd2_rn(av[p], h[p]);
+        for (int p = 0; p < P; ++p) av[p] = __fadd2_rn(av[p], cr[p]);
       }
-      if (a.gr) put_pairs<T, V, NV>(static_cast<T*>(a.gr) + out, at.col, at.has, av);
+      if (a.gr && live) put_pairs<T, V, NV>(static_cast<T*>(a.gr) + out, at.col, at.has, av);
       if (a.gx) {
         if (drop.on) keeps.apply(drop, at, row, av);
-        put_pairs<T, V, NV>(static_cast<T*>(a.gx) + out, at.col, at.has, av);
+        if (live) put_pairs<T, V, NV>(static_cast<T*>(a.gx) + out, at.col, at.has, av);
       }
+      if (MODE == kMixed && drop.on) keeps.next_row();
     } else {
       T* dst = static_cast<T*>(a.gx ? a.gx : a.gr);
-      if (dst) put_pairs<T, V, NV>(dst + out, at.col, at.has, av);
+      if (dst && live) put_pairs<T, V, NV>(dst + out, at.col, at.has, av);
     }
   }
+  // the sums' kernel may be launched; it waits until this one is done
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!a.gw && !a.gb) return;
+  feed.drain();  // the ring's memory takes the column sums
+  __syncthreads();
+  float* colsum = reinterpret_cast<float*>(ring);
   // the CTA's sums: the groups of a warp by shuffles, the warps (or the
   // groups of several warps) in turn
 #pragma unroll
@@ -736,8 +865,9 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
 
 // ---------------------------------------------------------------- launch
 // Lanes for a row of cols values in vectors of V, NV per lane, at least
-// min_lanes (a power of two).
-inline RowShape row_shape(int cols, int K, int V, int NV, int min_lanes) {
+// min_lanes (a power of two), and the groups of a CTA: as many as fill it, or
+// fewer where the rows would leave some SMs without a CTA.
+inline RowShape row_shape(int cols, int K, int V, int NV, int min_lanes, int rows, int sms) {
   int period = 1;  // K / gcd(K, V)
   while (period * V % K) ++period;
   const int vectors = cols / V;
@@ -750,16 +880,16 @@ inline RowShape row_shape(int cols, int K, int V, int NV, int min_lanes) {
     sh.lanes = (sh.active + 31) / 32 * 32;
   }
   sh.groups = sh.lanes < kRowThreads ? kRowThreads / sh.lanes : 1;
+  const int whole = sh.lanes < 32 ? 32 / sh.lanes : 1;  // groups of a warp
+  while (sh.groups / 2 >= whole && (long long)sms * (sh.groups / 2) >= rows) sh.groups /= 2;
   return sh;
 }
-
-constexpr int kMaxColSum = 2 * 16 * kMaxRowThreads * 4;  // bytes of the column sums of the widest row
 
 // dw and db from the parts (norm.cu).
 eqmp_status launch_norm_bwd_sum(const NormArgs& a, int L, cudaStream_t st);
 
 // CTAs of a persistent launch: what the device holds at a time, at most one
-// per group of rows.
+// per tile of rows.
 template <typename Kernel>
 inline int resident_grid(Kernel kernel, int threads, size_t smem, const DeviceInfo& dev, long long tiles,
                          int (&cache)[64][33]) {
@@ -774,60 +904,62 @@ inline int resident_grid(Kernel kernel, int threads, size_t smem, const DeviceIn
   return (int)(tiles < cap ? tiles : cap);
 }
 
-template <typename T, int L, int V, int NV, bool FUSED>
-static eqmp_status launch_fwd(const NormArgs& a, const RowShape& sh, const DeviceInfo& dev, cudaStream_t st) {
-  static int cache[64][33];
-  const int threads = sh.lanes * sh.groups;
-  auto kern = k_norm_rows<T, L, V, NV, FUSED>;
-  const int grid = resident_grid(kern, threads, 0, dev, ((long long)a.rows + sh.groups - 1) / sh.groups, cache);
-  if (grid < 1) return EQMP_ERR_CUDA;
-  kern<<<grid, threads, 0, st>>>(a, sh);
-  return cuda_status(cudaGetLastError());
-}
+constexpr int kMaxRingBytes = 220 * 1024;  // of dynamic shared memory, a CTA
 
-template <typename T, int L, int V, int NV, bool FUSED>
-static eqmp_status launch_bwd(NormArgs a, const RowShape& sh, const DeviceInfo& dev, cudaStream_t st) {
+template <typename T, int L, int V, int NV, bool BACKWARD, int MODE>
+static eqmp_status launch_mode(NormArgs a, const RowShape& sh, const DeviceInfo& dev, cudaStream_t st) {
   static int cache[64][33];
-  const int threads = sh.lanes * sh.groups;
-  const size_t smem = a.gw || a.gb ? sizeof(float) * ((size_t)a.cols + a.C) : 0;
-  auto kern = k_norm_bwd_rows<T, L, V, NV, FUSED>;
   static unsigned long long attr_done = 0;
-  if (ensure_smem_attr(kern, kMaxColSum, &attr_done) != cudaSuccess) return EQMP_ERR_CUDA;
-  int grid = resident_grid(kern, threads, smem, dev, ((long long)a.rows + sh.groups - 1) / sh.groups, cache);
-  if (grid < 1) return EQMP_ERR_CUDA;
-  if (grid > kMaxParts) grid = kMaxParts;
-  a.parts = grid;
-  kern<<<grid, threads, smem, st>>>(a, sh);
-  if (cudaGetLastError() != cudaSuccess) return EQMP_ERR_CUDA;
-  if ((!a.gw && !a.gb) || grid == 1) return EQMP_OK;
-  return launch_norm_bwd_sum(a, L, st);
+  const int threads = sh.lanes * sh.groups;
+  const long long tiles = ((long long)a.rows + sh.groups - 1) / sh.groups;
+  if constexpr (!BACKWARD) {
+    auto kern = k_norm_rows<T, L, V, NV, MODE>;
+    const size_t smem = (size_t)threads * Feed<T, V, NV, MODE ? 2 : 1, 0>::BYTES;
+    if (ensure_smem_attr(kern, kMaxRingBytes, &attr_done) != cudaSuccess) return EQMP_ERR_CUDA;
+    const int grid = resident_grid(kern, threads, smem, dev, tiles, cache);
+    if (grid < 1) return EQMP_ERR_CUDA;
+    kern<<<grid, threads, smem, st>>>(a, sh);
+    return cuda_status(cudaGetLastError());
+  } else {
+    auto kern = k_norm_bwd_rows<T, L, V, NV, MODE>;
+    if (ensure_smem_attr(kern, kMaxRingBytes, &attr_done) != cudaSuccess) return EQMP_ERR_CUDA;
+    const size_t feed = (size_t)threads * Feed<T, V, NV, MODE ? 3 : 2, 1 + Slots<L, V, NV>::GROUPS>::BYTES;
+    const size_t sums = sizeof(float) * ((size_t)a.cols + a.C), smem = feed > sums ? feed : sums;
+    int grid = resident_grid(kern, threads, smem, dev, tiles, cache);
+    if (grid < 1) return EQMP_ERR_CUDA;
+    if (grid > kMaxParts) grid = kMaxParts;
+    a.parts = grid;
+    kern<<<grid, threads, smem, st>>>(a, sh);
+    if (cudaGetLastError() != cudaSuccess) return EQMP_ERR_CUDA;
+    if ((!a.gw && !a.gb) || grid == 1) return EQMP_OK;
+    return launch_norm_bwd_sum(a, L, st);
+  }
 }
 
 template <typename T, int L, int V, int NV, bool BACKWARD>
 static eqmp_status launch_rows(const NormArgs& a, const RowShape& sh, const DeviceInfo& dev, cudaStream_t st) {
-  if constexpr (BACKWARD) {
-    const bool fused = a.r || a.drop.threshold || (a.gr && a.gx);
-    return fused ? launch_bwd<T, L, V, NV, true>(a, sh, dev, st) : launch_bwd<T, L, V, NV, false>(a, sh, dev, st);
-  } else {
-    const bool fused = a.r || a.drop.threshold || a.s;
-    return fused ? launch_fwd<T, L, V, NV, true>(a, sh, dev, st) : launch_fwd<T, L, V, NV, false>(a, sh, dev, st);
+  if (!a.r && !a.drop.threshold && !(BACKWARD ? a.gr && a.gx : a.s != nullptr))
+    return launch_mode<T, L, V, NV, BACKWARD, kPlain>(a, sh, dev, st);
+  if constexpr (L == 0 && V > 1) {
+    if (a.drop.threshold && a.drop.group == 1) return launch_mode<T, L, V, NV, BACKWARD, kDirect>(a, sh, dev, st);
   }
+  return launch_mode<T, L, V, NV, BACKWARD, kMixed>(a, sh, dev, st);
 }
 
-// 8 or 16 values a lane.  Forward: whichever leaves fewer places empty; 8
-// where both are equal and the row fits a warp (fewer registers, more rows in
-// flight).  Backward: 8 where the row fits, since 16 values of every array do
-// not fit 128 registers.
+// 16 values a lane share the sums' shuffles and barriers over more values; 8
+// leave more lanes to work on a row, which is faster where the rows are few,
+// and fit the registers of the lanes that handle single values.
 template <typename T, int L, int V, bool BACKWARD>
 static eqmp_status launch_rows_v(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st, bool* done) {
   constexpr int K = (L + 1) * (L + 1), N8 = 8 / V, N16 = 16 / V;
-  constexpr int least = L ? 8 : BACKWARD ? 2 : 1;  // what GroupSum needs
-  const RowShape s8 = row_shape(a.cols, K, V, N8, least), s16 = row_shape(a.cols, K, V, N16, least);
-  const int p8 = s8.lanes * N8, p16 = s16.lanes * N16;
-  const bool take8 = s8.lanes <= kMaxRowThreads && (BACKWARD || p8 < p16 || (p8 == p16 && s8.lanes <= 32));
-  *done = take8 || s16.lanes <= kMaxRowThreads;
+  constexpr int least = pow2_above(BACKWARD ? L + 2 : L + 1);  // what GroupSum needs
+  const RowShape s8 = row_shape(a.cols, K, V, N8, least, a.rows, dev.sms);
+  const RowShape s16 = row_shape(a.cols, K, V, N16, least, a.rows, dev.sms);
+  const bool few = (long long)a.rows * s8.lanes <= (long long)dev.sms * kMaxRowThreads;
+  *done = s16.lanes <= kMaxRowThreads;
   if (!*done) return EQMP_OK;
-  return take8 ? launch_rows<T, L, V, N8, BACKWARD>(a, s8, dev, st) : launch_rows<T, L, V, N16, BACKWARD>(a, s16, dev, st);
+  if (s8.lanes <= kMaxRowThreads && (V == 1 || few)) return launch_rows<T, L, V, N8, BACKWARD>(a, s8, dev, st);
+  return launch_rows<T, L, V, N16, BACKWARD>(a, s16, dev, st);
 }
 
 inline bool vec16(const void* p, long long ld, int bytes) {
