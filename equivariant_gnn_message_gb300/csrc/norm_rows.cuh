@@ -331,7 +331,7 @@ struct Keeps {
       half = at_row = 0;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        unit[j] = at.col[j] / group;
+        unit[j] = at.has[j] ? at.col[j] / group : 0;
         if (V > 1) left[V > 1 ? j : 0] = (int)((unit[j] + 1) * group - at.col[j]);
       }
     }
@@ -390,31 +390,30 @@ struct Keeps {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float& f = j & 1 ? p[j / 2].y : p[j / 2].x;
-        f = at.has[j] && kept(unit[j]) ? f * d.scale : 0.0f;
+        f = kept(unit[j]) ? f * d.scale : 0.0f;
       }
     } else {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float2* f = p + j * (V / 2);
-        const int n = left[j];
-        uint32_t keep = 0;  // bits of the vector's values
-        if (at.has[j]) {
-          keep = kept(unit[j]) ? (1u << V) - 1 : 0;
-          if ((L == 0 || at.K % V) && n < V) {
-            if (L > 0 || d.group >= V) {  // two units
-              keep = (keep & ((1u << n) - 1)) | (kept(unit[j] + 1) ? (1u << V) - (1u << n) : 0);
-            } else {
-              keep = 0;
-#pragma unroll 1
-              for (int i = 0; i < V; ++i) keep |= (uint32_t)kept((at.col[j] + i) / (uint32_t)d.group) << i;
-            }
-          }
-        }
 #pragma unroll
-        for (int s = 0; s < V / 2; ++s) {
-          f[s] = __fmul2_rn(f[s], both(d.scale));
-          f[s].x = keep >> (2 * s) & 1 ? f[s].x : 0.0f;
-          f[s].y = keep >> (2 * s + 1) & 1 ? f[s].y : 0.0f;
+        for (int s = 0; s < V / 2; ++s) f[s] = __fmul2_rn(f[s], both(d.scale));
+        if (L == 0 && d.group < V) {  // each value's unit by itself
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float& t = i & 1 ? f[i / 2].y : f[i / 2].x;
+            t = at.has[j] && kept((at.col[j] + i) / (uint32_t)d.group) ? t : 0.0f;
+          }
+        } else {  // two units at most
+          const int n = left[j];
+          const bool k0 = kept(unit[j]);
+          bool k1 = k0;
+          if ((L == 0 || at.K % V) && n < V && at.has[j]) k1 = kept(unit[j] + 1);
+#pragma unroll
+          for (int s = 0; s < V / 2; ++s) {
+            f[s].x = ((L && at.K % V == 0) || 2 * s < n ? k0 : k1) ? f[s].x : 0.0f;
+            f[s].y = ((L && at.K % V == 0) || 2 * s + 1 < n ? k0 : k1) ? f[s].y : 0.0f;
+          }
         }
       }
     }
