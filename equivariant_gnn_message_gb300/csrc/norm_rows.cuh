@@ -26,6 +26,7 @@ struct RowShape {
   int lanes;   // G
   int active;  // lanes that hold values
   int groups;  // rows of a CTA at a time
+  int run;     // forward: rounds of a CTA over neighbouring rows; 0: CTAs take turns
 };
 
 constexpr int kRowThreads = 256;     // of a CTA, where a group is smaller
@@ -516,14 +517,16 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
   __shared__ uint8_t bits[MODE == kMixed ? 2 * kKeepBytes : 1];
   extern __shared__ __align__(16) uint8_t ring[];
   const S at(sh, a.cols);
-  const int stride = gridDim.x * sh.groups;
-  int row = blockIdx.x * sh.groups + threadIdx.x / sh.lanes;
+  const int stride = sh.run ? sh.groups : gridDim.x * sh.groups;
+  const int begin = blockIdx.x * (sh.run ? sh.run : 1) * sh.groups;
+  const int end = sh.run ? min(a.rows, begin + sh.run * sh.groups) : a.rows;
+  int row = begin + threadIdx.x / sh.lanes;
   F feed(ring);
   const T* x = static_cast<const T*>(a.x) + row * a.x_ld;
   const T* r = static_cast<const T*>(a.r) + row * a.r_ld;
   int ahead = row;  // the row that is loaded next
   auto load_row = [&]() {
-    const bool live = ahead < a.rows;
+    const bool live = ahead < end;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       feed.load(0, j, x + at.col[j], at.has[j] && live);
@@ -567,7 +570,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
     __syncthreads();
   }
   // the same number of rounds for every group of the CTA
-  for (int base = blockIdx.x * sh.groups; base < a.rows; base += stride, row += stride) {
+  for (int base = begin; base < end; base += stride, row += stride) {
     float2 v[P], acc[PV];
     const uint32_t place = feed.wait();
     feed.get(place, 0, v);
@@ -582,7 +585,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
     }
     load_row();
     if (MODE == kMixed && drop.on) keeps.form_next(drop, sh, row, stride);
-    const bool live = row < a.rows;
+    const bool live = row < end;
     const long long out = (long long)row * a.cols;
     if (MODE && a.s && live) put_pairs<T, V, NV>(static_cast<T*>(a.s) + out, at.col, at.has, v);
     // the mean of degree 0
@@ -879,6 +882,7 @@ inline RowShape row_shape(int cols, int K, int V, int NV, int min_lanes, int row
     sh.lanes = (sh.active + 31) / 32 * 32;
   }
   sh.groups = sh.lanes < kRowThreads ? kRowThreads / sh.lanes : 1;
+  sh.run = 0;
   const int whole = sh.lanes < 32 ? 32 / sh.lanes : 1;  // groups of a warp
   while (sh.groups / 2 >= whole && (long long)sms * (sh.groups / 2) >= rows) sh.groups /= 2;
   return sh;
@@ -904,9 +908,10 @@ inline int resident_grid(Kernel kernel, int threads, size_t smem, const DeviceIn
 }
 
 constexpr int kMaxRingBytes = 220 * 1024;  // of dynamic shared memory, a CTA
+constexpr long long kRunBytes = 256 * 1024;
 
 template <typename T, int L, int V, int NV, bool BACKWARD, int MODE>
-static eqmp_status launch_mode(NormArgs a, const RowShape& sh, const DeviceInfo& dev, cudaStream_t st) {
+static eqmp_status launch_mode(NormArgs a, RowShape sh, const DeviceInfo& dev, cudaStream_t st) {
   static int cache[64][33];
   static unsigned long long attr_done = 0;
   const int threads = sh.lanes * sh.groups;
@@ -915,8 +920,18 @@ static eqmp_status launch_mode(NormArgs a, const RowShape& sh, const DeviceInfo&
     auto kern = k_norm_rows<T, L, V, NV, MODE>;
     const size_t smem = (size_t)threads * Feed<T, V, NV, MODE ? 2 : 1, 0>::BYTES;
     if (ensure_smem_attr(kern, kMaxRingBytes, &attr_done) != cudaSuccess) return EQMP_ERR_CUDA;
-    const int grid = resident_grid(kern, threads, smem, dev, tiles, cache);
+    int grid = resident_grid(kern, threads, smem, dev, tiles, cache);
     if (grid < 1) return EQMP_ERR_CUDA;
+    // Much work: CTAs in order, each over a run of about 256 KB, so that what
+    // is on the way stays a narrow window of DRAM (persistent CTAs drift
+    // apart: 100,000 x 64 x 16 fp32 with residual 281 us, in runs 238).
+    // Else persistent CTAs in turns, which share out little work evenly.
+    const long long bytes = (long long)sh.groups * a.cols * (long long)sizeof(T) * (2 + (a.r != nullptr) + (a.s != nullptr));
+    const int run = bytes < kRunBytes ? (int)(kRunBytes / bytes) : 1;
+    if (tiles / run >= 4ll * grid) {
+      sh.run = run;
+      grid = (int)((tiles + run - 1) / run);
+    }
     kern<<<grid, threads, smem, st>>>(a, sh);
     return cuda_status(cudaGetLastError());
   } else {
