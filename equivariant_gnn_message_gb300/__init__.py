@@ -607,20 +607,11 @@ def eqmp_fused_backward_noalloc(vec, x, row_offsets, src, dst, send_offsets, sen
 
 
 # ------------------------------------------------------------------ norms and dropout
-def _norm_input(t, name, dtype, shape, dev):
-    """Checks an input of the norms and returns its row stride.  A row (everything behind the first dimension) is
-    packed; the rows of a matrix may be any distance apart."""
-    _same(t, name, dtype, shape, dev)
-    if t.dim() == 2:
-        if t.stride(1) != 1 and shape[1] > 1 and shape[0] > 0:
-            raise ValueError(f"{name} must have contiguous rows")
-        return t.stride(0)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.stride(0)
+_L_MAX = {16: 3, 25: 4, 36: 5, 49: 6}  # components of a channel -> degree
 
 
-def _same(t, name, dtype, shape, dev):
+def _refuse(t, name, dtype, shape, dev):
+    """The error of a tensor that is not what an entry point needs."""
     import torch
 
     if not isinstance(t, torch.Tensor):
@@ -629,89 +620,98 @@ def _same(t, name, dtype, shape, dev):
         raise TypeError(f"{name} has dtype {t.dtype}, not {dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the current device")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _packed(t, name, dtype, shape, dev):
-    """Checks a packed tensor (or None) and returns its address."""
-    if t is None:
-        return None
-    _same(t, name, dtype, shape, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _packed(t, name, dtype, shape, dev, torch):
+    """Checks a packed tensor and returns its address."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev
+            or not t.is_contiguous()):
+        _refuse(t, name, dtype, shape, dev)
     return t.data_ptr()
 
 
-def _results(need, allowed, specs, out, dev):
-    """The requested result tensors, the caller's own from `out` where it has them, and the addresses of all."""
-    import torch
+def _rows(t, name, dtype, shape, dev, torch):
+    """Checks an input of rows and returns its address and row stride.  A row (everything behind the first dimension)
+    is packed; the rows of a matrix may be any distance apart."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, name, dtype, shape, dev)
+    if t.is_contiguous() or (len(shape) == 2 and (t.stride(1) == 1 or shape[1] == 1)):
+        return t.data_ptr(), t.stride(0)
+    raise ValueError(f"{name} must have contiguous rows" if len(shape) == 2 else f"{name} must be contiguous")
 
-    got, at = {}, {}
+
+def _result(out, k, like, dtype, shape, dev, torch):
+    """The result tensor k: the caller's own from `out`, or a new one on the device of `like`."""
+    t = out.get(k) if out else None
+    if t is None:
+        t = like.new_empty(shape, dtype=dtype)
+        return t, t.data_ptr()
+    return t, _packed(t, f"out[{k!r}]", dtype, shape, dev, torch)
+
+
+def _main_input(x, name, degree, torch):
+    """Checks the type and the form of a norm's main input; returns the current device and the degree."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype is not torch.float32 and x.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} has dtype {x.dtype}")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape = x.shape
+    if degree:
+        l_max = _L_MAX.get(shape[2], 0) if len(shape) == 3 else 0
+        if not l_max or shape[1] < 1:
+            raise ValueError(f"{name} must be [N, C, (l_max+1)^2] with l_max in 3..6 and C >= 1")
+        return torch.cuda.current_device(), l_max
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError(f"{name} must be [rows, cols] with cols >= 1")
+    return torch.cuda.current_device(), 0
+
+
+def _raw_stream(stream, dev, torch):
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _unknown(need, allowed):
     for k in need:
         if k not in allowed:
             raise ValueError(f"need has {k!r}; allowed are {', '.join(allowed)}")
-        dtype, shape = specs[k]
-        t = out.get(k) if out else None
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
-            at[k] = t.data_ptr()
-        else:
-            at[k] = _packed(t, f"out[{k!r}]", dtype, shape, dev)
-        got[k] = t
-    return got, at
-
-
-def _norm_case(x, name, degree):
-    """Storage type, device, shape and the sizes of w and b of a norm's main input."""
-    import torch
-
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    dtype, shape = x.dtype, tuple(x.shape)
-    if dtype is not torch.float32 and dtype is not torch.bfloat16:
-        raise TypeError(f"{name} has dtype {dtype}")
-    if not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    dev = torch.cuda.current_device()
-    if degree:
-        l_max = {16: 3, 25: 4, 36: 5, 49: 6}.get(shape[2] if len(shape) == 3 else 0)
-        if l_max is None or shape[1] < 1:
-            raise ValueError(f"{name} must be [N, C, (l_max+1)^2] with l_max in 3..6 and C >= 1")
-        return dtype, dev, shape, l_max, (l_max + 1, shape[1]), (shape[1],)
-    if len(shape) != 2 or shape[1] < 1:
-        raise ValueError(f"{name} must be [rows, cols] with cols >= 1")
-    return dtype, dev, shape, 0, (shape[1],), (shape[1],)
-
-
-def _raw_stream(stream, dev):
-    import torch
-
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _norm_forward(entry, degree, x, w, b, eps, residual, drop, need, out, stream):
     import torch
 
     f32 = torch.float32
-    dtype, dev, shape, l_max, w_shape, b_shape = _norm_case(x, "x", degree)
-    x_ld = _norm_input(x, "x", dtype, shape, dev)
-    r_ld = _norm_input(residual, "residual", dtype, shape, dev) if residual is not None else 0
-    wp, bp = _packed(w, "w", f32, w_shape, dev), _packed(b, "b", f32, b_shape, dev)
+    dev, l_max = _main_input(x, "x", degree, torch)
+    dtype, shape = x.dtype, x.shape
+    n, c = shape[0], shape[1]
+    xp, x_ld = _rows(x, "x", dtype, shape, dev, torch)
+    rp, r_ld = (None, 0) if residual is None else _rows(residual, "residual", dtype, shape, dev, torch)
+    wp = None if w is None else _packed(w, "w", f32, (l_max + 1, c) if degree else (c,), dev, torch)
+    bp = None if b is None else _packed(b, "b", f32, (c,), dev, torch)
     if need is None:
         need = ("y",) if residual is None else ("y", "s")
-    got, at = _results(need, ("y", "s", "stats"), {"y": (dtype, shape), "s": (dtype, shape),
-                                                   "stats": (f32, (shape[0], l_max + 2))}, out, dev)
+    got, sp, yp, tp = {}, None, None, None
+    if "y" in need:
+        got["y"], yp = _result(out, "y", x, dtype, shape, dev, torch)
+    if "s" in need:
+        got["s"], sp = _result(out, "s", x, dtype, shape, dev, torch)
+    if "stats" in need:
+        got["stats"], tp = _result(out, "stats", x, f32, (n, l_max + 2), dev, torch)
+    if len(got) != len(need):
+        _unknown(need, ("y", "s", "stats"))
     dt = EQMP_F32 if dtype is f32 else EQMP_BF16
     dr = _NO_DROP if drop is None else drop
-    r = None if residual is None else residual.data_ptr()
-    lib = load_library()
-    tail = (dr, wp, bp, eps, at.get("s"), at.get("y"), at.get("stats"), _raw_stream(stream, dev))
+    lib, st = load_library(), _raw_stream(stream, dev, torch)
     if degree:
-        st = lib.eqmp_degree_norm(x.data_ptr(), r, dt, shape[0], shape[1], l_max, *tail)
+        status = lib.eqmp_degree_norm(xp, rp, dt, n, c, l_max, dr, wp, bp, eps, sp, yp, tp, st)
     else:
-        st = lib.eqmp_layer_norm(x.data_ptr(), x_ld, r, r_ld, dt, shape[0], shape[1], *tail)
-    _check(st, entry)
+        status = lib.eqmp_layer_norm(xp, x_ld, rp, r_ld, dt, n, c, dr, wp, bp, eps, sp, yp, tp, st)
+    if status:
+        raise EqmpError(status, entry)
     return got
 
 
@@ -719,39 +719,47 @@ def _norm_backward(entry, degree, grad_y, s, stats, w, grad_s, drop, need, out, 
     import torch
 
     f32 = torch.float32
-    dtype, dev, shape, l_max, w_shape, b_shape = _norm_case(s, "s", degree)
-    s_ld = _norm_input(s, "s", dtype, shape, dev)
-    g_ld = _norm_input(grad_y, "grad_y", dtype, shape, dev)
-    gs_ld = _norm_input(grad_s, "grad_s", dtype, shape, dev) if grad_s is not None else 0
-    wp = _packed(w, "w", f32, w_shape, dev)
-    if stats is None:
-        raise TypeError("stats must be a torch.Tensor")
-    sp = _packed(stats, "stats", f32, (shape[0], l_max + 2), dev)
-    got, at = _results(need, ("x", "r", "w", "b"), {"x": (dtype, shape), "r": (dtype, shape), "w": (f32, w_shape),
-                                                    "b": (f32, b_shape)}, out, dev)
-    dt = EQMP_F32 if dtype is f32 else EQMP_BF16
-    dr = _NO_DROP if drop is None else drop
-    lib = load_library()
-    ws, nbytes = None, 0
-    if "w" in at or "b" in at:
-        nbytes = (lib.eqmp_degree_norm_backward_workspace_size(shape[0], shape[1], l_max) if degree else
-                  lib.eqmp_layer_norm_backward_workspace_size(shape[0], shape[1]))
-        if nbytes < 0:
-            raise EqmpError(EQMP_ERR_UNSUPPORTED, entry)
+    dev, l_max = _main_input(s, "s", degree, torch)
+    dtype, shape = s.dtype, s.shape
+    n, c = shape[0], shape[1]
+    w_shape = (l_max + 1, c) if degree else (c,)
+    xp, x_ld = _rows(s, "s", dtype, shape, dev, torch)
+    gp, g_ld = _rows(grad_y, "grad_y", dtype, shape, dev, torch)
+    rp, r_ld = (None, 0) if grad_s is None else _rows(grad_s, "grad_s", dtype, shape, dev, torch)
+    wp = None if w is None else _packed(w, "w", f32, w_shape, dev, torch)
+    tp = _packed(stats, "stats", f32, (n, l_max + 2), dev, torch)
+    got, grp, gxp, gwp, gbp, ws, nbytes = {}, None, None, None, None, None, 0
+    if "x" in need:
+        got["x"], gxp = _result(out, "x", s, dtype, shape, dev, torch)
+    if "r" in need:
+        got["r"], grp = _result(out, "r", s, dtype, shape, dev, torch)
+    if "w" in need:
+        got["w"], gwp = _result(out, "w", s, f32, w_shape, dev, torch)
+    if "b" in need:
+        got["b"], gbp = _result(out, "b", s, f32, (c,), dev, torch)
+    if len(got) != len(need):
+        _unknown(need, ("x", "r", "w", "b"))
+    lib, st = load_library(), _raw_stream(stream, dev, torch)
+    if gwp is not None or gbp is not None:
         if workspace is None:
-            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=f"cuda:{dev}")
+            nbytes = (lib.eqmp_degree_norm_backward_workspace_size(n, c, l_max) if degree else
+                      lib.eqmp_layer_norm_backward_workspace_size(n, c))
+            if nbytes < 0:
+                raise EqmpError(EQMP_ERR_UNSUPPORTED, entry)
+            workspace = s.new_empty(nbytes // 4 + 4, dtype=f32)
         else:
             _require(workspace, "workspace", torch.uint8)
             nbytes = workspace.numel()
         ws = workspace.data_ptr()
-    gs = None if grad_s is None else grad_s.data_ptr()
-    tail = (dr, wp, sp, at.get("r"), at.get("x"), at.get("w"), at.get("b"), ws, nbytes, _raw_stream(stream, dev))
+    dt = EQMP_F32 if dtype is f32 else EQMP_BF16
+    dr = _NO_DROP if drop is None else drop
     if degree:
-        st = lib.eqmp_degree_norm_backward(grad_y.data_ptr(), s.data_ptr(), gs, dt, shape[0], shape[1], l_max, *tail)
+        status = lib.eqmp_degree_norm_backward(gp, xp, rp, dt, n, c, l_max, dr, wp, tp, grp, gxp, gwp, gbp, ws, nbytes, st)
     else:
-        st = lib.eqmp_layer_norm_backward(grad_y.data_ptr(), g_ld, s.data_ptr(), s_ld, gs, gs_ld, dt, shape[0],
-                                          shape[1], *tail)
-    _check(st, entry)
+        status = lib.eqmp_layer_norm_backward(gp, g_ld, xp, x_ld, rp, r_ld, dt, n, c, dr, wp, tp, grp, gxp, gwp, gbp, ws,
+                                              nbytes, st)
+    if status:
+        raise EqmpError(status, entry)
     return got
 
 
@@ -762,27 +770,26 @@ def eqmp_dropout(x, drop, out=None, stream=None):
 
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
-    if x.dtype is not torch.float32 and x.dtype is not torch.bfloat16:
-        raise TypeError(f"x has dtype {x.dtype}")
+    dtype, shape = x.dtype, x.shape
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+        raise TypeError(f"x has dtype {dtype}")
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
-    dev, shape = torch.cuda.current_device(), tuple(x.shape)
-    if not shape:
-        raise ValueError("x must be [rows, ...]")
-    ld = _norm_input(x, "x", x.dtype, shape, dev)
-    if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
-    at = _packed(out, "out", x.dtype, shape, dev)
     cols = 1
     for n in shape[1:]:
         cols *= n
-    if cols < 1:
-        raise ValueError("x must have columns")
-    if out is x:
-        ld = cols
-    _check(load_library().eqmp_dropout(x.data_ptr(), ld, EQMP_F32 if x.dtype is torch.float32 else EQMP_BF16, shape[0],
-                                       cols, drop if drop is not None else _NO_DROP, at, _raw_stream(stream, dev)),
-           "eqmp_dropout")
+    if not shape or cols < 1:
+        raise ValueError("x must be [rows, ...] with values in a row")
+    dev = torch.cuda.current_device()
+    xp, ld = _rows(x, "x", dtype, shape, dev, torch)
+    if out is None:
+        out = x.new_empty(shape)
+    op = _packed(out, "out", dtype, shape, dev, torch)
+    status = load_library().eqmp_dropout(xp, cols if out is x else ld, EQMP_F32 if dtype is torch.float32 else EQMP_BF16,
+                                         shape[0], cols, _NO_DROP if drop is None else drop, op,
+                                         _raw_stream(stream, dev, torch))
+    if status:
+        raise EqmpError(status, "eqmp_dropout")
     return out
 
 
