@@ -647,7 +647,7 @@ def _result(out, k, like, dtype, shape, dev, torch):
     """The result tensor k: the caller's own from `out`, or a new one on the device of `like`."""
     t = out.get(k) if out else None
     if t is None:
-        t = like.new_empty(shape, dtype=dtype)
+        t = torch.empty(shape, dtype=dtype, device=like.device)
         return t, t.data_ptr()
     return t, _packed(t, f"out[{k!r}]", dtype, shape, dev, torch)
 
@@ -746,7 +746,7 @@ def _norm_backward(entry, degree, grad_y, s, stats, w, grad_s, drop, need, out, 
                       lib.eqmp_layer_norm_backward_workspace_size(n, c))
             if nbytes < 0:
                 raise EqmpError(EQMP_ERR_UNSUPPORTED, entry)
-            workspace = s.new_empty(nbytes // 4 + 4, dtype=f32)
+            workspace = torch.empty(nbytes // 4 + 4, dtype=f32, device=s.device)
         else:
             _require(workspace, "workspace", torch.uint8)
             nbytes = workspace.numel()
@@ -783,7 +783,7 @@ def eqmp_dropout(x, drop, out=None, stream=None):
     dev = torch.cuda.current_device()
     xp, ld = _rows(x, "x", dtype, shape, dev, torch)
     if out is None:
-        out = x.new_empty(shape)
+        out = torch.empty(shape, dtype=dtype, device=x.device)
     op = _packed(out, "out", dtype, shape, dev, torch)
     status = load_library().eqmp_dropout(xp, cols if out is x else ld, EQMP_F32 if dtype is torch.float32 else EQMP_BF16,
                                          shape[0], cols, _NO_DROP if drop is None else drop, op,
