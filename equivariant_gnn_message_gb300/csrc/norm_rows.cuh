@@ -29,7 +29,7 @@ struct RowShape {
   int run;     // forward: rounds of a CTA over neighbouring rows; 0: CTAs take turns
 };
 
-constexpr int kRowThreads = 256;     // of a CTA, where a group is smaller
+constexpr int kRowThreads = 128;     // of a CTA, where a group is smaller
 constexpr int kMaxRowThreads = 512;  // 128 registers a thread
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
@@ -114,7 +114,7 @@ struct Feed {
   static constexpr int B = sizeof(T) * V;  // bytes of a vector
   static constexpr bool RING = B >= 4;
   static constexpr int ROW = STREAMS * NV * B + WORDS * 4;  // bytes of a lane and row
-  static constexpr int DEPTH = !RING ? 2 : ROW <= 48 ? 4 : ROW <= 144 ? 3 : 2;
+  static constexpr int DEPTH = !RING ? 2 : WORDS ? (ROW <= 48 ? 4 : ROW <= 80 ? 3 : 2) : ROW <= 32 ? 3 : 2;
   static constexpr int BYTES = RING ? DEPTH * ROW : 0;  // of shared memory, a lane
   uint32_t ring, at;  // the ring; the place in it that is loaded next
   uint32_t step;      // bytes between a lane's vectors
@@ -908,7 +908,7 @@ inline int resident_grid(Kernel kernel, int threads, size_t smem, const DeviceIn
 }
 
 constexpr int kMaxRingBytes = 220 * 1024;  // of dynamic shared memory, a CTA
-constexpr long long kRunBytes = 256 * 1024;
+constexpr long long kRunBytes = 128 * 1024;
 
 template <typename T, int L, int V, int NV, bool BACKWARD, int MODE>
 static eqmp_status launch_mode(NormArgs a, RowShape sh, const DeviceInfo& dev, cudaStream_t st) {
@@ -922,7 +922,7 @@ static eqmp_status launch_mode(NormArgs a, RowShape sh, const DeviceInfo& dev, c
     if (ensure_smem_attr(kern, kMaxRingBytes, &attr_done) != cudaSuccess) return EQMP_ERR_CUDA;
     int grid = resident_grid(kern, threads, smem, dev, tiles, cache);
     if (grid < 1) return EQMP_ERR_CUDA;
-    // Much work: CTAs in order, each over a run of about 256 KB, so that what
+    // Much work: CTAs in order, each over a run of about 128 KB, so that what
     // is on the way stays a narrow window of DRAM (persistent CTAs drift
     // apart: 100,000 x 64 x 16 fp32 with residual 281 us, in runs 238).
     // Else persistent CTAs in turns, which share out little work evenly.
