@@ -422,33 +422,53 @@ struct Keeps {
 };
 
 // ---------------------------------------------------------------- sums
-// Sums N values over the lanes of each group, in a fixed order, and leaves
-// them spread over the lanes: value n is then fetched by a shuffle.  The
-// values are halved as the lanes are (each lane passes on the half that it
-// does not keep), so that N values take about as many shuffles as N + log2 G.
-// Groups of several warps exchange their warps' sums through red (two halves,
-// taken in turn, so that one barrier per sum is enough; every thread of the
-// CTA takes part).  A group has at least as many lanes as N rounded up to a
-// power of two.
+// Sums N values over the lanes of each group, in a fixed order; fetch(n) then
+// gives every lane value n.  Within a warp the values are halved as the lanes
+// are (each lane passes on the half that it does not keep), so that N values
+// take about as many shuffles as N + log2 G, and fetch() is one more.  The
+// warps of a larger group exchange their sums through red, where the rows of
+// missing warps up to a multiple of four stay zero.  Up to two values lie as
+// [n][warp] and fetch() adds a row, four warps a load; more lie as [warp][n],
+// each lane adds a column of them, and fetch() is a shuffle again.  Two halves
+// are taken in turn, so that one barrier of the group per sum is enough.  A
+// group has at least as many lanes as N rounded up to a power of two.
 constexpr int pow2_above(int n) { return n <= 1 ? 1 : 2 * pow2_above((n + 1) / 2); }
+constexpr int kRedWarps = kMaxRowThreads / 32 + 4;  // of all groups of a CTA, each rounded up to four
 
 template <int N>
 struct GroupSum {
   static constexpr int P = pow2_above(N);
-  static_assert(P <= 16, "more values than half a warp");
-  static constexpr int kRed = 2 * (kMaxRowThreads / 32) * P;  // floats of red
-  int lanes, warps, first;  // of the group: lanes, warps, its first warp
-  int base, each;           // value n is at lane base + n each
+  static constexpr bool ROWS = N <= 2;
+  static_assert(P <= 8, "more values than lanes of the smallest group");
+  static constexpr int kRed = 2 * P * kRedWarps;  // floats of red, 16-byte aligned
+  int lanes, warps4;  // of the group: lanes, warps rounded up to four
   float* red;
-  int half;
+  int sums, mine;  // in red: the group's sums, and this warp's place in them
+  int base, each;  // value n is at lane base + n each
   float val;
-  __device__ __forceinline__ GroupSum(int lanes_, float* red_) : lanes(lanes_), red(red_), half(0), val(0.0f) {
-    warps = lanes_ >> 5;
-    first = warps > 1 ? (int)(threadIdx.x >> 5) / warps * warps : 0;
-    base = lanes_ < 32 ? (int)(threadIdx.x & 31) / lanes_ * lanes_ : 0;
-    each = lanes_ > 32 ? 1 : lanes_ / P;
+  __device__ __forceinline__ GroupSum(int lanes_, float* red_) : lanes(lanes_), red(red_), val(0.0f) {
+    const int warps = lanes >> 5, group = threadIdx.x / lanes, warp = threadIdx.x / 32 - group * warps;
+    warps4 = (warps + 3) & ~3;
+    sums = group * P * warps4;
+    mine = ROWS ? warp : warp * P;
+    base = lanes < 32 ? (int)(threadIdx.x & 31) / lanes * lanes : 0;
+    each = lanes > 32 ? 1 : lanes / P;
+    if (lanes > 32) {
+      for (int i = threadIdx.x; i < kRed; i += blockDim.x) red[i] = 0.0f;
+      __syncthreads();
+    }
   }
-  __device__ __forceinline__ float fetch(int n) const { return __shfl_sync(0xffffffffu, val, base + n * each); }
+  __device__ __forceinline__ float fetch(int n) const {
+    if (!ROWS || lanes <= 32) return __shfl_sync(0xffffffffu, val, base + n * each);
+    const float4* at = reinterpret_cast<const float4*>(red + sums + n * warps4);
+    float4 t = at[0];
+    float v = (t.x + t.y) + (t.z + t.w);
+    for (int k = 1; k < warps4 / 4; ++k) {
+      t = at[k];
+      v += (t.x + t.y) + (t.z + t.w);
+    }
+    return v;
+  }
   __device__ __forceinline__ void operator()(const float (&v)[N]) {
     int o = (lanes < 32 ? lanes : 32) >> 1;
     float x[P];
@@ -467,15 +487,17 @@ struct GroupSum {
     for (; o > 0; o >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
     val = x[0];
     if (lanes <= 32) return;
-    const int lane = threadIdx.x & 31;
-    float* buf = red + half * (kRed / 2);
-    if (lane % (32 / P) == 0) buf[(threadIdx.x >> 5) * P + lane / (32 / P)] = val;
-    __syncthreads();
-    float t = 0.0f;
-    for (int k = lane / P; k < warps; k += 32 / P) t += buf[(first + k) * P + lane % P];
-    for (o = P; o < 32 && o < warps * P; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    val = t;
-    half ^= 1;
+    sums += sums < kRed / 2 ? kRed / 2 : -kRed / 2;
+    const int lane = threadIdx.x & 31, n = lane / (32 / P);
+    if (lane % (32 / P) == 0) red[sums + mine + (ROWS ? n * warps4 : n)] = val;
+    named_barrier(1 + threadIdx.x / lanes, lanes);
+    if (!ROWS) {
+      val = red[sums + lane];  // four rows of eight values, or eight of four (the last four are another group's or zero)
+      if (P == 4) val = lane < 4 * P ? val : 0.0f;
+      for (int i = lane + 4 * P; i < warps4 * P; i += 4 * P) val += lane < 4 * P ? red[sums + i] : 0.0f;
+#pragma unroll
+      for (int d = P; d < 4 * P; d <<= 1) val += __shfl_xor_sync(0xffffffffu, val, d);
+    }
   }
 };
 
@@ -513,7 +535,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
   using F = Feed<T, V, NV, MODE ? 2 : 1, 0>;
   constexpr int P = NV * V / 2, PV = S::PAIRS, NS = L + 1;
   constexpr bool EACH = L == 0 || V == 1;  // a bias per value; else one per vector, which has at most one degree 0
-  __shared__ float red1[GroupSum<1>::kRed], red2[GroupSum<NS>::kRed];
+  __shared__ __align__(16) float red1[GroupSum<1>::kRed], red2[GroupSum<NS>::kRed];
   __shared__ uint8_t bits[MODE == kMixed ? 2 * kKeepBytes : 1];
   extern __shared__ __align__(16) uint8_t ring[];
   const S at(sh, a.cols);
@@ -663,7 +685,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
   using F = Feed<T, V, NV, MODE ? 3 : 2, 1 + S::GROUPS>;
   constexpr int P = NV * V / 2, PV = S::PAIRS, NS = L + 2;
   constexpr bool EACH = L == 0 || V == 1;  // db per value; else per vector, which has at most one degree 0
-  __shared__ float red[GroupSum<NS>::kRed];
+  __shared__ __align__(16) float red[GroupSum<NS>::kRed];
   __shared__ uint8_t bits[MODE == kMixed ? 2 * kKeepBytes : 1];
   extern __shared__ __align__(16) uint8_t ring[];  // at the end the column sums: [cols] g h, [C] g
   const S at(sh, a.cols);
