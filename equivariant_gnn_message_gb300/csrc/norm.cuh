@@ -334,25 +334,36 @@ __global__ void __launch_bounds__(kWideSumX * kWideSumY) k_norm_bwd_wide_w(NormA
   }
 }
 
-// dw and db: the parts' sums.  Thread (x, y) adds the parts y, y + kSumY, ...
-// of column x, then the rows of the block are added in their order.
-constexpr int kSumX = 16, kSumY = 32;
+// dw and db: the parts' sums.  A block takes 8 columns; thread (x, y) adds the
+// parts y, y + 64, ... of column x (its loads go out together: the kernel is
+// one latency long), then the rows of the block are added in a fixed order.
+constexpr int kSumX = 8, kSumY = 64;
 constexpr int kMaxParts = 608;  // four CTAs on each of 152 SMs
 
 static __global__ void __launch_bounds__(kSumX * kSumY) k_norm_bwd_sum(NormArgs a, int L) {
-  __shared__ float red[kSumY][kSumX];
+  __shared__ float red[kSumX * kSumY / 32][kSumX];
   const long long M = (long long)(L + 2) * a.C, m = (long long)blockIdx.x * kSumX + threadIdx.x;
   float t = 0.0f;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // until the kernel that writes the parts is done
   if (m < M) {
-#pragma unroll 8
-    for (int p = threadIdx.y; p < a.parts; p += kSumY) t += a.part[p * M + m];
+    const float* from = a.part + m;
+    constexpr int N = (kMaxParts + kSumY - 1) / kSumY;
+    float v[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int p = threadIdx.y + k * kSumY;
+      v[k] = p < a.parts ? from[p * M] : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) t += v[k];
   }
-  red[threadIdx.y][threadIdx.x] = t;
+  t += __shfl_xor_sync(0xffffffffu, t, 8);
+  t += __shfl_xor_sync(0xffffffffu, t, 16);
+  if (threadIdx.y % 4 == 0) red[threadIdx.y / 4][threadIdx.x] = t;
   __syncthreads();
   if (threadIdx.y || m >= M) return;
 #pragma unroll
-  for (int k = 1; k < kSumY; ++k) t += red[k][threadIdx.x];
+  for (int k = 1; k < kSumY / 4; ++k) t += red[k][threadIdx.x];
   const long long nw = (long long)(L + 1) * a.C;
   if (m < nw) {
     if (a.gw) a.gw[m] = t;

@@ -114,7 +114,7 @@ struct Feed {
   static constexpr int B = sizeof(T) * V;  // bytes of a vector
   static constexpr bool RING = B >= 4;
   static constexpr int ROW = STREAMS * NV * B + WORDS * 4;  // bytes of a lane and row
-  static constexpr int DEPTH = !RING ? 2 : WORDS ? (ROW <= 48 ? 4 : ROW <= 80 ? 3 : 2) : ROW <= 32 ? 3 : 2;
+  static constexpr int DEPTH = !RING ? 2 : WORDS ? (ROW <= 48 ? 4 : ROW <= 80 ? 3 : 2) : ROW <= 32 ? 4 : 2;
   static constexpr int BYTES = RING ? DEPTH * ROW : 0;  // of shared memory, a lane
   uint32_t ring, at;  // the ring; the place in it that is loaded next
   uint32_t step;      // bytes between a lane's vectors
@@ -818,9 +818,9 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
   if (!a.gw && !a.gb) return;
   feed.drain();  // the ring's memory takes the column sums
   __syncthreads();
-  float* colsum = reinterpret_cast<float*>(ring);
-  // the CTA's sums: the groups of a warp by shuffles, the warps (or the
-  // groups of several warps) in turn
+  // The CTA's sums.  The groups of a warp are added by shuffles; then each
+  // warp (or group of several warps) puts its columns into a row of its own,
+  // [C][K padded to an odd number] g h and [C] g, and the rows are added.
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     if (o >= sh.lanes) {
@@ -836,47 +836,37 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
       }
     }
   }
+  constexpr int KP = S::K | 1;
+  float* sums = reinterpret_cast<float*>(ring);
   const int unit = sh.lanes <= 32 ? 32 : sh.lanes;  // threads that add together
-  const int units = blockDim.x / unit, mine = threadIdx.x / unit;
-  const bool speaks = (int)(threadIdx.x % unit) < sh.lanes;
-  for (int u = 0; u < units; ++u) {
-    if (u == mine && speaks) {
+  const int units = blockDim.x / unit, width = (KP + 1) * a.C;
+  if ((int)(threadIdx.x % unit) < sh.lanes) {
+    float* mine = sums + threadIdx.x / unit * width;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if (!at.has[j]) continue;
+    for (int j = 0; j < NV; ++j) {
+      if (!at.has[j]) continue;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int e = j * V + i, col = (int)at.col[j] + i;
-          const float t = e & 1 ? dw[e / 2].y : dw[e / 2].x;
-          colsum[col] = u ? colsum[col] + t : t;
-          if (EACH && col % S::K == 0) {
-            const float f = e & 1 ? db[EACH ? e / 2 : 0].y : db[EACH ? e / 2 : 0].x;
-            float* d = colsum + a.cols + col / S::K;
-            *d = u ? *d + f : f;
-          }
-        }
-        if (!EACH) {
-          const int c = (int)(at.col[j] + V - 1) / S::K;  // the channel that begins in the vector, if one does
-          if (c * S::K >= (int)at.col[j]) {
-            const float f = db[EACH ? 0 : j].x + db[EACH ? 0 : j].y;
-            float* d = colsum + a.cols + c;
-            *d = u ? *d + f : f;
-          }
-        }
+      for (int i = 0; i < V; ++i) {
+        const int e = j * V + i, col = (int)at.col[j] + i, c = col / S::K, k = col - c * S::K;
+        mine[c * KP + k] = e & 1 ? dw[e / 2].y : dw[e / 2].x;
+        if (EACH && k == 0) mine[KP * a.C + c] = e & 1 ? db[EACH ? e / 2 : 0].y : db[EACH ? e / 2 : 0].x;
+      }
+      if (!EACH) {
+        const int c = (int)(at.col[j] + V - 1) / S::K;  // the channel that begins in the vector, if one does
+        if (c * S::K >= (int)at.col[j]) mine[KP * a.C + c] = db[EACH ? 0 : j].x + db[EACH ? 0 : j].y;
       }
     }
-    __syncthreads();
   }
+  __syncthreads();
   const int M = (L + 2) * a.C, nw = (L + 1) * a.C;
   float* part = a.parts > 1 ? a.part + (long long)blockIdx.x * M : nullptr;
   for (int m = threadIdx.x; m < M; m += blockDim.x) {
     float t = 0.0f;
-    if (L && m < nw) {
-      const int l = m / a.C, c = m - l * a.C;
-      for (int k = l * l; k < (l + 1) * (l + 1); ++k) t += colsum[c * S::K + k];
-    } else {
-      t = colsum[L ? a.cols + m - nw : m];
-    }
+    const int l = m < nw ? m / a.C : 0, c = m - (m < nw ? l * a.C : nw);
+    const float* from = m < nw ? sums + c * KP + l * l : sums + KP * a.C + c;
+    const int orders = m < nw ? 2 * l + 1 : 1;
+    for (int u = 0; u < units; ++u, from += width)
+      for (int k = 0; k < orders; ++k) t += from[k];
     if (part)
       part[m] = t;
     else if (m < nw) {
@@ -960,7 +950,9 @@ static eqmp_status launch_mode(NormArgs a, RowShape sh, const DeviceInfo& dev, c
     auto kern = k_norm_bwd_rows<T, L, V, NV, MODE>;
     if (ensure_smem_attr(kern, kMaxRingBytes, &attr_done) != cudaSuccess) return EQMP_ERR_CUDA;
     const size_t feed = (size_t)threads * Feed<T, V, NV, MODE ? 3 : 2, 1 + Slots<L, V, NV>::GROUPS>::BYTES;
-    const size_t sums = sizeof(float) * ((size_t)a.cols + a.C), smem = feed > sums ? feed : sums;
+    constexpr int KP = ((L + 1) * (L + 1)) | 1;  // the CTA's column sums, one row for each warp or larger group
+    const size_t sums = sizeof(float) * (size_t)(KP + 1) * a.C * (sh.lanes <= 32 ? threads / 32 : sh.groups);
+    const size_t smem = feed > sums ? feed : sums;
     int grid = resident_grid(kern, threads, smem, dev, tiles, cache);
     if (grid < 1) return EQMP_ERR_CUDA;
     if (grid > kMaxParts) grid = kMaxParts;
