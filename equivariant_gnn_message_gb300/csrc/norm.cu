@@ -328,8 +328,10 @@ static eqmp_status run_dropout(const void* x, long long ld, void* out, int rows,
   constexpr int B = sizeof(T);
   const T* in = static_cast<const T*>(x);
   T* to = static_cast<T*>(out);
-  const bool vec = vec16(x, ld, B) && vec16(out, cols, B) && cols * (long long)B % 16 == 0;
-  return vec ? launch_drop<T, 16 / B>(in, ld, to, rows, cols, d, st) : launch_drop<T, 1>(in, ld, to, rows, cols, d, st);
+  Alignment al(B, cols);
+  al.add(x, ld);
+  al.add(out, cols);
+  return al.rows ? launch_drop<T, 16 / B>(in, ld, to, rows, cols, d, st) : launch_drop<T, 1>(in, ld, to, rows, cols, d, st);
 }
 
 }  // namespace eqmp

@@ -9,12 +9,21 @@
 // the degree is one value per slot i, and a row's sums go to their degrees
 // once per row, not once per value.
 //
+// SHIFT: rows that begin anywhere.  The rows of a group are a multiple of 8
+// apart, so all of them begin the same number of values, s < V, behind a
+// 16-byte boundary; the lanes take the vectors from that boundary on, columns
+// -s, V - s, ..., and only a row's first and last vector are partial: what the
+// first holds of the row before is masked, the copy of the last ends with the
+// row, and both are stored value by value.
+//
 // The values move from and to HBM once, so these kernels are bound by
 // instructions before they are bound by memory: a bf16 value that is read and
 // written once may cost about 20 of them.  Hence the arithmetic is on pairs
 // (fma.rn.f32x2), and sums of several values are scattered over the lanes as
 // they are formed.
 #pragma once
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -90,19 +99,6 @@ __device__ __forceinline__ void get_pairs(const Pack<T, V> (&v)[NV], float2 (&p)
   }
 }
 
-template <typename T, int V, int NV>
-__device__ __forceinline__ void put_pairs(T* row, const uint32_t (&col)[NV], const bool (&has)[NV],
-                                          const float2 (&p)[NV * V / 2]) {
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    if (!has[j]) continue;
-    if constexpr (V == 1)
-      store1(row + col[j], j & 1 ? p[j / 2].y : p[j / 2].x);
-    else
-      Pack<T, V>::store(row + col[j], p + j * (V / 2));
-  }
-}
-
 // ---------------------------------------------------------------- feed
 // The vectors of the rows to come.  A lane copies its own vectors of the next
 // DEPTH - 1 rows into shared memory asynchronously (cp.async; 0 is filled in
@@ -126,15 +122,16 @@ struct Feed {
     ring = RING ? smem_u32(smem) : 0;
   }
   __device__ __forceinline__ uint32_t row_bytes() const { return blockDim.x * ROW; }
-  __device__ __forceinline__ void load(int stream, int j, const T* p, bool ok) {
+  // `bytes` of vector j (0: none); the rest of the vector is 0.
+  __device__ __forceinline__ void load(int stream, int j, const T* p, int bytes) {
     if constexpr (RING) {
       const uint32_t to = ring + at + (stream * NV + j) * step + threadIdx.x * B;
       if constexpr (B == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(ok ? 16 : 0) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(bytes) : "memory");
       else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(p), "r"(ok ? 4 : 0) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(p), "r"(bytes) : "memory");
     } else {
-      if (ok)
+      if (bytes)
         reg[RING ? 0 : stream * NV + j].load(p);
       else
         reg[RING ? 0 : stream * NV + j].zero();
@@ -215,23 +212,28 @@ struct Feed {
 // GROUPS of one degree: all of them (L = 0, or V = 1), the first and the other
 // three of each four (K a multiple of 4: degrees begin at l^2 = 0 or 1 mod 4),
 // or each by itself.
-template <int L, int V, int NV>
+template <int L, int V, int NV, bool SHIFT>
 struct Slots {
+  static constexpr bool SHIFTED = SHIFT;
   static constexpr int K = (L + 1) * (L + 1);
   static constexpr bool FOURS = L > 0 && V > 1 && K % 4 == 0;
   static constexpr int GROUPS = L == 0 || V == 1 ? 1 : FOURS ? V / 2 : V;
   static constexpr int PAIRS = V > 1 ? V / 2 : 1;  // pairs of a vector
-  uint32_t col[NV];
+  using Col = std::conditional_t<SHIFT, int, uint32_t>;
+  Col col[NV];  // of a vector's first value; SHIFT: below 0 in front of the row
   bool has[NV];
+  int cols;
   int lane;         // within the group
   int cls[GROUPS];  // degree
   float2 first[PAIRS];  // 1 where a value is a degree 0, else 0
 
-  __device__ __forceinline__ Slots(const RowShape& sh, int cols) {
+  // `row`: the first row of the group.
+  __device__ __forceinline__ Slots(const RowShape& sh, int cols_, int row) : cols(cols_) {
     lane = threadIdx.x % sh.lanes;
+    const int shift = SHIFT ? (int)((uint32_t)row * (uint32_t)cols % V) : 0;  // V divides 2^32
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      col[j] = (lane + j * sh.active) * V;
+      col[j] = (lane + j * sh.active) * V - shift;
       has[j] = lane < sh.active && (int)col[j] < cols;
     }
     if constexpr (L == 0) {
@@ -239,7 +241,7 @@ struct Slots {
     } else {
 #pragma unroll
       for (int g = 0; g < GROUPS; ++g) {
-        const int k = (int)(col[0] + (FOURS ? g / 2 * 4 + g % 2 : g)) % K;
+        const int k = ((int)col[0] + K + (FOURS ? g / 2 * 4 + g % 2 : g)) % K;
         int l = 0;
 #pragma unroll
         for (int m = 1; m <= L; ++m) l += k >= m * m;
@@ -250,6 +252,25 @@ struct Slots {
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) f[g] = cls[g] == 0 ? 1.0f : 0.0f;
     spread(f, first);
+  }
+  // Whether value i of vector j is one of the row's.
+  __device__ __forceinline__ bool valid(int j, int i) const {
+    return has[j] && (!SHIFT || ((int)col[j] + i >= 0 && (int)col[j] + i < cols));
+  }
+  __device__ __forceinline__ bool whole(int j) const { return has[j] && (!SHIFT || ((int)col[j] >= 0 && (int)col[j] + V <= cols)); }
+  // How many of the values of vector j, from its first, do not lie behind the row.
+  __device__ __forceinline__ int count(int j) const { return !has[j] ? 0 : SHIFT && cols - (int)col[j] < V ? cols - (int)col[j] : V; }
+  // What the first vector holds of the row before is taken out.
+  __device__ __forceinline__ void mask_front(float2 (&p)[NV * V / 2]) const {
+    if constexpr (SHIFT) {
+      if (col[0] < 0) {
+#pragma unroll
+        for (int i = 0; i < V - 1; ++i) {
+          float& t = i & 1 ? p[i / 2].y : p[i / 2].x;
+          t = col[0] + i < 0 ? 0.0f : t;
+        }
+      }
+    }
   }
   // Whether pair s of a vector may hold a degree 0.
   __device__ __forceinline__ static constexpr bool may0(int s) { return !FOURS || s % 2 == 0; }
@@ -297,6 +318,26 @@ struct Slots {
   }
 };
 
+// Stores the values of a row that the lane has.
+template <typename T, int V, int NV, typename S>
+__device__ __forceinline__ void put_pairs(T* row, const S& at, const float2 (&p)[NV * V / 2]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (!at.has[j]) continue;
+    if constexpr (V == 1) {
+      store1(row + at.col[j], j & 1 ? p[j / 2].y : p[j / 2].x);
+    } else {
+      if (!S::SHIFTED || at.whole(j)) {
+        Pack<T, V>::store(row + at.col[j], p + j * (V / 2));
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (at.valid(j, i)) store1(row + at.col[j] + i, i & 1 ? p[j * (V / 2) + i / 2].y : p[j * (V / 2) + i / 2].x);
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------- dropout
 // Which of a lane's values the dropout keeps.  DIRECT (a draw per element,
 // V > 1): each lane draws for its own vectors.  Else the group forms the keep
@@ -305,10 +346,11 @@ struct Slots {
 // that has a part of it.  The bits are formed for as many rows at a time as
 // the lanes have blocks for (a batch), so that no warp of a group draws for
 // the others while they wait; the caller waits until they are visible.
-constexpr int kKeepBytes = kMaxRowThreads * 16 / 8 + kRowThreads;  // a bit a value, a byte each row begun
+constexpr int kKeepBytes = kMaxRowThreads * 16 / 8 + kRowThreads;  // a bit a value, a byte each row begun, one more
 
-template <int L, int V, int NV, bool DIRECT>
+template <typename S, int V, int NV, bool DIRECT>
 struct Keeps {
+  static constexpr bool L = S::K > 1;  // a draw for a channel of K values
   PhiloxBlock blocks[DIRECT ? NV : 1];
   uint32_t unit[DIRECT ? 1 : NV];       // of a vector's first value
   int left[V == 1 || DIRECT ? 1 : NV];  // how many of the vector's values it has
@@ -316,8 +358,7 @@ struct Keeps {
   int bytes;                            // of a row
   int batch, my_row, my_byte;           // rows of a batch; the place that this lane forms
   int half, at_row;                     // the current row's half and place in the batch
-  __device__ __forceinline__ Keeps(const Dropper& d, const Slots<L, V, NV>& at, const RowShape& sh, int cols,
-                                   uint8_t* smem) {
+  __device__ __forceinline__ Keeps(const Dropper& d, const S& at, const RowShape& sh, int cols, uint8_t* smem) {
     if (!d.on) return;
     if constexpr (DIRECT) {
 #pragma unroll
@@ -332,8 +373,8 @@ struct Keeps {
       half = at_row = 0;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        unit[j] = at.has[j] ? at.col[j] / group : 0;
-        if (V > 1) left[V > 1 ? j : 0] = (int)((unit[j] + 1) * group - at.col[j]);
+        unit[j] = at.has[j] && (int)at.col[j] > 0 ? (uint32_t)at.col[j] / group : 0;
+        if (V > 1) left[V > 1 ? j : 0] = (int)((unit[j] + 1) * group) - (int)at.col[j];
       }
     }
   }
@@ -370,8 +411,7 @@ struct Keeps {
     return bits[half * kKeepBytes + at_row * bytes + (n >> 3)] >> (n & 7) & 1;
   }
   // The values p of the current row, `row`, with the dropout applied.
-  __device__ __forceinline__ void apply(const Dropper& d, const Slots<L, V, NV>& at, int row,
-                                        float2 (&p)[NV * V / 2]) const {
+  __device__ __forceinline__ void apply(const Dropper& d, const S& at, int row, float2 (&p)[NV * V / 2]) const {
     if constexpr (DIRECT) {
       const PhiloxRow pr = d.of_row(row);
 #pragma unroll
@@ -399,17 +439,26 @@ struct Keeps {
         float2* f = p + j * (V / 2);
 #pragma unroll
         for (int s = 0; s < V / 2; ++s) f[s] = __fmul2_rn(f[s], both(d.scale));
-        if (L == 0 && d.group < V) {  // each value's unit by itself
+        if (S::SHIFTED && !L && d.group == 1) {  // V bits from some place on (of two bytes)
+          const uint8_t* b = bits + half * kKeepBytes + at_row * bytes + (unit[j] >> 3);
+          uint32_t keep = (b[0] | (uint32_t)b[1] << 8) >> (unit[j] & 7);
+          if ((int)at.col[j] < 0) keep <<= -(int)at.col[j];
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             float& t = i & 1 ? f[i / 2].y : f[i / 2].x;
-            t = at.has[j] && kept((at.col[j] + i) / (uint32_t)d.group) ? t : 0.0f;
+            t = keep >> i & 1 ? t : 0.0f;
+          }
+        } else if (!L && d.group < V) {  // each value's unit by itself
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float& t = i & 1 ? f[i / 2].y : f[i / 2].x;
+            t = at.valid(j, i) && kept((at.col[j] + i) / (uint32_t)d.group) ? t : 0.0f;
           }
         } else {  // two units at most
           const int n = left[j];
           const bool k0 = kept(unit[j]);
           bool k1 = k0;
-          if ((L == 0 || at.K % V) && n < V && at.has[j]) k1 = kept(unit[j] + 1);
+          if ((!L || at.K % V) && n < V && at.has[j]) k1 = kept(unit[j] + 1);
 #pragma unroll
           for (int s = 0; s < V / 2; ++s) {
             f[s].x = ((L && at.K % V == 0) || 2 * s < n ? k0 : k1) ? f[s].x : 0.0f;
@@ -509,17 +558,16 @@ enum : int {
 };
 
 // The weights of a lane's values.
-template <int L, int V, int NV>
-__device__ __forceinline__ void load_weights(const Slots<L, V, NV>& at, const NormArgs& a, float2 (&w)[NV * V / 2]) {
-  using S = Slots<L, V, NV>;
+template <int L, int V, int NV, typename S>
+__device__ __forceinline__ void load_weights(const S& at, const NormArgs& a, float2 (&w)[NV * V / 2]) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (int)(at.col[j] + i) / S::K;
+      const int c = ((int)at.col[j] + i) / S::K;
       int l = 0;
       if constexpr (L > 0) l = at.cls[S::GROUPS == 1 ? 0 : S::FOURS ? i / 4 * 2 + (i % 4 > 0) : i];
-      const float t = at.has[j] && a.w ? a.w[l * a.C + c] : 1.0f;
+      const float t = at.valid(j, i) && a.w ? a.w[l * a.C + c] : 1.0f;
       const int e = j * V + i;
       (e & 1 ? w[e / 2].y : w[e / 2].x) = t;
     }
@@ -529,20 +577,20 @@ __device__ __forceinline__ void load_weights(const Slots<L, V, NV>& at, const No
 // ---------------------------------------------------------------- forward
 // One pass: each value is loaded once, kept in registers through the mean and
 // the centred squares, and stored once.
-template <typename T, int L, int V, int NV, int MODE>
+template <typename T, int L, int V, int NV, bool SHIFT, int MODE>
 __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowShape sh) {
-  using S = Slots<L, V, NV>;
+  using S = Slots<L, V, NV, SHIFT>;
   using F = Feed<T, V, NV, MODE ? 2 : 1, 0>;
   constexpr int P = NV * V / 2, PV = S::PAIRS, NS = L + 1;
   constexpr bool EACH = L == 0 || V == 1;  // a bias per value; else one per vector, which has at most one degree 0
   __shared__ __align__(16) float red1[GroupSum<1>::kRed], red2[GroupSum<NS>::kRed];
-  __shared__ uint8_t bits[MODE == kMixed ? 2 * kKeepBytes : 1];
-  extern __shared__ __align__(16) uint8_t ring[];
-  const S at(sh, a.cols);
+  __shared__ uint8_t bits[MODE == kMixed ? 2 * kKeepBytes + 1 : 1];
+  extern __shared__ __align__(128) uint8_t ring[];
   const int stride = sh.run ? sh.groups : gridDim.x * sh.groups;
   const int begin = blockIdx.x * (sh.run ? sh.run : 1) * sh.groups;
   const int end = sh.run ? min(a.rows, begin + sh.run * sh.groups) : a.rows;
   int row = begin + threadIdx.x / sh.lanes;
+  const S at(sh, a.cols, row);
   F feed(ring);
   const T* x = static_cast<const T*>(a.x) + row * a.x_ld;
   const T* r = static_cast<const T*>(a.r) + row * a.r_ld;
@@ -551,8 +599,9 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
     const bool live = ahead < end;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      feed.load(0, j, x + at.col[j], at.has[j] && live);
-      if (MODE && a.r) feed.load(1, j, r + at.col[j], at.has[j] && live);
+      const int bytes = SHIFT ? (live ? at.count(j) * (int)sizeof(T) : 0) : at.has[j] && live ? V * (int)sizeof(T) : 0;
+      feed.load(0, j, x + at.col[j], bytes);
+      if (MODE && a.r) feed.load(1, j, r + at.col[j], bytes);
     }
     feed.loaded();
     ahead += stride;
@@ -564,22 +613,22 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
   GroupSum<1> sum1(sh.lanes, red1);
   GroupSum<NS> sum2(sh.lanes, red2);
   const Dropper drop(a.drop);
-  Keeps<L, V, NV, MODE == kDirect> keeps(drop, at, sh, a.cols, bits);
+  Keeps<S, V, NV, MODE == kDirect> keeps(drop, at, sh, a.cols, bits);
   float2 w[P], b[EACH ? P : NV];
   bool all = true;  // whether the lane's values are all of the row
-  load_weights<L, V, NV>(at, a, w);
+  load_weights<L, V, NV, S>(at, a, w);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    all = all && at.has[j];
+    all = all && at.whole(j);
     if constexpr (EACH) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int e = j * V + i, c = (int)(at.col[j] + i) / S::K;
-        (e & 1 ? b[e / 2].y : b[e / 2].x) = at.has[j] && a.b && at.cls[0] == 0 ? a.b[c] : 0.0f;
+        const int e = j * V + i, c = ((int)at.col[j] + i) / S::K;
+        (e & 1 ? b[e / 2].y : b[e / 2].x) = at.valid(j, i) && a.b && at.cls[0] == 0 ? a.b[c] : 0.0f;
       }
     } else {
-      const int c = (int)(at.col[j] + V - 1) / S::K;  // the channel that begins in the vector, if one does
-      b[j] = both(at.has[j] && a.b && c * S::K >= (int)at.col[j] ? a.b[c] : 0.0f);
+      const int c = ((int)at.col[j] + V - 1) / S::K;  // the channel that begins in the vector, if one does
+      b[j] = both(at.has[j] && a.b && c * S::K >= (int)at.col[j] && c < a.C ? a.b[c] : 0.0f);
     }
   }
   const float inv = 1.0f / (float)a.C;
@@ -596,11 +645,13 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
     float2 v[P], acc[PV];
     const uint32_t place = feed.wait();
     feed.get(place, 0, v);
+    at.mask_front(v);
     if constexpr (MODE != kPlain) {
       if (drop.on) keeps.apply(drop, at, row, v);
       if (a.r) {
         float2 f[P];
         feed.get(place, 1, f);
+        at.mask_front(f);
 #pragma unroll
         for (int p = 0; p < P; ++p) v[p] = __fadd2_rn(v[p], f[p]);
       }
@@ -609,7 +660,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
     if (MODE == kMixed && drop.on) keeps.form_next(drop, sh, row, stride);
     const bool live = row < end;
     const long long out = (long long)row * a.cols;
-    if (MODE && a.s && live) put_pairs<T, V, NV>(static_cast<T*>(a.s) + out, at.col, at.has, v);
+    if (MODE && a.s && live) put_pairs<T, V, NV>(static_cast<T*>(a.s) + out, at, v);
     // the mean of degree 0
     float part[1] = {0.0f};
 #pragma unroll
@@ -632,8 +683,8 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
     if (!all) {
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        v[p].x = at.has[V == 1 ? 2 * p : p / PV] ? v[p].x : 0.0f;
-        v[p].y = at.has[V == 1 ? 2 * p + 1 : p / PV] ? v[p].y : 0.0f;
+        v[p].x = at.valid(V == 1 ? 2 * p : p / PV, V == 1 ? 0 : p % PV * 2) ? v[p].x : 0.0f;
+        v[p].y = at.valid(V == 1 ? 2 * p + 1 : p / PV, V == 1 ? 0 : p % PV * 2 + 1) ? v[p].y : 0.0f;
       }
     }
 #pragma unroll
@@ -669,7 +720,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
       else
         v[p] = __fmul2_rn(h, w[p]);
     }
-    put_pairs<T, V, NV>(static_cast<T*>(a.y) + out, at.col, at.has, v);
+    put_pairs<T, V, NV>(static_cast<T*>(a.y) + out, at, v);
   }
 }
 
@@ -679,18 +730,18 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
 // over all the rows of its group.  At the end the groups of a CTA are added in
 // their order through shared memory, the orders of a degree with them, and
 // the CTA's (L+2) C sums go to its part of the workspace.
-template <typename T, int L, int V, int NV, int MODE>
+template <typename T, int L, int V, int NV, bool SHIFT, int MODE>
 __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, RowShape sh) {
-  using S = Slots<L, V, NV>;
+  using S = Slots<L, V, NV, SHIFT>;
   using F = Feed<T, V, NV, MODE ? 3 : 2, 1 + S::GROUPS>;
   constexpr int P = NV * V / 2, PV = S::PAIRS, NS = L + 2;
   constexpr bool EACH = L == 0 || V == 1;  // db per value; else per vector, which has at most one degree 0
   __shared__ __align__(16) float red[GroupSum<NS>::kRed];
-  __shared__ uint8_t bits[MODE == kMixed ? 2 * kKeepBytes : 1];
-  extern __shared__ __align__(16) uint8_t ring[];  // at the end the column sums: [cols] g h, [C] g
-  const S at(sh, a.cols);
+  __shared__ uint8_t bits[MODE == kMixed ? 2 * kKeepBytes + 1 : 1];
+  extern __shared__ __align__(128) uint8_t ring[];  // at the end the column sums: [cols] g h, [C] g
   const int stride = gridDim.x * sh.groups;
   int row = blockIdx.x * sh.groups + threadIdx.x / sh.lanes;
+  const S at(sh, a.cols, row);
   F feed(ring);
   const T* x = static_cast<const T*>(a.x) + row * a.x_ld;
   const T* g = static_cast<const T*>(a.g) + row * a.g_ld;
@@ -701,9 +752,10 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
     const bool live = ahead < a.rows;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      feed.load(0, j, x + at.col[j], at.has[j] && live);
-      feed.load(1, j, g + at.col[j], at.has[j] && live);
-      if (MODE && a.r) feed.load(2, j, r + at.col[j], at.has[j] && live);
+      const int bytes = SHIFT ? (live ? at.count(j) * (int)sizeof(T) : 0) : at.has[j] && live ? V * (int)sizeof(T) : 0;
+      feed.load(0, j, x + at.col[j], bytes);
+      feed.load(1, j, g + at.col[j], bytes);
+      if (MODE && a.r) feed.load(2, j, r + at.col[j], bytes);
     }
     feed.load_word(0, st, live);
 #pragma unroll
@@ -719,9 +771,9 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
   for (int d = 0; d < F::DEPTH - 1; ++d) load_row();
   GroupSum<NS> sum(sh.lanes, red);
   const Dropper drop(a.drop);
-  Keeps<L, V, NV, MODE == kDirect> keeps(drop, at, sh, a.cols, bits);
+  Keeps<S, V, NV, MODE == kDirect> keeps(drop, at, sh, a.cols, bits);
   float2 w[P], dw[P], db[EACH ? P : NV];
-  load_weights<L, V, NV>(at, a, w);
+  load_weights<L, V, NV, S>(at, a, w);
 #pragma unroll
   for (int p = 0; p < P; ++p) dw[p] = both(0.0f);
 #pragma unroll
@@ -737,6 +789,8 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
     const uint32_t place = feed.wait();
     feed.get(place, 0, h);
     feed.get(place, 1, av);
+    at.mask_front(h);
+    at.mask_front(av);
     if constexpr (MODE != kPlain && !F::RING) {
       if (a.r) feed.get(place, 2, cr);
     }
@@ -802,15 +856,15 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
 #pragma unroll
         for (int p = 0; p < P; ++p) av[p] = __fadd2_rn(av[p], cr[p]);
       }
-      if (a.gr && live) put_pairs<T, V, NV>(static_cast<T*>(a.gr) + out, at.col, at.has, av);
+      if (a.gr && live) put_pairs<T, V, NV>(static_cast<T*>(a.gr) + out, at, av);
       if (a.gx) {
         if (drop.on) keeps.apply(drop, at, row, av);
-        if (live) put_pairs<T, V, NV>(static_cast<T*>(a.gx) + out, at.col, at.has, av);
+        if (live) put_pairs<T, V, NV>(static_cast<T*>(a.gx) + out, at, av);
       }
       if (MODE == kMixed && drop.on) keeps.next_row();
     } else {
       T* dst = static_cast<T*>(a.gx ? a.gx : a.gr);
-      if (dst && live) put_pairs<T, V, NV>(dst + out, at.col, at.has, av);
+      if (dst && live) put_pairs<T, V, NV>(dst + out, at, av);
     }
   }
   // the sums' kernel may be launched; it waits until this one is done
@@ -818,12 +872,13 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
   if (!a.gw && !a.gb) return;
   feed.drain();  // the ring's memory takes the column sums
   __syncthreads();
-  // The CTA's sums.  The groups of a warp are added by shuffles; then each
-  // warp (or group of several warps) puts its columns into a row of its own,
-  // [C][K padded to an odd number] g h and [C] g, and the rows are added.
+  // The CTA's sums.  The groups of a warp are added by shuffles (SHIFT: their
+  // lanes have different columns); then each warp (or group) puts its columns
+  // into a row of its own, [C][K padded to an odd number] g h and [C] g, and
+  // the rows are added.
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    if (o >= sh.lanes) {
+    if (!SHIFT && o >= sh.lanes) {
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         dw[p].x += __shfl_xor_sync(0xffffffffu, dw[p].x, o);
@@ -838,7 +893,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
   }
   constexpr int KP = S::K | 1;
   float* sums = reinterpret_cast<float*>(ring);
-  const int unit = sh.lanes <= 32 ? 32 : sh.lanes;  // threads that add together
+  const int unit = !SHIFT && sh.lanes <= 32 ? 32 : sh.lanes;  // threads that add together
   const int units = blockDim.x / unit, width = (KP + 1) * a.C;
   if ((int)(threadIdx.x % unit) < sh.lanes) {
     float* mine = sums + threadIdx.x / unit * width;
@@ -847,13 +902,14 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
       if (!at.has[j]) continue;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
+        if (!at.valid(j, i)) continue;
         const int e = j * V + i, col = (int)at.col[j] + i, c = col / S::K, k = col - c * S::K;
         mine[c * KP + k] = e & 1 ? dw[e / 2].y : dw[e / 2].x;
         if (EACH && k == 0) mine[KP * a.C + c] = e & 1 ? db[EACH ? e / 2 : 0].y : db[EACH ? e / 2 : 0].x;
       }
       if (!EACH) {
-        const int c = (int)(at.col[j] + V - 1) / S::K;  // the channel that begins in the vector, if one does
-        if (c * S::K >= (int)at.col[j]) mine[KP * a.C + c] = db[EACH ? 0 : j].x + db[EACH ? 0 : j].y;
+        const int c = ((int)at.col[j] + V - 1) / S::K;  // the channel that begins in the vector, if one does
+        if (c * S::K >= (int)at.col[j] && c < a.C) mine[KP * a.C + c] = db[EACH ? 0 : j].x + db[EACH ? 0 : j].y;
       }
     }
   }
@@ -922,14 +978,14 @@ inline int resident_grid(Kernel kernel, int threads, size_t smem, const DeviceIn
 constexpr int kMaxRingBytes = 220 * 1024;  // of dynamic shared memory, a CTA
 constexpr long long kRunBytes = 128 * 1024;
 
-template <typename T, int L, int V, int NV, bool BACKWARD, int MODE>
+template <typename T, int L, int V, int NV, bool SHIFT, bool BACKWARD, int MODE>
 static eqmp_status launch_mode(NormArgs a, RowShape sh, const DeviceInfo& dev, cudaStream_t st) {
   static int cache[64][33];
   static unsigned long long attr_done = 0;
   const int threads = sh.lanes * sh.groups;
   const long long tiles = ((long long)a.rows + sh.groups - 1) / sh.groups;
   if constexpr (!BACKWARD) {
-    auto kern = k_norm_rows<T, L, V, NV, MODE>;
+    auto kern = k_norm_rows<T, L, V, NV, SHIFT, MODE>;
     const size_t smem = (size_t)threads * Feed<T, V, NV, MODE ? 2 : 1, 0>::BYTES;
     if (ensure_smem_attr(kern, kMaxRingBytes, &attr_done) != cudaSuccess) return EQMP_ERR_CUDA;
     int grid = resident_grid(kern, threads, smem, dev, tiles, cache);
@@ -940,22 +996,26 @@ static eqmp_status launch_mode(NormArgs a, RowShape sh, const DeviceInfo& dev, c
     // Else persistent CTAs in turns, which share out little work evenly.
     const long long bytes = (long long)sh.groups * a.cols * (long long)sizeof(T) * (2 + (a.r != nullptr) + (a.s != nullptr));
     const int run = bytes < kRunBytes ? (int)(kRunBytes / bytes) : 1;
-    if (tiles / run >= 4ll * grid) {
+    if (tiles / run >= 4ll * grid && (!SHIFT || sh.groups % 8 == 0)) {
       sh.run = run;
       grid = (int)((tiles + run - 1) / run);
     }
+    if (SHIFT && !sh.run && grid < tiles) grid = grid / 8 * 8;  // a group's rows are a multiple of 8 apart
+    if (grid < 1) return EQMP_ERR_UNSUPPORTED;
     kern<<<grid, threads, smem, st>>>(a, sh);
     return cuda_status(cudaGetLastError());
   } else {
-    auto kern = k_norm_bwd_rows<T, L, V, NV, MODE>;
+    auto kern = k_norm_bwd_rows<T, L, V, NV, SHIFT, MODE>;
     if (ensure_smem_attr(kern, kMaxRingBytes, &attr_done) != cudaSuccess) return EQMP_ERR_CUDA;
-    const size_t feed = (size_t)threads * Feed<T, V, NV, MODE ? 3 : 2, 1 + Slots<L, V, NV>::GROUPS>::BYTES;
-    constexpr int KP = ((L + 1) * (L + 1)) | 1;  // the CTA's column sums, one row for each warp or larger group
-    const size_t sums = sizeof(float) * (size_t)(KP + 1) * a.C * (sh.lanes <= 32 ? threads / 32 : sh.groups);
+    const size_t feed = (size_t)threads * Feed<T, V, NV, MODE ? 3 : 2, 1 + Slots<L, V, NV, SHIFT>::GROUPS>::BYTES;
+    constexpr int KP = ((L + 1) * (L + 1)) | 1;  // the CTA's column sums, one row for each warp or group
+    const size_t sums = sizeof(float) * (size_t)(KP + 1) * a.C * (!SHIFT && sh.lanes <= 32 ? threads / 32 : sh.groups);
     const size_t smem = feed > sums ? feed : sums;
     int grid = resident_grid(kern, threads, smem, dev, tiles, cache);
     if (grid < 1) return EQMP_ERR_CUDA;
     if (grid > kMaxParts) grid = kMaxParts;
+    if (SHIFT && grid < tiles) grid = grid / 8 * 8;  // a group's rows are a multiple of 8 apart
+    if (grid < 1) return EQMP_ERR_UNSUPPORTED;
     a.parts = grid;
     kern<<<grid, threads, smem, st>>>(a, sh);
     if (cudaGetLastError() != cudaSuccess) return EQMP_ERR_CUDA;
@@ -964,44 +1024,64 @@ static eqmp_status launch_mode(NormArgs a, RowShape sh, const DeviceInfo& dev, c
   }
 }
 
-template <typename T, int L, int V, int NV, bool BACKWARD>
+template <typename T, int L, int V, int NV, bool SHIFT, bool BACKWARD>
 static eqmp_status launch_rows(const NormArgs& a, const RowShape& sh, const DeviceInfo& dev, cudaStream_t st) {
   if (!a.r && !a.drop.threshold && !(BACKWARD ? a.gr && a.gx : a.s != nullptr))
-    return launch_mode<T, L, V, NV, BACKWARD, kPlain>(a, sh, dev, st);
-  if constexpr (L == 0 && V > 1) {
-    if (a.drop.threshold && a.drop.group == 1) return launch_mode<T, L, V, NV, BACKWARD, kDirect>(a, sh, dev, st);
+    return launch_mode<T, L, V, NV, SHIFT, BACKWARD, kPlain>(a, sh, dev, st);
+  if constexpr (L == 0 && V > 1 && !SHIFT) {
+    if (a.drop.threshold && a.drop.group == 1) return launch_mode<T, L, V, NV, SHIFT, BACKWARD, kDirect>(a, sh, dev, st);
   }
-  return launch_mode<T, L, V, NV, BACKWARD, kMixed>(a, sh, dev, st);
+  return launch_mode<T, L, V, NV, SHIFT, BACKWARD, kMixed>(a, sh, dev, st);
 }
 
 // 16 values a lane share the sums' shuffles and barriers over more values; 8
 // leave more lanes to work on a row, which is faster where the rows are few,
 // and fit the registers of the lanes that handle single values.
-template <typename T, int L, int V, bool BACKWARD>
+template <typename T, int L, int V, bool SHIFT, bool BACKWARD>
 static eqmp_status launch_rows_v(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st, bool* done) {
   constexpr int K = (L + 1) * (L + 1), N8 = 8 / V, N16 = 16 / V;
   constexpr int least = pow2_above(BACKWARD ? L + 2 : L + 1);  // what GroupSum needs
-  const RowShape s8 = row_shape(a.cols, K, V, N8, least, a.rows, dev.sms);
-  const RowShape s16 = row_shape(a.cols, K, V, N16, least, a.rows, dev.sms);
+  const int cols = SHIFT ? a.cols + 2 * (V - 1) : a.cols;      // a first and a last vector in part
+  const RowShape s8 = row_shape(cols, K, V, N8, least, a.rows, dev.sms);
+  const RowShape s16 = row_shape(cols, K, V, N16, least, a.rows, dev.sms);
   const bool few = (long long)a.rows * s8.lanes <= (long long)dev.sms * kMaxRowThreads;
   *done = s16.lanes <= kMaxRowThreads;
   if (!*done) return EQMP_OK;
-  if (s8.lanes <= kMaxRowThreads && (V == 1 || few)) return launch_rows<T, L, V, N8, BACKWARD>(a, s8, dev, st);
-  return launch_rows<T, L, V, N16, BACKWARD>(a, s16, dev, st);
+  if (s8.lanes <= kMaxRowThreads && (V == 1 || few || (SHIFT && BACKWARD))) return launch_rows<T, L, V, N8, SHIFT, BACKWARD>(a, s8, dev, st);
+  return launch_rows<T, L, V, N16, SHIFT, BACKWARD>(a, s16, dev, st);
 }
 
-inline bool vec16(const void* p, long long ld, int bytes) {
-  return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * bytes % 16 == 0);
-}
+// How the rows of the arrays in use lie: 16-byte aligned, beginning at the
+// same place behind a 16-byte boundary in all of them as packed rows do, or
+// otherwise.
+struct Alignment {
+  bool rows = true, alike = true;
+  int bytes;
+  long long cols;
+  Alignment(int bytes_, long long cols_) : bytes(bytes_), cols(cols_) { rows = cols * bytes % 16 == 0; }
+  void add(const void* p, long long ld) {
+    if (!p) return;
+    const bool base = reinterpret_cast<uintptr_t>(p) % 16 == 0;
+    rows = rows && base && ld * bytes % 16 == 0;
+    alike = alike && base && ld >= cols && (ld - cols) * bytes % 16 == 0;
+  }
+};
 
-// Runs the pass if the row fits; *done says whether it did.  Vectors of 16
-// bytes where every row of every array starts on one.
+// Runs the pass if the row fits; *done says whether it did.
 template <typename T, int L, bool BACKWARD>
 static eqmp_status launch_rows_l(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st, bool* done) {
-  constexpr int B = sizeof(T);
-  const bool vec = vec16(a.x, a.x_ld, B) && vec16(a.r, a.r_ld, B) && vec16(a.g, a.g_ld, B) && vec16(a.s, a.cols, B) &&
-                   vec16(a.y, a.cols, B) && vec16(a.gr, a.cols, B) && vec16(a.gx, a.cols, B) && a.cols * B % 16 == 0;
-  return vec ? launch_rows_v<T, L, 16 / B, BACKWARD>(a, dev, st, done) : launch_rows_v<T, L, 1, BACKWARD>(a, dev, st, done);
+  constexpr int V = 16 / sizeof(T);
+  Alignment al(sizeof(T), a.cols);
+  al.add(a.x, a.x_ld);
+  al.add(a.r, a.r_ld);
+  al.add(a.g, a.g_ld);
+  for (const void* p : {a.s, a.y, a.gr, a.gx}) al.add(p, a.cols);
+  if (al.rows) return launch_rows_v<T, L, V, false, BACKWARD>(a, dev, st, done);
+  if constexpr ((L + 1) * (L + 1) * sizeof(T) % 16 != 0) {
+    // narrow rows are mostly first and last vector
+    if (al.alike && a.cols >= 4 * V) return launch_rows_v<T, L, V, true, BACKWARD>(a, dev, st, done);
+  }
+  return launch_rows_v<T, L, 1, false, BACKWARD>(a, dev, st, done);
 }
 
 template <typename T, bool BACKWARD>

@@ -317,8 +317,66 @@ def test_many_rows_sum_of_gradients(eq):
         _check(c.backward(eq, got["s"], got["stats"]), *c.backward_bounds(got["s"], got["stats"]))
 
 
+@pytest.mark.parametrize("form", [dict(), dict(residual=True, p=0.2), dict(bf16=True), dict(bf16=True, residual=True, p=0.2),
+                                  dict(bf16=True, residual=True, p=0.2, pad=8), dict(p=0.2, pad=3)], ids=_id)
+@pytest.mark.parametrize("rows,cols", [(20011, 37), (5003, 131), (6001, 509), (2503, 1022), (70001, 33), (1500, 4101)])
+def test_rows_that_begin_anywhere(eq, rows, cols, form):
+    """Rows of odd widths, many to a CTA: they begin at every place behind a 16-byte boundary."""
+    c = Case((rows, cols), **form)
+    got = c.forward(eq)
+    _check(got, *c.forward_bounds())
+    _check(c.backward(eq, got["s"], got["stats"]), *c.backward_bounds(got["s"], got["stats"]))
+
+
+@pytest.mark.parametrize("group", [1, 3, 7, 11, 77])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_dropout_groups_on_rows_that_begin_anywhere(eq, group, bf16):
+    c = Case((3001, 231), bf16=bf16, residual=True, p=0.4, group=group)
+    got = c.forward(eq)
+    _check(got, *c.forward_bounds())
+    _check(c.backward(eq, got["s"], got["stats"]), *c.backward_bounds(got["s"], got["stats"]))
+
+
+@pytest.mark.parametrize("shape", [(3001, 5, 25), (2003, 7, 36), (1501, 13, 49), (999, 129, 25)], ids=str)
+@pytest.mark.parametrize("bf16", [False, True])
+def test_features_that_begin_anywhere(eq, shape, bf16):
+    c = Case(shape, bf16=bf16, residual=True, p=0.3)
+    got = c.forward(eq)
+    _check(got, *c.forward_bounds())
+    _check(c.backward(eq, got["s"], got["stats"]), *c.backward_bounds(got["s"], got["stats"]))
+
+
+def test_neighbours_of_the_rows_are_not_touched(eq):
+    """Results of odd rows in a larger buffer leave what lies around them, and NaN around the inputs does not enter."""
+    import torch
+
+    for dtype in (torch.float32, torch.bfloat16):
+        x = torch.randn(700, 203, device="cuda").to(dtype)
+        wide = torch.full((700 * 203 + 64,), float("nan"), device="cuda", dtype=dtype)
+        inside = wide[32:32 + x.numel()].view(700, 203)
+        inside.copy_(x)
+        out = torch.full_like(wide, 7.0)
+        y = out[32:32 + x.numel()].view(700, 203)
+        stats = torch.empty(700, 2, device="cuda")
+        eq.eqmp_layer_norm(inside, need=("y", "stats"), out=dict(y=y, stats=stats))
+        want = eq.eqmp_layer_norm(x, need=("y", "stats"))
+        assert torch.equal(y, want["y"]) and torch.equal(stats, want["stats"])
+        assert (out[:32] == 7).all() and (out[-32:] == 7).all()
+        gx = out[32:32 + x.numel()].view(700, 203).fill_(7.0)
+        got = eq.eqmp_layer_norm_backward(x, inside, stats, need=("x", "w"), out=dict(x=gx))
+        ref = eq.eqmp_layer_norm_backward(x, x, stats, need=("x", "w"))
+        assert torch.equal(gx, ref["x"]) and torch.equal(got["w"], ref["w"])
+        assert (out[:32] == 7).all() and (out[-32:] == 7).all()
+        pad = torch.full((700, 211 + (dtype is torch.float32)), float("nan"), device="cuda", dtype=dtype)
+        pad[:, :203] = x
+        # rows that lie otherwise may be summed in another order: equal within the bounds, not in every bit
+        _check(eq.eqmp_layer_norm(pad[:, :203]),
+               *nu.forward_bounds(host(x), None, None, 1e-5, None, None, dtype is torch.bfloat16))
+        assert torch.equal(eq.eqmp_dropout(pad[:, :203], eq.Dropout(0.3, 1)), eq.eqmp_dropout(x, eq.Dropout(0.3, 1)))
+
+
 def test_offsets_past_32_bits(eq):
-    """More than 2^31 elements: the last rows are those of a call on them alone, and the sums those of the parts."""
+    """More than 2^31 elements: the last rows against the oracle, and the sum of the gradient against its parts."""
     import torch
 
     rows, cols = 2_140_000, 1009  # 2.16e9 elements of bf16, odd rows
@@ -327,12 +385,10 @@ def test_offsets_past_32_bits(eq):
         x[i:i + (1 << 18)].normal_(generator=torch.Generator(device="cuda").manual_seed(i))
     got = eq.eqmp_layer_norm(x, need=("y", "stats"))
     tail = slice(rows - 100, rows)
-    want = eq.eqmp_layer_norm(x[tail].clone(), need=("y", "stats"))
-    assert torch.equal(got["y"][tail], want["y"]) and torch.equal(got["stats"][tail], want["stats"])
-    g = got.pop("y")  # as the gradient
-    back = eq.eqmp_layer_norm_backward(g, x, got["stats"], need=("x", "b"))
-    one = eq.eqmp_layer_norm_backward(g[tail].clone(), x[tail].clone(), want["stats"], need=("x",))
-    assert torch.equal(back["x"][tail], one["x"])
+    _check({k: got[k][tail] for k in got}, *nu.forward_bounds(host(x[tail]), None, None, 1e-5, None, None, True))
+    g, stats = got.pop("y"), got.pop("stats")  # y as the gradient
+    back = eq.eqmp_layer_norm_backward(g, x, stats, need=("x", "b"))
+    _check(dict(x=back["x"][tail]), *nu.backward_bounds(host(g[tail]), host(x[tail]), host(stats[tail]), None, None, None, True))
     b = sum(g[i:i + (1 << 18)].double().sum(0) for i in range(0, rows, 1 << 18))
     size = sum(g[i:i + (1 << 18)].double().abs().sum(0) for i in range(0, rows, 1 << 18))
     assert ((back["b"].double() - b).abs() <= (64 + rows // 64) * nu.U * size).all()
