@@ -217,57 +217,105 @@ static eqmp_status run_backward(Plane g, Plane x, Plane r, eqmp_dtype dtype, int
 
 // ---------------------------------------------------------------- dropout
 // A CTA takes `lanes` neighbouring vectors (a segment of the columns) of
-// kDropPasses * rows_per_pass rows; a thread keeps its columns, so that what
-// the generator makes of them is formed once, and loads its vectors before it
-// draws for them.  V = 1: the CTA forms the keep bits of its rows' units
-// together first, since neighbours share the generator's blocks.
+// kDropPasses * lines rows; a thread keeps its columns, so that what the
+// generator makes of them is formed once, and loads its vectors before it
+// draws for them.  Rows that begin on 16 bytes: each vector's draws are formed
+// by its thread.  Rows that begin anywhere (SHIFT, or V = 1 where they do not
+// begin alike): the CTA forms the keep bits of its rows' units together, since
+// neighbours share the generator's blocks, and a vector looks its bits up.
+// With SHIFT a CTA's rows are 8 apart, so that all of them begin at the same
+// place behind a 16-byte boundary (see norm_rows.cuh).
 constexpr int kDropThreads = 256, kDropPasses = 8;
 
 struct DropShape {
-  int lanes, segments, rows_per_pass;
+  int lanes, segments, lines;
 };
 
-template <typename T, int V>
+template <typename T, int V, bool SHIFT>
 __global__ void __launch_bounds__(kDropThreads) k_drop(const T* x, long long ld, T* out, int rows, int cols,
                                                        DropArgs d, DropShape sh) {
+  constexpr bool TABLE = V == 1 || SHIFT;
+  constexpr int APART = SHIFT ? 8 : 1;
   const Dropper drop(d);
-  extern __shared__ uint8_t bits[];  // V = 1: [row][byte], from the segment's first unit on, rounded down to a byte
+  extern __shared__ uint8_t bits[];  // TABLE: [row][byte], from the segment's first unit on, rounded down to a byte
   const int lane = threadIdx.x % sh.lanes, line = threadIdx.x / sh.lanes;
   const int seg = blockIdx.x % sh.segments, tile = blockIdx.x / sh.segments;
-  const int col = (seg * sh.lanes + lane) * V;
-  const int row0 = tile * (kDropPasses * sh.rows_per_pass);
-  const bool mine = line < sh.rows_per_pass && col < cols;
+  const int row0 = tile / APART * (APART * kDropPasses * sh.lines) + tile % APART;
+  const int step = APART * sh.lines;  // between a thread's rows
+  const int shift = SHIFT ? (int)((uint32_t)row0 * (uint32_t)cols % V) : 0;
+  const int seg_col = seg * sh.lanes * V - shift, col = seg_col + lane * V;
+  const bool mine = line < sh.lines && col < cols;
+  const int first_row = row0 + APART * line;
+  const int lo = col < 0 ? -col : 0, n = cols - col < V ? cols - col : V;  // the row's values of the vector
   Pack<T, V> in[kDropPasses];
 #pragma unroll
   for (int k = 0; k < kDropPasses; ++k) {
-    const int row = row0 + k * sh.rows_per_pass + line;
-    if (mine && row < rows) in[k].load(x + row * ld + col);
+    const int row = first_row + k * step;
+    // a whole vector may hold the end of the row before and the beginning of the next one
+    if (mine && row < rows) {
+      if (!SHIFT || n == V || row + 1 < rows)
+        in[k].load(x + row * ld + col);
+      else
+        in[k].load_part(x + row * ld + col, n);
+    }
   }
-  const uint32_t unit = (uint32_t)col / (uint32_t)drop.group;
-  if constexpr (V == 1) {
-    const uint32_t first = (uint32_t)(seg * sh.lanes) / (uint32_t)drop.group >> 3;
-    const uint32_t last = (uint32_t)(seg * sh.lanes + sh.lanes - 1) / (uint32_t)drop.group >> 3;
-    const int bytes = last - first + 1;
+  const uint32_t unit = (uint32_t)(col > 0 ? col : 0) / (uint32_t)drop.group;
+  const int left = (int)((unit + 1) * drop.group) - col;  // of the vector's values in its first unit
+  if constexpr (TABLE) {
+    const int last_col = seg_col + sh.lanes * V - 1 < cols - 1 ? seg_col + sh.lanes * V - 1 : cols - 1;
+    const uint32_t first = (uint32_t)(seg_col > 0 ? seg_col : 0) / (uint32_t)drop.group >> 3;
+    const int bytes = (int)((uint32_t)last_col / (uint32_t)drop.group >> 3) - (int)first + 1;
     if (drop.on) {
-      for (int i = threadIdx.x; i < bytes * kDropPasses * sh.rows_per_pass; i += blockDim.x)
-        bits[i] = (uint8_t)drop.keep_bits(drop.block(row0 + i / bytes, first + i % bytes));
+      for (int i = threadIdx.x; i < bytes * kDropPasses * sh.lines; i += blockDim.x)
+        bits[i] = (uint8_t)drop.keep_bits(drop.block(row0 + i / bytes * APART, first + i % bytes));
       __syncthreads();
     }
     const uint8_t* b = bits + line * bytes + ((unit >> 3) - first);
 #pragma unroll
-    for (int k = 0; k < kDropPasses; ++k) {
-      const int row = row0 + k * sh.rows_per_pass + line;
+    for (int k = 0; k < kDropPasses; ++k, b += sh.lines * bytes) {
+      const int row = first_row + k * step;
       if (!mine || row >= rows) break;
-      float f = load1(&in[k].v);
-      if (drop.on) f = b[k * sh.rows_per_pass * bytes] >> (unit & 7) & 1 ? f * drop.scale : 0.0f;
-      store1(out + (long long)row * cols + col, f);
+      T* to = out + (long long)row * cols + col;
+      if constexpr (V == 1) {
+        float f = load1(&in[k].v);
+        if (drop.on) f = *b >> (unit & 7) & 1 ? f * drop.scale : 0.0f;
+        store1(to, f);
+      } else {
+        float2 f[V / 2];
+        in[k].get(f);
+        if (drop.on) {
+          uint32_t keep;
+          if (drop.group == 1) {
+            keep = (b[0] | (uint32_t)b[1] << 8) >> (unit & 7);
+            keep <<= lo;
+          } else {  // one unit after the other
+            keep = *b >> (unit & 7) & 1 ? (1u << V) - 1 : 0;
+            uint32_t u = unit;
+#pragma unroll 1
+            for (int i = left; i < n; i += drop.group) {
+              ++u;
+              const uint32_t from = 1u << i, rest = (1u << V) - from;
+              keep = b[(u >> 3) - (unit >> 3)] >> (u & 7) & 1 ? keep | rest : keep & ~rest;
+            }
+          }
+#pragma unroll
+          for (int s = 0; s < V / 2; ++s) {
+            f[s] = __fmul2_rn(f[s], both(drop.scale));
+            f[s].x = keep >> (2 * s) & 1 ? f[s].x : 0.0f;
+            f[s].y = keep >> (2 * s + 1) & 1 ? f[s].y : 0.0f;
+          }
+        }
+        if (lo == 0 && n == V)
+          Pack<T, V>::store(to, f);
+        else
+          put_part(to, f, lo, n);
+      }
     }
   } else {
     const PhiloxBlock pb = drop.of_block(unit >> 3);
-    const int left = (int)((unit + 1) * drop.group - col);  // of the vector's values in its first unit
 #pragma unroll
     for (int k = 0; k < kDropPasses; ++k) {
-      const int row = row0 + k * sh.rows_per_pass + line;
+      const int row = first_row + k * step;
       if (!mine || row >= rows) break;
       float2 f[V / 2];
       in[k].get(f);
@@ -306,19 +354,21 @@ __global__ void __launch_bounds__(kDropThreads) k_drop(const T* x, long long ld,
   }
 }
 
-template <typename T, int V>
+template <typename T, int V, bool SHIFT>
 static eqmp_status launch_drop(const T* x, long long ld, T* out, int rows, int cols, const DropArgs& d, cudaStream_t st) {
-  const int vectors = cols / V;
+  const int vectors = SHIFT ? (cols + 2 * (V - 1)) / V : cols / V, apart = SHIFT ? 8 : 1;
   DropShape sh;
   sh.segments = (vectors + kDropThreads - 1) / kDropThreads;
   sh.lanes = (vectors + sh.segments - 1) / sh.segments;
-  sh.rows_per_pass = kDropThreads / sh.lanes;
-  const int threads = (sh.lanes * sh.rows_per_pass + 31) / 32 * 32;
-  const int tile = kDropPasses * sh.rows_per_pass;
-  const long long grid = ((long long)rows + tile - 1) / tile * sh.segments;
+  sh.lines = kDropThreads / sh.lanes;
+  if (sh.lines > rows / (apart * kDropPasses)) sh.lines = rows / (apart * kDropPasses) > 0 ? rows / (apart * kDropPasses) : 1;
+  const int threads = (sh.lanes * sh.lines + 31) / 32 * 32;
+  const int tile = kDropPasses * sh.lines;
+  const long long grid = ((long long)rows + apart * tile - 1) / (apart * tile) * apart * sh.segments;
   if (grid > INT32_MAX) return EQMP_ERR_UNSUPPORTED;
-  const size_t smem = V == 1 ? (size_t)(sh.lanes / 8 + 2) * tile : 0;
-  k_drop<T, V><<<(unsigned)grid, threads, smem, st>>>(x, ld, out, rows, cols, d, sh);
+  // a byte for eight units begun, one more read with the last
+  const size_t smem = V == 1 || SHIFT ? (size_t)(sh.lanes * V / 8 + 2) * tile + 1 : 0;
+  k_drop<T, V, SHIFT><<<(unsigned)grid, threads, smem, st>>>(x, ld, out, rows, cols, d, sh);
   return cuda_status(cudaGetLastError());
 }
 
@@ -331,7 +381,10 @@ static eqmp_status run_dropout(const void* x, long long ld, void* out, int rows,
   Alignment al(B, cols);
   al.add(x, ld);
   al.add(out, cols);
-  return al.rows ? launch_drop<T, 16 / B>(in, ld, to, rows, cols, d, st) : launch_drop<T, 1>(in, ld, to, rows, cols, d, st);
+  if (al.rows) return launch_drop<T, 16 / B, false>(in, ld, to, rows, cols, d, st);
+  // in place a row's last vector would read what another thread writes
+  if (al.alike && cols >= 4 * (16 / B) && in != to) return launch_drop<T, 16 / B, true>(in, ld, to, rows, cols, d, st);
+  return launch_drop<T, 1, false>(in, ld, to, rows, cols, d, st);
 }
 
 }  // namespace eqmp

@@ -52,6 +52,9 @@ template <>
 struct Pack<float, 4> {
   float4 v;
   __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void load_part(const float* p, int n) {  // the first n < 4 values
+    v = make_float4(p[0], n > 1 ? p[1] : 0.0f, n > 2 ? p[2] : 0.0f, 0.0f);
+  }
   __device__ __forceinline__ void zero() { v = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
   __device__ __forceinline__ void get(float2* f) const {
     f[0] = make_float2(v.x, v.y);
@@ -66,6 +69,11 @@ template <>
 struct Pack<__nv_bfloat16, 8> {
   uint4 v;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load_part(const __nv_bfloat16* p, int n) {  // the first n < 8 values
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+    auto pair = [&](int i) { return (i < n ? (uint32_t)h[i] : 0u) | (i + 1 < n ? (uint32_t)h[i + 1] << 16 : 0u); };
+    v = make_uint4(pair(0), pair(2), pair(4), pair(6));
+  }
   __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void get(float2* f) const {
     f[0] = make_float2(bf16_lo(v.x), bf16_hi(v.x));
@@ -83,6 +91,7 @@ template <typename T>
 struct Pack<T, 1> {
   T v;
   __device__ __forceinline__ void load(const T* p) { v = *p; }
+  __device__ __forceinline__ void load_part(const T* p, int) { v = *p; }
   __device__ __forceinline__ void zero() { v = T(0.0f); }
 };
 
@@ -260,6 +269,8 @@ struct Slots {
   __device__ __forceinline__ bool whole(int j) const { return has[j] && (!SHIFT || ((int)col[j] >= 0 && (int)col[j] + V <= cols)); }
   // How many of the values of vector j, from its first, do not lie behind the row.
   __device__ __forceinline__ int count(int j) const { return !has[j] ? 0 : SHIFT && cols - (int)col[j] < V ? cols - (int)col[j] : V; }
+  // How many values of vector 0 lie in front of the row.
+  __device__ __forceinline__ int front() const { return SHIFT && (int)col[0] < 0 ? -(int)col[0] : 0; }
   // What the first vector holds of the row before is taken out.
   __device__ __forceinline__ void mask_front(float2 (&p)[NV * V / 2]) const {
     if constexpr (SHIFT) {
@@ -269,6 +280,19 @@ struct Slots {
           float& t = i & 1 ? p[i / 2].y : p[i / 2].x;
           t = col[0] + i < 0 ? 0.0f : t;
         }
+      }
+    }
+  }
+  // Values that are not the row's become 0.
+  __device__ __forceinline__ void clear_outside(float2 (&p)[NV * V / 2]) const {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int n = count(j), lo = j ? 0 : front();
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = j * V + i;
+        float& t = e & 1 ? p[e / 2].y : p[e / 2].x;
+        t = i < n && i >= lo ? t : 0.0f;
       }
     }
   }
@@ -318,6 +342,34 @@ struct Slots {
   }
 };
 
+// Stores the values lo..n-1 of a vector, where either lo is 0 or n is V: in at
+// most three pieces, since the vector begins on 16 bytes.
+__device__ __forceinline__ void put_part(float* p, const float2* f, int lo, int n) {
+  if (lo == 0) {
+    if (n & 2) *reinterpret_cast<float2*>(p) = f[0];
+    if (n & 1) p[n & 2] = n & 2 ? f[1].x : f[0].x;
+  } else {
+    if (lo <= 2) *reinterpret_cast<float2*>(p + 2) = f[1];
+    if (lo & 1) p[lo] = lo == 1 ? f[0].y : f[1].y;
+  }
+}
+__device__ __forceinline__ void put_part(__nv_bfloat16* p, const float2* f, int lo, int n) {
+  const uint32_t w0 = pack_bf16x2(f[0].x, f[0].y), w1 = pack_bf16x2(f[1].x, f[1].y);
+  const uint32_t w2 = pack_bf16x2(f[2].x, f[2].y), w3 = pack_bf16x2(f[3].x, f[3].y);
+  if (lo == 0) {
+    const uint32_t a = n & 4 ? w2 : w0, b = n & 4 ? w3 : w1;
+    if (n & 4) *reinterpret_cast<uint2*>(p) = make_uint2(w0, w1);
+    if (n & 2) *reinterpret_cast<uint32_t*>(p + (n & 4)) = a;
+    if (n & 1) reinterpret_cast<uint16_t*>(p)[n & 6] = (uint16_t)(n & 2 ? b : a);
+  } else {
+    const int m = 8 - lo;  // values
+    const uint32_t a = m & 4 ? w1 : w3, b = m & 4 ? w0 : w2;
+    if (m & 4) *reinterpret_cast<uint2*>(p + 4) = make_uint2(w2, w3);
+    if (m & 2) *reinterpret_cast<uint32_t*>(p + (lo + (m & 1))) = a;
+    if (m & 1) reinterpret_cast<uint16_t*>(p)[lo] = (uint16_t)((m & 2 ? b : a) >> 16);
+  }
+}
+
 // Stores the values of a row that the lane has.
 template <typename T, int V, int NV, typename S>
 __device__ __forceinline__ void put_pairs(T* row, const S& at, const float2 (&p)[NV * V / 2]) {
@@ -327,13 +379,10 @@ __device__ __forceinline__ void put_pairs(T* row, const S& at, const float2 (&p)
     if constexpr (V == 1) {
       store1(row + at.col[j], j & 1 ? p[j / 2].y : p[j / 2].x);
     } else {
-      if (!S::SHIFTED || at.whole(j)) {
+      if (!S::SHIFTED || at.whole(j))
         Pack<T, V>::store(row + at.col[j], p + j * (V / 2));
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (at.valid(j, i)) store1(row + at.col[j] + i, i & 1 ? p[j * (V / 2) + i / 2].y : p[j * (V / 2) + i / 2].x);
-      }
+      else
+        put_part(row + at.col[j], p + j * (V / 2), j ? 0 : at.front(), at.count(j));
     }
   }
 }
@@ -680,13 +729,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
       if (!S::may0(p % PV)) continue;
       v[p] = L ? __ffma2_rn(both(-mean), at.first[p % PV], v[p]) : __fadd2_rn(both(-mean), v[p]);
     }
-    if (!all) {
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        v[p].x = at.valid(V == 1 ? 2 * p : p / PV, V == 1 ? 0 : p % PV * 2) ? v[p].x : 0.0f;
-        v[p].y = at.valid(V == 1 ? 2 * p + 1 : p / PV, V == 1 ? 0 : p % PV * 2 + 1) ? v[p].y : 0.0f;
-      }
-    }
+    if (!all) at.clear_outside(v);
 #pragma unroll
     for (int s = 0; s < PV; ++s) {
       acc[s] = __fmul2_rn(v[s], v[s]);
