@@ -251,8 +251,9 @@ __global__ void __launch_bounds__(kDropThreads) k_drop(const T* x, long long ld,
 #pragma unroll
   for (int k = 0; k < kDropPasses; ++k) {
     const int row = first_row + k * step;
+    if (SHIFT && (!mine || row >= rows)) break;
     // a whole vector may hold the end of the row before and the beginning of the next one
-    if (mine && row < rows) {
+    if (SHIFT || (mine && row < rows)) {
       if (!SHIFT || n == V || row + 1 < rows)
         in[k].load(x + row * ld + col);
       else
@@ -378,12 +379,11 @@ static eqmp_status run_dropout(const void* x, long long ld, void* out, int rows,
   constexpr int B = sizeof(T);
   const T* in = static_cast<const T*>(x);
   T* to = static_cast<T*>(out);
-  Alignment al(B, cols);
-  al.add(x, ld);
-  al.add(out, cols);
-  if (al.rows) return launch_drop<T, 16 / B, false>(in, ld, to, rows, cols, d, st);
+  const bool whole = cols * (long long)B % 16 == 0;
+  if (whole && on16(x) && on16(out) && ld * B % 16 == 0) return launch_drop<T, 16 / B, false>(in, ld, to, rows, cols, d, st);
   // in place a row's last vector would read what another thread writes
-  if (al.alike && cols >= 4 * (16 / B) && in != to) return launch_drop<T, 16 / B, true>(in, ld, to, rows, cols, d, st);
+  if (cols >= 4 * (16 / B) && in != to && on16(out) && lies_packed(x, ld, cols, B))
+    return launch_drop<T, 16 / B, true>(in, ld, to, rows, cols, d, st);
   return launch_drop<T, 1, false>(in, ld, to, rows, cols, d, st);
 }
 

@@ -36,7 +36,12 @@ struct RowShape {
   int active;  // lanes that hold values
   int groups;  // rows of a CTA at a time
   int run;     // forward: rounds of a CTA over neighbouring rows; 0: CTAs take turns
+  int apart;   // kShiftApart: the inputs that lie otherwise than the outputs
 };
+enum : int { kApartX = 1, kApartG = 2, kApartR = 4 };
+// Where rows begin: on 16 bytes; anywhere, in all arrays alike; anywhere, with
+// some fp32 inputs copied value by value.
+enum : int { kOn16 = 0, kShift = 1, kShiftApart = 2 };
 
 constexpr int kRowThreads = 128;     // of a CTA, where a group is smaller
 constexpr int kMaxRowThreads = 512;  // 128 registers a thread
@@ -146,6 +151,16 @@ struct Feed {
         reg[RING ? 0 : stream * NV + j].zero();
     }
   }
+  // Values lo..n-1 of vector j, each by itself; the rest is 0.
+  __device__ __forceinline__ void load_values(int stream, int j, const T* p, int lo, int n) {
+    if constexpr (sizeof(T) == 4 && V > 1) {
+      const uint32_t to = ring + at + (stream * NV + j) * step + threadIdx.x * B;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + 4 * i), "l"(p + i), "r"(i >= lo && i < n ? 4 : 0)
+                     : "memory");
+    }
+  }
   __device__ __forceinline__ void load_word(int k, const float* p, bool ok) {
     if constexpr (RING) {
       const uint32_t to = ring + at + STREAMS * NV * step + (k * blockDim.x + threadIdx.x) * 4;
@@ -221,14 +236,14 @@ struct Feed {
 // GROUPS of one degree: all of them (L = 0, or V = 1), the first and the other
 // three of each four (K a multiple of 4: degrees begin at l^2 = 0 or 1 mod 4),
 // or each by itself.
-template <int L, int V, int NV, bool SHIFT>
+template <int L, int V, int NV, int SHIFT>
 struct Slots {
-  static constexpr bool SHIFTED = SHIFT;
+  static constexpr int SHIFTED = SHIFT;
   static constexpr int K = (L + 1) * (L + 1);
   static constexpr bool FOURS = L > 0 && V > 1 && K % 4 == 0;
   static constexpr int GROUPS = L == 0 || V == 1 ? 1 : FOURS ? V / 2 : V;
   static constexpr int PAIRS = V > 1 ? V / 2 : 1;  // pairs of a vector
-  using Col = std::conditional_t<SHIFT, int, uint32_t>;
+  using Col = std::conditional_t<(SHIFT > 0), int, uint32_t>;
   Col col[NV];  // of a vector's first value; SHIFT: below 0 in front of the row
   bool has[NV];
   int cols;
@@ -599,6 +614,21 @@ struct GroupSum {
   }
 };
 
+// Vector j of one input of a row.
+template <typename F, typename S, typename T>
+__device__ __forceinline__ void load_vector(F& feed, int stream, int j, const T* row, const S& at, bool live, bool apart) {
+  constexpr int V = F::B / (int)sizeof(T);
+  if constexpr (S::SHIFTED) {
+    const int n = live ? at.count(j) : 0;
+    if (S::SHIFTED == kShiftApart && apart)
+      feed.load_values(stream, j, row + at.col[j], j ? 0 : at.front(), n);
+    else
+      feed.load(stream, j, row + at.col[j], n * (int)sizeof(T));
+  } else {
+    feed.load(stream, j, row + at.col[j], at.has[j] && live ? V * (int)sizeof(T) : 0);
+  }
+}
+
 // What stands in front of the norm, and behind it in the backward pass.
 enum : int {
   kPlain = 0,   // nothing
@@ -626,7 +656,7 @@ __device__ __forceinline__ void load_weights(const S& at, const NormArgs& a, flo
 // ---------------------------------------------------------------- forward
 // One pass: each value is loaded once, kept in registers through the mean and
 // the centred squares, and stored once.
-template <typename T, int L, int V, int NV, bool SHIFT, int MODE>
+template <typename T, int L, int V, int NV, int SHIFT, int MODE>
 __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowShape sh) {
   using S = Slots<L, V, NV, SHIFT>;
   using F = Feed<T, V, NV, MODE ? 2 : 1, 0>;
@@ -648,9 +678,8 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
     const bool live = ahead < end;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int bytes = SHIFT ? (live ? at.count(j) * (int)sizeof(T) : 0) : at.has[j] && live ? V * (int)sizeof(T) : 0;
-      feed.load(0, j, x + at.col[j], bytes);
-      if (MODE && a.r) feed.load(1, j, r + at.col[j], bytes);
+      load_vector(feed, 0, j, x, at, live, sh.apart & kApartX);
+      if (MODE && a.r) load_vector(feed, 1, j, r, at, live, sh.apart & kApartR);
     }
     feed.loaded();
     ahead += stride;
@@ -773,7 +802,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
 // over all the rows of its group.  At the end the groups of a CTA are added in
 // their order through shared memory, the orders of a degree with them, and
 // the CTA's (L+2) C sums go to its part of the workspace.
-template <typename T, int L, int V, int NV, bool SHIFT, int MODE>
+template <typename T, int L, int V, int NV, int SHIFT, int MODE>
 __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, RowShape sh) {
   using S = Slots<L, V, NV, SHIFT>;
   using F = Feed<T, V, NV, MODE ? 3 : 2, 1 + S::GROUPS>;
@@ -795,10 +824,9 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
     const bool live = ahead < a.rows;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int bytes = SHIFT ? (live ? at.count(j) * (int)sizeof(T) : 0) : at.has[j] && live ? V * (int)sizeof(T) : 0;
-      feed.load(0, j, x + at.col[j], bytes);
-      feed.load(1, j, g + at.col[j], bytes);
-      if (MODE && a.r) feed.load(2, j, r + at.col[j], bytes);
+      load_vector(feed, 0, j, x, at, live, sh.apart & kApartX);
+      load_vector(feed, 1, j, g, at, live, sh.apart & kApartG);
+      if (MODE && a.r) load_vector(feed, 2, j, r, at, live, sh.apart & kApartR);
     }
     feed.load_word(0, st, live);
 #pragma unroll
@@ -993,7 +1021,7 @@ inline RowShape row_shape(int cols, int K, int V, int NV, int min_lanes, int row
     sh.lanes = (sh.active + 31) / 32 * 32;
   }
   sh.groups = sh.lanes < kRowThreads ? kRowThreads / sh.lanes : 1;
-  sh.run = 0;
+  sh.run = sh.apart = 0;
   const int whole = sh.lanes < 32 ? 32 / sh.lanes : 1;  // groups of a warp
   while (sh.groups / 2 >= whole && (long long)sms * (sh.groups / 2) >= rows) sh.groups /= 2;
   return sh;
@@ -1021,7 +1049,7 @@ inline int resident_grid(Kernel kernel, int threads, size_t smem, const DeviceIn
 constexpr int kMaxRingBytes = 220 * 1024;  // of dynamic shared memory, a CTA
 constexpr long long kRunBytes = 128 * 1024;
 
-template <typename T, int L, int V, int NV, bool SHIFT, bool BACKWARD, int MODE>
+template <typename T, int L, int V, int NV, int SHIFT, bool BACKWARD, int MODE>
 static eqmp_status launch_mode(NormArgs a, RowShape sh, const DeviceInfo& dev, cudaStream_t st) {
   static int cache[64][33];
   static unsigned long long attr_done = 0;
@@ -1067,11 +1095,11 @@ static eqmp_status launch_mode(NormArgs a, RowShape sh, const DeviceInfo& dev, c
   }
 }
 
-template <typename T, int L, int V, int NV, bool SHIFT, bool BACKWARD>
+template <typename T, int L, int V, int NV, int SHIFT, bool BACKWARD>
 static eqmp_status launch_rows(const NormArgs& a, const RowShape& sh, const DeviceInfo& dev, cudaStream_t st) {
   if (!a.r && !a.drop.threshold && !(BACKWARD ? a.gr && a.gx : a.s != nullptr))
     return launch_mode<T, L, V, NV, SHIFT, BACKWARD, kPlain>(a, sh, dev, st);
-  if constexpr (L == 0 && V > 1 && !SHIFT) {
+  if constexpr (L == 0 && V > 1 && SHIFT == kOn16) {
     if (a.drop.threshold && a.drop.group == 1) return launch_mode<T, L, V, NV, SHIFT, BACKWARD, kDirect>(a, sh, dev, st);
   }
   return launch_mode<T, L, V, NV, SHIFT, BACKWARD, kMixed>(a, sh, dev, st);
@@ -1080,51 +1108,52 @@ static eqmp_status launch_rows(const NormArgs& a, const RowShape& sh, const Devi
 // 16 values a lane share the sums' shuffles and barriers over more values; 8
 // leave more lanes to work on a row, which is faster where the rows are few,
 // and fit the registers of the lanes that handle single values.
-template <typename T, int L, int V, bool SHIFT, bool BACKWARD>
-static eqmp_status launch_rows_v(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st, bool* done) {
+template <typename T, int L, int V, int SHIFT, bool BACKWARD>
+static eqmp_status launch_rows_v(const NormArgs& a, int apart, const DeviceInfo& dev, cudaStream_t st, bool* done) {
   constexpr int K = (L + 1) * (L + 1), N8 = 8 / V, N16 = 16 / V;
   constexpr int least = pow2_above(BACKWARD ? L + 2 : L + 1);  // what GroupSum needs
   const int cols = SHIFT ? a.cols + 2 * (V - 1) : a.cols;      // a first and a last vector in part
-  const RowShape s8 = row_shape(cols, K, V, N8, least, a.rows, dev.sms);
-  const RowShape s16 = row_shape(cols, K, V, N16, least, a.rows, dev.sms);
+  RowShape s8 = row_shape(cols, K, V, N8, least, a.rows, dev.sms);
+  RowShape s16 = row_shape(cols, K, V, N16, least, a.rows, dev.sms);
+  s8.apart = s16.apart = apart;
   const bool few = (long long)a.rows * s8.lanes <= (long long)dev.sms * kMaxRowThreads;
   *done = s16.lanes <= kMaxRowThreads;
   if (!*done) return EQMP_OK;
-  if (s8.lanes <= kMaxRowThreads && (V == 1 || few || (SHIFT && BACKWARD))) return launch_rows<T, L, V, N8, SHIFT, BACKWARD>(a, s8, dev, st);
+  if (s8.lanes <= kMaxRowThreads && (V == 1 || few || (SHIFT != kOn16 && BACKWARD))) return launch_rows<T, L, V, N8, SHIFT, BACKWARD>(a, s8, dev, st);
   return launch_rows<T, L, V, N16, SHIFT, BACKWARD>(a, s16, dev, st);
 }
 
-// How the rows of the arrays in use lie: 16-byte aligned, beginning at the
-// same place behind a 16-byte boundary in all of them as packed rows do, or
-// otherwise.
-struct Alignment {
-  bool rows = true, alike = true;
-  int bytes;
-  long long cols;
-  Alignment(int bytes_, long long cols_) : bytes(bytes_), cols(cols_) { rows = cols * bytes % 16 == 0; }
-  void add(const void* p, long long ld) {
-    if (!p) return;
-    const bool base = reinterpret_cast<uintptr_t>(p) % 16 == 0;
-    rows = rows && base && ld * bytes % 16 == 0;
-    alike = alike && base && ld >= cols && (ld - cols) * bytes % 16 == 0;
-  }
-};
+inline bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Runs the pass if the row fits; *done says whether it did.
+// Whether the rows of an array begin where packed rows of `cols` elements do,
+// counted from a 16-byte boundary.
+inline bool lies_packed(const void* p, long long ld, long long cols, int bytes) {
+  return on16(p) && ld >= cols && (ld - cols) * bytes % 16 == 0;
+}
+
+// Runs the pass if the row fits; *done says whether it did.  Vectors of 16
+// bytes where the outputs begin on 16 bytes and the inputs lie as they do;
+// fp32 inputs that lie otherwise are copied value by value into the vectors'
+// places.  Else, and where rows would be mostly first and last vector, lanes
+// handle single values.
 template <typename T, int L, bool BACKWARD>
 static eqmp_status launch_rows_l(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st, bool* done) {
-  constexpr int V = 16 / sizeof(T);
-  Alignment al(sizeof(T), a.cols);
-  al.add(a.x, a.x_ld);
-  al.add(a.r, a.r_ld);
-  al.add(a.g, a.g_ld);
-  for (const void* p : {a.s, a.y, a.gr, a.gx}) al.add(p, a.cols);
-  if (al.rows) return launch_rows_v<T, L, V, false, BACKWARD>(a, dev, st, done);
-  if constexpr ((L + 1) * (L + 1) * sizeof(T) % 16 != 0) {
-    // narrow rows are mostly first and last vector
-    if (al.alike && a.cols >= 4 * V) return launch_rows_v<T, L, V, true, BACKWARD>(a, dev, st, done);
+  constexpr int B = sizeof(T), V = 16 / B;
+  const bool outputs = on16(a.s) && on16(a.y) && on16(a.gr) && on16(a.gx);
+  const bool whole = a.cols * (long long)B % 16 == 0;  // vectors
+  auto apart = [&](const void* p, long long ld, int bit) {
+    if (!p || (whole && on16(p) && ld * B % 16 == 0) || (!whole && lies_packed(p, ld, a.cols, B))) return 0;
+    return bit;
+  };
+  const int which = apart(a.x, a.x_ld, kApartX) | apart(a.g, a.g_ld, kApartG) | apart(a.r, a.r_ld, kApartR);
+  if (outputs && whole && !which) return launch_rows_v<T, L, V, kOn16, BACKWARD>(a, 0, dev, st, done);
+  if constexpr ((L + 1) * (L + 1) * B % 16 != 0) {
+    if (outputs && a.cols >= 4 * V && !which) return launch_rows_v<T, L, V, kShift, BACKWARD>(a, 0, dev, st, done);
   }
-  return launch_rows_v<T, L, 1, false, BACKWARD>(a, dev, st, done);
+  if constexpr (L == 0 && B == 4) {  // features are packed
+    if (outputs && a.cols >= 4 * V) return launch_rows_v<T, L, V, kShiftApart, BACKWARD>(a, which, dev, st, done);
+  }
+  return launch_rows_v<T, L, 1, kOn16, BACKWARD>(a, 0, dev, st, done);
 }
 
 template <typename T, bool BACKWARD>
