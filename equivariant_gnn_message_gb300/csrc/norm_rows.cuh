@@ -636,9 +636,31 @@ enum : int {
   kDirect = 2,  // as kMixed, with dropout by element drawn lane by lane (V > 1, L = 0)
 };
 
+// The values of a parameter [cols] at a lane's columns, in vectors of 16 bytes
+// (L = 0, rows on 16 bytes, the parameter too); `otherwise` outside the row.
+template <int V, int NV, typename S>
+__device__ __forceinline__ void load_columns(const S& at, const float* from, float otherwise, float2 (&w)[NV * V / 2]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      float4 t = make_float4(otherwise, otherwise, otherwise, otherwise);
+      if (at.has[j]) t = *reinterpret_cast<const float4*>(from + at.col[j] + i);
+      w[(j * V + i) / 2] = make_float2(t.x, t.y);
+      w[(j * V + i) / 2 + 1] = make_float2(t.z, t.w);
+    }
+  }
+}
+
 // The weights of a lane's values.
 template <int L, int V, int NV, typename S>
 __device__ __forceinline__ void load_weights(const S& at, const NormArgs& a, float2 (&w)[NV * V / 2]) {
+  if constexpr (L == 0 && V > 1 && S::SHIFTED == kOn16) {
+    if (a.w && reinterpret_cast<uintptr_t>(a.w) % 16 == 0) {
+      load_columns<V, NV>(at, a.w, 1.0f, w);
+      return;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
 #pragma unroll
@@ -695,9 +717,15 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
   float2 w[P], b[EACH ? P : NV];
   bool all = true;  // whether the lane's values are all of the row
   load_weights<L, V, NV, S>(at, a, w);
+  bool biased = false;
+  if constexpr (L == 0 && V > 1 && SHIFT == kOn16) {
+    biased = a.b && reinterpret_cast<uintptr_t>(a.b) % 16 == 0;
+    if (biased) load_columns<V, NV>(at, a.b, 0.0f, b);
+  }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     all = all && at.whole(j);
+    if (biased) continue;
     if constexpr (EACH) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -989,11 +1017,15 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
   float* part = a.parts > 1 ? a.part + (long long)blockIdx.x * M : nullptr;
   for (int m = threadIdx.x; m < M; m += blockDim.x) {
     float t = 0.0f;
-    const int l = m < nw ? m / a.C : 0, c = m - (m < nw ? l * a.C : nw);
-    const float* from = m < nw ? sums + c * KP + l * l : sums + KP * a.C + c;
-    const int orders = m < nw ? 2 * l + 1 : 1;
-    for (int u = 0; u < units; ++u, from += width)
-      for (int k = 0; k < orders; ++k) t += from[k];
+    if constexpr (L == 0) {
+      for (int u = 0; u < units; ++u) t += sums[u * width + m];
+    } else {
+      const int l = m < nw ? m / a.C : 0, c = m - (m < nw ? l * a.C : nw);
+      const float* from = m < nw ? sums + c * KP + l * l : sums + KP * a.C + c;
+      const int orders = m < nw ? 2 * l + 1 : 1;
+      for (int u = 0; u < units; ++u, from += width)
+        for (int k = 0; k < orders; ++k) t += from[k];
+    }
     if (part)
       part[m] = t;
     else if (m < nw) {
@@ -1007,8 +1039,10 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
 // ---------------------------------------------------------------- launch
 // Lanes for a row of cols values in vectors of V, NV per lane, at least
 // min_lanes (a power of two), and the groups of a CTA: as many as fill it, or
-// fewer where the rows would leave some SMs without a CTA.
-inline RowShape row_shape(int cols, int K, int V, int NV, int min_lanes, int rows, int sms) {
+// fewer where the rows would leave some SMs without a CTA.  Not so if one CTA
+// is to do it all (`single` rounds of it at most): a backward pass of one CTA
+// needs no second launch for the weight sums, which costs more than the rounds.
+inline RowShape row_shape(int cols, int K, int V, int NV, int min_lanes, int rows, int sms, int single) {
   int period = 1;  // K / gcd(K, V)
   while (period * V % K) ++period;
   const int vectors = cols / V;
@@ -1022,6 +1056,7 @@ inline RowShape row_shape(int cols, int K, int V, int NV, int min_lanes, int row
   }
   sh.groups = sh.lanes < kRowThreads ? kRowThreads / sh.lanes : 1;
   sh.run = sh.apart = 0;
+  if (rows <= single * sh.groups) return sh;
   const int whole = sh.lanes < 32 ? 32 / sh.lanes : 1;  // groups of a warp
   while (sh.groups / 2 >= whole && (long long)sms * (sh.groups / 2) >= rows) sh.groups /= 2;
   return sh;
@@ -1046,6 +1081,7 @@ inline int resident_grid(Kernel kernel, int threads, size_t smem, const DeviceIn
   return (int)(tiles < cap ? tiles : cap);
 }
 
+constexpr int kSingle = 4;                 // rounds
 constexpr int kMaxRingBytes = 220 * 1024;  // of dynamic shared memory, a CTA
 constexpr long long kRunBytes = 128 * 1024;
 
@@ -1084,8 +1120,9 @@ static eqmp_status launch_mode(NormArgs a, RowShape sh, const DeviceInfo& dev, c
     const size_t smem = feed > sums ? feed : sums;
     int grid = resident_grid(kern, threads, smem, dev, tiles, cache);
     if (grid < 1) return EQMP_ERR_CUDA;
+    if (tiles <= kSingle && (!SHIFT || sh.groups % 8 == 0)) grid = 1;
     if (grid > kMaxParts) grid = kMaxParts;
-    if (SHIFT && grid < tiles) grid = grid / 8 * 8;  // a group's rows are a multiple of 8 apart
+    if (SHIFT && grid < tiles && grid > 1) grid = grid / 8 * 8;  // a group's rows are a multiple of 8 apart
     if (grid < 1) return EQMP_ERR_UNSUPPORTED;
     a.parts = grid;
     kern<<<grid, threads, smem, st>>>(a, sh);
@@ -1113,8 +1150,9 @@ static eqmp_status launch_rows_v(const NormArgs& a, int apart, const DeviceInfo&
   constexpr int K = (L + 1) * (L + 1), N8 = 8 / V, N16 = 16 / V;
   constexpr int least = pow2_above(BACKWARD ? L + 2 : L + 1);  // what GroupSum needs
   const int cols = SHIFT ? a.cols + 2 * (V - 1) : a.cols;      // a first and a last vector in part
-  RowShape s8 = row_shape(cols, K, V, N8, least, a.rows, dev.sms);
-  RowShape s16 = row_shape(cols, K, V, N16, least, a.rows, dev.sms);
+  const int single = BACKWARD ? kSingle : 0;
+  RowShape s8 = row_shape(cols, K, V, N8, least, a.rows, dev.sms, single);
+  RowShape s16 = row_shape(cols, K, V, N16, least, a.rows, dev.sms, single);
   s8.apart = s16.apart = apart;
   const bool few = (long long)a.rows * s8.lanes <= (long long)dev.sms * kMaxRowThreads;
   *done = s16.lanes <= kMaxRowThreads;
