@@ -661,6 +661,20 @@ __device__ __forceinline__ void load_weights(const S& at, const NormArgs& a, flo
       return;
     }
   }
+  if constexpr (L > 0 && V > 1 && S::K % V == 0) {  // a vector lies in one channel
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float t[S::GROUPS];
+#pragma unroll
+      for (int g = 0; g < S::GROUPS; ++g)
+        t[g] = at.has[j] && a.w ? a.w[at.cls[g] * a.C + (int)at.col[j] / S::K] : 1.0f;
+      float2 p[S::PAIRS];
+      S::spread(t, p);
+#pragma unroll
+      for (int k = 0; k < S::PAIRS; ++k) w[j * S::PAIRS + k] = p[k];
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
 #pragma unroll
@@ -1002,9 +1016,10 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         if (!at.valid(j, i)) continue;
-        const int e = j * V + i, col = (int)at.col[j] + i, c = col / S::K, k = col - c * S::K;
-        mine[c * KP + k] = e & 1 ? dw[e / 2].y : dw[e / 2].x;
-        if (EACH && k == 0) mine[KP * a.C + c] = e & 1 ? db[EACH ? e / 2 : 0].y : db[EACH ? e / 2 : 0].x;
+        const int e = j * V + i, col = (int)at.col[j] + i;
+        const int c = (S::K % V == 0 ? (int)at.col[j] : col) / S::K;  // its place: c KP + col - c K
+        mine[col + c * (KP - S::K)] = e & 1 ? dw[e / 2].y : dw[e / 2].x;
+        if (EACH && col == c * S::K) mine[KP * a.C + c] = e & 1 ? db[EACH ? e / 2 : 0].y : db[EACH ? e / 2 : 0].x;
       }
       if (!EACH) {
         const int c = ((int)at.col[j] + V - 1) / S::K;  // the channel that begins in the vector, if one does
@@ -1013,26 +1028,28 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
     }
   }
   __syncthreads();
-  const int M = (L + 2) * a.C, nw = (L + 1) * a.C;
-  float* part = a.parts > 1 ? a.part + (long long)blockIdx.x * M : nullptr;
-  for (int m = threadIdx.x; m < M; m += blockDim.x) {
-    float t = 0.0f;
-    if constexpr (L == 0) {
-      for (int u = 0; u < units; ++u) t += sums[u * width + m];
-    } else {
-      const int l = m < nw ? m / a.C : 0, c = m - (m < nw ? l * a.C : nw);
-      const float* from = m < nw ? sums + c * KP + l * l : sums + KP * a.C + c;
-      const int orders = m < nw ? 2 * l + 1 : 1;
-      for (int u = 0; u < units; ++u, from += width)
-        for (int k = 0; k < orders; ++k) t += from[k];
+  float* to_w = a.gw;
+  float* to_b = a.gb;
+  if (a.parts > 1) {
+    to_w = a.part + (long long)blockIdx.x * (L + 2) * a.C;
+    to_b = to_w + (L + 1) * a.C;
+  }
+  for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
+    float t[L + 2];
+#pragma unroll
+    for (int l = 0; l < L + 2; ++l) t[l] = 0.0f;
+    for (int u = 0; u < units; ++u) {
+      const float* from = sums + u * width;
+#pragma unroll
+      for (int l = 0; l <= L; ++l)
+#pragma unroll
+        for (int k = l * l; k < (l + 1) * (l + 1); ++k) t[l] += from[c * KP + k];
+      t[L + 1] += from[KP * a.C + c];
     }
-    if (part)
-      part[m] = t;
-    else if (m < nw) {
-      if (a.gw) a.gw[m] = t;
-    } else if (a.gb) {
-      a.gb[m - nw] = t;
-    }
+#pragma unroll
+    for (int l = 0; l <= L; ++l)
+      if (to_w) to_w[l * a.C + c] = t[l];
+    if (to_b) to_b[c] = t[L + 1];
   }
 }
 
