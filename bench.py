@@ -36,6 +36,7 @@ Multi-GPU: independent replicas (weak scaling), no collective on the data
 path; barrier + max over ranks for timing.
 """
 import argparse
+import gc
 import json
 import os
 import subprocess
@@ -706,6 +707,11 @@ def main():
             for i in range(2 * PIPE):
                 runs[i % PIPE]()
             torch.cuda.synchronize()
+            # a collection of the interpreter's garbage takes 150 us; whether one
+            # falls into this span of about 450 us hangs on how many objects the
+            # imports made, not on the steps
+            gc.collect()
+            gc.disable()
             barrier()
             t_beg, t_end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
             t_beg.record(streams[0])
@@ -724,6 +730,7 @@ def main():
             t_end.record(streams[0])
             torch.cuda.synchronize()
             barrier()
+            gc.enable()
             e2e_ms = max_over_ranks(t_beg.elapsed_time(t_end) / args.steps)
             e2e_mode = (f"pipelined: {PIPE} streams, one device block each, each step one CUDA graph launch "
                         "(eqmp_plan_staged), no L2 flush (inputs arrive by copy)")
