@@ -704,14 +704,14 @@ def main():
                                          w=di["w"], R=di["R"], M=di["M"]) for dp, di, o, ho in pipe_sets]
             runs = [lambda b=b: plans[b].launch(streams[b]) for b in range(PIPE)]
             host_bytes = [ps[3].view(torch.uint8).numpy().reshape(-1) for ps in pipe_sets]
-            for i in range(2 * PIPE):
-                runs[i % PIPE]()
-            torch.cuda.synchronize()
             # a collection of the interpreter's garbage takes 150 us; whether one
             # falls into this span of about 450 us hangs on how many objects the
             # imports made, not on the steps
             gc.collect()
             gc.disable()
+            for i in range(2 * PIPE):
+                runs[i % PIPE]()
+            torch.cuda.synchronize()
             barrier()
             t_beg, t_end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
             t_beg.record(streams[0])
