@@ -193,7 +193,9 @@ __device__ __forceinline__ void cta_sum(float (&v)[NV], float* red) {
   }
 }
 
-// Any shape, forward: one CTA per row, which reads the row three times.
+// Any shape, forward: one CTA per row, which reads the row three times.  Takes
+// the rows that are too wide for registers (over 8192 values): 1800 x 16384
+// fp32 147 us, 24 % of the measured copy rate, bound by its single values.
 template <typename T, int L>
 __global__ void __launch_bounds__(kWideThreads) k_norm_wide(NormArgs a) {
   constexpr int K = (L + 1) * (L + 1);

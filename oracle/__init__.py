@@ -16,6 +16,8 @@ Modules
          per-edge radial weights W = R.M) and the sum into receivers.
   backward  the chain rule of that layer: gradients of x, w (or R and M)
          and of the edge vectors through the harmonics.
+  norm   dropout from a counter-based generator, and the layer norm of rows and
+         by degree, with their gradients.
   graph  the radius graph (ordered pairs closer than the cutoff, CSR by
          receiver), with the cutoff decision taken in float32; open
          boundaries, or a periodic orthorhombic box (every image within
