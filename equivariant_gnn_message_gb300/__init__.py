@@ -671,6 +671,10 @@ def _main_input(x, name, degree, torch):
     return torch.cuda.current_device(), 0
 
 
+def _not_dropout(drop):
+    raise TypeError(f"drop must be a Dropout, not {type(drop).__name__}")
+
+
 def _raw_stream(stream, dev, torch):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
@@ -704,7 +708,7 @@ def _norm_forward(entry, degree, x, w, b, eps, residual, drop, need, out, stream
     if len(got) != len(need):
         _unknown(need, ("y", "s", "stats"))
     dt = EQMP_F32 if dtype is f32 else EQMP_BF16
-    dr = _NO_DROP if drop is None else drop
+    dr = _NO_DROP if drop is None else drop if isinstance(drop, Dropout) else _not_dropout(drop)
     lib, st = load_library(), _raw_stream(stream, dev, torch)
     if degree:
         status = lib.eqmp_degree_norm(xp, rp, dt, n, c, l_max, dr, wp, bp, eps, sp, yp, tp, st)
@@ -752,7 +756,7 @@ def _norm_backward(entry, degree, grad_y, s, stats, w, grad_s, drop, need, out, 
             nbytes = workspace.numel()
         ws = workspace.data_ptr()
     dt = EQMP_F32 if dtype is f32 else EQMP_BF16
-    dr = _NO_DROP if drop is None else drop
+    dr = _NO_DROP if drop is None else drop if isinstance(drop, Dropout) else _not_dropout(drop)
     if degree:
         status = lib.eqmp_degree_norm_backward(gp, xp, rp, dt, n, c, l_max, dr, wp, tp, grp, gxp, gwp, gbp, ws, nbytes, st)
     else:
@@ -785,8 +789,9 @@ def eqmp_dropout(x, drop, out=None, stream=None):
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=x.device)
     op = _packed(out, "out", dtype, shape, dev, torch)
+    dr = _NO_DROP if drop is None else drop if isinstance(drop, Dropout) else _not_dropout(drop)
     status = load_library().eqmp_dropout(xp, cols if out is x else ld, EQMP_F32 if dtype is torch.float32 else EQMP_BF16,
-                                         shape[0], cols, _NO_DROP if drop is None else drop, op,
+                                         shape[0], cols, dr, op,
                                          _raw_stream(stream, dev, torch))
     if status:
         raise EqmpError(status, "eqmp_dropout")

@@ -39,12 +39,15 @@ static bool overlap(const Plane& a, const Plane& b, long long rows, long long co
   return a0 < b1 && b0 < a1;
 }
 
+// A row stride of up to 2^31 elements, so that 2^30 rows stay in 64 bits.
+static bool stride_ok(long long ld) { return ld >= 0 && ld <= 1ll << 31; }
+
 // Inputs: aligned, strides that address forward.  Outputs (packed): aligned,
 // apart from the inputs and from one another.
 static bool planes_ok(const Plane* in, int n_in, void* const* outs, int n_out, long long rows, long long cols,
                       int bytes) {
   for (int i = 0; i < n_in; ++i)
-    if (in[i].p && (!aligned(in[i].p, bytes) || in[i].ld < 0)) return false;
+    if (in[i].p && (!aligned(in[i].p, bytes) || !stride_ok(in[i].ld))) return false;
   for (int o = 0; o < n_out; ++o) {
     if (!outs[o]) continue;
     if (!aligned(outs[o], bytes)) return false;
@@ -460,8 +463,8 @@ eqmp_status eqmp_dropout(const void* x, int64_t x_ld, eqmp_dtype dtype, int64_t 
   if (ds != EQMP_OK) return ds;
   if (rows == 0) return EQMP_OK;
   const int bytes = dtype == EQMP_BF16 ? 2 : 4;
-  if (!x || !out || x_ld < 0 || !aligned(x, bytes) || !aligned(out, bytes)) return EQMP_ERR_INVALID_ARG;
-  const bool in_place = x == out && x_ld == cols;  // each element is read before it is written, by one thread
+  if (!x || !out || !stride_ok(x_ld) || !aligned(x, bytes) || !aligned(out, bytes)) return EQMP_ERR_INVALID_ARG;
+  const bool in_place = x == out && (x_ld == cols || rows == 1);  // each element is read before it is written, by one thread
   if (!in_place && overlap(Plane{x, x_ld}, Plane{out, cols}, rows, cols, bytes)) return EQMP_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dtype == EQMP_BF16 ? run_dropout<__nv_bfloat16>(x, x_ld, out, (int)rows, (int)cols, d, st)

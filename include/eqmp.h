@@ -406,18 +406,21 @@ typedef struct {
  *     type for all of them); w, b, stats, grad_w and grad_b are fp32.
  *     Statistics and sums are fp32; a bf16 result is rounded once, on its
  *     store.
- *   - Inputs with a `_ld` argument are rows `_ld` elements apart (any value
- *     >= 0: cols for packed rows, more for a slice of a wider matrix, 0 for
- *     one row that stands for all).  Everything else is packed.  No alignment
+ *   - Inputs with a `_ld` argument are rows `_ld` elements apart (0 to 2^31:
+ *     cols for packed rows, more for a slice of a wider matrix, 0 for one row
+ *     that stands for all).  Everything else is packed.  No alignment
  *     beyond the element's own is needed; 16-byte aligned rows are faster.
  *   - Up to 2^30 rows of up to 2^30 values (EQMP_ERR_UNSUPPORTED above).
  *     rows == 0 launches no kernel; the sums over rows are then 0.
  *   - Outputs may be NULL to skip them, and must not overlap the inputs or
  *     one another (EQMP_ERR_INVALID_ARG), but for eqmp_dropout in place.
  *   - Results are bitwise reproducible on one device: every sum has a fixed
- *     order, and nothing is added by atomics.
- *   - A NaN or an infinity in a row makes that row's y NaN, as the formula
- *     does; other rows are not touched.
+ *     order, and nothing is added by atomics.  The order of a row's sums hangs
+ *     on the sizes, the alignment and, for rows that do not begin on 16 bytes,
+ *     on where the row lies, so calls of another form may differ in rounding.
+ *   - A NaN or an infinity in a row goes where the formula takes it (into the
+ *     whole y of the row, or of its degree, and into the weight gradients);
+ *     the other rows' results are not touched.
  */
 
 /*

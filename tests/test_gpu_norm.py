@@ -299,6 +299,12 @@ def test_broadcast_rows_and_no_rows(eq):
     x = torch.randn(1, 96, device="cuda")
     y = eq.eqmp_layer_norm(x.expand(30, 96))["y"]  # a row stride of 0
     assert torch.equal(y, eq.eqmp_layer_norm(x)["y"].expand(30, 96))
+    for dtype in (torch.float32, torch.bfloat16):  # a broadcast gradient, odd rows
+        x, g = torch.randn(301, 77, device="cuda").to(dtype), torch.randn(1, 77, device="cuda").to(dtype)
+        stats = eq.eqmp_layer_norm(x, need=("stats",))["stats"]
+        got = eq.eqmp_layer_norm_backward(g.expand(301, 77), x, stats, grad_s=g.expand(301, 77), need=("x", "w", "b"))
+        gg = host(g).repeat(301, 0)
+        _check(got, *nu.backward_bounds(gg, host(x), host(stats), None, gg, None, dtype is torch.bfloat16))
     for shape in ((0, 96), (0, 8, 16)):
         c = Case(shape)
         got = c.forward(eq)
@@ -435,5 +441,12 @@ def test_refusals(eq):
         eq.Dropout(0.5, 1, step=torch.zeros(1, device="cuda"))
     with pytest.raises(TypeError):
         eq.eqmp_dropout(x.double(), d)
+    with pytest.raises(TypeError):
+        eq.eqmp_dropout(x, 0.1)
+    with pytest.raises(TypeError):
+        eq.eqmp_layer_norm(x, drop=0.1)
+    row = torch.randn(1, 33, device="cuda")
+    want = eq.eqmp_dropout(row, d)
+    assert torch.equal(eq.eqmp_dropout(row.as_strided((1, 33), (40, 1)), d, out=row), want)  # one row, in place
     with pytest.raises(ValueError):
         eq.eqmp_dropout(x, d, out=f32(8, 4))

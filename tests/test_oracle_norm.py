@@ -120,7 +120,7 @@ def test_c_entries_refuse_bad_arguments_before_any_launch():
         return d
 
     assert forward(rows=0) == eq.EQMP_OK and forward(y=None) == eq.EQMP_OK
-    for kw in (dict(x=None), dict(ld=-1), dict(dtype=2), dict(rows=-1), dict(cols=0), dict(eps=-1.0), dict(eps=float("nan")),
+    for kw in (dict(x=None), dict(ld=-1), dict(ld=(1 << 31) + 1), dict(dtype=2), dict(rows=-1), dict(cols=0), dict(eps=-1.0), dict(eps=float("nan")),
                dict(eps=float("inf")), dict(x=ctypes.c_void_p((1 << 20) + 2)), dict(y=at(0)), dict(s=at(1)),
                dict(w=ctypes.c_void_p(6)), dict(y=ctypes.c_void_p((1 << 20) + 4)), dict(drop=drop(-0.5)),
                dict(drop=drop(float("nan"))), dict(drop=drop(1.5)), dict(drop=drop(0.5, 3))):
