@@ -1181,20 +1181,37 @@ static eqmp_status launch_rows(const NormArgs& a, const RowShape& sh, const Devi
 
 // 16 values a lane share the sums' shuffles and barriers over more values; 8
 // leave more lanes to work on a row, which is faster where the rows are few,
-// and fit the registers of the lanes that handle single values.
+// and fit the registers of the lanes that handle single values and of the
+// backward pass of rows that begin anywhere.  The forward layer norm also
+// takes 12 (fp32) or 24 where those leave fewer places of a group empty (24 at
+// 768 columns: one warp, every lane full, for two of which a quarter idles).
 template <typename T, int L, int V, int SHIFT, bool BACKWARD>
 static eqmp_status launch_rows_v(const NormArgs& a, int apart, const DeviceInfo& dev, cudaStream_t st, bool* done) {
   constexpr int K = (L + 1) * (L + 1), N8 = 8 / V, N16 = 16 / V;
   constexpr int least = pow2_above(BACKWARD ? L + 2 : L + 1);  // what GroupSum needs
   const int cols = SHIFT ? a.cols + 2 * (V - 1) : a.cols;      // a first and a last vector in part
   const int single = BACKWARD ? kSingle : 0;
-  RowShape s8 = row_shape(cols, K, V, N8, least, a.rows, dev.sms, single);
-  RowShape s16 = row_shape(cols, K, V, N16, least, a.rows, dev.sms, single);
-  s8.apart = s16.apart = apart;
+  auto shape = [&](int NV) {
+    RowShape sh = row_shape(cols, K, V, NV, least, a.rows, dev.sms, single);
+    sh.apart = apart;
+    return sh;
+  };
+  const RowShape s8 = shape(N8), s16 = shape(N16);
   const bool few = (long long)a.rows * s8.lanes <= (long long)dev.sms * kMaxRowThreads;
   *done = s16.lanes <= kMaxRowThreads;
   if (!*done) return EQMP_OK;
-  if (s8.lanes <= kMaxRowThreads && (V == 1 || few || (SHIFT != kOn16 && BACKWARD))) return launch_rows<T, L, V, N8, SHIFT, BACKWARD>(a, s8, dev, st);
+  if (s8.lanes <= kMaxRowThreads && (V == 1 || few || (SHIFT != kOn16 && BACKWARD)))
+    return launch_rows<T, L, V, N8, SHIFT, BACKWARD>(a, s8, dev, st);
+  if constexpr (L == 0 && V > 1 && !BACKWARD) {
+    const RowShape s24 = shape(24 / V);
+    const int places = s16.lanes * 16;
+    if constexpr (V == 4) {
+      const RowShape s12 = shape(3);
+      if (s12.lanes * 12 < places && s12.lanes * 12 <= s24.lanes * 24)
+        return launch_rows<T, L, V, 3, SHIFT, BACKWARD>(a, s12, dev, st);
+    }
+    if (s24.lanes * 24 < places) return launch_rows<T, L, V, 24 / V, SHIFT, BACKWARD>(a, s24, dev, st);
+  }
   return launch_rows<T, L, V, N16, SHIFT, BACKWARD>(a, s16, dev, st);
 }
 
