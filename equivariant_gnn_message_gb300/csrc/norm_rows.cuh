@@ -740,11 +740,26 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
   GroupSum<NS> sum2(sh.lanes, red2);
   const Dropper drop(a.drop);
   Keeps<S, V, NV, MODE == kDirect> keeps(drop, at, sh, a.cols, bits);
-  float2 w[P], b[EACH ? P : NV];
+  // 32 values a lane: w and b wait in shared memory, one copy for all groups
+  // (each of one warp, all with the same columns)
+  constexpr bool SHARED = NV * V == 32;
+  constexpr int PR = SHARED ? 2 : P;  // pairs in registers
+  float4* shared_wb = reinterpret_cast<float4*>(ring + blockDim.x * F::BYTES);
+  float2 w[PR], b[EACH ? PR : NV];
   bool all = true;  // whether the lane's values are all of the row
-  load_weights<L, V, NV, S>(at, a, w);
-  bool biased = false;
-  if constexpr (L == 0 && V > 1 && SHIFT == kOn16) {
+  if constexpr (SHARED) {
+    for (int i = threadIdx.x; i < 32 * NV * V; i += blockDim.x) {
+      const int lane = i / 4 % 32, v4 = i / 128, col = (lane + v4 / (V / 4) * sh.active) * V + v4 % (V / 4) * 4 + i % 4;
+      const bool in = lane < sh.active && col < a.cols;
+      reinterpret_cast<float*>(shared_wb)[i] = in && a.w ? a.w[col] : 1.0f;
+      reinterpret_cast<float*>(shared_wb + 32 * NV * V / 4)[i] = in && a.b ? a.b[col] : 0.0f;
+    }
+    __syncthreads();
+  } else {
+    load_weights<L, V, NV, S>(at, a, w);
+  }
+  bool biased = SHARED;
+  if constexpr (L == 0 && V > 1 && SHIFT == kOn16 && !SHARED) {
     biased = a.b && reinterpret_cast<uintptr_t>(a.b) % 16 == 0;
     if (biased) load_columns<V, NV>(at, a.b, 0.0f, b);
   }
@@ -756,7 +771,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int e = j * V + i, c = ((int)at.col[j] + i) / S::K;
-        (e & 1 ? b[e / 2].y : b[e / 2].x) = at.valid(j, i) && a.b && at.cls[0] == 0 ? a.b[c] : 0.0f;
+        (e & 1 ? b[e / 2 % PR].y : b[e / 2 % PR].x) = at.valid(j, i) && a.b && at.cls[0] == 0 ? a.b[c] : 0.0f;
       }
     } else {
       const int c = ((int)at.col[j] + V - 1) / S::K;  // the channel that begins in the vector, if one does
@@ -839,12 +854,21 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const float2 h = __fmul2_rn(v[p], qs[p % PV]);
+      if constexpr (SHARED) {
+        if (p % 2 == 0) {
+          const float4 wv = shared_wb[p / 2 * 32 + at.lane], bv = shared_wb[32 * NV * V / 4 + p / 2 * 32 + at.lane];
+          w[0] = make_float2(wv.x, wv.y);
+          w[1] = make_float2(wv.z, wv.w);
+          b[0] = make_float2(bv.x, bv.y);
+          b[1] = make_float2(bv.z, bv.w);
+        }
+      }
       if (EACH)
-        v[p] = __ffma2_rn(h, w[p], b[EACH ? p : 0]);
+        v[p] = __ffma2_rn(h, w[p % PR], b[EACH ? p % PR : 0]);
       else if (S::may0(p % PV))
-        v[p] = __ffma2_rn(h, w[p], __fmul2_rn(b[EACH ? 0 : p / PV], at.first[p % PV]));
+        v[p] = __ffma2_rn(h, w[p % PR], __fmul2_rn(b[EACH ? 0 : p / PV], at.first[p % PV]));
       else
-        v[p] = __fmul2_rn(h, w[p]);
+        v[p] = __fmul2_rn(h, w[p % PR]);
     }
     put_pairs<T, V, NV>(static_cast<T*>(a.y) + out, at, v);
   }
@@ -1130,7 +1154,7 @@ static eqmp_status launch_mode(NormArgs a, RowShape sh, const DeviceInfo& dev, c
   const long long tiles = ((long long)a.rows + sh.groups - 1) / sh.groups;
   if constexpr (!BACKWARD) {
     auto kern = k_norm_rows<T, L, V, NV, SHIFT, MODE>;
-    const size_t smem = (size_t)threads * Feed<T, V, NV, MODE ? 2 : 1, 0>::BYTES;
+    const size_t smem = (size_t)threads * Feed<T, V, NV, MODE ? 2 : 1, 0>::BYTES + (NV * V == 32 ? 2 * 32 * 32 * 4 : 0);
     if (ensure_smem_attr(kern, kMaxRingBytes, &attr_done) != cudaSuccess) return EQMP_ERR_CUDA;
     int grid = resident_grid(kern, threads, smem, dev, tiles, cache);
     if (grid < 1) return EQMP_ERR_CUDA;
@@ -1184,7 +1208,10 @@ static eqmp_status launch_rows(const NormArgs& a, const RowShape& sh, const Devi
 // and fit the registers of the lanes that handle single values and of the
 // backward pass of rows that begin anywhere.  The forward layer norm also
 // takes 12 (fp32) or 24 where those leave fewer places of a group empty (24 at
-// 768 columns: one warp, every lane full, for two of which a quarter idles).
+// 768 columns: one warp, every lane full, for two of which a quarter idles) or
+// as many and fewer warps (1536 columns: 24.0 us for 20,000 bf16 rows, 29.7
+// with 16),
+// and bf16 32 where one warp then does for two (769 to 1024 columns).
 template <typename T, int L, int V, int SHIFT, bool BACKWARD>
 static eqmp_status launch_rows_v(const NormArgs& a, int apart, const DeviceInfo& dev, cudaStream_t st, bool* done) {
   constexpr int K = (L + 1) * (L + 1), N8 = 8 / V, N16 = 16 / V;
@@ -1204,13 +1231,18 @@ static eqmp_status launch_rows_v(const NormArgs& a, int apart, const DeviceInfo&
     return launch_rows<T, L, V, N8, SHIFT, BACKWARD>(a, s8, dev, st);
   if constexpr (L == 0 && V > 1 && !BACKWARD) {
     const RowShape s24 = shape(24 / V);
+    if constexpr (V == 8 && SHIFT == kOn16) {
+      const RowShape s32 = shape(4);
+      if (s32.lanes == 32 && s24.lanes > 32) return launch_rows<T, L, V, 4, SHIFT, BACKWARD>(a, s32, dev, st);
+    }
     const int places = s16.lanes * 16;
     if constexpr (V == 4) {
       const RowShape s12 = shape(3);
       if (s12.lanes * 12 < places && s12.lanes * 12 <= s24.lanes * 24)
         return launch_rows<T, L, V, 3, SHIFT, BACKWARD>(a, s12, dev, st);
     }
-    if (s24.lanes * 24 < places) return launch_rows<T, L, V, 24 / V, SHIFT, BACKWARD>(a, s24, dev, st);
+    if (s24.lanes * 24 < places || (s24.lanes * 24 == places && s16.lanes > 32))
+      return launch_rows<T, L, V, 24 / V, SHIFT, BACKWARD>(a, s24, dev, st);
   }
   return launch_rows<T, L, V, N16, SHIFT, BACKWARD>(a, s16, dev, st);
 }
