@@ -875,6 +875,10 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
 }
 
 // ---------------------------------------------------------------- backward
+// Words of a row's statistics that a lane copies.  A group has at least 8
+// lanes where L > 0, and the L + 2 <= 8 words go to the first of each warp.
+constexpr int stat_words(int L) { return L == 0 ? 2 : 1; }
+
 // One pass over g and s (and dL/ds): the row's sums of a and a h, then dL/ds
 // and dL/dx from the registers, while each lane adds g h and g of its columns
 // over all the rows of its group.  At the end the groups of a CTA are added in
@@ -891,7 +895,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
 template <typename T, int L, int V, int NV, int SHIFT, int MODE>
 __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, RowShape sh) {
   using S = Slots<L, V, NV, SHIFT>;
-  using F = Feed<T, V, NV, MODE ? 3 : 2, 1 + S::GROUPS>;
+  using F = Feed<T, V, NV, MODE ? 3 : 2, stat_words(L)>;
   constexpr int P = NV * V / 2, PV = S::PAIRS, NS = L + 2;
   constexpr bool EACH = L == 0 || V == 1;  // db per value; else per vector, which has at most one degree 0
   __shared__ __align__(16) float red[GroupSum<NS>::kRed];
@@ -914,9 +918,12 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
       load_vector(feed, 1, j, g, at, live, sh.apart & kApartG);
       if (MODE && a.r) load_vector(feed, 2, j, r, at, live, sh.apart & kApartR);
     }
-    feed.load_word(0, st, live);
-#pragma unroll
-    for (int k = 0; k < S::GROUPS; ++k) feed.load_word(1 + k, st + 1 + at.cls[k], live);
+    if constexpr (L == 0) {
+      feed.load_word(0, st, live);
+      feed.load_word(1, st + 1, live);
+    } else {  // one word a lane, passed on by shuffles
+      feed.load_word(0, st + min((int)(threadIdx.x & 7), L + 1), live);
+    }
     feed.loaded();
     ahead += stride;
     x += stride * a.x_ld;
@@ -939,6 +946,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
   float scale[S::GROUPS];
 #pragma unroll
   for (int k = 0; k < S::GROUPS; ++k) scale[k] = -inv / (float)(2 * at.cls[k] + 1);
+  const int first_lane = sh.lanes < 32 ? (int)(threadIdx.x & 31) / sh.lanes * sh.lanes : 0;  // of the group, in the warp
   for (int base = blockIdx.x * sh.groups; base < a.rows; base += stride, row += stride) {
     const bool live = row < a.rows;
     float2 h[P], av[P], cr[MODE ? P : 1], qs[PV];
@@ -951,9 +959,16 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
     if constexpr (MODE != kPlain && !F::RING) {
       if (a.r) feed.get(place, 2, cr);
     }
-    const float2 mu = both(-feed.get_word(place, 0));
+    float2 mu;
+    if constexpr (L == 0) {
+      mu = both(-feed.get_word(place, 0));
+      q[0] = feed.get_word(place, 1);
+    } else {
+      const float word = feed.get_word(place, 0);
+      mu = both(-__shfl_sync(0xffffffffu, word, first_lane));
 #pragma unroll
-    for (int k = 0; k < S::GROUPS; ++k) q[k] = feed.get_word(place, 1 + k);
+      for (int k = 0; k < S::GROUPS; ++k) q[k] = __shfl_sync(0xffffffffu, word, first_lane + 1 + at.cls[k]);
+    }
     load_row();
     if (MODE == kMixed && drop.on) keeps.form_now(drop, sh, row, stride);
     S::spread(q, qs);
@@ -1175,7 +1190,7 @@ static eqmp_status launch_mode(NormArgs a, RowShape sh, const DeviceInfo& dev, c
   } else {
     auto kern = k_norm_bwd_rows<T, L, V, NV, SHIFT, MODE>;
     if (ensure_smem_attr(kern, kMaxRingBytes, &attr_done) != cudaSuccess) return EQMP_ERR_CUDA;
-    const size_t feed = (size_t)threads * Feed<T, V, NV, MODE ? 3 : 2, 1 + Slots<L, V, NV, SHIFT>::GROUPS>::BYTES;
+    const size_t feed = (size_t)threads * Feed<T, V, NV, MODE ? 3 : 2, stat_words(L)>::BYTES;
     constexpr int KP = ((L + 1) * (L + 1)) | 1;  // the CTA's column sums, one row for each warp or group
     const size_t sums = sizeof(float) * (size_t)(KP + 1) * a.C * (!SHIFT && sh.lanes <= 32 ? threads / 32 : sh.groups);
     const size_t smem = feed > sums ? feed : sums;
