@@ -607,6 +607,7 @@ def eqmp_fused_backward_noalloc(vec, x, row_offsets, src, dst, send_offsets, sen
 
 
 # ------------------------------------------------------------------ norms and dropout
+_OUT_NAMES = {k: f"out[{k!r}]" for k in ("y", "s", "stats", "x", "r", "w", "b")}
 _L_MAX = {16: 3, 25: 4, 36: 5, 49: 6}  # components of a channel -> degree
 
 
@@ -645,11 +646,10 @@ def _rows(t, name, dtype, shape, dev, torch):
 
 def _result(out, k, like, dtype, shape, dev, torch):
     """The result tensor k: the caller's own from `out`, or a new one on the device of `like`."""
-    t = out.get(k) if out else None
-    if t is None:
+    if out is None or (t := out.get(k)) is None:
         t = torch.empty(shape, dtype=dtype, device=like.device)
         return t, t.data_ptr()
-    return t, _packed(t, f"out[{k!r}]", dtype, shape, dev, torch)
+    return t, _packed(t, _OUT_NAMES[k], dtype, shape, dev, torch)
 
 
 def _main_input(x, name, degree, torch):
