@@ -22,7 +22,7 @@
 // 43 lane instructions at full issue, and about half of that keeps pace.  Hence
 // the arithmetic is on pairs (fma.rn.f32x2), sums of several values are
 // scattered over the lanes as they are formed, rows to come are copied
-// asynchronously, and a lane holds 16 values where it can, so that what is done
+// asynchronously, and a lane holds 16 values or more where it can, so that what is done
 // once a row is shared by more of them.  Tried and not kept: two or four rows
 // of a group at once in registers (10,000 x 128 x 16 bf16 backward 71 us against
 // 55 then: spills), weights in shared memory instead of registers (49 against
@@ -700,10 +700,10 @@ __device__ __forceinline__ void load_weights(const S& at, const NormArgs& a, flo
 // One pass: each value is loaded once, kept in registers through the mean and
 // the centred squares (two sums, so that a large mean costs no digits), and
 // stored once.  GPU time on one GB300, share of the measured copy rate:
-//   1,909,372 x 64 bf16                          77.4 us  96 %   (bound by HBM)
+//   1,909,372 x 64 bf16                          77.2 us  96 %   (bound by HBM)
 //   100,000 x 64 x 16 fp32, residual, dropout     237 us 102 %   (bound by HBM)
-//   10,000 x 1024 bf16, residual, dropout        17.5 us  69 %   (instructions: the generator's, the conversions')
-//   16,516 x 131 fp32 out of rows of 189          8.4 us  31 %   (instructions; half of the lanes' places are used)
+//   10,000 x 1024 bf16, residual, dropout        16.9 us  72 %   (instructions: the generator's, the conversions')
+//   16,516 x 131 fp32 out of rows of 189          7.1 us  36 %   (instructions: x is copied value by value)
 template <typename T, int L, int V, int NV, int SHIFT, int MODE>
 __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowShape sh) {
   using S = Slots<L, V, NV, SHIFT>;
@@ -888,9 +888,9 @@ constexpr int stat_words(int L) { return L == 0 ? 2 : 1; }
 // were this tail before it had one barrier and one load latency; about 3 now).
 // CTAs are persistent: with many short ones the tails cost more than the order
 // of DRAM gains (45 against 60 us and more at 10,000 x 128 x 16).
-//   477,664 x 128 bf16                            58.9 us  93 %   (HBM, then the tail)
-//   20,000 x 32 x 49 fp32                         64.8 us  86 %   (HBM, barriers of a row's warps)
-//   10,000 x 128 x 16 bf16, residual, dropout     39.0 us  78 %   (instructions)
+//   477,664 x 128 bf16                            59.1 us  93 %   (HBM, then the tail)
+//   20,000 x 32 x 49 fp32                         61.8 us  90 %   (HBM, barriers of a row's warps)
+//   10,000 x 128 x 16 bf16, residual, dropout     35.7 us  85 %   (instructions)
 //   16,516 x 509 fp32, residual, dropout          32.3 us  77 %   (instructions: partial vectors, keep bits)
 template <typename T, int L, int V, int NV, int SHIFT, int MODE>
 __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, RowShape sh) {
