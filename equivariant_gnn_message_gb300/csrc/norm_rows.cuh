@@ -1253,7 +1253,7 @@ static eqmp_status launch_rows_v(const NormArgs& a, int apart, const DeviceInfo&
     const int places = s16.lanes * 16;
     if constexpr (V == 4) {
       const RowShape s12 = shape(3);
-      if (s12.lanes * 12 < places && s12.lanes * 12 <= s24.lanes * 24)
+      if (s12.lanes <= kMaxRowThreads && s12.lanes * 12 < places && s12.lanes * 12 <= s24.lanes * 24)
         return launch_rows<T, L, V, 3, SHIFT, BACKWARD>(a, s12, dev, st);
     }
     if (s24.lanes * 24 < places || (s24.lanes * 24 == places && s16.lanes > 32))

@@ -128,6 +128,16 @@ def test_layer_norm_parity(eq, rows, cols, form):
     _check(back, *c.backward_bounds(got["s"], got["stats"]))
 
 
+@pytest.mark.parametrize("form", [dict(), dict(residual=True, p=0.2), dict(bf16=True, residual=True, p=0.2)], ids=_id)
+@pytest.mark.parametrize("cols", [6148, 6852, 8064, 48, 96, 768, 900, 1024, 1536, 6147])
+def test_widths_between_lane_counts(eq, cols, form):
+    """Widths at which the number of values a lane holds changes, up to the most lanes that a row may have."""
+    c = Case((301, cols), **form)
+    got = c.forward(eq)
+    _check(got, *c.forward_bounds())
+    _check(c.backward(eq, got["s"], got["stats"]), *c.backward_bounds(got["s"], got["stats"]))
+
+
 FEATURES = [(1, 1, 16), (7, 3, 16), (100, 8, 16), (33, 32, 16), (9, 128, 16), (3, 300, 16), (64, 5, 25), (17, 32, 25),
             (5, 64, 36), (31, 7, 36), (20, 32, 49), (3, 129, 49), (2, 400, 49), (700, 4, 16), (2, 1100, 16)]
 
