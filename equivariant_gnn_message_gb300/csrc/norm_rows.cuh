@@ -872,6 +872,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
     }
     put_pairs<T, V, NV>(static_cast<T*>(a.y) + out, at, v);
   }
+  feed.drain();  // the zeros of the rows behind the last one
 }
 
 // ---------------------------------------------------------------- backward
@@ -1041,8 +1042,8 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
   }
   // the sums' kernel may be launched; it waits until this one is done
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  feed.drain();  // the zeros of the rows behind the last one; the ring's memory takes the column sums
   if (!a.gw && !a.gb) return;
-  feed.drain();  // the ring's memory takes the column sums
   __syncthreads();
   // The CTA's sums.  The groups of a warp are added by shuffles (SHIFT: their
   // lanes have different columns); then each warp (or group) puts its columns
