@@ -200,6 +200,24 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream, temporary=False):
+    """Memory for kernels on `stream` (None: the current one).
+
+    The allocator hands freed memory out again in the order of the stream that it was allocated on, so it is allocated
+    on the stream of the kernels; a result is recorded on the current stream as well, where the caller will use it."""
+    import torch
+
+    if stream is None or stream.cuda_stream == (current := torch.cuda.current_stream()).cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if not temporary:
+        t.record_stream(current)
+    return t
+
+
 def _require(t, name, dtype=None, cuda=True):
     import torch
 
@@ -644,10 +662,13 @@ def _rows(t, name, dtype, shape, dev, torch):
     raise ValueError(f"{name} must have contiguous rows" if len(shape) == 2 else f"{name} must be contiguous")
 
 
-def _result(out, k, like, dtype, shape, dev, torch):
+def _result(out, k, like, dtype, shape, dev, torch, stream):
     """The result tensor k: the caller's own from `out`, or a new one on the device of `like`."""
     if out is None or (t := out.get(k)) is None:
-        t = torch.empty(shape, dtype=dtype, device=like.device)
+        if stream is None:
+            t = torch.empty(shape, dtype=dtype, device=like.device)
+        else:
+            t = _empty(shape, dtype, like.device, stream)
         return t, t.data_ptr()
     return t, _packed(t, _OUT_NAMES[k], dtype, shape, dev, torch)
 
@@ -700,11 +721,11 @@ def _norm_forward(entry, degree, x, w, b, eps, residual, drop, need, out, stream
         need = ("y",) if residual is None else ("y", "s")
     got, sp, yp, tp = {}, None, None, None
     if "y" in need:
-        got["y"], yp = _result(out, "y", x, dtype, shape, dev, torch)
+        got["y"], yp = _result(out, "y", x, dtype, shape, dev, torch, stream)
     if "s" in need:
-        got["s"], sp = _result(out, "s", x, dtype, shape, dev, torch)
+        got["s"], sp = _result(out, "s", x, dtype, shape, dev, torch, stream)
     if "stats" in need:
-        got["stats"], tp = _result(out, "stats", x, f32, (n, l_max + 2), dev, torch)
+        got["stats"], tp = _result(out, "stats", x, f32, (n, l_max + 2), dev, torch, stream)
     if len(got) != len(need):
         _unknown(need, ("y", "s", "stats"))
     dt = EQMP_F32 if dtype is f32 else EQMP_BF16
@@ -734,13 +755,13 @@ def _norm_backward(entry, degree, grad_y, s, stats, w, grad_s, drop, need, out, 
     tp = _packed(stats, "stats", f32, (n, l_max + 2), dev, torch)
     got, grp, gxp, gwp, gbp, ws, nbytes = {}, None, None, None, None, None, 0
     if "x" in need:
-        got["x"], gxp = _result(out, "x", s, dtype, shape, dev, torch)
+        got["x"], gxp = _result(out, "x", s, dtype, shape, dev, torch, stream)
     if "r" in need:
-        got["r"], grp = _result(out, "r", s, dtype, shape, dev, torch)
+        got["r"], grp = _result(out, "r", s, dtype, shape, dev, torch, stream)
     if "w" in need:
-        got["w"], gwp = _result(out, "w", s, f32, w_shape, dev, torch)
+        got["w"], gwp = _result(out, "w", s, f32, w_shape, dev, torch, stream)
     if "b" in need:
-        got["b"], gbp = _result(out, "b", s, f32, (c,), dev, torch)
+        got["b"], gbp = _result(out, "b", s, f32, (c,), dev, torch, stream)
     if len(got) != len(need):
         _unknown(need, ("x", "r", "w", "b"))
     lib, st = load_library(), _raw_stream(stream, dev, torch)
@@ -750,7 +771,7 @@ def _norm_backward(entry, degree, grad_y, s, stats, w, grad_s, drop, need, out, 
                       lib.eqmp_layer_norm_backward_workspace_size(n, c))
             if nbytes < 0:
                 raise EqmpError(EQMP_ERR_UNSUPPORTED, entry)
-            workspace = torch.empty(nbytes // 4 + 4, dtype=f32, device=s.device)
+            workspace = _empty(nbytes // 4 + 4, f32, s.device, stream, temporary=True)
         else:
             _require(workspace, "workspace", torch.uint8)
             nbytes = workspace.numel()
@@ -787,7 +808,7 @@ def eqmp_dropout(x, drop, out=None, stream=None):
     dev = torch.cuda.current_device()
     xp, ld = _rows(x, "x", dtype, shape, dev, torch)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=x.device)
+        out = _empty(shape, dtype, x.device, stream)
     op = _packed(out, "out", dtype, shape, dev, torch)
     dr = _NO_DROP if drop is None else drop if isinstance(drop, Dropout) else _not_dropout(drop)
     status = load_library().eqmp_dropout(xp, cols if out is x else ld, EQMP_F32 if dtype is torch.float32 else EQMP_BF16,

@@ -1,0 +1,40 @@
+"""Calls on a stream that is not the current one (GPU)."""
+import pytest
+
+from tests.test_gpu_norm import Case, eq  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+SLEEP = 20_000_000  # clocks, about 10 ms: the calls below are made before the first kernel runs
+
+
+def _busy_sides(n):
+    import torch
+
+    sides = [torch.cuda.Stream() for _ in range(n)]
+    for s in sides:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(SLEEP)
+    return sides
+
+
+@pytest.mark.parametrize("shape", [(5000, 96), (70, 9000), (700, 16, 25)], ids=str)
+def test_norm_temporaries_outlive_the_call(eq, shape):  # noqa: F811
+    """Backward calls wait on two side streams while the current stream takes and overwrites memory of the sizes of their
+    workspaces and results: the gradients are those of the lone call, to the bit."""
+    import torch
+
+    cases = [Case(shape, residual=True, p=0.2, seed=k) for k in (0, 1)]
+    saved = [c.forward(eq) for c in cases]
+    want = [c.backward(eq, a["s"], a["stats"]) for c, a in zip(cases, saved)]
+    torch.cuda.synchronize()
+    got = [c.backward(eq, a["s"], a["stats"], stream=s) for c, a, s in zip(cases, saved, _busy_sides(2))]
+    size = getattr(eq, "eqmp_degree_norm_backward_workspace_size" if len(shape) == 3 else
+                   "eqmp_layer_norm_backward_workspace_size")(*(shape[:2] + (4,) * (len(shape) == 3)))
+    taken = [torch.full((n,), float("nan"), device="cuda")
+             for n in [size // 4 + 4, size // 4] * 4 + [v.numel() for v in want[0].values()] * 4]
+    torch.cuda.synchronize()
+    assert all(torch.isnan(t).all() for t in taken)
+    for g, w in zip(got, want):
+        assert all(torch.equal(g[k], w[k]) for k in w)
