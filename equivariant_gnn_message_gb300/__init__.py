@@ -200,19 +200,20 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _empty(shape, dtype, device, stream, temporary=False):
-    """Memory for kernels on `stream` (None: the current one).
+def _empty(shape, dtype, device, stream, temporary=False, zero=False):
+    """Memory for kernels on `stream` (None: the current one), filled with zeros there if asked for.
 
     The allocator hands freed memory out again in the order of the stream that it was allocated on, so it is allocated
     on the stream of the kernels; a result is recorded on the current stream as well, where the caller will use it."""
     import torch
 
+    make = torch.zeros if zero else torch.empty
     if stream is None or stream.cuda_stream == (current := torch.cuda.current_stream()).cuda_stream:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream.cuda_stream)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = make(shape, dtype=dtype, device=device)
     if not temporary:
         t.record_stream(current)
     return t
@@ -257,7 +258,7 @@ def eqmp_sh(vec, Y=None, stream=None):
     if vec.dim() != 2 or vec.shape[1] != 3:
         raise ValueError("vec must be [E, 3]")
     if Y is None:
-        Y = torch.empty((E, 16), dtype=torch.float32, device=vec.device)
+        Y = _empty((E, 16), torch.float32, vec.device, stream)
     _require(Y, "Y", torch.float32)
     if tuple(Y.shape) != (E, 16):
         raise ValueError("Y must be [E, 16]")
@@ -279,7 +280,7 @@ def _layer(fn_name, edge_in, x, row_offsets, src, w, R, M, out, stream, n_edges)
     N = row_offsets.shape[0] - 1
     E = n_edges if n_edges is not None else edge_in.shape[0]
     if out is None:
-        out = torch.empty((N, C, 16), dtype=x.dtype, device=x.device)
+        out = _empty((N, C, 16), x.dtype, x.device, stream)
     _require(out, "out", x.dtype)
     if tuple(out.shape) != (N, C, 16):
         raise ValueError("out must be [N, C, 16]")
@@ -473,7 +474,7 @@ def eqmp_fused_lmax(l_max, vec, x, row_offsets, src, w=None, R=None, M=None, out
     n_src, C = x.shape[0], x.shape[1]
     N = row_offsets.shape[0] - 1
     if out is None:
-        out = torch.empty((N, C, nc), dtype=torch.float32, device=x.device)
+        out = _empty((N, C, nc), torch.float32, x.device, stream)
     _require(out, "out", torch.float32)
     if tuple(out.shape) != (N, C, nc):
         raise ValueError(f"out must be [N, C, {nc}]")
@@ -557,7 +558,7 @@ def sender_view(src, n_src):
     return offs, order
 
 
-def _backward_prepare(vec, x, row_offsets, src, dst, send_offsets, send_edges, grad_out, w, R, M, need):
+def _backward_prepare(vec, x, row_offsets, src, dst, send_offsets, send_edges, grad_out, w, R, M, need, stream):
     """Checks of the backward's inputs and its requested output tensors."""
     import torch
 
@@ -579,16 +580,16 @@ def _backward_prepare(vec, x, row_offsets, src, dst, send_offsets, send_edges, g
     dev = x.device
     out = {}
     if "x" in need:
-        out["x"] = torch.empty((n_src, C, 16), dtype=torch.float32, device=dev)
+        out["x"] = _empty((n_src, C, 16), torch.float32, dev, stream)
     if "vec" in need:
-        out["vec"] = torch.zeros((E, 3), dtype=torch.float32, device=dev)
+        out["vec"] = _empty((E, 3), torch.float32, dev, stream, zero=True)
     if radial:
         if "R" in need:
-            out["R"] = torch.zeros((E, 8), dtype=torch.float32, device=dev)
+            out["R"] = _empty((E, 8), torch.float32, dev, stream, zero=True)
         if "M" in need:
-            out["M"] = torch.empty((8, 34 * C), dtype=torch.float32, device=dev)
+            out["M"] = _empty((8, 34 * C), torch.float32, dev, stream)
     elif "w" in need:
-        out["w"] = torch.empty((34, C), dtype=torch.float32, device=dev)
+        out["w"] = _empty((34, C), torch.float32, dev, stream)
     wt = (Weights(ctypes.c_void_p(w.data_ptr()), None, None, 0) if not radial else
           Weights(None, ctypes.c_void_p(R.data_ptr()), ctypes.c_void_p(M.data_ptr()), R.shape[1]))
     head = (_ptr(vec), _ptr(x), n_src, _ptr(row_offsets), _ptr(src), _ptr(dst), _ptr(send_offsets),
@@ -603,12 +604,12 @@ def eqmp_fused_backward(vec, x, row_offsets, src, dst, send_offsets, send_edges,
     import torch
 
     out, head, (N, E, C, radial) = _backward_prepare(vec, x, row_offsets, src, dst, send_offsets,
-                                                     send_edges, grad_out, w, R, M, need)
+                                                     send_edges, grad_out, w, R, M, need, stream)
     lib = load_library()
     nbytes = int(lib.eqmp_fused_backward_workspace_size(N, E, C, 1 if radial else 0))
     if nbytes < 0:
         raise EqmpError(EQMP_ERR_CUDA, "eqmp_fused_backward_workspace_size")
-    ws = torch.empty(max(nbytes // 4, 4), dtype=torch.float32, device=x.device)
+    ws = _empty(max(nbytes // 4, 4), torch.float32, x.device, stream, temporary=True)
     _check(lib.eqmp_fused_backward(*head, _ptr(ws), ws.numel() * 4, _stream(stream)), "eqmp_fused_backward")
     return out
 
@@ -619,7 +620,7 @@ def eqmp_fused_backward_noalloc(vec, x, row_offsets, src, dst, send_offsets, sen
     workspace (the C entry point allocates no device memory; this wrapper
     only allocates the requested output tensors through torch)."""
     out, head, _ = _backward_prepare(vec, x, row_offsets, src, dst, send_offsets, send_edges, grad_out,
-                                     w, R, M, need)
+                                     w, R, M, need, stream)
     _check(load_library().eqmp_fused_backward_noalloc(*head, _stream(stream)), "eqmp_fused_backward_noalloc")
     return out
 

@@ -45,3 +45,22 @@ def _check_streams(gpu, calls):
 
 def test_norms_allocate_on_the_stream_of_the_call(gpu):
     _check_streams(gpu, _norm_calls(gpu))
+
+
+def _layer_calls(gpu):
+    t, i32 = gpu.tensor, lambda n: gpu.tensor(n, dtype=torch.int32)
+    graph = (t(6, 3), t(4, 8, 16), i32(5), i32(6))
+    back = graph + (i32(6), i32(5), i32(6), t(4, 8, 16))
+    shared, radial = dict(w=t(34, 8)), dict(R=t(6, 8), M=t(8, 34 * 8))
+    yield lambda s: eq.eqmp_sh(graph[0], stream=s)
+    yield lambda s: eq.eqmp_tp_scatter(t(6, 16), *graph[1:], stream=s, **shared)
+    for weights in (shared, radial):
+        yield lambda s: eq.eqmp_fused(*graph, stream=s, **weights)
+        yield lambda s: eq.eqmp_fused_so2(*graph, stream=s, **weights)
+        yield lambda s: eq.eqmp_fused_backward(*back, need=("x", "w", "R", "M", "vec"), stream=s, **weights)
+        yield lambda s: eq.eqmp_fused_backward_noalloc(*back, need=("x", "w", "R", "M", "vec"), stream=s, **weights)
+    yield lambda s: eq.eqmp_fused_lmax(4, graph[0], t(4, 8, 25), *graph[2:], w=t(65, 8), stream=s)
+
+
+def test_message_layers_allocate_on_the_stream_of_the_call(gpu):
+    _check_streams(gpu, _layer_calls(gpu))

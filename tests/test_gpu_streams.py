@@ -38,3 +38,36 @@ def test_norm_temporaries_outlive_the_call(eq, shape):  # noqa: F811
     assert all(torch.isnan(t).all() for t in taken)
     for g, w in zip(got, want):
         assert all(torch.equal(g[k], w[k]) for k in w)
+
+
+@pytest.mark.parametrize("mode", ["shared", "radial"])
+def test_layer_temporaries_outlive_the_call(eq, mode):  # noqa: F811
+    """The message layer and its gradients on a waiting side stream, as above; the zeros that gradients begin with are
+    written before the kernels add to them.  To the tolerance of the layer's parity tests, against the lone call."""
+    import numpy as np
+    import torch
+
+    from equivariant_gnn_message_gb300.inputs import make_workload
+    from tests.gpu_util import TOL, host, rel_err, to_device, weights_kw
+
+    wl = make_workload(n_atoms=300, cutoff=5.0, channels=32, weights=mode, storage="f32", seed=3)
+    d = to_device(wl)
+    up = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    so, se = eq.sender_view(wl.src, wl.n_atoms)
+    g = torch.randn(wl.n_atoms, 32, 16, device="cuda")
+    need = ("x", "vec", "w") if mode == "shared" else ("x", "vec", "R", "M")
+    back = (d["vec"], d["x"], d["off"], d["src"], up(wl.dst), up(so), up(se), g)
+    calls = (lambda s: dict(out=eq.eqmp_fused(d["vec"], d["x"], d["off"], d["src"], stream=s, **weights_kw(d))),
+             lambda s: eq.eqmp_fused_backward(*back, need=need, stream=s, **weights_kw(d)))
+    for call in calls:
+        want = call(None)
+        torch.cuda.synchronize()
+        side, = _busy_sides(1)
+        got = call(side)
+        sizes = [v.numel() for v in want.values()] + [lib_size // 4 for lib_size in (
+            eq.load_library().eqmp_fused_backward_workspace_size(wl.n_atoms, wl.n_edges, 32, int(mode == "radial")),)]
+        taken = [torch.full((n,), float("nan"), device="cuda") for n in sizes * 4]
+        torch.cuda.synchronize()
+        assert eq.eqmp_device_error() == 0 and all(torch.isnan(t).all() for t in taken)
+        for k in want:
+            assert rel_err(host(got[k]), host(want[k])) <= TOL["f32"], k
