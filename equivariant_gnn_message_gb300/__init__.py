@@ -200,6 +200,14 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _torch_stream(stream):
+    import torch
+
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream.cuda_stream)
+
+
 def _empty(shape, dtype, device, stream, temporary=False, zero=False):
     """Memory for kernels on `stream` (None: the current one), filled with zeros there if asked for.
 
@@ -210,9 +218,7 @@ def _empty(shape, dtype, device, stream, temporary=False, zero=False):
     make = torch.zeros if zero else torch.empty
     if stream is None or stream.cuda_stream == (current := torch.cuda.current_stream()).cuda_stream:
         return make(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_torch_stream(stream)):
         t = make(shape, dtype=dtype, device=device)
     if not temporary:
         t.record_stream(current)
@@ -509,30 +515,31 @@ def eqmp_radius_graph(pos, cutoff, e_cap=None, dst=False, rev=False, stream=None
     lib = load_library()
     N = pos.shape[0]
     dev = pos.device
-    ws = torch.empty(max(int(lib.eqmp_radius_graph_workspace_size(N)), 256), dtype=torch.uint8, device=dev)
-    off = torch.empty(N + 1, dtype=torch.int32, device=dev)
-    e_total = torch.empty(1, dtype=torch.int64, device=dev)
+    ws = _empty(max(int(lib.eqmp_radius_graph_workspace_size(N)), 256), torch.uint8, dev, stream, temporary=True)
+    off = _empty(N + 1, torch.int32, dev, stream)
+    e_total = _empty(1, torch.int64, dev, stream, temporary=True)
     cap = int(64 * N if e_cap is None else e_cap)
     st = _stream(stream)
     for _ in range(2):
-        out = dict(off=off, src=torch.empty(cap, dtype=torch.int32, device=dev),
-                   vec=torch.empty((cap, 3), dtype=torch.float32, device=dev))
+        out = dict(off=off, src=_empty(cap, torch.int32, dev, stream),
+                   vec=_empty((cap, 3), torch.float32, dev, stream))
         if dst:
-            out["dst"] = torch.empty(cap, dtype=torch.int32, device=dev)
+            out["dst"] = _empty(cap, torch.int32, dev, stream)
         if rev:
-            out["rev"] = torch.empty(cap, dtype=torch.int32, device=dev)
+            out["rev"] = _empty(cap, torch.int32, dev, stream)
         if box is None:
             _check(lib.eqmp_radius_graph(_ptr(pos), N, float(cutoff), _ptr(off), _ptr(out["src"]),
                                          _ptr(out["vec"]), _ptr(out.get("dst")), _ptr(out.get("rev")), cap,
                                          _ptr(e_total), _ptr(ws), ws.numel(), st), "eqmp_radius_graph")
         else:
-            out["img"] = torch.empty(cap, dtype=torch.int32, device=dev)
+            out["img"] = _empty(cap, torch.int32, dev, stream)
             lengths = (ctypes.c_float * 3)(*[float(v) for v in box])
             _check(lib.eqmp_radius_graph_pbc(_ptr(pos), N, float(cutoff), lengths, _ptr(off), _ptr(out["src"]),
                                              _ptr(out["vec"]), _ptr(out["img"]), _ptr(out.get("dst")),
                                              _ptr(out.get("rev")), cap, _ptr(e_total), _ptr(ws), ws.numel(), st),
                    "eqmp_radius_graph_pbc")
-        E = int(e_total.item())
+        with torch.cuda.stream(_torch_stream(stream)):  # the count is read behind the kernels that write it
+            E = int(e_total.item())
         if E < 0:
             raise EqmpError(EQMP_ERR_INVALID_ARG, "eqmp_radius_graph: positions non-finite or out of range"
                             " (outside the box, with periodic boundaries)"

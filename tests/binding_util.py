@@ -14,7 +14,8 @@ class FakeStream:
 class FakeTensor(torch.Tensor):
     """Host memory under the name of a GPU; `made_on`: the current stream when the binding allocated it."""
 
-    gpu, made_on, recorded = 0, None, ()
+    gpu, made_on, recorded, read_on = 0, None, (), None
+    world = None  # of the FakeGpu that made it
     is_cuda = property(lambda self: True)
 
     def get_device(self):
@@ -22,6 +23,10 @@ class FakeTensor(torch.Tensor):
 
     def record_stream(self, stream):
         self.recorded += (stream.cuda_stream,)
+
+    def item(self):
+        self.read_on = self.world.current.cuda_stream
+        return self.world.counts.pop(0)
 
 
 class FakeLibrary:
@@ -41,12 +46,13 @@ class FakeLibrary:
 class FakeGpu:
     def __init__(self, monkeypatch, eq):
         self.lib, self.current, self.made = FakeLibrary(), FakeStream(7), []
+        self.counts = []  # what item() returns
         empty, zeros = torch.empty, torch.zeros
 
         def allocate(make):
             def fn(*shape, dtype=None, device=None):
                 t = make(*shape, dtype=dtype).as_subclass(FakeTensor)
-                t.made_on = self.current.cuda_stream
+                t.made_on, t.world = self.current.cuda_stream, self
                 self.made.append(t)  # kept: no address comes twice
                 return t
 
@@ -54,7 +60,7 @@ class FakeGpu:
 
         @contextlib.contextmanager
         def on(stream):
-            before, self.current = self.current, stream
+            before, self.current = self.current, stream or self.current
             yield
             self.current = before
 

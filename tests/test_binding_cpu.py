@@ -64,3 +64,21 @@ def _layer_calls(gpu):
 
 def test_message_layers_allocate_on_the_stream_of_the_call(gpu):
     _check_streams(gpu, _layer_calls(gpu))
+
+
+@pytest.mark.parametrize("box", [None, (9.0, 9.0, 9.0)])
+def test_radius_graph_reads_its_count_on_the_stream_of_the_call(gpu, box):
+    """The edge count is read in the order of the kernels, also when the call is repeated for more room."""
+    for stream, want in ((None, 7), (FakeStream(SIDE), SIDE)):
+        gpu.made.clear()
+        gpu.lib.calls.clear()
+        gpu.counts = [700, 700]
+        out, E = eq.eqmp_radius_graph(gpu.tensor(10, 3), 1.0, dst=True, rev=True, stream=stream, box=box)
+        assert E == 700 and out["src"].shape == (700,) and gpu.current.cuda_stream == 7
+        runs = [args for name, args in gpu.lib.calls if not name.endswith("_size")]
+        assert len(runs) == 2 and all(args[-1] == want for args in runs)
+        read = [t for t in gpu.made if t.read_on is not None]
+        assert len(read) == 1 and read[0].read_on == want
+        for t in gpu.made:
+            assert gpu.given(t) and t.made_on == want
+        assert out["off"].recorded == ((7,) if want == SIDE else ())

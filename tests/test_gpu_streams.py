@@ -71,3 +71,19 @@ def test_layer_temporaries_outlive_the_call(eq, mode):  # noqa: F811
         assert eq.eqmp_device_error() == 0 and all(torch.isnan(t).all() for t in taken)
         for k in want:
             assert rel_err(host(got[k]), host(want[k])) <= TOL["f32"], k
+
+
+@pytest.mark.parametrize("e_cap", [None, 100])
+@pytest.mark.parametrize("box", [None, (12.0, 12.0, 12.0)])
+def test_radius_graph_on_a_waiting_stream(eq, box, e_cap):  # noqa: F811
+    """The count is that of this call, not what lay in its place: the same edges, to the bit, with room and without."""
+    import torch
+
+    pos = torch.rand(200, 3, device="cuda") * 12
+    want, E = eq.eqmp_radius_graph(pos, 4.0, e_cap=e_cap, dst=True, rev=True, box=box)
+    torch.cuda.synchronize()
+    side, = _busy_sides(1)
+    got, n = eq.eqmp_radius_graph(pos, 4.0, e_cap=e_cap, dst=True, rev=True, box=box, stream=side)
+    torch.cuda.synchronize()
+    assert n == E > 100 and set(got) == set(want)
+    assert all(torch.equal(got[k], want[k]) for k in want)
