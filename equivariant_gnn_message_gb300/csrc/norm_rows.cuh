@@ -256,7 +256,7 @@ struct Slots {
   int cols;
   int lane;         // within the group
   int cls[GROUPS];  // degree
-  float2 first[PAIRS];  // 1 where a value is a degree 0, else 0
+  uint2 zero[PAIRS];  // all bits where a value is of degree 0, else none
 
   // `row`: the first row of the group.
   __device__ __forceinline__ Slots(const RowShape& sh, int cols_, int row) : cols(cols_) {
@@ -280,9 +280,12 @@ struct Slots {
       }
     }
     float f[GROUPS];
+    float2 first[PAIRS];
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) f[g] = cls[g] == 0 ? 1.0f : 0.0f;
     spread(f, first);
+#pragma unroll
+    for (int s = 0; s < PAIRS; ++s) zero[s] = make_uint2(first[s].x != 0.0f ? ~0u : 0u, first[s].y != 0.0f ? ~0u : 0u);
   }
   // Whether value i of vector j is one of the row's.
   __device__ __forceinline__ bool valid(int j, int i) const {
@@ -318,8 +321,26 @@ struct Slots {
       }
     }
   }
-  // Whether pair s of a vector may hold a degree 0.
+  // Whether pair s of a vector may hold a degree 0 (with FOURS its first value only).
   __device__ __forceinline__ static constexpr bool may0(int s) { return !FOURS || s % 2 == 0; }
+  // The degree 0 of pair s (with L = 0 all of it), 0 in place of what is of another degree.  By selection: a product
+  // with 0 would carry a NaN or an infinity from one degree into another.
+  __device__ __forceinline__ float2 only0(int s, float2 v) const {
+    if (L == 0) return v;
+    return make_float2(__uint_as_float(__float_as_uint(v.x) & zero[s].x),
+                       FOURS ? 0.0f : __uint_as_float(__float_as_uint(v.y) & zero[s].y));
+  }
+  // The degree 0 of vector j, or 0 where it has none: a vector has one at most.
+  __device__ __forceinline__ float degree0(const float2* p) const {
+    uint32_t t = 0;
+#pragma unroll
+    for (int s = 0; s < PAIRS; ++s) {
+      if (!may0(s)) continue;
+      t |= __float_as_uint(p[s].x) & zero[s].x;
+      if (!FOURS) t |= __float_as_uint(p[s].y) & zero[s].y;
+    }
+    return __uint_as_float(t);
+  }
   // One value per group put to the pairs of a vector.
   __device__ __forceinline__ static void spread(const float (&g)[GROUPS], float2 (&p)[PAIRS]) {
 #pragma unroll
@@ -816,17 +837,18 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
       float2 t = v[s];
 #pragma unroll
       for (int p = s + PV; p < P; p += PV) t = __fadd2_rn(t, v[p]);
-      if (L) t = __fmul2_rn(t, at.first[s]);
+      t = at.only0(s, t);
       part[0] += t.x + t.y;
     }
     sum1(part);
     const float mean = sum1.fetch(0) * inv;
     // centred; what lies outside the row stays 0
+    float2 mu[PV];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      if (!S::may0(p % PV)) continue;
-      v[p] = L ? __ffma2_rn(both(-mean), at.first[p % PV], v[p]) : __fadd2_rn(both(-mean), v[p]);
-    }
+    for (int s = 0; s < PV; ++s) mu[s] = at.only0(s, both(-mean));
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      if (S::may0(p % PV)) v[p] = __fadd2_rn(mu[p % PV], v[p]);
     if (!all) at.clear_outside(v);
 #pragma unroll
     for (int s = 0; s < PV; ++s) {
@@ -866,7 +888,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
       if (EACH)
         v[p] = __ffma2_rn(h, w[p % PR], b[EACH ? p % PR : 0]);
       else if (S::may0(p % PV))
-        v[p] = __ffma2_rn(h, w[p % PR], __fmul2_rn(b[EACH ? 0 : p / PV], at.first[p % PV]));
+        v[p] = __ffma2_rn(h, w[p % PR], at.only0(p % PV, b[EACH ? 0 : p / PV]));
       else
         v[p] = __fmul2_rn(h, w[p % PR]);
     }
@@ -899,6 +921,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
   using F = Feed<T, V, NV, MODE ? 3 : 2, stat_words(L)>;
   constexpr int P = NV * V / 2, PV = S::PAIRS, NS = L + 2;
   constexpr bool EACH = L == 0 || V == 1;  // db per value; else per vector, which has at most one degree 0
+  constexpr int DB = EACH ? P : (NV + 1) / 2;  // pairs: of two values, or of two vectors
   __shared__ __align__(16) float red[GroupSum<NS>::kRed];
   __shared__ uint8_t bits[MODE == kMixed ? 2 * kKeepBytes + 1 : 1];
   extern __shared__ __align__(128) uint8_t ring[];  // at the end the column sums: [cols] g h, [C] g
@@ -937,12 +960,12 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
   GroupSum<NS> sum(sh.lanes, red);
   const Dropper drop(a.drop);
   Keeps<S, V, NV, MODE == kDirect> keeps(drop, at, sh, a.cols, bits);
-  float2 w[P], dw[P], db[EACH ? P : NV];
+  float2 w[P], dw[P], db[DB];
   load_weights<L, V, NV, S>(at, a, w);
 #pragma unroll
   for (int p = 0; p < P; ++p) dw[p] = both(0.0f);
 #pragma unroll
-  for (int p = 0; p < (EACH ? P : NV); ++p) db[p] = both(0.0f);
+  for (int p = 0; p < DB; ++p) db[p] = both(0.0f);
   const float inv = 1.0f / (float)a.C;
   float scale[S::GROUPS];
 #pragma unroll
@@ -973,22 +996,23 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
     load_row();
     if (MODE == kMixed && drop.on) keeps.form_now(drop, sh, row, stride);
     S::spread(q, qs);
-    float2 sa[PV], sah[PV];
+    float2 sa[PV], sah[PV], mus[PV];
 #pragma unroll
-    for (int s = 0; s < PV; ++s) sa[s] = sah[s] = both(0.0f);
+    for (int s = 0; s < PV; ++s) {
+      sa[s] = sah[s] = both(0.0f);
+      mus[s] = at.only0(s, mu);
+    }
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int s = p % PV;
-      if (L == 0)
-        h[p] = __fadd2_rn(h[p], mu);
-      else if (S::may0(s))
-        h[p] = __ffma2_rn(mu, at.first[s], h[p]);
+      if (S::may0(s)) h[p] = __fadd2_rn(h[p], mus[s]);
       h[p] = __fmul2_rn(h[p], qs[s]);
       dw[p] = __ffma2_rn(av[p], h[p], dw[p]);
-      if (EACH)
-        db[EACH ? p : 0] = __fadd2_rn(db[EACH ? p : 0], av[p]);
-      else if (S::may0(s))
-        db[EACH ? 0 : p / PV] = __ffma2_rn(av[p], at.first[s], db[EACH ? 0 : p / PV]);
+      if (EACH) db[EACH ? p : 0] = __fadd2_rn(db[EACH ? p : 0], av[p]);
+      if (!EACH && s == 0) {
+        float& t = p / PV & 1 ? db[EACH ? 0 : p / PV / 2].y : db[EACH ? 0 : p / PV / 2].x;
+        t += at.degree0(av + p);
+      }
       av[p] = __fmul2_rn(av[p], w[p]);
       if (S::may0(s)) sa[s] = __fadd2_rn(sa[s], av[p]);
       sah[s] = __ffma2_rn(av[p], h[p], sah[s]);
@@ -998,7 +1022,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
 #pragma unroll
     for (int s = 0; s < PV; ++s) {
       if (!S::may0(s)) continue;
-      if (L) sa[s] = __fmul2_rn(sa[s], at.first[s]);
+      sa[s] = at.only0(s, sa[s]);
       tot[0] += sa[s].x + sa[s].y;
     }
     at.by_degree(sah, tot + 1);
@@ -1013,8 +1037,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
 #pragma unroll
     for (int s = 0; s < PV; ++s) {
       if (!S::may0(s)) continue;
-      sa[s] = __fmul2_rn(qs[s], both(m0));
-      if (L) sa[s] = __fmul2_rn(sa[s], at.first[s]);
+      sa[s] = at.only0(s, __fmul2_rn(qs[s], both(m0)));
     }
 #pragma unroll
     for (int p = 0; p < P; ++p) {
@@ -1058,7 +1081,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
         dw[p].y += __shfl_xor_sync(0xffffffffu, dw[p].y, o);
       }
 #pragma unroll
-      for (int p = 0; p < (EACH ? P : NV); ++p) {
+      for (int p = 0; p < DB; ++p) {
         db[p].x += __shfl_xor_sync(0xffffffffu, db[p].x, o);
         db[p].y += __shfl_xor_sync(0xffffffffu, db[p].y, o);
       }
@@ -1083,7 +1106,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, Ro
       }
       if (!EACH) {
         const int c = ((int)at.col[j] + V - 1) / S::K;  // the channel that begins in the vector, if one does
-        if (c * S::K >= (int)at.col[j] && c < a.C) mine[KP * a.C + c] = db[EACH ? 0 : j].x + db[EACH ? 0 : j].y;
+        if (c * S::K >= (int)at.col[j] && c < a.C) mine[KP * a.C + c] = j & 1 ? db[EACH ? 0 : j / 2].y : db[EACH ? 0 : j / 2].x;
       }
     }
   }
