@@ -32,30 +32,47 @@ struct Plane {
   long long ld;
 };
 
-static bool overlap(const Plane& a, const Plane& b, long long rows, long long cols, int bytes) {
-  if (!a.p || !b.p) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  const uintptr_t a1 = a0 + ((rows - 1) * a.ld + cols) * bytes, b1 = b0 + ((rows - 1) * b.ld + cols) * bytes;
-  return a0 < b1 && b0 < a1;
+// The memory of an argument; NULL and empty ones meet nothing.
+struct Span {
+  uintptr_t begin, end;
+};
+
+static Span span(const void* p, long long bytes) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  return Span{at, p && bytes > 0 ? at + (uintptr_t)bytes : at};
+}
+
+static Span span(const Plane& a, long long rows, long long cols, int bytes) {
+  return span(a.p, rows > 0 ? ((rows - 1) * a.ld + cols) * bytes : 0);
+}
+
+static Span span(const DropArgs& d) { return span(d.step, sizeof(*d.step)); }
+
+static bool meet(const Span& a, const Span& b) {
+  return a.begin < a.end && b.begin < b.end && a.begin < b.end && b.begin < a.end;
+}
+
+// Outputs apart from the inputs and from one another.
+template <int I, int O>
+static bool outputs_apart(const Span (&in)[I], const Span (&out)[O]) {
+  for (int o = 0; o < O; ++o) {
+    for (int i = 0; i < I; ++i)
+      if (meet(in[i], out[o])) return false;
+    for (int q = 0; q < o; ++q)
+      if (meet(out[q], out[o])) return false;
+  }
+  return true;
 }
 
 // A row stride of up to 2^31 elements, so that 2^30 rows stay in 64 bits.
 static bool stride_ok(long long ld) { return ld >= 0 && ld <= 1ll << 31; }
 
-// Inputs: aligned, strides that address forward.  Outputs (packed): aligned,
-// apart from the inputs and from one another.
-static bool planes_ok(const Plane* in, int n_in, void* const* outs, int n_out, long long rows, long long cols,
-                      int bytes) {
+// Inputs: aligned, strides that address forward.  Outputs (packed): aligned.
+static bool planes_ok(const Plane* in, int n_in, void* const* outs, int n_out, int bytes) {
   for (int i = 0; i < n_in; ++i)
     if (in[i].p && (!aligned(in[i].p, bytes) || !stride_ok(in[i].ld))) return false;
-  for (int o = 0; o < n_out; ++o) {
-    if (!outs[o]) continue;
+  for (int o = 0; o < n_out; ++o)
     if (!aligned(outs[o], bytes)) return false;
-    for (int i = 0; i < n_in; ++i)
-      if (overlap(in[i], Plane{outs[o], cols}, rows, cols, bytes)) return false;
-    for (int q = 0; q < o; ++q)
-      if (overlap(Plane{outs[q], cols}, Plane{outs[o], cols}, rows, cols, bytes)) return false;
-  }
   return true;
 }
 
@@ -155,10 +172,15 @@ static eqmp_status run_forward(Plane x, Plane r, eqmp_dtype dtype, int64_t rows,
   if (ds != EQMP_OK) return ds;
   if (rows == 0 || (!s && !y && !stats)) return EQMP_OK;
   const bool bf16 = dtype == EQMP_BF16;
+  const int bytes = bf16 ? 2 : 4;
   const Plane in[] = {x, r};
   void* const outs[] = {s, y};
-  if (!x.p || !planes_ok(in, 2, outs, 2, rows, C * K, bf16 ? 2 : 4)) return EQMP_ERR_INVALID_ARG;
+  if (!x.p || !planes_ok(in, 2, outs, 2, bytes)) return EQMP_ERR_INVALID_ARG;
   if (!aligned(w, 4) || !aligned(b, 4) || !aligned(stats, 4)) return EQMP_ERR_INVALID_ARG;
+  const Span reads[] = {span(x, rows, C * K, bytes), span(r, rows, C * K, bytes), span(w, (L + 1) * C * 4), span(b, C * 4),
+                        span(a.drop)};
+  const Span writes[] = {span(s, rows * C * K * bytes), span(y, rows * C * K * bytes), span(stats, rows * (L + 2) * 4)};
+  if (!outputs_apart(reads, writes)) return EQMP_ERR_INVALID_ARG;
   a.x = x.p;
   a.x_ld = x.ld;
   a.r = r.p;
@@ -186,15 +208,22 @@ static eqmp_status run_backward(Plane g, Plane x, Plane r, eqmp_dtype dtype, int
   if (ds != EQMP_OK) return ds;
   if (!gr && !gx && !gw && !gb) return EQMP_OK;
   if (!aligned(gw, 4) || !aligned(gb, 4)) return EQMP_ERR_INVALID_ARG;
+  const bool bf16 = dtype == EQMP_BF16;
+  const int bytes = bf16 ? 2 : 4;
+  const Plane in[] = {x, g, r};
+  if (rows > 0 && !planes_ok(in, 3, nullptr, 0, bytes)) return EQMP_ERR_INVALID_ARG;
+  const Span reads[] = {span(x, rows, C * K, bytes), span(g, rows, C * K, bytes), span(r, rows, C * K, bytes),
+                        span(w, (L + 1) * C * 4), span(stats, rows * (L + 2) * 4), span(a.drop)};
+  const Span writes[] = {span(gr, rows * C * K * bytes), span(gx, rows * C * K * bytes), span(gw, (L + 1) * C * 4),
+                         span(gb, C * 4), span(workspace, gw || gb ? workspace_bytes(rows, C, L) : 0)};
+  if (!outputs_apart(reads, writes)) return EQMP_ERR_INVALID_ARG;
   if (rows == 0) {  // no row: the sums are zero
     if (gw && cudaMemsetAsync(gw, 0, (size_t)(L + 1) * C * 4, st) != cudaSuccess) return EQMP_ERR_CUDA;
     if (gb && cudaMemsetAsync(gb, 0, (size_t)C * 4, st) != cudaSuccess) return EQMP_ERR_CUDA;
     return EQMP_OK;
   }
-  const bool bf16 = dtype == EQMP_BF16;
-  const Plane in[] = {x, g, r};
   void* const outs[] = {gr, gx};
-  if (!x.p || !g.p || !stats || !planes_ok(in, 3, outs, 2, rows, C * K, bf16 ? 2 : 4)) return EQMP_ERR_INVALID_ARG;
+  if (!x.p || !g.p || !stats || !planes_ok(nullptr, 0, outs, 2, bytes)) return EQMP_ERR_INVALID_ARG;
   if (!aligned(w, 4) || !aligned(stats, 4)) return EQMP_ERR_INVALID_ARG;
   if ((gw || gb) && (!workspace || !aligned(workspace, 16) || ws_bytes < workspace_bytes(rows, C, L)))
     return EQMP_ERR_INVALID_ARG;
@@ -465,7 +494,9 @@ eqmp_status eqmp_dropout(const void* x, int64_t x_ld, eqmp_dtype dtype, int64_t 
   const int bytes = dtype == EQMP_BF16 ? 2 : 4;
   if (!x || !out || !stride_ok(x_ld) || !aligned(x, bytes) || !aligned(out, bytes)) return EQMP_ERR_INVALID_ARG;
   const bool in_place = x == out && (x_ld == cols || rows == 1);  // each element is read before it is written, by one thread
-  if (!in_place && overlap(Plane{x, x_ld}, Plane{out, cols}, rows, cols, bytes)) return EQMP_ERR_INVALID_ARG;
+  const Span reads[] = {in_place ? Span{} : span(Plane{x, x_ld}, rows, cols, bytes), span(d)};
+  const Span writes[] = {span(out, rows * cols * bytes)};
+  if (!outputs_apart(reads, writes)) return EQMP_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dtype == EQMP_BF16 ? run_dropout<__nv_bfloat16>(x, x_ld, out, (int)rows, (int)cols, d, st)
                             : run_dropout<float>(x, x_ld, out, (int)rows, (int)cols, d, st);

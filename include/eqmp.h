@@ -412,8 +412,9 @@ typedef struct {
  *     beyond the element's own is needed; 16-byte aligned rows are faster.
  *   - Up to 2^30 rows of up to 2^30 values (EQMP_ERR_UNSUPPORTED above).
  *     rows == 0 launches no kernel; the sums over rows are then 0.
- *   - Outputs may be NULL to skip them, and must not overlap the inputs or
- *     one another (EQMP_ERR_INVALID_ARG), but for eqmp_dropout in place.
+ *   - Outputs may be NULL to skip them.  They and the workspace must not
+ *     overlap the inputs (w, b, stats and the step counter among them) or one
+ *     another (EQMP_ERR_INVALID_ARG), but for eqmp_dropout in place.
  *   - Results are bitwise reproducible on one device: every sum has a fixed
  *     order, and nothing is added by atomics.  The order of a row's sums hangs
  *     on the sizes, the alignment and, for rows that do not begin on 16 bytes,
