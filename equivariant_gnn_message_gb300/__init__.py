@@ -782,6 +782,8 @@ def _norm_backward(entry, degree, grad_y, s, stats, w, grad_s, drop, need, out, 
             workspace = _empty(nbytes // 4 + 4, f32, s.device, stream, temporary=True)
         else:
             _require(workspace, "workspace", torch.uint8)
+            if workspace.get_device() != dev:
+                raise ValueError("workspace must be a CUDA tensor on the current device")
             nbytes = workspace.numel()
         ws = workspace.data_ptr()
     dt = EQMP_F32 if dtype is f32 else EQMP_BF16

@@ -82,3 +82,15 @@ def test_radius_graph_reads_its_count_on_the_stream_of_the_call(gpu, box):
         for t in gpu.made:
             assert gpu.given(t) and t.made_on == want
         assert out["off"].recorded == ((7,) if want == SIDE else ())
+
+
+def test_workspace_of_another_gpu_is_refused(gpu):
+    t = gpu.tensor
+    x, feat, ws = t(5, 8), t(5, 8, 16), lambda g: t(4096, dtype=torch.uint8, gpu=g)
+    for call in (lambda ws: eq.eqmp_layer_norm_backward(x, x, t(5, 2), workspace=ws),
+                 lambda ws: eq.eqmp_degree_norm_backward(feat, feat, t(5, 5), workspace=ws)):
+        call(ws(0))
+        gpu.lib.calls.clear()
+        with pytest.raises(ValueError, match="workspace must be a CUDA tensor on the current device"):
+            call(ws(1))
+        assert not gpu.lib.calls
