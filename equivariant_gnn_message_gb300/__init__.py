@@ -73,6 +73,7 @@ class Dropout(ctypes.Structure):
     value that is added to offset when the kernel runs (for recorded CUDA graphs)."""
     _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
                 ("step_ptr", ctypes.c_void_p), ("group", ctypes.c_int32)]
+    step = None
 
     def __init__(self, p, seed, offset=0, group=1, step=None):
         if not 0.0 <= p <= 1.0:
@@ -700,8 +701,12 @@ def _main_input(x, name, degree, torch):
     return torch.cuda.current_device(), 0
 
 
-def _not_dropout(drop):
-    raise TypeError(f"drop must be a Dropout, not {type(drop).__name__}")
+def _drop(drop, dev):
+    if not isinstance(drop, Dropout):
+        raise TypeError(f"drop must be a Dropout, not {type(drop).__name__}")
+    if drop.step is not None and drop.step.get_device() != dev:
+        raise ValueError("drop's step must be a CUDA tensor on the current device")
+    return drop
 
 
 def _raw_stream(stream, dev, torch):
@@ -737,7 +742,7 @@ def _norm_forward(entry, degree, x, w, b, eps, residual, drop, need, out, stream
     if len(got) != len(need):
         _unknown(need, ("y", "s", "stats"))
     dt = EQMP_F32 if dtype is f32 else EQMP_BF16
-    dr = _NO_DROP if drop is None else drop if isinstance(drop, Dropout) else _not_dropout(drop)
+    dr = _NO_DROP if drop is None else _drop(drop, dev)
     lib, st = load_library(), _raw_stream(stream, dev, torch)
     if degree:
         status = lib.eqmp_degree_norm(xp, rp, dt, n, c, l_max, dr, wp, bp, eps, sp, yp, tp, st)
@@ -787,7 +792,7 @@ def _norm_backward(entry, degree, grad_y, s, stats, w, grad_s, drop, need, out, 
             nbytes = workspace.numel()
         ws = workspace.data_ptr()
     dt = EQMP_F32 if dtype is f32 else EQMP_BF16
-    dr = _NO_DROP if drop is None else drop if isinstance(drop, Dropout) else _not_dropout(drop)
+    dr = _NO_DROP if drop is None else _drop(drop, dev)
     if degree:
         status = lib.eqmp_degree_norm_backward(gp, xp, rp, dt, n, c, l_max, dr, wp, tp, grp, gxp, gwp, gbp, ws, nbytes, st)
     else:
@@ -820,7 +825,7 @@ def eqmp_dropout(x, drop, out=None, stream=None):
     if out is None:
         out = _empty(shape, dtype, x.device, stream)
     op = _packed(out, "out", dtype, shape, dev, torch)
-    dr = _NO_DROP if drop is None else drop if isinstance(drop, Dropout) else _not_dropout(drop)
+    dr = _NO_DROP if drop is None else _drop(drop, dev)
     status = load_library().eqmp_dropout(xp, cols if out is x else ld, EQMP_F32 if dtype is torch.float32 else EQMP_BF16,
                                          shape[0], cols, dr, op,
                                          _raw_stream(stream, dev, torch))

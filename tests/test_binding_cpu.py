@@ -94,3 +94,21 @@ def test_workspace_of_another_gpu_is_refused(gpu):
         with pytest.raises(ValueError, match="workspace must be a CUDA tensor on the current device"):
             call(ws(1))
         assert not gpu.lib.calls
+
+
+def test_step_counter_of_another_gpu_is_refused(gpu):
+    t = gpu.tensor
+    x, feat = t(5, 8), t(5, 8, 16)
+
+    def drop(g, group=1):
+        return eq.Dropout(0.5, 1, group=group, step=t(1, dtype=torch.int64, gpu=g))
+
+    for call in (lambda g: eq.eqmp_dropout(x, drop(g)), lambda g: eq.eqmp_layer_norm(x, drop=drop(g)),
+                 lambda g: eq.eqmp_layer_norm_backward(x, x, t(5, 2), drop=drop(g)),
+                 lambda g: eq.eqmp_degree_norm(feat, drop=drop(g, 16)),
+                 lambda g: eq.eqmp_degree_norm_backward(feat, feat, t(5, 5), drop=drop(g, 16))):
+        call(0)
+        gpu.lib.calls.clear()
+        with pytest.raises(ValueError, match="step must be a CUDA tensor on the current device"):
+            call(1)
+        assert not [name for name, _ in gpu.lib.calls if not name.endswith("_size")]
