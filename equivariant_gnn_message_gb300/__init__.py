@@ -219,8 +219,11 @@ def _empty(shape, dtype, device, stream, temporary=False, zero=False):
     make = torch.zeros if zero else torch.empty
     if stream is None or stream.cuda_stream == (current := torch.cuda.current_stream()).cuda_stream:
         return make(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(_torch_stream(stream)):
+    torch.cuda.set_stream(_torch_stream(stream))
+    try:
         t = make(shape, dtype=dtype, device=device)
+    finally:
+        torch.cuda.set_stream(current)
     if not temporary:
         t.record_stream(current)
     return t

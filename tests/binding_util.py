@@ -64,9 +64,12 @@ class FakeGpu:
             yield
             self.current = before
 
+        def set_stream(stream):
+            self.current = stream
+
         for where, name, value in ((torch, "empty", allocate(empty)), (torch, "zeros", allocate(zeros)),
-                                   (torch.cuda, "stream", on), (torch.cuda, "Stream", FakeStream),
-                                   (torch.cuda, "current_stream", lambda *a: self.current),
+                                   (torch.cuda, "stream", on), (torch.cuda, "set_stream", set_stream),
+                                   (torch.cuda, "Stream", FakeStream), (torch.cuda, "current_stream", lambda *a: self.current),
                                    (torch.cuda, "current_device", lambda: 0),
                                    (torch._C, "_cuda_getCurrentRawStream", lambda dev: self.current.cuda_stream),
                                    (eq, "load_library", lambda: self.lib)):
