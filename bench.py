@@ -706,8 +706,8 @@ def main():
             host_bytes = [ps[3].view(torch.uint8).numpy().reshape(-1) for ps in pipe_sets]
             # a collection of the interpreter's garbage takes 150 us; whether one
             # falls into this span of about 450 us hangs on how many objects the
-            # imports made, not on the steps
-            gc.collect()
+            # imports made, not on the steps.  None is made in front of the span
+            # either: a walk over all objects leaves the host's caches cold for it
             gc.disable()
             for i in range(2 * PIPE):
                 runs[i % PIPE]()
