@@ -29,6 +29,10 @@ Entry points (same names as the C ABI):
   eqmp_layer_norm_backward(grad_y, s, stats, w, grad_s=, drop=) -> dict of gradients
   eqmp_degree_norm(x, w, b, residual=, drop=)   -> dict, on node features [N, C, (l_max+1)^2]
   eqmp_degree_norm_backward(grad_y, s, stats, w, grad_s=, drop=) -> dict of gradients
+
+stream= (default: torch's current stream) is the stream that a call's kernels run on.  The inputs must be ready there.
+Results that the call allocates come from that stream's pool and are recorded on the current stream as well, so they may
+be used and freed on either; the current stream has to wait for the call's stream before it reads them.
 """
 import ctypes
 import os

@@ -194,8 +194,10 @@ __device__ __forceinline__ void cta_sum(float (&v)[NV], float* red) {
 }
 
 // Any shape, forward: one CTA per row, which reads the row three times.  Takes
-// the rows that are too wide for registers (over 8192 values): 1800 x 16384
-// fp32 147 us, 24 % of the measured copy rate, bound by its single values.
+// the rows that are too wide for the registers of one CTA: over 8192 values, by
+// degree over 8192, 8000, 8064 and 7840 at l_max 3 to 6 (whole periods of lanes),
+// up to 14 less where rows begin anywhere.  1800 x 16384 fp32 147 us, 24 % of the
+// measured copy rate, bound by its single values.
 template <typename T, int L>
 __global__ void __launch_bounds__(kWideThreads) k_norm_wide(NormArgs a) {
   constexpr int K = (L + 1) * (L + 1);

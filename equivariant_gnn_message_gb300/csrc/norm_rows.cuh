@@ -723,8 +723,11 @@ __device__ __forceinline__ void load_weights(const S& at, const NormArgs& a, flo
 // stored once.  GPU time on one GB300, share of the measured copy rate:
 //   1,909,372 x 64 bf16                          77.2 us  96 %   (bound by HBM)
 //   100,000 x 64 x 16 fp32, residual, dropout     237 us 102 %   (bound by HBM)
-//   10,000 x 1024 bf16, residual, dropout        16.9 us  72 %   (instructions: the generator's, the conversions')
-//   16,516 x 131 fp32 out of rows of 189          7.1 us  36 %   (instructions: x is copied value by value)
+//   10,000 x 1024 bf16, residual, dropout        16.9 us  72 %   (about 5 us to fill and to empty the device, the
+//       rest at the copy rate: 15.9 us for 9000 rows, 20.7 for 13,000, without a step where a round begins; 40,000
+//       rows 56.4 us, 86 %)
+//   16,516 x 131 fp32 out of rows of 189          7.3 us  35 %   (instructions, 63 a value: x is copied value by value)
+//   20,000 x 64 x 25 bf16                        53.0 us  36 %   (instructions, 45 a value: eight degrees a vector)
 template <typename T, int L, int V, int NV, int SHIFT, int MODE>
 __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowShape sh) {
   using S = Slots<L, V, NV, SHIFT>;
@@ -859,7 +862,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_rows(NormArgs a, RowSha
     float sq[NS];
     at.by_degree(acc, sq);
     sum2(sq);
-    float q[S::GROUPS];
+    float q[S::GROUPS];  // the approximate root is within 2 units in the last place
 #pragma unroll
     for (int g = 0; g < S::GROUPS; ++g) q[g] = rsqrtf(sum2.fetch(at.cls[g]) * scale[g] + a.eps);
     if (a.stats) {
@@ -913,8 +916,10 @@ constexpr int stat_words(int L) { return L == 0 ? 2 : 1; }
 // of DRAM gains (45 against 60 us and more at 10,000 x 128 x 16).
 //   477,664 x 128 bf16                            59.1 us  93 %   (HBM, then the tail)
 //   20,000 x 32 x 49 fp32                         61.8 us  90 %   (HBM, barriers of a row's warps)
-//   10,000 x 128 x 16 bf16, residual, dropout     35.7 us  85 %   (instructions)
-//   16,516 x 509 fp32, residual, dropout          32.3 us  77 %   (instructions: partial vectors, keep bits)
+//   10,000 x 128 x 16 bf16, residual, dropout     35.6 us  85 %   (instructions, 38 a value)
+//   16,516 x 509 fp32, residual, dropout          32.2 us  77 %   (instructions, 73 a value: partial vectors, keep bits)
+//   40,000 x 768 bf16                             47.1 us  58 %   (a quarter of the places empty, two warps' barrier a row)
+//   20,000 x 64 x 25 bf16                         67.1 us  42 %   (instructions, 49 a value: eight degrees a vector, spills)
 template <typename T, int L, int V, int NV, int SHIFT, int MODE>
 __global__ void __launch_bounds__(kMaxRowThreads) k_norm_bwd_rows(NormArgs a, RowShape sh) {
   using S = Slots<L, V, NV, SHIFT>;
@@ -1250,7 +1255,9 @@ static eqmp_status launch_rows(const NormArgs& a, const RowShape& sh, const Devi
 // 768 columns: one warp, every lane full, for two of which a quarter idles) or
 // as many and fewer warps (1536 columns: 24.0 us for 20,000 bf16 rows, 29.7
 // with 16),
-// and bf16 32 where one warp then does for two (769 to 1024 columns).
+// and bf16 32 where one warp then does for two (769 to 1024 columns).  The
+// norms by degree and the backward passes do not weigh empty places: 40,000 x
+// 768 bf16 backward fills 48 of 64 lanes, 100,000 x 8 x 49 39 % of its places.
 template <typename T, int L, int V, int SHIFT, bool BACKWARD>
 static eqmp_status launch_rows_v(const NormArgs& a, int apart, const DeviceInfo& dev, cudaStream_t st, bool* done) {
   constexpr int K = (L + 1) * (L + 1), N8 = 8 / V, N16 = 16 / V;
