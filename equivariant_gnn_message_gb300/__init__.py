@@ -29,6 +29,13 @@ Entry points (same names as the C ABI):
   eqmp_layer_norm_backward(grad_y, s, stats, w, grad_s=, drop=) -> dict of gradients
   eqmp_degree_norm(x, w, b, residual=, drop=)   -> dict, on node features [N, C, (l_max+1)^2]
   eqmp_degree_norm_backward(grad_y, s, stats, w, grad_s=, drop=) -> dict of gradients
+  eqmp_head_norm(q, k, wq, wk, pos=, freq=)     -> dict(q, k[, rstd]): norm of each head, rotation by position
+  eqmp_head_norm_backward(grad_q, grad_k, q, k, rstd, wq, wk, pos=, freq=) -> dict of gradients
+  eqmp_edge_bias(vec, borders, table)           -> dict(bias, bucket) by the edges' lengths
+  eqmp_edge_bias_backward(grad_bias, bucket, n_buckets) -> dict(table)
+  eqmp_edge_attention(q, k, v, row_offsets, src, bias=) -> dict(out[, stats])
+  eqmp_edge_attention_backward(grad_out, q, k, v, stats, row_offsets, src, dst, send_offsets, send_edges, bias=)
+                                                -> dict of gradients
 
 stream= (default: torch's current stream) is the stream that a call's kernels run on.  The inputs must be ready there.
 Results that the call allocates come from that stream's pool and are recorded on the current stream as well, so they may
@@ -45,7 +52,11 @@ __all__ = [
     "eqmp_device_error", "eqmp_fused_backward", "eqmp_fused_backward_noalloc", "eqmp_radius_graph", "eqmp_fused_lmax",
     "eqmp_num_paths_lmax", "eqmp_watchdog_selftest", "eqmp_fp32_peak_probe", "sender_view",
     "Dropout", "eqmp_dropout", "eqmp_layer_norm", "eqmp_layer_norm_backward", "eqmp_layer_norm_backward_workspace_size",
-    "eqmp_degree_norm", "eqmp_degree_norm_backward", "eqmp_degree_norm_backward_workspace_size", "EQMP_OK", "EQMP_ERR_INVALID_ARG", "EQMP_ERR_UNSUPPORTED",
+    "eqmp_degree_norm", "eqmp_degree_norm_backward", "eqmp_degree_norm_backward_workspace_size",
+    "eqmp_head_norm", "eqmp_head_norm_backward", "eqmp_head_norm_backward_workspace_size",
+    "eqmp_edge_bias", "eqmp_edge_bias_backward", "eqmp_edge_bias_backward_workspace_size",
+    "eqmp_edge_attention", "eqmp_edge_attention_workspace_size",
+    "eqmp_edge_attention_backward", "eqmp_edge_attention_backward_workspace_size", "EQMP_OK", "EQMP_ERR_INVALID_ARG", "EQMP_ERR_UNSUPPORTED",
     "EQMP_ERR_CUDA", "EQMP_ERR_DEVICE_TIMEOUT", "EQMP_ERR_GRAPH",
 ]
 
@@ -178,6 +189,23 @@ def load_library():
     lib.eqmp_layer_norm_backward_workspace_size.restype = i64
     lib.eqmp_degree_norm_backward_workspace_size.argtypes = [i64, i32, i32]
     lib.eqmp_degree_norm_backward_workspace_size.restype = i64
+    lib.eqmp_head_norm.argtypes = [vp, i64, i32, vp, i64, i32, i32, i64, i32, vp, vp, f32, vp, vp, i32, vp, vp, vp, vp]
+    lib.eqmp_head_norm_backward.argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, i64, i32, i32, i64, i32, vp, vp, vp, vp, vp,
+                                            i32, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.eqmp_edge_bias.argtypes = [vp, i64, vp, i32, vp, i32, vp, vp, vp]
+    lib.eqmp_edge_bias_backward.argtypes = [vp, vp, i64, i32, i32, vp, vp, i64, vp]
+    rows = [vp, i64, vp, i64, vp, i64]
+    lib.eqmp_edge_attention.argtypes = rows + [i32, i64, i64, i64, i32, i32, i32, vp, vp, vp, f32, vp, vp, vp, i64, vp]
+    lib.eqmp_edge_attention_backward.argtypes = [vp, i64] + rows + [i32, i64, i64, i64, i32, i32, i32, vp, vp, vp, vp, vp, i64,
+                                                                    vp, f32, vp, vp, vp, vp, vp, vp, i64, vp]
+    for name in ("head_norm", "edge_bias", "edge_attention"):
+        getattr(lib, "eqmp_" + name).restype = getattr(lib, f"eqmp_{name}_backward").restype = i32
+    lib.eqmp_head_norm_backward_workspace_size.argtypes = [i64, i32]
+    lib.eqmp_edge_bias_backward_workspace_size.argtypes = [i64, i32, i32]
+    lib.eqmp_edge_attention_workspace_size.argtypes = [i64, i32, i32]
+    lib.eqmp_edge_attention_backward_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32]
+    for name in ("head_norm_backward", "edge_bias_backward", "edge_attention", "edge_attention_backward"):
+        getattr(lib, f"eqmp_{name}_workspace_size").restype = i64
     _lib = lib
     return lib
 
@@ -641,7 +669,8 @@ def eqmp_fused_backward_noalloc(vec, x, row_offsets, src, dst, send_offsets, sen
 
 
 # ------------------------------------------------------------------ norms and dropout
-_OUT_NAMES = {k: f"out[{k!r}]" for k in ("y", "s", "stats", "x", "r", "w", "b")}
+_OUT_NAMES = {k: f"out[{k!r}]" for k in ("y", "s", "stats", "x", "r", "w", "b", "q", "k", "v", "wq", "wk", "pos", "rstd",
+                                               "bias", "bucket", "table", "out")}
 _L_MAX = {16: 3, 25: 4, 36: 5, 49: 6}  # components of a channel -> degree
 
 
@@ -884,3 +913,321 @@ def eqmp_layer_norm_backward_workspace_size(rows, cols):
 def eqmp_degree_norm_backward_workspace_size(n, channels, l_max):
     """Bytes of workspace that eqmp_degree_norm_backward needs for grad_w and grad_b."""
     return int(load_library().eqmp_degree_norm_backward_workspace_size(int(n), int(channels), int(l_max)))
+
+
+# ------------------------------------------------------------------ attention over a receiver's edges
+def _heads(t, name, dtype, shape, dev, torch):
+    """Checks a tensor [N, H, D] and returns its address and the distance between nodes.  A node's heads are packed; the
+    nodes may be any distance apart."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, name, dtype, shape, dev)
+    n, h, d = shape
+    if t.is_contiguous():
+        return t.data_ptr(), h * d
+    if (t.stride(2) == 1 or d == 1) and (t.stride(1) == d or h == 1):
+        return t.data_ptr(), t.stride(0) if n > 1 else h * d
+    raise ValueError(f"{name} must have contiguous heads")
+
+
+def _head_input(x, name, torch):
+    """Checks the type and the form of a main input [N, H, D]; returns the current device."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype is not torch.float32 and x.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} has dtype {x.dtype}")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dim() != 3 or x.shape[1] < 1 or x.shape[2] < 1:
+        raise ValueError(f"{name} must be [N, H, D] with H >= 1 and D >= 1")
+    return torch.cuda.current_device()
+
+
+def _workspace(workspace, nbytes, entry, like, dev, stream, torch):
+    """Address and size of a call's workspace: the caller's, or a temporary one."""
+    if nbytes < 0:
+        raise EqmpError(EQMP_ERR_UNSUPPORTED, entry)
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0, None
+        workspace = _empty(nbytes, torch.uint8, like.device, stream, temporary=True)
+        return workspace.data_ptr(), nbytes, workspace
+    _require(workspace, "workspace", torch.uint8)
+    if workspace.get_device() != dev:
+        raise ValueError("workspace must be a CUDA tensor on the current device")
+    return workspace.data_ptr(), workspace.numel(), workspace
+
+
+def _positions(pos, freq, n, d, dev, torch):
+    """Addresses of positions and frequencies and the number of axes; 0 axes without them."""
+    if pos is None and freq is None:
+        return None, None, 0
+    if pos is None or freq is None:
+        raise ValueError("give pos and freq together")
+    if not isinstance(pos, torch.Tensor) or pos.dim() != 2 or not 1 <= pos.shape[1] <= 3:
+        raise ValueError("pos must be a tensor [N, axes] with 1 to 3 axes")
+    if d % 2:
+        raise ValueError("a rotation needs an even head size")
+    axes, f32 = pos.shape[1], torch.float32
+    return _packed(pos, "pos", f32, (n, axes), dev, torch), _packed(freq, "freq", f32, (d // 2, axes), dev, torch), axes
+
+
+def eqmp_head_norm(q, k=None, wq=None, wk=None, eps=1e-6, pos=None, freq=None, need=None, out=None, stream=None):
+    """Norm of each head of the queries q [N, Hq, D] and keys k [N, Hk, D] (fp32 or bf16) by its root mean square, times
+    wq, wk (fp32 [D] or None), then the rotation of its pairs (2p, 2p+1) by the angles
+    theta[n, p] = sum_a pos[n, a] freq[p, a] (pos [N, axes], freq [D/2, axes], fp32; None: no rotation).
+
+    Returns a dict of what `need` names: "q", "k" (the default) and "rstd" ([N, Hq + Hk], for the backward pass).  `out`
+    may hold tensors to write into, by the same names.  q and k may be slices of one projection (packed heads, nodes any
+    distance apart)."""
+    import torch
+
+    f32 = torch.float32
+    dev = _head_input(q, "q", torch)
+    dtype, (n, hq, d) = q.dtype, q.shape
+    hk = 0
+    if k is not None:
+        _head_input(k, "k", torch)
+        hk = k.shape[1]
+    qp, q_ld = _heads(q, "q", dtype, q.shape, dev, torch)
+    kp, k_ld = (None, 0) if k is None else _heads(k, "k", dtype, (n, hk, d), dev, torch)
+    wqp = None if wq is None else _packed(wq, "wq", f32, (d,), dev, torch)
+    wkp = None if wk is None else _packed(wk, "wk", f32, (d,), dev, torch)
+    pp, fp, axes = _positions(pos, freq, n, d, dev, torch)
+    if need is None:
+        need = ("q",) if k is None else ("q", "k")
+    got, oq, ok, rp = {}, None, None, None
+    if "q" in need:
+        got["q"], oq = _result(out, "q", q, dtype, (n, hq, d), dev, torch, stream)
+    if "k" in need:
+        if k is None:
+            raise ValueError("need has 'k', and there are no keys")
+        got["k"], ok = _result(out, "k", q, dtype, (n, hk, d), dev, torch, stream)
+    if "rstd" in need:
+        got["rstd"], rp = _result(out, "rstd", q, f32, (n, hq + hk), dev, torch, stream)
+    if len(got) != len(need):
+        _unknown(need, ("q", "k", "rstd"))
+    status = load_library().eqmp_head_norm(qp, q_ld, hq, kp, k_ld, hk, EQMP_F32 if dtype is f32 else EQMP_BF16, n, d, wqp, wkp,
+                                           eps, pp, fp, axes, oq, ok, rp, _raw_stream(stream, dev, torch))
+    if status:
+        raise EqmpError(status, "eqmp_head_norm")
+    return got
+
+
+def eqmp_head_norm_backward(grad_q, grad_k, q, k, rstd, wq=None, wk=None, pos=None, freq=None, need=None, out=None,
+                            workspace=None, stream=None):
+    """Gradients of eqmp_head_norm from those of its results, its inputs and its rstd (grad_k and k None: queries alone).
+
+    Returns a dict of what `need` names: "q", "k", "wq", "wk" (the default, keys' where there are keys) and "pos"."""
+    import torch
+
+    f32 = torch.float32
+    dev = _head_input(q, "q", torch)
+    dtype, (n, hq, d) = q.dtype, q.shape
+    if (k is None) != (grad_k is None):
+        raise ValueError("give k and grad_k together")
+    hk = 0
+    if k is not None:
+        _head_input(k, "k", torch)
+        hk = k.shape[1]
+    qp, q_ld = _heads(q, "q", dtype, q.shape, dev, torch)
+    gqp, gq_ld = _heads(grad_q, "grad_q", dtype, q.shape, dev, torch)
+    kp, k_ld = (None, 0) if k is None else _heads(k, "k", dtype, (n, hk, d), dev, torch)
+    gkp, gk_ld = (None, 0) if k is None else _heads(grad_k, "grad_k", dtype, (n, hk, d), dev, torch)
+    wqp = None if wq is None else _packed(wq, "wq", f32, (d,), dev, torch)
+    wkp = None if wk is None else _packed(wk, "wk", f32, (d,), dev, torch)
+    rp = _packed(rstd, "rstd", f32, (n, hq + hk), dev, torch)
+    pp, fp, axes = _positions(pos, freq, n, d, dev, torch)
+    allowed = ("q", "wq") + (("k", "wk") if hk else ()) + (("pos",) if axes else ())
+    if need is None:
+        need = ("q", "k", "wq", "wk") if hk else ("q", "wq")
+    _unknown(need, allowed)
+    got, oq, ok, owq, owk, op = {}, None, None, None, None, None
+    if "q" in need:
+        got["q"], oq = _result(out, "q", q, dtype, (n, hq, d), dev, torch, stream)
+    if "k" in need:
+        got["k"], ok = _result(out, "k", q, dtype, (n, hk, d), dev, torch, stream)
+    if "wq" in need:
+        got["wq"], owq = _result(out, "wq", q, f32, (d,), dev, torch, stream)
+    if "wk" in need:
+        got["wk"], owk = _result(out, "wk", q, f32, (d,), dev, torch, stream)
+    if "pos" in need:
+        got["pos"], op = _result(out, "pos", q, f32, (n, axes), dev, torch, stream)
+    lib = load_library()
+    ws, nbytes, held = None, 0, None
+    if owq is not None or owk is not None:
+        ws, nbytes, held = _workspace(workspace, lib.eqmp_head_norm_backward_workspace_size(n, d), "eqmp_head_norm_backward", q,
+                                      dev, stream, torch)
+    status = lib.eqmp_head_norm_backward(gqp, gq_ld, gkp, gk_ld, qp, q_ld, hq, kp, k_ld, hk,
+                                         EQMP_F32 if dtype is f32 else EQMP_BF16, n, d, wqp, wkp, rp, pp, fp, axes, oq, ok, owq,
+                                         owk, op, ws, nbytes, _raw_stream(stream, dev, torch))
+    if status:
+        raise EqmpError(status, "eqmp_head_norm_backward")
+    return got
+
+
+def eqmp_head_norm_backward_workspace_size(n, head_size):
+    """Bytes of workspace that eqmp_head_norm_backward needs for the weights' gradients."""
+    return int(load_library().eqmp_head_norm_backward_workspace_size(int(n), int(head_size)))
+
+
+def eqmp_edge_bias(vec, borders, table, need=("bias", "bucket"), out=None, stream=None):
+    """The learned bias of each edge and head by the bucket of the edge's length: bucket[e] = the number of borders
+    [B-1] (fp32, ascending) that are at most |vec[e]| (vec [E, 3] fp32), bias[e] = table[bucket[e]] (table [B, H] fp32).
+
+    Returns a dict of what `need` names: "bias" [E, H] and "bucket" [E] int32 (for the backward pass).  `out` may hold
+    tensors to write into."""
+    import torch
+
+    f32 = torch.float32
+    for t, name in ((vec, "vec"), (table, "table")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    if vec.dim() != 2 or table.dim() != 2 or table.shape[0] < 1 or table.shape[1] < 1:
+        raise ValueError("vec must be [E, 3], table [B, H] with B, H >= 1")
+    dev = torch.cuda.current_device()
+    n, (b, h) = vec.shape[0], table.shape
+    vp = _packed(vec, "vec", f32, (n, 3), dev, torch)
+    tp = _packed(table, "table", f32, (b, h), dev, torch)
+    bp = _packed(borders, "borders", f32, (b - 1,), dev, torch)
+    got, op, kp = {}, None, None
+    if "bias" in need:
+        got["bias"], op = _result(out, "bias", vec, f32, (n, h), dev, torch, stream)
+    if "bucket" in need:
+        got["bucket"], kp = _result(out, "bucket", vec, torch.int32, (n,), dev, torch, stream)
+    if len(got) != len(need):
+        _unknown(need, ("bias", "bucket"))
+    status = load_library().eqmp_edge_bias(vp, n, bp, b, tp, h, op, kp, _raw_stream(stream, dev, torch))
+    if status:
+        raise EqmpError(status, "eqmp_edge_bias")
+    return got
+
+
+def eqmp_edge_bias_backward(grad_bias, bucket, n_buckets, out=None, workspace=None, stream=None):
+    """Gradient of eqmp_edge_bias's table, dict(table=[n_buckets, H]): the sums of grad_bias [E, H] (fp32) over the edges of
+    each bucket."""
+    import torch
+
+    f32 = torch.float32
+    if not isinstance(grad_bias, torch.Tensor):
+        raise TypeError("grad_bias must be a torch.Tensor")
+    if grad_bias.dim() != 2 or grad_bias.shape[1] < 1:
+        raise ValueError("grad_bias must be [E, H] with H >= 1")
+    if n_buckets < 1:
+        raise ValueError("n_buckets must be at least 1")
+    dev = torch.cuda.current_device()
+    n, h = grad_bias.shape
+    gp = _packed(grad_bias, "grad_bias", f32, (n, h), dev, torch)
+    kp = _packed(bucket, "bucket", torch.int32, (n,), dev, torch)
+    table, tp = _result(out, "table", grad_bias, f32, (n_buckets, h), dev, torch, stream)
+    lib = load_library()
+    ws, nbytes, held = _workspace(workspace, lib.eqmp_edge_bias_backward_workspace_size(n, n_buckets, h),
+                                  "eqmp_edge_bias_backward", grad_bias, dev, stream, torch)
+    status = lib.eqmp_edge_bias_backward(gp, kp, n, n_buckets, h, tp, ws, nbytes, _raw_stream(stream, dev, torch))
+    if status:
+        raise EqmpError(status, "eqmp_edge_bias_backward")
+    return dict(table=table)
+
+
+def eqmp_edge_bias_backward_workspace_size(n_edges, n_buckets, heads):
+    """Bytes of workspace that eqmp_edge_bias_backward needs."""
+    return int(load_library().eqmp_edge_bias_backward_workspace_size(int(n_edges), int(n_buckets), int(heads)))
+
+
+def _attention_inputs(q, k, v, row_offsets, src, bias, torch):
+    """Checks of what both passes of the attention take; the sizes and the arguments in the order of the C call."""
+    f32, i32 = torch.float32, torch.int32
+    dev = _head_input(q, "q", torch)
+    _head_input(k, "k", torch)
+    _head_input(v, "v", torch)
+    dtype, (n, h, d), n_src, dv = q.dtype, q.shape, k.shape[0], v.shape[2]
+    qp, q_ld = _heads(q, "q", dtype, (n, h, d), dev, torch)
+    kp, k_ld = _heads(k, "k", dtype, (n_src, h, d), dev, torch)
+    vp, v_ld = _heads(v, "v", dtype, (n_src, h, dv), dev, torch)
+    op = _packed(row_offsets, "row_offsets", i32, (n + 1,), dev, torch)
+    if not isinstance(src, torch.Tensor) or src.dim() != 1:
+        raise ValueError("src must be a tensor [E]")
+    e = src.shape[0]
+    sp = _packed(src, "src", i32, (e,), dev, torch)
+    bp = None if bias is None else _packed(bias, "bias", f32, (e, h), dev, torch)
+    rows = (qp, q_ld, kp, k_ld, vp, v_ld, EQMP_F32 if dtype is f32 else EQMP_BF16, n, n_src, e, h, d, dv, op, sp)
+    return dev, dtype, (n, n_src, e, h, d, dv), rows, bp
+
+
+def eqmp_edge_attention(q, k, v, row_offsets, src, bias=None, scale=None, need=("out",), out=None, workspace=None, stream=None):
+    """Attention over a receiver's edges: softmax over the edges e of receiver i of scale q[i].k[src[e]] + bias[e], and the
+    sum of v[src[e]] by it, for each head.  q [N, H, D], k [N_src, H, D], v [N_src, H, Dv] (fp32 or bf16, one type; packed
+    heads, nodes any distance apart), bias [E, H] fp32 or None, scale 1 / sqrt(D) by default.  v may be node features
+    [N_src, C, K] as features.view(N_src, H, C // H * K).
+
+    An edge whose bias is -inf is left out; a receiver without an edge gets zeros.  Returns a dict of what `need` names:
+    "out" [N, H, Dv] and "stats" ([N, H, 2], for the backward pass).  `out` may hold tensors to write into."""
+    import torch
+
+    dev, dtype, (n, n_src, e, h, d, dv), rows, bp = _attention_inputs(q, k, v, row_offsets, src, bias, torch)
+    got, op, tp = {}, None, None
+    if "out" in need:
+        got["out"], op = _result(out, "out", q, dtype, (n, h, dv), dev, torch, stream)
+    if "stats" in need:
+        got["stats"], tp = _result(out, "stats", q, torch.float32, (n, h, 2), dev, torch, stream)
+    if len(got) != len(need):
+        _unknown(need, ("out", "stats"))
+    lib = load_library()
+    ws, nbytes, held = _workspace(workspace, lib.eqmp_edge_attention_workspace_size(e, h, dv), "eqmp_edge_attention", q, dev,
+                                  stream, torch)
+    status = lib.eqmp_edge_attention(*rows, bp, d ** -0.5 if scale is None else scale, op, tp, ws, nbytes,
+                                     _raw_stream(stream, dev, torch))
+    if status:
+        raise EqmpError(status, "eqmp_edge_attention")
+    return got
+
+
+def eqmp_edge_attention_backward(grad_out, q, k, v, stats, row_offsets, src, dst, send_offsets, send_edges, bias=None,
+                                 scale=None, need=("q", "k", "v"), out=None, workspace=None, stream=None):
+    """Gradients of eqmp_edge_attention from grad_out [N, H, Dv], the forward call's inputs and its stats.  dst, send_offsets
+    and send_edges: the sender view of the edges, as eqmp_fused_backward (None where neither "k" nor "v" is asked for).
+
+    Returns a dict of what `need` names: "q", "k", "v" and "bias" ([E, H])."""
+    import torch
+
+    f32, i32 = torch.float32, torch.int32
+    dev, dtype, (n, n_src, e, h, d, dv), rows, bp = _attention_inputs(q, k, v, row_offsets, src, bias, torch)
+    gp, g_ld = _heads(grad_out, "grad_out", dtype, (n, h, dv), dev, torch)
+    tp = _packed(stats, "stats", f32, (n, h, 2), dev, torch)
+    dp, sop, sep, e_send = None, None, None, 0
+    if "k" in need or "v" in need:
+        if not isinstance(send_edges, torch.Tensor) or send_edges.dim() != 1:
+            raise ValueError("send_edges must be a tensor [E_send]")
+        e_send = send_edges.shape[0]
+        dp = _packed(dst, "dst", i32, (e,), dev, torch)
+        sop = _packed(send_offsets, "send_offsets", i32, (n_src + 1,), dev, torch)
+        sep = _packed(send_edges, "send_edges", i32, (e_send,), dev, torch)
+    got, gq, gk, gv, gb = {}, None, None, None, None
+    if "q" in need:
+        got["q"], gq = _result(out, "q", q, dtype, (n, h, d), dev, torch, stream)
+    if "k" in need:
+        got["k"], gk = _result(out, "k", q, dtype, (n_src, h, d), dev, torch, stream)
+    if "v" in need:
+        got["v"], gv = _result(out, "v", q, dtype, (n_src, h, dv), dev, torch, stream)
+    if "bias" in need:
+        got["bias"], gb = _result(out, "bias", q, f32, (e, h), dev, torch, stream)
+    if len(got) != len(need):
+        _unknown(need, ("q", "k", "v", "bias"))
+    lib = load_library()
+    ws, nbytes, held = _workspace(workspace, lib.eqmp_edge_attention_backward_workspace_size(n, e, e_send, h, d, dv),
+                                  "eqmp_edge_attention_backward", q, dev, stream, torch)
+    status = lib.eqmp_edge_attention_backward(gp, g_ld, *rows, dp, sop, sep, e_send, bp, d ** -0.5 if scale is None else scale, tp,
+                                              gq, gk, gv, gb, ws, nbytes, _raw_stream(stream, dev, torch))
+    if status:
+        raise EqmpError(status, "eqmp_edge_attention_backward")
+    return got
+
+
+def eqmp_edge_attention_workspace_size(n_edges, heads, value_size):
+    """Bytes of workspace that eqmp_edge_attention needs (0: none)."""
+    return int(load_library().eqmp_edge_attention_workspace_size(int(n_edges), int(heads), int(value_size)))
+
+
+def eqmp_edge_attention_backward_workspace_size(n, n_edges, n_send_edges, heads, head_size, value_size):
+    """Bytes of workspace that eqmp_edge_attention_backward needs."""
+    return int(load_library().eqmp_edge_attention_backward_workspace_size(int(n), int(n_edges), int(n_send_edges), int(heads),
+                                                                           int(head_size), int(value_size)))

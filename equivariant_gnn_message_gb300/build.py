@@ -18,7 +18,9 @@ BUILD = os.path.join(HERE, "_build")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(BUILD, "libeqmp.so")
 UNITS = ["abi.cu", "shared_f32.cu", "shared_bf16.cu", "radial.cu", "bwd.cu", "so2.cu", "graph.cu", "shared_dx.cu", "hl.cu",
-         "norm.cu", "norm_fwd_f32.cu", "norm_fwd_bf16.cu", "norm_bwd_f32.cu", "norm_bwd_bf16.cu"]
+         "norm.cu", "norm_fwd_f32.cu", "norm_fwd_bf16.cu", "norm_bwd_f32.cu", "norm_bwd_bf16.cu",
+         "head_norm.cu", "edge_bias.cu", "attn.cu", "attn_fwd_f32.cu", "attn_fwd_bf16.cu", "attn_recv_f32.cu",
+         "attn_recv_bf16.cu", "attn_send_f32.cu", "attn_send_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

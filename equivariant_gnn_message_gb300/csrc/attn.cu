@@ -1,0 +1,208 @@
+// Entry points of the attention over a receiver's edges: argument checks and
+// the choice of the kernels' forms.  Contracts are in include/eqmp.h.
+#include <math.h>
+
+#include "attn_launch.cuh"
+#include "host_args.h"
+
+namespace eqmp {
+
+constexpr int kMaxDim = 256, kMaxValueDim = 1024, kMaxHeads = 1024;
+constexpr int64_t kMaxCount = 1ll << 30;  // nodes and edges: an index plus a stride of the launch stays an int
+
+// dbias alone, where no sender's gradient is asked for.
+__global__ void __launch_bounds__(256) k_attn_bias(AttnArgs a) {
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= a.N) return;
+  const int e0 = clamped(__ldg(a.off + row), a.E), e1 = clamped(__ldg(a.off + row + 1), a.E);
+  const long long end = (long long)e1 * a.H;
+  for (long long i = (long long)e0 * a.H + lane; i < end; i += 32) {
+    const float2 pd = a.pd[i];
+    a.gbias[i] = pd.x < 0.0f ? 0.0f : pd.x * (pd.y - a.delta[(long long)row * a.H + i % a.H]);
+  }
+}
+
+struct Sizes {
+  int64_t N, Ns, E;
+  int32_t H, D, Dv;
+};
+
+static eqmp_status check_sizes(const Sizes& n, eqmp_dtype dtype, float scale) {
+  if (n.N < 0 || n.Ns < 0 || n.E < 0 || n.H < 1 || n.D < 1 || n.Dv < 1) return EQMP_ERR_INVALID_ARG;
+  if (dtype != EQMP_F32 && dtype != EQMP_BF16) return EQMP_ERR_INVALID_ARG;
+  if (!isfinite(scale)) return EQMP_ERR_INVALID_ARG;
+  const bool fits = n.N <= kMaxCount && n.Ns <= kMaxCount && n.E <= kMaxCount && n.H <= kMaxHeads && n.D <= kMaxDim &&
+                    n.Dv <= kMaxValueDim;
+  return fits ? EQMP_OK : EQMP_ERR_UNSUPPORTED;
+}
+
+// Blocks that rows of more than two are cut into: at least 128 edges, at most
+// 2048 blocks in all, so that the parts stay a few MB.
+static void cut(int64_t E, int* block, int* blocks) {
+  const int64_t want = (E + 2047) / 2048;
+  *block = (int)(want < 128 ? 128 : (want + 127) / 128 * 128);
+  *blocks = E > 2 * *block ? (int)((E + *block - 1) / *block) : 0;
+}
+
+static int64_t part_bytes(int64_t E, int64_t H, int64_t width) {
+  int block, blocks;
+  cut(E, &block, &blocks);
+  return 2ll * blocks * H * width * 4;
+}
+
+static int64_t forward_workspace(const Sizes& n) { return part_bytes(n.E, n.H, n.Dv + 2); }
+
+struct BackwardSpace {
+  int64_t pd, delta, part;
+  int64_t total() const { return pd + delta + part; }
+};
+
+static BackwardSpace backward_workspace(const Sizes& n, int64_t E_send) {
+  const int64_t recv = part_bytes(n.E, n.H, 2 * n.D + 1), send = part_bytes(E_send, n.H, n.D + n.Dv);
+  return BackwardSpace{n.E * n.H * 8 + 15 & ~15ll, n.N * n.H * 4 + 15 & ~15ll, recv > send ? recv : send};
+}
+
+// 16-byte vectors where every head of every row begins on 16 bytes, else single
+// values.  The fewest lanes a head whose registers hold it; more of them where
+// there are too few rows to fill the device.
+static AttnForm form_of(const Sizes& n, int64_t rows, int bytes, bool vectors) {
+  AttnForm f;
+  f.V = vectors ? 16 / bytes : 1;
+  const int k = (n.D + f.V - 1) / f.V, v = (n.Dv + f.V - 1) / f.V;
+  auto fits = [&](int G) {
+    const int most_k = vectors ? 2 : G == 8 ? 4 : 8, most_v = vectors ? 32 / f.V : G == 8 ? 16 : 32;
+    return (k + G - 1) / G <= most_k && (v + G - 1) / G <= most_v;
+  };
+  f.G = 8;
+  while (f.G < 32 && (!fits(f.G) || n.H * f.G * 2 <= 32 || rows * ((n.H * f.G + 31) / 32) < 152 * 16)) f.G *= vectors ? 2 : 4;
+  f.KN = (k + f.G - 1) / f.G;
+  f.VN = (v + f.G - 1) / f.G;
+  return f;
+}
+
+static bool on16(const void* p, long long ld, int bytes) { return aligned(p, 16) && ld * bytes % 16 == 0; }
+
+}  // namespace eqmp
+
+using namespace eqmp;
+
+extern "C" {
+
+int64_t eqmp_edge_attention_workspace_size(int64_t E, int32_t H, int32_t Dv) {
+  const Sizes n{0, 0, E, H, 1, Dv};
+  return check_sizes(n, EQMP_F32, 1.0f) == EQMP_OK ? forward_workspace(n) : -1;
+}
+
+eqmp_status eqmp_edge_attention(const void* q, int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
+                                eqmp_dtype dtype, int64_t N, int64_t N_src, int64_t E, int32_t H, int32_t D, int32_t Dv,
+                                const int32_t* row_offsets, const int32_t* src, const float* bias, float scale,
+                                void* out, float* stats, void* workspace, int64_t workspace_bytes, eqmp_stream_t stream) {
+  const Sizes n{N, N_src, E, H, D, Dv};
+  const eqmp_status zs = check_sizes(n, dtype, scale);
+  if (zs != EQMP_OK) return zs;
+  if (N == 0 || (!out && !stats)) return EQMP_OK;
+  const int bytes = dtype == EQMP_BF16 ? 2 : 4;
+  const Plane in[] = {{q, q_ld}, {k, k_ld}, {v, v_ld}};
+  void* const outs[] = {out};
+  if (!q || !row_offsets || (E > 0 && (!src || (N_src > 0 && (!k || !v))))) return EQMP_ERR_INVALID_ARG;
+  if (!planes_ok(in, 3, outs, 1, bytes) || !aligned(row_offsets, 4) || !aligned(src, 4) || !aligned(bias, 4) ||
+      !aligned(stats, 4))
+    return EQMP_ERR_INVALID_ARG;
+  const int64_t ws = forward_workspace(n);
+  if (ws > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < ws)) return EQMP_ERR_INVALID_ARG;
+  const int64_t HD = (int64_t)H * D, HV = (int64_t)H * Dv;
+  const Span reads[] = {span(in[0], N, HD, bytes), span(in[1], N_src, HD, bytes), span(in[2], N_src, HV, bytes),
+                        span(row_offsets, (N + 1) * 4), span(src, E * 4), span(bias, E * H * 4)};
+  const Span writes[] = {span(out, N * HV * bytes), span(stats, N * H * 8), span(workspace, ws)};
+  if (!outputs_apart(reads, writes)) return EQMP_ERR_INVALID_ARG;
+  AttnArgs a{};
+  a.q = q, a.q_ld = q_ld, a.k = k, a.k_ld = k_ld, a.v = v, a.v_ld = v_ld;
+  a.bias = bias, a.off = row_offsets, a.src = src;
+  a.out = out, a.stats = stats, a.part = static_cast<float*>(workspace);
+  a.scale = scale;
+  a.N = (int)N, a.Ns = (int)N_src, a.E = (int)E, a.H = H, a.D = D, a.Dv = Dv;
+  cut(E, &a.block, &a.blocks);
+  const bool vectors = on16(q, q_ld, bytes) && on16(k, k_ld, bytes) && on16(v, v_ld, bytes) && aligned(out, 16) &&
+                       D * bytes % 16 == 0 && Dv * bytes % 16 == 0;
+  const AttnForm f = form_of(n, N, bytes, vectors);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return dtype == EQMP_BF16 ? launch_attn_fwd_bf16(a, f, st) : launch_attn_fwd_f32(a, f, st);
+}
+
+int64_t eqmp_edge_attention_backward_workspace_size(int64_t N, int64_t E, int64_t E_send, int32_t H, int32_t D, int32_t Dv) {
+  const Sizes n{N, 0, E, H, D, Dv};
+  if (check_sizes(n, EQMP_F32, 1.0f) != EQMP_OK || E_send < 0 || E_send > kMaxCount) return -1;
+  return backward_workspace(n, E_send).total();
+}
+
+eqmp_status eqmp_edge_attention_backward(const void* grad_out, int64_t grad_out_ld, const void* q, int64_t q_ld,
+                                         const void* k, int64_t k_ld, const void* v, int64_t v_ld, eqmp_dtype dtype,
+                                         int64_t N, int64_t N_src, int64_t E, int32_t H, int32_t D, int32_t Dv,
+                                         const int32_t* row_offsets, const int32_t* src, const int32_t* dst,
+                                         const int32_t* send_offsets, const int32_t* send_edges, int64_t E_send,
+                                         const float* bias, float scale, const float* stats, void* grad_q, void* grad_k,
+                                         void* grad_v, float* grad_bias, void* workspace, int64_t workspace_bytes,
+                                         eqmp_stream_t stream) {
+  const Sizes n{N, N_src, E, H, D, Dv};
+  const eqmp_status zs = check_sizes(n, dtype, scale);
+  if (zs != EQMP_OK) return zs;
+  if (E_send < 0) return EQMP_ERR_INVALID_ARG;
+  if (E_send > kMaxCount) return EQMP_ERR_UNSUPPORTED;
+  const bool send = (grad_k || grad_v) && N_src > 0;
+  if (!grad_q && !send && !grad_bias) return EQMP_OK;
+  const int bytes = dtype == EQMP_BF16 ? 2 : 4;
+  const Plane in[] = {{q, q_ld}, {k, k_ld}, {v, v_ld}, {grad_out, grad_out_ld}};
+  void* const outs[] = {grad_q, grad_k, grad_v};
+  if (N > 0 && (!q || !grad_out || !stats || !row_offsets)) return EQMP_ERR_INVALID_ARG;
+  if (N > 0 && E > 0 && (!src || (N_src > 0 && (!k || !v)))) return EQMP_ERR_INVALID_ARG;
+  if (send && (!send_offsets || (E_send > 0 && (!send_edges || (E > 0 && !dst))))) return EQMP_ERR_INVALID_ARG;
+  if (!planes_ok(in, 4, outs, 3, bytes)) return EQMP_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)row_offsets, (const void*)src, (const void*)dst, (const void*)send_offsets,
+                        (const void*)send_edges, (const void*)bias, (const void*)stats, (const void*)grad_bias})
+    if (!aligned(p, 4)) return EQMP_ERR_INVALID_ARG;
+  const BackwardSpace ws = backward_workspace(n, E_send);
+  if (ws.total() > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < ws.total())) return EQMP_ERR_INVALID_ARG;
+  const int64_t HD = (int64_t)H * D, HV = (int64_t)H * Dv;
+  const Span reads[] = {span(in[0], N, HD, bytes), span(in[1], N_src, HD, bytes), span(in[2], N_src, HV, bytes),
+                        span(in[3], N, HV, bytes), span(row_offsets, (N + 1) * 4), span(src, E * 4), span(dst, E * 4),
+                        span(send_offsets, (N_src + 1) * 4), span(send_edges, E_send * 4), span(bias, E * H * 4),
+                        span(stats, N * H * 8)};
+  const Span writes[] = {span(grad_q, N * HD * bytes), span(grad_k, N_src * HD * bytes), span(grad_v, N_src * HV * bytes),
+                         span(grad_bias, E * H * 4), span(workspace, ws.total())};
+  if (!outputs_apart(reads, writes)) return EQMP_ERR_INVALID_ARG;
+  char* const space = static_cast<char*>(workspace);
+  AttnArgs a{};
+  a.q = q, a.q_ld = q_ld, a.k = k, a.k_ld = k_ld, a.v = v, a.v_ld = v_ld, a.g = grad_out, a.g_ld = grad_out_ld;
+  a.bias = bias, a.off = row_offsets, a.src = src, a.dst = dst, a.send_off = send_offsets, a.send_edges = send_edges;
+  a.stats = const_cast<float*>(stats);
+  a.gq = grad_q, a.gk = grad_k, a.gv = grad_v, a.gbias = grad_bias;
+  a.delta = reinterpret_cast<float*>(space + ws.pd);
+  a.part = reinterpret_cast<float*>(space + ws.pd + ws.delta);
+  a.scale = scale;
+  a.N = (int)N, a.Ns = (int)N_src, a.E = (int)E, a.E_send = (int)E_send, a.H = H, a.D = D, a.Dv = Dv;
+  a.pd = send || grad_bias ? reinterpret_cast<float2*>(space) : nullptr;
+  const bool vectors = on16(q, q_ld, bytes) && on16(k, k_ld, bytes) && on16(v, v_ld, bytes) && on16(grad_out, grad_out_ld, bytes) &&
+                       aligned(grad_q, 16) && aligned(grad_k, 16) && aligned(grad_v, 16) && D * bytes % 16 == 0 &&
+                       Dv * bytes % 16 == 0;
+  const bool bf16 = dtype == EQMP_BF16;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // the bias of edges that no pass below reaches
+  if (grad_bias && E > 0 && (!send || E_send != E) && cudaMemsetAsync(grad_bias, 0, (size_t)E * H * 4, st) != cudaSuccess)
+    return EQMP_ERR_CUDA;
+  if (N > 0) {
+    cut(E, &a.block, &a.blocks);
+    const AttnForm f = form_of(n, N, bytes, vectors);
+    const eqmp_status s = bf16 ? launch_attn_recv_bf16(a, f, st) : launch_attn_recv_f32(a, f, st);
+    if (s != EQMP_OK) return s;
+  }
+  if (send) {
+    cut(E_send, &a.block, &a.blocks);
+    const AttnForm f = form_of(n, N_src, bytes, vectors);
+    return bf16 ? launch_attn_send_bf16(a, f, st) : launch_attn_send_f32(a, f, st);
+  }
+  if (!grad_bias || N == 0) return EQMP_OK;
+  k_attn_bias<<<(unsigned)((N + 7) / 8), 256, 0, st>>>(a);
+  return cuda_status(cudaGetLastError());
+}
+
+}  // extern "C"

@@ -1,0 +1,76 @@
+// Which form of the attention kernels a call gets, and their launches.
+#pragma once
+
+#include "attn.cuh"
+#include "launch.h"
+
+namespace eqmp {
+
+enum { kAttnFwd, kAttnRecv, kAttnSend };
+
+// A form: V elements a vector, G lanes a head, up to KN vectors of a key and VN
+// of a value a lane.
+struct AttnForm {
+  int V, G, KN, VN;
+};
+
+// One launcher for each pass and type (attn_*.cu).
+#define EQMP_ATTN_LAUNCHER(name) eqmp_status name(const AttnArgs& a, const AttnForm& f, cudaStream_t st)
+EQMP_ATTN_LAUNCHER(launch_attn_fwd_f32);
+EQMP_ATTN_LAUNCHER(launch_attn_fwd_bf16);
+EQMP_ATTN_LAUNCHER(launch_attn_recv_f32);
+EQMP_ATTN_LAUNCHER(launch_attn_recv_bf16);
+EQMP_ATTN_LAUNCHER(launch_attn_send_f32);
+EQMP_ATTN_LAUNCHER(launch_attn_send_bf16);
+
+template <int PASS, typename T, int V, int G, int KN, int VN>
+eqmp_status launch_attn_form(const AttnArgs& a, cudaStream_t st) {
+  constexpr int VALUES = VN * V, U = VALUES <= 16 ? 4 : VALUES <= 32 ? 2 : 1;
+  const int rows = PASS == kAttnSend ? a.Ns : a.N;
+  const dim3 grid((unsigned)((rows + a.blocks + kAttnWarps - 1) / kAttnWarps), (unsigned)((a.H * G + 31) / 32));
+  if constexpr (PASS == kAttnFwd)
+    k_attn_fwd<T, V, G, KN, VN, U><<<grid, 32 * kAttnWarps, 0, st>>>(a);
+  else if constexpr (PASS == kAttnRecv)
+    k_attn_bwd_recv<T, V, G, KN, VN, U><<<grid, 32 * kAttnWarps, 0, st>>>(a);
+  else
+    k_attn_bwd_send<T, V, G, KN, VN, U><<<grid, 32 * kAttnWarps, 0, st>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return EQMP_ERR_CUDA;
+  if (!a.blocks) return EQMP_OK;
+  // the parts of long rows: launched while the pass before it runs, and over at once where there are none
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.blocks, (unsigned)a.H);
+  cfg.blockDim = dim3(kJoinX, kJoinY);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  constexpr int MODE = PASS == kAttnFwd ? kJoinFwd : PASS == kAttnRecv ? kJoinRecv : kJoinSend;
+  return cuda_status(cudaLaunchKernelEx(&cfg, k_attn_join<MODE, T>, a));
+}
+
+template <int PASS, typename T, int V, int G>
+eqmp_status launch_attn_lanes(const AttnArgs& a, const AttnForm& f, cudaStream_t st) {
+  if (f.KN <= 1 && f.VN <= 1) return launch_attn_form<PASS, T, V, G, 1, 1>(a, st);
+  if (f.KN <= 1 && f.VN <= 2) return launch_attn_form<PASS, T, V, G, 1, 2>(a, st);
+  if (f.KN <= 1 && f.VN <= 4) return launch_attn_form<PASS, T, V, G, 1, 4>(a, st);
+  if (f.VN <= 2) return launch_attn_form<PASS, T, V, G, 2, 2>(a, st);
+  if (f.VN <= 4) return launch_attn_form<PASS, T, V, G, 2, 4>(a, st);
+  return launch_attn_form<PASS, T, V, G, 2, 8>(a, st);
+}
+
+template <int PASS, typename T>
+eqmp_status launch_attn(const AttnArgs& a, const AttnForm& f, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  if (f.V == V) {
+    if (f.G == 8) return launch_attn_lanes<PASS, T, V, 8>(a, f, st);
+    if (f.G == 16) return launch_attn_lanes<PASS, T, V, 16>(a, f, st);
+    return launch_attn_lanes<PASS, T, V, 32>(a, f, st);
+  }
+  if (f.G == 8) return launch_attn_form<PASS, T, 1, 8, 4, 16>(a, st);
+  if (f.KN <= 2 && f.VN <= 8) return launch_attn_form<PASS, T, 1, 32, 2, 8>(a, st);
+  return launch_attn_form<PASS, T, 1, 32, 8, 32>(a, st);
+}
+
+}  // namespace eqmp

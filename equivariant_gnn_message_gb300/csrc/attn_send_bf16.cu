@@ -1,0 +1,5 @@
+#include "attn_launch.cuh"
+
+namespace eqmp {
+EQMP_ATTN_LAUNCHER(launch_attn_send_bf16) { return launch_attn<kAttnSend, __nv_bfloat16>(a, f, st); }
+}  // namespace eqmp

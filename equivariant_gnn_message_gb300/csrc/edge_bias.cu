@@ -1,0 +1,213 @@
+// A learned bias of each edge and head by the bucket of the edge's length, and
+// the gradient of its table (sm_103a).  Contracts are in include/eqmp.h.
+//
+//   bucket[e] = #{b : borders[b] <= |vec_e|},  bias[e][h] = table[bucket[e]][h]
+//   dtable[b][h] = sum of dbias[e][h] over the edges of bucket b
+#include <cuda_runtime.h>
+
+#include "host_args.h"
+#include "launch.h"
+
+namespace eqmp {
+
+constexpr int kMaxBuckets = 1024, kMaxBiasHeads = 256;
+constexpr int64_t kMaxEdges = 1ll << 30;
+
+struct BiasArgs {
+  const float *vec, *borders, *table;
+  float* bias;
+  int* bucket;
+  const float* grad;
+  float* gtable;
+  float* part;  // [parts][B][H]
+  int E, B, H, parts;
+};
+
+// ---------------------------------------------------------------- forward
+constexpr int kBiasThreads = 256, kBiasEdges = 512;  // edges of a CTA's tile
+constexpr int kTableFloats = 8192;                   // a larger table is read through L1
+
+// Squares of fp32 values are exact in 64 bits, so that a length next to a border
+// is decided by one rounding of the sum of three, and the same everywhere.
+__device__ __forceinline__ int bucket_of(const float* vec, const float* borders, int n) {
+  const double x = vec[0], y = vec[1], z = vec[2];
+  const double d = __dadd_rn(__dadd_rn(x * x, y * y), z * z);
+  int lo = 0, len = n;  // borders[0..lo) <= |vec|
+  while (len > 0) {
+    const int half = len / 2;
+    const double b = borders[lo + half];
+    if (b * b <= d) {
+      lo += half + 1;
+      len -= half + 1;
+    } else {
+      len = half;
+    }
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kBiasThreads) k_edge_bias(BiasArgs a) {
+  extern __shared__ float shared[];  // borders, then the table where it fits
+  __shared__ int at[kBiasEdges];
+  const bool fits = a.B * a.H <= kTableFloats;
+  float* const table = shared + (a.B - 1 + 3) / 4 * 4;
+  for (int i = threadIdx.x; i < a.B - 1; i += blockDim.x) shared[i] = a.borders[i];
+  if (fits && a.bias)
+    for (int i = threadIdx.x; i < a.B * a.H; i += blockDim.x) table[i] = a.table[i];
+  const float* const from = fits ? table : a.table;
+  for (long long e0 = (long long)blockIdx.x * kBiasEdges; e0 < a.E; e0 += (long long)gridDim.x * kBiasEdges) {
+    const int n = a.E - e0 < kBiasEdges ? (int)(a.E - e0) : kBiasEdges;
+    __syncthreads();  // borders are here; the last tile's buckets have been read
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      const int b = bucket_of(a.vec + 3 * (e0 + i), shared, a.B - 1);
+      at[i] = b;
+      if (a.bucket) a.bucket[e0 + i] = b;
+    }
+    __syncthreads();
+    if (!a.bias) continue;
+    float* out = a.bias + e0 * a.H;
+    for (int i = threadIdx.x; i < n * a.H; i += blockDim.x) out[i] = from[at[i / a.H] * a.H + i % a.H];
+  }
+}
+
+// ---------------------------------------------------------------- backward
+// A CTA sums a range of edges into copies of the table in shared memory: thread
+// (r, h) alone adds to column h of copy r, so the order is fixed and nothing is
+// atomic.  Then the copies are added, and k_edge_bias_sum adds the CTAs' parts.
+constexpr int kGradThreads = 256;
+constexpr int kCopyFloats = 20480;  // of the copies of a CTA
+
+__global__ void __launch_bounds__(kGradThreads) k_edge_bias_bwd(BiasArgs a, int heads, int copies) {
+  extern __shared__ float copy[];  // [copies][B][heads]
+  const int h0 = blockIdx.y * heads, hn = min(heads, a.H - h0), size = a.B * heads;
+  for (int i = threadIdx.x; i < copies * size; i += blockDim.x) copy[i] = 0.0f;
+  __syncthreads();
+  const int h = threadIdx.x % heads, r = threadIdx.x / heads;
+  const int begin = (int)((long long)a.E * blockIdx.x / a.parts), end = (int)((long long)a.E * (blockIdx.x + 1) / a.parts);
+  if (r < copies && h < hn) {
+    float* mine = copy + r * size + h;
+    for (int e = begin + r; e < end; e += copies) {
+      const int b = __ldg(a.bucket + e);
+      if ((unsigned)b < (unsigned)a.B) mine[b * heads] += a.grad[(long long)e * a.H + h0 + h];
+    }
+  }
+  __syncthreads();
+  float* out = a.parts > 1 ? a.part + (long long)blockIdx.x * a.B * a.H : a.gtable;
+  for (int i = threadIdx.x; i < a.B * hn; i += blockDim.x) {
+    const int at = i / hn * heads + i % hn;
+    float t = 0.0f;
+    for (int c = 0; c < copies; ++c) t += copy[c * size + at];
+    out[(long long)(i / hn) * a.H + h0 + i % hn] = t;
+  }
+}
+
+constexpr int kBiasSumX = 32, kBiasSumY = 16;
+
+__global__ void __launch_bounds__(kBiasSumX * kBiasSumY) k_edge_bias_sum(BiasArgs a) {
+  __shared__ float red[kBiasSumY][kBiasSumX];
+  const int i = blockIdx.x * kBiasSumX + threadIdx.x, n = a.B * a.H;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // until the kernel that writes the parts is done
+  float t = 0.0f;
+  if (i < n)
+    for (int p = threadIdx.y; p < a.parts; p += kBiasSumY) t += a.part[(long long)p * n + i];
+  red[threadIdx.y][threadIdx.x] = t;
+  __syncthreads();
+  if (threadIdx.y || i >= n) return;
+#pragma unroll
+  for (int y = 1; y < kBiasSumY; ++y) t += red[y][threadIdx.x];
+  a.gtable[i] = t;
+}
+
+// CTAs of the backward pass: two on each of 152 SMs, at least 1024 edges each,
+// and no more than 64 MB of parts.
+static int grad_parts(int64_t E, int64_t B, int64_t H) {
+  int64_t n = (E + 1023) / 1024;
+  const int64_t most = (16ll << 20) / (B * H);
+  if (n > 304) n = 304;
+  if (n > most) n = most;
+  return n < 1 ? 1 : (int)n;
+}
+
+static eqmp_status check(int64_t E, int32_t B, int32_t H) {
+  if (E < 0 || B < 1 || H < 1) return EQMP_ERR_INVALID_ARG;
+  return E > kMaxEdges || B > kMaxBuckets || H > kMaxBiasHeads ? EQMP_ERR_UNSUPPORTED : EQMP_OK;
+}
+
+static int64_t grad_workspace(int64_t E, int64_t B, int64_t H) {
+  const int parts = grad_parts(E, B, H);
+  return parts > 1 ? parts * B * H * 4 : 0;
+}
+
+}  // namespace eqmp
+
+using namespace eqmp;
+
+extern "C" {
+
+eqmp_status eqmp_edge_bias(const float* vec, int64_t E, const float* borders, int32_t B, const float* table, int32_t H,
+                           float* bias, int32_t* bucket, eqmp_stream_t stream) {
+  const eqmp_status cs = check(E, B, H);
+  if (cs != EQMP_OK) return cs;
+  if (E == 0 || (!bias && !bucket)) return EQMP_OK;
+  if (!vec || (B > 1 && !borders) || (bias && !table)) return EQMP_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)vec, (const void*)borders, (const void*)table, (const void*)bias, (const void*)bucket})
+    if (!aligned(p, 4)) return EQMP_ERR_INVALID_ARG;
+  const Span reads[] = {span(vec, E * 12), span(borders, (B - 1) * 4), span(table, bias ? (int64_t)B * H * 4 : 0)};
+  const Span writes[] = {span(bias, E * H * 4), span(bucket, E * 4)};
+  if (!outputs_apart(reads, writes)) return EQMP_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  const eqmp_status ds = device_info(&dev);
+  if (ds != EQMP_OK) return ds;
+  BiasArgs a{};
+  a.vec = vec, a.borders = borders, a.table = table, a.bias = bias, a.bucket = bucket;
+  a.E = (int)E, a.B = B, a.H = H;
+  const int64_t tiles = (E + kBiasEdges - 1) / kBiasEdges, most = (int64_t)dev.sms * 8;
+  const int smem = ((B - 1 + 3) / 4 * 4 + (B * H <= kTableFloats ? B * H : 0)) * 4;
+  k_edge_bias<<<(unsigned)(tiles < most ? tiles : most), kBiasThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  return cuda_status(cudaGetLastError());
+}
+
+int64_t eqmp_edge_bias_backward_workspace_size(int64_t E, int32_t B, int32_t H) {
+  return check(E, B, H) == EQMP_OK ? grad_workspace(E, B, H) : -1;
+}
+
+eqmp_status eqmp_edge_bias_backward(const float* grad_bias, const int32_t* bucket, int64_t E, int32_t B, int32_t H,
+                                    float* grad_table, void* workspace, int64_t workspace_bytes, eqmp_stream_t stream) {
+  const eqmp_status cs = check(E, B, H);
+  if (cs != EQMP_OK) return cs;
+  if (!grad_table) return EQMP_OK;
+  if (!aligned(grad_bias, 4) || !aligned(bucket, 4) || !aligned(grad_table, 4)) return EQMP_ERR_INVALID_ARG;
+  if (E > 0 && (!grad_bias || !bucket)) return EQMP_ERR_INVALID_ARG;
+  const int64_t ws = grad_workspace(E, B, H);
+  if (ws > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < ws)) return EQMP_ERR_INVALID_ARG;
+  const Span reads[] = {span(grad_bias, E * H * 4), span(bucket, E * 4)};
+  const Span writes[] = {span(grad_table, (int64_t)B * H * 4), span(workspace, ws)};
+  if (!outputs_apart(reads, writes)) return EQMP_ERR_INVALID_ARG;
+  BiasArgs a{};
+  a.bucket = const_cast<int*>(bucket), a.grad = grad_bias, a.gtable = grad_table, a.part = static_cast<float*>(workspace);
+  a.E = (int)E, a.B = B, a.H = H, a.parts = grad_parts(E, B, H);
+  // heads of a CTA: all, or as many as one copy of the table has room for
+  int heads = H < kCopyFloats / B ? H : kCopyFloats / B;
+  int copies = kGradThreads / heads;
+  if (copies > kCopyFloats / (B * heads)) copies = kCopyFloats / (B * heads);
+  const int smem = copies * B * heads * 4;
+  static unsigned long long done = 0;
+  if (ensure_smem_attr(k_edge_bias_bwd, kCopyFloats * 4, &done) != cudaSuccess) return EQMP_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const dim3 grid((unsigned)a.parts, (unsigned)((H + heads - 1) / heads));
+  k_edge_bias_bwd<<<grid, kGradThreads, smem, st>>>(a, heads, copies);
+  if (cudaGetLastError() != cudaSuccess) return EQMP_ERR_CUDA;
+  if (a.parts == 1) return EQMP_OK;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((B * H + kBiasSumX - 1) / kBiasSumX));
+  cfg.blockDim = dim3(kBiasSumX, kBiasSumY);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, k_edge_bias_sum, a));
+}
+
+}  // extern "C"

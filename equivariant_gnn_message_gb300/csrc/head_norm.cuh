@@ -1,0 +1,342 @@
+// Norms of queries and keys for each head, with the rotation by a node's
+// position in the same pass (sm_103a).
+//
+//   r = (mean_d x^2 + eps)^-1/2,  u = x r w          over the D values of a head
+//   theta[p] = sum_a pos[a] freq[p][a]               p: the pair (2p, 2p+1)
+//   y[2p] = u[2p] cos - u[2p+1] sin,  y[2p+1] = u[2p] sin + u[2p+1] cos
+// Backward, with g = dL/dy turned back by -theta (b):
+//   a = b w,  dx = r (a - x r mean_d(a x r)),  dw = sum b x r
+//   dpos[a] = sum_{heads, p} freq[p][a] (b[2p+1] u[2p] - b[2p] u[2p+1])
+// (a rotation turns g and y alike, so the last one needs no y).
+//
+// A warp takes a node: the angles of its pairs are formed once and serve all its
+// heads.  Memory binds: x is read once and y written once.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace eqmp {
+
+struct HeadNormArgs {
+  const void *q, *k;          // [N][Hq][D], [N][Hk][D]
+  const void *gq, *gk;        // backward: dL/d of the outputs
+  long long q_ld, k_ld, gq_ld, gk_ld;
+  const float *wq, *wk;       // [D] or NULL
+  const float *pos, *freq;    // [N][axes], [D/2][axes] or NULL
+  void *oq, *ok;              // forward: the outputs; backward: the gradients of q and k
+  float* rstd;                // [N][Hq+Hk]
+  float *gwq, *gwk, *gpos;
+  float* part;                // [parts][2][D]
+  float eps;
+  int N, Hq, Hk, D, axes;
+};
+
+constexpr int kHeadWarps = 4;
+
+// An angle in turns, reduced to half a turn: the frequency in turns is held as
+// the sum of two floats, and the product's rounding error is kept, so that a
+// position of 10^5 turns has its angle to 10^-7 of a turn.  (In one float the
+// product alone would be off by 10^-2.)
+struct Turns {
+  float hi, lo;
+  __device__ __forceinline__ void set(float freq) {
+    const double t = (double)freq * 0.15915494309189535;  // 1 / (2 pi)
+    hi = (float)t;
+    lo = (float)(t - hi);
+  }
+  __device__ __forceinline__ float of(float pos) const {
+    const float t = pos * hi, rest = fmaf(pos, lo, fmaf(pos, hi, -t));
+    return t - rintf(t) + rest;
+  }
+};
+
+// The share of a head's row that a lane holds: NV vectors of V elements, the
+// j-th at (j G + l) V.  V = 2: single loads, the last pair may be half.
+template <typename T, int V, int G, int NV>
+struct HeadShare {
+  static constexpr bool WIDE = V * sizeof(T) == 16;
+  uint4 raw[WIDE ? NV : 1];
+  T one[WIDE ? 1 : NV * V];
+  __device__ __forceinline__ void load(const T* row, int l, int D, bool ok) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * G + l) * V;
+      if constexpr (WIDE) {
+        raw[j] = ok && c < D ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) one[j * V + i] = ok && c + i < D ? row[c + i] : T(0.0f);
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[NV * V]) const {
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (V == 4) {
+            f[j * V + i] = __uint_as_float(w[i]);
+          } else {
+            f[j * V + 2 * i] = __uint_as_float(w[i] << 16);
+            f[j * V + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV * V; ++i) f[i] = (float)one[i];
+    }
+  }
+  static __device__ __forceinline__ void store(T* row, int l, int D, const float (&f)[NV * V]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * G + l) * V;
+      if (c >= D) break;
+      if constexpr (V == 4) {
+        *reinterpret_cast<float4*>(row + c) = make_float4(f[j * V], f[j * V + 1], f[j * V + 2], f[j * V + 3]);
+      } else if constexpr (V == 8) {
+        __nv_bfloat162 b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = __floats2bfloat162_rn(f[j * V + 2 * i], f[j * V + 2 * i + 1]);
+        *reinterpret_cast<uint4*>(row + c) = *reinterpret_cast<const uint4*>(b);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (c + i < D) row[c + i] = T(f[j * V + i]);
+      }
+    }
+  }
+};
+
+// The lane's weights of queries and keys; 1 where there are none.
+template <int V, int G, int NV>
+__device__ __forceinline__ void load_weights(const float* w, int l, int D, float (&f)[NV * V]) {
+#pragma unroll
+  for (int i = 0; i < NV * V; ++i) {
+    const int c = (i / V * G + l) * V + i % V;
+    f[i] = w && c < D ? w[c] : 1.0f;
+  }
+}
+
+// The frequencies of the lane's pairs, and a node's cosines and sines.
+template <int V, int G, int NV>
+struct Rotation {
+  static constexpr int P = NV * V / 2;
+  Turns f[P][3];
+  __device__ __forceinline__ void set(const float* freq, int axes, int l, int D) {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        const int pair = ((2 * p / V * G + l) * V + 2 * p % V) / 2;
+        f[p][x].set(x < axes && pair < D / 2 ? freq[(long long)pair * axes + x] : 0.0f);
+      }
+  }
+  __device__ __forceinline__ void at(const float (&pos)[3], int axes, float (&c)[P], float (&s)[P]) const {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      float t = f[p][0].of(pos[0]);
+      if (axes > 1) t += f[p][1].of(pos[1]);
+      if (axes > 2) t += f[p][2].of(pos[2]);
+      t -= rintf(t);
+      sincospif(2.0f * t, &s[p], &c[p]);
+    }
+  }
+};
+
+__device__ __forceinline__ void load_pos(const HeadNormArgs& a, int node, float (&pos)[3]) {
+#pragma unroll
+  for (int x = 0; x < 3; ++x) pos[x] = x < a.axes ? __ldg(a.pos + (long long)node * a.axes + x) : 0.0f;
+}
+
+template <typename T, int V, int G, int NV, int U>
+__global__ void __launch_bounds__(32 * kHeadWarps) k_head_norm(HeadNormArgs a) {
+  constexpr int W = NV * V, P = W / 2, AT_ONCE = 32 / G;
+  const int lane = threadIdx.x & 31, l = lane % G, warps = gridDim.x * kHeadWarps, heads = a.Hq + a.Hk;
+  float wq[W], wk[W];
+  load_weights<V, G, NV>(a.wq, l, a.D, wq);
+  load_weights<V, G, NV>(a.wk, l, a.D, wk);
+  Rotation<V, G, NV> rot;
+  if (a.axes) rot.set(a.freq, a.axes, l, a.D);
+  for (int node = blockIdx.x * kHeadWarps + (threadIdx.x >> 5); node < a.N; node += warps) {
+    const T* q = static_cast<const T*>(a.q) + node * a.q_ld;
+    const T* k = static_cast<const T*>(a.k) + node * a.k_ld;
+    float cs[P], sn[P], pos[3];
+    if (a.axes) {
+      load_pos(a, node, pos);
+      rot.at(pos, a.axes, cs, sn);
+    }
+    for (int t0 = lane / G; t0 - lane / G < heads; t0 += U * AT_ONCE) {
+      HeadShare<T, V, G, NV> x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = t0 + u * AT_ONCE;
+        x[u].load(t < a.Hq ? q + (long long)t * a.D : k + (long long)(t - a.Hq) * a.D, l, a.D, t < heads);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = t0 + u * AT_ONCE;
+        float f[W], ss = 0.0f;
+        x[u].get(f);
+#pragma unroll
+        for (int i = 0; i < W; ++i) ss = fmaf(f[i], f[i], ss);
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (t >= heads) continue;
+        const bool query = t < a.Hq;
+        const float r = 1.0f / sqrtf(ss / (float)a.D + a.eps);
+        if (a.rstd && l == 0) a.rstd[(long long)node * heads + t] = r;
+#pragma unroll
+        for (int i = 0; i < W; ++i) f[i] *= r * (query ? wq[i] : wk[i]);
+        if (a.axes)
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            const float u0 = f[2 * p], u1 = f[2 * p + 1];
+            f[2 * p] = u0 * cs[p] - u1 * sn[p];
+            f[2 * p + 1] = u0 * sn[p] + u1 * cs[p];
+          }
+        T* out = static_cast<T*>(query ? a.oq : a.ok);
+        const long long row = query ? (long long)node * a.Hq + t : (long long)node * a.Hk + (t - a.Hq);
+        if (out) HeadShare<T, V, G, NV>::store(out + row * a.D, l, a.D, f);
+      }
+    }
+  }
+}
+
+template <typename T, int V, int G, int NV, int U>
+__global__ void __launch_bounds__(32 * kHeadWarps) k_head_norm_bwd(HeadNormArgs a) {
+  constexpr int W = NV * V, P = W / 2, AT_ONCE = 32 / G;
+  __shared__ float red[kHeadWarps][2 * G * W];
+  const int lane = threadIdx.x & 31, l = lane % G, warp = threadIdx.x >> 5, warps = gridDim.x * kHeadWarps;
+  const int heads = a.Hq + a.Hk;
+  float wq[W], wk[W], dwq[W], dwk[W];
+  load_weights<V, G, NV>(a.wq, l, a.D, wq);
+  load_weights<V, G, NV>(a.wk, l, a.D, wk);
+#pragma unroll
+  for (int i = 0; i < W; ++i) dwq[i] = dwk[i] = 0.0f;
+  Rotation<V, G, NV> rot;
+  if (a.axes) rot.set(a.freq, a.axes, l, a.D);
+  for (int node = blockIdx.x * kHeadWarps + warp; node < a.N; node += warps) {
+    float cs[P], sn[P], turn[P], pos[3];
+    if (a.axes) {
+      load_pos(a, node, pos);
+      rot.at(pos, a.axes, cs, sn);
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) turn[p] = 0.0f;
+    for (int t0 = lane / G; t0 - lane / G < heads; t0 += U * AT_ONCE) {
+      HeadShare<T, V, G, NV> x[U], g[U];
+      float r[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = t0 + u * AT_ONCE, hk = t - a.Hq;
+        const T* xp = static_cast<const T*>(t < a.Hq ? a.q : a.k);
+        const T* gp = static_cast<const T*>(t < a.Hq ? a.gq : a.gk);
+        x[u].load(xp + (t < a.Hq ? node * a.q_ld + (long long)t * a.D : node * a.k_ld + (long long)hk * a.D), l, a.D, t < heads);
+        g[u].load(gp + (t < a.Hq ? node * a.gq_ld + (long long)t * a.D : node * a.gk_ld + (long long)hk * a.D), l, a.D, t < heads);
+        r[u] = t < heads ? __ldg(a.rstd + (long long)node * heads + t) : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = t0 + u * AT_ONCE;
+        const bool query = t < a.Hq, ok = t < heads;
+        float h[W], b[W], mean = 0.0f;
+        x[u].get(h);
+        g[u].get(b);
+#pragma unroll
+        for (int i = 0; i < W; ++i) h[i] *= r[u];
+        if (a.axes)
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            const float g0 = b[2 * p], g1 = b[2 * p + 1];
+            b[2 * p] = g0 * cs[p] + g1 * sn[p];
+            b[2 * p + 1] = g1 * cs[p] - g0 * sn[p];
+            const float u0 = h[2 * p] * (query ? wq[2 * p] : wk[2 * p]);
+            const float u1 = h[2 * p + 1] * (query ? wq[2 * p + 1] : wk[2 * p + 1]);
+            if (ok) turn[p] += b[2 * p + 1] * u0 - b[2 * p] * u1;
+          }
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const float d = b[i] * h[i];
+          if (ok && query) dwq[i] += d;
+          if (ok && !query) dwk[i] += d;
+          b[i] *= query ? wq[i] : wk[i];
+          mean = fmaf(b[i], h[i], mean);
+        }
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
+        if (!ok) continue;
+        mean /= (float)a.D;
+#pragma unroll
+        for (int i = 0; i < W; ++i) b[i] = r[u] * fmaf(-h[i], mean, b[i]);
+        T* out = static_cast<T*>(query ? a.oq : a.ok);
+        const long long row = query ? (long long)node * a.Hq + t : (long long)node * a.Hk + (t - a.Hq);
+        if (out) HeadShare<T, V, G, NV>::store(out + row * a.D, l, a.D, b);
+      }
+    }
+    if (a.gpos) {
+      float d[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int x = 0; x < 3; ++x) d[x] = fmaf(turn[p], rot.f[p][x].hi, d[x]);
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) d[x] += __shfl_xor_sync(0xffffffffu, d[x], o);
+        if (lane == 0 && x < a.axes) a.gpos[(long long)node * a.axes + x] = d[x] * 6.2831853071795865f;
+      }
+    }
+  }
+  if (!a.part) return;
+  // over the groups of a warp, then over the warps, in a fixed order
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+#pragma unroll
+    for (int o = G; o < 32; o <<= 1) {
+      dwq[i] += __shfl_xor_sync(0xffffffffu, dwq[i], o);
+      dwk[i] += __shfl_xor_sync(0xffffffffu, dwk[i], o);
+    }
+    if (lane < G) {
+      const int c = (i / V * G + l) * V + i % V;
+      red[warp][c] = dwq[i];
+      red[warp][G * W + c] = dwk[i];
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * a.D; i += blockDim.x) {
+    const int c = i < a.D ? i : G * W + i - a.D;
+    float t = red[0][c];
+#pragma unroll
+    for (int w = 1; w < kHeadWarps; ++w) t += red[w][c];
+    a.part[(long long)blockIdx.x * 2 * a.D + i] = t;
+  }
+}
+
+// dw: the sums of the CTAs' parts, 8 columns a block.
+constexpr int kHeadSumX = 8, kHeadSumY = 32;
+
+static __global__ void __launch_bounds__(kHeadSumX * kHeadSumY) k_head_norm_sum(HeadNormArgs a, int parts) {
+  __shared__ float red[kHeadSumY][kHeadSumX];
+  const int c = blockIdx.x * kHeadSumX + threadIdx.x;
+  float t = 0.0f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // until the kernel that writes the parts is done
+  if (c < 2 * a.D)
+    for (int p = threadIdx.y; p < parts; p += kHeadSumY) t += a.part[(long long)p * 2 * a.D + c];
+  red[threadIdx.y][threadIdx.x] = t;
+  __syncthreads();
+  if (threadIdx.y || c >= 2 * a.D) return;
+#pragma unroll
+  for (int y = 1; y < kHeadSumY; ++y) t += red[y][threadIdx.x];
+  if (c < a.D) {
+    if (a.gwq) a.gwq[c] = t;
+  } else if (a.gwk) {
+    a.gwk[c - a.D] = t;
+  }
+}
+
+}  // namespace eqmp

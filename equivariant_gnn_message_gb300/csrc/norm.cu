@@ -2,13 +2,12 @@
 // Contracts are in include/eqmp.h, the formulas in norm.cuh.
 #include <math.h>
 
+#include "host_args.h"
 #include "launch.h"
 #include "norm.cuh"
 #include "norm_rows.cuh"
 
 namespace eqmp {
-
-static bool aligned(const void* p, int dtype_bytes) { return reinterpret_cast<uintptr_t>(p) % dtype_bytes == 0; }
 
 // Checks d for rows of `cols` columns and resolves its rate to 1/65536.
 static eqmp_status drop_args(const eqmp_drop& d, long long cols, DropArgs* out) {
@@ -26,55 +25,7 @@ static eqmp_status drop_args(const eqmp_drop& d, long long cols, DropArgs* out) 
   return EQMP_OK;
 }
 
-// One strided matrix: rows of `cols` elements, `ld` elements apart.
-struct Plane {
-  const void* p;
-  long long ld;
-};
-
-// The memory of an argument; NULL and empty ones meet nothing.
-struct Span {
-  uintptr_t begin, end;
-};
-
-static Span span(const void* p, long long bytes) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-  return Span{at, p && bytes > 0 ? at + (uintptr_t)bytes : at};
-}
-
-static Span span(const Plane& a, long long rows, long long cols, int bytes) {
-  return span(a.p, rows > 0 ? ((rows - 1) * a.ld + cols) * bytes : 0);
-}
-
 static Span span(const DropArgs& d) { return span(d.step, sizeof(*d.step)); }
-
-static bool meet(const Span& a, const Span& b) {
-  return a.begin < a.end && b.begin < b.end && a.begin < b.end && b.begin < a.end;
-}
-
-// Outputs apart from the inputs and from one another.
-template <int I, int O>
-static bool outputs_apart(const Span (&in)[I], const Span (&out)[O]) {
-  for (int o = 0; o < O; ++o) {
-    for (int i = 0; i < I; ++i)
-      if (meet(in[i], out[o])) return false;
-    for (int q = 0; q < o; ++q)
-      if (meet(out[q], out[o])) return false;
-  }
-  return true;
-}
-
-// A row stride of up to 2^31 elements, so that 2^30 rows stay in 64 bits.
-static bool stride_ok(long long ld) { return ld >= 0 && ld <= 1ll << 31; }
-
-// Inputs: aligned, strides that address forward.  Outputs (packed): aligned.
-static bool planes_ok(const Plane* in, int n_in, void* const* outs, int n_out, int bytes) {
-  for (int i = 0; i < n_in; ++i)
-    if (in[i].p && (!aligned(in[i].p, bytes) || !stride_ok(in[i].ld))) return false;
-  for (int o = 0; o < n_out; ++o)
-    if (!aligned(outs[o], bytes)) return false;
-  return true;
-}
 
 static int rows_grid(long long rows, const DeviceInfo& dev) {
   const long long cap = (long long)dev.sms * 8;

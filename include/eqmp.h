@@ -500,6 +500,155 @@ eqmp_status eqmp_degree_norm_backward(const void* grad_y, const void* s, const v
                                       void* workspace, int64_t workspace_bytes, eqmp_stream_t stream);
 
 /*
+ * Conventions shared by the entry points of the attention over edges below
+ *   - q, k, v, their gradients and out are fp32 or bf16 (`dtype`, one type for
+ *     all of them); the bias, statistics, weights, tables and their gradients
+ *     are fp32.  Scores, statistics and sums are fp32; a bf16 result is rounded
+ *     once, on its store.
+ *   - q [N][H][D] and its like: a node's heads are packed, nodes lie `_ld`
+ *     elements apart (0 to 2^31: H*D for packed nodes, more for a slice of a
+ *     wider projection, 0 for one node that stands for all).  Results are
+ *     packed.  No alignment beyond the element's own is needed; heads that all
+ *     begin on 16 bytes are faster.
+ *   - Up to 2^30 nodes and 2^30 edges, D up to 256 (EQMP_ERR_UNSUPPORTED above).
+ *   - Results may be NULL to skip them.  They and the workspace must not overlap
+ *     the inputs or one another (EQMP_ERR_INVALID_ARG).
+ *   - Workspaces are device memory, 16-byte aligned, of at least the bytes that
+ *     the call's _workspace_size function gives (-1 for sizes that are not
+ *     supported; 0: NULL will do); contents on entry are ignored.  No other call
+ *     may use one until this one completes.
+ *   - Results are bitwise reproducible on one device: every sum has a fixed
+ *     order, and nothing is added by atomics.
+ */
+
+/*
+ * Norms of queries and keys for each head, and the rotation of their pairs by a
+ * node's position, in one pass over q [N][Hq][D] and k [N][Hk][D] (Hk == 0:
+ * queries alone, k NULL):
+ *   r = 1 / sqrt(mean_d(x^2) + eps)            (over the D values of a head)
+ *   u = x r w[d]
+ *   theta[p] = sum_a pos[n][a] freq[p][a]      (p = 0 .. D/2-1; radians)
+ *   y[2p] = u[2p] cos(theta) - u[2p+1] sin(theta)
+ *   y[2p+1] = u[2p] sin(theta) + u[2p+1] cos(theta)
+ * so that q.k of two nodes hangs on the difference of their positions.
+ *   wq, wk  [D], NULL: 1
+ *   eps     >= 0, finite
+ *   pos     [N][axes], freq [D/2][axes], axes 1..3: a place in a chain or a time
+ *           (axes 1), or coordinates with wave vectors (axes 3: then the result
+ *           turns with the frame, unlike the rest of the layer).  Angles are
+ *           reduced exactly: positions of many turns keep their angle.
+ *   axes 0: no rotation (pos, freq unused, D may be odd; with a rotation it is
+ *           even, EQMP_ERR_INVALID_ARG otherwise)
+ *   out_q [N][Hq][D], out_k [N][Hk][D], written
+ *   rstd  [N][Hq+Hk], written: r, queries first, for the backward pass
+ */
+eqmp_status eqmp_head_norm(const void* q, int64_t q_ld, int32_t Hq, const void* k, int64_t k_ld, int32_t Hk,
+                           eqmp_dtype dtype, int64_t N, int32_t D, const float* wq, const float* wk, float eps,
+                           const float* pos, const float* freq, int32_t axes, void* out_q, void* out_k, float* rstd,
+                           eqmp_stream_t stream);
+
+/*
+ * Gradients of eqmp_head_norm, given grad_yq = dL/d(out_q), grad_yk, the forward
+ * call's inputs and its rstd.  With b = dL/dy turned back by -theta, a = b w:
+ *   grad_q, grad_k    r (a - x r mean_d(a x r)), packed
+ *   grad_wq, grad_wk  [D]        sums of b x r over nodes and heads
+ *   grad_pos          [N][axes]  sum over heads and p of
+ *                                freq[p] (b[2p+1] u[2p] - b[2p] u[2p+1]); axes > 0
+ * freq takes no gradient.  The workspace is needed for grad_wq and grad_wk only.
+ */
+int64_t eqmp_head_norm_backward_workspace_size(int64_t N, int32_t D);
+
+eqmp_status eqmp_head_norm_backward(const void* grad_yq, int64_t grad_yq_ld, const void* grad_yk, int64_t grad_yk_ld,
+                                    const void* q, int64_t q_ld, int32_t Hq, const void* k, int64_t k_ld, int32_t Hk,
+                                    eqmp_dtype dtype, int64_t N, int32_t D, const float* wq, const float* wk,
+                                    const float* rstd, const float* pos, const float* freq, int32_t axes, void* grad_q,
+                                    void* grad_k, float* grad_wq, float* grad_wk, float* grad_pos, void* workspace,
+                                    int64_t workspace_bytes, eqmp_stream_t stream);
+
+/*
+ * A learned bias of each edge and head, by the bucket of the edge's length:
+ *   bucket[e] = the number of borders that are <= |vec_e|     (0 .. B-1)
+ *   bias[e][h] = table[bucket[e]][h]
+ *   vec      [E][3] fp32
+ *   borders  [B-1] fp32, >= 0 and ascending (B == 1: NULL).  The comparison is
+ *            made on squares in 64 bits, ((x*x + y*y) + z*z) >= b*b, each
+ *            operation rounded on its own.  A NaN falls into bucket 0.
+ *   table    [B][H] fp32; 1 <= B <= 1024, 1 <= H <= 256 (EQMP_ERR_UNSUPPORTED
+ *            above)
+ *   bias     [E][H] fp32, written; bucket [E] int32, written: for the backward
+ *            pass, and for other tables on the same graph
+ * Unordered borders give some bucket of 0 .. B-1.
+ */
+eqmp_status eqmp_edge_bias(const float* vec, int64_t E, const float* borders, int32_t B, const float* table, int32_t H,
+                           float* bias, int32_t* bucket, eqmp_stream_t stream);
+
+/*
+ * Gradient of eqmp_edge_bias: grad_table[b][h] = sum of grad_bias[e][h] over the
+ * edges of bucket b, every entry written.  An edge whose bucket is outside
+ * 0 .. B-1 adds nothing.  (The buckets are constant between borders: the lengths
+ * take no gradient.)
+ */
+int64_t eqmp_edge_bias_backward_workspace_size(int64_t E, int32_t B, int32_t H);
+
+eqmp_status eqmp_edge_bias_backward(const float* grad_bias, const int32_t* bucket, int64_t E, int32_t B, int32_t H,
+                                    float* grad_table, void* workspace, int64_t workspace_bytes, eqmp_stream_t stream);
+
+/*
+ * Attention over a receiver's edges (E2Former-V2 section 2.2 describes the
+ * node-centric streaming with a running softmax): for each receiver i and head h,
+ * over its edges e with senders j = src[e],
+ *   s[e] = scale q[i][h].k[j][h] + bias[e][h]
+ *   m = max_e s[e],  z = sum_e exp(s[e] - m)
+ *   out[i][h] = sum_e exp(s[e] - m) / z  v[j][h]
+ *   q      [N][H][D], k [N_src][H][D], v [N_src][H][Dv].  v may be node features
+ *          [N_src][C][K], seen with Dv = C/H * K: with invariant q, k and bias the
+ *          weights are invariant, and out turns with the frame as v does.
+ *   bias   [E][H] fp32 or NULL: 0
+ *   scale  finite (1 / sqrt(D) as a rule)
+ *   row_offsets, src: as eqmp_fused; a sender outside 0 .. N_src-1 reads as zeros
+ *   out    [N][H][Dv], written
+ *   stats  [N][H][2], written: m and z, for the backward pass
+ * An edge whose bias or score is -inf is left out: nothing of its key and value
+ * enters, a NaN or an infinity neither.  A receiver with no edge left gets
+ * out = 0, m = z = 0.  Other NaNs and infinities go where the formula takes them,
+ * within their receiver and head.
+ * H up to 1024, Dv up to 1024 (EQMP_ERR_UNSUPPORTED above).  A receiver of very
+ * many edges is spread over the device; its parts are added in a fixed order.
+ */
+int64_t eqmp_edge_attention_workspace_size(int64_t E, int32_t H, int32_t Dv);
+
+eqmp_status eqmp_edge_attention(const void* q, int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
+                                eqmp_dtype dtype, int64_t N, int64_t N_src, int64_t E, int32_t H, int32_t D, int32_t Dv,
+                                const int32_t* row_offsets, const int32_t* src, const float* bias, float scale,
+                                void* out, float* stats, void* workspace, int64_t workspace_bytes, eqmp_stream_t stream);
+
+/*
+ * Gradients of eqmp_edge_attention, given grad_out = dL/dout, the forward call's
+ * inputs and its stats.  With p = exp(s - m) / z and dp = grad_out[i][h].v[j][h]:
+ *   ds[e]      p (dp - sum over the row's edges of p dp)
+ *   grad_q     [N][H][D]       scale sum_e ds k[j]
+ *   grad_k     [N_src][H][D]   scale sum over the sender's edges of ds q[i]
+ *   grad_v     [N_src][H][Dv]  sum over the sender's edges of p grad_out[i]
+ *   grad_bias  [E][H]          ds
+ * Edges that were left out have no part in any of them (grad_bias 0).  grad_k and
+ * grad_v need dst [E] and the sender view (send_offsets [N_src+1], send_edges
+ * [E_send]) of the same edges, as eqmp_fused_backward (the three may be NULL where
+ * neither is asked for).  Every row of the results is written; grad_bias is 0 for
+ * edges of no receiver of this call.
+ */
+int64_t eqmp_edge_attention_backward_workspace_size(int64_t N, int64_t E, int64_t E_send, int32_t H, int32_t D,
+                                                    int32_t Dv);
+
+eqmp_status eqmp_edge_attention_backward(const void* grad_out, int64_t grad_out_ld, const void* q, int64_t q_ld,
+                                         const void* k, int64_t k_ld, const void* v, int64_t v_ld, eqmp_dtype dtype,
+                                         int64_t N, int64_t N_src, int64_t E, int32_t H, int32_t D, int32_t Dv,
+                                         const int32_t* row_offsets, const int32_t* src, const int32_t* dst,
+                                         const int32_t* send_offsets, const int32_t* send_edges, int64_t E_send,
+                                         const float* bias, float scale, const float* stats, void* grad_q, void* grad_k,
+                                         void* grad_v, float* grad_bias, void* workspace, int64_t workspace_bytes,
+                                         eqmp_stream_t stream);
+
+/*
  * Synchronous check of the graph preconditions on device data:
  * 0 <= row_offsets[0] <= ... <= row_offsets[N] <= E and
  * 0 <= src[e] < N_src for every e in [row_offsets[0], row_offsets[N]).
