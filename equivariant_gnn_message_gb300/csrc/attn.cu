@@ -77,6 +77,8 @@ static AttnForm form_of(const Sizes& n, int64_t rows, int bytes, bool vectors) {
   while (f.G < 32 && (!fits(f.G) || n.H * f.G * 2 <= 32 || rows * ((n.H * f.G + 31) / 32) < 152 * 16)) f.G *= vectors ? 2 : 4;
   f.KN = (k + f.G - 1) / f.G;
   f.VN = (v + f.G - 1) / f.G;
+  const int64_t each = rows * ((n.H * f.G + 31) / 32) / (152 * 8 * 4);
+  f.rows_each = (int)(each < 1 ? 1 : each > 16 ? 16 : each);
   return f;
 }
 

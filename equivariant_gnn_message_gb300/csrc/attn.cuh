@@ -38,6 +38,7 @@ struct AttnArgs {
   float scale;
   int N, Ns, E, E_send, H, D, Dv;
   int block, blocks;  // edges of a block of a long row, blocks in all (0: rows are not split)
+  int rows_each;      // rows of a warp in the kernels of attn_ring.cuh
 };
 
 constexpr int kAttnWarps = 4;  // of a CTA, each with its own piece

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "attn.cuh"
+#include "attn_ring.cuh"
 #include "launch.h"
 
 namespace eqmp {
@@ -12,6 +13,7 @@ enum { kAttnFwd, kAttnRecv, kAttnSend };
 // of a value a lane.
 struct AttnForm {
   int V, G, KN, VN;
+  int rows_each;
 };
 
 // One launcher for each pass and type (attn_*.cu).
@@ -23,20 +25,11 @@ EQMP_ATTN_LAUNCHER(launch_attn_recv_bf16);
 EQMP_ATTN_LAUNCHER(launch_attn_send_f32);
 EQMP_ATTN_LAUNCHER(launch_attn_send_bf16);
 
-template <int PASS, typename T, int V, int G, int KN, int VN>
-eqmp_status launch_attn_form(const AttnArgs& a, cudaStream_t st) {
-  constexpr int VALUES = VN * V, U = VALUES <= 16 ? 4 : VALUES <= 32 ? 2 : 1;
-  const int rows = PASS == kAttnSend ? a.Ns : a.N;
-  const dim3 grid((unsigned)((rows + a.blocks + kAttnWarps - 1) / kAttnWarps), (unsigned)((a.H * G + 31) / 32));
-  if constexpr (PASS == kAttnFwd)
-    k_attn_fwd<T, V, G, KN, VN, U><<<grid, 32 * kAttnWarps, 0, st>>>(a);
-  else if constexpr (PASS == kAttnRecv)
-    k_attn_bwd_recv<T, V, G, KN, VN, U><<<grid, 32 * kAttnWarps, 0, st>>>(a);
-  else
-    k_attn_bwd_send<T, V, G, KN, VN, U><<<grid, 32 * kAttnWarps, 0, st>>>(a);
+// The parts of long rows: launched while the pass before it runs, and over at once where there are none.
+template <int PASS, typename T>
+eqmp_status launch_attn_join(const AttnArgs& a, cudaStream_t st) {
   if (cudaGetLastError() != cudaSuccess) return EQMP_ERR_CUDA;
   if (!a.blocks) return EQMP_OK;
-  // the parts of long rows: launched while the pass before it runs, and over at once where there are none
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -50,23 +43,56 @@ eqmp_status launch_attn_form(const AttnArgs& a, cudaStream_t st) {
   return cuda_status(cudaLaunchKernelEx(&cfg, k_attn_join<MODE, T>, a));
 }
 
-template <int PASS, typename T, int V, int G>
+template <int PASS, typename T, int V, int G, int KN, int VN>
+eqmp_status launch_attn_form(const AttnArgs& a, cudaStream_t st) {
+  constexpr int VALUES = VN * V, U = VALUES <= 16 ? 4 : VALUES <= 32 ? 2 : 1;
+  const int rows = PASS == kAttnSend ? a.Ns : a.N;
+  const dim3 grid((unsigned)((rows + a.blocks + kAttnWarps - 1) / kAttnWarps), (unsigned)((a.H * G + 31) / 32));
+  if constexpr (PASS == kAttnFwd)
+    k_attn_fwd<T, V, G, KN, VN, U><<<grid, 32 * kAttnWarps, 0, st>>>(a);
+  else if constexpr (PASS == kAttnRecv)
+    k_attn_bwd_recv<T, V, G, KN, VN, U><<<grid, 32 * kAttnWarps, 0, st>>>(a);
+  else
+    k_attn_bwd_send<T, V, G, KN, VN, U><<<grid, 32 * kAttnWarps, 0, st>>>(a);
+  return launch_attn_join<PASS, T>(a, st);
+}
+
+template <int PASS, typename T, int G, int KN, int VN>
+eqmp_status launch_attn_ring(const AttnArgs& a, cudaStream_t st) {
+  constexpr int SMEM = RingShape<G, KN, VN, PASS == kAttnSend ? 16 : 4>::CTA;
+  const long long rows = PASS == kAttnSend ? a.Ns : a.N, workers = a.blocks + (rows + a.rows_each - 1) / a.rows_each;
+  const dim3 grid((unsigned)((workers + kRingWarps - 1) / kRingWarps), (unsigned)((a.H * G + 31) / 32));
+  static unsigned long long done = 0;
+  auto run = [&](auto kernel) {
+    if (ensure_smem_attr(kernel, SMEM, &done) != cudaSuccess) return EQMP_ERR_CUDA;
+    kernel<<<grid, 32 * kRingWarps, SMEM, st>>>(a);
+    return launch_attn_join<PASS, T>(a, st);
+  };
+  if constexpr (PASS == kAttnFwd)
+    return run(k_attn_fwd_ring<T, G, KN, VN>);
+  else if constexpr (PASS == kAttnRecv)
+    return run(k_attn_recv_ring<T, G, KN, VN>);
+  else
+    return run(k_attn_send_ring<T, G, KN, VN>);
+}
+
+template <int PASS, typename T, int G>
 eqmp_status launch_attn_lanes(const AttnArgs& a, const AttnForm& f, cudaStream_t st) {
-  if (f.KN <= 1 && f.VN <= 1) return launch_attn_form<PASS, T, V, G, 1, 1>(a, st);
-  if (f.KN <= 1 && f.VN <= 2) return launch_attn_form<PASS, T, V, G, 1, 2>(a, st);
-  if (f.KN <= 1 && f.VN <= 4) return launch_attn_form<PASS, T, V, G, 1, 4>(a, st);
-  if (f.VN <= 2) return launch_attn_form<PASS, T, V, G, 2, 2>(a, st);
-  if (f.VN <= 4) return launch_attn_form<PASS, T, V, G, 2, 4>(a, st);
-  return launch_attn_form<PASS, T, V, G, 2, 8>(a, st);
+  if (f.KN <= 1 && f.VN <= 1) return launch_attn_ring<PASS, T, G, 1, 1>(a, st);
+  if (f.KN <= 1 && f.VN <= 2) return launch_attn_ring<PASS, T, G, 1, 2>(a, st);
+  if (f.KN <= 1 && f.VN <= 4) return launch_attn_ring<PASS, T, G, 1, 4>(a, st);
+  if (f.VN <= 2) return launch_attn_ring<PASS, T, G, 2, 2>(a, st);
+  if (f.VN <= 4) return launch_attn_ring<PASS, T, G, 2, 4>(a, st);
+  return launch_attn_ring<PASS, T, G, 2, 8>(a, st);
 }
 
 template <int PASS, typename T>
-eqmp_status launch_attn(const AttnArgs& a, const AttnForm& f, cudaStream_t st) {
-  constexpr int V = 16 / sizeof(T);
-  if (f.V == V) {
-    if (f.G == 8) return launch_attn_lanes<PASS, T, V, 8>(a, f, st);
-    if (f.G == 16) return launch_attn_lanes<PASS, T, V, 16>(a, f, st);
-    return launch_attn_lanes<PASS, T, V, 32>(a, f, st);
+eqmp_status launch_attn(AttnArgs a, const AttnForm& f, cudaStream_t st) {
+  a.rows_each = f.rows_each;
+  if (f.V > 1) {
+    if (f.G == 8) return launch_attn_lanes<PASS, T, 8>(a, f, st);
+    if (f.G == 16) return launch_attn_lanes<PASS, T, 16>(a, f, st);
+    return launch_attn_lanes<PASS, T, 32>(a, f, st);
   }
   if (f.G == 8) return launch_attn_form<PASS, T, 1, 8, 4, 16>(a, st);
   if (f.KN <= 2 && f.VN <= 8) return launch_attn_form<PASS, T, 1, 32, 2, 8>(a, st);

@@ -1,0 +1,627 @@
+// The attention kernels for rows whose heads begin on 16 bytes (sm_103a).
+//
+// A warp takes 32 / G heads of a few neighbouring rows and walks over their
+// edges, U at a time.  The edges' rows come through a ring in shared memory by
+// asynchronous copies, STAGES - 1 batches ahead and across the ends of rows, so
+// that neither the indices nor the rows are waited for; a lane copies just the
+// bytes that it will read itself.  What is left is bound by the gather through
+// L2 (and by DRAM where the heads of a launch's slice of all nodes do not stay
+// in L2).
+#pragma once
+
+#include "attn.cuh"
+
+namespace eqmp {
+
+constexpr int kRingWarps = 2;  // of a CTA
+
+__device__ __forceinline__ void copy_async16(uint32_t to, const void* from, bool ok) {  // zeros where not ok
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(ok ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(N), "r"(ok ? N : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float4 lds128(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 lds64(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds32(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// 16 bytes as pairs of fp32 values.
+template <typename T>
+__device__ __forceinline__ void pairs_of(const float4& v, float2 (&f)[8 / sizeof(T)]) {
+  if constexpr (sizeof(T) == 4) {
+    f[0] = make_float2(v.x, v.y);
+    f[1] = make_float2(v.z, v.w);
+  } else {
+    const float w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t b = __float_as_uint(w[i]);
+      f[i] = make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+    }
+  }
+}
+
+// What a worker does: n rows from `row` on; lane i < n holds the edges and the
+// slot of the i-th (see Piece).
+struct Work {
+  int row, n;
+  int e0, e1, slot;
+};
+
+__device__ __forceinline__ Work find_work(const Rows& r, int w, int rows_each) {
+  const int lane = threadIdx.x & 31;
+  Work t{0, 0, 0, 0, -1};
+  if (w < r.blocks) {
+    const Piece p = find_piece(r, w);
+    if (p.row < 0) return t;
+    return Work{p.row, 1, p.e0, p.e1, p.slot};
+  }
+  const long long first = (long long)(w - r.blocks) * rows_each;
+  if (first >= r.n) return t;
+  t.row = (int)first;
+  t.n = min(rows_each, r.n - t.row);
+  if (lane < t.n) {
+    t.e0 = clamped(__ldg(r.off + t.row + lane), r.E);
+    t.e1 = max(t.e0, clamped(__ldg(r.off + t.row + lane + 1), r.E));
+    if (is_long(r, t.e0, t.e1)) {
+      t.slot = r.blocks + t.e0 / r.block;
+      t.e1 = min(t.e1, (t.e0 / r.block + 1) * r.block);
+    }
+  }
+  return t;
+}
+
+// The batches of a worker's edges in order: its rows' edges U at a time.
+struct Walk {
+  int i, e, end;  // the row, the batch's first edge, the row's end
+  __device__ __forceinline__ void start(const Work& w) {
+    i = -1;
+    e = end = 0;
+    next_row(w);
+  }
+  __device__ __forceinline__ void next_row(const Work& w) {
+    while (e >= end && ++i < w.n) {
+      e = __shfl_sync(0xffffffffu, w.e0, i);
+      end = __shfl_sync(0xffffffffu, w.e1, i);
+    }
+  }
+  __device__ __forceinline__ bool over(const Work& w) const { return i >= w.n; }
+};
+
+// Values of consecutive places of an index list, a lane each, loaded 32 places
+// ahead; a jump in the list loads anew.
+struct Ahead {
+  int c, now, next;
+  __device__ __forceinline__ int load(const int* list, int at, int n) const {
+    return at < n ? __ldg(list + at) : -1;
+  }
+  __device__ __forceinline__ void start(const int* list, int e, int n) {
+    const int lane = threadIdx.x & 31;
+    c = e;
+    now = load(list, e + lane, n);
+    next = load(list, e + 32 + lane, n);
+  }
+  __device__ __forceinline__ void to(const int* list, int e, int n) {
+    if (e - c < 32) return;
+    if (e - c >= 64) {
+      start(list, e, n);
+      return;
+    }
+    c += 32;
+    now = next;
+    next = load(list, c + 32 + (threadIdx.x & 31), n);
+  }
+  // lane t gets the value of place e + t; e is at most 31 behind c
+  __device__ __forceinline__ int from(int e) const {
+    const int at = e - c + (threadIdx.x & 31);
+    const int a = __shfl_sync(0xffffffffu, now, at & 31), b = __shfl_sync(0xffffffffu, next, at & 31);
+    return at < 32 ? a : b;
+  }
+};
+
+// The sums over the G lanes of a head of NV values (a power of two up to G):
+// lane l gets that of value l % NV.
+template <int G, int NV>
+__device__ __forceinline__ float scatter_sum(float (&v)[NV], int l) {
+#pragma unroll
+  for (int half = NV / 2; half > 0; half /= 2) {
+    const bool upper = l & half;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float send = upper ? v[i] : v[i + half], keep = upper ? v[i + half] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, half);
+    }
+  }
+#pragma unroll
+  for (int o = NV; o < G; o *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return v[0];
+}
+
+// The shape of a ring: U edges a batch, each of A + B vectors a lane, and per
+// batch a few bytes for every edge and head.
+template <int G, int A, int B, int SMALL>
+struct RingShape {
+  static constexpr int VECS = A + B;
+  static constexpr int U = 4;
+  static constexpr int HEADS = 32 / G;
+  static constexpr int SMALL_AT = U * VECS * 512;
+  static constexpr int BATCH = SMALL_AT + (U * HEADS * SMALL + 127) / 128 * 128;
+  static constexpr int STAGES = VECS <= 2 ? 4 : VECS <= 6 ? 3 : 2;
+  static constexpr int WARP = STAGES * BATCH;
+  static constexpr int CTA = kRingWarps * WARP;
+};
+
+template <typename T, int G, int NV>
+__device__ __forceinline__ void load_row(const T* row, int l, int cols, bool ok, float4 (&v)[NV]) {
+  constexpr int V = 16 / sizeof(T);
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    v[j] = ok && (j * G + l) * V < cols ? __ldg(reinterpret_cast<const float4*>(row + (j * G + l) * V)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+}
+
+template <typename T, int NV>
+__device__ __forceinline__ void unpack(const float4 (&v)[NV], float by, float2 (&f)[NV * 8 / sizeof(T)]) {
+  constexpr int P = 8 / sizeof(T);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    float2 p[P];
+    pairs_of<T>(v[j], p);
+#pragma unroll
+    for (int i = 0; i < P; ++i) f[j * P + i] = make_float2(p[i].x * by, p[i].y * by);
+  }
+}
+
+// sum += by * the lane's vectors at `at` (512 bytes apart); nothing where a
+// left-out edge's row must not be seen.
+template <typename T, int NV>
+__device__ __forceinline__ void add_row(uint32_t at, float by, float2 (&sum)[NV * 8 / sizeof(T)], bool hide) {
+  constexpr int P = 8 / sizeof(T);
+  const float2 b = make_float2(by, by);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    float4 v = lds128(at + j * 512);
+    if (hide) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float2 p[P];
+    pairs_of<T>(v, p);
+#pragma unroll
+    for (int i = 0; i < P; ++i) sum[j * P + i] = __ffma2_rn(b, p[i], sum[j * P + i]);
+  }
+}
+
+template <typename T, int NV>
+__device__ __forceinline__ float dot_row(uint32_t at, const float2 (&with)[NV * 8 / sizeof(T)]) {
+  constexpr int P = 8 / sizeof(T);
+  float2 t = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    float2 p[P];
+    pairs_of<T>(lds128(at + j * 512), p);
+#pragma unroll
+    for (int i = 0; i < P; ++i) t = __ffma2_rn(p[i], with[j * P + i], t);
+  }
+  return t.x + t.y;
+}
+
+template <typename T, int G, int NV>
+__device__ __forceinline__ void store_row(T* row, int l, int cols, const float2 (&x)[NV * 8 / sizeof(T)], float by) {
+  constexpr int P = 8 / sizeof(T), V = 2 * P;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if ((j * G + l) * V >= cols) break;
+    float f[V];
+#pragma unroll
+    for (int i = 0; i < P; ++i) f[2 * i] = x[j * P + i].x * by, f[2 * i + 1] = x[j * P + i].y * by;
+    Vec<T, V>::store(row + (j * G + l) * V, f);
+  }
+}
+
+template <typename T, int G, int NV>
+__device__ __forceinline__ void store_row_part(float* row, int l, int cols, const float2 (&x)[NV * 8 / sizeof(T)]) {
+  constexpr int P = 8 / sizeof(T), V = 2 * P;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int c = (j * G + l) * V + 2 * i;
+      if (c < cols) row[c] = x[j * P + i].x, row[c + 1] = x[j * P + i].y;
+    }
+}
+
+// ---------------------------------------------------------------- forward
+template <typename T, int G, int KN, int VN>
+__global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(AttnArgs a) {
+  using Shape = RingShape<G, KN, VN, 4>;
+  constexpr int U = Shape::U, V = 16 / sizeof(T), KP = KN * V / 2, VP = VN * V / 2;
+  extern __shared__ __align__(128) uint8_t space[];
+  const Rows rows{a.off, a.N, a.E, a.block, a.blocks};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G, hh = lane / G;
+  const Work w = find_work(rows, blockIdx.x * kRingWarps + warp, a.rows_each);
+  if (w.n == 0) return;
+  const int h = blockIdx.y * (32 / G) + hh;
+  const bool mine = h < a.H;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(space) + warp * Shape::WARP, at_lane = ring + lane * 16;
+  const T* const k = static_cast<const T*>(a.k) + (long long)h * a.D + l * V;
+  const T* const v = static_cast<const T*>(a.v) + (long long)h * a.Dv + l * V;
+
+  Walk put;
+  put.start(w);
+  Ahead src;
+  src.start(a.src, put.e, a.E);
+  int put_stage = 0;
+  auto copy_batch = [&] {  // the next batch's rows and biases, into the stage that has been read
+    if (!put.over(w)) {
+      src.to(a.src, put.e, a.E);
+      const int mine_src = src.from(put.e);
+      const uint32_t to = at_lane + put_stage * Shape::BATCH;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = __shfl_sync(0xffffffffu, mine_src, u);
+        const bool ok = mine && put.e + u < put.end && (unsigned)j < (unsigned)a.Ns;
+        const T *kr = k + (ok ? j * a.k_ld : 0), *vr = v + (ok ? j * a.v_ld : 0);
+#pragma unroll
+        for (int i = 0; i < KN; ++i)
+          copy_async16(to + (u * Shape::VECS + i) * 512, kr + i * G * V, ok && (i * G + l) * V < a.D);
+#pragma unroll
+        for (int i = 0; i < VN; ++i)
+          copy_async16(to + (u * Shape::VECS + KN + i) * 512, vr + i * G * V, ok && (i * G + l) * V < a.Dv);
+      }
+      if (a.bias && l < U && mine && put.e + l < put.end)
+        copy_async<4>(ring + put_stage * Shape::BATCH + Shape::SMALL_AT + (hh * U + l) * 4, a.bias + (long long)(put.e + l) * a.H + h, true);
+      put.e += U;
+      put.next_row(w);
+    }
+    copy_commit();
+    if (++put_stage == Shape::STAGES) put_stage = 0;
+  };
+#pragma unroll
+  for (int i = 0; i < Shape::STAGES - 1; ++i) copy_batch();
+
+  float4 q_next[KN];
+  auto load_q = [&](int i) {
+    load_row<T, G, KN>(static_cast<const T*>(a.q) + (w.row + i) * a.q_ld + (long long)h * a.D, l, a.D, mine && i < w.n, q_next);
+  };
+  load_q(0);
+  int stage = 0;
+  for (int i = 0; i < w.n; ++i) {
+    const int e0 = __shfl_sync(0xffffffffu, w.e0, i), e1 = __shfl_sync(0xffffffffu, w.e1, i);
+    const int slot = __shfl_sync(0xffffffffu, w.slot, i);
+    float2 q[KP], acc[VP];
+    unpack<T, KN>(q_next, a.scale, q);
+    load_q(i + 1);
+#pragma unroll
+    for (int x = 0; x < VP; ++x) acc[x] = make_float2(0.0f, 0.0f);
+    float m = EQMP_NEG_INF, z = 0.0f;  // z: of the edges of the lane's place in a batch
+    for (int e = e0; e < e1; e += U) {
+      copy_wait<Shape::STAGES - 2>();
+      __syncwarp();
+      copy_batch();
+      const uint32_t at = at_lane + stage * Shape::BATCH;
+      float s[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) s[u] = dot_row<T, KN>(at + u * Shape::VECS * 512, q);
+      float score = scatter_sum<G, U>(s, l);  // of edge e + l % U
+      const bool in = e + l % U < e1;
+      const float bias = a.bias && mine && in ? lds32(ring + stage * Shape::BATCH + Shape::SMALL_AT + (hh * U + l % U) * 4) : 0.0f;
+      score = !in || bias == EQMP_NEG_INF ? EQMP_NEG_INF : score + bias;
+      float top = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      top = fmaxf(top, m);
+      const float base = top == EQMP_NEG_INF ? 0.0f : top;
+      if (__any_sync(0xffffffffu, top != m)) {
+        const float keep = __expf(m - base);
+        z *= keep;
+#pragma unroll
+        for (int x = 0; x < VP; ++x) acc[x] = __fmul2_rn(acc[x], make_float2(keep, keep));
+      }
+      m = top;
+      const float p = __expf(score - base);
+      z += p;
+      const bool hide = __any_sync(0xffffffffu, in && score == EQMP_NEG_INF);  // a weight of 0 would keep a NaN
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float pu = __shfl_sync(0xffffffffu, p, lane - l + u);
+        add_row<T, VN>(at + (u * Shape::VECS + KN) * 512, pu, acc, hide && __shfl_sync(0xffffffffu, score, lane - l + u) == EQMP_NEG_INF);
+      }
+      if (++stage == Shape::STAGES) stage = 0;
+    }
+    z += __shfl_xor_sync(0xffffffffu, z, 1);
+    z += __shfl_xor_sync(0xffffffffu, z, 2);
+    if (!mine) continue;
+    if (slot >= 0) {
+      float* to = a.part + ((long long)slot * a.H + h) * (a.Dv + 2);
+      if (l == 0) to[0] = m, to[1] = z;
+      store_row_part<T, G, VN>(to + 2, l, a.Dv, acc);
+      continue;
+    }
+    const long long to = (long long)(w.row + i) * a.H + h;
+    if (a.stats && l == 0) {
+      a.stats[2 * to] = z == 0.0f ? 0.0f : m;
+      a.stats[2 * to + 1] = z;
+    }
+    if (a.out) store_row<T, G, VN>(static_cast<T*>(a.out) + to * a.Dv, l, a.Dv, acc, z == 0.0f ? 0.0f : 1.0f / z);
+  }
+  copy_wait<0>();
+}
+
+// ---------------------------------------------------------------- backward
+template <typename T, int G, int KN, int VN>
+__global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(AttnArgs a) {
+  using Shape = RingShape<G, KN, VN, 4>;
+  constexpr int U = Shape::U, V = 16 / sizeof(T), KP = KN * V / 2, VP = VN * V / 2;
+  extern __shared__ __align__(128) uint8_t space[];
+  const Rows rows{a.off, a.N, a.E, a.block, a.blocks};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G, hh = lane / G;
+  const Work w = find_work(rows, blockIdx.x * kRingWarps + warp, a.rows_each);
+  if (w.n == 0) return;
+  const int h = blockIdx.y * (32 / G) + hh;
+  const bool mine = h < a.H;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(space) + warp * Shape::WARP, at_lane = ring + lane * 16;
+  const T* const k = static_cast<const T*>(a.k) + (long long)h * a.D + l * V;
+  const T* const v = static_cast<const T*>(a.v) + (long long)h * a.Dv + l * V;
+
+  Walk put;
+  put.start(w);
+  Ahead src;
+  src.start(a.src, put.e, a.E);
+  int put_stage = 0;
+  auto copy_batch = [&] {
+    if (!put.over(w)) {
+      src.to(a.src, put.e, a.E);
+      const int mine_src = src.from(put.e);
+      const uint32_t to = at_lane + put_stage * Shape::BATCH;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = __shfl_sync(0xffffffffu, mine_src, u);
+        const bool ok = mine && put.e + u < put.end && (unsigned)j < (unsigned)a.Ns;
+        const T *kr = k + (ok ? j * a.k_ld : 0), *vr = v + (ok ? j * a.v_ld : 0);
+#pragma unroll
+        for (int i = 0; i < KN; ++i)
+          copy_async16(to + (u * Shape::VECS + i) * 512, kr + i * G * V, ok && (i * G + l) * V < a.D);
+#pragma unroll
+        for (int i = 0; i < VN; ++i)
+          copy_async16(to + (u * Shape::VECS + KN + i) * 512, vr + i * G * V, ok && (i * G + l) * V < a.Dv);
+      }
+      if (a.bias && l < U && mine && put.e + l < put.end)
+        copy_async<4>(ring + put_stage * Shape::BATCH + Shape::SMALL_AT + (hh * U + l) * 4, a.bias + (long long)(put.e + l) * a.H + h, true);
+      put.e += U;
+      put.next_row(w);
+    }
+    copy_commit();
+    if (++put_stage == Shape::STAGES) put_stage = 0;
+  };
+#pragma unroll
+  for (int i = 0; i < Shape::STAGES - 1; ++i) copy_batch();
+
+  float4 q_next[KN], g_next[VN];
+  float2 st_next;
+  auto load_next = [&](int i) {
+    const bool ok = mine && i < w.n;
+    load_row<T, G, KN>(static_cast<const T*>(a.q) + (w.row + i) * a.q_ld + (long long)h * a.D, l, a.D, ok, q_next);
+    load_row<T, G, VN>(static_cast<const T*>(a.g) + (w.row + i) * a.g_ld + (long long)h * a.Dv, l, a.Dv, ok, g_next);
+    const float* st = a.stats + 2 * ((long long)(w.row + i) * a.H + h);
+    st_next = ok ? make_float2(__ldg(st), __ldg(st + 1)) : make_float2(0.0f, 0.0f);
+  };
+  load_next(0);
+  int stage = 0;
+  for (int i = 0; i < w.n; ++i) {
+    const int e0 = __shfl_sync(0xffffffffu, w.e0, i), e1 = __shfl_sync(0xffffffffu, w.e1, i);
+    const int slot = __shfl_sync(0xffffffffu, w.slot, i);
+    float2 q[KP], g[VP], pdk[KP], pk[KP];
+    unpack<T, KN>(q_next, a.scale, q);
+    unpack<T, VN>(g_next, 1.0f, g);
+    const float m = st_next.x, z = st_next.y, rz = 1.0f / z;
+    load_next(i + 1);
+#pragma unroll
+    for (int x = 0; x < KP; ++x) pdk[x] = pk[x] = make_float2(0.0f, 0.0f);
+    float delta = 0.0f;
+    for (int e = e0; e < e1; e += U) {
+      copy_wait<Shape::STAGES - 2>();
+      __syncwarp();
+      copy_batch();
+      const uint32_t at = at_lane + stage * Shape::BATCH;
+      float s[2 * U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        s[u] = dot_row<T, KN>(at + u * Shape::VECS * 512, q);
+        s[U + u] = dot_row<T, VN>(at + (u * Shape::VECS + KN) * 512, g);
+      }
+      const float one = scatter_sum<G, 2 * U>(s, l), other = __shfl_xor_sync(0xffffffffu, one, U);
+      float score = l & U ? other : one, dp = l & U ? one : other;  // of edge e + l % U
+      const bool in = e + l % U < e1;
+      const float bias = a.bias && mine && in ? lds32(ring + stage * Shape::BATCH + Shape::SMALL_AT + (hh * U + l % U) * 4) : 0.0f;
+      score = bias == EQMP_NEG_INF ? EQMP_NEG_INF : score + bias;
+      const bool left_out = !in || score == EQMP_NEG_INF || z == 0.0f;
+      const float p = left_out ? 0.0f : __expf(score - m) * rz;
+      dp = left_out ? 0.0f : dp;
+      if (a.pd && l < U && mine && in) a.pd[(long long)(e + l) * a.H + h] = make_float2(left_out ? -1.0f : p, dp);
+      const float pdp = p * dp;
+      delta += pdp;
+      const unsigned out = __ballot_sync(0xffffffffu, in && left_out);  // a weight of 0 would keep a NaN
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float pu = __shfl_sync(0xffffffffu, p, lane - l + u), pdpu = __shfl_sync(0xffffffffu, pdp, lane - l + u);
+        const bool hide = out && (out >> (lane - l + u) & 1);
+        const uint32_t from = at + u * Shape::VECS * 512;
+#pragma unroll
+        for (int j = 0; j < KN; ++j) {
+          float4 vec = lds128(from + j * 512);
+          if (hide) vec = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          float2 x[V / 2];
+          pairs_of<T>(vec, x);
+#pragma unroll
+          for (int y = 0; y < V / 2; ++y) {
+            pk[j * V / 2 + y] = __ffma2_rn(make_float2(pu, pu), x[y], pk[j * V / 2 + y]);
+            pdk[j * V / 2 + y] = __ffma2_rn(make_float2(pdpu, pdpu), x[y], pdk[j * V / 2 + y]);
+          }
+        }
+      }
+      if (++stage == Shape::STAGES) stage = 0;
+    }
+    delta += __shfl_xor_sync(0xffffffffu, delta, 1);
+    delta += __shfl_xor_sync(0xffffffffu, delta, 2);
+    if (!mine) continue;
+    if (slot >= 0) {
+      float* to = a.part + ((long long)slot * a.H + h) * (2 * a.D + 1);
+      if (l == 0) to[0] = delta;
+      store_row_part<T, G, KN>(to + 1, l, a.D, pdk);
+      store_row_part<T, G, KN>(to + 1 + a.D, l, a.D, pk);
+      continue;
+    }
+    const long long to = (long long)(w.row + i) * a.H + h;
+    if (l == 0) a.delta[to] = delta;
+    if (a.gq) {
+#pragma unroll
+      for (int x = 0; x < KP; ++x) pdk[x] = __ffma2_rn(make_float2(-delta, -delta), pk[x], pdk[x]);
+      store_row<T, G, KN>(static_cast<T*>(a.gq) + to * a.D, l, a.D, pdk, a.scale);
+    }
+  }
+  copy_wait<0>();
+}
+
+template <typename T, int G, int KN, int VN>
+__global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(AttnArgs a) {
+  using Shape = RingShape<G, KN, VN, 16>;  // p and dp, delta, the edge's number
+  constexpr int U = Shape::U, V = 16 / sizeof(T), KP = KN * V / 2, VP = VN * V / 2, HEADS = 32 / G;
+  constexpr int DELTA_AT = Shape::SMALL_AT + U * HEADS * 8;
+  extern __shared__ __align__(128) uint8_t space[];
+  const Rows rows{a.send_off, a.Ns, a.E_send, a.block, a.blocks};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G, hh = lane / G;
+  const Work w = find_work(rows, blockIdx.x * kRingWarps + warp, a.rows_each);
+  if (w.n == 0) return;
+  const int h = blockIdx.y * HEADS + hh;
+  const bool mine = h < a.H;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(space) + warp * Shape::WARP, at_lane = ring + lane * 16;
+  const T* const q = static_cast<const T*>(a.q) + (long long)h * a.D + l * V;
+  const T* const g = static_cast<const T*>(a.g) + (long long)h * a.Dv + l * V;
+
+  Walk put;
+  put.start(w);
+  // a place's edge is loaded 64 places ahead, its receiver 32
+  Ahead edges;
+  auto receiver = [&](int edge) { return (unsigned)edge < (unsigned)a.E ? __ldg(a.dst + edge) : -1; };
+  int later, dst_now, dst_next;
+  auto start = [&] {
+    edges.start(a.send_edges, put.e, a.E_send);
+    later = edges.load(a.send_edges, put.e + 64 + lane, a.E_send);
+    dst_now = receiver(edges.now);
+    dst_next = receiver(edges.next);
+  };
+  start();
+  int put_stage = 0;
+  auto copy_batch = [&] {
+    if (!put.over(w)) {
+      if (put.e - edges.c >= 64) {
+        start();
+      } else if (put.e - edges.c >= 32) {
+        edges.c += 32;
+        edges.now = edges.next;
+        edges.next = later;
+        later = edges.load(a.send_edges, edges.c + 64 + lane, a.E_send);
+        dst_now = dst_next;
+        dst_next = receiver(edges.next);
+      }
+      const int at = put.e - edges.c + lane, my_edge = edges.from(put.e);
+      const int d0 = __shfl_sync(0xffffffffu, dst_now, at & 31), d1 = __shfl_sync(0xffffffffu, dst_next, at & 31);
+      const int my_dst = at < 32 ? d0 : d1;
+      const uint32_t stage_at = ring + put_stage * Shape::BATCH, to = at_lane + put_stage * Shape::BATCH;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = __shfl_sync(0xffffffffu, my_dst, u);
+        const bool ok = mine && put.e + u < put.end && (unsigned)i < (unsigned)a.N;
+        const T *qr = q + (ok ? i * a.q_ld : 0), *gr = g + (ok ? i * a.g_ld : 0);
+#pragma unroll
+        for (int x = 0; x < KN; ++x)
+          copy_async16(to + (u * Shape::VECS + x) * 512, qr + x * G * V, ok && (x * G + l) * V < a.D);
+#pragma unroll
+        for (int x = 0; x < VN; ++x)
+          copy_async16(to + (u * Shape::VECS + KN + x) * 512, gr + x * G * V, ok && (x * G + l) * V < a.Dv);
+      }
+      // lane l < U of a head: the small values of edge l; p = -1 where there is no such edge
+      const int e = __shfl_sync(0xffffffffu, my_edge, l % U), i = __shfl_sync(0xffffffffu, my_dst, l % U);
+      if (l < U) {
+        const bool in = mine && put.e + l < put.end, ok = in && (unsigned)i < (unsigned)a.N;
+        const uint32_t pd = stage_at + Shape::SMALL_AT + (hh * U + l) * 8, delta = stage_at + DELTA_AT + (hh * U + l) * 4;
+        if (ok) {
+          copy_async<8>(pd, a.pd + (long long)e * a.H + h, true);
+          copy_async<4>(delta, a.delta + (long long)i * a.H + h, true);
+        } else {
+          asm volatile("st.shared.v2.f32 [%0], {%1, %1};" ::"r"(pd), "f"(-1.0f) : "memory");
+        }
+        asm volatile("st.shared.s32 [%0], %1;" ::"r"(delta + U * HEADS * 4), "r"(in ? e : -1) : "memory");
+      }
+      put.e += U;
+      put.next_row(w);
+    }
+    copy_commit();
+    if (++put_stage == Shape::STAGES) put_stage = 0;
+  };
+#pragma unroll
+  for (int i = 0; i < Shape::STAGES - 1; ++i) copy_batch();
+
+  int stage = 0;
+  for (int i = 0; i < w.n; ++i) {
+    const int e0 = __shfl_sync(0xffffffffu, w.e0, i), e1 = __shfl_sync(0xffffffffu, w.e1, i);
+    const int slot = __shfl_sync(0xffffffffu, w.slot, i);
+    float2 gk[KP], gv[VP];
+#pragma unroll
+    for (int x = 0; x < KP; ++x) gk[x] = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int x = 0; x < VP; ++x) gv[x] = make_float2(0.0f, 0.0f);
+    for (int c = e0; c < e1; c += U) {
+      copy_wait<Shape::STAGES - 2>();
+      __syncwarp();
+      copy_batch();
+      const uint32_t stage_at = ring + stage * Shape::BATCH, at = at_lane + stage * Shape::BATCH;
+      // the lane's own edge: l % U
+      const uint32_t item = hh * U + l % U;
+      const float2 pd = lds64(stage_at + Shape::SMALL_AT + item * 8);
+      const bool left_out = pd.x < 0.0f;
+      const float p = left_out ? 0.0f : pd.x, ds = left_out ? 0.0f : p * (pd.y - lds32(stage_at + DELTA_AT + item * 4));
+      if (a.gbias && l < U && mine) {
+        const int edge = __float_as_int(lds32(stage_at + DELTA_AT + (U * HEADS + item) * 4));
+        if ((unsigned)edge < (unsigned)a.E) a.gbias[(long long)edge * a.H + h] = ds;
+      }
+      const unsigned out = __ballot_sync(0xffffffffu, left_out && c + l % U < e1);  // a weight of 0 would keep a NaN
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float pu = __shfl_sync(0xffffffffu, p, lane - l + u), dsu = __shfl_sync(0xffffffffu, ds, lane - l + u);
+        const bool hide = out && (out >> (lane - l + u) & 1);
+        add_row<T, KN>(at + u * Shape::VECS * 512, dsu, gk, hide);
+        add_row<T, VN>(at + (u * Shape::VECS + KN) * 512, pu, gv, hide);
+      }
+      if (++stage == Shape::STAGES) stage = 0;
+    }
+    if (!mine) continue;
+    if (slot >= 0) {
+      float* to = a.part + ((long long)slot * a.H + h) * (a.D + a.Dv);
+      store_row_part<T, G, KN>(to, l, a.D, gk);
+      store_row_part<T, G, VN>(to + a.D, l, a.Dv, gv);
+      continue;
+    }
+    const long long to = (long long)(w.row + i) * a.H + h;
+    if (a.gk) store_row<T, G, KN>(static_cast<T*>(a.gk) + to * a.D, l, a.D, gk, a.scale);
+    if (a.gv) store_row<T, G, VN>(static_cast<T*>(a.gv) + to * a.Dv, l, a.Dv, gv, 1.0f);
+  }
+  copy_wait<0>();
+}
+
+}  // namespace eqmp
