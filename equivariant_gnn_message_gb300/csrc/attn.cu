@@ -82,7 +82,10 @@ static AttnForm form_of(const Sizes& n, int64_t rows, int bytes, bool vectors) {
   return f;
 }
 
-static bool on16(const void* p, long long ld, int bytes) { return aligned(p, 16) && ld * bytes % 16 == 0; }
+// Rows on 16 bytes, below 2^32 bytes apart.
+static bool on16(const void* p, long long ld, int bytes) {
+  return aligned(p, 16) && ld * bytes % 16 == 0 && ld * bytes < 1ll << 32;
+}
 
 }  // namespace eqmp
 

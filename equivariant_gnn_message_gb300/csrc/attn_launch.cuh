@@ -5,6 +5,10 @@
 #include "attn_ring.cuh"
 #include "launch.h"
 
+#ifndef TUNE_U
+#define TUNE_U (KN + VN <= 5 ? 4 : 2)
+#endif
+
 namespace eqmp {
 
 enum { kAttnFwd, kAttnRecv, kAttnSend };
@@ -59,7 +63,8 @@ eqmp_status launch_attn_form(const AttnArgs& a, cudaStream_t st) {
 
 template <int PASS, typename T, int G, int KN, int VN>
 eqmp_status launch_attn_ring(const AttnArgs& a, cudaStream_t st) {
-  constexpr int SMEM = RingShape<G, KN, VN, PASS == kAttnSend ? 16 : 4>::CTA;
+  constexpr int U = TUNE_U;
+  constexpr int SMEM = RingShape<G, KN, VN, U, PASS == kAttnSend ? 16 : 4>::CTA;
   const long long rows = PASS == kAttnSend ? a.Ns : a.N, workers = a.blocks + (rows + a.rows_each - 1) / a.rows_each;
   const dim3 grid((unsigned)((workers + kRingWarps - 1) / kRingWarps), (unsigned)((a.H * G + 31) / 32));
   static unsigned long long done = 0;
@@ -69,11 +74,11 @@ eqmp_status launch_attn_ring(const AttnArgs& a, cudaStream_t st) {
     return launch_attn_join<PASS, T>(a, st);
   };
   if constexpr (PASS == kAttnFwd)
-    return run(k_attn_fwd_ring<T, G, KN, VN>);
+    return run(k_attn_fwd_ring<T, G, KN, VN, U>);
   else if constexpr (PASS == kAttnRecv)
-    return run(k_attn_recv_ring<T, G, KN, VN>);
+    return run(k_attn_recv_ring<T, G, KN, VN, U>);
   else
-    return run(k_attn_send_ring<T, G, KN, VN>);
+    return run(k_attn_send_ring<T, G, KN, VN, U>);
 }
 
 template <int PASS, typename T, int G>

@@ -4,7 +4,8 @@
 // edges, U at a time.  The edges' rows come through a ring in shared memory by
 // asynchronous copies, STAGES - 1 batches ahead and across the ends of rows, so
 // that neither the indices nor the rows are waited for; a lane copies just the
-// bytes that it will read itself.  What is left is bound by the gather through
+// bytes that it will read itself.  Places of a batch behind its row's end are
+// filled with zeros.  What is left is bound by the gather through
 // L2 (and by DRAM where the heads of a launch's slice of all nodes do not stay
 // in L2).
 #pragma once
@@ -13,14 +14,20 @@
 
 namespace eqmp {
 
-constexpr int kRingWarps = 2;  // of a CTA
+#ifndef TUNE_WARPS
+#define TUNE_WARPS 2
+#endif
+#ifndef TUNE_STAGES
+#define TUNE_STAGES 2
+#endif
+constexpr int kRingWarps = TUNE_WARPS;  // of a CTA
 
-__device__ __forceinline__ void copy_async16(uint32_t to, const void* from, bool ok) {  // zeros where not ok
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(ok ? 16 : 0) : "memory");
+__device__ __forceinline__ void copy_async16(uint32_t to, const void* from, int bytes) {  // 16, or 0 for zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 template <int N>
-__device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool ok) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(N), "r"(ok ? N : 0) : "memory");
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(N) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -156,16 +163,16 @@ __device__ __forceinline__ float scatter_sum(float (&v)[NV], int l) {
   return v[0];
 }
 
-// The shape of a ring: U edges a batch, each of A + B vectors a lane, and per
+// The shape of a ring: U edges a batch, each of KN + VN vectors a lane, and per
 // batch a few bytes for every edge and head.
-template <int G, int A, int B, int SMALL>
+template <int G, int KN, int VN, int U_, int SMALL>
 struct RingShape {
-  static constexpr int VECS = A + B;
-  static constexpr int U = 4;
+  static constexpr int VECS = KN + VN;
+  static constexpr int U = U_;
   static constexpr int HEADS = 32 / G;
   static constexpr int SMALL_AT = U * VECS * 512;
   static constexpr int BATCH = SMALL_AT + (U * HEADS * SMALL + 127) / 128 * 128;
-  static constexpr int STAGES = VECS <= 2 ? 4 : VECS <= 6 ? 3 : 2;
+  static constexpr int STAGES = TUNE_STAGES;
   static constexpr int WARP = STAGES * BATCH;
   static constexpr int CTA = kRingWarps * WARP;
 };
@@ -190,18 +197,15 @@ __device__ __forceinline__ void unpack(const float4 (&v)[NV], float by, float2 (
   }
 }
 
-// sum += by * the lane's vectors at `at` (512 bytes apart); nothing where a
-// left-out edge's row must not be seen.
+// sum += by * the lane's vectors at `at` (512 bytes apart).
 template <typename T, int NV>
-__device__ __forceinline__ void add_row(uint32_t at, float by, float2 (&sum)[NV * 8 / sizeof(T)], bool hide) {
+__device__ __forceinline__ void add_row(uint32_t at, float by, float2 (&sum)[NV * 8 / sizeof(T)]) {
   constexpr int P = 8 / sizeof(T);
   const float2 b = make_float2(by, by);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    float4 v = lds128(at + j * 512);
-    if (hide) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float2 p[P];
-    pairs_of<T>(v, p);
+    pairs_of<T>(lds128(at + j * 512), p);
 #pragma unroll
     for (int i = 0; i < P; ++i) sum[j * P + i] = __ffma2_rn(b, p[i], sum[j * P + i]);
   }
@@ -246,11 +250,100 @@ __device__ __forceinline__ void store_row_part(float* row, int l, int cols, cons
     }
 }
 
+// The lane's vectors of a node's head: where they lie, and which of them the
+// lane has.  Rows lie `pitch` bytes apart, below 2^32.
+template <typename T, int G, int NV>
+struct Lanes {
+  const char* base;
+  uint32_t pitch;
+  bool has[NV];
+  __device__ __forceinline__ Lanes(const void* p, long long ld, int h, int cols, int l, bool mine)
+      : base(static_cast<const char*>(p) + ((long long)h * cols + l * (16 / sizeof(T))) * sizeof(T)), pitch((uint32_t)(ld * sizeof(T))) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) has[i] = mine && (i * G + l) * (int)(16 / sizeof(T)) < cols;
+  }
+  __device__ __forceinline__ void copy(uint32_t to, uint32_t node, int bytes) const {
+    const char* from = base + (unsigned long long)node * pitch;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (has[i]) copy_async16(to + i * 512, from + i * G * 16, bytes);
+  }
+  // Zeros where no copy will write.
+  __device__ __forceinline__ void clear(uint32_t at) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (!has[i]) asm volatile("st.shared.v4.f32 [%0], {%1, %1, %1, %1};" ::"r"(at + i * 512), "f"(0.0f) : "memory");
+  }
+};
+
+template <typename Shape, typename A, typename B>
+__device__ __forceinline__ void clear_ring(const A& a, const B& b, int a_vecs, uint32_t at_lane) {
+#pragma unroll 1
+  for (int i = 0; i < Shape::STAGES * Shape::U; ++i) {
+    const uint32_t at = at_lane + i / Shape::U * Shape::BATCH + i % Shape::U * Shape::VECS * 512;
+    a.clear(at);
+    b.clear(at + a_vecs * 512);
+  }
+}
+
+// Keys, values and biases of the receivers' passes, into the stages in turn.
+template <typename T, int G, int KN, int VN, int U_>
+struct Feed {
+  using Shape = RingShape<G, KN, VN, U_, 4>;
+  const Lanes<T, G, KN> k;
+  const Lanes<T, G, VN> v;
+  const float* const bias;  // of edge l and the lane's head; NULL: none for this lane
+  const int l;
+  uint32_t to, to_bias;  // where the next batch goes
+  int stage;
+  Walk put;
+  Ahead src;
+
+  __device__ __forceinline__ Feed(const AttnArgs& a, const Work& w, uint32_t ring, int lane, int l, int hh, int h, bool mine)
+      : k(a.k, a.k_ld, h, a.D, l, mine), v(a.v, a.v_ld, h, a.Dv, l, mine),
+        bias(a.bias && mine && l < Shape::U ? a.bias + (long long)l * a.H + h : nullptr), l(l), to(ring + lane * 16),
+        to_bias(ring + Shape::SMALL_AT + (hh * Shape::U + l) * 4), stage(0) {
+    clear_ring<Shape>(k, v, KN, to);
+    put.start(w);
+    src.start(a.src, put.e, a.E);
+#pragma unroll
+    for (int i = 0; i < Shape::STAGES - 1; ++i) batch(a, w);
+  }
+  __device__ __forceinline__ void batch(const AttnArgs& a, const Work& w) {
+    if (!put.over(w)) {
+      src.to(a.src, put.e, a.E);
+      int node = src.from(put.e);
+      const int n = put.end - put.e;
+      const bool ok = (unsigned)node < (unsigned)a.Ns;  // a sender that is none reads as zeros
+      const unsigned there = __ballot_sync(0xffffffffu, ok) & (n < Shape::U ? (1u << n) - 1 : 0xffffffffu);
+      node = ok ? node : 0;
+#pragma unroll
+      for (int u = 0; u < Shape::U; ++u) {
+        const int j = __shfl_sync(0xffffffffu, node, u), bytes = (there >> u & 1) * 16;
+        k.copy(to + u * Shape::VECS * 512, j, bytes);
+        v.copy(to + (u * Shape::VECS + KN) * 512, j, bytes);
+      }
+      if (bias && l < n) copy_async<4>(to_bias, bias + (long long)put.e * a.H);
+      put.e += Shape::U;
+      put.next_row(w);
+    }
+    copy_commit();
+    const bool wrap = ++stage == Shape::STAGES;
+    if (wrap) stage = 0;
+    const uint32_t step = wrap ? (uint32_t)(-(Shape::STAGES - 1) * Shape::BATCH) : (uint32_t)Shape::BATCH;
+    to += step;
+    to_bias += step;
+  }
+};
+
+// Place u of a batch is left out, by a ballot of the lanes' own places.
+__device__ __forceinline__ bool is_out(unsigned out, int lane, int l, int u) { return out >> (lane - l + u) & 1; }
+
 // ---------------------------------------------------------------- forward
-template <typename T, int G, int KN, int VN>
-__global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(AttnArgs a) {
-  using Shape = RingShape<G, KN, VN, 4>;
-  constexpr int U = Shape::U, V = 16 / sizeof(T), KP = KN * V / 2, VP = VN * V / 2;
+template <typename T, int G, int KN, int VN, int U>
+__global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_constant__ AttnArgs a) {
+  using Shape = RingShape<G, KN, VN, U, 4>;
+  constexpr int V = 16 / sizeof(T), KP = KN * V / 2, VP = VN * V / 2;
   extern __shared__ __align__(128) uint8_t space[];
   const Rows rows{a.off, a.N, a.E, a.block, a.blocks};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G, hh = lane / G;
@@ -258,72 +351,43 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(AttnArgs a) {
   if (w.n == 0) return;
   const int h = blockIdx.y * (32 / G) + hh;
   const bool mine = h < a.H;
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(space) + warp * Shape::WARP, at_lane = ring + lane * 16;
-  const T* const k = static_cast<const T*>(a.k) + (long long)h * a.D + l * V;
-  const T* const v = static_cast<const T*>(a.v) + (long long)h * a.Dv + l * V;
-
-  Walk put;
-  put.start(w);
-  Ahead src;
-  src.start(a.src, put.e, a.E);
-  int put_stage = 0;
-  auto copy_batch = [&] {  // the next batch's rows and biases, into the stage that has been read
-    if (!put.over(w)) {
-      src.to(a.src, put.e, a.E);
-      const int mine_src = src.from(put.e);
-      const uint32_t to = at_lane + put_stage * Shape::BATCH;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int j = __shfl_sync(0xffffffffu, mine_src, u);
-        const bool ok = mine && put.e + u < put.end && (unsigned)j < (unsigned)a.Ns;
-        const T *kr = k + (ok ? j * a.k_ld : 0), *vr = v + (ok ? j * a.v_ld : 0);
-#pragma unroll
-        for (int i = 0; i < KN; ++i)
-          copy_async16(to + (u * Shape::VECS + i) * 512, kr + i * G * V, ok && (i * G + l) * V < a.D);
-#pragma unroll
-        for (int i = 0; i < VN; ++i)
-          copy_async16(to + (u * Shape::VECS + KN + i) * 512, vr + i * G * V, ok && (i * G + l) * V < a.Dv);
-      }
-      if (a.bias && l < U && mine && put.e + l < put.end)
-        copy_async<4>(ring + put_stage * Shape::BATCH + Shape::SMALL_AT + (hh * U + l) * 4, a.bias + (long long)(put.e + l) * a.H + h, true);
-      put.e += U;
-      put.next_row(w);
-    }
-    copy_commit();
-    if (++put_stage == Shape::STAGES) put_stage = 0;
-  };
-#pragma unroll
-  for (int i = 0; i < Shape::STAGES - 1; ++i) copy_batch();
-
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(space) + warp * Shape::WARP;
+  Feed<T, G, KN, VN, U> feed(a, w, ring, lane, l, hh, h, mine);
   float4 q_next[KN];
   auto load_q = [&](int i) {
     load_row<T, G, KN>(static_cast<const T*>(a.q) + (w.row + i) * a.q_ld + (long long)h * a.D, l, a.D, mine && i < w.n, q_next);
   };
   load_q(0);
-  int stage = 0;
+  const uint32_t at0 = ring + lane * 16, bias0 = ring + Shape::SMALL_AT + (hh * U + l % U) * 4;
+  uint32_t stage_at = 0;
+#pragma unroll 1
   for (int i = 0; i < w.n; ++i) {
     const int e0 = __shfl_sync(0xffffffffu, w.e0, i), e1 = __shfl_sync(0xffffffffu, w.e1, i);
-    const int slot = __shfl_sync(0xffffffffu, w.slot, i);
     float2 q[KP], acc[VP];
     unpack<T, KN>(q_next, a.scale, q);
     load_q(i + 1);
 #pragma unroll
     for (int x = 0; x < VP; ++x) acc[x] = make_float2(0.0f, 0.0f);
     float m = EQMP_NEG_INF, z = 0.0f;  // z: of the edges of the lane's place in a batch
+#pragma unroll 1
     for (int e = e0; e < e1; e += U) {
       copy_wait<Shape::STAGES - 2>();
       __syncwarp();
-      copy_batch();
-      const uint32_t at = at_lane + stage * Shape::BATCH;
+      feed.batch(a, w);
+      const uint32_t at = at0 + stage_at;
       float s[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) s[u] = dot_row<T, KN>(at + u * Shape::VECS * 512, q);
       float score = scatter_sum<G, U>(s, l);  // of edge e + l % U
-      const bool in = e + l % U < e1;
-      const float bias = a.bias && mine && in ? lds32(ring + stage * Shape::BATCH + Shape::SMALL_AT + (hh * U + l % U) * 4) : 0.0f;
-      score = !in || bias == EQMP_NEG_INF ? EQMP_NEG_INF : score + bias;
-      float top = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const bool in = mine && e + l % U < e1;
+      if (a.bias) {
+        const float bias = lds32(bias0 + stage_at);
+        score = bias == EQMP_NEG_INF ? EQMP_NEG_INF : score + bias;
+      }
+      if (!in) score = EQMP_NEG_INF;
+      float top = score;
+#pragma unroll
+      for (int o = 1; o < U; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       top = fmaxf(top, m);
       const float base = top == EQMP_NEG_INF ? 0.0f : top;
       if (__any_sync(0xffffffffu, top != m)) {
@@ -335,16 +399,22 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(AttnArgs a) {
       m = top;
       const float p = __expf(score - base);
       z += p;
-      const bool hide = __any_sync(0xffffffffu, in && score == EQMP_NEG_INF);  // a weight of 0 would keep a NaN
+      const unsigned out = __ballot_sync(0xffffffffu, in && score == EQMP_NEG_INF);
+      if (out) {  // left out: a weight of 0 would keep a NaN
+#pragma unroll 1
+        for (int u = 0; u < U; ++u) {
+          const float pu = __shfl_sync(0xffffffffu, p, lane - l + u);
+          if (!is_out(out, lane, l, u)) add_row<T, VN>(at + (u * Shape::VECS + KN) * 512, pu, acc);
+        }
+      } else {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float pu = __shfl_sync(0xffffffffu, p, lane - l + u);
-        add_row<T, VN>(at + (u * Shape::VECS + KN) * 512, pu, acc, hide && __shfl_sync(0xffffffffu, score, lane - l + u) == EQMP_NEG_INF);
+        for (int u = 0; u < U; ++u) add_row<T, VN>(at + (u * Shape::VECS + KN) * 512, __shfl_sync(0xffffffffu, p, lane - l + u), acc);
       }
-      if (++stage == Shape::STAGES) stage = 0;
+      stage_at = stage_at == (Shape::STAGES - 1) * Shape::BATCH ? 0 : stage_at + Shape::BATCH;
     }
-    z += __shfl_xor_sync(0xffffffffu, z, 1);
-    z += __shfl_xor_sync(0xffffffffu, z, 2);
+#pragma unroll
+    for (int o = 1; o < U; o *= 2) z += __shfl_xor_sync(0xffffffffu, z, o);
+    const int slot = __shfl_sync(0xffffffffu, w.slot, i);
     if (!mine) continue;
     if (slot >= 0) {
       float* to = a.part + ((long long)slot * a.H + h) * (a.Dv + 2);
@@ -363,10 +433,10 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------- backward
-template <typename T, int G, int KN, int VN>
-__global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(AttnArgs a) {
-  using Shape = RingShape<G, KN, VN, 4>;
-  constexpr int U = Shape::U, V = 16 / sizeof(T), KP = KN * V / 2, VP = VN * V / 2;
+template <typename T, int G, int KN, int VN, int U>
+__global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(const __grid_constant__ AttnArgs a) {
+  using Shape = RingShape<G, KN, VN, U, 4>;
+  constexpr int V = 16 / sizeof(T), KP = KN * V / 2, VP = VN * V / 2;
   extern __shared__ __align__(128) uint8_t space[];
   const Rows rows{a.off, a.N, a.E, a.block, a.blocks};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G, hh = lane / G;
@@ -374,43 +444,8 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(AttnArgs a) 
   if (w.n == 0) return;
   const int h = blockIdx.y * (32 / G) + hh;
   const bool mine = h < a.H;
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(space) + warp * Shape::WARP, at_lane = ring + lane * 16;
-  const T* const k = static_cast<const T*>(a.k) + (long long)h * a.D + l * V;
-  const T* const v = static_cast<const T*>(a.v) + (long long)h * a.Dv + l * V;
-
-  Walk put;
-  put.start(w);
-  Ahead src;
-  src.start(a.src, put.e, a.E);
-  int put_stage = 0;
-  auto copy_batch = [&] {
-    if (!put.over(w)) {
-      src.to(a.src, put.e, a.E);
-      const int mine_src = src.from(put.e);
-      const uint32_t to = at_lane + put_stage * Shape::BATCH;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int j = __shfl_sync(0xffffffffu, mine_src, u);
-        const bool ok = mine && put.e + u < put.end && (unsigned)j < (unsigned)a.Ns;
-        const T *kr = k + (ok ? j * a.k_ld : 0), *vr = v + (ok ? j * a.v_ld : 0);
-#pragma unroll
-        for (int i = 0; i < KN; ++i)
-          copy_async16(to + (u * Shape::VECS + i) * 512, kr + i * G * V, ok && (i * G + l) * V < a.D);
-#pragma unroll
-        for (int i = 0; i < VN; ++i)
-          copy_async16(to + (u * Shape::VECS + KN + i) * 512, vr + i * G * V, ok && (i * G + l) * V < a.Dv);
-      }
-      if (a.bias && l < U && mine && put.e + l < put.end)
-        copy_async<4>(ring + put_stage * Shape::BATCH + Shape::SMALL_AT + (hh * U + l) * 4, a.bias + (long long)(put.e + l) * a.H + h, true);
-      put.e += U;
-      put.next_row(w);
-    }
-    copy_commit();
-    if (++put_stage == Shape::STAGES) put_stage = 0;
-  };
-#pragma unroll
-  for (int i = 0; i < Shape::STAGES - 1; ++i) copy_batch();
-
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(space) + warp * Shape::WARP;
+  Feed<T, G, KN, VN, U> feed(a, w, ring, lane, l, hh, h, mine);
   float4 q_next[KN], g_next[VN];
   float2 st_next;
   auto load_next = [&](int i) {
@@ -421,10 +456,11 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(AttnArgs a) 
     st_next = ok ? make_float2(__ldg(st), __ldg(st + 1)) : make_float2(0.0f, 0.0f);
   };
   load_next(0);
-  int stage = 0;
+  const uint32_t at0 = ring + lane * 16, bias0 = ring + Shape::SMALL_AT + (hh * U + l % U) * 4;
+  uint32_t stage_at = 0;
+#pragma unroll 1
   for (int i = 0; i < w.n; ++i) {
     const int e0 = __shfl_sync(0xffffffffu, w.e0, i), e1 = __shfl_sync(0xffffffffu, w.e1, i);
-    const int slot = __shfl_sync(0xffffffffu, w.slot, i);
     float2 q[KP], g[VP], pdk[KP], pk[KP];
     unpack<T, KN>(q_next, a.scale, q);
     unpack<T, VN>(g_next, 1.0f, g);
@@ -433,51 +469,71 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(AttnArgs a) 
 #pragma unroll
     for (int x = 0; x < KP; ++x) pdk[x] = pk[x] = make_float2(0.0f, 0.0f);
     float delta = 0.0f;
+#pragma unroll 1
     for (int e = e0; e < e1; e += U) {
       copy_wait<Shape::STAGES - 2>();
       __syncwarp();
-      copy_batch();
-      const uint32_t at = at_lane + stage * Shape::BATCH;
-      float s[2 * U];
+      feed.batch(a, w);
+      const uint32_t at = at0 + stage_at;
+      float score, dp;  // of edge e + l % U
+      if constexpr (2 * U <= G) {
+        float s[2 * U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        s[u] = dot_row<T, KN>(at + u * Shape::VECS * 512, q);
-        s[U + u] = dot_row<T, VN>(at + (u * Shape::VECS + KN) * 512, g);
+        for (int u = 0; u < U; ++u) {
+          s[u] = dot_row<T, KN>(at + u * Shape::VECS * 512, q);
+          s[U + u] = dot_row<T, VN>(at + (u * Shape::VECS + KN) * 512, g);
+        }
+        const float one = scatter_sum<G, 2 * U>(s, l), other = __shfl_xor_sync(0xffffffffu, one, U);
+        score = l & U ? other : one;
+        dp = l & U ? one : other;
+      } else {
+        float s[U], d[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          s[u] = dot_row<T, KN>(at + u * Shape::VECS * 512, q);
+          d[u] = dot_row<T, VN>(at + (u * Shape::VECS + KN) * 512, g);
+        }
+        score = scatter_sum<G, U>(s, l);
+        dp = scatter_sum<G, U>(d, l);
       }
-      const float one = scatter_sum<G, 2 * U>(s, l), other = __shfl_xor_sync(0xffffffffu, one, U);
-      float score = l & U ? other : one, dp = l & U ? one : other;  // of edge e + l % U
-      const bool in = e + l % U < e1;
-      const float bias = a.bias && mine && in ? lds32(ring + stage * Shape::BATCH + Shape::SMALL_AT + (hh * U + l % U) * 4) : 0.0f;
-      score = bias == EQMP_NEG_INF ? EQMP_NEG_INF : score + bias;
-      const bool left_out = !in || score == EQMP_NEG_INF || z == 0.0f;
-      const float p = left_out ? 0.0f : __expf(score - m) * rz;
-      dp = left_out ? 0.0f : dp;
-      if (a.pd && l < U && mine && in) a.pd[(long long)(e + l) * a.H + h] = make_float2(left_out ? -1.0f : p, dp);
+      const bool in = mine && e + l % U < e1;
+      if (a.bias) {
+        const float bias = lds32(bias0 + stage_at);
+        score = bias == EQMP_NEG_INF ? EQMP_NEG_INF : score + bias;
+      }
+      const bool left_out = score == EQMP_NEG_INF || z == 0.0f;
+      const float p = left_out || !in ? 0.0f : __expf(score - m) * rz;
+      dp = left_out || !in ? 0.0f : dp;
+      if (a.pd && l < U && in) a.pd[(long long)(e + l) * a.H + h] = make_float2(left_out ? -1.0f : p, dp);
       const float pdp = p * dp;
       delta += pdp;
-      const unsigned out = __ballot_sync(0xffffffffu, in && left_out);  // a weight of 0 would keep a NaN
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
+      const unsigned out = __ballot_sync(0xffffffffu, in && left_out);  // left out: a weight of 0 would keep a NaN
+      auto add = [&](int u) {
         const float pu = __shfl_sync(0xffffffffu, p, lane - l + u), pdpu = __shfl_sync(0xffffffffu, pdp, lane - l + u);
-        const bool hide = out && (out >> (lane - l + u) & 1);
-        const uint32_t from = at + u * Shape::VECS * 512;
+        if (out && is_out(out, lane, l, u)) return;
 #pragma unroll
         for (int j = 0; j < KN; ++j) {
-          float4 vec = lds128(from + j * 512);
-          if (hide) vec = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           float2 x[V / 2];
-          pairs_of<T>(vec, x);
+          pairs_of<T>(lds128(at + (u * Shape::VECS + j) * 512), x);
 #pragma unroll
           for (int y = 0; y < V / 2; ++y) {
             pk[j * V / 2 + y] = __ffma2_rn(make_float2(pu, pu), x[y], pk[j * V / 2 + y]);
             pdk[j * V / 2 + y] = __ffma2_rn(make_float2(pdpu, pdpu), x[y], pdk[j * V / 2 + y]);
           }
         }
+      };
+      if (out) {
+#pragma unroll 1
+        for (int u = 0; u < U; ++u) add(u);
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) add(u);
       }
-      if (++stage == Shape::STAGES) stage = 0;
+      stage_at = stage_at == (Shape::STAGES - 1) * Shape::BATCH ? 0 : stage_at + Shape::BATCH;
     }
-    delta += __shfl_xor_sync(0xffffffffu, delta, 1);
-    delta += __shfl_xor_sync(0xffffffffu, delta, 2);
+#pragma unroll
+    for (int o = 1; o < U; o *= 2) delta += __shfl_xor_sync(0xffffffffu, delta, o);
+    const int slot = __shfl_sync(0xffffffffu, w.slot, i);
     if (!mine) continue;
     if (slot >= 0) {
       float* to = a.part + ((long long)slot * a.H + h) * (2 * a.D + 1);
@@ -497,11 +553,11 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(AttnArgs a) 
   copy_wait<0>();
 }
 
-template <typename T, int G, int KN, int VN>
-__global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(AttnArgs a) {
-  using Shape = RingShape<G, KN, VN, 16>;  // p and dp, delta, the edge's number
-  constexpr int U = Shape::U, V = 16 / sizeof(T), KP = KN * V / 2, VP = VN * V / 2, HEADS = 32 / G;
-  constexpr int DELTA_AT = Shape::SMALL_AT + U * HEADS * 8;
+template <typename T, int G, int KN, int VN, int U>
+__global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(const __grid_constant__ AttnArgs a) {
+  using Shape = RingShape<G, KN, VN, U, 16>;  // p and dp, delta, the edge's number
+  constexpr int V = 16 / sizeof(T), KP = KN * V / 2, VP = VN * V / 2, HEADS = 32 / G;
+  constexpr int DELTA_AT = Shape::SMALL_AT + U * HEADS * 8, EDGE_AT = DELTA_AT + U * HEADS * 4;
   extern __shared__ __align__(128) uint8_t space[];
   const Rows rows{a.send_off, a.Ns, a.E_send, a.block, a.blocks};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G, hh = lane / G;
@@ -509,9 +565,11 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(AttnArgs a) 
   if (w.n == 0) return;
   const int h = blockIdx.y * HEADS + hh;
   const bool mine = h < a.H;
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(space) + warp * Shape::WARP, at_lane = ring + lane * 16;
-  const T* const q = static_cast<const T*>(a.q) + (long long)h * a.D + l * V;
-  const T* const g = static_cast<const T*>(a.g) + (long long)h * a.Dv + l * V;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(space) + warp * Shape::WARP, at0 = ring + lane * 16;
+  const uint32_t item = hh * U + l % U;  // of the small values: the lane's own edge
+  const Lanes<T, G, KN> q(a.q, a.q_ld, h, a.D, l, mine);
+  const Lanes<T, G, VN> g(a.g, a.g_ld, h, a.Dv, l, mine);
+  clear_ring<Shape>(q, g, KN, at0);
 
   Walk put;
   put.start(w);
@@ -526,7 +584,7 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(AttnArgs a) 
     dst_next = receiver(edges.next);
   };
   start();
-  int put_stage = 0;
+  uint32_t put_at = 0;
   auto copy_batch = [&] {
     if (!put.over(w)) {
       if (put.e - edges.c >= 64) {
@@ -539,77 +597,78 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(AttnArgs a) 
         dst_now = dst_next;
         dst_next = receiver(edges.next);
       }
-      const int at = put.e - edges.c + lane, my_edge = edges.from(put.e);
+      const int at = put.e - edges.c + lane, my_edge = edges.from(put.e), n = put.end - put.e;
       const int d0 = __shfl_sync(0xffffffffu, dst_now, at & 31), d1 = __shfl_sync(0xffffffffu, dst_next, at & 31);
       const int my_dst = at < 32 ? d0 : d1;
-      const uint32_t stage_at = ring + put_stage * Shape::BATCH, to = at_lane + put_stage * Shape::BATCH;
+      const bool ok = lane < n && (unsigned)my_dst < (unsigned)a.N;
+      const unsigned there = __ballot_sync(0xffffffffu, ok);
+      const int node = ok ? my_dst : 0;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = __shfl_sync(0xffffffffu, my_dst, u);
-        const bool ok = mine && put.e + u < put.end && (unsigned)i < (unsigned)a.N;
-        const T *qr = q + (ok ? i * a.q_ld : 0), *gr = g + (ok ? i * a.g_ld : 0);
-#pragma unroll
-        for (int x = 0; x < KN; ++x)
-          copy_async16(to + (u * Shape::VECS + x) * 512, qr + x * G * V, ok && (x * G + l) * V < a.D);
-#pragma unroll
-        for (int x = 0; x < VN; ++x)
-          copy_async16(to + (u * Shape::VECS + KN + x) * 512, gr + x * G * V, ok && (x * G + l) * V < a.Dv);
+        const int i = __shfl_sync(0xffffffffu, node, u), bytes = (there >> u & 1) * 16;
+        q.copy(at0 + put_at + u * Shape::VECS * 512, i, bytes);
+        g.copy(at0 + put_at + (u * Shape::VECS + KN) * 512, i, bytes);
       }
-      // lane l < U of a head: the small values of edge l; p = -1 where there is no such edge
-      const int e = __shfl_sync(0xffffffffu, my_edge, l % U), i = __shfl_sync(0xffffffffu, my_dst, l % U);
+      // lane l < U of a head: the small values of edge l; p = -1 where there is no such edge, or no receiver
+      const int e = __shfl_sync(0xffffffffu, my_edge, l % U), i = __shfl_sync(0xffffffffu, node, l % U);
       if (l < U) {
-        const bool in = mine && put.e + l < put.end, ok = in && (unsigned)i < (unsigned)a.N;
-        const uint32_t pd = stage_at + Shape::SMALL_AT + (hh * U + l) * 8, delta = stage_at + DELTA_AT + (hh * U + l) * 4;
-        if (ok) {
-          copy_async<8>(pd, a.pd + (long long)e * a.H + h, true);
-          copy_async<4>(delta, a.delta + (long long)i * a.H + h, true);
+        const uint32_t small = ring + put_at;
+        if (mine && (there >> l & 1)) {
+          copy_async<8>(small + Shape::SMALL_AT + item * 8, a.pd + (long long)e * a.H + h);
+          copy_async<4>(small + DELTA_AT + item * 4, a.delta + (long long)i * a.H + h);
         } else {
-          asm volatile("st.shared.v2.f32 [%0], {%1, %1};" ::"r"(pd), "f"(-1.0f) : "memory");
+          asm volatile("st.shared.v2.f32 [%0], {%1, %1};" ::"r"(small + Shape::SMALL_AT + item * 8), "f"(-1.0f) : "memory");
         }
-        asm volatile("st.shared.s32 [%0], %1;" ::"r"(delta + U * HEADS * 4), "r"(in ? e : -1) : "memory");
+        asm volatile("st.shared.s32 [%0], %1;" ::"r"(small + EDGE_AT + item * 4), "r"(l < n ? e : -1) : "memory");
       }
       put.e += U;
       put.next_row(w);
     }
     copy_commit();
-    if (++put_stage == Shape::STAGES) put_stage = 0;
+    put_at = put_at == (Shape::STAGES - 1) * Shape::BATCH ? 0 : put_at + Shape::BATCH;
   };
 #pragma unroll
   for (int i = 0; i < Shape::STAGES - 1; ++i) copy_batch();
 
-  int stage = 0;
+  uint32_t stage_at = 0;
+#pragma unroll 1
   for (int i = 0; i < w.n; ++i) {
     const int e0 = __shfl_sync(0xffffffffu, w.e0, i), e1 = __shfl_sync(0xffffffffu, w.e1, i);
-    const int slot = __shfl_sync(0xffffffffu, w.slot, i);
     float2 gk[KP], gv[VP];
 #pragma unroll
     for (int x = 0; x < KP; ++x) gk[x] = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int x = 0; x < VP; ++x) gv[x] = make_float2(0.0f, 0.0f);
+#pragma unroll 1
     for (int c = e0; c < e1; c += U) {
       copy_wait<Shape::STAGES - 2>();
       __syncwarp();
       copy_batch();
-      const uint32_t stage_at = ring + stage * Shape::BATCH, at = at_lane + stage * Shape::BATCH;
-      // the lane's own edge: l % U
-      const uint32_t item = hh * U + l % U;
-      const float2 pd = lds64(stage_at + Shape::SMALL_AT + item * 8);
+      const uint32_t at = at0 + stage_at, small = ring + stage_at;
+      const float2 pd = lds64(small + Shape::SMALL_AT + item * 8);
       const bool left_out = pd.x < 0.0f;
-      const float p = left_out ? 0.0f : pd.x, ds = left_out ? 0.0f : p * (pd.y - lds32(stage_at + DELTA_AT + item * 4));
+      const float p = left_out ? 0.0f : pd.x, ds = left_out ? 0.0f : p * (pd.y - lds32(small + DELTA_AT + item * 4));
       if (a.gbias && l < U && mine) {
-        const int edge = __float_as_int(lds32(stage_at + DELTA_AT + (U * HEADS + item) * 4));
+        const int edge = __float_as_int(lds32(small + EDGE_AT + item * 4));
         if ((unsigned)edge < (unsigned)a.E) a.gbias[(long long)edge * a.H + h] = ds;
       }
-      const unsigned out = __ballot_sync(0xffffffffu, left_out && c + l % U < e1);  // a weight of 0 would keep a NaN
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
+      const unsigned out = __ballot_sync(0xffffffffu, mine && left_out && c + l % U < e1);  // a weight of 0 would keep a NaN
+      auto add = [&](int u) {
         const float pu = __shfl_sync(0xffffffffu, p, lane - l + u), dsu = __shfl_sync(0xffffffffu, ds, lane - l + u);
-        const bool hide = out && (out >> (lane - l + u) & 1);
-        add_row<T, KN>(at + u * Shape::VECS * 512, dsu, gk, hide);
-        add_row<T, VN>(at + (u * Shape::VECS + KN) * 512, pu, gv, hide);
+        if (out && is_out(out, lane, l, u)) return;
+        add_row<T, KN>(at + u * Shape::VECS * 512, dsu, gk);
+        add_row<T, VN>(at + (u * Shape::VECS + KN) * 512, pu, gv);
+      };
+      if (out) {
+#pragma unroll 1
+        for (int u = 0; u < U; ++u) add(u);
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) add(u);
       }
-      if (++stage == Shape::STAGES) stage = 0;
+      stage_at = stage_at == (Shape::STAGES - 1) * Shape::BATCH ? 0 : stage_at + Shape::BATCH;
     }
+    const int slot = __shfl_sync(0xffffffffu, w.slot, i);
     if (!mine) continue;
     if (slot >= 0) {
       float* to = a.part + ((long long)slot * a.H + h) * (a.D + a.Dv);
