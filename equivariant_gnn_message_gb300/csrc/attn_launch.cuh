@@ -5,10 +5,6 @@
 #include "attn_ring.cuh"
 #include "launch.h"
 
-#ifndef TUNE_U
-#define TUNE_U (KN + VN <= 5 ? 4 : 2)
-#endif
-
 namespace eqmp {
 
 enum { kAttnFwd, kAttnRecv, kAttnSend };
@@ -63,7 +59,7 @@ eqmp_status launch_attn_form(const AttnArgs& a, cudaStream_t st) {
 
 template <int PASS, typename T, int G, int KN, int VN>
 eqmp_status launch_attn_ring(const AttnArgs& a, cudaStream_t st) {
-  constexpr int U = TUNE_U;
+  constexpr int U = KN + VN <= 4 || (sizeof(T) == 2 && KN + VN <= 5) ? 4 : 2;
   constexpr int SMEM = RingShape<G, KN, VN, U, PASS == kAttnSend ? 16 : 4>::CTA;
   const long long rows = PASS == kAttnSend ? a.Ns : a.N, workers = a.blocks + (rows + a.rows_each - 1) / a.rows_each;
   const dim3 grid((unsigned)((workers + kRingWarps - 1) / kRingWarps), (unsigned)((a.H * G + 31) / 32));

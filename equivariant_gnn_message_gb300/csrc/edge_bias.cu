@@ -24,13 +24,16 @@ struct BiasArgs {
 };
 
 // ---------------------------------------------------------------- forward
-constexpr int kBiasThreads = 256, kBiasEdges = 512;  // edges of a CTA's tile
-constexpr int kTableFloats = 8192;                   // a larger table is read through L1
+// A CTA finds the buckets of a tile of edges, then writes the tile's rows of the
+// table side by side.  The search is made in fp32 on squares, and again in 64
+// bits (whose rate is 1/60 of it here) only where a border is near.
+constexpr int kBiasThreads = 256, kBiasEdges = 1024;  // edges of a CTA's tile
+constexpr int kTableFloats = 4096;                    // a larger table is read through L1
 
 // Squares of fp32 values are exact in 64 bits, so that a length next to a border
 // is decided by one rounding of the sum of three, and the same everywhere.
-__device__ __forceinline__ int bucket_of(const float* vec, const float* borders, int n) {
-  const double x = vec[0], y = vec[1], z = vec[2];
+__device__ __noinline__ int bucket_exact(float vx, float vy, float vz, const float* borders, int n) {
+  const double x = vx, y = vy, z = vz;
   const double d = __dadd_rn(__dadd_rn(x * x, y * y), z * z);
   int lo = 0, len = n;  // borders[0..lo) <= |vec|
   while (len > 0) {
@@ -46,56 +49,115 @@ __device__ __forceinline__ int bucket_of(const float* vec, const float* borders,
   return lo;
 }
 
+// In fp32 the sum of squares is off by 3 2^-24 of itself at most, and a border's
+// square by 2^-24, as long as nothing over- or underflows: a border whose square
+// is 2^-20 away or more is on the side that it seems to be on.
+__device__ __forceinline__ int bucket_of(float x, float y, float z, const float* borders, const float* squares, int n) {
+  const float d = fmaf(x, x, fmaf(y, y, z * z));
+  int lo = 0, len = n;
+  while (len > 0) {
+    const int half = len / 2;
+    const bool up = squares[lo + half] <= d;
+    lo = up ? lo + half + 1 : lo;
+    len = up ? len - half - 1 : half;
+  }
+  const float below = lo > 0 ? squares[lo - 1] : 0.0f, above = lo < n ? squares[lo] : __int_as_float(0x7f800000);
+  const bool clear = d > 1e-30f && d < 1e30f && below <= d * (1.0f - 0x1p-20f) && above >= d * (1.0f + 0x1p-20f);
+  return clear ? lo : bucket_exact(x, y, z, borders, n);
+}
+
+template <typename F>  // float4 where H is a multiple of 4 and everything lies on 16 bytes, else float
 __global__ void __launch_bounds__(kBiasThreads) k_edge_bias(BiasArgs a) {
-  extern __shared__ float shared[];  // borders, then the table where it fits
+  constexpr int V = sizeof(F) / 4;
+  extern __shared__ __align__(16) float shared[];  // borders, their squares, then the table where it fits
   __shared__ int at[kBiasEdges];
+  const int n = a.B - 1, width = a.H / V;
   const bool fits = a.B * a.H <= kTableFloats;
-  float* const table = shared + (a.B - 1 + 3) / 4 * 4;
-  for (int i = threadIdx.x; i < a.B - 1; i += blockDim.x) shared[i] = a.borders[i];
+  float *const borders = shared, *const squares = shared + n;
+  F* const table = reinterpret_cast<F*>(shared + (2 * n + 3) / 4 * 4);
+  for (int i = threadIdx.x; i < n; i += kBiasThreads) {
+    const float b = a.borders[i];
+    borders[i] = b;
+    squares[i] = b * b;
+  }
   if (fits && a.bias)
-    for (int i = threadIdx.x; i < a.B * a.H; i += blockDim.x) table[i] = a.table[i];
-  const float* const from = fits ? table : a.table;
+    for (int i = threadIdx.x; i < a.B * width; i += kBiasThreads) table[i] = reinterpret_cast<const F*>(a.table)[i];
+  const F* const from = fits ? table : reinterpret_cast<const F*>(a.table);
+  // a thread's place in the rows that the CTA writes at a time
+  const int lines = kBiasThreads / width, line = threadIdx.x / width, col = threadIdx.x % width;
   for (long long e0 = (long long)blockIdx.x * kBiasEdges; e0 < a.E; e0 += (long long)gridDim.x * kBiasEdges) {
-    const int n = a.E - e0 < kBiasEdges ? (int)(a.E - e0) : kBiasEdges;
-    __syncthreads();  // borders are here; the last tile's buckets have been read
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      const int b = bucket_of(a.vec + 3 * (e0 + i), shared, a.B - 1);
+    const int count = a.E - e0 < kBiasEdges ? (int)(a.E - e0) : kBiasEdges;
+    const float* vec = a.vec + 3 * e0;
+    constexpr int EACH = kBiasEdges / kBiasThreads;
+    float v[EACH][3];
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+      const int i = k * kBiasThreads + threadIdx.x;
+#pragma unroll
+      for (int x = 0; x < 3; ++x) v[k][x] = i < count ? __ldg(vec + 3 * i + x) : 0.0f;
+    }
+    __syncthreads();  // borders and table are here; the last tile's buckets have been read
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+      const int i = k * kBiasThreads + threadIdx.x;
+      if (i >= count) break;
+      const int b = bucket_of(v[k][0], v[k][1], v[k][2], borders, squares, n);
       at[i] = b;
       if (a.bucket) a.bucket[e0 + i] = b;
     }
     __syncthreads();
-    if (!a.bias) continue;
-    float* out = a.bias + e0 * a.H;
-    for (int i = threadIdx.x; i < n * a.H; i += blockDim.x) out[i] = from[at[i / a.H] * a.H + i % a.H];
+    if (!a.bias || line >= lines) continue;
+    F* out = reinterpret_cast<F*>(a.bias + e0 * a.H) + col;
+#pragma unroll 4
+    for (int i = line; i < count; i += lines) out[(long long)i * width] = from[at[i] * width + col];
   }
 }
 
 // ---------------------------------------------------------------- backward
 // A CTA sums a range of edges into copies of the table in shared memory: thread
 // (r, h) alone adds to column h of copy r, so the order is fixed and nothing is
-// atomic.  Then the copies are added, and k_edge_bias_sum adds the CTAs' parts.
-constexpr int kGradThreads = 256;
-constexpr int kCopyFloats = 20480;  // of the copies of a CTA
+// atomic.  The next edges' values are loaded while the last ones are added.  Then
+// the copies are added, and k_edge_bias_sum adds the CTAs' parts.
+constexpr int kGradThreads = 256, kGradAhead = 8;
+constexpr int kCopyFloats = 16384;  // of the copies of a CTA: three CTAs an SM
 
 __global__ void __launch_bounds__(kGradThreads) k_edge_bias_bwd(BiasArgs a, int heads, int copies) {
   extern __shared__ float copy[];  // [copies][B][heads]
   const int h0 = blockIdx.y * heads, hn = min(heads, a.H - h0), size = a.B * heads;
-  for (int i = threadIdx.x; i < copies * size; i += blockDim.x) copy[i] = 0.0f;
-  __syncthreads();
   const int h = threadIdx.x % heads, r = threadIdx.x / heads;
   const int begin = (int)((long long)a.E * blockIdx.x / a.parts), end = (int)((long long)a.E * (blockIdx.x + 1) / a.parts);
-  if (r < copies && h < hn) {
-    float* mine = copy + r * size + h;
-    for (int e = begin + r; e < end; e += copies) {
-      const int b = __ldg(a.bucket + e);
-      if ((unsigned)b < (unsigned)a.B) mine[b * heads] += a.grad[(long long)e * a.H + h0 + h];
+  const bool mine = r < copies && h < hn;
+  const float* grad = a.grad + h0 + h;
+  int b[kGradAhead];
+  float g[kGradAhead];
+  auto load = [&](int e) {
+#pragma unroll
+    for (int k = 0; k < kGradAhead; ++k) {
+      const int i = e + k * copies;
+      b[k] = mine && i < end ? __ldg(a.bucket + i) : -1;
+      g[k] = mine && i < end ? __ldg(grad + (long long)i * a.H) : 0.0f;
     }
+  };
+  load(begin + r);
+  for (int i = threadIdx.x; i < copies * size; i += kGradThreads) copy[i] = 0.0f;
+  __syncthreads();
+  float* const own = copy + r * size + h;
+  for (int e = begin + r; mine && e < end; e += kGradAhead * copies) {
+    int now_b[kGradAhead];
+    float now_g[kGradAhead];
+#pragma unroll
+    for (int k = 0; k < kGradAhead; ++k) now_b[k] = b[k], now_g[k] = g[k];
+    load(e + kGradAhead * copies);
+#pragma unroll
+    for (int k = 0; k < kGradAhead; ++k)
+      if ((unsigned)now_b[k] < (unsigned)a.B) own[now_b[k] * heads] += now_g[k];
   }
   __syncthreads();
   float* out = a.parts > 1 ? a.part + (long long)blockIdx.x * a.B * a.H : a.gtable;
-  for (int i = threadIdx.x; i < a.B * hn; i += blockDim.x) {
+  for (int i = threadIdx.x; i < a.B * hn; i += kGradThreads) {
     const int at = i / hn * heads + i % hn;
     float t = 0.0f;
+#pragma unroll 8
     for (int c = 0; c < copies; ++c) t += copy[c * size + at];
     out[(long long)(i / hn) * a.H + h0 + i % hn] = t;
   }
@@ -108,8 +170,10 @@ __global__ void __launch_bounds__(kBiasSumX * kBiasSumY) k_edge_bias_sum(BiasArg
   const int i = blockIdx.x * kBiasSumX + threadIdx.x, n = a.B * a.H;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // until the kernel that writes the parts is done
   float t = 0.0f;
-  if (i < n)
+  if (i < n) {
+#pragma unroll 8
     for (int p = threadIdx.y; p < a.parts; p += kBiasSumY) t += a.part[(long long)p * n + i];
+  }
   red[threadIdx.y][threadIdx.x] = t;
   __syncthreads();
   if (threadIdx.y || i >= n) return;
@@ -118,12 +182,12 @@ __global__ void __launch_bounds__(kBiasSumX * kBiasSumY) k_edge_bias_sum(BiasArg
   a.gtable[i] = t;
 }
 
-// CTAs of the backward pass: two on each of 152 SMs, at least 1024 edges each,
+// CTAs of the backward pass: three on each of 152 SMs, at least 256 edges each,
 // and no more than 64 MB of parts.
 static int grad_parts(int64_t E, int64_t B, int64_t H) {
-  int64_t n = (E + 1023) / 1024;
+  int64_t n = (E + 255) / 256;
   const int64_t most = (16ll << 20) / (B * H);
-  if (n > 304) n = 304;
+  if (n > 456) n = 456;
   if (n > most) n = most;
   return n < 1 ? 1 : (int)n;
 }
@@ -162,8 +226,13 @@ eqmp_status eqmp_edge_bias(const float* vec, int64_t E, const float* borders, in
   a.vec = vec, a.borders = borders, a.table = table, a.bias = bias, a.bucket = bucket;
   a.E = (int)E, a.B = B, a.H = H;
   const int64_t tiles = (E + kBiasEdges - 1) / kBiasEdges, most = (int64_t)dev.sms * 8;
-  const int smem = ((B - 1 + 3) / 4 * 4 + (B * H <= kTableFloats ? B * H : 0)) * 4;
-  k_edge_bias<<<(unsigned)(tiles < most ? tiles : most), kBiasThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  const int smem = ((2 * (B - 1) + 3) / 4 * 4 + (B * H <= kTableFloats ? B * H : 0)) * 4;
+  const unsigned grid = (unsigned)(tiles < most ? tiles : most);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (H % 4 == 0 && aligned(table, 16) && aligned(bias, 16))
+    k_edge_bias<float4><<<grid, kBiasThreads, smem, st>>>(a);
+  else
+    k_edge_bias<float><<<grid, kBiasThreads, smem, st>>>(a);
   return cuda_status(cudaGetLastError());
 }
 

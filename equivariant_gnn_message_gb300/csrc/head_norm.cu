@@ -10,7 +10,7 @@
 namespace eqmp {
 
 constexpr int kMaxHeadDim = 256, kMaxHeads = 65536;
-constexpr int kHeadCtas = 8;  // on each SM, in the backward pass: each leaves a part of dw
+constexpr int kHeadCtas = 2;  // on each SM, in the backward pass: each leaves a part of dw
 
 static eqmp_status check(int64_t N, int32_t Hq, int32_t Hk, int32_t D, eqmp_dtype dtype, const float* pos, const float* freq,
                          int32_t axes) {
@@ -33,7 +33,7 @@ static eqmp_status launch(const HeadNormArgs& a, bool backward, cudaStream_t st)
     DeviceInfo dev;
     const eqmp_status s = device_info(&dev);
     if (s != EQMP_OK) return s;
-    const long long most = (long long)dev.sms * 16;
+    const long long most = (long long)dev.sms * 8;
     k_head_norm<T, V, G, NV, U><<<(unsigned)(ctas < most ? ctas : most), 32 * kHeadWarps, 0, st>>>(a);
     return cuda_status(cudaGetLastError());
   }

@@ -9,8 +9,9 @@
 //   dpos[a] = sum_{heads, p} freq[p][a] (b[2p+1] u[2p] - b[2p] u[2p+1])
 // (a rotation turns g and y alike, so the last one needs no y).
 //
-// A warp takes a node: the angles of its pairs are formed once and serve all its
-// heads.  Memory binds: x is read once and y written once.
+// A warp takes a few nodes: the cosines and sines of their pairs are formed once,
+// by all lanes, and kept in shared memory for all heads.  Memory binds: x is read
+// once and y written once.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -33,7 +34,8 @@ struct HeadNormArgs {
   int N, Hq, Hk, D, axes;
 };
 
-constexpr int kHeadWarps = 4;
+constexpr int kHeadWarps = 8;       // of a CTA
+constexpr int kHeadAngles = 64;     // pairs of a warp's nodes at a time; a node has at most 128
 
 // An angle in turns, reduced to half a turn: the frequency in turns is held as
 // the sum of two floats, and the product's rounding error is kept, so that a
@@ -122,86 +124,97 @@ __device__ __forceinline__ void load_weights(const float* w, int l, int D, float
   }
 }
 
-// The frequencies of the lane's pairs, and a node's cosines and sines.
-template <int V, int G, int NV>
-struct Rotation {
-  static constexpr int P = NV * V / 2;
-  Turns f[P][3];
-  __device__ __forceinline__ void set(const float* freq, int axes, int l, int D) {
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int x = 0; x < 3; ++x) {
-        const int pair = ((2 * p / V * G + l) * V + 2 * p % V) / 2;
-        f[p][x].set(x < axes && pair < D / 2 ? freq[(long long)pair * axes + x] : 0.0f);
-      }
-  }
-  __device__ __forceinline__ void at(const float (&pos)[3], int axes, float (&c)[P], float (&s)[P]) const {
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      float t = f[p][0].of(pos[0]);
-      if (axes > 1) t += f[p][1].of(pos[1]);
-      if (axes > 2) t += f[p][2].of(pos[2]);
-      t -= rintf(t);
-      sincospif(2.0f * t, &s[p], &c[p]);
-    }
-  }
-};
+// The angles of a warp's nodes.  freq: the pairs' frequencies in turns, [pair][axis]
+// (shared by the CTA); turn: the cosines and sines of the warp's nodes,
+// [node][pair].  A warp has as many nodes at a time as keep its lanes busy.
+__device__ __forceinline__ int nodes_at_once(int pairs) { return pairs >= kHeadAngles ? 1 : kHeadAngles / pairs; }
 
-__device__ __forceinline__ void load_pos(const HeadNormArgs& a, int node, float (&pos)[3]) {
+__device__ __forceinline__ void load_freq(const HeadNormArgs& a, Turns* freq) {
+  for (int i = threadIdx.x; i < a.D / 2 * a.axes; i += blockDim.x) freq[i].set(a.freq[i]);
+}
+
+__device__ __forceinline__ void form_turns(const HeadNormArgs& a, const Turns* freq, float2* turn, int node0, int nodes) {
+  const int pairs = a.D / 2;
+  __syncwarp();  // the last nodes' have been read
+  for (int i = threadIdx.x & 31; i < nodes * pairs; i += 32) {
+    const int n = i / pairs, p = i - n * pairs;
+    const float* pos = a.pos + (long long)(node0 + n) * a.axes;
+    float t = freq[p * a.axes].of(__ldg(pos));
+    for (int x = 1; x < a.axes; ++x) t += freq[p * a.axes + x].of(__ldg(pos + x));
+    t -= rintf(t);
+    float s, c;
+    sincospif(2.0f * t, &s, &c);
+    turn[i] = make_float2(c, s);
+  }
+  __syncwarp();
+}
+
+// The lane's pairs of a node.
+template <int V, int G, int NV>
+__device__ __forceinline__ void load_turns(const float2* turn, int pairs, int l, float2 (&t)[NV * V / 2]) {
 #pragma unroll
-  for (int x = 0; x < 3; ++x) pos[x] = x < a.axes ? __ldg(a.pos + (long long)node * a.axes + x) : 0.0f;
+  for (int p = 0; p < NV * V / 2; ++p) {
+    const int pair = ((2 * p / V * G + l) * V + 2 * p % V) / 2;
+    t[p] = pair < pairs ? turn[pair] : make_float2(1.0f, 0.0f);
+  }
 }
 
 template <typename T, int V, int G, int NV, int U>
 __global__ void __launch_bounds__(32 * kHeadWarps) k_head_norm(HeadNormArgs a) {
   constexpr int W = NV * V, P = W / 2, AT_ONCE = 32 / G;
-  const int lane = threadIdx.x & 31, l = lane % G, warps = gridDim.x * kHeadWarps, heads = a.Hq + a.Hk;
+  __shared__ Turns freq[128 * 3];
+  __shared__ float2 turns[kHeadWarps][128];
+  const int lane = threadIdx.x & 31, l = lane % G, heads = a.Hq + a.Hk, pairs = a.D / 2;
+  const int each = a.axes ? nodes_at_once(pairs) : 1;
+  float2* const turn = turns[threadIdx.x >> 5];
   float wq[W], wk[W];
   load_weights<V, G, NV>(a.wq, l, a.D, wq);
   load_weights<V, G, NV>(a.wk, l, a.D, wk);
-  Rotation<V, G, NV> rot;
-  if (a.axes) rot.set(a.freq, a.axes, l, a.D);
-  for (int node = blockIdx.x * kHeadWarps + (threadIdx.x >> 5); node < a.N; node += warps) {
-    const T* q = static_cast<const T*>(a.q) + node * a.q_ld;
-    const T* k = static_cast<const T*>(a.k) + node * a.k_ld;
-    float cs[P], sn[P], pos[3];
-    if (a.axes) {
-      load_pos(a, node, pos);
-      rot.at(pos, a.axes, cs, sn);
-    }
-    for (int t0 = lane / G; t0 - lane / G < heads; t0 += U * AT_ONCE) {
-      HeadShare<T, V, G, NV> x[U];
+  if (a.axes) load_freq(a, freq);
+  __syncthreads();
+  const long long step = (long long)gridDim.x * kHeadWarps * each;
+  for (long long node0 = ((long long)blockIdx.x * kHeadWarps + (threadIdx.x >> 5)) * each; node0 < a.N; node0 += step) {
+    const int nodes = a.N - node0 < each ? (int)(a.N - node0) : each;
+    if (a.axes) form_turns(a, freq, turn, (int)node0, nodes);
+    for (int n = 0; n < nodes; ++n) {
+      const int node = (int)node0 + n;
+      const T* q = static_cast<const T*>(a.q) + node * a.q_ld;
+      const T* k = static_cast<const T*>(a.k) + node * a.k_ld;
+      float2 cs[P];
+      if (a.axes) load_turns<V, G, NV>(turn + n * pairs, pairs, l, cs);
+      for (int t0 = lane / G; t0 - lane / G < heads; t0 += U * AT_ONCE) {
+        HeadShare<T, V, G, NV> x[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = t0 + u * AT_ONCE;
-        x[u].load(t < a.Hq ? q + (long long)t * a.D : k + (long long)(t - a.Hq) * a.D, l, a.D, t < heads);
-      }
+        for (int u = 0; u < U; ++u) {
+          const int t = t0 + u * AT_ONCE;
+          x[u].load(t < a.Hq ? q + (long long)t * a.D : k + (long long)(t - a.Hq) * a.D, l, a.D, t < heads);
+        }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = t0 + u * AT_ONCE;
-        float f[W], ss = 0.0f;
-        x[u].get(f);
+        for (int u = 0; u < U; ++u) {
+          const int t = t0 + u * AT_ONCE;
+          float f[W], ss = 0.0f;
+          x[u].get(f);
 #pragma unroll
-        for (int i = 0; i < W; ++i) ss = fmaf(f[i], f[i], ss);
+          for (int i = 0; i < W; ++i) ss = fmaf(f[i], f[i], ss);
 #pragma unroll
-        for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (t >= heads) continue;
-        const bool query = t < a.Hq;
-        const float r = 1.0f / sqrtf(ss / (float)a.D + a.eps);
-        if (a.rstd && l == 0) a.rstd[(long long)node * heads + t] = r;
+          for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          if (t >= heads) continue;
+          const bool query = t < a.Hq;
+          const float r = 1.0f / sqrtf(ss / (float)a.D + a.eps);
+          if (a.rstd && l == 0) a.rstd[(long long)node * heads + t] = r;
 #pragma unroll
-        for (int i = 0; i < W; ++i) f[i] *= r * (query ? wq[i] : wk[i]);
-        if (a.axes)
+          for (int i = 0; i < W; ++i) f[i] *= r * (query ? wq[i] : wk[i]);
+          if (a.axes)
 #pragma unroll
-          for (int p = 0; p < P; ++p) {
-            const float u0 = f[2 * p], u1 = f[2 * p + 1];
-            f[2 * p] = u0 * cs[p] - u1 * sn[p];
-            f[2 * p + 1] = u0 * sn[p] + u1 * cs[p];
-          }
-        T* out = static_cast<T*>(query ? a.oq : a.ok);
-        const long long row = query ? (long long)node * a.Hq + t : (long long)node * a.Hk + (t - a.Hq);
-        if (out) HeadShare<T, V, G, NV>::store(out + row * a.D, l, a.D, f);
+            for (int p = 0; p < P; ++p) {
+              const float u0 = f[2 * p], u1 = f[2 * p + 1];
+              f[2 * p] = u0 * cs[p].x - u1 * cs[p].y;
+              f[2 * p + 1] = u0 * cs[p].y + u1 * cs[p].x;
+            }
+          T* out = static_cast<T*>(query ? a.oq : a.ok);
+          const long long row = query ? (long long)node * a.Hq + t : (long long)node * a.Hk + (t - a.Hq);
+          if (out) HeadShare<T, V, G, NV>::store(out + row * a.D, l, a.D, f);
+        }
       }
     }
   }
@@ -210,85 +223,96 @@ __global__ void __launch_bounds__(32 * kHeadWarps) k_head_norm(HeadNormArgs a) {
 template <typename T, int V, int G, int NV, int U>
 __global__ void __launch_bounds__(32 * kHeadWarps) k_head_norm_bwd(HeadNormArgs a) {
   constexpr int W = NV * V, P = W / 2, AT_ONCE = 32 / G;
+  __shared__ Turns freq[128 * 3];
+  __shared__ float2 turns[kHeadWarps][128];
   __shared__ float red[kHeadWarps][2 * G * W];
-  const int lane = threadIdx.x & 31, l = lane % G, warp = threadIdx.x >> 5, warps = gridDim.x * kHeadWarps;
-  const int heads = a.Hq + a.Hk;
+  const int lane = threadIdx.x & 31, l = lane % G, warp = threadIdx.x >> 5, heads = a.Hq + a.Hk, pairs = a.D / 2;
+  const int each = a.axes ? nodes_at_once(pairs) : 1;
+  float2* const turn = turns[warp];
   float wq[W], wk[W], dwq[W], dwk[W];
   load_weights<V, G, NV>(a.wq, l, a.D, wq);
   load_weights<V, G, NV>(a.wk, l, a.D, wk);
 #pragma unroll
   for (int i = 0; i < W; ++i) dwq[i] = dwk[i] = 0.0f;
-  Rotation<V, G, NV> rot;
-  if (a.axes) rot.set(a.freq, a.axes, l, a.D);
-  for (int node = blockIdx.x * kHeadWarps + warp; node < a.N; node += warps) {
-    float cs[P], sn[P], turn[P], pos[3];
-    if (a.axes) {
-      load_pos(a, node, pos);
-      rot.at(pos, a.axes, cs, sn);
-    }
+  if (a.axes) load_freq(a, freq);
+  __syncthreads();
+  const long long step = (long long)gridDim.x * kHeadWarps * each;
+  for (long long node0 = ((long long)blockIdx.x * kHeadWarps + warp) * each; node0 < a.N; node0 += step) {
+    const int nodes = a.N - node0 < each ? (int)(a.N - node0) : each;
+    if (a.axes) form_turns(a, freq, turn, (int)node0, nodes);
+    for (int n = 0; n < nodes; ++n) {
+      const int node = (int)node0 + n;
+      float2 cs[P];
+      float turned[P];
+      if (a.axes) load_turns<V, G, NV>(turn + n * pairs, pairs, l, cs);
 #pragma unroll
-    for (int p = 0; p < P; ++p) turn[p] = 0.0f;
-    for (int t0 = lane / G; t0 - lane / G < heads; t0 += U * AT_ONCE) {
-      HeadShare<T, V, G, NV> x[U], g[U];
-      float r[U];
+      for (int p = 0; p < P; ++p) turned[p] = 0.0f;
+      for (int t0 = lane / G; t0 - lane / G < heads; t0 += U * AT_ONCE) {
+        HeadShare<T, V, G, NV> x[U], g[U];
+        float r[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = t0 + u * AT_ONCE, hk = t - a.Hq;
-        const T* xp = static_cast<const T*>(t < a.Hq ? a.q : a.k);
-        const T* gp = static_cast<const T*>(t < a.Hq ? a.gq : a.gk);
-        x[u].load(xp + (t < a.Hq ? node * a.q_ld + (long long)t * a.D : node * a.k_ld + (long long)hk * a.D), l, a.D, t < heads);
-        g[u].load(gp + (t < a.Hq ? node * a.gq_ld + (long long)t * a.D : node * a.gk_ld + (long long)hk * a.D), l, a.D, t < heads);
-        r[u] = t < heads ? __ldg(a.rstd + (long long)node * heads + t) : 0.0f;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = t0 + u * AT_ONCE;
-        const bool query = t < a.Hq, ok = t < heads;
-        float h[W], b[W], mean = 0.0f;
-        x[u].get(h);
-        g[u].get(b);
-#pragma unroll
-        for (int i = 0; i < W; ++i) h[i] *= r[u];
-        if (a.axes)
-#pragma unroll
-          for (int p = 0; p < P; ++p) {
-            const float g0 = b[2 * p], g1 = b[2 * p + 1];
-            b[2 * p] = g0 * cs[p] + g1 * sn[p];
-            b[2 * p + 1] = g1 * cs[p] - g0 * sn[p];
-            const float u0 = h[2 * p] * (query ? wq[2 * p] : wk[2 * p]);
-            const float u1 = h[2 * p + 1] * (query ? wq[2 * p + 1] : wk[2 * p + 1]);
-            if (ok) turn[p] += b[2 * p + 1] * u0 - b[2 * p] * u1;
-          }
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-          const float d = b[i] * h[i];
-          if (ok && query) dwq[i] += d;
-          if (ok && !query) dwk[i] += d;
-          b[i] *= query ? wq[i] : wk[i];
-          mean = fmaf(b[i], h[i], mean);
+        for (int u = 0; u < U; ++u) {
+          const int t = t0 + u * AT_ONCE, hk = t - a.Hq;
+          const T* xp = static_cast<const T*>(t < a.Hq ? a.q : a.k);
+          const T* gp = static_cast<const T*>(t < a.Hq ? a.gq : a.gk);
+          x[u].load(xp + (t < a.Hq ? node * a.q_ld + (long long)t * a.D : node * a.k_ld + (long long)hk * a.D), l, a.D, t < heads);
+          g[u].load(gp + (t < a.Hq ? node * a.gq_ld + (long long)t * a.D : node * a.gk_ld + (long long)hk * a.D), l, a.D, t < heads);
+          r[u] = t < heads ? __ldg(a.rstd + (long long)node * heads + t) : 0.0f;
         }
 #pragma unroll
-        for (int o = G / 2; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
-        if (!ok) continue;
-        mean /= (float)a.D;
+        for (int u = 0; u < U; ++u) {
+          const int t = t0 + u * AT_ONCE;
+          const bool query = t < a.Hq, ok = t < heads;
+          float h[W], b[W], mean = 0.0f;
+          x[u].get(h);
+          g[u].get(b);
 #pragma unroll
-        for (int i = 0; i < W; ++i) b[i] = r[u] * fmaf(-h[i], mean, b[i]);
-        T* out = static_cast<T*>(query ? a.oq : a.ok);
-        const long long row = query ? (long long)node * a.Hq + t : (long long)node * a.Hk + (t - a.Hq);
-        if (out) HeadShare<T, V, G, NV>::store(out + row * a.D, l, a.D, b);
+          for (int i = 0; i < W; ++i) h[i] *= r[u];
+          if (a.axes)
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+              const float g0 = b[2 * p], g1 = b[2 * p + 1];
+              b[2 * p] = g0 * cs[p].x + g1 * cs[p].y;
+              b[2 * p + 1] = g1 * cs[p].x - g0 * cs[p].y;
+              const float u0 = h[2 * p] * (query ? wq[2 * p] : wk[2 * p]);
+              const float u1 = h[2 * p + 1] * (query ? wq[2 * p + 1] : wk[2 * p + 1]);
+              if (ok) turned[p] += b[2 * p + 1] * u0 - b[2 * p] * u1;
+            }
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            const float d = b[i] * h[i];
+            if (ok && query) dwq[i] += d;
+            if (ok && !query) dwk[i] += d;
+            b[i] *= query ? wq[i] : wk[i];
+            mean = fmaf(b[i], h[i], mean);
+          }
+#pragma unroll
+          for (int o = G / 2; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
+          if (!ok) continue;
+          mean /= (float)a.D;
+#pragma unroll
+          for (int i = 0; i < W; ++i) b[i] = r[u] * fmaf(-h[i], mean, b[i]);
+          T* out = static_cast<T*>(query ? a.oq : a.ok);
+          const long long row = query ? (long long)node * a.Hq + t : (long long)node * a.Hk + (t - a.Hq);
+          if (out) HeadShare<T, V, G, NV>::store(out + row * a.D, l, a.D, b);
+        }
       }
-    }
-    if (a.gpos) {
-      float d[3] = {0.0f, 0.0f, 0.0f};
+      if (a.gpos) {
+        float d[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int p = 0; p < P; ++p)
+        for (int p = 0; p < P; ++p) {
+          const int pair = ((2 * p / V * G + l) * V + 2 * p % V) / 2;
 #pragma unroll
-        for (int x = 0; x < 3; ++x) d[x] = fmaf(turn[p], rot.f[p][x].hi, d[x]);
+          for (int x = 0; x < 3; ++x)
+            if (pair < pairs && x < a.axes) d[x] = fmaf(turned[p], freq[pair * a.axes + x].hi, d[x]);
+        }
 #pragma unroll
-      for (int x = 0; x < 3; ++x) {
+        for (int x = 0; x < 3; ++x) {
+          if (x >= a.axes) break;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) d[x] += __shfl_xor_sync(0xffffffffu, d[x], o);
-        if (lane == 0 && x < a.axes) a.gpos[(long long)node * a.axes + x] = d[x] * 6.2831853071795865f;
+          for (int o = 16; o > 0; o >>= 1) d[x] += __shfl_xor_sync(0xffffffffu, d[x], o);
+          if (lane == 0) a.gpos[(long long)node * a.axes + x] = d[x] * 6.2831853071795865f;
+        }
       }
     }
   }
@@ -325,8 +349,10 @@ static __global__ void __launch_bounds__(kHeadSumX * kHeadSumY) k_head_norm_sum(
   const int c = blockIdx.x * kHeadSumX + threadIdx.x;
   float t = 0.0f;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // until the kernel that writes the parts is done
-  if (c < 2 * a.D)
+  if (c < 2 * a.D) {
+#pragma unroll 8
     for (int p = threadIdx.y; p < parts; p += kHeadSumY) t += a.part[(long long)p * 2 * a.D + c];
+  }
   red[threadIdx.y][threadIdx.x] = t;
   __syncthreads();
   if (threadIdx.y || c >= 2 * a.D) return;

@@ -151,7 +151,7 @@ def test_workspace_sizes(lib):
     assert lib.eqmp_edge_attention_workspace_size(-1, 8, 128) == lib.eqmp_edge_attention_workspace_size(5, 8, 1025) == -1
     assert lib.eqmp_edge_attention_backward_workspace_size(5, 5, 2 ** 30 + 1, 8, 8, 8) == -1
     assert lib.eqmp_head_norm_backward_workspace_size(5, 257) == -1 and lib.eqmp_head_norm_backward_workspace_size(0, 8) == 0
-    assert lib.eqmp_edge_bias_backward_workspace_size(1024, 64, 8) == 0 and lib.eqmp_edge_bias_backward_workspace_size(5, 0, 8) == -1
+    assert lib.eqmp_edge_bias_backward_workspace_size(256, 64, 8) == 0 and lib.eqmp_edge_bias_backward_workspace_size(5, 0, 8) == -1
 
 
 # ------------------------------------------------------------------ the binding
