@@ -36,11 +36,11 @@ static eqmp_status check_sizes(const Sizes& n, eqmp_dtype dtype, float scale) {
   return fits ? EQMP_OK : EQMP_ERR_UNSUPPORTED;
 }
 
-// Blocks that rows of more than two are cut into: at least 128 edges, at most
+// Blocks that rows of more than two are cut into: at least 32 edges, at most
 // 2048 blocks in all, so that the parts stay a few MB.
 static void cut(int64_t E, int* block, int* blocks) {
   const int64_t want = (E + 2047) / 2048;
-  *block = (int)(want < 128 ? 128 : (want + 127) / 128 * 128);
+  *block = (int)(want < 32 ? 32 : (want + 31) / 32 * 32);
   *blocks = E > 2 * *block ? (int)((E + *block - 1) / *block) : 0;
 }
 
@@ -62,29 +62,45 @@ static BackwardSpace backward_workspace(const Sizes& n, int64_t E_send) {
   return BackwardSpace{n.E * n.H * 8 + 15 & ~15ll, n.N * n.H * 4 + 15 & ~15ll, recv > send ? recv : send};
 }
 
-// 16-byte vectors where every head of every row begins on 16 bytes, else single
-// values.  The fewest lanes a head whose registers hold it; more of them where
-// there are too few rows to fill the device.
-static AttnForm form_of(const Sizes& n, int64_t rows, int bytes, bool vectors) {
+// What every head of every row begins on, at most 16 bytes: gathered over the
+// addresses, row pitches and head sizes of a call.
+struct Alignment {
+  unsigned long long bits = 16;
+  void add(const void* p) { bits |= reinterpret_cast<uintptr_t>(p); }
+  void add(const void* p, long long ld, int bytes) {
+    if (!p) return;
+    add(p);
+    bits |= (unsigned long long)(ld * bytes);
+    if (ld * bytes >= 1ll << 32) bits |= 1;  // rows too far apart for the rings' 32-bit pitches
+  }
+  int bytes() const { return (int)(bits & -bits); }
+};
+
+// The widest vectors that the alignment allows, and for them the fewest lanes a
+// head whose registers hold it; more lanes where there are too few rows to fill
+// the device.  Heads that the forms with vectors of 8 or 4 bytes do not hold, and
+// bf16 heads that begin anywhere, take the general kernels.
+static AttnForm form_of(const Sizes& n, int64_t rows, int bytes, int alignment) {
   AttnForm f;
-  f.V = vectors ? 16 / bytes : 1;
-  const int k = (n.D + f.V - 1) / f.V, v = (n.Dv + f.V - 1) / f.V;
-  auto fits = [&](int G) {
-    const int most_k = vectors ? 2 : G == 8 ? 4 : 8, most_v = vectors ? 32 / f.V : G == 8 ? 16 : 32;
-    return (k + G - 1) / G <= most_k && (v + G - 1) / G <= most_v;
-  };
-  f.G = 8;
-  while (f.G < 32 && (!fits(f.G) || n.H * f.G * 2 <= 32 || rows * ((n.H * f.G + 31) / 32) < 152 * 16)) f.G *= vectors ? 2 : 4;
-  f.KN = (k + f.G - 1) / f.G;
-  f.VN = (v + f.G - 1) / f.G;
+  for (f.VB = alignment < 4 ? 0 : alignment; f.VB >= 4; f.VB /= 2) {
+    const int k = (n.D * bytes + f.VB - 1) / f.VB, v = (n.Dv * bytes + f.VB - 1) / f.VB;
+    auto fits = [&](int G) { return k <= 2 * G && v <= 8 * G; };
+    f.G = f.VB == 16 ? 8 : f.VB == 8 ? 16 : 32;
+    if (f.VB == 16)
+      while (f.G < 32 && (!fits(f.G) || n.H * f.G * 2 <= 32 || rows * ((n.H * f.G + 31) / 32) < 152 * 16)) f.G *= 2;
+    f.KN = (k + f.G - 1) / f.G;
+    f.VN = (v + f.G - 1) / f.G;
+    if (fits(f.G)) break;
+  }
+  if (f.VB < 4) {
+    f.VB = 0;
+    f.G = n.D <= 32 && n.Dv <= 128 && n.H > 2 && rows * ((n.H + 3) / 4) >= 152 * 16 ? 8 : 32;
+    f.KN = (n.D + f.G - 1) / f.G;
+    f.VN = (n.Dv + f.G - 1) / f.G;
+  }
   const int64_t each = rows * ((n.H * f.G + 31) / 32) / (152 * 8 * 4);
   f.rows_each = (int)(each < 1 ? 1 : each > 16 ? 16 : each);
   return f;
-}
-
-// Rows on 16 bytes, below 2^32 bytes apart.
-static bool on16(const void* p, long long ld, int bytes) {
-  return aligned(p, 16) && ld * bytes % 16 == 0 && ld * bytes < 1ll << 32;
 }
 
 }  // namespace eqmp
@@ -127,9 +143,11 @@ eqmp_status eqmp_edge_attention(const void* q, int64_t q_ld, const void* k, int6
   a.scale = scale;
   a.N = (int)N, a.Ns = (int)N_src, a.E = (int)E, a.H = H, a.D = D, a.Dv = Dv;
   cut(E, &a.block, &a.blocks);
-  const bool vectors = on16(q, q_ld, bytes) && on16(k, k_ld, bytes) && on16(v, v_ld, bytes) && aligned(out, 16) &&
-                       D * bytes % 16 == 0 && Dv * bytes % 16 == 0;
-  const AttnForm f = form_of(n, N, bytes, vectors);
+  Alignment at;
+  at.add(q, q_ld, bytes), at.add(k, k_ld, bytes), at.add(v, v_ld, bytes);
+  at.add(out);
+  at.bits |= (unsigned long long)D * bytes | (unsigned long long)Dv * bytes;
+  const AttnForm f = form_of(n, N, bytes, at.bytes());
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dtype == EQMP_BF16 ? launch_attn_fwd_bf16(a, f, st) : launch_attn_fwd_f32(a, f, st);
 }
@@ -186,9 +204,10 @@ eqmp_status eqmp_edge_attention_backward(const void* grad_out, int64_t grad_out_
   a.scale = scale;
   a.N = (int)N, a.Ns = (int)N_src, a.E = (int)E, a.E_send = (int)E_send, a.H = H, a.D = D, a.Dv = Dv;
   a.pd = send || grad_bias ? reinterpret_cast<float2*>(space) : nullptr;
-  const bool vectors = on16(q, q_ld, bytes) && on16(k, k_ld, bytes) && on16(v, v_ld, bytes) && on16(grad_out, grad_out_ld, bytes) &&
-                       aligned(grad_q, 16) && aligned(grad_k, 16) && aligned(grad_v, 16) && D * bytes % 16 == 0 &&
-                       Dv * bytes % 16 == 0;
+  Alignment at;
+  at.add(q, q_ld, bytes), at.add(k, k_ld, bytes), at.add(v, v_ld, bytes), at.add(grad_out, grad_out_ld, bytes);
+  at.add(grad_q), at.add(grad_k), at.add(grad_v);
+  at.bits |= (unsigned long long)D * bytes | (unsigned long long)Dv * bytes;
   const bool bf16 = dtype == EQMP_BF16;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // the bias of edges that no pass below reaches
@@ -196,13 +215,13 @@ eqmp_status eqmp_edge_attention_backward(const void* grad_out, int64_t grad_out_
     return EQMP_ERR_CUDA;
   if (N > 0) {
     cut(E, &a.block, &a.blocks);
-    const AttnForm f = form_of(n, N, bytes, vectors);
+    const AttnForm f = form_of(n, N, bytes, at.bytes());
     const eqmp_status s = bf16 ? launch_attn_recv_bf16(a, f, st) : launch_attn_recv_f32(a, f, st);
     if (s != EQMP_OK) return s;
   }
   if (send) {
     cut(E_send, &a.block, &a.blocks);
-    const AttnForm f = form_of(n, N_src, bytes, vectors);
+    const AttnForm f = form_of(n, N_src, bytes, at.bytes());
     return bf16 ? launch_attn_send_bf16(a, f, st) : launch_attn_send_f32(a, f, st);
   }
   if (!grad_bias || N == 0) return EQMP_OK;

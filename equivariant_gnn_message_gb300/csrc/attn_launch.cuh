@@ -9,10 +9,10 @@ namespace eqmp {
 
 enum { kAttnFwd, kAttnRecv, kAttnSend };
 
-// A form: V elements a vector, G lanes a head, up to KN vectors of a key and VN
-// of a value a lane.
+// A form: vectors of VB bytes (0: the general kernels, value by value), G lanes a
+// head, up to KN vectors of a key and VN of a value a lane; rows of a warp.
 struct AttnForm {
-  int V, G, KN, VN;
+  int VB, G, KN, VN;
   int rows_each;
 };
 
@@ -57,10 +57,10 @@ eqmp_status launch_attn_form(const AttnArgs& a, cudaStream_t st) {
   return launch_attn_join<PASS, T>(a, st);
 }
 
-template <int PASS, typename T, int G, int KN, int VN>
+template <int PASS, typename T, int VB, int G, int KN, int VN>
 eqmp_status launch_attn_ring(const AttnArgs& a, cudaStream_t st) {
-  constexpr int U = KN + VN <= 4 || (sizeof(T) == 2 && KN + VN <= 5) ? 4 : 2;
-  constexpr int SMEM = RingShape<G, KN, VN, U, PASS == kAttnSend ? 16 : 4>::CTA;
+  constexpr int U = KN + VN <= 4 || (sizeof(T) == 2 && KN + VN <= 5) || VB < 16 ? 4 : 2;
+  constexpr int SMEM = RingShape<VB, G, KN, VN, U, PASS == kAttnSend ? 16 : 4>::CTA;
   const long long rows = PASS == kAttnSend ? a.Ns : a.N, workers = a.blocks + (rows + a.rows_each - 1) / a.rows_each;
   const dim3 grid((unsigned)((workers + kRingWarps - 1) / kRingWarps), (unsigned)((a.H * G + 31) / 32));
   static unsigned long long done = 0;
@@ -70,31 +70,34 @@ eqmp_status launch_attn_ring(const AttnArgs& a, cudaStream_t st) {
     return launch_attn_join<PASS, T>(a, st);
   };
   if constexpr (PASS == kAttnFwd)
-    return run(k_attn_fwd_ring<T, G, KN, VN, U>);
+    return run(k_attn_fwd_ring<T, VB, G, KN, VN, U>);
   else if constexpr (PASS == kAttnRecv)
-    return run(k_attn_recv_ring<T, G, KN, VN, U>);
+    return run(k_attn_recv_ring<T, VB, G, KN, VN, U>);
   else
-    return run(k_attn_send_ring<T, G, KN, VN, U>);
+    return run(k_attn_send_ring<T, VB, G, KN, VN, U>);
 }
 
-template <int PASS, typename T, int G>
+template <int PASS, typename T, int VB, int G>
 eqmp_status launch_attn_lanes(const AttnArgs& a, const AttnForm& f, cudaStream_t st) {
-  if (f.KN <= 1 && f.VN <= 1) return launch_attn_ring<PASS, T, G, 1, 1>(a, st);
-  if (f.KN <= 1 && f.VN <= 2) return launch_attn_ring<PASS, T, G, 1, 2>(a, st);
-  if (f.KN <= 1 && f.VN <= 4) return launch_attn_ring<PASS, T, G, 1, 4>(a, st);
-  if (f.VN <= 2) return launch_attn_ring<PASS, T, G, 2, 2>(a, st);
-  if (f.VN <= 4) return launch_attn_ring<PASS, T, G, 2, 4>(a, st);
-  return launch_attn_ring<PASS, T, G, 2, 8>(a, st);
+  if constexpr (VB == 16) {
+    if (f.KN <= 1 && f.VN <= 1) return launch_attn_ring<PASS, T, VB, G, 1, 1>(a, st);
+  }
+  if (f.KN <= 1 && f.VN <= 2) return launch_attn_ring<PASS, T, VB, G, 1, 2>(a, st);
+  if (f.KN <= 1 && f.VN <= 4) return launch_attn_ring<PASS, T, VB, G, 1, 4>(a, st);
+  if (f.VN <= 4) return launch_attn_ring<PASS, T, VB, G, 2, 4>(a, st);
+  return launch_attn_ring<PASS, T, VB, G, 2, 8>(a, st);
 }
 
 template <int PASS, typename T>
 eqmp_status launch_attn(AttnArgs a, const AttnForm& f, cudaStream_t st) {
   a.rows_each = f.rows_each;
-  if (f.V > 1) {
-    if (f.G == 8) return launch_attn_lanes<PASS, T, 8>(a, f, st);
-    if (f.G == 16) return launch_attn_lanes<PASS, T, 16>(a, f, st);
-    return launch_attn_lanes<PASS, T, 32>(a, f, st);
+  if (f.VB == 16) {
+    if (f.G == 8) return launch_attn_lanes<PASS, T, 16, 8>(a, f, st);
+    if (f.G == 16) return launch_attn_lanes<PASS, T, 16, 16>(a, f, st);
+    return launch_attn_lanes<PASS, T, 16, 32>(a, f, st);
   }
+  if (f.VB == 8) return launch_attn_lanes<PASS, T, 8, 16>(a, f, st);
+  if (f.VB == 4) return launch_attn_lanes<PASS, T, 4, 32>(a, f, st);
   if (f.G == 8) return launch_attn_form<PASS, T, 1, 8, 4, 16>(a, st);
   if (f.KN <= 2 && f.VN <= 8) return launch_attn_form<PASS, T, 1, 32, 2, 8>(a, st);
   return launch_attn_form<PASS, T, 1, 32, 8, 32>(a, st);

@@ -1,4 +1,5 @@
-// The attention kernels for rows whose heads begin on 16 bytes (sm_103a).
+// The attention kernels for rows whose heads all begin on 16, 8 or 4 bytes
+// (VB; sm_103a).
 //
 // A warp takes 32 / G heads of a few neighbouring rows and walks over their
 // edges, U at a time.  The edges' rows come through a ring in shared memory by
@@ -16,8 +17,12 @@ namespace eqmp {
 
 constexpr int kRingWarps = 2;  // of a CTA
 
-__device__ __forceinline__ void copy_async16(uint32_t to, const void* from, int bytes) {  // 16, or 0 for zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+template <int N>
+__device__ __forceinline__ void copy_row(uint32_t to, const void* from, int bytes) {  // N bytes, or 0 for zeros
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(N), "r"(bytes) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
@@ -45,18 +50,44 @@ __device__ __forceinline__ float lds32(uint32_t at) {
   return v;
 }
 
-// 16 bytes as pairs of fp32 values.
-template <typename T>
-__device__ __forceinline__ void pairs_of(const float4& v, float2 (&f)[8 / sizeof(T)]) {
-  if constexpr (sizeof(T) == 4) {
-    f[0] = make_float2(v.x, v.y);
-    f[1] = make_float2(v.z, v.w);
-  } else {
-    const float w[4] = {v.x, v.y, v.z, v.w};
+// VB bytes of a row, and their values as pairs (a single fp32 value with a zero).
+template <int VB>
+struct RawOf;
+template <>
+struct RawOf<16> {
+  using type = float4;
+  static __device__ __forceinline__ float4 lds(uint32_t at) { return lds128(at); }
+};
+template <>
+struct RawOf<8> {
+  using type = float2;
+  static __device__ __forceinline__ float2 lds(uint32_t at) { return lds64(at); }
+};
+template <>
+struct RawOf<4> {
+  using type = float;
+  static __device__ __forceinline__ float lds(uint32_t at) { return lds32(at); }
+};
+
+template <typename T, int VB>
+struct RowVec {
+  using Raw = typename RawOf<VB>::type;
+  static constexpr int EL = VB / sizeof(T), PAIRS = (EL + 1) / 2;
+};
+
+__device__ __forceinline__ float word_of(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ float word_of(const float2& v, int i) { return i == 0 ? v.x : v.y; }
+__device__ __forceinline__ float word_of(const float& v, int) { return v; }
+
+template <typename T, int VB>
+__device__ __forceinline__ void pairs_of(const typename RowVec<T, VB>::Raw& v, float2 (&f)[RowVec<T, VB>::PAIRS]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t b = __float_as_uint(w[i]);
+  for (int i = 0; i < RowVec<T, VB>::PAIRS; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t b = __float_as_uint(word_of(v, i));
       f[i] = make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+    } else {
+      f[i] = make_float2(word_of(v, 2 * i), VB == 4 ? 0.0f : word_of(v, 2 * i + 1));
     }
   }
 }
@@ -164,114 +195,130 @@ __device__ __forceinline__ float scatter_sum(float (&v)[NV], int l) {
 // their cells, forward: fp32 2 edges and 3 stages 786 us, 2 and 2 871, 4 and 2
 // 865, 4 and 3 1147 (six warps); bf16 at 10,000 atoms, 48 edges a row, values of
 // 256: 4 and 2 259 us, 2 and 3 269, 4 and 3 322.
-template <int G, int KN, int VN, int U_, int SMALL>
+template <int VB, int G, int KN, int VN, int U_, int SMALL>
 struct RingShape {
   static constexpr int VECS = KN + VN;
   static constexpr int U = U_;
   static constexpr int HEADS = 32 / G;
-  static constexpr int SMALL_AT = U * VECS * 512;
+  static constexpr int VEC = 32 * VB;  // a vector of every lane
+  static constexpr int SMALL_AT = U * VECS * VEC;
   static constexpr int BATCH = SMALL_AT + (U * HEADS * SMALL + 127) / 128 * 128;
-  static constexpr int STAGES = U * VECS <= 10 ? 3 : 2;
+  static constexpr int STAGES = U * VECS * VB <= 160 ? 3 : 2;
   static constexpr int WARP = STAGES * BATCH;
   static constexpr int CTA = kRingWarps * WARP;
 };
 
-template <typename T, int G, int NV>
-__device__ __forceinline__ void load_row(const T* row, int l, int cols, bool ok, float4 (&v)[NV]) {
-  constexpr int V = 16 / sizeof(T);
+template <typename T, int VB, int G, int NV>
+__device__ __forceinline__ void load_row(const T* row, int l, int cols, bool ok, typename RowVec<T, VB>::Raw (&v)[NV]) {
+  using Raw = typename RowVec<T, VB>::Raw;
+  constexpr int EL = RowVec<T, VB>::EL;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
-    v[j] = ok && (j * G + l) * V < cols ? __ldg(reinterpret_cast<const float4*>(row + (j * G + l) * V)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    v[j] = ok && (j * G + l) * EL < cols ? __ldg(reinterpret_cast<const Raw*>(row + (j * G + l) * EL)) : Raw{};
 }
 
-template <typename T, int NV>
-__device__ __forceinline__ void unpack(const float4 (&v)[NV], float by, float2 (&f)[NV * 8 / sizeof(T)]) {
-  constexpr int P = 8 / sizeof(T);
+template <typename T, int VB, int NV>
+__device__ __forceinline__ void unpack(const typename RowVec<T, VB>::Raw (&v)[NV], float by, float2 (&f)[NV * RowVec<T, VB>::PAIRS]) {
+  constexpr int P = RowVec<T, VB>::PAIRS;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     float2 p[P];
-    pairs_of<T>(v[j], p);
+    pairs_of<T, VB>(v[j], p);
 #pragma unroll
     for (int i = 0; i < P; ++i) f[j * P + i] = make_float2(p[i].x * by, p[i].y * by);
   }
 }
 
-// sum += by * the lane's vectors at `at` (512 bytes apart).
-template <typename T, int NV>
-__device__ __forceinline__ void add_row(uint32_t at, float by, float2 (&sum)[NV * 8 / sizeof(T)]) {
-  constexpr int P = 8 / sizeof(T);
+// sum += by * the lane's vectors at `at`.
+template <typename T, int VB, int NV>
+__device__ __forceinline__ void add_row(uint32_t at, float by, float2 (&sum)[NV * RowVec<T, VB>::PAIRS]) {
+  constexpr int P = RowVec<T, VB>::PAIRS;
   const float2 b = make_float2(by, by);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     float2 p[P];
-    pairs_of<T>(lds128(at + j * 512), p);
+    pairs_of<T, VB>(RawOf<VB>::lds(at + j * 32 * VB), p);
 #pragma unroll
     for (int i = 0; i < P; ++i) sum[j * P + i] = __ffma2_rn(b, p[i], sum[j * P + i]);
   }
 }
 
-template <typename T, int NV>
-__device__ __forceinline__ float dot_row(uint32_t at, const float2 (&with)[NV * 8 / sizeof(T)]) {
-  constexpr int P = 8 / sizeof(T);
+template <typename T, int VB, int NV>
+__device__ __forceinline__ float dot_row(uint32_t at, const float2 (&with)[NV * RowVec<T, VB>::PAIRS]) {
+  constexpr int P = RowVec<T, VB>::PAIRS;
   float2 t = make_float2(0.0f, 0.0f);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     float2 p[P];
-    pairs_of<T>(lds128(at + j * 512), p);
+    pairs_of<T, VB>(RawOf<VB>::lds(at + j * 32 * VB), p);
 #pragma unroll
     for (int i = 0; i < P; ++i) t = __ffma2_rn(p[i], with[j * P + i], t);
   }
   return t.x + t.y;
 }
 
-template <typename T, int G, int NV>
-__device__ __forceinline__ void store_row(T* row, int l, int cols, const float2 (&x)[NV * 8 / sizeof(T)], float by) {
-  constexpr int P = 8 / sizeof(T), V = 2 * P;
+template <typename T, int VB, int G, int NV>
+__device__ __forceinline__ void store_row(T* row, int l, int cols, const float2 (&x)[NV * RowVec<T, VB>::PAIRS], float by) {
+  constexpr int P = RowVec<T, VB>::PAIRS, EL = RowVec<T, VB>::EL;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    if ((j * G + l) * V >= cols) break;
-    float f[V];
+    if ((j * G + l) * EL >= cols) break;
+    T* const to = row + (j * G + l) * EL;
+    float f[2 * P];
 #pragma unroll
     for (int i = 0; i < P; ++i) f[2 * i] = x[j * P + i].x * by, f[2 * i + 1] = x[j * P + i].y * by;
-    Vec<T, V>::store(row + (j * G + l) * V, f);
+    if constexpr (sizeof(T) == 4 && VB == 16) {
+      *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
+    } else if constexpr (sizeof(T) == 4 && VB == 8) {
+      *reinterpret_cast<float2*>(to) = make_float2(f[0], f[1]);
+    } else if constexpr (sizeof(T) == 4) {
+      *to = f[0];
+    } else {
+      __nv_bfloat162 b[P];
+#pragma unroll
+      for (int i = 0; i < P; ++i) b[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      *reinterpret_cast<typename RowVec<T, VB>::Raw*>(to) = *reinterpret_cast<const typename RowVec<T, VB>::Raw*>(b);
+    }
   }
 }
 
-template <typename T, int G, int NV>
-__device__ __forceinline__ void store_row_part(float* row, int l, int cols, const float2 (&x)[NV * 8 / sizeof(T)]) {
-  constexpr int P = 8 / sizeof(T), V = 2 * P;
+template <typename T, int VB, int G, int NV>
+__device__ __forceinline__ void store_row_part(float* row, int l, int cols, const float2 (&x)[NV * RowVec<T, VB>::PAIRS]) {
+  constexpr int P = RowVec<T, VB>::PAIRS, EL = RowVec<T, VB>::EL;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int c = (j * G + l) * V + 2 * i;
-      if (c < cols) row[c] = x[j * P + i].x, row[c + 1] = x[j * P + i].y;
+    for (int i = 0; i < EL; ++i) {
+      const int c = (j * G + l) * EL + i;
+      if (c < cols) row[c] = i % 2 ? x[j * P + i / 2].y : x[j * P + i / 2].x;
     }
 }
 
 // The lane's vectors of a node's head: where they lie, and which of them the
 // lane has.  Rows lie `pitch` bytes apart, below 2^32.
-template <typename T, int G, int NV>
+template <typename T, int VB, int G, int NV>
 struct Lanes {
   const char* base;
   uint32_t pitch;
   bool has[NV];
   __device__ __forceinline__ Lanes(const void* p, long long ld, int h, int cols, int l, bool mine)
-      : base(static_cast<const char*>(p) + ((long long)h * cols + l * (16 / sizeof(T))) * sizeof(T)), pitch((uint32_t)(ld * sizeof(T))) {
+      : base(static_cast<const char*>(p) + (long long)h * cols * (int)sizeof(T) + l * VB), pitch((uint32_t)(ld * sizeof(T))) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) has[i] = mine && (i * G + l) * (int)(16 / sizeof(T)) < cols;
+    for (int i = 0; i < NV; ++i) has[i] = mine && (i * G + l) * VB < cols * (int)sizeof(T);
   }
   __device__ __forceinline__ void copy(uint32_t to, uint32_t node, int bytes) const {
     const char* from = base + (unsigned long long)node * pitch;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (has[i]) copy_async16(to + i * 512, from + i * G * 16, bytes);
+      if (has[i]) copy_row<VB>(to + i * 32 * VB, from + i * G * VB, bytes);
   }
   // Zeros where no copy will write.
   __device__ __forceinline__ void clear(uint32_t at) const {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (!has[i]) asm volatile("st.shared.v4.f32 [%0], {%1, %1, %1, %1};" ::"r"(at + i * 512), "f"(0.0f) : "memory");
+      if (!has[i])
+#pragma unroll
+        for (int b = 0; b < VB; b += 4) asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + i * 32 * VB + b), "f"(0.0f) : "memory");
   }
 };
 
@@ -279,18 +326,18 @@ template <typename Shape, typename A, typename B>
 __device__ __forceinline__ void clear_ring(const A& a, const B& b, int a_vecs, uint32_t at_lane) {
 #pragma unroll 1
   for (int i = 0; i < Shape::STAGES * Shape::U; ++i) {
-    const uint32_t at = at_lane + i / Shape::U * Shape::BATCH + i % Shape::U * Shape::VECS * 512;
+    const uint32_t at = at_lane + i / Shape::U * Shape::BATCH + i % Shape::U * Shape::VECS * Shape::VEC;
     a.clear(at);
-    b.clear(at + a_vecs * 512);
+    b.clear(at + a_vecs * Shape::VEC);
   }
 }
 
 // Keys, values and biases of the receivers' passes, into the stages in turn.
-template <typename T, int G, int KN, int VN, int U_>
+template <typename T, int VB, int G, int KN, int VN, int U_>
 struct Feed {
-  using Shape = RingShape<G, KN, VN, U_, 4>;
-  const Lanes<T, G, KN> k;
-  const Lanes<T, G, VN> v;
+  using Shape = RingShape<VB, G, KN, VN, U_, 4>;
+  const Lanes<T, VB, G, KN> k;
+  const Lanes<T, VB, G, VN> v;
   const float* const bias;  // of edge l and the lane's head; NULL: none for this lane
   const int l;
   uint32_t to, to_bias;  // where the next batch goes
@@ -300,7 +347,7 @@ struct Feed {
 
   __device__ __forceinline__ Feed(const AttnArgs& a, const Work& w, uint32_t ring, int lane, int l, int hh, int h, bool mine)
       : k(a.k, a.k_ld, h, a.D, l, mine), v(a.v, a.v_ld, h, a.Dv, l, mine),
-        bias(a.bias && mine && l < Shape::U ? a.bias + (long long)l * a.H + h : nullptr), l(l), to(ring + lane * 16),
+        bias(a.bias && mine && l < Shape::U ? a.bias + (long long)l * a.H + h : nullptr), l(l), to(ring + lane * VB),
         to_bias(ring + Shape::SMALL_AT + (hh * Shape::U + l) * 4), stage(0) {
     clear_ring<Shape>(k, v, KN, to);
     put.start(w);
@@ -318,9 +365,9 @@ struct Feed {
       node = ok ? node : 0;
 #pragma unroll
       for (int u = 0; u < Shape::U; ++u) {
-        const int j = __shfl_sync(0xffffffffu, node, u), bytes = (there >> u & 1) * 16;
-        k.copy(to + u * Shape::VECS * 512, j, bytes);
-        v.copy(to + (u * Shape::VECS + KN) * 512, j, bytes);
+        const int j = __shfl_sync(0xffffffffu, node, u), bytes = (there >> u & 1) * VB;
+        k.copy(to + u * Shape::VECS * Shape::VEC, j, bytes);
+        v.copy(to + (u * Shape::VECS + KN) * Shape::VEC, j, bytes);
       }
       if (bias && l < n) copy_async<4>(to_bias, bias + (long long)put.e * a.H);
       put.e += Shape::U;
@@ -339,10 +386,10 @@ struct Feed {
 __device__ __forceinline__ bool is_out(unsigned out, int lane, int l, int u) { return out >> (lane - l + u) & 1; }
 
 // ---------------------------------------------------------------- forward
-template <typename T, int G, int KN, int VN, int U>
+template <typename T, int VB, int G, int KN, int VN, int U>
 __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_constant__ AttnArgs a) {
-  using Shape = RingShape<G, KN, VN, U, 4>;
-  constexpr int V = 16 / sizeof(T), KP = KN * V / 2, VP = VN * V / 2;
+  using Shape = RingShape<VB, G, KN, VN, U, 4>;
+  constexpr int P = RowVec<T, VB>::PAIRS, KP = KN * P, VP = VN * P;
   extern __shared__ __align__(128) uint8_t space[];
   const Rows rows{a.off, a.N, a.E, a.block, a.blocks};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G, hh = lane / G;
@@ -351,19 +398,19 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_
   const int h = blockIdx.y * (32 / G) + hh;
   const bool mine = h < a.H;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(space) + warp * Shape::WARP;
-  Feed<T, G, KN, VN, U> feed(a, w, ring, lane, l, hh, h, mine);
-  float4 q_next[KN];
+  Feed<T, VB, G, KN, VN, U> feed(a, w, ring, lane, l, hh, h, mine);
+  typename RowVec<T, VB>::Raw q_next[KN];
   auto load_q = [&](int i) {
-    load_row<T, G, KN>(static_cast<const T*>(a.q) + (w.row + i) * a.q_ld + (long long)h * a.D, l, a.D, mine && i < w.n, q_next);
+    load_row<T, VB, G, KN>(static_cast<const T*>(a.q) + (w.row + i) * a.q_ld + (long long)h * a.D, l, a.D, mine && i < w.n, q_next);
   };
   load_q(0);
-  const uint32_t at0 = ring + lane * 16, bias0 = ring + Shape::SMALL_AT + (hh * U + l % U) * 4;
+  const uint32_t at0 = ring + lane * VB, bias0 = ring + Shape::SMALL_AT + (hh * U + l % U) * 4;
   uint32_t stage_at = 0;
 #pragma unroll 1
   for (int i = 0; i < w.n; ++i) {
     const int e0 = __shfl_sync(0xffffffffu, w.e0, i), e1 = __shfl_sync(0xffffffffu, w.e1, i);
     float2 q[KP], acc[VP];
-    unpack<T, KN>(q_next, a.scale, q);
+    unpack<T, VB, KN>(q_next, a.scale, q);
     load_q(i + 1);
 #pragma unroll
     for (int x = 0; x < VP; ++x) acc[x] = make_float2(0.0f, 0.0f);
@@ -376,7 +423,7 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_
       const uint32_t at = at0 + stage_at;
       float s[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) s[u] = dot_row<T, KN>(at + u * Shape::VECS * 512, q);
+      for (int u = 0; u < U; ++u) s[u] = dot_row<T, VB, KN>(at + u * Shape::VECS * Shape::VEC, q);
       float score = scatter_sum<G, U>(s, l);  // of edge e + l % U
       const bool in = mine && e + l % U < e1;
       if (a.bias) {
@@ -403,11 +450,11 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_
 #pragma unroll 1
         for (int u = 0; u < U; ++u) {
           const float pu = __shfl_sync(0xffffffffu, p, lane - l + u);
-          if (!is_out(out, lane, l, u)) add_row<T, VN>(at + (u * Shape::VECS + KN) * 512, pu, acc);
+          if (!is_out(out, lane, l, u)) add_row<T, VB, VN>(at + (u * Shape::VECS + KN) * Shape::VEC, pu, acc);
         }
       } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u) add_row<T, VN>(at + (u * Shape::VECS + KN) * 512, __shfl_sync(0xffffffffu, p, lane - l + u), acc);
+        for (int u = 0; u < U; ++u) add_row<T, VB, VN>(at + (u * Shape::VECS + KN) * Shape::VEC, __shfl_sync(0xffffffffu, p, lane - l + u), acc);
       }
       stage_at = stage_at == (Shape::STAGES - 1) * Shape::BATCH ? 0 : stage_at + Shape::BATCH;
     }
@@ -418,7 +465,7 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_
     if (slot >= 0) {
       float* to = a.part + ((long long)slot * a.H + h) * (a.Dv + 2);
       if (l == 0) to[0] = m, to[1] = z;
-      store_row_part<T, G, VN>(to + 2, l, a.Dv, acc);
+      store_row_part<T, VB, G, VN>(to + 2, l, a.Dv, acc);
       continue;
     }
     const long long to = (long long)(w.row + i) * a.H + h;
@@ -426,16 +473,16 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_
       a.stats[2 * to] = z == 0.0f ? 0.0f : m;
       a.stats[2 * to + 1] = z;
     }
-    if (a.out) store_row<T, G, VN>(static_cast<T*>(a.out) + to * a.Dv, l, a.Dv, acc, z == 0.0f ? 0.0f : 1.0f / z);
+    if (a.out) store_row<T, VB, G, VN>(static_cast<T*>(a.out) + to * a.Dv, l, a.Dv, acc, z == 0.0f ? 0.0f : 1.0f / z);
   }
   copy_wait<0>();
 }
 
 // ---------------------------------------------------------------- backward
-template <typename T, int G, int KN, int VN, int U>
+template <typename T, int VB, int G, int KN, int VN, int U>
 __global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(const __grid_constant__ AttnArgs a) {
-  using Shape = RingShape<G, KN, VN, U, 4>;
-  constexpr int V = 16 / sizeof(T), KP = KN * V / 2, VP = VN * V / 2;
+  using Shape = RingShape<VB, G, KN, VN, U, 4>;
+  constexpr int P = RowVec<T, VB>::PAIRS, KP = KN * P, VP = VN * P;
   extern __shared__ __align__(128) uint8_t space[];
   const Rows rows{a.off, a.N, a.E, a.block, a.blocks};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G, hh = lane / G;
@@ -444,25 +491,25 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(const __grid
   const int h = blockIdx.y * (32 / G) + hh;
   const bool mine = h < a.H;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(space) + warp * Shape::WARP;
-  Feed<T, G, KN, VN, U> feed(a, w, ring, lane, l, hh, h, mine);
-  float4 q_next[KN], g_next[VN];
+  Feed<T, VB, G, KN, VN, U> feed(a, w, ring, lane, l, hh, h, mine);
+  typename RowVec<T, VB>::Raw q_next[KN], g_next[VN];
   float2 st_next;
   auto load_next = [&](int i) {
     const bool ok = mine && i < w.n;
-    load_row<T, G, KN>(static_cast<const T*>(a.q) + (w.row + i) * a.q_ld + (long long)h * a.D, l, a.D, ok, q_next);
-    load_row<T, G, VN>(static_cast<const T*>(a.g) + (w.row + i) * a.g_ld + (long long)h * a.Dv, l, a.Dv, ok, g_next);
+    load_row<T, VB, G, KN>(static_cast<const T*>(a.q) + (w.row + i) * a.q_ld + (long long)h * a.D, l, a.D, ok, q_next);
+    load_row<T, VB, G, VN>(static_cast<const T*>(a.g) + (w.row + i) * a.g_ld + (long long)h * a.Dv, l, a.Dv, ok, g_next);
     const float* st = a.stats + 2 * ((long long)(w.row + i) * a.H + h);
     st_next = ok ? make_float2(__ldg(st), __ldg(st + 1)) : make_float2(0.0f, 0.0f);
   };
   load_next(0);
-  const uint32_t at0 = ring + lane * 16, bias0 = ring + Shape::SMALL_AT + (hh * U + l % U) * 4;
+  const uint32_t at0 = ring + lane * VB, bias0 = ring + Shape::SMALL_AT + (hh * U + l % U) * 4;
   uint32_t stage_at = 0;
 #pragma unroll 1
   for (int i = 0; i < w.n; ++i) {
     const int e0 = __shfl_sync(0xffffffffu, w.e0, i), e1 = __shfl_sync(0xffffffffu, w.e1, i);
     float2 q[KP], g[VP], pdk[KP], pk[KP];
-    unpack<T, KN>(q_next, a.scale, q);
-    unpack<T, VN>(g_next, 1.0f, g);
+    unpack<T, VB, KN>(q_next, a.scale, q);
+    unpack<T, VB, VN>(g_next, 1.0f, g);
     const float m = st_next.x, z = st_next.y, rz = 1.0f / z;
     load_next(i + 1);
 #pragma unroll
@@ -479,8 +526,8 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(const __grid
         float s[2 * U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          s[u] = dot_row<T, KN>(at + u * Shape::VECS * 512, q);
-          s[U + u] = dot_row<T, VN>(at + (u * Shape::VECS + KN) * 512, g);
+          s[u] = dot_row<T, VB, KN>(at + u * Shape::VECS * Shape::VEC, q);
+          s[U + u] = dot_row<T, VB, VN>(at + (u * Shape::VECS + KN) * Shape::VEC, g);
         }
         const float one = scatter_sum<G, 2 * U>(s, l), other = __shfl_xor_sync(0xffffffffu, one, U);
         score = l & U ? other : one;
@@ -489,8 +536,8 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(const __grid
         float s[U], d[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          s[u] = dot_row<T, KN>(at + u * Shape::VECS * 512, q);
-          d[u] = dot_row<T, VN>(at + (u * Shape::VECS + KN) * 512, g);
+          s[u] = dot_row<T, VB, KN>(at + u * Shape::VECS * Shape::VEC, q);
+          d[u] = dot_row<T, VB, VN>(at + (u * Shape::VECS + KN) * Shape::VEC, g);
         }
         score = scatter_sum<G, U>(s, l);
         dp = scatter_sum<G, U>(d, l);
@@ -512,12 +559,12 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(const __grid
         if (out && is_out(out, lane, l, u)) return;
 #pragma unroll
         for (int j = 0; j < KN; ++j) {
-          float2 x[V / 2];
-          pairs_of<T>(lds128(at + (u * Shape::VECS + j) * 512), x);
+          float2 x[P];
+          pairs_of<T, VB>(RawOf<VB>::lds(at + (u * Shape::VECS + j) * Shape::VEC), x);
 #pragma unroll
-          for (int y = 0; y < V / 2; ++y) {
-            pk[j * V / 2 + y] = __ffma2_rn(make_float2(pu, pu), x[y], pk[j * V / 2 + y]);
-            pdk[j * V / 2 + y] = __ffma2_rn(make_float2(pdpu, pdpu), x[y], pdk[j * V / 2 + y]);
+          for (int y = 0; y < P; ++y) {
+            pk[j * P + y] = __ffma2_rn(make_float2(pu, pu), x[y], pk[j * P + y]);
+            pdk[j * P + y] = __ffma2_rn(make_float2(pdpu, pdpu), x[y], pdk[j * P + y]);
           }
         }
       };
@@ -537,8 +584,8 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(const __grid
     if (slot >= 0) {
       float* to = a.part + ((long long)slot * a.H + h) * (2 * a.D + 1);
       if (l == 0) to[0] = delta;
-      store_row_part<T, G, KN>(to + 1, l, a.D, pdk);
-      store_row_part<T, G, KN>(to + 1 + a.D, l, a.D, pk);
+      store_row_part<T, VB, G, KN>(to + 1, l, a.D, pdk);
+      store_row_part<T, VB, G, KN>(to + 1 + a.D, l, a.D, pk);
       continue;
     }
     const long long to = (long long)(w.row + i) * a.H + h;
@@ -546,16 +593,16 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(const __grid
     if (a.gq) {
 #pragma unroll
       for (int x = 0; x < KP; ++x) pdk[x] = __ffma2_rn(make_float2(-delta, -delta), pk[x], pdk[x]);
-      store_row<T, G, KN>(static_cast<T*>(a.gq) + to * a.D, l, a.D, pdk, a.scale);
+      store_row<T, VB, G, KN>(static_cast<T*>(a.gq) + to * a.D, l, a.D, pdk, a.scale);
     }
   }
   copy_wait<0>();
 }
 
-template <typename T, int G, int KN, int VN, int U>
+template <typename T, int VB, int G, int KN, int VN, int U>
 __global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(const __grid_constant__ AttnArgs a) {
-  using Shape = RingShape<G, KN, VN, U, 16>;  // p and dp, delta, the edge's number
-  constexpr int V = 16 / sizeof(T), KP = KN * V / 2, VP = VN * V / 2, HEADS = 32 / G;
+  using Shape = RingShape<VB, G, KN, VN, U, 16>;  // p and dp, delta, the edge's number
+  constexpr int P = RowVec<T, VB>::PAIRS, KP = KN * P, VP = VN * P, HEADS = 32 / G;
   constexpr int DELTA_AT = Shape::SMALL_AT + U * HEADS * 8, EDGE_AT = DELTA_AT + U * HEADS * 4;
   extern __shared__ __align__(128) uint8_t space[];
   const Rows rows{a.send_off, a.Ns, a.E_send, a.block, a.blocks};
@@ -564,10 +611,10 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(const __grid
   if (w.n == 0) return;
   const int h = blockIdx.y * HEADS + hh;
   const bool mine = h < a.H;
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(space) + warp * Shape::WARP, at0 = ring + lane * 16;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(space) + warp * Shape::WARP, at0 = ring + lane * VB;
   const uint32_t item = hh * U + l % U;  // of the small values: the lane's own edge
-  const Lanes<T, G, KN> q(a.q, a.q_ld, h, a.D, l, mine);
-  const Lanes<T, G, VN> g(a.g, a.g_ld, h, a.Dv, l, mine);
+  const Lanes<T, VB, G, KN> q(a.q, a.q_ld, h, a.D, l, mine);
+  const Lanes<T, VB, G, VN> g(a.g, a.g_ld, h, a.Dv, l, mine);
   clear_ring<Shape>(q, g, KN, at0);
 
   Walk put;
@@ -604,9 +651,9 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(const __grid
       const int node = ok ? my_dst : 0;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = __shfl_sync(0xffffffffu, node, u), bytes = (there >> u & 1) * 16;
-        q.copy(at0 + put_at + u * Shape::VECS * 512, i, bytes);
-        g.copy(at0 + put_at + (u * Shape::VECS + KN) * 512, i, bytes);
+        const int i = __shfl_sync(0xffffffffu, node, u), bytes = (there >> u & 1) * VB;
+        q.copy(at0 + put_at + u * Shape::VECS * Shape::VEC, i, bytes);
+        g.copy(at0 + put_at + (u * Shape::VECS + KN) * Shape::VEC, i, bytes);
       }
       // lane l < U of a head: the small values of edge l; p = -1 where there is no such edge, or no receiver
       const int e = __shfl_sync(0xffffffffu, my_edge, l % U), i = __shfl_sync(0xffffffffu, node, l % U);
@@ -655,8 +702,8 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(const __grid
       auto add = [&](int u) {
         const float pu = __shfl_sync(0xffffffffu, p, lane - l + u), dsu = __shfl_sync(0xffffffffu, ds, lane - l + u);
         if (out && is_out(out, lane, l, u)) return;
-        add_row<T, KN>(at + u * Shape::VECS * 512, dsu, gk);
-        add_row<T, VN>(at + (u * Shape::VECS + KN) * 512, pu, gv);
+        add_row<T, VB, KN>(at + u * Shape::VECS * Shape::VEC, dsu, gk);
+        add_row<T, VB, VN>(at + (u * Shape::VECS + KN) * Shape::VEC, pu, gv);
       };
       if (out) {
 #pragma unroll 1
@@ -671,13 +718,13 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(const __grid
     if (!mine) continue;
     if (slot >= 0) {
       float* to = a.part + ((long long)slot * a.H + h) * (a.D + a.Dv);
-      store_row_part<T, G, KN>(to, l, a.D, gk);
-      store_row_part<T, G, VN>(to + a.D, l, a.Dv, gv);
+      store_row_part<T, VB, G, KN>(to, l, a.D, gk);
+      store_row_part<T, VB, G, VN>(to + a.D, l, a.Dv, gv);
       continue;
     }
     const long long to = (long long)(w.row + i) * a.H + h;
-    if (a.gk) store_row<T, G, KN>(static_cast<T*>(a.gk) + to * a.D, l, a.D, gk, a.scale);
-    if (a.gv) store_row<T, G, VN>(static_cast<T*>(a.gv) + to * a.Dv, l, a.Dv, gv, 1.0f);
+    if (a.gk) store_row<T, VB, G, KN>(static_cast<T*>(a.gk) + to * a.D, l, a.D, gk, a.scale);
+    if (a.gv) store_row<T, VB, G, VN>(static_cast<T*>(a.gv) + to * a.Dv, l, a.Dv, gv, 1.0f);
   }
   copy_wait<0>();
 }

@@ -145,7 +145,7 @@ def test_sizes(lib, name):
 
 
 def test_workspace_sizes(lib):
-    assert lib.eqmp_edge_attention_workspace_size(256, 8, 128) == 0 < lib.eqmp_edge_attention_workspace_size(257, 8, 128)
+    assert lib.eqmp_edge_attention_workspace_size(64, 8, 128) == 0 < lib.eqmp_edge_attention_workspace_size(65, 8, 128)
     # the parts of a large graph stay small beside its rows
     assert lib.eqmp_edge_attention_workspace_size(1909372, 8, 128) < 20 << 20
     assert lib.eqmp_edge_attention_workspace_size(-1, 8, 128) == lib.eqmp_edge_attention_workspace_size(5, 8, 1025) == -1

@@ -24,7 +24,7 @@ def eq():
 
 
 MIXED = [0, 1, 2, 3, 31, 32, 33, 0, 5, 19, 64, 65, 4, 7, 0]
-LONG = [3, 700, 0, 300, 257, 256, 1, 128]  # split rows: blocks of 128 edges, cut at any place
+LONG = [3, 700, 0, 300, 257, 256, 1, 128]  # split rows: blocks of 32 edges, cut at any place
 
 
 class Problem:
@@ -79,7 +79,7 @@ class Problem:
         return got, grads
 
 
-SHAPES = [(1, 1, 1), (4, 16, 128), (8, 32, 128), (3, 5, 49), (2, 64, 256), (5, 18, 100), (1, 256, 1024), (12, 8, 16),
+SHAPES = [(1, 1, 1), (4, 18, 50), (2, 65, 30), (4, 6, 10), (4, 16, 128), (8, 32, 128), (3, 5, 49), (2, 64, 256), (5, 18, 100), (1, 256, 1024), (12, 8, 16),
           (6, 24, 72), (16, 4, 4), (2, 33, 300), (3, 128, 512), (8, 32, 256), (33, 8, 8)]
 
 
