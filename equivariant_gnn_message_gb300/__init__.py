@@ -1137,8 +1137,9 @@ def _attention_inputs(q, k, v, row_offsets, src, bias, torch):
     """Checks of what both passes of the attention take; the sizes and the arguments in the order of the C call."""
     f32, i32 = torch.float32, torch.int32
     dev = _head_input(q, "q", torch)
-    _head_input(k, "k", torch)
-    _head_input(v, "v", torch)
+    if not (isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor) and k.dim() == 3 and v.dim() == 3 and v.shape[2] > 0):
+        _head_input(k, "k", torch)
+        _head_input(v, "v", torch)
     dtype, (n, h, d), n_src, dv = q.dtype, q.shape, k.shape[0], v.shape[2]
     qp, q_ld = _heads(q, "q", dtype, (n, h, d), dev, torch)
     kp, k_ld = _heads(k, "k", dtype, (n_src, h, d), dev, torch)

@@ -85,9 +85,9 @@ static AttnForm form_of(const Sizes& n, int64_t rows, int bytes, int alignment) 
   for (f.VB = alignment < 4 ? 0 : alignment; f.VB >= 4; f.VB /= 2) {
     const int k = (n.D * bytes + f.VB - 1) / f.VB, v = (n.Dv * bytes + f.VB - 1) / f.VB;
     auto fits = [&](int G) { return k <= 2 * G && v <= 8 * G; };
-    f.G = f.VB == 16 ? 8 : f.VB == 8 ? 16 : 32;
-    if (f.VB == 16)
-      while (f.G < 32 && (!fits(f.G) || n.H * f.G * 2 <= 32 || rows * ((n.H * f.G + 31) / 32) < 152 * 16)) f.G *= 2;
+    f.G = 8;
+    while (f.G < 32 && (!fits(f.G) || n.H * f.G * 2 <= 32 || rows * ((n.H * f.G + 31) / 32) < 152 * 16)) f.G *= 2;
+    if (f.VB < 16 && f.G > 8) f.G = f.VB == 8 ? 16 : 32;
     f.KN = (k + f.G - 1) / f.G;
     f.VN = (v + f.G - 1) / f.G;
     if (fits(f.G)) break;

@@ -39,6 +39,7 @@ struct AttnArgs {
   int N, Ns, E, E_send, H, D, Dv;
   int block, blocks;  // edges of a block of a long row, blocks in all (0: rows are not split)
   int rows_each;      // rows of a warp in the kernels of attn_ring.cuh
+  int early;          // the kernel that joins long rows may be launched at once
 };
 
 constexpr int kAttnWarps = 4;  // of a CTA, each with its own piece
@@ -110,6 +111,13 @@ __device__ __forceinline__ Piece find_piece(const Rows& r, int w) {
   t.e0 = x;
   t.e1 = min(e1, x + r.block);
   return t;
+}
+
+// Lets k_attn_join be launched while this kernel runs: its CTAs look for long rows
+// and wait.  Only where all CTAs fit on the device at once, so that none is kept
+// from its place.
+__device__ __forceinline__ void let_join_start(const AttnArgs& a) {
+  if (a.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- vectors
@@ -246,6 +254,7 @@ __device__ __forceinline__ void head_sum(float (&t)[U]) {
 // time, with the running maximum and sum of a softmax.
 template <typename T, int V, int G, int KN, int VN, int U>
 __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_fwd(AttnArgs a) {
+  let_join_start(a);
   const Rows rows{a.off, a.N, a.E, a.block, a.blocks};
   const Piece t = find_piece(rows, blockIdx.x * kAttnWarps + (threadIdx.x >> 5));
   if (t.row < 0) return;
@@ -325,6 +334,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_fwd(AttnArgs a) {
 //   dq = scale (sum_e p dp k  -  delta sum_e p k)
 template <typename T, int V, int G, int KN, int VN, int U>
 __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_recv(AttnArgs a) {
+  let_join_start(a);
   const Rows rows{a.off, a.N, a.E, a.block, a.blocks};
   const Piece t = find_piece(rows, blockIdx.x * kAttnWarps + (threadIdx.x >> 5));
   if (t.row < 0) return;
@@ -400,6 +410,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_recv(AttnArgs a) {
 // the rows of their receivers, in the order of the sender view; and dbias.
 template <typename T, int V, int G, int KN, int VN, int U>
 __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_send(AttnArgs a) {
+  let_join_start(a);
   const Rows rows{a.send_off, a.Ns, a.E_send, a.block, a.blocks};
   const Piece t = find_piece(rows, blockIdx.x * kAttnWarps + (threadIdx.x >> 5));
   if (t.row < 0) return;
@@ -459,32 +470,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_send(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------- joining
-// The parts of a long row, one CTA a row and head: threadIdx.x goes over the
-// columns, threadIdx.y over the parts.  Block c's CTA works when block c is the
-// first that begins inside the row.
+// The parts of long rows.  A CTA looks at kJoinY blocks, a warp each: a row is
+// joined where the first block that begins inside it is found.  For each such row
+// and head threadIdx.x then goes over the columns, threadIdx.y over the parts.
 enum { kJoinFwd, kJoinRecv, kJoinSend };
 constexpr int kJoinX = 32, kJoinY = 16;
 
 template <int MODE, typename T>
-__global__ void __launch_bounds__(kJoinX * kJoinY) k_attn_join(AttnArgs a) {
-  __shared__ float red[kJoinY][kJoinX];
-  __shared__ int range[3];
-  const Rows rows = MODE == kJoinSend ? Rows{a.send_off, a.Ns, a.E_send, a.block, a.blocks}
-                                      : Rows{a.off, a.N, a.E, a.block, a.blocks};
-  const int c = blockIdx.x, h = blockIdx.y, x = threadIdx.x, y = threadIdx.y;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // until the kernel that writes the parts is done
-  if (y == 0) {
-    const Piece t = find_piece(rows, c);
-    int first = -1, last = -1;
-    if (t.row >= 0) {
-      const int e0 = clamped(__ldg(rows.off + t.row), rows.E), e1 = clamped(__ldg(rows.off + t.row + 1), rows.E);
-      if (e0 / rows.block == c - 1) first = c, last = (e1 - 1) / rows.block;
-    }
-    if (x == 0) range[0] = first, range[1] = last, range[2] = t.row;
-  }
-  __syncthreads();
-  const int first = range[0], last = range[1], row = range[2];
-  if (first < 0) return;
+__device__ void join_row(const AttnArgs& a, int first, int last, int row, int h, float (&red)[kJoinY][kJoinX]) {
+  const int x = threadIdx.x, y = threadIdx.y;
   const int width = MODE == kJoinFwd ? a.Dv + 2 : MODE == kJoinRecv ? 2 * a.D + 1 : a.D + a.Dv;
   // part 0: the row's beginning, in the slot of the block where it lies; then the blocks
   auto part = [&](int i) { return a.part + ((long long)(i ? first + i - 1 : a.blocks + first - 1) * a.H + h) * width; };
@@ -553,6 +547,30 @@ __global__ void __launch_bounds__(kJoinX * kJoinY) k_attn_join(AttnArgs a) {
         Vec<T, 1>::store(static_cast<T*>(a.gv) + at * a.Dv + col - a.D, &t);
       }
     }
+  }
+}
+
+template <int MODE, typename T>
+__global__ void __launch_bounds__(kJoinX * kJoinY) k_attn_join(const __grid_constant__ AttnArgs a) {
+  __shared__ float red[kJoinY][kJoinX];
+  __shared__ int range[kJoinY][3];
+  const Rows rows = MODE == kJoinSend ? Rows{a.send_off, a.Ns, a.E_send, a.block, a.blocks}
+                                      : Rows{a.off, a.N, a.E, a.block, a.blocks};
+  const int x = threadIdx.x, y = threadIdx.y, c = blockIdx.x * kJoinY + y;
+  Piece t;
+  t.row = -1;
+  if (c < a.blocks) t = find_piece(rows, c);
+  int first = -1, last = -1;
+  if (t.row >= 0) {
+    const int e0 = clamped(__ldg(rows.off + t.row), rows.E), e1 = clamped(__ldg(rows.off + t.row + 1), rows.E);
+    if (e0 / rows.block == c - 1) first = c, last = (e1 - 1) / rows.block;
+  }
+  if (x == 0) range[y][0] = first, range[y][1] = last, range[y][2] = t.row;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // until the kernel that writes the parts is done
+  __syncthreads();
+  for (int i = 0; i < kJoinY; ++i) {
+    if (range[i][0] < 0) continue;
+    for (int h = blockIdx.y; h < a.H; h += gridDim.y) join_row<MODE, T>(a, range[i][0], range[i][1], range[i][2], h, red);
   }
 }
 

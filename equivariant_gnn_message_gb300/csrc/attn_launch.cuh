@@ -34,7 +34,7 @@ eqmp_status launch_attn_join(const AttnArgs& a, cudaStream_t st) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.blocks, (unsigned)a.H);
+  cfg.gridDim = dim3((unsigned)((a.blocks + kJoinY - 1) / kJoinY), (unsigned)(a.H < 16 ? a.H : 16));
   cfg.blockDim = dim3(kJoinX, kJoinY);
   cfg.stream = st;
   cfg.attrs = &attr;
@@ -44,10 +44,11 @@ eqmp_status launch_attn_join(const AttnArgs& a, cudaStream_t st) {
 }
 
 template <int PASS, typename T, int V, int G, int KN, int VN>
-eqmp_status launch_attn_form(const AttnArgs& a, cudaStream_t st) {
+eqmp_status launch_attn_form(AttnArgs a, cudaStream_t st) {
   constexpr int VALUES = VN * V, U = VALUES <= 16 ? 4 : VALUES <= 32 ? 2 : 1;
   const int rows = PASS == kAttnSend ? a.Ns : a.N;
   const dim3 grid((unsigned)((rows + a.blocks + kAttnWarps - 1) / kAttnWarps), (unsigned)((a.H * G + 31) / 32));
+  a.early = (long long)grid.x * grid.y <= 152 * 2;
   if constexpr (PASS == kAttnFwd)
     k_attn_fwd<T, V, G, KN, VN, U><<<grid, 32 * kAttnWarps, 0, st>>>(a);
   else if constexpr (PASS == kAttnRecv)
@@ -58,11 +59,12 @@ eqmp_status launch_attn_form(const AttnArgs& a, cudaStream_t st) {
 }
 
 template <int PASS, typename T, int VB, int G, int KN, int VN>
-eqmp_status launch_attn_ring(const AttnArgs& a, cudaStream_t st) {
+eqmp_status launch_attn_ring(AttnArgs a, cudaStream_t st) {
   constexpr int U = KN + VN <= 4 || (sizeof(T) == 2 && KN + VN <= 5) || VB < 16 ? 4 : 2;
   constexpr int SMEM = RingShape<VB, G, KN, VN, U, PASS == kAttnSend ? 16 : 4>::CTA;
   const long long rows = PASS == kAttnSend ? a.Ns : a.N, workers = a.blocks + (rows + a.rows_each - 1) / a.rows_each;
   const dim3 grid((unsigned)((workers + kRingWarps - 1) / kRingWarps), (unsigned)((a.H * G + 31) / 32));
+  a.early = (long long)grid.x * grid.y <= 152 * 4;
   static unsigned long long done = 0;
   auto run = [&](auto kernel) {
     if (ensure_smem_attr(kernel, SMEM, &done) != cudaSuccess) return EQMP_ERR_CUDA;
@@ -88,6 +90,13 @@ eqmp_status launch_attn_lanes(const AttnArgs& a, const AttnForm& f, cudaStream_t
   return launch_attn_ring<PASS, T, VB, G, 2, 8>(a, st);
 }
 
+// Short heads on 8 or 4 bytes: eight lanes each.
+template <int PASS, typename T, int VB>
+eqmp_status launch_attn_few(const AttnArgs& a, const AttnForm& f, cudaStream_t st) {
+  if (f.KN <= 1 && f.VN <= 2) return launch_attn_ring<PASS, T, VB, 8, 1, 2>(a, st);
+  return launch_attn_ring<PASS, T, VB, 8, 2, 8>(a, st);
+}
+
 template <int PASS, typename T>
 eqmp_status launch_attn(AttnArgs a, const AttnForm& f, cudaStream_t st) {
   a.rows_each = f.rows_each;
@@ -96,8 +105,8 @@ eqmp_status launch_attn(AttnArgs a, const AttnForm& f, cudaStream_t st) {
     if (f.G == 16) return launch_attn_lanes<PASS, T, 16, 16>(a, f, st);
     return launch_attn_lanes<PASS, T, 16, 32>(a, f, st);
   }
-  if (f.VB == 8) return launch_attn_lanes<PASS, T, 8, 16>(a, f, st);
-  if (f.VB == 4) return launch_attn_lanes<PASS, T, 4, 32>(a, f, st);
+  if (f.VB == 8) return f.G == 8 ? launch_attn_few<PASS, T, 8>(a, f, st) : launch_attn_lanes<PASS, T, 8, 16>(a, f, st);
+  if (f.VB == 4) return f.G == 8 ? launch_attn_few<PASS, T, 4>(a, f, st) : launch_attn_lanes<PASS, T, 4, 32>(a, f, st);
   if (f.G == 8) return launch_attn_form<PASS, T, 1, 8, 4, 16>(a, st);
   if (f.KN <= 2 && f.VN <= 8) return launch_attn_form<PASS, T, 1, 32, 2, 8>(a, st);
   return launch_attn_form<PASS, T, 1, 32, 8, 32>(a, st);

@@ -391,6 +391,7 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_
   using Shape = RingShape<VB, G, KN, VN, U, 4>;
   constexpr int P = RowVec<T, VB>::PAIRS, KP = KN * P, VP = VN * P;
   extern __shared__ __align__(128) uint8_t space[];
+  let_join_start(a);
   const Rows rows{a.off, a.N, a.E, a.block, a.blocks};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G, hh = lane / G;
   const Work w = find_work(rows, blockIdx.x * kRingWarps + warp, a.rows_each);
@@ -484,6 +485,7 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(const __grid
   using Shape = RingShape<VB, G, KN, VN, U, 4>;
   constexpr int P = RowVec<T, VB>::PAIRS, KP = KN * P, VP = VN * P;
   extern __shared__ __align__(128) uint8_t space[];
+  let_join_start(a);
   const Rows rows{a.off, a.N, a.E, a.block, a.blocks};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G, hh = lane / G;
   const Work w = find_work(rows, blockIdx.x * kRingWarps + warp, a.rows_each);
@@ -605,6 +607,7 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(const __grid
   constexpr int P = RowVec<T, VB>::PAIRS, KP = KN * P, VP = VN * P, HEADS = 32 / G;
   constexpr int DELTA_AT = Shape::SMALL_AT + U * HEADS * 8, EDGE_AT = DELTA_AT + U * HEADS * 4;
   extern __shared__ __align__(128) uint8_t space[];
+  let_join_start(a);
   const Rows rows{a.send_off, a.Ns, a.E_send, a.block, a.blocks};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G, hh = lane / G;
   const Work w = find_work(rows, blockIdx.x * kRingWarps + warp, a.rows_each);

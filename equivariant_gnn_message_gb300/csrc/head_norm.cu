@@ -25,6 +25,13 @@ static int64_t head_workspace(int64_t N, int32_t D) {
   return (ctas < most ? ctas : most) * 2 * D * 4;
 }
 
+// A warp has as many nodes at a time as keep its lanes busy with their angles,
+// but one where there are few.
+static int nodes_at_once(int64_t N, int32_t D, int32_t axes) {
+  const int64_t most = axes && D / 2 < kHeadAngles ? kHeadAngles / (D / 2) : 1, share = N / (152 * 64);
+  return (int)(share < 1 ? 1 : share < most ? share : most);
+}
+
 template <typename T, int V, int G, int NV>
 static eqmp_status launch(const HeadNormArgs& a, bool backward, cudaStream_t st) {
   constexpr int U = NV * V <= 4 ? 4 : 2;
@@ -101,7 +108,7 @@ eqmp_status eqmp_head_norm(const void* q, int64_t q_ld, int32_t Hq, const void* 
   HeadNormArgs a{};
   a.q = q, a.q_ld = q_ld, a.k = k, a.k_ld = k_ld, a.wq = wq, a.wk = wk, a.eps = eps;
   a.pos = pos, a.freq = freq, a.axes = axes, a.oq = out_q, a.ok = out_k, a.rstd = rstd;
-  a.N = (int)N, a.Hq = Hq, a.Hk = Hk, a.D = D;
+  a.N = (int)N, a.Hq = Hq, a.Hk = Hk, a.D = D, a.each = nodes_at_once(N, D, axes);
   const bool vectors = on16(q, q_ld, bytes) && (!Hk || on16(k, k_ld, bytes)) && aligned(out_q, 16) && aligned(out_k, 16) &&
                        D * bytes % 16 == 0;
   return run(a, dtype, vectors, false, reinterpret_cast<cudaStream_t>(stream));
@@ -148,7 +155,7 @@ eqmp_status eqmp_head_norm_backward(const void* grad_yq, int64_t grad_yq_ld, con
   a.wq = wq, a.wk = wk, a.rstd = const_cast<float*>(rstd), a.pos = pos, a.freq = freq, a.axes = axes;
   a.oq = grad_q, a.ok = grad_k, a.gwq = grad_wq, a.gwk = grad_wk, a.gpos = grad_pos;
   a.part = ws > 0 ? static_cast<float*>(workspace) : nullptr;
-  a.N = (int)N, a.Hq = Hq, a.Hk = Hk, a.D = D;
+  a.N = (int)N, a.Hq = Hq, a.Hk = Hk, a.D = D, a.each = nodes_at_once(N, D, axes);
   const bool vectors = on16(q, q_ld, bytes) && on16(grad_yq, grad_yq_ld, bytes) && aligned(grad_q, 16) && aligned(grad_k, 16) &&
                        (!Hk || (on16(k, k_ld, bytes) && on16(grad_yk, grad_yk_ld, bytes))) && D * bytes % 16 == 0;
   return run(a, dtype, vectors, true, st);

@@ -32,10 +32,11 @@ struct HeadNormArgs {
   float* part;                // [parts][2][D]
   float eps;
   int N, Hq, Hk, D, axes;
+  int each;  // nodes of a warp at a time
 };
 
 constexpr int kHeadWarps = 8;       // of a CTA
-constexpr int kHeadAngles = 64;     // pairs of a warp's nodes at a time; a node has at most 128
+constexpr int kHeadAngles = 64;     // pairs of a warp's nodes at a time, or those of one node (at most 128)
 
 // An angle in turns, reduced to half a turn: the frequency in turns is held as
 // the sum of two floats, and the product's rounding error is kept, so that a
@@ -126,8 +127,7 @@ __device__ __forceinline__ void load_weights(const float* w, int l, int D, float
 
 // The angles of a warp's nodes.  freq: the pairs' frequencies in turns, [pair][axis]
 // (shared by the CTA); turn: the cosines and sines of the warp's nodes,
-// [node][pair].  A warp has as many nodes at a time as keep its lanes busy.
-__device__ __forceinline__ int nodes_at_once(int pairs) { return pairs >= kHeadAngles ? 1 : kHeadAngles / pairs; }
+// [node][pair].
 
 __device__ __forceinline__ void load_freq(const HeadNormArgs& a, Turns* freq) {
   for (int i = threadIdx.x; i < a.D / 2 * a.axes; i += blockDim.x) freq[i].set(a.freq[i]);
@@ -159,76 +159,120 @@ __device__ __forceinline__ void load_turns(const float2* turn, int pairs, int l,
   }
 }
 
+// A warp's way through its nodes and their heads, U * 32 / G heads at a time.
+struct HeadWalk {
+  long long node, node0, step;  // the node, the first of its batch of `each`, from batch to batch
+  int each, t0, heads, stride;
+  __device__ __forceinline__ HeadWalk(const HeadNormArgs& a, int each, int stride)
+      : node0(((long long)blockIdx.x * kHeadWarps + (threadIdx.x >> 5)) * each), step((long long)gridDim.x * kHeadWarps * each), each(each),
+        t0(0), heads(a.Hq + a.Hk), stride(stride) {
+    node = node0;
+  }
+  __device__ __forceinline__ void next(int N) {
+    t0 += stride;
+    if (t0 < heads) return;
+    t0 = 0;
+    ++node;
+    if (node - node0 < each && node < N) return;
+    node0 += step;
+    node = node0;
+  }
+};
+
+// A step's rows are loaded before its angles are formed, and the first ones before
+// anything else.  (Loading a step ahead costs the registers of two steps: 100,000
+// nodes, 8 + 8 heads of 32, bf16 68 us for 59, backward fp32 160 for 138.)
 template <typename T, int V, int G, int NV, int U>
-__global__ void __launch_bounds__(32 * kHeadWarps) k_head_norm(HeadNormArgs a) {
+__global__ void __launch_bounds__(32 * kHeadWarps) k_head_norm(const __grid_constant__ HeadNormArgs a) {
   constexpr int W = NV * V, P = W / 2, AT_ONCE = 32 / G;
   __shared__ Turns freq[128 * 3];
   __shared__ float2 turns[kHeadWarps][128];
   const int lane = threadIdx.x & 31, l = lane % G, heads = a.Hq + a.Hk, pairs = a.D / 2;
-  const int each = a.axes ? nodes_at_once(pairs) : 1;
+  const int each = a.each;
   float2* const turn = turns[threadIdx.x >> 5];
+  HeadWalk at(a, each, U * AT_ONCE);
+  HeadShare<T, V, G, NV> x[U];
+  auto load = [&] {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = at.t0 + lane / G + u * AT_ONCE;
+      const bool ok = at.node < a.N && t < heads;
+      const long long node = ok ? at.node : 0;
+      x[u].load(t < a.Hq ? static_cast<const T*>(a.q) + node * a.q_ld + (long long)t * a.D
+                         : static_cast<const T*>(a.k) + node * a.k_ld + (long long)(t - a.Hq) * a.D, l, a.D, ok);
+    }
+  };
+  load();
+  bool first = true;
   float wq[W], wk[W];
   load_weights<V, G, NV>(a.wq, l, a.D, wq);
   load_weights<V, G, NV>(a.wk, l, a.D, wk);
   if (a.axes) load_freq(a, freq);
   __syncthreads();
-  const long long step = (long long)gridDim.x * kHeadWarps * each;
-  for (long long node0 = ((long long)blockIdx.x * kHeadWarps + (threadIdx.x >> 5)) * each; node0 < a.N; node0 += step) {
-    const int nodes = a.N - node0 < each ? (int)(a.N - node0) : each;
-    if (a.axes) form_turns(a, freq, turn, (int)node0, nodes);
-    for (int n = 0; n < nodes; ++n) {
-      const int node = (int)node0 + n;
-      const T* q = static_cast<const T*>(a.q) + node * a.q_ld;
-      const T* k = static_cast<const T*>(a.k) + node * a.k_ld;
-      float2 cs[P];
-      if (a.axes) load_turns<V, G, NV>(turn + n * pairs, pairs, l, cs);
-      for (int t0 = lane / G; t0 - lane / G < heads; t0 += U * AT_ONCE) {
-        HeadShare<T, V, G, NV> x[U];
+  float2 cs[P];
+  for (; at.node < a.N; at.next(a.N)) {
+    if (!first) load();
+    first = false;
+    if (a.axes && at.t0 == 0) {
+      if (at.node == at.node0) form_turns(a, freq, turn, (int)at.node0, (int)(a.N - at.node0 < each ? a.N - at.node0 : each));
+      load_turns<V, G, NV>(turn + (int)(at.node - at.node0) * pairs, pairs, l, cs);
+    }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int t = t0 + u * AT_ONCE;
-          x[u].load(t < a.Hq ? q + (long long)t * a.D : k + (long long)(t - a.Hq) * a.D, l, a.D, t < heads);
+    for (int u = 0; u < U; ++u) {
+      const int t = at.t0 + lane / G + u * AT_ONCE;
+      float f[W], ss = 0.0f;
+      x[u].get(f);
+#pragma unroll
+      for (int i = 0; i < W; ++i) ss = fmaf(f[i], f[i], ss);
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (t >= heads) continue;
+      const bool query = t < a.Hq;
+      const float r = 1.0f / sqrtf(ss / (float)a.D + a.eps);
+      if (a.rstd && l == 0) a.rstd[at.node * heads + t] = r;
+#pragma unroll
+      for (int i = 0; i < W; ++i) f[i] *= r * (query ? wq[i] : wk[i]);
+      if (a.axes)
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const float u0 = f[2 * p], u1 = f[2 * p + 1];
+          f[2 * p] = u0 * cs[p].x - u1 * cs[p].y;
+          f[2 * p + 1] = u0 * cs[p].y + u1 * cs[p].x;
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int t = t0 + u * AT_ONCE;
-          float f[W], ss = 0.0f;
-          x[u].get(f);
-#pragma unroll
-          for (int i = 0; i < W; ++i) ss = fmaf(f[i], f[i], ss);
-#pragma unroll
-          for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          if (t >= heads) continue;
-          const bool query = t < a.Hq;
-          const float r = 1.0f / sqrtf(ss / (float)a.D + a.eps);
-          if (a.rstd && l == 0) a.rstd[(long long)node * heads + t] = r;
-#pragma unroll
-          for (int i = 0; i < W; ++i) f[i] *= r * (query ? wq[i] : wk[i]);
-          if (a.axes)
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-              const float u0 = f[2 * p], u1 = f[2 * p + 1];
-              f[2 * p] = u0 * cs[p].x - u1 * cs[p].y;
-              f[2 * p + 1] = u0 * cs[p].y + u1 * cs[p].x;
-            }
-          T* out = static_cast<T*>(query ? a.oq : a.ok);
-          const long long row = query ? (long long)node * a.Hq + t : (long long)node * a.Hk + (t - a.Hq);
-          if (out) HeadShare<T, V, G, NV>::store(out + row * a.D, l, a.D, f);
-        }
-      }
+      T* out = static_cast<T*>(query ? a.oq : a.ok);
+      const long long row = query ? at.node * a.Hq + t : at.node * a.Hk + (t - a.Hq);
+      if (out) HeadShare<T, V, G, NV>::store(out + row * a.D, l, a.D, f);
     }
   }
 }
 
 template <typename T, int V, int G, int NV, int U>
-__global__ void __launch_bounds__(32 * kHeadWarps) k_head_norm_bwd(HeadNormArgs a) {
+__global__ void __launch_bounds__(32 * kHeadWarps) k_head_norm_bwd(const __grid_constant__ HeadNormArgs a) {
   constexpr int W = NV * V, P = W / 2, AT_ONCE = 32 / G;
   __shared__ Turns freq[128 * 3];
   __shared__ float2 turns[kHeadWarps][128];
   __shared__ float red[kHeadWarps][2 * G * W];
   const int lane = threadIdx.x & 31, l = lane % G, warp = threadIdx.x >> 5, heads = a.Hq + a.Hk, pairs = a.D / 2;
-  const int each = a.axes ? nodes_at_once(pairs) : 1;
+  const int each = a.each;
   float2* const turn = turns[warp];
+  HeadWalk at(a, each, U * AT_ONCE);
+  HeadShare<T, V, G, NV> x[U], g[U];
+  float r[U];
+  auto load = [&] {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = at.t0 + lane / G + u * AT_ONCE, hk = t - a.Hq;
+      const bool query = t < a.Hq, ok = at.node < a.N && t < heads;
+      const long long node = ok ? at.node : 0;
+      x[u].load(static_cast<const T*>(query ? a.q : a.k) + (query ? node * a.q_ld + (long long)t * a.D : node * a.k_ld + (long long)hk * a.D),
+                l, a.D, ok);
+      g[u].load(static_cast<const T*>(query ? a.gq : a.gk) + (query ? node * a.gq_ld + (long long)t * a.D : node * a.gk_ld + (long long)hk * a.D),
+                l, a.D, ok);
+      r[u] = ok ? __ldg(a.rstd + node * heads + t) : 0.0f;
+    }
+  };
+  load();
+  bool first = true;
   float wq[W], wk[W], dwq[W], dwk[W];
   load_weights<V, G, NV>(a.wq, l, a.D, wq);
   load_weights<V, G, NV>(a.wk, l, a.D, wk);
@@ -236,83 +280,69 @@ __global__ void __launch_bounds__(32 * kHeadWarps) k_head_norm_bwd(HeadNormArgs 
   for (int i = 0; i < W; ++i) dwq[i] = dwk[i] = 0.0f;
   if (a.axes) load_freq(a, freq);
   __syncthreads();
-  const long long step = (long long)gridDim.x * kHeadWarps * each;
-  for (long long node0 = ((long long)blockIdx.x * kHeadWarps + warp) * each; node0 < a.N; node0 += step) {
-    const int nodes = a.N - node0 < each ? (int)(a.N - node0) : each;
-    if (a.axes) form_turns(a, freq, turn, (int)node0, nodes);
-    for (int n = 0; n < nodes; ++n) {
-      const int node = (int)node0 + n;
-      float2 cs[P];
-      float turned[P];
-      if (a.axes) load_turns<V, G, NV>(turn + n * pairs, pairs, l, cs);
+  float2 cs[P];
+  float turned[P];
+  for (; at.node < a.N; at.next(a.N)) {
+    if (!first) load();
+    first = false;
+    if (a.axes && at.t0 == 0) {
+      if (at.node == at.node0) form_turns(a, freq, turn, (int)at.node0, (int)(a.N - at.node0 < each ? a.N - at.node0 : each));
+      load_turns<V, G, NV>(turn + (int)(at.node - at.node0) * pairs, pairs, l, cs);
 #pragma unroll
       for (int p = 0; p < P; ++p) turned[p] = 0.0f;
-      for (int t0 = lane / G; t0 - lane / G < heads; t0 += U * AT_ONCE) {
-        HeadShare<T, V, G, NV> x[U], g[U];
-        float r[U];
+    }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int t = t0 + u * AT_ONCE, hk = t - a.Hq;
-          const T* xp = static_cast<const T*>(t < a.Hq ? a.q : a.k);
-          const T* gp = static_cast<const T*>(t < a.Hq ? a.gq : a.gk);
-          x[u].load(xp + (t < a.Hq ? node * a.q_ld + (long long)t * a.D : node * a.k_ld + (long long)hk * a.D), l, a.D, t < heads);
-          g[u].load(gp + (t < a.Hq ? node * a.gq_ld + (long long)t * a.D : node * a.gk_ld + (long long)hk * a.D), l, a.D, t < heads);
-          r[u] = t < heads ? __ldg(a.rstd + (long long)node * heads + t) : 0.0f;
-        }
+    for (int u = 0; u < U; ++u) {
+      const int t = at.t0 + lane / G + u * AT_ONCE;
+      const bool query = t < a.Hq, ok = t < heads;
+      float h[W], b[W], mean = 0.0f;
+      x[u].get(h);
+      g[u].get(b);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int t = t0 + u * AT_ONCE;
-          const bool query = t < a.Hq, ok = t < heads;
-          float h[W], b[W], mean = 0.0f;
-          x[u].get(h);
-          g[u].get(b);
-#pragma unroll
-          for (int i = 0; i < W; ++i) h[i] *= r[u];
-          if (a.axes)
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-              const float g0 = b[2 * p], g1 = b[2 * p + 1];
-              b[2 * p] = g0 * cs[p].x + g1 * cs[p].y;
-              b[2 * p + 1] = g1 * cs[p].x - g0 * cs[p].y;
-              const float u0 = h[2 * p] * (query ? wq[2 * p] : wk[2 * p]);
-              const float u1 = h[2 * p + 1] * (query ? wq[2 * p + 1] : wk[2 * p + 1]);
-              if (ok) turned[p] += b[2 * p + 1] * u0 - b[2 * p] * u1;
-            }
-#pragma unroll
-          for (int i = 0; i < W; ++i) {
-            const float d = b[i] * h[i];
-            if (ok && query) dwq[i] += d;
-            if (ok && !query) dwk[i] += d;
-            b[i] *= query ? wq[i] : wk[i];
-            mean = fmaf(b[i], h[i], mean);
-          }
-#pragma unroll
-          for (int o = G / 2; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
-          if (!ok) continue;
-          mean /= (float)a.D;
-#pragma unroll
-          for (int i = 0; i < W; ++i) b[i] = r[u] * fmaf(-h[i], mean, b[i]);
-          T* out = static_cast<T*>(query ? a.oq : a.ok);
-          const long long row = query ? (long long)node * a.Hq + t : (long long)node * a.Hk + (t - a.Hq);
-          if (out) HeadShare<T, V, G, NV>::store(out + row * a.D, l, a.D, b);
-        }
-      }
-      if (a.gpos) {
-        float d[3] = {0.0f, 0.0f, 0.0f};
+      for (int i = 0; i < W; ++i) h[i] *= r[u];
+      if (a.axes)
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          const int pair = ((2 * p / V * G + l) * V + 2 * p % V) / 2;
-#pragma unroll
-          for (int x = 0; x < 3; ++x)
-            if (pair < pairs && x < a.axes) d[x] = fmaf(turned[p], freq[pair * a.axes + x].hi, d[x]);
+          const float g0 = b[2 * p], g1 = b[2 * p + 1];
+          b[2 * p] = g0 * cs[p].x + g1 * cs[p].y;
+          b[2 * p + 1] = g1 * cs[p].x - g0 * cs[p].y;
+          const float u0 = h[2 * p] * (query ? wq[2 * p] : wk[2 * p]);
+          const float u1 = h[2 * p + 1] * (query ? wq[2 * p + 1] : wk[2 * p + 1]);
+          if (ok) turned[p] += b[2 * p + 1] * u0 - b[2 * p] * u1;
         }
 #pragma unroll
-        for (int x = 0; x < 3; ++x) {
-          if (x >= a.axes) break;
+      for (int i = 0; i < W; ++i) {
+        const float d = b[i] * h[i];
+        if (ok && query) dwq[i] += d;
+        if (ok && !query) dwk[i] += d;
+        b[i] *= query ? wq[i] : wk[i];
+        mean = fmaf(b[i], h[i], mean);
+      }
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) d[x] += __shfl_xor_sync(0xffffffffu, d[x], o);
-          if (lane == 0) a.gpos[(long long)node * a.axes + x] = d[x] * 6.2831853071795865f;
-        }
+      for (int o = G / 2; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
+      if (!ok) continue;
+      mean /= (float)a.D;
+#pragma unroll
+      for (int i = 0; i < W; ++i) b[i] = r[u] * fmaf(-h[i], mean, b[i]);
+      T* out = static_cast<T*>(query ? a.oq : a.ok);
+      const long long row = query ? at.node * a.Hq + t : at.node * a.Hk + (t - a.Hq);
+      if (out) HeadShare<T, V, G, NV>::store(out + row * a.D, l, a.D, b);
+    }
+    if (a.gpos && at.t0 + at.stride >= heads) {
+      float d[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int pair = ((2 * p / V * G + l) * V + 2 * p % V) / 2;
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+          if (pair < pairs && x < a.axes) d[x] = fmaf(turned[p], freq[pair * a.axes + x].hi, d[x]);
+      }
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        if (x >= a.axes) break;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) d[x] += __shfl_xor_sync(0xffffffffu, d[x], o);
+        if (lane == 0) a.gpos[at.node * a.axes + x] = d[x] * 6.2831853071795865f;
       }
     }
   }
