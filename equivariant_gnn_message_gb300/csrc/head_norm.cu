@@ -10,7 +10,7 @@
 namespace eqmp {
 
 constexpr int kMaxHeadDim = 256, kMaxHeads = 65536;
-constexpr int kHeadCtas = 2;  // on each SM, in the backward pass: each leaves a part of dw
+constexpr int kHeadCtas = 3;  // on each SM, in the backward pass: each leaves a part of dw
 
 static eqmp_status check(int64_t N, int32_t Hq, int32_t Hk, int32_t D, eqmp_dtype dtype, const float* pos, const float* freq,
                          int32_t axes) {
@@ -25,17 +25,17 @@ static int64_t head_workspace(int64_t N, int32_t D) {
   return (ctas < most ? ctas : most) * 2 * D * 4;
 }
 
-// A warp has as many nodes at a time as keep its lanes busy with their angles,
-// but one where there are few.
-static int nodes_at_once(int64_t N, int32_t D, int32_t axes) {
-  const int64_t most = axes && D / 2 < kHeadAngles ? kHeadAngles / (D / 2) : 1, share = N / (152 * 64);
-  return (int)(share < 1 ? 1 : share < most ? share : most);
-}
-
 template <typename T, int V, int G, int NV>
-static eqmp_status launch(const HeadNormArgs& a, bool backward, cudaStream_t st) {
-  constexpr int U = NV * V <= 4 ? 4 : 2;
-  const long long ctas = ((long long)a.N + kHeadWarps - 1) / kHeadWarps;
+static eqmp_status launch(HeadNormArgs a, bool backward, cudaStream_t st) {
+  // Rows of a step: four of up to 64 values, else two (their angles lie in shared memory); backward one where a lane
+  // has 8 values of x and of g, so that three CTAs fit an SM.  100,000 x 16 heads of 32, backward: fp32 four rows 117
+  // us, two 121; 50,000 x 8 of 128 two 119, four 124; bf16 one row 113 us, two 129 (two CTAs).
+  constexpr int U = G * NV * V <= 64 ? 4 : 2, U_BWD = NV * V >= 8 ? 1 : U;
+  const int most = backward ? U_BWD : U, share = a.N / (152 * 64);
+  a.each = share < 1 ? 1 : share < most ? share : most;
+  a.shift = 0;
+  while (a.shift < 5 && 1 << a.shift < a.D / 2) ++a.shift;
+  const long long ctas = ((long long)a.N + kHeadWarps * a.each - 1) / (kHeadWarps * a.each);
   if (!backward) {
     DeviceInfo dev;
     const eqmp_status s = device_info(&dev);
@@ -45,7 +45,7 @@ static eqmp_status launch(const HeadNormArgs& a, bool backward, cudaStream_t st)
     return cuda_status(cudaGetLastError());
   }
   const int parts = (int)(ctas < 152 * kHeadCtas ? ctas : 152 * kHeadCtas);
-  k_head_norm_bwd<T, V, G, NV, U><<<parts, 32 * kHeadWarps, 0, st>>>(a);
+  k_head_norm_bwd<T, V, G, NV, U_BWD><<<parts, 32 * kHeadWarps, 0, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return EQMP_ERR_CUDA;
   if (!a.part) return EQMP_OK;
   cudaLaunchAttribute attr;
@@ -108,7 +108,7 @@ eqmp_status eqmp_head_norm(const void* q, int64_t q_ld, int32_t Hq, const void* 
   HeadNormArgs a{};
   a.q = q, a.q_ld = q_ld, a.k = k, a.k_ld = k_ld, a.wq = wq, a.wk = wk, a.eps = eps;
   a.pos = pos, a.freq = freq, a.axes = axes, a.oq = out_q, a.ok = out_k, a.rstd = rstd;
-  a.N = (int)N, a.Hq = Hq, a.Hk = Hk, a.D = D, a.each = nodes_at_once(N, D, axes);
+  a.N = (int)N, a.Hq = Hq, a.Hk = Hk, a.D = D;
   const bool vectors = on16(q, q_ld, bytes) && (!Hk || on16(k, k_ld, bytes)) && aligned(out_q, 16) && aligned(out_k, 16) &&
                        D * bytes % 16 == 0;
   return run(a, dtype, vectors, false, reinterpret_cast<cudaStream_t>(stream));
@@ -155,7 +155,7 @@ eqmp_status eqmp_head_norm_backward(const void* grad_yq, int64_t grad_yq_ld, con
   a.wq = wq, a.wk = wk, a.rstd = const_cast<float*>(rstd), a.pos = pos, a.freq = freq, a.axes = axes;
   a.oq = grad_q, a.ok = grad_k, a.gwq = grad_wq, a.gwk = grad_wk, a.gpos = grad_pos;
   a.part = ws > 0 ? static_cast<float*>(workspace) : nullptr;
-  a.N = (int)N, a.Hq = Hq, a.Hk = Hk, a.D = D, a.each = nodes_at_once(N, D, axes);
+  a.N = (int)N, a.Hq = Hq, a.Hk = Hk, a.D = D;
   const bool vectors = on16(q, q_ld, bytes) && on16(grad_yq, grad_yq_ld, bytes) && aligned(grad_q, 16) && aligned(grad_k, 16) &&
                        (!Hk || (on16(k, k_ld, bytes) && on16(grad_yk, grad_yk_ld, bytes))) && D * bytes % 16 == 0;
   return run(a, dtype, vectors, true, st);

@@ -32,11 +32,11 @@ struct HeadNormArgs {
   float* part;                // [parts][2][D]
   float eps;
   int N, Hq, Hk, D, axes;
-  int each;  // nodes of a warp at a time
+  int each;   // nodes of a warp at a time
+  int shift;  // see form_turns
 };
 
 constexpr int kHeadWarps = 8;       // of a CTA
-constexpr int kHeadAngles = 64;     // pairs of a warp's nodes at a time, or those of one node (at most 128)
 
 // An angle in turns, reduced to half a turn: the frequency in turns is held as
 // the sum of two floats, and the product's rounding error is kept, so that a
@@ -133,18 +133,25 @@ __device__ __forceinline__ void load_freq(const HeadNormArgs& a, Turns* freq) {
   for (int i = threadIdx.x; i < a.D / 2 * a.axes; i += blockDim.x) freq[i].set(a.freq[i]);
 }
 
+// 2^shift lanes a node: the least power of two that holds its pairs, at most 32.
 __device__ __forceinline__ void form_turns(const HeadNormArgs& a, const Turns* freq, float2* turn, int node0, int nodes) {
-  const int pairs = a.D / 2;
+  const int pairs = a.D / 2, lane = threadIdx.x & 31, side = 1 << a.shift;
   __syncwarp();  // the last nodes' have been read
-  for (int i = threadIdx.x & 31; i < nodes * pairs; i += 32) {
-    const int n = i / pairs, p = i - n * pairs;
+  for (int n = lane >> a.shift; n < nodes; n += 32 >> a.shift) {
     const float* pos = a.pos + (long long)(node0 + n) * a.axes;
-    float t = freq[p * a.axes].of(__ldg(pos));
-    for (int x = 1; x < a.axes; ++x) t += freq[p * a.axes + x].of(__ldg(pos + x));
-    t -= rintf(t);
-    float s, c;
-    sincospif(2.0f * t, &s, &c);
-    turn[i] = make_float2(c, s);
+    float x[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) x[i] = i < a.axes ? __ldg(pos + i) : 0.0f;
+    for (int p = lane & (side - 1); p < pairs; p += side) {
+      const Turns* f = freq + p * a.axes;
+      float t = f[0].of(x[0]);
+      if (a.axes > 1) t += f[1].of(x[1]);
+      if (a.axes > 2) t += f[2].of(x[2]);
+      t -= rintf(t);
+      float s, c;
+      sincospif(2.0f * t, &s, &c);
+      turn[n * pairs + p] = make_float2(c, s);
+    }
   }
   __syncwarp();
 }
@@ -153,196 +160,209 @@ __device__ __forceinline__ void form_turns(const HeadNormArgs& a, const Turns* f
 template <int V, int G, int NV>
 __device__ __forceinline__ void load_turns(const float2* turn, int pairs, int l, float2 (&t)[NV * V / 2]) {
 #pragma unroll
-  for (int p = 0; p < NV * V / 2; ++p) {
-    const int pair = ((2 * p / V * G + l) * V + 2 * p % V) / 2;
-    t[p] = pair < pairs ? turn[pair] : make_float2(1.0f, 0.0f);
+  for (int j = 0; j < NV; ++j) {
+    const int first = (j * G + l) * (V / 2);
+#pragma unroll
+    for (int p = 0; p < V / 2; ++p) t[j * V / 2 + p] = make_float2(1.0f, 0.0f);
+    if (first < pairs)  // all of a vector's pairs are there, or none
+#pragma unroll
+      for (int p = 0; p < V / 2; ++p) t[j * V / 2 + p] = turn[first + p];
   }
 }
 
-// A warp's way through its nodes and their heads, U * 32 / G heads at a time.
-struct HeadWalk {
-  long long node, node0, step;  // the node, the first of its batch of `each`, from batch to batch
-  int each, t0, heads, stride;
-  __device__ __forceinline__ HeadWalk(const HeadNormArgs& a, int each, int stride)
-      : node0(((long long)blockIdx.x * kHeadWarps + (threadIdx.x >> 5)) * each), step((long long)gridDim.x * kHeadWarps * each), each(each),
-        t0(0), heads(a.Hq + a.Hk), stride(stride) {
-    node = node0;
-  }
-  __device__ __forceinline__ void next(int N) {
-    t0 += stride;
-    if (t0 < heads) return;
-    t0 = 0;
-    ++node;
-    if (node - node0 < each && node < N) return;
-    node0 += step;
-    node = node0;
+// The U rows of a step: the same 32 / G heads of neighbouring nodes, so that what
+// hangs on the heads alone (addresses, weights) is found once for all of them; or,
+// where there are few nodes, the next heads of one node.  Either way they are on
+// their way together.
+template <typename T>
+struct HeadStep {
+  int t, heads, first, nodes;  // the lane's first head, of how many; their place in rstd; nodes there
+  bool key, by_head;
+  __device__ __forceinline__ HeadStep(const HeadNormArgs& a, bool key, int t, int nodes)
+      : t(t), heads(key ? a.Hk : a.Hq), first(key ? a.Hq : 0), nodes(nodes), key(key), by_head(a.each == 1) {}
+  template <int AT_ONCE>
+  __device__ __forceinline__ bool has(int u) const {
+    return by_head ? nodes > 0 && t + u * AT_ONCE < heads : u < nodes && t < heads;
   }
 };
 
-// A step's rows are loaded before its angles are formed, and the first ones before
-// anything else.  (Loading a step ahead costs the registers of two steps: 100,000
-// nodes, 8 + 8 heads of 32, bf16 68 us for 59, backward fp32 160 for 138.)
+// Where a step's rows lie in an array: the first, and the distance between them.
+template <typename T>
+struct HeadRows {
+  const T* x;
+  long long step;
+  template <int AT_ONCE>
+  static __device__ __forceinline__ HeadRows at(const HeadNormArgs& a, const HeadStep<T>& s, const void* q, long long q_ld, const void* k,
+                                                long long k_ld, int node0) {
+    const long long ld = s.key ? k_ld : q_ld;
+    return HeadRows{static_cast<const T*>(s.key ? k : q) + node0 * ld + s.t * a.D, s.by_head ? (long long)AT_ONCE * a.D : ld};
+  }
+};
+
 template <typename T, int V, int G, int NV, int U>
-__global__ void __launch_bounds__(32 * kHeadWarps) k_head_norm(const __grid_constant__ HeadNormArgs a) {
+__global__ void __launch_bounds__(32 * kHeadWarps, 4) k_head_norm(const __grid_constant__ HeadNormArgs a) {
   constexpr int W = NV * V, P = W / 2, AT_ONCE = 32 / G;
+  using Share = HeadShare<T, V, G, NV>;
   __shared__ Turns freq[128 * 3];
-  __shared__ float2 turns[kHeadWarps][128];
-  const int lane = threadIdx.x & 31, l = lane % G, heads = a.Hq + a.Hk, pairs = a.D / 2;
-  const int each = a.each;
+  __shared__ __align__(16) float2 turns[kHeadWarps][U * G * W / 2];
+  const int lane = threadIdx.x & 31, l = lane % G, all = a.Hq + a.Hk, pairs = a.D / 2;
   float2* const turn = turns[threadIdx.x >> 5];
-  HeadWalk at(a, each, U * AT_ONCE);
-  HeadShare<T, V, G, NV> x[U];
-  auto load = [&] {
+  const float per_d = 1.0f / (float)a.D;
+  bool ready = false;
+  for (int node0 = (int)(blockIdx.x * kHeadWarps + (threadIdx.x >> 5)) * a.each;; node0 += gridDim.x * kHeadWarps * a.each) {
+    const int nodes = min(a.N - node0, a.each);
+    if (nodes <= 0 && ready) break;
+    bool fresh = true;
+    for (int key = 0; key < (a.Hk ? 2 : 1); ++key) {
+      float w[W];
+      load_weights<V, G, NV>(key ? a.wk : a.wq, l, a.D, w);
+      T* const out = static_cast<T*>(key ? a.ok : a.oq);
+      for (int t0 = 0; t0 < (key ? a.Hk : a.Hq); t0 += a.each == 1 ? U * AT_ONCE : AT_ONCE) {
+        const HeadStep<T> s(a, key, t0 + lane / G, nodes);
+        const HeadRows<T> from = HeadRows<T>::template at<AT_ONCE>(a, s, a.q, a.q_ld, a.k, a.k_ld, node0);
+        const int row0 = s.by_head ? AT_ONCE : s.heads, rstd0 = s.by_head ? AT_ONCE : all;  // from one row to the next
+        Share x[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int t = at.t0 + lane / G + u * AT_ONCE;
-      const bool ok = at.node < a.N && t < heads;
-      const long long node = ok ? at.node : 0;
-      x[u].load(t < a.Hq ? static_cast<const T*>(a.q) + node * a.q_ld + (long long)t * a.D
-                         : static_cast<const T*>(a.k) + node * a.k_ld + (long long)(t - a.Hq) * a.D, l, a.D, ok);
-    }
-  };
-  load();
-  bool first = true;
-  float wq[W], wk[W];
-  load_weights<V, G, NV>(a.wq, l, a.D, wq);
-  load_weights<V, G, NV>(a.wk, l, a.D, wk);
-  if (a.axes) load_freq(a, freq);
-  __syncthreads();
-  float2 cs[P];
-  for (; at.node < a.N; at.next(a.N)) {
-    if (!first) load();
-    first = false;
-    if (a.axes && at.t0 == 0) {
-      if (at.node == at.node0) form_turns(a, freq, turn, (int)at.node0, (int)(a.N - at.node0 < each ? a.N - at.node0 : each));
-      load_turns<V, G, NV>(turn + (int)(at.node - at.node0) * pairs, pairs, l, cs);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int t = at.t0 + lane / G + u * AT_ONCE;
-      float f[W], ss = 0.0f;
-      x[u].get(f);
-#pragma unroll
-      for (int i = 0; i < W; ++i) ss = fmaf(f[i], f[i], ss);
-#pragma unroll
-      for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (t >= heads) continue;
-      const bool query = t < a.Hq;
-      const float r = 1.0f / sqrtf(ss / (float)a.D + a.eps);
-      if (a.rstd && l == 0) a.rstd[at.node * heads + t] = r;
-#pragma unroll
-      for (int i = 0; i < W; ++i) f[i] *= r * (query ? wq[i] : wk[i]);
-      if (a.axes)
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const float u0 = f[2 * p], u1 = f[2 * p + 1];
-          f[2 * p] = u0 * cs[p].x - u1 * cs[p].y;
-          f[2 * p + 1] = u0 * cs[p].y + u1 * cs[p].x;
+        for (int u = 0; u < U; ++u) x[u].load(from.x + u * from.step, l, a.D, s.template has<AT_ONCE>(u));
+        if (fresh) {
+          if (!ready) {  // once, behind the first rows' loads
+            if (a.axes) load_freq(a, freq);
+            __syncthreads();
+            ready = true;
+          }
+          if (a.axes) form_turns(a, freq, turn, node0, nodes);
+          fresh = false;
         }
-      T* out = static_cast<T*>(query ? a.oq : a.ok);
-      const long long row = query ? at.node * a.Hq + t : at.node * a.Hk + (t - a.Hq);
-      if (out) HeadShare<T, V, G, NV>::store(out + row * a.D, l, a.D, f);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float f[W], ss = 0.0f;
+          x[u].get(f);
+#pragma unroll
+          for (int i = 0; i < W; ++i) ss = fmaf(f[i], f[i], ss);
+#pragma unroll
+          for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          if (!s.template has<AT_ONCE>(u)) continue;
+          const float r = rsqrtf(fmaf(ss, per_d, a.eps));
+          if (a.rstd && l == 0) a.rstd[(long long)node0 * all + s.first + s.t + u * rstd0] = r;
+#pragma unroll
+          for (int i = 0; i < W; ++i) f[i] *= r * w[i];
+          if (a.axes) {
+            float2 cs[P];
+            load_turns<V, G, NV>(turn + (s.by_head ? 0 : u * pairs), pairs, l, cs);
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+              const float u0 = f[2 * p], u1 = f[2 * p + 1];
+              f[2 * p] = u0 * cs[p].x - u1 * cs[p].y;
+              f[2 * p + 1] = u0 * cs[p].y + u1 * cs[p].x;
+            }
+          }
+          if (out) Share::store(out + ((long long)node0 * s.heads + s.t + u * row0) * a.D, l, a.D, f);
+        }
+      }
     }
   }
 }
 
 template <typename T, int V, int G, int NV, int U>
-__global__ void __launch_bounds__(32 * kHeadWarps) k_head_norm_bwd(const __grid_constant__ HeadNormArgs a) {
+__global__ void __launch_bounds__(32 * kHeadWarps, 3) k_head_norm_bwd(const __grid_constant__ HeadNormArgs a) {
   constexpr int W = NV * V, P = W / 2, AT_ONCE = 32 / G;
+  using Share = HeadShare<T, V, G, NV>;
   __shared__ Turns freq[128 * 3];
-  __shared__ float2 turns[kHeadWarps][128];
+  __shared__ __align__(16) float2 turns[kHeadWarps][U * G * W / 2];
   __shared__ float red[kHeadWarps][2 * G * W];
-  const int lane = threadIdx.x & 31, l = lane % G, warp = threadIdx.x >> 5, heads = a.Hq + a.Hk, pairs = a.D / 2;
-  const int each = a.each;
+  const int lane = threadIdx.x & 31, l = lane % G, warp = threadIdx.x >> 5, all = a.Hq + a.Hk, pairs = a.D / 2;
   float2* const turn = turns[warp];
-  HeadWalk at(a, each, U * AT_ONCE);
-  HeadShare<T, V, G, NV> x[U], g[U];
-  float r[U];
-  auto load = [&] {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int t = at.t0 + lane / G + u * AT_ONCE, hk = t - a.Hq;
-      const bool query = t < a.Hq, ok = at.node < a.N && t < heads;
-      const long long node = ok ? at.node : 0;
-      x[u].load(static_cast<const T*>(query ? a.q : a.k) + (query ? node * a.q_ld + (long long)t * a.D : node * a.k_ld + (long long)hk * a.D),
-                l, a.D, ok);
-      g[u].load(static_cast<const T*>(query ? a.gq : a.gk) + (query ? node * a.gq_ld + (long long)t * a.D : node * a.gk_ld + (long long)hk * a.D),
-                l, a.D, ok);
-      r[u] = ok ? __ldg(a.rstd + node * heads + t) : 0.0f;
-    }
-  };
-  load();
-  bool first = true;
-  float wq[W], wk[W], dwq[W], dwk[W];
-  load_weights<V, G, NV>(a.wq, l, a.D, wq);
-  load_weights<V, G, NV>(a.wk, l, a.D, wk);
+  const float per_d = 1.0f / (float)a.D;
+  float dwq[W], dwk[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) dwq[i] = dwk[i] = 0.0f;
   if (a.axes) load_freq(a, freq);
   __syncthreads();
-  float2 cs[P];
-  float turned[P];
-  for (; at.node < a.N; at.next(a.N)) {
-    if (!first) load();
-    first = false;
-    if (a.axes && at.t0 == 0) {
-      if (at.node == at.node0) form_turns(a, freq, turn, (int)at.node0, (int)(a.N - at.node0 < each ? a.N - at.node0 : each));
-      load_turns<V, G, NV>(turn + (int)(at.node - at.node0) * pairs, pairs, l, cs);
+  for (int node0 = (int)(blockIdx.x * kHeadWarps + warp) * a.each; node0 < a.N; node0 += gridDim.x * kHeadWarps * a.each) {
+    const int nodes = min(a.N - node0, a.each);
+    if (a.axes) form_turns(a, freq, turn, node0, nodes);
+    float turned[U][P];
 #pragma unroll
-      for (int p = 0; p < P; ++p) turned[p] = 0.0f;
-    }
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int t = at.t0 + lane / G + u * AT_ONCE;
-      const bool query = t < a.Hq, ok = t < heads;
-      float h[W], b[W], mean = 0.0f;
-      x[u].get(h);
-      g[u].get(b);
+      for (int p = 0; p < P; ++p) turned[u][p] = 0.0f;
+    auto run = [&](bool key, float (&dw)[W]) {
+      float w[W];
+      load_weights<V, G, NV>(key ? a.wk : a.wq, l, a.D, w);
+      T* const out = static_cast<T*>(key ? a.ok : a.oq);
+      for (int t0 = 0; t0 < (key ? a.Hk : a.Hq); t0 += a.each == 1 ? U * AT_ONCE : AT_ONCE) {
+        const HeadStep<T> s(a, key, t0 + lane / G, nodes);
+        const HeadRows<T> from = HeadRows<T>::template at<AT_ONCE>(a, s, a.q, a.q_ld, a.k, a.k_ld, node0);
+        const HeadRows<T> from_g = HeadRows<T>::template at<AT_ONCE>(a, s, a.gq, a.gq_ld, a.gk, a.gk_ld, node0);
+        const int row0 = s.by_head ? AT_ONCE : s.heads, rstd0 = s.by_head ? AT_ONCE : all;
+        Share x[U], g[U];
+        float r[U];
 #pragma unroll
-      for (int i = 0; i < W; ++i) h[i] *= r[u];
-      if (a.axes)
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const float g0 = b[2 * p], g1 = b[2 * p + 1];
-          b[2 * p] = g0 * cs[p].x + g1 * cs[p].y;
-          b[2 * p + 1] = g1 * cs[p].x - g0 * cs[p].y;
-          const float u0 = h[2 * p] * (query ? wq[2 * p] : wk[2 * p]);
-          const float u1 = h[2 * p + 1] * (query ? wq[2 * p + 1] : wk[2 * p + 1]);
-          if (ok) turned[p] += b[2 * p + 1] * u0 - b[2 * p] * u1;
+        for (int u = 0; u < U; ++u) {
+          const bool ok = s.template has<AT_ONCE>(u);
+          x[u].load(from.x + u * from.step, l, a.D, ok);
+          g[u].load(from_g.x + u * from_g.step, l, a.D, ok);
+          r[u] = ok ? __ldg(a.rstd + (long long)node0 * all + s.first + s.t + u * rstd0) : 0.0f;
         }
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const float d = b[i] * h[i];
-        if (ok && query) dwq[i] += d;
-        if (ok && !query) dwk[i] += d;
-        b[i] *= query ? wq[i] : wk[i];
-        mean = fmaf(b[i], h[i], mean);
+        for (int u = 0; u < U; ++u) {  // rows that are not there are zeros and change no sum
+          float h[W], b[W], mean = 0.0f;
+          x[u].get(h);
+          g[u].get(b);
+#pragma unroll
+          for (int i = 0; i < W; ++i) h[i] *= r[u];
+          if (a.axes) {
+            float2 cs[P];
+            load_turns<V, G, NV>(turn + (s.by_head || u >= nodes ? 0 : u * pairs), pairs, l, cs);
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+              const float g0 = b[2 * p], g1 = b[2 * p + 1];
+              b[2 * p] = g0 * cs[p].x + g1 * cs[p].y;
+              b[2 * p + 1] = g1 * cs[p].x - g0 * cs[p].y;
+              if (a.gpos) turned[u][p] += b[2 * p + 1] * (h[2 * p] * w[2 * p]) - b[2 * p] * (h[2 * p + 1] * w[2 * p + 1]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            dw[i] = fmaf(b[i], h[i], dw[i]);
+            b[i] *= w[i];
+            mean = fmaf(b[i], h[i], mean);
+          }
+#pragma unroll
+          for (int o = G / 2; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
+          if (!out || !s.template has<AT_ONCE>(u)) continue;
+          mean *= per_d;
+#pragma unroll
+          for (int i = 0; i < W; ++i) b[i] = r[u] * fmaf(-h[i], mean, b[i]);
+          Share::store(out + ((long long)node0 * s.heads + s.t + u * row0) * a.D, l, a.D, b);
+        }
       }
+    };
+    run(false, dwq);
+    if (a.Hk) run(true, dwk);
+    if (!a.gpos) continue;
+    if (a.each == 1)  // one node's heads
 #pragma unroll
-      for (int o = G / 2; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
-      if (!ok) continue;
-      mean /= (float)a.D;
+      for (int u = 1; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < W; ++i) b[i] = r[u] * fmaf(-h[i], mean, b[i]);
-      T* out = static_cast<T*>(query ? a.oq : a.ok);
-      const long long row = query ? at.node * a.Hq + t : at.node * a.Hk + (t - a.Hq);
-      if (out) HeadShare<T, V, G, NV>::store(out + row * a.D, l, a.D, b);
-    }
-    if (a.gpos && at.t0 + at.stride >= heads) {
+        for (int p = 0; p < P; ++p) turned[0][p] += turned[u][p];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (u >= nodes) break;
       float d[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int pair = ((2 * p / V * G + l) * V + 2 * p % V) / 2;
 #pragma unroll
         for (int x = 0; x < 3; ++x)
-          if (pair < pairs && x < a.axes) d[x] = fmaf(turned[p], freq[pair * a.axes + x].hi, d[x]);
+          if (pair < pairs && x < a.axes) d[x] = fmaf(turned[u][p], freq[pair * a.axes + x].hi, d[x]);
       }
 #pragma unroll
       for (int x = 0; x < 3; ++x) {
         if (x >= a.axes) break;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) d[x] += __shfl_xor_sync(0xffffffffu, d[x], o);
-        if (lane == 0) a.gpos[at.node * a.axes + x] = d[x] * 6.2831853071795865f;
+        if (lane == 0) a.gpos[(long long)(node0 + u) * a.axes + x] = d[x] * 6.2831853071795865f;
       }
     }
   }
