@@ -386,6 +386,8 @@ struct Feed {
 __device__ __forceinline__ bool is_out(unsigned out, int lane, int l, int u) { return out >> (lane - l + u) & 1; }
 
 // ---------------------------------------------------------------- forward
+constexpr float kAhead = 8.0f;  // weights of up to e^8: the sums keep their relative error
+
 template <typename T, int VB, int G, int KN, int VN, int U>
 __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_constant__ AttnArgs a) {
   using Shape = RingShape<VB, G, KN, VN, U, 4>;
@@ -415,7 +417,9 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_
     load_q(i + 1);
 #pragma unroll
     for (int x = 0; x < VP; ++x) acc[x] = make_float2(0.0f, 0.0f);
-    float m = EQMP_NEG_INF, z = 0.0f;  // z: of the edges of the lane's place in a batch
+    // Weights are taken relative to m, a score of the row; only a score that is kAhead above it moves it, so that hardly a
+    // batch has to find its largest score and scale the sums.  z: of the edges of the lane's place in a batch, as largest.
+    float m = EQMP_NEG_INF, largest = EQMP_NEG_INF, z = 0.0f;
 #pragma unroll 1
     for (int e = e0; e < e1; e += U) {
       copy_wait<Shape::STAGES - 2>();
@@ -432,18 +436,19 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_
         score = bias == EQMP_NEG_INF ? EQMP_NEG_INF : score + bias;
       }
       if (!in) score = EQMP_NEG_INF;
-      float top = score;
+      largest = fmaxf(largest, score);
+      if (__any_sync(0xffffffffu, score > m + kAhead)) {
+        float top = score;
 #pragma unroll
-      for (int o = 1; o < U; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      top = fmaxf(top, m);
-      const float base = top == EQMP_NEG_INF ? 0.0f : top;
-      if (__any_sync(0xffffffffu, top != m)) {
-        const float keep = __expf(m - base);
+        for (int o = 1; o < U; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = fmaxf(top, m);
+        const float keep = top == EQMP_NEG_INF ? 1.0f : __expf(m - top);
         z *= keep;
 #pragma unroll
         for (int x = 0; x < VP; ++x) acc[x] = __fmul2_rn(acc[x], make_float2(keep, keep));
+        m = top;
       }
-      m = top;
+      const float base = m == EQMP_NEG_INF ? 0.0f : m;
       const float p = __expf(score - base);
       z += p;
       const unsigned out = __ballot_sync(0xffffffffu, in && score == EQMP_NEG_INF);
@@ -460,19 +465,25 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_
       stage_at = stage_at == (Shape::STAGES - 1) * Shape::BATCH ? 0 : stage_at + Shape::BATCH;
     }
 #pragma unroll
-    for (int o = 1; o < U; o *= 2) z += __shfl_xor_sync(0xffffffffu, z, o);
+    for (int o = 1; o < U; o *= 2) {
+      z += __shfl_xor_sync(0xffffffffu, z, o);
+      largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, o));
+    }
+    const float from_m = largest == EQMP_NEG_INF ? 1.0f : __expf(m - largest);  // sums relative to the largest score
     const int slot = __shfl_sync(0xffffffffu, w.slot, i);
     if (!mine) continue;
     if (slot >= 0) {
       float* to = a.part + ((long long)slot * a.H + h) * (a.Dv + 2);
-      if (l == 0) to[0] = m, to[1] = z;
+      if (l == 0) to[0] = largest, to[1] = z * from_m;
+#pragma unroll
+      for (int x = 0; x < VP; ++x) acc[x] = __fmul2_rn(acc[x], make_float2(from_m, from_m));
       store_row_part<T, VB, G, VN>(to + 2, l, a.Dv, acc);
       continue;
     }
     const long long to = (long long)(w.row + i) * a.H + h;
     if (a.stats && l == 0) {
-      a.stats[2 * to] = z == 0.0f ? 0.0f : m;
-      a.stats[2 * to + 1] = z;
+      a.stats[2 * to] = z == 0.0f ? 0.0f : largest;
+      a.stats[2 * to + 1] = z * from_m;
     }
     if (a.out) store_row<T, VB, G, VN>(static_cast<T*>(a.out) + to * a.Dv, l, a.Dv, acc, z == 0.0f ? 0.0f : 1.0f / z);
   }
