@@ -922,10 +922,9 @@ def _heads(t, name, dtype, shape, dev, torch):
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _refuse(t, name, dtype, shape, dev)
     n, h, d = shape
-    if t.is_contiguous():
-        return t.data_ptr(), h * d
-    if (t.stride(2) == 1 or d == 1) and (t.stride(1) == d or h == 1):
-        return t.data_ptr(), t.stride(0) if n > 1 else h * d
+    node, head, one = t.stride()
+    if (one == 1 or d == 1) and (head == d or h == 1):
+        return t.data_ptr(), node if n > 1 else h * d
     raise ValueError(f"{name} must have contiguous heads")
 
 

@@ -80,8 +80,9 @@ struct Alignment {
 // head whose registers hold it; more lanes where there are too few rows to fill
 // the device.  Heads that the forms with vectors of 8 or 4 bytes do not hold, and
 // bf16 heads that begin anywhere, take the general kernels.
-static AttnForm form_of(const Sizes& n, int64_t rows, int bytes, int alignment) {
+static AttnForm form_of(const Sizes& n, int64_t rows, int64_t gathered, int bytes, int alignment) {
   AttnForm f;
+  if (gathered == 0) alignment = 0;  // the rings' copies of nothing need an address that is one
   for (f.VB = alignment < 4 ? 0 : alignment; f.VB >= 4; f.VB /= 2) {
     const int k = (n.D * bytes + f.VB - 1) / f.VB, v = (n.Dv * bytes + f.VB - 1) / f.VB;
     auto fits = [&](int G) { return k <= 2 * G && v <= 8 * G; };
@@ -147,7 +148,7 @@ eqmp_status eqmp_edge_attention(const void* q, int64_t q_ld, const void* k, int6
   at.add(q, q_ld, bytes), at.add(k, k_ld, bytes), at.add(v, v_ld, bytes);
   at.add(out);
   at.bits |= (unsigned long long)D * bytes | (unsigned long long)Dv * bytes;
-  const AttnForm f = form_of(n, N, bytes, at.bytes());
+  const AttnForm f = form_of(n, N, N_src, bytes, at.bytes());
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dtype == EQMP_BF16 ? launch_attn_fwd_bf16(a, f, st) : launch_attn_fwd_f32(a, f, st);
 }
@@ -215,13 +216,13 @@ eqmp_status eqmp_edge_attention_backward(const void* grad_out, int64_t grad_out_
     return EQMP_ERR_CUDA;
   if (N > 0) {
     cut(E, &a.block, &a.blocks);
-    const AttnForm f = form_of(n, N, bytes, at.bytes());
+    const AttnForm f = form_of(n, N, N_src, bytes, at.bytes());
     const eqmp_status s = bf16 ? launch_attn_recv_bf16(a, f, st) : launch_attn_recv_f32(a, f, st);
     if (s != EQMP_OK) return s;
   }
   if (send) {
     cut(E_send, &a.block, &a.blocks);
-    const AttnForm f = form_of(n, N_src, bytes, at.bytes());
+    const AttnForm f = form_of(n, N_src, N, bytes, at.bytes());
     return bf16 ? launch_attn_send_bf16(a, f, st) : launch_attn_send_f32(a, f, st);
   }
   if (!grad_bias || N == 0) return EQMP_OK;

@@ -333,3 +333,111 @@ def test_gradients_against_differences(eq):
         step = lambda t: loss({**args, name: args[name] + t * d})  # noqa: B023,E731
         diff, grad = (step(1e-5) - step(-1e-5)) / 2e-5, host(grads[name])
         assert abs(diff - (grad * d).sum()) <= 1e-3 * np.sqrt((grad ** 2).sum() * (d ** 2).sum() / grad.size), name
+
+
+def test_edges_without_any_sender(eq):
+    """Receivers with edges and no node that sends: all senders read as zeros, so the weights are those of the bias."""
+    import torch
+
+    p = Problem(4, 16, 32, "f32", [3, 0, 5])
+    got = eq.eqmp_edge_attention(p.q, p.k[:0], p.v[:0], *p.graph, bias=p.bias, need=("out", "stats"))
+    rows = [p.bias[:3], p.bias[3:8]]
+    for i, b in ((0, rows[0]), (2, rows[1])):
+        m = b.max(0).values
+        assert torch.equal(got["stats"][i, :, 0], m)
+        assert torch.allclose(got["stats"][i, :, 1], (b - m).exp().sum(0), rtol=1e-6)
+    assert not got["out"].any() and not got["stats"][1].any()
+
+
+def test_offsets_beyond_32_bits(eq):
+    """Nodes whose keys and values lie more than 2^31 elements into their tensors, and rows more than 2^32 bytes apart."""
+    import torch
+
+    H, D, V, n = 8, 32, 1024, 300_000  # values: 2.4e9 elements
+    v = torch.zeros(n, H, V, dtype=torch.bfloat16, device="cuda")
+    far = [0, 1, 131072, 262143, n - 2, n - 1]
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    rows = torch.randn(len(far), H, V, generator=gen, device="cuda").bfloat16()
+    v[far] = rows
+    k = torch.zeros(n, H, D, dtype=torch.bfloat16, device="cuda")
+    k[far] = torch.randn(len(far), H, D, generator=gen, device="cuda").bfloat16()
+    q = torch.randn(2, H, D, generator=gen, device="cuda").bfloat16()
+    off, src = torch.tensor([0, 6, 6], dtype=torch.int32, device="cuda"), torch.tensor(far, dtype=torch.int32, device="cuda")
+    got = eq.eqmp_edge_attention(q, k, v, off, src, need=("out", "stats"))
+    near = eq.eqmp_edge_attention(q, k[far].contiguous(), rows, off, torch.arange(6, dtype=torch.int32, device="cuda"), need=("out", "stats"))
+    assert torch.equal(got["out"], near["out"]) and torch.equal(got["stats"], near["stats"])
+    # the same nodes as receivers of the gradients
+    g = torch.randn(2, H, V, generator=gen, device="cuda").bfloat16()
+    send_off = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    for i, node in enumerate(far):
+        send_off[node + 1:] = i + 1
+    back = eq.eqmp_edge_attention_backward(g, q, k, v, got["stats"], off, src, torch.zeros(6, dtype=torch.int32, device="cuda"), send_off,
+                                           torch.arange(6, dtype=torch.int32, device="cuda"), need=("v",))["v"]
+    p = (q[0].float()[None] * k[far].float()).sum(2) * D ** -0.5
+    p = torch.softmax(p, 0)[:, :, None] * g[0].float()
+    assert torch.allclose(back[far].float(), p, rtol=2 ** -7, atol=1e-6)
+    back[far] = 0
+    assert not back.any()
+    del back, v
+    wide = torch.zeros(3, 2 ** 31, dtype=torch.bfloat16, device="cuda")  # 4 GB from row to row
+    wide[:, :H * D] = torch.randn(3, H * D, generator=gen, device="cuda").bfloat16()
+    kw = wide[:, :H * D].unflatten(1, (H, D))
+    src3, off3 = torch.tensor([2, 0, 1], dtype=torch.int32, device="cuda"), torch.tensor([0, 3, 3], dtype=torch.int32, device="cuda")
+    vv = torch.randn(3, H, 64, generator=gen, device="cuda").bfloat16()
+    a, b = (eq.eqmp_edge_attention(q, t, vv, off3, src3)["out"] for t in (kw, kw.contiguous()))
+    assert torch.allclose(a.float(), b.float(), rtol=2 ** -7, atol=1e-6)
+
+
+def test_two_calls_at_once(eq):
+    """Calls on two waiting streams and two recorded graphs replayed together: each has its own memory, results as alone."""
+    import torch
+
+    a, b = Problem(8, 32, 128, "f32", MIXED * 8, seed=1), Problem(8, 32, 128, "f32", LONG * 4, seed=2)
+    want = []
+    for p in (a, b):
+        f = p.forward(eq)
+        want.append((f, p.backward(eq, f["stats"])))
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    for s in sides:
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(5_000_000)
+    got = []
+    for p, s in zip((a, b), sides):
+        f = p.forward(eq, stream=s)
+        got.append((f, p.backward(eq, f["stats"], stream=s)))
+    torch.cuda.synchronize()
+    tapes, held = [], []
+    for p in (a, b):
+        tape = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(tape):
+            f = p.forward(eq)
+            held.append((f, p.backward(eq, f["stats"])))
+        tapes.append(tape)
+    for tape, s in zip(tapes, sides):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(5_000_000)
+            tape.replay()
+    torch.cuda.synchronize()
+    for results in (got, held):
+        for (f, g), (f0, g0) in zip(results, want):
+            assert all(torch.equal(f[k], f0[k]) for k in f0) and all(torch.equal(g[k], g0[k]) for k in g0)
+
+
+def test_temporaries_outlive_the_call(eq):
+    """The workspaces of calls that wait on a side stream are not handed to the current one."""
+    import torch
+
+    from tests.test_gpu_streams import _busy_sides
+
+    p = Problem(4, 16, 32, "f32", LONG, masked=0.1)
+    f = p.forward(eq)
+    want = p.backward(eq, f["stats"])
+    torch.cuda.synchronize()
+    side, = _busy_sides(1)
+    got = p.backward(eq, f["stats"], stream=side)
+    E = len(p.src)
+    sizes = [eq.eqmp_edge_attention_backward_workspace_size(len(LONG), E, E, 4, 16, 32)] * 4 + [v.numel() * 4 for v in want.values()] * 4
+    taken = [torch.full((n // 4,), float("nan"), device="cuda") for n in sizes]
+    torch.cuda.synchronize()
+    assert all(torch.isnan(t).all() for t in taken) and all(torch.equal(got[k], want[k]) for k in want)
