@@ -37,11 +37,17 @@ static eqmp_status check_sizes(const Sizes& n, eqmp_dtype dtype, float scale) {
 }
 
 // Blocks that rows of more than two are cut into: at least 32 edges, at most
-// 2048 blocks in all, so that the parts stay a few MB.
+// 2048 blocks in all, so that the parts stay a few MB.  Graphs of up to kWhole
+// edges are not cut: there the launches that join the parts cost more than they
+// save (64 atoms, 742 edges, backward: 30 us of a caller's time with them, 25
+// without), unless nearly all edges are one node's (1000 edges of one receiver:
+// one warp a head takes 70 us for them, 18 in blocks).
+constexpr int64_t kWhole = 1024;
+
 static void cut(int64_t E, int* block, int* blocks) {
   const int64_t want = (E + 2047) / 2048;
   *block = (int)(want < 32 ? 32 : (want + 31) / 32 * 32);
-  *blocks = E > 2 * *block ? (int)((E + *block - 1) / *block) : 0;
+  *blocks = E > kWhole ? (int)((E + *block - 1) / *block) : 0;
 }
 
 static int64_t part_bytes(int64_t E, int64_t H, int64_t width) {

@@ -56,7 +56,7 @@ def calls(lib, dtype=0):
                dict(g=big * H * 4, bucket=big * 4, gt=B * H * 4, ws=lib.eqmp_edge_bias_backward_workspace_size(big, B, H)), ("gt", "ws"),
                "g bucket E B H gt ws ws_bytes st", **{**size, "E": big}, B=B,
                ws_bytes=lib.eqmp_edge_bias_backward_workspace_size(big, B, H))
-    big = 400
+    big = 1400
     rows = dict(q=N * H * D * b, k=NS * H * D * b, v=NS * H * DV * b)
     lds = dict(q_ld=H * D, v_ld=H * DV, scale=0.5)
     yield Call(lib, "eqmp_edge_attention",
@@ -145,7 +145,7 @@ def test_sizes(lib, name):
 
 
 def test_workspace_sizes(lib):
-    assert lib.eqmp_edge_attention_workspace_size(64, 8, 128) == 0 < lib.eqmp_edge_attention_workspace_size(65, 8, 128)
+    assert lib.eqmp_edge_attention_workspace_size(1024, 8, 128) == 0 < lib.eqmp_edge_attention_workspace_size(1025, 8, 128)
     # the parts of a large graph stay small beside its rows
     assert lib.eqmp_edge_attention_workspace_size(1909372, 8, 128) < 20 << 20
     assert lib.eqmp_edge_attention_workspace_size(-1, 8, 128) == lib.eqmp_edge_attention_workspace_size(5, 8, 1025) == -1
