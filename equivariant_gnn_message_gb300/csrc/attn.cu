@@ -39,9 +39,9 @@ static eqmp_status check_sizes(const Sizes& n, eqmp_dtype dtype, float scale) {
 // Blocks that rows of more than two are cut into: at least 32 edges, at most
 // 2048 blocks in all, so that the parts stay a few MB.  Graphs of up to kWhole
 // edges are not cut: there the launches that join the parts cost more than they
-// save (64 atoms, 742 edges, backward: 30 us of a caller's time with them, 25
-// without), unless nearly all edges are one node's (1000 edges of one receiver:
-// one warp a head takes 70 us for them, 18 in blocks).
+// save (64 atoms, 742 edges: forward 24.5 us a call with them, 19.4 without,
+// backward 38 and 34), unless nearly all edges are one node's (1000 edges of one
+// receiver: 119 us by one warp a head, 24 in blocks).
 constexpr int64_t kWhole = 1024;
 
 static void cut(int64_t E, int* block, int* blocks) {

@@ -470,11 +470,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_send(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------- joining
-// The parts of long rows.  A CTA looks at kJoinY blocks, a warp each: a row is
-// joined where the first block that begins inside it is found.  For each such row
-// and head threadIdx.x then goes over the columns, threadIdx.y over the parts.
+// The parts of long rows.  A CTA looks at kJoinBlocks blocks, a lane each: a row
+// is joined where the first block that begins inside it is found.  For each such
+// row and head threadIdx.x then goes over the columns, threadIdx.y over the parts.
+// (Where no row is long, the search is all of it.  By a warp for each block and
+// head it was 6.6 M instructions and 12 us on its own at 60,000 rows.)
 enum { kJoinFwd, kJoinRecv, kJoinSend };
-constexpr int kJoinX = 32, kJoinY = 16;
+constexpr int kJoinX = 32, kJoinY = 8, kJoinBlocks = 16;
 
 template <int MODE, typename T>
 __device__ void join_row(const AttnArgs& a, int first, int last, int row, int h, float (&red)[kJoinY][kJoinX]) {
@@ -553,22 +555,30 @@ __device__ void join_row(const AttnArgs& a, int first, int last, int row, int h,
 template <int MODE, typename T>
 __global__ void __launch_bounds__(kJoinX * kJoinY) k_attn_join(const __grid_constant__ AttnArgs a) {
   __shared__ float red[kJoinY][kJoinX];
-  __shared__ int range[kJoinY][3];
+  __shared__ int range[kJoinBlocks][3];
   const Rows rows = MODE == kJoinSend ? Rows{a.send_off, a.Ns, a.E_send, a.block, a.blocks}
                                       : Rows{a.off, a.N, a.E, a.block, a.blocks};
-  const int x = threadIdx.x, y = threadIdx.y, c = blockIdx.x * kJoinY + y;
-  Piece t;
-  t.row = -1;
-  if (c < a.blocks) t = find_piece(rows, c);
-  int first = -1, last = -1;
-  if (t.row >= 0) {
-    const int e0 = clamped(__ldg(rows.off + t.row), rows.E), e1 = clamped(__ldg(rows.off + t.row + 1), rows.E);
-    if (e0 / rows.block == c - 1) first = c, last = (e1 - 1) / rows.block;
+  if (threadIdx.y == 0 && threadIdx.x < kJoinBlocks) {
+    const int c = blockIdx.x * kJoinBlocks + threadIdx.x, x = c * rows.block;
+    int first = -1, last = -1, row = -1, past = rows.n;  // off[row] <= x < off[past], in words
+    if (c < rows.blocks) {
+      while (past - row > 1) {
+        const int mid = row + (past - row) / 2;
+        if (__ldg(rows.off + mid) <= x)
+          row = mid;
+        else
+          past = mid;
+      }
+      if (row >= 0) {
+        const int e0 = clamped(__ldg(rows.off + row), rows.E), e1 = clamped(__ldg(rows.off + row + 1), rows.E);
+        if (is_long(rows, e0, e1) && e0 < x && x < e1 && e0 / rows.block == c - 1) first = c, last = (e1 - 1) / rows.block;
+      }
+    }
+    range[threadIdx.x][0] = first, range[threadIdx.x][1] = last, range[threadIdx.x][2] = row;
   }
-  if (x == 0) range[y][0] = first, range[y][1] = last, range[y][2] = t.row;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // until the kernel that writes the parts is done
   __syncthreads();
-  for (int i = 0; i < kJoinY; ++i) {
+  for (int i = 0; i < kJoinBlocks; ++i) {
     if (range[i][0] < 0) continue;
     for (int h = blockIdx.y; h < a.H; h += gridDim.y) join_row<MODE, T>(a, range[i][0], range[i][1], range[i][2], h, red);
   }

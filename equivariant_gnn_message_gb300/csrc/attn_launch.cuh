@@ -34,7 +34,7 @@ eqmp_status launch_attn_join(const AttnArgs& a, cudaStream_t st) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.blocks + kJoinY - 1) / kJoinY), (unsigned)(a.H < 16 ? a.H : 16));
+  cfg.gridDim = dim3((unsigned)((a.blocks + kJoinBlocks - 1) / kJoinBlocks), (unsigned)(a.H < 16 ? a.H : 16));
   cfg.blockDim = dim3(kJoinX, kJoinY);
   cfg.stream = st;
   cfg.attrs = &attr;
