@@ -121,7 +121,7 @@ __device__ __forceinline__ void let_join_start(const AttnArgs& a) {
 }
 
 // ---------------------------------------------------------------- vectors
-// V elements of T at a time: 16 bytes where everything lies on 16, else one.
+// V elements of T at a time.
 template <typename T, int V>
 struct Vec;
 
@@ -249,6 +249,10 @@ __device__ __forceinline__ void head_sum(float (&t)[U]) {
 #define EQMP_NEG_INF __int_as_float(0xff800000)
 
 // ---------------------------------------------------------------- forward
+// The general kernels: rows whose heads begin anywhere (bf16), and long heads of
+// odd sizes, value by value.  Bound by the latency of one batch after the other:
+// 100,000 atoms, 8 heads of 32 + 128 fp32 values, 2237 us forward with vectors of
+// 16 bytes, which the rings of attn_ring.cuh have taken over since.
 // One warp per piece of a row and 32 / G heads; G lanes hold a head's query and
 // its sum in registers, and the edges' keys and values pass once, U edges at a
 // time, with the running maximum and sum of a softmax.
