@@ -9,7 +9,9 @@
 //   dq[i] = scale sum_e ds k,  dk[j] = scale sum_{src_e = j} ds q,
 //   dv[j] = sum_{src_e = j} p g,  dbias = ds
 // An edge with s = -inf is left out: nothing of its rows enters a sum.  A row
-// with no edge left has m = z = 0, zeros as its result and no gradients.
+// with no edge left has m = z = 0, zeros as its result and no gradients.  A row
+// with one edge left has its value as the result and no gradients but the
+// value's: ds is exactly 0, not what rounding leaves of dp - delta.
 // Scores, statistics and sums are fp32; bf16 is the storage of q, k, v, out and
 // their gradients, rounded once on the store.  delta is summed from the row's
 // own p and dp, not from the stored out, whose rounding would reach the fp32
@@ -124,42 +126,6 @@ __device__ __forceinline__ void let_join_start(const AttnArgs& a) {
 // V elements of T at a time.
 template <typename T, int V>
 struct Vec;
-
-template <>
-struct Vec<float, 4> {
-  float4 v;
-  __device__ __forceinline__ void load(const float* p, bool ok) {
-    v = ok ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  }
-  __device__ __forceinline__ void zero() { v = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
-  __device__ __forceinline__ void get(float (&f)[4]) const { f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w; }
-  static __device__ __forceinline__ void store(float* p, const float* f) {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-  }
-};
-
-template <>
-struct Vec<__nv_bfloat16, 8> {
-  uint4 v;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p, bool ok) {
-    v = ok ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
-  }
-  __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
-    __nv_bfloat162 b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(b);
-  }
-};
 
 template <typename T>
 struct Vec<T, 1> {
@@ -347,7 +313,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_recv(AttnArgs a) {
   const T* k = static_cast<const T*>(a.k) + (long long)h * a.D;
   const T* v = static_cast<const T*>(a.v) + (long long)h * a.Dv;
   const long long at = (long long)t.row * a.H + h;
-  float q[KN * V], g[VN * V], pdk[KN * V], pk[KN * V], delta = 0.0f;
+  float q[KN * V], g[VN * V], pdk[KN * V], pk[KN * V], delta = 0.0f, dps = 0.0f;
+  int live = 0;
   {
     Frag<T, V, G, KN> f;
     f.load(static_cast<const T*>(a.q) + t.row * a.q_ld + (long long)h * a.D, l, a.D, mine);
@@ -389,12 +356,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_recv(AttnArgs a) {
         if (a.pd && l == 0 && mine && b + u < n)
           a.pd[(long long)(e + b + u) * a.H + h] = make_float2(left_out ? -1.0f : p, dp);
         delta = fmaf(p, dp, delta);
+        dps += dp;
+        live += !left_out;
         kf[u].add_to(pdk, p * dp);
         kf[u].add_to(pk, p);
       }
     }
   }
   if (!mine) return;
+  const bool alone = live == 1;  // the only edge's weight is 1, whatever its score
   if (t.slot >= 0) {
     float* to = a.part + ((long long)t.slot * a.H + h) * (2 * a.D + 1);
     if (l == 0) to[0] = delta;
@@ -402,10 +372,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_recv(AttnArgs a) {
     store_part<V, G, KN>(to + 1 + a.D, l, a.D, pk);
     return;
   }
+  if (alone) delta = dps;
   if (a.delta && l == 0) a.delta[at] = delta;
   if (a.gq) {
 #pragma unroll
-    for (int i = 0; i < KN * V; ++i) pdk[i] = fmaf(-delta, pk[i], pdk[i]);
+    for (int i = 0; i < KN * V; ++i) pdk[i] = alone ? 0.0f : fmaf(-delta, pk[i], pdk[i]);
     store_share<T, V, G, KN>(static_cast<T*>(a.gq) + at * a.D, l, a.D, pdk, a.scale);
   }
 }

@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(const __grid
     load_next(i + 1);
 #pragma unroll
     for (int x = 0; x < KP; ++x) pdk[x] = pk[x] = make_float2(0.0f, 0.0f);
-    float delta = 0.0f;
+    float delta = 0.0f, dps = 0.0f, live = 0.0f;
 #pragma unroll 1
     for (int e = e0; e < e1; e += U) {
       copy_wait<Shape::STAGES - 2>();
@@ -573,6 +573,8 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(const __grid
       if (a.pd && l < U && in) a.pd[(long long)(e + l) * a.H + h] = make_float2(left_out ? -1.0f : p, dp);
       const float pdp = p * dp;
       delta += pdp;
+      dps += dp;
+      live += left_out || !in ? 0.0f : 1.0f;
       const unsigned out = __ballot_sync(0xffffffffu, in && left_out);  // left out: a weight of 0 would keep a NaN
       auto add = [&](int u) {
         const float pu = __shfl_sync(0xffffffffu, p, lane - l + u), pdpu = __shfl_sync(0xffffffffu, pdp, lane - l + u);
@@ -598,8 +600,14 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(const __grid
       stage_at = stage_at == (Shape::STAGES - 1) * Shape::BATCH ? 0 : stage_at + Shape::BATCH;
     }
 #pragma unroll
-    for (int o = 1; o < U; o *= 2) delta += __shfl_xor_sync(0xffffffffu, delta, o);
+    for (int o = 1; o < U; o *= 2) {
+      delta += __shfl_xor_sync(0xffffffffu, delta, o);
+      dps += __shfl_xor_sync(0xffffffffu, dps, o);
+      live += __shfl_xor_sync(0xffffffffu, live, o);
+    }
     const int slot = __shfl_sync(0xffffffffu, w.slot, i);
+    const bool alone = live == 1.0f && slot < 0;  // the row's only edge: its weight is 1, whatever its score
+    if (alone) delta = dps;
     if (!mine) continue;
     if (slot >= 0) {
       float* to = a.part + ((long long)slot * a.H + h) * (2 * a.D + 1);
@@ -612,7 +620,7 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(const __grid
     if (l == 0) a.delta[to] = delta;
     if (a.gq) {
 #pragma unroll
-      for (int x = 0; x < KP; ++x) pdk[x] = __ffma2_rn(make_float2(-delta, -delta), pk[x], pdk[x]);
+      for (int x = 0; x < KP; ++x) pdk[x] = alone ? make_float2(0.0f, 0.0f) : __ffma2_rn(make_float2(-delta, -delta), pk[x], pdk[x]);
       store_row<T, VB, G, KN>(static_cast<T*>(a.gq) + to * a.D, l, a.D, pdk, a.scale);
     }
   }

@@ -630,7 +630,8 @@ eqmp_status eqmp_edge_attention(const void* q, int64_t q_ld, const void* k, int6
  *   grad_k     [N_src][H][D]   scale sum over the sender's edges of ds q[i]
  *   grad_v     [N_src][H][Dv]  sum over the sender's edges of p grad_out[i]
  *   grad_bias  [E][H]          ds
- * Edges that were left out have no part in any of them (grad_bias 0).  grad_k and
+ * Edges that were left out have no part in any of them (grad_bias 0).  The only
+ * edge of a receiver has ds = 0, exactly.  grad_k and
  * grad_v need dst [E] and the sender view (send_offsets [N_src+1], send_edges
  * [E_send]) of the same edges, as eqmp_fused_backward (the three may be NULL where
  * neither is asked for).  Every row of the results is written; grad_bias is 0 for

@@ -441,3 +441,45 @@ def test_temporaries_outlive_the_call(eq):
     taken = [torch.full((n // 4,), float("nan"), device="cuda") for n in sizes]
     torch.cuda.synchronize()
     assert all(torch.isnan(t).all() for t in taken) and all(torch.equal(got[k], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("shape", [(4, 16, 32), (3, 7, 9)], ids=str)
+def test_a_graph_that_is_none_does_no_harm(eq, shape):
+    """Offsets that go up and down and lie outside, senders, receivers and edge numbers of any value: indices are clamped or
+    their edges left out, so the results are some numbers and the next call is sound."""
+    import torch
+
+    p = Problem(*shape, "f32", LONG, seed=9)
+    good = p.forward(eq)
+    rng = np.random.default_rng(1)
+    E, n = len(p.src), len(LONG)
+    up = lambda a: torch.from_numpy(np.asarray(a, np.int32)).cuda()  # noqa: E731
+    wild = lambda k: up(rng.integers(-2 ** 31, 2 ** 31, k))  # noqa: E731
+    near = lambda lo, hi, k: up(rng.integers(lo, hi, k))  # noqa: E731
+    for off, src, senders in ((near(-50, E + 50, n + 1), near(-3, n + 3, E), (near(-3, n + 3, E), near(-50, E + 50, n + 1), near(-9, E + 9, E))),
+                              (wild(n + 1), wild(E), (wild(E), wild(n + 1), wild(E)))):
+        got = eq.eqmp_edge_attention(p.q, p.k, p.v, off, src, bias=p.bias, need=("out", "stats"))
+        back = eq.eqmp_edge_attention_backward(p.g, p.q, p.k, p.v, got["stats"], off, src, *senders, bias=p.bias,
+                                               need=("q", "k", "v", "bias"))
+        torch.cuda.synchronize()
+        assert got["out"].shape == good["out"].shape and back["bias"].shape == (E, shape[0])
+    again = p.forward(eq)
+    assert torch.equal(again["out"], good["out"])
+
+
+@pytest.mark.parametrize("shape", [(4, 16, 128), (3, 6, 10), (2, 5, 49), (5, 7, 9)], ids=str)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_the_only_edge_of_a_receiver(eq, shape, dtype):
+    """Its weight is 1 whatever the score: the value is the result, and nothing but the value has a gradient, with the pass's own
+    statistics and with those of another order of the sums."""
+    import torch
+
+    p = Problem(*shape, dtype, [1, 1, 3, 1, 0, 1], seed=4)
+    p.bias[2:4] = -float("inf")  # the third row keeps one of its three edges
+    got = p.forward(eq)
+    for i, e in enumerate([0, 1, 4, 5, None, 6]):
+        if e is not None:
+            assert torch.equal(got["out"][i], p.v[int(p.src[e])])
+    for stats in (got["stats"], torch.stack((got["stats"][:, :, 0] * (1 + 2.0 ** -22), got["stats"][:, :, 1]), 2)):
+        g = p.backward(eq, stats)
+        assert not g["q"].any() and not g["k"].any() and not g["bias"].any() and g["v"].any()
