@@ -197,11 +197,10 @@ __device__ __forceinline__ float scatter_sum(float (&v)[NV], int l) {
 
 // The shape of a ring: U edges a batch, each of KN + VN vectors a lane, and per
 // batch a few bytes for every edge and head.
-// A stage of 5 to 10 KB and two or three of them leave room for ten to 14 warps on
-// an SM.  Measured at 100,000 atoms, 8 heads of 32 + 128, atoms in the order of
-// their cells, forward: fp32 2 edges and 3 stages 786 us, 2 and 2 871, 4 and 2
-// 865, 4 and 3 1147 (six warps); bf16 at 10,000 atoms, 48 edges a row, values of
-// 256: 4 and 2 259 us, 2 and 3 269, 4 and 3 322.
+// Two stages of 5 to 10 KB leave room for 10 to 20 warps on an SM.  Measured, forward:
+// 100,000 atoms in the order of their cells, fp32, 8 heads of 32 + 128: 2 edges and 2
+// stages 630 us, 2 and 3 697, 4 and 2 727, 4 and 3 1049; 10,000 atoms of 48 edges, bf16,
+// 8 heads of 32 + 256: 4 and 2 191, 2 and 2 203, 2 and 3 229.
 template <int VB, int G, int KN, int VN, int U_, int SMALL>
 struct RingShape {
   static constexpr int VECS = KN + VN;
@@ -209,8 +208,8 @@ struct RingShape {
   static constexpr int HEADS = 32 / G;
   static constexpr int VEC = 32 * VB;  // a vector of every lane
   static constexpr int SMALL_AT = U * VECS * VEC;
-  static constexpr int BATCH = SMALL_AT + (U * HEADS * SMALL + 127) / 128 * 128;
-  static constexpr int STAGES = U * VECS * VB <= 160 ? 3 : 2;
+  static constexpr int BATCH = SMALL_AT + (U * HEADS * SMALL + 31) / 32 * 32;
+  static constexpr int STAGES = 2;
   static constexpr int WARP = STAGES * BATCH;
   static constexpr int CTA = kRingWarps * WARP;
 };
