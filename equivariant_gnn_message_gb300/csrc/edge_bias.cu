@@ -3,6 +3,7 @@
 //
 //   bucket[e] = #{b : borders[b] <= |vec_e|},  bias[e][h] = table[bucket[e]][h]
 //   dtable[b][h] = sum of dbias[e][h] over the edges of bucket b
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include "host_args.h"
@@ -128,13 +129,12 @@ constexpr int kCopyFloats = 16384;  // of the copies of a CTA: three CTAs an SM
 __device__ __forceinline__ void add_to(float& t, float v) { t += v; }
 __device__ __forceinline__ void add_to(float2& t, const float2& v) { t.x += v.x, t.y += v.y; }
 
+// Sums the edges [begin, end) into the CTA's copies.
 template <typename F>  // float2 or float: heads of a thread
-__global__ void __launch_bounds__(kGradThreads) k_edge_bias_bwd(BiasArgs a, int heads, int copies) {
+__device__ __forceinline__ void sum_range(const BiasArgs& a, float* copy, int heads, int copies, int begin, int end) {
   constexpr int V = sizeof(F) / 4;
-  extern __shared__ __align__(16) float copy[];  // [copies][B][heads]
   const int h0 = blockIdx.y * heads, hn = min(heads, a.H - h0), size = a.B * heads, width = heads / V;
   const int h = threadIdx.x % width * V, r = threadIdx.x / width;
-  const int begin = (int)((long long)a.E * blockIdx.x / a.parts), end = (int)((long long)a.E * (blockIdx.x + 1) / a.parts);
   const bool mine = r < copies && h < hn;
   const float* grad = a.grad + h0 + h;
   int b[kGradAhead];
@@ -167,14 +167,48 @@ __global__ void __launch_bounds__(kGradThreads) k_edge_bias_bwd(BiasArgs a, int 
       }
   }
   __syncthreads();
-  float* out = a.parts > 1 ? a.part + (long long)blockIdx.x * a.B * a.H : a.gtable;
-  for (int i = threadIdx.x; i < a.B * hn; i += kGradThreads) {
+}
+
+// The sum of a CTA's copies at one place of the table.
+__device__ __forceinline__ float sum_copies(const float* copy, int copies, int size, int at) {
+  float t = 0.0f;
+#pragma unroll 8
+  for (int c = 0; c < copies; ++c) t += copy[c * size + at];
+  return t;
+}
+
+template <typename F>
+__global__ void __launch_bounds__(kGradThreads) k_edge_bias_bwd(BiasArgs a, int heads, int copies) {
+  extern __shared__ __align__(16) float copy[];  // [copies][B][heads]
+  const int h0 = blockIdx.y * heads, hn = min(heads, a.H - h0);
+  sum_range<F>(a, copy, heads, copies, (int)((long long)a.E * blockIdx.x / a.parts), (int)((long long)a.E * (blockIdx.x + 1) / a.parts));
+  float* const out = a.part + (long long)blockIdx.x * a.B * a.H;
+  for (int i = threadIdx.x; i < a.B * hn; i += kGradThreads)
+    out[(long long)(i / hn) * a.H + h0 + i % hn] = sum_copies(copy, copies, a.B * heads, i / hn * heads + i % hn);
+}
+
+// Few edges: a cluster of CTAs, which adds its sums through distributed shared
+// memory, in the order of the CTAs.  One launch in place of two, and no workspace:
+// 16,516 edges, 4 heads, 32 buckets 16.5 -> 7.1 us a call, 5.1 on the GPU either way.
+constexpr int kGradCluster = 8;
+constexpr int64_t kFewEdges = 32768;
+
+template <typename F>
+__global__ void __cluster_dims__(kGradCluster, 1, 1) __launch_bounds__(kGradThreads) k_edge_bias_bwd_few(BiasArgs a, int heads, int copies) {
+  extern __shared__ __align__(16) float copy[];
+  const auto cluster = cooperative_groups::this_cluster();
+  const int h0 = blockIdx.y * heads, hn = min(heads, a.H - h0), size = a.B * heads, rank = blockIdx.x;
+  sum_range<F>(a, copy, heads, copies, (int)((long long)a.E * rank / kGradCluster), (int)((long long)a.E * (rank + 1) / kGradCluster));
+  for (int i = threadIdx.x; i < size; i += kGradThreads) copy[i] = sum_copies(copy, copies, size, i);  // a thread's own place
+  cluster.sync();
+  for (int i = rank * kGradThreads + threadIdx.x; i < a.B * hn; i += kGradCluster * kGradThreads) {
     const int at = i / hn * heads + i % hn;
     float t = 0.0f;
-#pragma unroll 8
-    for (int c = 0; c < copies; ++c) t += copy[c * size + at];
-    out[(long long)(i / hn) * a.H + h0 + i % hn] = t;
+#pragma unroll
+    for (int c = 0; c < kGradCluster; ++c) t += cluster.map_shared_rank(copy, c)[at];
+    a.gtable[(long long)(i / hn) * a.H + h0 + i % hn] = t;
   }
+  cluster.sync();  // no CTA leaves while its sums are read
 }
 
 constexpr int kBiasSumX = 32, kBiasSumY = 16;
@@ -197,8 +231,9 @@ __global__ void __launch_bounds__(kBiasSumX * kBiasSumY) k_edge_bias_sum(BiasArg
 }
 
 // CTAs of the backward pass: three on each of 152 SMs, at least 256 edges each,
-// and no more than 64 MB of parts.
+// and no more than 64 MB of parts; 0: the cluster of CTAs for few edges.
 static int grad_parts(int64_t E, int64_t B, int64_t H) {
+  if (E <= kFewEdges) return 0;
   int64_t n = (E + 255) / 256;
   const int64_t most = (16ll << 20) / (B * H);
   if (n > 456) n = 456;
@@ -213,7 +248,7 @@ static eqmp_status check(int64_t E, int32_t B, int32_t H) {
 
 static int64_t grad_workspace(int64_t E, int64_t B, int64_t H) {
   const int parts = grad_parts(E, B, H);
-  return parts > 1 ? parts * B * H * 4 : 0;
+  return parts * B * H * 4;
 }
 
 }  // namespace eqmp
@@ -276,17 +311,18 @@ eqmp_status eqmp_edge_bias_backward(const float* grad_bias, const int32_t* bucke
   if (copies > kCopyFloats / (B * heads)) copies = kCopyFloats / (B * heads);
   const int smem = copies * B * heads * 4;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid((unsigned)a.parts, (unsigned)((H + heads - 1) / heads));
-  static unsigned long long done[2] = {0, 0};
+  const dim3 grid((unsigned)(a.parts ? a.parts : kGradCluster), (unsigned)((H + heads - 1) / heads));
+  static unsigned long long done[4] = {0, 0, 0, 0};
   auto run = [&](auto kernel, unsigned long long* mask) {
     if (ensure_smem_attr(kernel, kCopyFloats * 4, mask) != cudaSuccess) return false;
     kernel<<<grid, kGradThreads, smem, st>>>(a, heads, copies);
-    return true;
+    return cudaGetLastError() == cudaSuccess;
   };
-  const bool set = V == 2 ? run(k_edge_bias_bwd<float2>, done) : run(k_edge_bias_bwd<float>, done + 1);
-  if (!set) return EQMP_ERR_CUDA;
-  if (cudaGetLastError() != cudaSuccess) return EQMP_ERR_CUDA;
-  if (a.parts == 1) return EQMP_OK;
+  if (!a.parts) {
+    const bool set = V == 2 ? run(k_edge_bias_bwd_few<float2>, done) : run(k_edge_bias_bwd_few<float>, done + 1);
+    return set ? EQMP_OK : EQMP_ERR_CUDA;
+  }
+  if (!(V == 2 ? run(k_edge_bias_bwd<float2>, done + 2) : run(k_edge_bias_bwd<float>, done + 3))) return EQMP_ERR_CUDA;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;

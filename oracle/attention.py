@@ -47,7 +47,7 @@ def head_norm_backward(g, x, rstd, w=None, theta=None, freq=None):
 def edge_bucket(vec, borders):
     v, b = np.asarray(vec, np.float64), np.asarray(borders, np.float64)
     square = (v[:, 0] * v[:, 0] + v[:, 1] * v[:, 1]) + v[:, 2] * v[:, 2]
-    return np.array([int(sum(s >= x * x for x in b)) for s in square], np.int32)
+    return np.array([int((s >= b * b).sum()) for s in square], np.int32)
 
 
 def edge_bias_backward(grad, bucket, n_buckets):

@@ -51,7 +51,7 @@ def calls(lib, dtype=0):
                q_ld=H * D, k_ld=2 * D, HK=2, axes=3, ws_bytes=lib.eqmp_head_norm_backward_workspace_size(N, D))
     yield Call(lib, "eqmp_edge_bias", dict(vec=E * 12, borders=(B - 1) * 4, table=B * H * 4, bias=E * H * 4, bucket=E * 4),
                ("bias", "bucket"), "vec E borders B table H bias bucket st", **size, B=B)
-    big = 5000
+    big = 50000
     yield Call(lib, "eqmp_edge_bias_backward",
                dict(g=big * H * 4, bucket=big * 4, gt=B * H * 4, ws=lib.eqmp_edge_bias_backward_workspace_size(big, B, H)), ("gt", "ws"),
                "g bucket E B H gt ws ws_bytes st", **{**size, "E": big}, B=B,
@@ -151,7 +151,7 @@ def test_workspace_sizes(lib):
     assert lib.eqmp_edge_attention_workspace_size(-1, 8, 128) == lib.eqmp_edge_attention_workspace_size(5, 8, 1025) == -1
     assert lib.eqmp_edge_attention_backward_workspace_size(5, 5, 2 ** 30 + 1, 8, 8, 8) == -1
     assert lib.eqmp_head_norm_backward_workspace_size(5, 257) == -1 and lib.eqmp_head_norm_backward_workspace_size(0, 8) == 0
-    assert lib.eqmp_edge_bias_backward_workspace_size(256, 64, 8) == 0 and lib.eqmp_edge_bias_backward_workspace_size(5, 0, 8) == -1
+    assert lib.eqmp_edge_bias_backward_workspace_size(32768, 64, 8) == 0 and lib.eqmp_edge_bias_backward_workspace_size(5, 0, 8) == -1
 
 
 # ------------------------------------------------------------------ the binding
