@@ -41,7 +41,6 @@ struct AttnArgs {
   int N, Ns, E, E_send, H, D, Dv;
   int block, blocks;  // edges of a block of a long row, blocks in all (0: rows are not split)
   int rows_each;      // rows of a warp in the kernels of attn_ring.cuh
-  int early;          // the kernel that joins long rows may be launched at once
 };
 
 constexpr int kAttnWarps = 4;  // of a CTA, each with its own piece
@@ -113,13 +112,6 @@ __device__ __forceinline__ Piece find_piece(const Rows& r, int w) {
   t.e0 = x;
   t.e1 = min(e1, x + r.block);
   return t;
-}
-
-// Lets k_attn_join be launched while this kernel runs: its CTAs look for long rows
-// and wait.  Only where all CTAs fit on the device at once, so that none is kept
-// from its place.
-__device__ __forceinline__ void let_join_start(const AttnArgs& a) {
-  if (a.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- vectors
@@ -224,7 +216,6 @@ __device__ __forceinline__ void head_sum(float (&t)[U]) {
 // time, with the running maximum and sum of a softmax.
 template <typename T, int V, int G, int KN, int VN, int U>
 __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_fwd(AttnArgs a) {
-  let_join_start(a);
   const Rows rows{a.off, a.N, a.E, a.block, a.blocks};
   const Piece t = find_piece(rows, blockIdx.x * kAttnWarps + (threadIdx.x >> 5));
   if (t.row < 0) return;
@@ -304,7 +295,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_fwd(AttnArgs a) {
 //   dq = scale (sum_e p dp k  -  delta sum_e p k)
 template <typename T, int V, int G, int KN, int VN, int U>
 __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_recv(AttnArgs a) {
-  let_join_start(a);
   const Rows rows{a.off, a.N, a.E, a.block, a.blocks};
   const Piece t = find_piece(rows, blockIdx.x * kAttnWarps + (threadIdx.x >> 5));
   if (t.row < 0) return;
@@ -385,7 +375,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_recv(AttnArgs a) {
 // the rows of their receivers, in the order of the sender view; and dbias.
 template <typename T, int V, int G, int KN, int VN, int U>
 __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_send(AttnArgs a) {
-  let_join_start(a);
   const Rows rows{a.send_off, a.Ns, a.E_send, a.block, a.blocks};
   const Piece t = find_piece(rows, blockIdx.x * kAttnWarps + (threadIdx.x >> 5));
   if (t.row < 0) return;

@@ -44,11 +44,10 @@ eqmp_status launch_attn_join(const AttnArgs& a, cudaStream_t st) {
 }
 
 template <int PASS, typename T, int V, int G, int KN, int VN>
-eqmp_status launch_attn_form(AttnArgs a, cudaStream_t st) {
+eqmp_status launch_attn_form(const AttnArgs& a, cudaStream_t st) {
   constexpr int VALUES = VN * V, U = VALUES <= 16 ? 4 : VALUES <= 32 ? 2 : 1;
   const int rows = PASS == kAttnSend ? a.Ns : a.N;
   const dim3 grid((unsigned)((rows + a.blocks + kAttnWarps - 1) / kAttnWarps), (unsigned)((a.H * G + 31) / 32));
-  a.early = (long long)grid.x * grid.y <= 152 * 2;
   if constexpr (PASS == kAttnFwd)
     k_attn_fwd<T, V, G, KN, VN, U><<<grid, 32 * kAttnWarps, 0, st>>>(a);
   else if constexpr (PASS == kAttnRecv)
@@ -59,12 +58,11 @@ eqmp_status launch_attn_form(AttnArgs a, cudaStream_t st) {
 }
 
 template <int PASS, typename T, int VB, int G, int KN, int VN>
-eqmp_status launch_attn_ring(AttnArgs a, cudaStream_t st) {
+eqmp_status launch_attn_ring(const AttnArgs& a, cudaStream_t st) {
   constexpr int U = KN + VN <= 4 || (sizeof(T) == 2 && KN + VN <= 5) || VB < 16 ? 4 : 2;
   constexpr int SMEM = RingShape<VB, G, KN, VN, U, PASS == kAttnSend ? 16 : 4>::CTA;
   const long long rows = PASS == kAttnSend ? a.Ns : a.N, workers = a.blocks + (rows + a.rows_each - 1) / a.rows_each;
   const dim3 grid((unsigned)((workers + kRingWarps - 1) / kRingWarps), (unsigned)((a.H * G + 31) / 32));
-  a.early = (long long)grid.x * grid.y <= 152 * 4;
   static unsigned long long done = 0;
   auto run = [&](auto kernel) {
     if (ensure_smem_attr(kernel, SMEM, &done) != cudaSuccess) return EQMP_ERR_CUDA;

@@ -9,10 +9,10 @@
 // filled with zeros.
 //
 // The gather binds.  100,000 atoms, 19 edges each, 8 heads of 32 + 128 fp32 values
-// (9.8 GB of rows an edge list through L2): atoms in the order of their cells 755
-// us forward (13 TB/s), 820 and 840 the two passes backward; in no order 1115 us,
+// (9.8 GB of rows an edge list through L2): atoms in the order of their cells 630
+// us forward (15 TB/s), 758 and 712 the two passes backward; in no order 1110 us,
 // by DRAM (32 % of the rows hit L2).  10,000 atoms, 48 edges each, 8 heads of 32 +
-// 256 bf16 values: 205, 245 and 225 us, with 53 % of the issue slots at 9 warps an
+// 256 bf16 values: 191, 233 and 215 us, with 53 % of the issue slots at 9 warps an
 // SM, which is what shared memory has room for.
 #pragma once
 
@@ -399,7 +399,6 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_
   using Shape = RingShape<VB, G, KN, VN, U, 4>;
   constexpr int P = RowVec<T, VB>::PAIRS, KP = KN * P, VP = VN * P;
   extern __shared__ __align__(128) uint8_t space[];
-  let_join_start(a);
   const Rows rows{a.off, a.N, a.E, a.block, a.blocks};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G, hh = lane / G;
   const Work w = find_work(rows, blockIdx.x * kRingWarps + warp, a.rows_each);
@@ -502,7 +501,6 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(const __grid
   using Shape = RingShape<VB, G, KN, VN, U, 4>;
   constexpr int P = RowVec<T, VB>::PAIRS, KP = KN * P, VP = VN * P;
   extern __shared__ __align__(128) uint8_t space[];
-  let_join_start(a);
   const Rows rows{a.off, a.N, a.E, a.block, a.blocks};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G, hh = lane / G;
   const Work w = find_work(rows, blockIdx.x * kRingWarps + warp, a.rows_each);
@@ -632,7 +630,6 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(const __grid
   constexpr int P = RowVec<T, VB>::PAIRS, KP = KN * P, VP = VN * P, HEADS = 32 / G;
   constexpr int DELTA_AT = Shape::SMALL_AT + U * HEADS * 8, EDGE_AT = DELTA_AT + U * HEADS * 4;
   extern __shared__ __align__(128) uint8_t space[];
-  let_join_start(a);
   const Rows rows{a.send_off, a.Ns, a.E_send, a.block, a.blocks};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G, hh = lane / G;
   const Work w = find_work(rows, blockIdx.x * kRingWarps + warp, a.rows_each);
