@@ -10,7 +10,7 @@
 //
 // The gather binds.  100,000 atoms, 19 edges each, 8 heads of 32 + 128 fp32 values
 // (9.8 GB of rows an edge list through L2): atoms in the order of their cells 630
-// us forward (15 TB/s), 758 and 712 the two passes backward; in no order 1110 us,
+// us forward (15 TB/s), 725 and 709 the two passes backward; in no order 1110 us,
 // by DRAM (32 % of the rows hit L2).  10,000 atoms, 48 edges each, 8 heads of 32 +
 // 256 bf16 values: 191, 233 and 215 us, with 53 % of the issue slots at 9 warps an
 // SM, which is what shared memory has room for.
@@ -496,8 +496,14 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_
 }
 
 // ---------------------------------------------------------------- backward
+// fp32 rows of up to five vectors a lane: registers for 18 warps an SM (725 us where the
+// compiler's own choice takes 758; a bound of 20 takes 757).  0 leaves it to the
+// compiler: bf16 rows of 1 + 4 vectors at a bound of 1 took 249 us for 235.
+template <typename T, int VB, int KN, int VN>
+constexpr int kRecvWarps = sizeof(T) == 4 && VB == 16 && KN + VN <= 5 ? 18 : 0;
+
 template <typename T, int VB, int G, int KN, int VN, int U>
-__global__ void __launch_bounds__(32 * kRingWarps) k_attn_recv_ring(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(32 * kRingWarps, (kRecvWarps<T, VB, KN, VN>)) k_attn_recv_ring(const __grid_constant__ AttnArgs a) {
   using Shape = RingShape<VB, G, KN, VN, U, 4>;
   constexpr int P = RowVec<T, VB>::PAIRS, KP = KN * P, VP = VN * P;
   extern __shared__ __align__(128) uint8_t space[];
