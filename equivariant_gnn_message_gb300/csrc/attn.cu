@@ -10,18 +10,6 @@ namespace eqmp {
 constexpr int kMaxDim = 256, kMaxValueDim = 1024, kMaxHeads = 1024;
 constexpr int64_t kMaxCount = 1ll << 30;  // nodes and edges: an index plus a stride of the launch stays an int
 
-// dbias alone, where no sender's gradient is asked for.
-__global__ void __launch_bounds__(256) k_attn_bias(AttnArgs a) {
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= a.N) return;
-  const int e0 = clamped(__ldg(a.off + row), a.E), e1 = clamped(__ldg(a.off + row + 1), a.E);
-  const long long end = (long long)e1 * a.H;
-  for (long long i = (long long)e0 * a.H + lane; i < end; i += 32) {
-    const float2 pd = a.pd[i];
-    a.gbias[i] = pd.x < 0.0f ? 0.0f : pd.x * (pd.y - a.delta[(long long)row * a.H + i % a.H]);
-  }
-}
-
 struct Sizes {
   int64_t N, Ns, E;
   int32_t H, D, Dv;
@@ -207,7 +195,7 @@ eqmp_status eqmp_edge_attention_backward(const void* grad_out, int64_t grad_out_
   char* const space = static_cast<char*>(workspace);
   AttnArgs a{};
   a.q = q, a.q_ld = q_ld, a.k = k, a.k_ld = k_ld, a.v = v, a.v_ld = v_ld, a.g = grad_out, a.g_ld = grad_out_ld;
-  a.bias = bias, a.off = row_offsets, a.src = src, a.dst = dst, a.send_off = send_offsets, a.send_edges = send_edges;
+  a.bias = bias, a.off = row_offsets, a.src = src, a.dst = send ? dst : nullptr, a.send_off = send_offsets, a.send_edges = send_edges;
   a.stats = const_cast<float*>(stats);
   a.gq = grad_q, a.gk = grad_k, a.gv = grad_v, a.gbias = grad_bias;
   a.delta = reinterpret_cast<float*>(space + ws.pd);
@@ -221,23 +209,20 @@ eqmp_status eqmp_edge_attention_backward(const void* grad_out, int64_t grad_out_
   at.bits |= (unsigned long long)D * bytes | (unsigned long long)Dv * bytes;
   const bool bf16 = dtype == EQMP_BF16;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // the bias of edges that no pass below reaches
-  if (grad_bias && E > 0 && (!send || E_send != E) && cudaMemsetAsync(grad_bias, 0, (size_t)E * H * 4, st) != cudaSuccess)
-    return EQMP_ERR_CUDA;
   if (N > 0) {
     cut(E, &a.block, &a.blocks);
     const AttnForm f = form_of(n, N, N_src, bytes, at.bytes());
     const eqmp_status s = bf16 ? launch_attn_recv_bf16(a, f, st) : launch_attn_recv_f32(a, f, st);
     if (s != EQMP_OK) return s;
   }
-  if (send) {
-    cut(E_send, &a.block, &a.blocks);
-    const AttnForm f = form_of(n, N_src, N, bytes, at.bytes());
-    return bf16 ? launch_attn_send_bf16(a, f, st) : launch_attn_send_f32(a, f, st);
+  if (N == 0 && grad_bias && E > 0) {
+    if (cudaMemsetAsync(grad_bias, 0, (size_t)E * H * 4, st) != cudaSuccess) return EQMP_ERR_CUDA;
+    a.gbias = nullptr;
   }
-  if (!grad_bias || N == 0) return EQMP_OK;
-  k_attn_bias<<<(unsigned)((N + 7) / 8), 256, 0, st>>>(a);
-  return cuda_status(cudaGetLastError());
+  if (!send) return launch_attn_finish<float>(a, 0, st);
+  cut(E_send, &a.block, &a.blocks);
+  const AttnForm f = form_of(n, N_src, N, bytes, at.bytes());
+  return bf16 ? launch_attn_send_bf16(a, f, st) : launch_attn_send_f32(a, f, st);
 }
 
 }  // extern "C"

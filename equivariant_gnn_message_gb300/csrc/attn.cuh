@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_recv(AttnArgs a) {
 }
 
 // The senders' pass: each sender's dk and dv from the p and dp of its edges and
-// the rows of their receivers, in the order of the sender view; and dbias.
+// the rows of their receivers, in the order of the sender view.
 template <typename T, int V, int G, int KN, int VN, int U>
 __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_send(AttnArgs a) {
   const Rows rows{a.send_off, a.Ns, a.E_send, a.block, a.blocks};
@@ -396,15 +396,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_send(AttnArgs a) {
       Frag<T, V, G, VN> gf[U];
       float2 pd[U];
       float delta[U];
-      int edge[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        edge[u] = __shfl_sync(0xffffffffu, my_edge, b + u);
-        const int i = __shfl_sync(0xffffffffu, my_dst, b + u);
+        const int edge = __shfl_sync(0xffffffffu, my_edge, b + u), i = __shfl_sync(0xffffffffu, my_dst, b + u);
         const bool ok = mine && (unsigned)i < (unsigned)a.N;
         qf[u].load(q + i * a.q_ld, l, a.D, ok);
         gf[u].load(g + i * a.g_ld, l, a.Dv, ok);
-        pd[u] = ok ? a.pd[(long long)edge[u] * a.H + h] : make_float2(-1.0f, 0.0f);
+        pd[u] = ok ? a.pd[(long long)edge * a.H + h] : make_float2(-1.0f, 0.0f);
         delta[u] = ok ? a.delta[(long long)i * a.H + h] : 0.0f;
       }
 #pragma unroll
@@ -415,7 +413,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_send(AttnArgs a) {
           gf[u].zero();
         }
         const float p = left_out ? 0.0f : pd[u].x, ds = left_out ? 0.0f : p * (pd[u].y - delta[u]);
-        if (a.gbias && l == 0 && mine && (unsigned)edge[u] < (unsigned)a.E) a.gbias[(long long)edge[u] * a.H + h] = ds;
         qf[u].add_to(gk, ds);
         gf[u].add_to(gv, p);
       }
@@ -516,26 +513,27 @@ __device__ void join_row(const AttnArgs& a, int first, int last, int row, int h,
   }
 }
 
+// The blocks of CTA x of the join, for the heads y, y + ny, ...
 template <int MODE, typename T>
-__global__ void __launch_bounds__(kJoinX * kJoinY) k_attn_join(const __grid_constant__ AttnArgs a) {
+__device__ __forceinline__ void join_blocks(const AttnArgs& a, int x, int y, int ny) {
   __shared__ float red[kJoinY][kJoinX];
   __shared__ int range[kJoinBlocks][3];
   const Rows rows = MODE == kJoinSend ? Rows{a.send_off, a.Ns, a.E_send, a.block, a.blocks}
                                       : Rows{a.off, a.N, a.E, a.block, a.blocks};
   if (threadIdx.y == 0 && threadIdx.x < kJoinBlocks) {
-    const int c = blockIdx.x * kJoinBlocks + threadIdx.x, x = c * rows.block;
-    int first = -1, last = -1, row = -1, past = rows.n;  // off[row] <= x < off[past], in words
+    const int c = x * kJoinBlocks + threadIdx.x, at = c * rows.block;
+    int first = -1, last = -1, row = -1, past = rows.n;  // off[row] <= at < off[past], in words
     if (c < rows.blocks) {
       while (past - row > 1) {
         const int mid = row + (past - row) / 2;
-        if (__ldg(rows.off + mid) <= x)
+        if (__ldg(rows.off + mid) <= at)
           row = mid;
         else
           past = mid;
       }
       if (row >= 0) {
         const int e0 = clamped(__ldg(rows.off + row), rows.E), e1 = clamped(__ldg(rows.off + row + 1), rows.E);
-        if (is_long(rows, e0, e1) && e0 < x && x < e1 && e0 / rows.block == c - 1) first = c, last = (e1 - 1) / rows.block;
+        if (is_long(rows, e0, e1) && e0 < at && at < e1 && e0 / rows.block == c - 1) first = c, last = (e1 - 1) / rows.block;
       }
     }
     range[threadIdx.x][0] = first, range[threadIdx.x][1] = last, range[threadIdx.x][2] = row;
@@ -544,8 +542,73 @@ __global__ void __launch_bounds__(kJoinX * kJoinY) k_attn_join(const __grid_cons
   __syncthreads();
   for (int i = 0; i < kJoinBlocks; ++i) {
     if (range[i][0] < 0) continue;
-    for (int h = blockIdx.y; h < a.H; h += gridDim.y) join_row<MODE, T>(a, range[i][0], range[i][1], range[i][2], h, red);
+    for (int h = y; h < a.H; h += ny) join_row<MODE, T>(a, range[i][0], range[i][1], range[i][2], h, red);
   }
+}
+
+template <int MODE, typename T>
+__global__ void __launch_bounds__(kJoinX * kJoinY) k_attn_join(const __grid_constant__ AttnArgs a) {
+  join_blocks<MODE, T>(a, blockIdx.x, blockIdx.y, gridDim.y);
+}
+
+// dbias = ds, from the p and dp of the receivers' pass: a warp for 32 edges and all their heads.  It goes by the rows and
+// not by the sender view, which need not list an edge whose sender is none, nor one that lies outside every row: those
+// are written too, the latter as 0.
+constexpr int kFinishEdges = 32 * kJoinY;  // of a CTA
+
+// The row that holds the lane's edge (-1: none): dst where it is right, else searched for between the rows of the warp's
+// first and last edge.
+__device__ __forceinline__ int row_of_lane(const AttnArgs& a, int first, int e, int last) {
+  auto holds = [&](int row) { return (unsigned)row < (unsigned)a.N && __ldg(a.off + row) <= e && e < __ldg(a.off + row + 1); };
+  int row = a.dst ? __ldg(a.dst + e) : -1;
+  if (__all_sync(0xffffffffu, holds(row))) return row;
+  const Rows rows{a.off, a.N, a.E, 0, 0};
+  row = row_of_edge(rows, first);
+  int past = row_of_edge(rows, last) + 1;  // off[row] <= e < off[past], in words
+  while (past - row > 1) {
+    const int mid = row + (past - row) / 2;
+    if (__ldg(a.off + mid) <= e)
+      row = mid;
+    else
+      past = mid;
+  }
+  return holds(row) ? row : -1;
+}
+
+__device__ __forceinline__ void bias_of_edges(const AttnArgs& a, int x) {
+  const int lane = threadIdx.x, e0 = (x * kJoinY + threadIdx.y) * 32, n = min(32, a.E - e0);
+  const int row = n > 0 ? row_of_lane(a, e0, e0 + min(lane, n - 1), e0 + n - 1) : -1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long first = (long long)e0 * a.H;
+  const int items = n * a.H, step_t = 32 / a.H, step_h = 32 % a.H;
+  int t = lane / a.H, h = lane % a.H;  // of the lane's item: the edge and the head
+  constexpr int AHEAD = 8;             // items on their way together
+  for (int i = lane; i - lane < items; i += 32 * AHEAD) {
+    float2 pd[AHEAD];
+    float delta[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int r = __shfl_sync(0xffffffffu, row, t & 31);
+      const bool in = i + 32 * k < items && r >= 0;
+      pd[k] = in ? a.pd[first + i + 32 * k] : make_float2(-1.0f, 0.0f);
+      delta[k] = in ? a.delta[(long long)r * a.H + h] : 0.0f;
+      t += step_t;
+      h += step_h;
+      if (h >= a.H) h -= a.H, ++t;
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (i + 32 * k < items) a.gbias[first + i + 32 * k] = pd[k].x < 0.0f ? 0.0f : pd[k].x * (pd[k].y - delta[k]);
+  }
+}
+
+// The end of the backward pass: the long rows of the senders, `joins` CTAs of the first, and dbias.  One launch for both.
+template <typename T>
+__global__ void __launch_bounds__(kJoinX * kJoinY) k_attn_finish(const __grid_constant__ AttnArgs a, int joins, int ny) {
+  if ((int)blockIdx.x < joins)
+    join_blocks<kJoinSend, T>(a, blockIdx.x / ny, blockIdx.x % ny, ny);
+  else
+    bias_of_edges(a, blockIdx.x - joins);
 }
 
 }  // namespace eqmp

@@ -25,22 +25,37 @@ EQMP_ATTN_LAUNCHER(launch_attn_recv_bf16);
 EQMP_ATTN_LAUNCHER(launch_attn_send_f32);
 EQMP_ATTN_LAUNCHER(launch_attn_send_bf16);
 
-// The parts of long rows: launched while the pass before it runs, and over at once where there are none.
-template <int PASS, typename T>
-eqmp_status launch_attn_join(const AttnArgs& a, cudaStream_t st) {
-  if (cudaGetLastError() != cudaSuccess) return EQMP_ERR_CUDA;
-  if (!a.blocks) return EQMP_OK;
+// A kernel that waits for the one before it by itself (griddepcontrol.wait).
+template <typename Kernel, typename... Args>
+eqmp_status launch_behind(Kernel kernel, dim3 grid, cudaStream_t st, const Args&... args) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.blocks + kJoinBlocks - 1) / kJoinBlocks), (unsigned)(a.H < 16 ? a.H : 16));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(kJoinX, kJoinY);
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  constexpr int MODE = PASS == kAttnFwd ? kJoinFwd : PASS == kAttnRecv ? kJoinRecv : kJoinSend;
-  return cuda_status(cudaLaunchKernelEx(&cfg, k_attn_join<MODE, T>, a));
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+
+// The end of the backward pass: the senders' long rows, cut into `blocks` blocks, and dbias.
+template <typename T>
+eqmp_status launch_attn_finish(const AttnArgs& a, int blocks, cudaStream_t st) {
+  const int ny = a.H < 16 ? a.H : 16, joins = (blocks + kJoinBlocks - 1) / kJoinBlocks * ny;
+  const int ctas = joins + (a.gbias ? (int)(((long long)a.E + kFinishEdges - 1) / kFinishEdges) : 0);
+  return ctas ? launch_behind(k_attn_finish<T>, dim3((unsigned)ctas), st, a, joins, ny) : EQMP_OK;
+}
+
+// The parts of long rows: the kernel is over at once where there are none.
+template <int PASS, typename T>
+eqmp_status launch_attn_join(const AttnArgs& a, cudaStream_t st) {
+  if (cudaGetLastError() != cudaSuccess) return EQMP_ERR_CUDA;
+  if constexpr (PASS == kAttnSend) return launch_attn_finish<T>(a, a.blocks, st);
+  if (!a.blocks) return EQMP_OK;
+  const dim3 grid((unsigned)((a.blocks + kJoinBlocks - 1) / kJoinBlocks), (unsigned)(a.H < 16 ? a.H : 16));
+  return launch_behind(k_attn_join<PASS == kAttnFwd ? kJoinFwd : kJoinRecv, T>, grid, st, a);
 }
 
 template <int PASS, typename T, int V, int G, int KN, int VN>
@@ -60,7 +75,7 @@ eqmp_status launch_attn_form(const AttnArgs& a, cudaStream_t st) {
 template <int PASS, typename T, int VB, int G, int KN, int VN>
 eqmp_status launch_attn_ring(const AttnArgs& a, cudaStream_t st) {
   constexpr int U = KN + VN <= 4 || (sizeof(T) == 2 && KN + VN <= 5) || VB < 16 ? 4 : 2;
-  constexpr int SMEM = RingShape<VB, G, KN, VN, U, PASS == kAttnSend ? 16 : 4>::CTA;
+  constexpr int SMEM = RingShape<VB, G, KN, VN, U, PASS == kAttnSend ? 12 : 4>::CTA;
   const long long rows = PASS == kAttnSend ? a.Ns : a.N, workers = a.blocks + (rows + a.rows_each - 1) / a.rows_each;
   const dim3 grid((unsigned)((workers + kRingWarps - 1) / kRingWarps), (unsigned)((a.H * G + 31) / 32));
   static unsigned long long done = 0;

@@ -632,9 +632,9 @@ __global__ void __launch_bounds__(32 * kRingWarps, (kRecvWarps<T, VB, KN, VN>)) 
 
 template <typename T, int VB, int G, int KN, int VN, int U>
 __global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(const __grid_constant__ AttnArgs a) {
-  using Shape = RingShape<VB, G, KN, VN, U, 16>;  // p and dp, delta, the edge's number
+  using Shape = RingShape<VB, G, KN, VN, U, 12>;  // p and dp, delta
   constexpr int P = RowVec<T, VB>::PAIRS, KP = KN * P, VP = VN * P, HEADS = 32 / G;
-  constexpr int DELTA_AT = Shape::SMALL_AT + U * HEADS * 8, EDGE_AT = DELTA_AT + U * HEADS * 4;
+  constexpr int DELTA_AT = Shape::SMALL_AT + U * HEADS * 8;
   extern __shared__ __align__(128) uint8_t space[];
   const Rows rows{a.send_off, a.Ns, a.E_send, a.block, a.blocks};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G, hh = lane / G;
@@ -696,7 +696,6 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(const __grid
         } else {
           asm volatile("st.shared.v2.f32 [%0], {%1, %1};" ::"r"(small + Shape::SMALL_AT + item * 8), "f"(-1.0f) : "memory");
         }
-        asm volatile("st.shared.s32 [%0], %1;" ::"r"(small + EDGE_AT + item * 4), "r"(l < n ? e : -1) : "memory");
       }
       put.e += U;
       put.next_row(w);
@@ -725,10 +724,6 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(const __grid
       const float2 pd = lds64(small + Shape::SMALL_AT + item * 8);
       const bool left_out = pd.x < 0.0f;
       const float p = left_out ? 0.0f : pd.x, ds = left_out ? 0.0f : p * (pd.y - lds32(small + DELTA_AT + item * 4));
-      if (a.gbias && l < U && mine) {
-        const int edge = __float_as_int(lds32(small + EDGE_AT + item * 4));
-        if ((unsigned)edge < (unsigned)a.E) a.gbias[(long long)edge * a.H + h] = ds;
-      }
       const unsigned out = __ballot_sync(0xffffffffu, mine && left_out && c + l % U < e1);  // a weight of 0 would keep a NaN
       auto add = [&](int u) {
         const float pu = __shfl_sync(0xffffffffu, p, lane - l + u), dsu = __shfl_sync(0xffffffffu, ds, lane - l + u);

@@ -634,8 +634,10 @@ eqmp_status eqmp_edge_attention(const void* q, int64_t q_ld, const void* k, int6
  * edge of a receiver has ds = 0, exactly.  grad_k and
  * grad_v need dst [E] and the sender view (send_offsets [N_src+1], send_edges
  * [E_send]) of the same edges, as eqmp_fused_backward (the three may be NULL where
- * neither is asked for).  Every row of the results is written; grad_bias is 0 for
- * edges of no receiver of this call.
+ * neither is asked for).  The sender view need not list edges whose sender is
+ * outside 0 .. N_src-1.  Every row of the results is written; grad_bias goes by
+ * the receivers' rows, whatever the sender view lists, and is 0 for edges of no
+ * receiver of this call.
  */
 int64_t eqmp_edge_attention_backward_workspace_size(int64_t N, int64_t E, int64_t E_send, int32_t H, int32_t D,
                                                     int32_t Dv);
