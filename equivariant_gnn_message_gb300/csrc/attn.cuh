@@ -371,6 +371,19 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_recv(AttnArgs a) {
   }
 }
 
+// The receiver of an edge for the senders' pass.  Edges before the first row or behind the last (lists of fixed length, a
+// range of receivers) have none, whatever dst holds: the receivers' pass has not written their p and dp.
+struct Receivers {
+  const int* dst;
+  unsigned first, count;  // the edges of the rows
+  __device__ __forceinline__ explicit Receivers(const AttnArgs& a) : dst(a.dst), first(0), count(0) {
+    if (a.N == 0) return;
+    const int lo = clamped(__ldg(a.off), a.E), hi = clamped(__ldg(a.off + a.N), a.E);
+    first = lo, count = max(hi - lo, 0);
+  }
+  __device__ __forceinline__ int of(int edge) const { return (unsigned)edge - first < count ? __ldg(dst + edge) : -1; }
+};
+
 // The senders' pass: each sender's dk and dv from the p and dp of its edges and
 // the rows of their receivers, in the order of the sender view.
 template <typename T, int V, int G, int KN, int VN, int U>
@@ -387,9 +400,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_send(AttnArgs a) {
   for (int i = 0; i < KN * V; ++i) gk[i] = 0.0f;
 #pragma unroll
   for (int i = 0; i < VN * V; ++i) gv[i] = 0.0f;
+  const Receivers receivers(a);
   for (int c = t.e0; c < t.e1; c += 32) {
     const int my_edge = c + lane < t.e1 ? __ldg(a.send_edges + c + lane) : -1;
-    const int my_dst = (unsigned)my_edge < (unsigned)a.E ? __ldg(a.dst + my_edge) : -1;
+    const int my_dst = receivers.of(my_edge);
     const int n = min(32, t.e1 - c);
     for (int b = 0; b < n; b += U) {
       Frag<T, V, G, KN> qf[U];

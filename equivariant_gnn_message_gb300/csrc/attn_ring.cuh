@@ -652,13 +652,13 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(const __grid
   put.start(w);
   // a place's edge is loaded 64 places ahead, its receiver 32
   Ahead edges;
-  auto receiver = [&](int edge) { return (unsigned)edge < (unsigned)a.E ? __ldg(a.dst + edge) : -1; };
+  const Receivers receivers(a);
   int later, dst_now, dst_next;
   auto start = [&] {
     edges.start(a.send_edges, put.e, a.E_send);
     later = edges.load(a.send_edges, put.e + 64 + lane, a.E_send);
-    dst_now = receiver(edges.now);
-    dst_next = receiver(edges.next);
+    dst_now = receivers.of(edges.now);
+    dst_next = receivers.of(edges.next);
   };
   start();
   uint32_t put_at = 0;
@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_send_ring(const __grid
         edges.next = later;
         later = edges.load(a.send_edges, edges.c + 64 + lane, a.E_send);
         dst_now = dst_next;
-        dst_next = receiver(edges.next);
+        dst_next = receivers.of(edges.next);
       }
       const int at = put.e - edges.c + lane, my_edge = edges.from(put.e), n = put.end - put.e;
       const int d0 = __shfl_sync(0xffffffffu, dst_now, at & 31), d1 = __shfl_sync(0xffffffffu, dst_next, at & 31);

@@ -637,7 +637,8 @@ eqmp_status eqmp_edge_attention(const void* q, int64_t q_ld, const void* k, int6
  * neither is asked for).  The sender view need not list edges whose sender is
  * outside 0 .. N_src-1.  Every row of the results is written; grad_bias goes by
  * the receivers' rows, whatever the sender view lists, and is 0 for edges of no
- * receiver of this call.
+ * receiver of this call.  Such edges (before row_offsets[0] or from row_offsets[N]
+ * on) have no part in grad_k and grad_v either, if the sender view lists them.
  */
 int64_t eqmp_edge_attention_backward_workspace_size(int64_t N, int64_t E, int64_t E_send, int32_t H, int32_t D,
                                                     int32_t Dv);

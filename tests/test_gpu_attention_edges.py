@@ -92,3 +92,33 @@ def test_bias_gradients_of_any_number_of_heads(eq, H):  # noqa: F811
                                                None, bias=p.bias, need=("bias",), out=dict(bias=_stale(p, len(p.src))["bias"]))["bias"]
         lo, hi = int(p.off[a]), int(p.off[b])
         assert torch.equal(part[lo:hi], every[lo:hi]) and not part[:lo].any() and not part[hi:].any()
+
+
+@pytest.mark.parametrize("degrees", [MIXED, LONG], ids=["mixed", "long"])
+@pytest.mark.parametrize("shape,dtype", [((4, 16, 32), "f32"), ((3, 7, 9), "bf16"), ((2, 65, 30), "f32")], ids=str)
+def test_padded_edge_lists(eq, shape, dtype, degrees):  # noqa: F811
+    """Lists of fixed length, with edges behind the last row and before the first that name real nodes and stand in the sender
+    view: they are part of no receiver, so nothing has a gradient from them, whatever the workspace held."""
+    import torch
+
+    whole = Problem(*shape, dtype, degrees, seed=3)
+    stats = whole.forward(eq)["stats"]
+    want, bound = backward_bounds(host(whole.g), *whole.host_args()[:3], host(stats), *whole.host_args()[3:], None, whole.bf16)
+    n, E = len(degrees), len(whole.src)
+    rng = np.random.default_rng(1)
+    for before, behind in ((0, 37), (5, 0), (70, 130)):
+        p = Problem(*shape, dtype, degrees, seed=3)
+        join = lambda a, fill: np.concatenate((fill(before), a, fill(behind)))  # noqa: B023,E731
+        zeros, any_node = (lambda k: np.zeros(k, np.int32)), (lambda k: rng.integers(0, n, k).astype(np.int32))
+        for fill in (zeros, any_node):
+            src, dst = join(whole.src, fill), join(whole.dst, fill)
+            off, edges = eq.sender_view(src, n)
+            p.graph, p.senders = (_up(whole.off + before), _up(src)), (_up(dst), _up(off), _up(edges))
+            pad = lambda k: torch.zeros(k, shape[0], device="cuda")  # noqa: E731
+            p.bias = torch.cat((pad(before), whole.bias, pad(behind)))
+            got = p.backward(eq, stats, out=_stale(p, len(src)), workspace=_workspace(eq, p, len(src), len(edges)))
+            assert not got["bias"][:before].any() and not got["bias"][before + E:].any()
+            got["bias"] = got["bias"][before:before + E]
+            # long rows are cut where the whole list is: the same to the bounds
+            for name in NEED:
+                assert worst(host(got[name]), want[name], bound[name]) <= 1, name
