@@ -52,7 +52,7 @@ struct BackwardSpace {
 };
 
 static BackwardSpace backward_workspace(const Sizes& n, int64_t E_send) {
-  const int64_t recv = part_bytes(n.E, n.H, 2 * n.D + 1), send = part_bytes(E_send, n.H, n.D + n.Dv);
+  const int64_t recv = part_bytes(n.E, n.H, 2 * n.D + 3), send = part_bytes(E_send, n.H, n.D + n.Dv);
   return BackwardSpace{n.E * n.H * 8 + 15 & ~15ll, n.N * n.H * 4 + 15 & ~15ll, recv > send ? recv : send};
 }
 

@@ -303,8 +303,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_recv(AttnArgs a) {
   const T* k = static_cast<const T*>(a.k) + (long long)h * a.D;
   const T* v = static_cast<const T*>(a.v) + (long long)h * a.Dv;
   const long long at = (long long)t.row * a.H + h;
-  float q[KN * V], g[VN * V], pdk[KN * V], pk[KN * V], delta = 0.0f, dps = 0.0f;
-  int live = 0;
+  float q[KN * V], g[VN * V], pdk[KN * V], pk[KN * V], delta = 0.0f, dps = 0.0f, live = 0.0f;
   {
     Frag<T, V, G, KN> f;
     f.load(static_cast<const T*>(a.q) + t.row * a.q_ld + (long long)h * a.D, l, a.D, mine);
@@ -347,19 +346,19 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_recv(AttnArgs a) {
           a.pd[(long long)(e + b + u) * a.H + h] = make_float2(left_out ? -1.0f : p, dp);
         delta = fmaf(p, dp, delta);
         dps += dp;
-        live += !left_out;
+        live += left_out ? 0.0f : 1.0f;
         kf[u].add_to(pdk, p * dp);
         kf[u].add_to(pk, p);
       }
     }
   }
   if (!mine) return;
-  const bool alone = live == 1;  // the only edge's weight is 1, whatever its score
+  const bool alone = live == 1.0f;  // the row's only edge: its weight is 1, whatever its score
   if (t.slot >= 0) {
-    float* to = a.part + ((long long)t.slot * a.H + h) * (2 * a.D + 1);
-    if (l == 0) to[0] = delta;
-    store_part<V, G, KN>(to + 1, l, a.D, pdk);
-    store_part<V, G, KN>(to + 1 + a.D, l, a.D, pk);
+    float* to = a.part + ((long long)t.slot * a.H + h) * (2 * a.D + 3);
+    if (l == 0) to[0] = delta, to[1] = dps, to[2] = live;
+    store_part<V, G, KN>(to + 3, l, a.D, pdk);
+    store_part<V, G, KN>(to + 3 + a.D, l, a.D, pk);
     return;
   }
   if (alone) delta = dps;
@@ -456,7 +455,7 @@ constexpr int kJoinX = 32, kJoinY = 8, kJoinBlocks = 16;
 template <int MODE, typename T>
 __device__ void join_row(const AttnArgs& a, int first, int last, int row, int h, float (&red)[kJoinY][kJoinX]) {
   const int x = threadIdx.x, y = threadIdx.y;
-  const int width = MODE == kJoinFwd ? a.Dv + 2 : MODE == kJoinRecv ? 2 * a.D + 1 : a.D + a.Dv;
+  const int width = MODE == kJoinFwd ? a.Dv + 2 : MODE == kJoinRecv ? 2 * a.D + 3 : a.D + a.Dv;
   // part 0: the row's beginning, in the slot of the block where it lies; then the blocks
   auto part = [&](int i) { return a.part + ((long long)(i ? first + i - 1 : a.blocks + first - 1) * a.H + h) * width; };
   const int parts = last - first + 2;
@@ -493,21 +492,24 @@ __device__ void join_row(const AttnArgs& a, int first, int last, int row, int h,
       }
     }
   } else if constexpr (MODE == kJoinRecv) {
-    float delta = 0.0f;
-    for (int i = y; i < parts; i += kJoinY) delta += part(i)[0];
+    float delta = 0.0f, dps = 0.0f, live = 0.0f;
+    for (int i = y; i < parts; i += kJoinY) delta += part(i)[0], dps += part(i)[1], live += part(i)[2];
     delta = over_y(delta, false);
+    dps = over_y(dps, false);
+    const bool alone = over_y(live, false) == 1.0f;  // the row's only edge, all others left out
+    if (alone) delta = dps;
     if (a.delta && x == 0 && y == 0) a.delta[at] = delta;
     if (!a.gq) return;
     for (int col = x; col - x < a.D; col += kJoinX) {
       float t = 0.0f, s = 0.0f;
       if (col < a.D)
         for (int i = y; i < parts; i += kJoinY) {
-          t += part(i)[1 + col];
-          s += part(i)[1 + a.D + col];
+          t += part(i)[3 + col];
+          s += part(i)[3 + a.D + col];
         }
       t = over_y(t, false);
       s = over_y(s, false);
-      t = a.scale * fmaf(-delta, s, t);
+      t = alone ? 0.0f : a.scale * fmaf(-delta, s, t);
       if (y == 0 && col < a.D) Vec<T, 1>::store(static_cast<T*>(a.gq) + at * a.D + col, &t);
     }
   } else {

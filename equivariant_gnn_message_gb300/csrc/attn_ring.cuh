@@ -609,16 +609,16 @@ __global__ void __launch_bounds__(32 * kRingWarps, (kRecvWarps<T, VB, KN, VN>)) 
       live += __shfl_xor_sync(0xffffffffu, live, o);
     }
     const int slot = __shfl_sync(0xffffffffu, w.slot, i);
-    const bool alone = live == 1.0f && slot < 0;  // the row's only edge: its weight is 1, whatever its score
-    if (alone) delta = dps;
     if (!mine) continue;
     if (slot >= 0) {
-      float* to = a.part + ((long long)slot * a.H + h) * (2 * a.D + 1);
-      if (l == 0) to[0] = delta;
-      store_row_part<T, VB, G, KN>(to + 1, l, a.D, pdk);
-      store_row_part<T, VB, G, KN>(to + 1 + a.D, l, a.D, pk);
+      float* to = a.part + ((long long)slot * a.H + h) * (2 * a.D + 3);
+      if (l == 0) to[0] = delta, to[1] = dps, to[2] = live;
+      store_row_part<T, VB, G, KN>(to + 3, l, a.D, pdk);
+      store_row_part<T, VB, G, KN>(to + 3 + a.D, l, a.D, pk);
       continue;
     }
+    const bool alone = live == 1.0f;  // the row's only edge: its weight is 1, whatever its score
+    if (alone) delta = dps;
     const long long to = (long long)(w.row + i) * a.H + h;
     if (l == 0) a.delta[to] = delta;
     if (a.gq) {

@@ -631,7 +631,7 @@ eqmp_status eqmp_edge_attention(const void* q, int64_t q_ld, const void* k, int6
  *   grad_v     [N_src][H][Dv]  sum over the sender's edges of p grad_out[i]
  *   grad_bias  [E][H]          ds
  * Edges that were left out have no part in any of them (grad_bias 0).  The only
- * edge of a receiver has ds = 0, exactly.  grad_k and
+ * edge of a receiver, or the only one left of it, has ds = 0, exactly.  grad_k and
  * grad_v need dst [E] and the sender view (send_offsets [N_src+1], send_edges
  * [E_send]) of the same edges, as eqmp_fused_backward (the three may be NULL where
  * neither is asked for).  The sender view need not list edges whose sender is

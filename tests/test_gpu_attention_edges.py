@@ -122,3 +122,26 @@ def test_padded_edge_lists(eq, shape, dtype, degrees):  # noqa: F811
             # long rows are cut where the whole list is: the same to the bounds
             for name in NEED:
                 assert worst(host(got[name]), want[name], bound[name]) <= 1, name
+
+
+@pytest.mark.parametrize("shape", [(4, 16, 128), (3, 6, 10), (2, 5, 49), (5, 7, 9), (2, 200, 300)], ids=str)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_the_only_edge_left_of_a_long_row(eq, shape, dtype):  # noqa: F811
+    """Rows that are cut into parts, all edges but one masked, another one for each head: as the only edge of a short row."""
+    import torch
+
+    degrees, H = [700, 2, 300, 400, 65], shape[0]
+    p = Problem(*shape, dtype, degrees, seed=4)
+    left = np.array([[(97 * i + 263 * h + (0, d - 1)[h % 2]) % d for h in range(H)] for i, d in enumerate(degrees)]) + p.off[:-1, None]
+    bias = torch.full_like(p.bias, -float("inf"))
+    for i in range(len(degrees)):
+        for h in range(H):
+            bias[left[i, h], h] = p.bias[left[i, h], h]
+    p.bias = bias
+    got = p.forward(eq)
+    for i in range(len(degrees)):
+        for h in range(H):
+            assert torch.equal(got["out"][i, h], p.v[int(p.src[left[i, h]]), h])
+    for stats in (got["stats"], torch.stack((got["stats"][:, :, 0] * (1 + 2.0 ** -22), got["stats"][:, :, 1]), 2)):
+        g = p.backward(eq, stats)
+        assert not g["q"].any() and not g["k"].any() and not g["bias"].any() and g["v"].any()
