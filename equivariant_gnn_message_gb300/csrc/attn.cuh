@@ -290,6 +290,12 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_fwd(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------- backward
+// sum_e ds k from pdk = sum_e p dp k and pk = sum_e p k.  For the only edge of a row ds is 0, and 0 k is formed, so that a
+// NaN, or an infinity in dp, is kept.
+__device__ __forceinline__ float query_sum(bool alone, float delta, float pdk, float pk) {
+  return fmaf(alone ? delta - delta : -delta, pk, alone ? 0.0f : pdk);
+}
+
 // The receivers' pass: p and dp of each edge from one reading of its key and
 // value, and dq without a second one:
 //   dq = scale (sum_e p dp k  -  delta sum_e p k)
@@ -365,7 +371,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_recv(AttnArgs a) {
   if (a.delta && l == 0) a.delta[at] = delta;
   if (a.gq) {
 #pragma unroll
-    for (int i = 0; i < KN * V; ++i) pdk[i] = alone ? 0.0f : fmaf(-delta, pk[i], pdk[i]);
+    for (int i = 0; i < KN * V; ++i) pdk[i] = query_sum(alone, delta, pdk[i], pk[i]);
     store_share<T, V, G, KN>(static_cast<T*>(a.gq) + at * a.D, l, a.D, pdk, a.scale);
   }
 }
@@ -509,7 +515,7 @@ __device__ void join_row(const AttnArgs& a, int first, int last, int row, int h,
         }
       t = over_y(t, false);
       s = over_y(s, false);
-      t = alone ? 0.0f : a.scale * fmaf(-delta, s, t);
+      t = a.scale * query_sum(alone, delta, t, s);
       if (y == 0 && col < a.D) Vec<T, 1>::store(static_cast<T*>(a.gq) + at * a.D + col, &t);
     }
   } else {

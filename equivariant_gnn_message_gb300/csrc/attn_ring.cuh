@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(32 * kRingWarps, (kRecvWarps<T, VB, KN, VN>)) 
     if (l == 0) a.delta[to] = delta;
     if (a.gq) {
 #pragma unroll
-      for (int x = 0; x < KP; ++x) pdk[x] = alone ? make_float2(0.0f, 0.0f) : __ffma2_rn(make_float2(-delta, -delta), pk[x], pdk[x]);
+      for (int x = 0; x < KP; ++x) pdk[x] = make_float2(query_sum(alone, delta, pdk[x].x, pk[x].x), query_sum(alone, delta, pdk[x].y, pk[x].y));
       store_row<T, VB, G, KN>(static_cast<T*>(a.gq) + to * a.D, l, a.D, pdk, a.scale);
     }
   }

@@ -145,3 +145,36 @@ def test_the_only_edge_left_of_a_long_row(eq, shape, dtype):  # noqa: F811
     for stats in (got["stats"], torch.stack((got["stats"][:, :, 0] * (1 + 2.0 ** -22), got["stats"][:, :, 1]), 2)):
         g = p.backward(eq, stats)
         assert not g["q"].any() and not g["k"].any() and not g["bias"].any() and g["v"].any()
+
+
+@pytest.mark.parametrize("shape", [(4, 16, 128), (2, 5, 49), (3, 7, 9)], ids=str)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("where", ["g", "v", "k", "bias"])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_the_only_edge_and_values_that_are_none(eq, shape, dtype, where, bad):  # noqa: F811
+    """NaN and infinities around a receiver's only edge, of a short row and of a cut one: gradients are NaN where the formula's are."""
+    H = shape[0]
+    p = Problem(*shape, dtype, [1, 3, 1100], n_src=1104, seed=4)
+    p.src[:] = np.arange(1104)  # each edge has its own sender
+    p.graph = (p.graph[0], _up(p.src))
+    off, edges = eq.sender_view(p.src, 1104)
+    p.senders = (p.senders[0], _up(off), _up(edges))
+    p.bias[1:4][:2] = -float("inf")
+    p.bias[4:] = -float("inf")
+    p.bias[777] = 0.5
+    for row, edge in ((0, 0), (1, 3), (2, 777)):
+        if where == "g":
+            p.g[row, H // 2, 1] = bad
+        elif where == "bias":
+            p.bias[edge, H // 2] = bad
+        elif where == "v":
+            p.v[edge, H // 2, 1] = bad
+        else:  # a score of plus infinity, or NaN
+            p.k[edge, H // 2, 1] = bad if p.q[row, H // 2, 1] > 0 else -bad
+    stats = p.forward(eq)["stats"]
+    got = p.backward(eq, stats)
+    with np.errstate(invalid="ignore"):
+        want, bound = backward_bounds(host(p.g), *p.host_args()[:3], host(stats), *p.host_args()[3:], None, p.bf16)
+    for name in NEED:
+        b = np.where(np.isfinite(bound[name]), bound[name], 1e-37)  # masked edges beside a NaN: 0
+        assert worst(host(got[name]), want[name], b) <= 1, name
