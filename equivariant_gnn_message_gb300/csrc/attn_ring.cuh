@@ -392,7 +392,9 @@ struct Feed {
 __device__ __forceinline__ bool is_out(unsigned out, int lane, int l, int u) { return out >> (lane - l + u) & 1; }
 
 // ---------------------------------------------------------------- forward
-constexpr float kAhead = 8.0f;  // weights of up to e^8: the sums keep their relative error
+// How far a score may lie above m before the sums are scaled, and what the weights are multiplied by, so that they stay
+// below 1 (e^8 2^-12 = 0.73) and the sums within the range of the values'.  A power of two rounds nothing.
+constexpr float kAhead = 8.0f, kDown = 0x1p-12f;
 
 template <typename T, int VB, int G, int KN, int VN, int U>
 __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_constant__ AttnArgs a) {
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_
         m = top;
       }
       const float base = m == EQMP_NEG_INF ? 0.0f : m;
-      const float p = __expf(score - base);
+      const float p = __expf(score - base) * kDown;
       z += p;
       const unsigned out = __ballot_sync(0xffffffffu, in && score == EQMP_NEG_INF);
       if (out) {  // left out: a weight of 0 would keep a NaN
@@ -474,7 +476,7 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_
       z += __shfl_xor_sync(0xffffffffu, z, o);
       largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, o));
     }
-    const float from_m = largest == EQMP_NEG_INF ? 1.0f : __expf(m - largest);  // sums relative to the largest score
+    const float from_m = largest == EQMP_NEG_INF ? 1.0f : __expf(m - largest) * (1.0f / kDown);  // sums relative to the largest score
     const int slot = __shfl_sync(0xffffffffu, w.slot, i);
     if (!mine) continue;
     if (slot >= 0) {

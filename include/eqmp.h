@@ -611,7 +611,9 @@ eqmp_status eqmp_edge_bias_backward(const float* grad_bias, const int32_t* bucke
  * An edge whose bias or score is -inf is left out: nothing of its key and value
  * enters, a NaN or an infinity neither.  A receiver with no edge left gets
  * out = 0, m = z = 0.  Other NaNs and infinities go where the formula takes them,
- * within their receiver and head.
+ * within their receiver and head.  The sums are divided by z at the end, and
+ * their weights are at most 1 until then: |v| summed over a receiver's edges has
+ * to stay within fp32's range (3.4e38).
  * H up to 1024, Dv up to 1024 (EQMP_ERR_UNSUPPORTED above).  A receiver of very
  * many edges is spread over the device; its parts are added in a fixed order.
  */
