@@ -25,26 +25,35 @@ static eqmp_status check_sizes(const Sizes& n, eqmp_dtype dtype, float scale) {
 }
 
 // Blocks that rows of more than two are cut into: at least 32 edges, at most
-// 2048 blocks in all, so that the parts stay a few MB.  Graphs of up to kWhole
+// 2048 blocks in all, and fewer of wide heads, so that their parts (`values`
+// each, two a block) stay below 64 MB, or are those of 8 blocks.  Graphs of up to kWhole
 // edges are not cut: there the launches that join the parts cost more than they
 // save (64 atoms, 742 edges: forward 24.5 us a call with them, 19.4 without,
 // backward 38 and 34), unless nearly all edges are one node's (1000 edges of one
 // receiver: 119 us by one warp a head, 24 in blocks).
-constexpr int64_t kWhole = 1024;
+constexpr int64_t kWhole = 1024, kPartBytes = 64ll << 20;
 
-static void cut(int64_t E, int* block, int* blocks) {
-  const int64_t want = (E + 2047) / 2048;
+static void cut(int64_t E, int64_t values, int* block, int* blocks) {
+  int64_t most = kPartBytes / (2 * 4 * values);
+  most = most < 8 ? 8 : most > 2048 ? 2048 : most;
+  const int64_t want = (E + most - 1) / most;
   *block = (int)(want < 32 ? 32 : (want + 31) / 32 * 32);
   *blocks = E > kWhole ? (int)((E + *block - 1) / *block) : 0;
 }
 
-static int64_t part_bytes(int64_t E, int64_t H, int64_t width) {
+// Values of a part: the row's maximum, sum and result; its sums of p dp, of dp and of edges, and of p dp k and p k; its
+// gradients of key and value.
+static int64_t forward_values(const Sizes& n) { return (int64_t)n.H * (n.Dv + 2); }
+static int64_t recv_values(const Sizes& n) { return (int64_t)n.H * (2 * n.D + 3); }
+static int64_t send_values(const Sizes& n) { return (int64_t)n.H * (n.D + n.Dv); }
+
+static int64_t part_bytes(int64_t E, int64_t values) {
   int block, blocks;
-  cut(E, &block, &blocks);
-  return 2ll * blocks * H * width * 4;
+  cut(E, values, &block, &blocks);
+  return 2ll * blocks * values * 4;
 }
 
-static int64_t forward_workspace(const Sizes& n) { return part_bytes(n.E, n.H, n.Dv + 2); }
+static int64_t forward_workspace(const Sizes& n) { return part_bytes(n.E, forward_values(n)); }
 
 struct BackwardSpace {
   int64_t pd, delta, part;
@@ -52,7 +61,7 @@ struct BackwardSpace {
 };
 
 static BackwardSpace backward_workspace(const Sizes& n, int64_t E_send) {
-  const int64_t recv = part_bytes(n.E, n.H, 2 * n.D + 3), send = part_bytes(E_send, n.H, n.D + n.Dv);
+  const int64_t recv = part_bytes(n.E, recv_values(n)), send = part_bytes(E_send, send_values(n));
   return BackwardSpace{n.E * n.H * 8 + 15 & ~15ll, n.N * n.H * 4 + 15 & ~15ll, recv > send ? recv : send};
 }
 
@@ -141,7 +150,7 @@ eqmp_status eqmp_edge_attention(const void* q, int64_t q_ld, const void* k, int6
   a.out = out, a.stats = stats, a.part = static_cast<float*>(workspace);
   a.scale = scale;
   a.N = (int)N, a.Ns = (int)N_src, a.E = (int)E, a.H = H, a.D = D, a.Dv = Dv;
-  cut(E, &a.block, &a.blocks);
+  cut(E, forward_values(n), &a.block, &a.blocks);
   Alignment at;
   at.add(q, q_ld, bytes), at.add(k, k_ld, bytes), at.add(v, v_ld, bytes);
   at.add(out);
@@ -210,7 +219,7 @@ eqmp_status eqmp_edge_attention_backward(const void* grad_out, int64_t grad_out_
   const bool bf16 = dtype == EQMP_BF16;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (N > 0) {
-    cut(E, &a.block, &a.blocks);
+    cut(E, recv_values(n), &a.block, &a.blocks);
     const AttnForm f = form_of(n, N, N_src, bytes, at.bytes());
     const eqmp_status s = bf16 ? launch_attn_recv_bf16(a, f, st) : launch_attn_recv_f32(a, f, st);
     if (s != EQMP_OK) return s;
@@ -220,7 +229,7 @@ eqmp_status eqmp_edge_attention_backward(const void* grad_out, int64_t grad_out_
     a.gbias = nullptr;
   }
   if (!send) return launch_attn_finish<float>(a, 0, st);
-  cut(E_send, &a.block, &a.blocks);
+  cut(E_send, send_values(n), &a.block, &a.blocks);
   const AttnForm f = form_of(n, N_src, N, bytes, at.bytes());
   return bf16 ? launch_attn_send_bf16(a, f, st) : launch_attn_send_f32(a, f, st);
 }
