@@ -2,6 +2,7 @@
 import numpy as np
 import pytest
 
+from tests import attention_forms as forms
 from tests.attention_util import backward_bounds, forward_bounds, worst
 from tests.gpu_util import host
 from tests.test_gpu_attention import Problem, eq  # noqa: F401
@@ -40,3 +41,18 @@ def test_blocks_of_more_than_32_edges(eq, shape, dtype):  # noqa: F811
     degrees = [int(d) for d in np.concatenate(([70_000], rng.integers(0, 300, 100), [129, 128, 127, 20_000, 0, 257]))]
     p = Problem(*shape, dtype, degrees, n_src=50, masked=0.05, seed=3)
     _check_heads(eq, p, list(range(shape[0])))
+
+
+@pytest.mark.parametrize("name", forms.cases())
+def test_forms_of_large_graphs(eq, name):  # noqa: F811
+    """Each form against the oracle, several rows a warp among them; and the case gets the form that it is for."""
+    p = forms.problem(eq, name)
+    H = p.q.shape[1]
+    _check_heads(eq, p, sorted({0, 1, H // 2, H - 1}))
+    rows, form, each = forms.cases()[name][4:]
+    found = forms.forms(lambda: p.backward(eq, p.forward(eq)["stats"]))
+    assert set(found) == {"fwd", "recv", "send"}
+    for ring, numbers, ctas in found.values():
+        assert ring == (each is not None) and numbers == form
+        if ring:  # a CTA for each block of 32 edges, and for each few rows
+            assert ctas == -(-len(p.src) // 32) + -(-rows // each)
