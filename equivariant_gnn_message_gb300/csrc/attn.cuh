@@ -309,7 +309,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_recv(AttnArgs a) {
   const T* k = static_cast<const T*>(a.k) + (long long)h * a.D;
   const T* v = static_cast<const T*>(a.v) + (long long)h * a.Dv;
   const long long at = (long long)t.row * a.H + h;
-  float q[KN * V], g[VN * V], pdk[KN * V], pk[KN * V], delta = 0.0f, dps = 0.0f, live = 0.0f;
+  float q[KN * V], g[VN * V], pdk[KN * V], pk[KN * V], delta = 0.0f, dps = 0.0f;
+  int live = 0;
   {
     Frag<T, V, G, KN> f;
     f.load(static_cast<const T*>(a.q) + t.row * a.q_ld + (long long)h * a.D, l, a.D, mine);
@@ -352,14 +353,14 @@ __global__ void __launch_bounds__(32 * kAttnWarps) k_attn_bwd_recv(AttnArgs a) {
           a.pd[(long long)(e + b + u) * a.H + h] = make_float2(left_out ? -1.0f : p, dp);
         delta = fmaf(p, dp, delta);
         dps += dp;
-        live += left_out ? 0.0f : 1.0f;
+        live += !left_out;
         kf[u].add_to(pdk, p * dp);
         kf[u].add_to(pk, p);
       }
     }
   }
   if (!mine) return;
-  const bool alone = live == 1.0f;  // the row's only edge: its weight is 1, whatever its score
+  const bool alone = live == 1;  // the row's only edge: its weight is 1, whatever its score
   if (t.slot >= 0) {
     float* to = a.part + ((long long)t.slot * a.H + h) * (2 * a.D + 3);
     if (l == 0) to[0] = delta, to[1] = dps, to[2] = live;
