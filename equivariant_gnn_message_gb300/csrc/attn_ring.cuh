@@ -10,10 +10,11 @@
 //
 // The gather binds.  100,000 atoms, 19 edges each, 8 heads of 32 + 128 fp32 values
 // (9.8 GB of rows an edge list through L2): atoms in the order of their cells 630
-// us forward (15 TB/s), 725 and 709 the two passes backward; in no order 1110 us,
-// by DRAM (32 % of the rows hit L2).  10,000 atoms, 48 edges each, 8 heads of 32 +
-// 256 bf16 values: 191, 233 and 215 us, with 53 % of the issue slots at 9 warps an
-// SM, which is what shared memory has room for.
+// us forward (15 TB/s), 724 and 715 the two passes backward (the latter with the
+// bias's gradient); in no order 1110 us, by DRAM (a third of the rows hits L2).
+// 10,000 atoms, 48 edges each, 8 heads of 32 + 256 bf16 values: 193, 231 and 218 us,
+// with 48 to 56 % of the issue slots at 9 warps an SM, which is what shared memory
+// has room for.
 #pragma once
 
 #include "attn.cuh"
@@ -498,9 +499,10 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_attn_fwd_ring(const __grid_
 }
 
 // ---------------------------------------------------------------- backward
-// fp32 rows of up to five vectors a lane: registers for 18 warps an SM (725 us where the
-// compiler's own choice takes 758; a bound of 20 takes 757).  0 leaves it to the
-// compiler: bf16 rows of 1 + 4 vectors at a bound of 1 took 249 us for 235.
+// fp32 rows of up to five vectors a lane: registers for 18 warps an SM (96, and 16 bytes
+// a thread spilled: 724 us where the compiler's own choice of 126 takes 758; a bound of 20
+// takes 757).  0 leaves it to the compiler: bf16 rows of 1 + 4 vectors at a bound of 1
+// took 249 us for 235.
 template <typename T, int VB, int KN, int VN>
 constexpr int kRecvWarps = sizeof(T) == 4 && VB == 16 && KN + VN <= 5 ? 18 : 0;
 

@@ -28,8 +28,9 @@ struct BiasArgs {
 // A CTA finds the buckets of a tile of edges, then writes the tile's rows of the
 // table side by side.  The search is made in fp32 on squares, and again in 64
 // bits (whose rate is 1/60 of it here) only where a border is near.  1,909,372
-// edges, 8 heads, 64 buckets: 16 us, 83 % of the copy rate (105 with every search
-// in 64 bits and rows of single values).
+// edges, 8 heads, 64 buckets: 19 us with cold caches, 71 % of the copy rate (16 where a
+// replayed graph finds part of its inputs in L2), 20.5 a call; 105 with every search
+// in 64 bits and rows of single values.
 constexpr int kBiasThreads = 256, kBiasEdges = 1024;  // edges of a CTA's tile
 constexpr int kTableFloats = 4096;                    // a larger table is read through L1
 
@@ -121,8 +122,10 @@ __global__ void __launch_bounds__(kBiasThreads) k_edge_bias(BiasArgs a) {
 // (r, h) alone adds to column h of copy r, so the order is fixed and nothing is
 // atomic.  The next edges' values are loaded while the last ones are added.  Then
 // the copies are added, and k_edge_bias_sum adds the CTAs' parts.  A thread takes
-// two heads where it can: 1,909,372 edges, 8 heads, 64 buckets 20 us, one head 24,
-// four 36 (the copies leave room for too few threads).
+// two heads where it can: 1,909,372 edges, 8 heads, 64 buckets 20 us from a replayed
+// graph (22 with cold caches, 24.7 a call), one head 24, four 36 (the copies leave room
+// for too few threads).  There are 32 copies of 64 buckets and 8 heads, so half of the
+// threads have none and wait at the barrier, the main stall.
 constexpr int kGradThreads = 256, kGradAhead = 8;
 constexpr int kCopyFloats = 16384;  // of the copies of a CTA: three CTAs an SM
 

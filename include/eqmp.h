@@ -530,7 +530,9 @@ eqmp_status eqmp_degree_norm_backward(const void* grad_y, const void* s, const v
  *   theta[p] = sum_a pos[n][a] freq[p][a]      (p = 0 .. D/2-1; radians)
  *   y[2p] = u[2p] cos(theta) - u[2p+1] sin(theta)
  *   y[2p+1] = u[2p] sin(theta) + u[2p+1] cos(theta)
- * so that q.k of two nodes hangs on the difference of their positions.
+ * so that q.k of two nodes hangs on the difference of their positions.  Squares
+ * are summed in fp32: |x| has to stay below 1e18, and where eps is 0 above 1e-18
+ * for a value of each head.
  *   wq, wk  [D], NULL: 1
  *   eps     >= 0, finite
  *   pos     [N][axes], freq [D/2][axes], axes 1..3: a place in a chain or a time
