@@ -52,10 +52,13 @@ eqmp_status launch_attn_finish(const AttnArgs& a, int blocks, cudaStream_t st) {
 template <int PASS, typename T>
 eqmp_status launch_attn_join(const AttnArgs& a, cudaStream_t st) {
   if (cudaGetLastError() != cudaSuccess) return EQMP_ERR_CUDA;
-  if constexpr (PASS == kAttnSend) return launch_attn_finish<T>(a, a.blocks, st);
-  if (!a.blocks) return EQMP_OK;
-  const dim3 grid((unsigned)((a.blocks + kJoinBlocks - 1) / kJoinBlocks), (unsigned)(a.H < 16 ? a.H : 16));
-  return launch_behind(k_attn_join<PASS == kAttnFwd ? kJoinFwd : kJoinRecv, T>, grid, st, a);
+  if constexpr (PASS == kAttnSend) {
+    return launch_attn_finish<T>(a, a.blocks, st);
+  } else {
+    if (!a.blocks) return EQMP_OK;
+    const dim3 grid((unsigned)((a.blocks + kJoinBlocks - 1) / kJoinBlocks), (unsigned)(a.H < 16 ? a.H : 16));
+    return launch_behind(k_attn_join<PASS == kAttnFwd ? kJoinFwd : kJoinRecv, T>, grid, st, a);
+  }
 }
 
 template <int PASS, typename T, int V, int G, int KN, int VN>
